@@ -614,6 +614,143 @@ gtp_status gtp_rs_local_sum(const void *const *slices, int32_t P, int64_t n, gtp
 gtp_status gtp_rs_local_sum_rows(const void *slices, int64_t row_bytes, int32_t P, int64_t n,
                                  gtp_dtype in_dt, void *out, gtp_dtype out_dt, gtp_stream stream);
 
+/* ----------------------------------------------------------------------- MXFP4
+ * OCP microscaled 4-bit weights, activations and gradients, the format below MXFP8's: packed
+ * E2M1 elements (two to a byte, the even one in the low nibble) and one E8M0 scale byte, e + 127,
+ * per block of 32 consecutive elements of a row.  A view's rows are padded with zeros to whole
+ * blocks, so any size quantizes; its scales lie in the tiled layout, padding bytes zero:
+ *   view of a [rows, cols] matrix: codes [rows, ceil(cols / 32) * 16 bytes], scales
+ *   gtp_sf_tiled_bytes(rows, ceil(cols / 32)) bytes, both 16-byte aligned.
+ * Rounding of a block with largest magnitude amax:
+ *   nearest     e = floor(log2 amax) - 2 (the OCP rule), code = RNE_E2M1(x / 2^e), saturated at 6;
+ *   stochastic  e = the least with amax <= 6 * 2^e (nothing saturates); y = |x| / 2^e, kept to 23
+ *               fractional bits below 1, lies between two grid points a step s (0.5, 1 or 2) apart
+ *               and goes up where (y - low) / s + (2 r + 1) / 512 >= 1, r the element's random byte:
+ *               the mean of a code is y to 1/512 of a step, which keeps gradients unbiased.
+ * Scale bytes clamp at 0; a block holding NaN or Inf gets byte 0xFF and codes 0 and reads as NaN.
+ */
+
+/* The counter-based generator (Philox4x32-10, Salmon et al., SC 2011) of stochastic rounding and
+ * dropout.  Every draw is a function of (seed, offset, where it is used), so a forward and its
+ * backward draw the same mask from the same pair and nothing random is kept.  Give each use of a
+ * seed its own offset (say, layer and step).  key = seed; counter = (group | stream << 30, row,
+ * offset low, offset high); streams: 0 dropout (groups of 8 columns, 16 bits a column), 1 and 2
+ * rounding of a rowwise and of a columnwise view (groups of 16 elements of the view's row, 8 bits
+ * an element), bits taken in order from the low end of the four words. */
+typedef struct {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t *device_offset; /* device pointer to one word added to offset when the kernel runs
+                                    (a captured graph's step count), 8-byte aligned; NULL = none */
+} gtp_rng;
+
+/* src[rows, cols] (F32 or BF16, row stride src_ld elements, element-aligned) -> the rowwise view
+ * (row_codes, row_scales) and / or the columnwise view (col_codes, col_scales: the rowwise view of
+ * src^T, [cols, ceil(rows / 32) * 16 bytes]), which dgrad and wgrad contract over.  A NULL pair is
+ * not written; both views of one source cost one read of it.  rng: host pointer, NULL rounds to
+ * nearest.  No output may overlap src or another output (GTP_E_ARG). */
+gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int64_t rows, int64_t cols,
+                              int64_t src_ld, uint8_t *row_codes, uint8_t *row_scales,
+                              uint8_t *col_codes, uint8_t *col_scales, const gtp_rng *rng,
+                              gtp_stream stream);
+
+/* A view's values, out[rows, cols] (F32 or BF16, contiguous, element-aligned): exact in both types
+ * below 2^128, Inf from there on (an element above 1.5 * 2^127 stochastically rounded up). */
+gtp_status gtp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                int64_t cols, void *out, gtp_dtype out_dt, gtp_stream stream);
+
+/* The three products of a linear on MXFP4 views, block-scaled FP4 tensor cores, fp32 accumulation:
+ *   Y[M,N]  (bf16) = dq(Xq) dq(Wq)^T     rowwise views of X[M,K] and W[N,K]
+ *   dX[M,K] (bf16) = dq(dYq) dq(Wtq)^T   rowwise view of dY[M,N], columnwise view of W
+ *   grad_data[grad_offset : +N*K].view(N,K) += dq(dYtq) dq(Xtq)^T (fp32)   columnwise views of dY, X
+ * Any M and any contraction length (0 writes zeros / adds nothing); the outputs' rows are multiples
+ * of 16 bytes (N % 8, K % 8, K % 4 and grad_offset % 4 == 0, else GTP_E_ALIGN); the view inside the
+ * buffer (GTP_E_RANGE); no output overlaps an input (GTP_E_ARG).  The accumulate's summation order
+ * may differ between runs, as gtp_linear_wgrad_accum's. */
+gtp_status gtp_linear_fprop_mxfp4(const uint8_t *Xq, const uint8_t *Xs, const uint8_t *Wq,
+                                  const uint8_t *Ws, void *Y, int64_t M, int64_t N, int64_t K,
+                                  gtp_stream stream);
+gtp_status gtp_linear_dgrad_mxfp4(const uint8_t *dYq, const uint8_t *dYs, const uint8_t *Wtq,
+                                  const uint8_t *Wts, void *dX, int64_t M, int64_t N, int64_t K,
+                                  gtp_stream stream);
+gtp_status gtp_linear_wgrad_accum_mxfp4(const uint8_t *dYtq, const uint8_t *dYts, const uint8_t *Xtq,
+                                        const uint8_t *Xts, float *grad_data, int64_t grad_offset,
+                                        int64_t grad_numel_total, int64_t M, int64_t N, int64_t K,
+                                        gtp_stream stream);
+
+/* ------------------------------------------------------------------------ rotary positions
+ * Between the QKV product and attention: pair i of a head at position p turns by p f_i,
+ *   (a, b) -> (a cos - b sin, a sin + b cos) * scale,
+ * and its gradient by the opposite angle (inverse = 1).  Pairs are (i, i + rot_dim / 2) or, with
+ * interleaved = 1, (2 i, 2 i + 1); elements from rot_dim on keep their values (rot_dim <= head_dim).
+ * The angle is taken as p * turns[i] modulo 2^64, turns[i] = round(f_i / 2 pi * 2^64): exact at any
+ * position.  fp32 arithmetic, one rounding. */
+typedef enum {
+  GTP_ROTARY_UNSCALED = 0, /* f_i = base^(-2 i / rot_dim)                                         */
+  GTP_ROTARY_LINEAR = 1,   /* f_i / factor                                                        */
+  GTP_ROTARY_BASE = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) in place of base            */
+  GTP_ROTARY_BANDS = 3,    /* keep f_i + (1 - keep) f_i / factor, keep = (turns over the context - */
+                           /*   low_turns) / (high_turns - low_turns), clamped to [0, 1]           */
+  GTP_ROTARY_RAMP = 4      /* the same blend, linear in i between the pairs that make high_turns   */
+                           /*   and low_turns; scale 0.1 ln(factor) + 1                            */
+} gtp_rotary_scaling;
+
+typedef struct {
+  double base;           /* > 1                                                           */
+  double factor;         /* >= 1, the context's extension (all but UNSCALED)              */
+  double low_turns;      /* BANDS, RAMP: turns over the trained context below which a     */
+  double high_turns;     /*   pair is fully stretched, and above which it is kept          */
+  int64_t context;       /* BANDS, RAMP: trained context, > 0                              */
+  int32_t rot_dim;       /* even, 2 to 256                                                 */
+  int32_t scaling;       /* gtp_rotary_scaling                                             */
+  int32_t reserved[2];   /* 0                                                              */
+} gtp_rotary_config;
+
+/* turns[rot_dim / 2] and *scale (host arrays) for gtp_rotary.  Host only; needs no GPU. */
+gtp_status gtp_rotary_turns(const gtp_rotary_config *cfg, uint64_t *turns, float *scale);
+
+/* Heads (t, g, h), t < tokens, g < groups, h < heads, at src + t src_token + g src_group +
+ * h src_head (element strides; a head's elements are contiguous), likewise dst: the packed QKV
+ * product [tokens, groups, queries + key + value, head_dim] rotates its queries and keys as
+ * groups x (queries + 1) heads of a group stride of queries + 2.  dst may be src exactly (in place)
+ * and otherwise may not overlap it; the heads of dst may not overlap each other (GTP_E_ARG). */
+typedef struct {
+  const void *src;
+  void *dst;
+  const void *positions;           /* device [tokens], int32 or int64, any sign; NULL:            */
+  int64_t pos0;                    /*   pos0 + (t / tokens_per_position) % positions_per_sequence */
+  int64_t tokens_per_position;     /*   >= 1 (the batch of a sequence-major batch)                */
+  int64_t positions_per_sequence;  /*   >= 0; 0: no modulus                                       */
+  int64_t tokens;
+  int64_t src_token, src_group, src_head, dst_token, dst_group, dst_head;
+  const uint64_t *turns;           /* host, rot_dim / 2 entries                                   */
+  int32_t groups, heads, head_dim, rot_dim; /* rot_dim even, 2 to 256                             */
+  int32_t dtype;                   /* GTP_F32 or GTP_BF16, both src and dst                       */
+  int32_t positions64, interleaved, inverse; /* 0 or 1                                            */
+  float scale;
+  int32_t reserved;                /* 0                                                           */
+} gtp_rotary_desc;
+
+gtp_status gtp_rotary(const gtp_rotary_desc *desc, gtp_stream stream);
+
+/* ------------------------------------------------------------------------ dropout
+ * After the projections: out = residual + dropout(x), and its gradient.  The mask is drawn again in
+ * the backward from the same (seed, offset) and never stored:
+ *   keep(i, j) = r >= T, r 16 random bits, T = round(65536 p)  (p to the nearest 1/65536)
+ *   out = residual + (keep ? x * 65536 / (65536 - T) : 0);   dx = keep ? dout * 65536 / (65536 - T) : 0
+ * A dropped element contributes 0 whatever it holds; p = 1 drops everything.  The residual's own
+ * gradient is dout.  fp32 arithmetic, one rounding.
+ * x, residual and out are [rows, cols] with row strides x_ld, residual_ld, out_ld (elements, >=
+ * cols), each F32 or BF16 and element-aligned; residual has out's type and may be NULL (no add).
+ * out may be x or residual exactly (same start, stride and type), else it may not overlap them. */
+gtp_status gtp_dropout_add(const void *x, gtp_dtype x_dt, int64_t x_ld, const void *residual,
+                           int64_t residual_ld, void *out, gtp_dtype out_dt, int64_t out_ld,
+                           int64_t rows, int64_t cols, float p, const gtp_rng *rng,
+                           gtp_stream stream);
+gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld, void *dx,
+                            gtp_dtype dx_dt, int64_t dx_ld, int64_t rows, int64_t cols, float p,
+                            const gtp_rng *rng, gtp_stream stream);
+
 /* ------------------------------------------------------------------ diagnostics
  * Every wait inside the tensor-core kernels has a time limit.  A wait that runs out sets
  * a bit in a per-device word and the kernel unwinds (its results are then invalid):

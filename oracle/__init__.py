@@ -32,6 +32,10 @@ Modules:
   nvfp4         NVFP4 quantize (block 16, tensor scale) and its fprop  (pinned)
   sf_layout     the tiled order of scale bytes                         (pinned)
   rs_sum        the local fp32 sum of the all-to-all reduce-scatter    (pinned)
+  philox        the counter-based generator of rounding and dropout    (pinned)
+  mxfp4         MXFP4 quantize (block 32, two roundings), the products (pinned)
+  rotary        rotary positions and their frequencies                 (pinned)
+  dropout       dropout with the residual add, and its gradient        (pinned)
 
 Every function is pinned by a ``-m "not gpu"`` test against something other than
 itself (page-printed values under tests/golden/, closed forms, library special cases,

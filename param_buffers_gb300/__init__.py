@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 from . import abi
 
@@ -28,6 +28,9 @@ __all__ = [
     "gtp_linear_dgrad_mxfp8", "gtp_linear_wgrad_accum_mxfp8", "gtp_nvfp4_quantize_rowwise",
     "gtp_linear_fprop_nvfp4", "gtp_sf_tiled_bytes", "gtp_sf_tile", "gtp_mxfp8_quantize_rowwise_tiled",
     "gtp_nvfp4_quantize_rowwise_tiled", "gtp_linear_fprop_mxfp8_tiled", "gtp_linear_fprop_nvfp4_tiled",
+    "Rng", "gtp_mxfp4_views", "gtp_mxfp4_quantize", "gtp_mxfp4_dequantize", "gtp_linear_fprop_mxfp4",
+    "gtp_linear_dgrad_mxfp4", "gtp_linear_wgrad_accum_mxfp4", "RotaryConfig", "gtp_rotary_turns", "gtp_rotary",
+    "gtp_dropout_add", "gtp_dropout_grad",
     "gtp_wait_timeouts", "gtp_selftest_wait_timeout",
 ]
 
@@ -786,3 +789,240 @@ def gtp_linear_fprop_nvfp4_tiled(Xq, Xs_tiled, x_amax, Wq, Ws_tiled, w_amax, Y, 
     _check(lib().gtp_linear_fprop_nvfp4_tiled(_ptr(Xq), _ptr(Xs_tiled), _ptr(x_amax), _ptr(Wq), _ptr(Ws_tiled),
                                               _ptr(w_amax), _ptr(Y), M, N, K, _stream(stream)),
            "gtp_linear_fprop_nvfp4_tiled")
+
+
+# ----------------------------------------------------------------------------- MXFP4
+
+class Rng(NamedTuple):
+    """The counter-based generator of stochastic rounding and dropout: every draw is a function of
+    (seed, offset, place).  device_offset: a one-element int64 CUDA tensor added to offset when the
+    kernel runs (the step count of a captured graph), or None.  A plain tuple serves as well."""
+    seed: int
+    offset: int
+    device_offset: object = None
+
+
+def _rng(rng):
+    if rng is None:
+        return None
+    seed, offset, *device = rng
+    word = device[0] if device else None
+    if word is not None:
+        import torch
+        if word.dtype != torch.int64 or word.numel() != 1 or not word.is_cuda:
+            raise TypeError("device_offset must be a one-element int64 CUDA tensor")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset are unsigned 64-bit numbers")
+    return C.byref(abi.gtp_rng(seed, offset, _ptr(word)))
+
+
+def _float_dtype(t, name: str) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return abi.GTP_BF16
+    if t.dtype == torch.float32:
+        return abi.GTP_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows(t, name: str):
+    """(dtype, row stride) of a 2-D float matrix whose rows are contiguous."""
+    dt = _float_dtype(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return dt, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _mxfp4_view(view, rows: int, cols: int, name: str):
+    import torch
+    if view is None:
+        return 0, 0
+    codes, scales = view
+    _require(codes, torch.uint8, f"{name} codes", 2)
+    if tuple(codes.shape) != (rows, 16 * -(-cols // 32)):
+        raise ValueError(f"{name} codes must be [{rows}, {16 * -(-cols // 32)}]")
+    _require_tiled(scales, rows, -(-cols // 32), f"{name} scales")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def gtp_mxfp4_views(rows: int, cols: int, device="cuda"):
+    """Buffers of the rowwise and the columnwise view of a [rows, cols] matrix, (codes, scales) each."""
+    import torch
+
+    def view(r, c):
+        b = -(-c // 32)
+        return (torch.empty(r, 16 * b, dtype=torch.uint8, device=device),
+                torch.empty(-(-r // 128) * -(-b // 4) * 512, dtype=torch.uint8, device=device))
+    return view(rows, cols), view(cols, rows)
+
+
+def gtp_mxfp4_quantize(src, row=None, col=None, rng=None, stream=None) -> None:
+    """src[R,C] (fp32 or bf16, contiguous rows of any stride) -> its rowwise and / or columnwise MXFP4
+    view, each a (codes, scales) pair as gtp_mxfp4_views makes them.  rng None rounds to nearest, an
+    Rng stochastically."""
+    dt, ld = _rows(src, "src")
+    R, Cc = src.shape
+    rc, rs = _mxfp4_view(row, R, Cc, "rowwise")
+    cc, cs = _mxfp4_view(col, Cc, R, "columnwise")
+    _check(lib().gtp_mxfp4_quantize(src.data_ptr(), dt, R, Cc, ld, rc, rs, cc, cs, _rng(rng), _stream(stream)),
+           "gtp_mxfp4_quantize")
+
+
+def gtp_mxfp4_dequantize(codes, scales, out, stream=None) -> None:
+    """The values of an MXFP4 view, out[R,C] (fp32 or bf16, contiguous)."""
+    dt = _float_dtype(out, "out")
+    _require(out, out.dtype, "out", 2)
+    R, Cc = out.shape
+    c, s = _mxfp4_view((codes, scales), R, Cc, "view")
+    _check(lib().gtp_mxfp4_dequantize(c, s, R, Cc, out.data_ptr(), dt, _stream(stream)), "gtp_mxfp4_dequantize")
+
+
+def _mxfp4_product(Aq, As, Bq, Bs, names: str):
+    """Pointers of two views contracted over their rows, and that length (padded to whole blocks)."""
+    import torch
+    for t, n in zip((Aq, Bq), names.split()):
+        _require(t, torch.uint8, n, 2)
+    K = 2 * Aq.shape[1]
+    if Bq.shape[1] != Aq.shape[1] or K % 32:
+        raise ValueError("shape mismatch: both views hold the contraction's whole blocks")
+    for t, q, n in ((As, Aq, "scales of " + names.split()[0]), (Bs, Bq, "scales of " + names.split()[1])):
+        _require_tiled(t, q.shape[0], K // 32, n)
+    return Aq.data_ptr(), As.data_ptr(), Bq.data_ptr(), Bs.data_ptr(), K
+
+
+def gtp_linear_fprop_mxfp4(Xq, Xs, Wq, Ws, Y, stream=None) -> None:
+    """Y[M,N] (bf16) = dq(Xq, Xs) dq(Wq, Ws)^T, the rowwise MXFP4 views of X[M,K] and W[N,K]."""
+    import torch
+    *ptrs, K = _mxfp4_product(Xq, Xs, Wq, Ws, "Xq Wq")
+    _require(Y, torch.bfloat16, "Y", 2)
+    M, N = Xq.shape[0], Wq.shape[0]
+    if tuple(Y.shape) != (M, N):
+        raise ValueError("shape mismatch: Y [M,N]")
+    _check(lib().gtp_linear_fprop_mxfp4(*ptrs, Y.data_ptr(), M, N, K, _stream(stream)), "gtp_linear_fprop_mxfp4")
+
+
+def gtp_linear_dgrad_mxfp4(dYq, dYs, Wtq, Wts, dX, stream=None) -> None:
+    """dX[M,K] (bf16) = dq(dYq, dYs) dq(Wtq, Wts)^T: dY[M,N] rowwise, W[N,K] columnwise."""
+    import torch
+    *ptrs, N = _mxfp4_product(dYq, dYs, Wtq, Wts, "dYq Wtq")
+    _require(dX, torch.bfloat16, "dX", 2)
+    M, K = dYq.shape[0], Wtq.shape[0]
+    if tuple(dX.shape) != (M, K):
+        raise ValueError("shape mismatch: dX [M,K]")
+    _check(lib().gtp_linear_dgrad_mxfp4(*ptrs, dX.data_ptr(), M, N, K, _stream(stream)), "gtp_linear_dgrad_mxfp4")
+
+
+def gtp_linear_wgrad_accum_mxfp4(dYtq, dYts, Xtq, Xts, grad_data, grad_offset: int, stream=None) -> None:
+    """grad_data[grad_offset:+N*K].view(N,K) += dq(dYtq, dYts) dq(Xtq, Xts)^T (fp32), the columnwise MXFP4
+    views of dY[M,N] and X[M,K]."""
+    import torch
+    *ptrs, M = _mxfp4_product(dYtq, dYts, Xtq, Xts, "dYtq Xtq")
+    _require(grad_data, torch.float32, "grad_data")
+    _check(lib().gtp_linear_wgrad_accum_mxfp4(*ptrs, grad_data.data_ptr(), int(grad_offset), grad_data.numel(), M,
+                                              dYtq.shape[0], Xtq.shape[0], _stream(stream)),
+           "gtp_linear_wgrad_accum_mxfp4")
+
+
+# ----------------------------------------------------------------------------- rotary positions
+
+@dataclass(frozen=True)
+class RotaryConfig:
+    """Frequencies of the rotated pairs; scaling: "unscaled", "linear", "base", "bands" or "ramp" (the
+    rules of gtp_rotary_scaling)."""
+    rot_dim: int
+    base: float = 10000.0
+    scaling: str = "unscaled"
+    factor: float = 1.0
+    low_turns: float = 1.0
+    high_turns: float = 4.0
+    context: int = 8192
+
+
+_ROTARY_SCALING = {"unscaled": abi.GTP_ROTARY_UNSCALED, "linear": abi.GTP_ROTARY_LINEAR, "base": abi.GTP_ROTARY_BASE,
+                   "bands": abi.GTP_ROTARY_BANDS, "ramp": abi.GTP_ROTARY_RAMP}
+
+
+def gtp_rotary_turns(config: RotaryConfig):
+    """(turns, scale) for gtp_rotary: the pairs' turns a position as 64-bit fractions (a ctypes array of
+    rot_dim / 2) and the factor of the rotated values.  Host only."""
+    if config.scaling not in _ROTARY_SCALING:
+        raise ValueError(f"unknown scaling {config.scaling!r}")
+    c = abi.gtp_rotary_config(config.base, config.factor, config.low_turns, config.high_turns, int(config.context),
+                              int(config.rot_dim), _ROTARY_SCALING[config.scaling])
+    turns, scale = (C.c_uint64 * max(1, int(config.rot_dim) // 2))(), C.c_float()
+    _check(lib().gtp_rotary_turns(C.byref(c), turns, C.byref(scale)), "gtp_rotary_turns")
+    return turns, scale.value
+
+
+def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: float = 1.0, inverse: bool = False,
+               pos0: int = 0, tokens_per_position: int = 1, positions_per_sequence: int = 0, stream=None) -> None:
+    """Rotates the heads of src into dst (which may be src: in place), [tokens, heads, head_dim] or
+    [tokens, groups, heads, head_dim] views of any strides with contiguous heads, fp32 or bf16; the first
+    2 * len(turns) elements of a head turn, the others keep their values.  positions: int32 or int64
+    CUDA tensor of the tokens' positions, or None for
+    pos0 + (t // tokens_per_position) % positions_per_sequence (0: no modulus).  layout: "half" pairs
+    (i, i + rot_dim/2), "interleaved" (2i, 2i+1).  inverse=True is the gradient."""
+    import torch
+    dt = _float_dtype(src, "src")
+    if dst.dtype != src.dtype or dst.shape != src.shape:
+        raise ValueError("dst must have src's dtype and shape")
+    if src.dim() not in (3, 4):
+        raise ValueError("src must be [tokens, heads, head_dim] or [tokens, groups, heads, head_dim]")
+    D = src.shape[-1]
+    if D > 1 and (src.stride(-1) != 1 or dst.stride(-1) != 1):
+        raise ValueError("heads must be contiguous")
+    if layout not in ("half", "interleaved"):
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    T, G, H = (src.shape[0], 1, src.shape[1]) if src.dim() == 3 else src.shape[:3]
+    ss, ds = src.stride(), dst.stride()
+    if src.dim() == 3:
+        ss, ds = (ss[0], 0, ss[1]), (ds[0], 0, ds[1])
+    wide = 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be int32 or int64")
+        wide = int(positions.dtype == torch.int64)
+        _require(positions, positions.dtype, "positions", 1)
+        if positions.numel() != T:
+            raise ValueError("one position a token")
+    if not isinstance(turns, C.Array):
+        turns = (C.c_uint64 * len(turns))(*turns)
+    d = abi.gtp_rotary_desc(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
+                            positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
+                            C.addressof(turns), G, H, D, 2 * len(turns), dt, wide, int(layout == "interleaved"),
+                            int(bool(inverse)), scale, 0)
+    _check(lib().gtp_rotary(C.byref(d), _stream(stream)), "gtp_rotary")
+
+
+# ----------------------------------------------------------------------------- dropout
+
+def gtp_dropout_add(x, residual, out, p: float, rng, stream=None) -> None:
+    """out = residual + dropout(x) (residual None: no add), [R,C] fp32 or bf16 with contiguous rows of any
+    stride; residual has out's dtype.  out may be x or residual.  rng: an Rng, the gradient's too."""
+    xd, xl = _rows(x, "x")
+    od, ol = _rows(out, "out")
+    rl = 0
+    if residual is not None:
+        rd, rl = _rows(residual, "residual")
+        if rd != od or residual.shape != out.shape:
+            raise ValueError("residual must have out's dtype and shape")
+    if x.shape != out.shape:
+        raise ValueError("x and out must have the same shape")
+    _check(lib().gtp_dropout_add(x.data_ptr(), xd, xl, _ptr(residual), rl, out.data_ptr(), od, ol, x.shape[0],
+                                 x.shape[1], p, _rng(rng), _stream(stream)),
+           "gtp_dropout_add")
+
+
+def gtp_dropout_grad(dout, dx, p: float, rng, stream=None) -> None:
+    """dx = the gradient of dropout(x) from dout under the forward's p and rng; dx may be dout."""
+    gd, gl = _rows(dout, "dout")
+    xd, xl = _rows(dx, "dx")
+    if dout.shape != dx.shape:
+        raise ValueError("dout and dx must have the same shape")
+    _check(lib().gtp_dropout_grad(dout.data_ptr(), gd, gl, dx.data_ptr(), xd, xl, dx.shape[0], dx.shape[1], p,
+                                  _rng(rng), _stream(stream)),
+           "gtp_dropout_grad")

@@ -82,6 +82,29 @@ class gtp_adam_hparams(C.Structure):
                 ("grad_scale", C.c_void_p)]
 
 
+class gtp_rng(C.Structure):
+    _fields_ = [("seed", C.c_uint64), ("offset", C.c_uint64), ("device_offset", C.c_void_p)]
+
+
+# gtp_rotary_scaling
+GTP_ROTARY_UNSCALED, GTP_ROTARY_LINEAR, GTP_ROTARY_BASE, GTP_ROTARY_BANDS, GTP_ROTARY_RAMP = range(5)
+
+
+class gtp_rotary_config(C.Structure):
+    _fields_ = [("base", C.c_double), ("factor", C.c_double), ("low_turns", C.c_double), ("high_turns", C.c_double),
+                ("context", C.c_int64), ("rot_dim", C.c_int32), ("scaling", C.c_int32), ("reserved", C.c_int32 * 2)]
+
+
+class gtp_rotary_desc(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("positions", C.c_void_p), ("pos0", C.c_int64),
+                ("tokens_per_position", C.c_int64), ("positions_per_sequence", C.c_int64), ("tokens", C.c_int64),
+                ("src_token", C.c_int64), ("src_group", C.c_int64), ("src_head", C.c_int64),
+                ("dst_token", C.c_int64), ("dst_group", C.c_int64), ("dst_head", C.c_int64), ("turns", C.c_void_p),
+                ("groups", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32), ("rot_dim", C.c_int32),
+                ("dtype", C.c_int32), ("positions64", C.c_int32), ("interleaved", C.c_int32), ("inverse", C.c_int32),
+                ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
@@ -127,6 +150,15 @@ PROTOTYPES = {
     "gtp_linear_dgrad_mxfp8_tiled": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
     "gtp_linear_wgrad_accum_mxfp8_tiled": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, I64, I64, VP]),
     "gtp_linear_fprop_nvfp4_tiled": (I32, [VP, VP, VP, VP, VP, VP, VP, I64, I64, I64, VP]),
+    "gtp_mxfp4_quantize": (I32, [VP, I32, I64, I64, I64, VP, VP, VP, VP, P(gtp_rng), VP]),
+    "gtp_mxfp4_dequantize": (I32, [VP, VP, I64, I64, VP, I32, VP]),
+    "gtp_linear_fprop_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
+    "gtp_linear_dgrad_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
+    "gtp_linear_wgrad_accum_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, I64, I64, VP]),
+    "gtp_rotary_turns": (I32, [P(gtp_rotary_config), P(C.c_uint64), P(C.c_float)]),
+    "gtp_rotary": (I32, [P(gtp_rotary_desc), VP]),
+    "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
+    "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
     "gtp_wait_timeouts": (I32, [P(C.c_uint32), I32]),
     "gtp_selftest_wait_timeout": (I32, [I64, VP]),
     "gtp_grad_norm_workspace_bytes": (C.c_size_t, [P(gtp_bucket_desc), I32]),

@@ -1,4 +1,4 @@
-// The block-scaled GEMMs on the 5th-generation tensor cores: MXFP8 (forward, dgrad and
+// The block-scaled GEMMs on the 5th-generation tensor cores: MXFP8 and MXFP4 (forward, dgrad and
 // wgrad-accumulate on the rowwise / columnwise views) and NVFP4 (forward).
 //
 // Page: "Generalized Tensor Parallelism (GTP)" (Megatron-Core developer guide), §1.3
@@ -19,7 +19,10 @@ namespace {
 //          of K block k reads byte k of it through the sf_id field);
 //   NVFP4  kind::mxf4nvf4.block_scale.scale_vec::4X: packed E2M1 elements, one E4M3
 //          scale per 16; a stage holds 256 K (four scale words per row, one per MMA of
-//          K 64), and the epilogue multiplies by 1 / (S_A S_B), the per-tensor scales.
+//          K 64), and the epilogue multiplies by 1 / (S_A S_B), the per-tensor scales;
+//   MXFP4  kind::mxf4.block_scale.scale_vec::2X: packed E2M1 elements, one E8M0 scale per 32;
+//          a stage holds 256 K (two scale words per row; the MMA of K block k reads bytes
+//          2 (k % 2) and the next of word k / 2).  Tiled scales and the CTA pair only.
 // The scales arrive in the natural [rows, K/block] byte layout; the producer warp
 // gathers, per stage, each row's scale words and writes them where
 // tcgen05.cp.32x128b.warpx4 expects them: for every 128 rows and word w, the word of row
@@ -27,7 +30,7 @@ namespace {
 // column r / 32 of the word's 4-column group (8 columns for the 256 B rows).
 //   tensor memory: columns [0, 256) fp32 accumulator, then the A scale groups (4 columns
 //   per word and stage), then the B scale groups (8 columns per word and stage).
-enum { kMxfp8 = 0, kNvfp4 = 1 };
+enum { kMxfp8 = 0, kNvfp4 = 1, kMxfp4 = 2 };
 
 // A TMA tile store with an L2 cache policy (createpolicy), for an output streamed once that
 // should not push the operands every wave re-reads out of L2.
@@ -57,11 +60,11 @@ constexpr int kBsEpiBuf = 32 * 64;  // per epilogue warp: 32 rows x 64 bytes (64
 template <int FMT, int S = 3>
 struct BlockScaled {
   static constexpr int STAGES = S;
-  static constexpr int WORDS = FMT == kMxfp8 ? 1 : 4;       // scale words per row per stage
+  static constexpr int WORDS = FMT == kMxfp8 ? 1 : FMT == kMxfp4 ? 2 : 4;  // scale words per row per stage
   static constexpr int K_STAGE = FMT == kMxfp8 ? 128 : 256;  // K elements per stage
   static constexpr int BK = 128;                             // code bytes per row per stage
   static constexpr int UKB = 32;                             // code bytes per instruction
-  static constexpr int SF_BLOCK = FMT == kMxfp8 ? 32 : 16;   // K elements per scale
+  static constexpr int SF_BLOCK = FMT == kNvfp4 ? 16 : 32;   // K elements per scale
   static constexpr int A_STAGE = BM * BK;                    // 16 KB
   static constexpr int B_STAGE = BN * BK;                    // 32 KB
   static constexpr int SFA_STAGE = BM * 4 * WORDS;
@@ -571,7 +574,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
       // One thread issuing all five fell behind the MMAs.
       if (lane == 0) {
         const uint32_t full0 = mapa_shared(&full[0], 0);
-        const int wrow = p.k_dim / (4 * F::SF_BLOCK);  // atoms per 128-row tile
+        // atoms per 128-row tile.  MXFP4's atoms are planes of a 3-D tensor instead, one per row
+        // tile: a contraction that ends inside a stage then reads zeros, not the next tile's scales
+        // (whose 0xFF would make NaN of the zero codes past the end)
+        const int wrow = FMT == kMxfp4 ? 0 : p.k_dim / (4 * F::SF_BLOCK);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -586,9 +592,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
             const uint32_t bar = full0 + uint32_t(stage) * 8u;
             uint8_t *slot = sSF + stage * F::SF_SLOT;
             const int w0 = kb * F::WORDS;
-            tma_load_2d_pair(&tmSA, bar, slot, 0, (2 * tm + int(rank)) * wrow + w0);
-            tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, 2 * tn * wrow + w0);
-            tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, (2 * tn + 1) * wrow + w0);
+            if constexpr (FMT == kMxfp4) {
+              tma_load_3d_pair(&tmSA, bar, slot, 0, w0, 2 * tm + int(rank));
+              tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, w0, 2 * tn);
+              tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, w0, 2 * tn + 1);
+            } else {
+              tma_load_2d_pair(&tmSA, bar, slot, 0, (2 * tm + int(rank)) * wrow + w0);
+              tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, 2 * tn * wrow + w0);
+              tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, (2 * tn + 1) * wrow + w0);
+            }
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -905,6 +917,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
               if (FMT == kMxfp8)
                 mma_mxf8_block_scale_pair(tmem_base, ad, bd, idesc_mxf8_e4m3(F::BMP, BN, uint32_t(k)), sfa_t, sfb_t,
                                           acc);
+              else if (FMT == kMxfp4)
+                mma_mxf4_block_scale_pair(tmem_base, ad, bd, idesc_mxf4_e2m1(F::BMP, BN, 2u * uint32_t(k & 1)),
+                                          sfa_t + 4 * (k >> 1), sfb_t + 8 * (k >> 1), acc);
               else
                 mma_nvf4_block_scale_pair(tmem_base, ad, bd, idesc_nvf4_e2m1(F::BMP, BN), sfa_t + 4 * k,
                                           sfb_t + 8 * k, acc);
@@ -1024,8 +1039,10 @@ gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, c
   static std::atomic<uint64_t> configured{0};
   if (gtp_status e = configure(kernel, F::SMEM_TOTAL, configured, dev.device)) return e;
   return gtp::launch_overlapped(kernel, grid, F::THREADS, F::SMEM_TOTAL, st,
-                                FMT == kMxfp8 ? "gemm_mxfp8_pair" : "gemm_nvfp4_pair", a, b, d, sa, sb, As, Bs,
-                                a_amax, b_amax, p);
+                                FMT == kMxfp8   ? "gemm_mxfp8_pair"
+                                : FMT == kMxfp4 ? "gemm_mxfp4_pair"
+                                                : "gemm_nvfp4_pair",
+                                a, b, d, sa, sb, As, Bs, a_amax, b_amax, p);
 }
 
 // The CTA pair unless the output has at most 128 rows (half of every pair tile would be
@@ -1132,6 +1149,42 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
     if (p.k_blocks / p.splits <= 16)
       return launch_blockscaled<FMT, EPI, 4>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
   return launch_blockscaled<FMT, EPI, 3>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
+}
+
+// The MXFP4 products: any contraction length (code rows hold whole blocks of 32, zero past the end;
+// TMA reads zeros beyond them, codes and scales alike, up to the stage's 256).
+template <int EPI>
+gtp_status run_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, const uint8_t *Bs, void *D, int64_t m_dim,
+                     int64_t n_dim, int64_t k_dim, bool allow_split, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  using F = BlockScaledPair<kMxfp4, 5, true, true>;
+  constexpr CU kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, kU32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  constexpr CUtensorMapSwizzle kSW64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  const int64_t blocks = (k_dim + 31) / 32, row_bytes = 16 * blocks, words = (blocks + 3) / 4;
+  CUtensorMap a, b, d, sa, sb;
+  if (gtp_status s = gtp::encode_tmap_2d(&a, kU8, Aq, row_bytes, m_dim, row_bytes, F::BK, F::BMC, kSW128)) return s;
+  if (gtp_status s = gtp::encode_tmap_2d(&b, kU8, Bq, row_bytes, n_dim, row_bytes, F::BK, F::BNC, kSW128)) return s;
+  if (gtp_status s = gtp::encode_tmap_3d(&sa, kU32, As, 128, words, (m_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
+    return s;
+  if (gtp_status s = gtp::encode_tmap_3d(&sb, kU32, Bs, 128, words, (n_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
+    return s;
+  if (gtp_status s = EPI == kStoreBf16 ? gtp::encode_tmap_2d(&d, kBF16, D, n_dim, m_dim, n_dim * 2, 32, 32, kSW64)
+                                       : gtp::encode_tmap_2d(&d, kF32, D, n_dim, m_dim, n_dim * 4, 16, 32, kSW64))
+    return s;
+  Problem p;
+  p.m_dim = int(m_dim);
+  p.n_dim = int(n_dim);
+  p.k_dim = int(k_dim);
+  p.tiles_m = int((m_dim + F::BMP - 1) / F::BMP);
+  p.tiles_n = int((n_dim + BN - 1) / BN);
+  p.k_blocks = int((k_dim + F::K_STAGE - 1) / F::K_STAGE);
+  const int tiles = p.tiles_m * p.tiles_n, pairs = dev.sm_count / 2;
+  p.splits = allow_split ? choose_splits(tiles, p.k_blocks, pairs) : 1;
+  p.num_units = tiles * p.splits;
+  p.group_m = 2;
+  finalize_problem(p);
+  const int grid = 2 * std::min(p.num_units, pairs);
+  return launch_blockscaled_pair<kMxfp4, EPI, 5, true, true>(a, b, d, sa, sb, As, Bs, nullptr, nullptr, p, grid, dev,
+                                                             st);
 }
 
 template <int EPI>
@@ -1296,6 +1349,73 @@ extern "C" gtp_status gtp_linear_fprop_mxfp8_tiled(const uint8_t *Xq, const uint
   if (K == 0) return gtp::launch_zero_bytes(Y, M * N * 2, st, dev.sm_count);
   return run_blockscaled<kMxfp8, kStoreBf16>(Xq, Xs_tiled, Wq, Ws_tiled, nullptr, nullptr, Y, M, N, K, false, dev, st,
                                              true);
+}
+
+namespace {
+// Checks of the MXFP4 products: any contraction, everything 16-byte aligned, outputs apart from inputs.
+gtp_status check_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, const uint8_t *Bs, const void *D,
+                       int64_t m_dim, int64_t n_dim, int64_t k_dim, int out_bytes) {
+  if (gtp_status s = check_mxfp8(Aq, As, Bq, Bs, D, m_dim, n_dim, k_dim, out_bytes, 1)) return s;
+  if (m_dim == 0 || n_dim == 0 || k_dim == 0) return GTP_OK;
+  if (!gtp::aligned16(As) || !gtp::aligned16(Bs))
+    return gtp::fail(GTP_E_ALIGN, "tiled scale pointers must be 16-byte aligned");
+  // units and the output's elements are counted in 31 bits and 64 bits
+  if ((m_dim + 255) / 256 * ((n_dim + 255) / 256) > (int64_t(1) << 27))
+    return gtp::fail(GTP_E_SHAPE, "more than 2^27 output tiles");
+  const int64_t blocks = (k_dim + 31) / 32, words = (blocks + 3) / 4;
+  const gtp::ByteRange out = gtp::byte_range(D, m_dim * n_dim * out_bytes);
+  const gtp::ByteRange in[4] = {gtp::byte_range(Aq, m_dim * blocks * 16), gtp::byte_range(Bq, n_dim * blocks * 16),
+                                gtp::byte_range(As, (m_dim + 127) / 128 * words * 512),
+                                gtp::byte_range(Bs, (n_dim + 127) / 128 * words * 512)};
+  for (const gtp::ByteRange &r : in)
+    if (gtp::overlap(out, r)) return gtp::fail(GTP_E_ARG, "the output overlaps an input");
+  return GTP_OK;
+}
+
+gtp_status store_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, const uint8_t *Bs, void *D,
+                       int64_t m_dim, int64_t n_dim, int64_t k_dim, gtp_stream stream) {
+  if (gtp_status s = check_mxfp4(Aq, As, Bq, Bs, D, m_dim, n_dim, k_dim, 2)) return s;
+  if (m_dim == 0 || n_dim == 0) return GTP_OK;
+  gtp::DeviceInfo dev;
+  if (gtp_status s = gtp::require_sm103(&dev)) return s;
+  cudaStream_t st = gtp::as_stream(stream);
+  if (k_dim == 0) return gtp::launch_zero_bytes(D, m_dim * n_dim * 2, st, dev.sm_count);
+  return run_mxfp4<kStoreBf16>(Aq, As, Bq, Bs, D, m_dim, n_dim, k_dim, false, dev, st);
+}
+}  // namespace
+
+extern "C" gtp_status gtp_linear_fprop_mxfp4(const uint8_t *Xq, const uint8_t *Xs, const uint8_t *Wq,
+                                             const uint8_t *Ws, void *Y, int64_t M, int64_t N, int64_t K,
+                                             gtp_stream stream) {
+  gtp::clear_error();
+  return store_mxfp4(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+}
+
+extern "C" gtp_status gtp_linear_dgrad_mxfp4(const uint8_t *dYq, const uint8_t *dYs, const uint8_t *Wtq,
+                                             const uint8_t *Wts, void *dX, int64_t M, int64_t N, int64_t K,
+                                             gtp_stream stream) {
+  gtp::clear_error();
+  return store_mxfp4(dYq, dYs, Wtq, Wts, dX, M, K, N, stream);
+}
+
+extern "C" gtp_status gtp_linear_wgrad_accum_mxfp4(const uint8_t *dYtq, const uint8_t *dYts, const uint8_t *Xtq,
+                                                   const uint8_t *Xts, float *grad_data, int64_t grad_offset,
+                                                   int64_t grad_numel_total, int64_t M, int64_t N, int64_t K,
+                                                   gtp_stream stream) {
+  gtp::clear_error();
+  if (grad_offset < 0 || grad_numel_total < 0) return gtp::fail(GTP_E_ARG, "negative offset or size");
+  if (M < 0 || N < 0 || K < 0) return gtp::fail(GTP_E_ARG, "negative dimension");
+  if (N > kMaxDim || K > kMaxDim) return gtp::fail(GTP_E_SHAPE, "dimension above 2^30");
+  if (N * K > grad_numel_total - grad_offset)
+    return gtp::fail(GTP_E_RANGE, "view [%lld, +%lld) exceeds the grad buffer (%lld)", (long long)grad_offset,
+                     (long long)(N * K), (long long)grad_numel_total);
+  if (grad_offset % 4) return gtp::fail(GTP_E_ALIGN, "grad_offset must be a multiple of 4 elements");
+  float *view = grad_data ? grad_data + grad_offset : nullptr;
+  if (gtp_status s = check_mxfp4(dYtq, dYts, Xtq, Xts, view, N, K, M, 4)) return s;
+  if (M == 0 || N == 0 || K == 0) return GTP_OK;
+  gtp::DeviceInfo dev;
+  if (gtp_status s = gtp::require_sm103(&dev)) return s;
+  return run_mxfp4<kReduceAddF32>(dYtq, dYts, Xtq, Xts, view, N, K, M, true, dev, gtp::as_stream(stream));
 }
 
 namespace gtp {
