@@ -36,44 +36,129 @@ struct DropArgs {
   gtp::RngArgs rng;
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// One thread per group of eight columns.
-template <typename TI, typename TO, bool RES>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a, int64_t groups,
-                                                           int64_t total) {
-  gtp::ptx::allow_dependents();
-  gtp::ptx::wait_prior_grid();
-  const uint64_t offset = gtp::rng_offset(a.rng);
-  const int64_t stride = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t row = i / groups, g = i - row * groups;
-    const uint4 d = gtp::philox(a.rng.k0, a.rng.k1, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
-                                uint32_t(offset), uint32_t(offset >> 32));
-    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-    const TI *x = static_cast<const TI *>(a.x) + row * a.x_ld;
-    const TO *res = static_cast<const TO *>(a.residual) + (RES ? row * a.residual_ld : 0);
-    TO *out = static_cast<TO *>(a.out) + row * a.out_ld;
+// Eight consecutive elements as fp32, by 16-byte vectors or, up to `n` of them, one by one.
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int n, float (&x)[8]) {
+  if (VEC) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t j = 8 * g + k;
-      if (j < a.cols) {
-        const uint32_t r = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-        float v = r >= a.threshold ? to_f32(x[j]) * a.scale : 0.f;
-        if (RES) v += to_f32(res[j]);
-        out[j] = TO(v);
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k] : 0.f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, float (&x)[8]) {
+  if (VEC) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);  // bf16 -> fp32 is exact
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k]) : 0.f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float *p, int n, const float (&x)[8]) {
+  if (VEC) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = x[k];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, int n, const float (&x)[8]) {
+  if (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = __float2bfloat16_rn(x[k]);
+  }
+}
+
+// A thread owns one group of eight columns (one generator call) in ROWS rows at a time, whose loads
+// are in flight together; blocks are blockDim.x groups wide and step down the rows.
+constexpr int kRows = 2;
+
+template <typename TI, typename TO, bool RES, bool VEC>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
+  gtp::ptx::allow_dependents();
+  const int64_t g = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t left = a.cols - 8 * g;
+  gtp::ptx::wait_prior_grid();
+  if (left <= 0) return;
+  const int n = VEC ? 8 : int(min(left, int64_t(8)));
+  const uint64_t offset = gtp::rng_offset(a.rng);
+  const int64_t step = int64_t(gridDim.y) * blockDim.y;
+  for (int64_t r0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r0 < a.rows; r0 += kRows * step) {
+    float x[kRows][8], res[kRows][8];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t row = r0 + i * step;
+      if (row < a.rows) {
+        load8<VEC>(static_cast<const TI *>(a.x) + row * a.x_ld + 8 * g, n, x[i]);
+        if (RES) load8<VEC>(static_cast<const TO *>(a.residual) + row * a.residual_ld + 8 * g, n, res[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t row = r0 + i * step;
+      if (row < a.rows) {
+        const uint4 d = gtp::philox(a.rng.k0, a.rng.k1, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
+                                    uint32_t(offset), uint32_t(offset >> 32));
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t r = k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu;
+          y[k] = r >= a.threshold ? x[i][k] * a.scale : 0.f;
+          if (RES) y[k] += res[i][k];
+        }
+        store8<VEC>(static_cast<TO *>(a.out) + row * a.out_ld + 8 * g, n, y);
       }
     }
   }
 }
 
+template <typename TI, typename TO, bool RES>
+gtp_status launch(const DropArgs &a, bool vec, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  const int64_t groups = (a.cols + 7) / 8;
+  int tx = 1;
+  while (tx < kThreads && tx < groups) tx *= 2;
+  const dim3 block(tx, kThreads / tx);
+  const int64_t gx = (groups + tx - 1) / tx, want = (a.rows + block.y * kRows - 1) / (block.y * kRows);
+  const int64_t fill = (int64_t(dev.sm_count) * 8 + gx - 1) / gx;  // a grid that fills the SMs
+  const dim3 grid(unsigned(gx), unsigned(std::max<int64_t>(1, std::min<int64_t>({want, fill, 65535}))));
+  return vec ? gtp::launch_overlapped(dropout_kernel<TI, TO, RES, true>, grid, block, 0, st, "dropout", a)
+             : gtp::launch_overlapped(dropout_kernel<TI, TO, RES, false>, grid, block, 0, st, "dropout", a);
+}
+
 template <typename TI, typename TO>
 gtp_status launch(const DropArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  const int64_t groups = (a.cols + 7) / 8, total = a.rows * groups;
-  const int grid = int(std::min<int64_t>((total + kThreads - 1) / kThreads, int64_t(dev.sm_count) * 8));
-  if (a.residual) return gtp::launch_overlapped(dropout_kernel<TI, TO, true>, grid, kThreads, 0, st, "dropout_add", a, groups, total);
-  return gtp::launch_overlapped(dropout_kernel<TI, TO, false>, grid, kThreads, 0, st, "dropout", a, groups, total);
+  // vectors where every row of every array starts on 16 bytes and holds whole groups
+  const auto whole = [&](const void *p, int64_t ld, size_t es) {
+    return gtp::aligned16(p) && (a.rows == 1 || ld * int64_t(es) % 16 == 0);
+  };
+  const bool vec = a.cols % 8 == 0 && whole(a.x, a.x_ld, sizeof(TI)) && whole(a.out, a.out_ld, sizeof(TO)) &&
+                   (!a.residual || whole(a.residual, a.residual_ld, sizeof(TO)));
+  return a.residual ? launch<TI, TO, true>(a, vec, dev, st) : launch<TI, TO, false>(a, vec, dev, st);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;

@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "device.h"
 #include "mx4_block.cuh"
@@ -26,75 +27,236 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+// A tile of 128 x 128 source elements makes exactly one 512-byte atom of scale bytes in each view, so
+// a block reads its tile once and writes both views: codes in 64-byte runs, scales as one atom each.
+//
+// Rows: a thread takes 16 consecutive elements of 4 rows (32 apart), two lanes a block of 32.  On the
+// way the tile goes to shared memory; then a thread takes 32 rows of two adjacent columns (bf16, one
+// 32-bit word a row) or of one column twice (fp32), so a column's block needs no shuffle.  The words
+// of a row are rotated by 8 per 32 rows: the four row blocks of a column, which neighbouring lanes
+// hold so that they write its 64 bytes together, then lie in different banks.
+constexpr int kTile = 128;
 
-// One thread per block of a view: element k of view row r is src[r * row_stride + k * elem_stride].
-template <typename T, bool STOCH>
-__global__ void __launch_bounds__(kThreads)
-    mx4_view_kernel(const T *__restrict__ src, int64_t row_stride, int64_t elem_stride, int64_t rows, int64_t len,
-                    uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int64_t blocks, int64_t words,
-                    int64_t total, uint32_t stream, const gtp::RngArgs rng) {
-  gtp::ptx::allow_dependents();
-  gtp::ptx::wait_prior_grid();
-  const uint64_t offset = STOCH ? gtp::rng_offset(rng) : 0;
-  const int64_t stride = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / (4 * words), b = i - r * (4 * words);
-    uint32_t byte = 0;
-    if (r < rows && b < blocks) {
-      float x[4][8];
-      uint32_t amax = 0;
+template <typename T>
+struct Tile {
+  static constexpr int PER = 4 / sizeof(T);            // elements of a 32-bit word
+  static constexpr int WORDS = kTile / PER;            // words of a tile row
+  static constexpr int THREAD_WORDS = 16 / PER;        // words of a thread's 16 elements
+  static constexpr int BYTES = kTile * WORDS * 4;
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int64_t e = 32 * b + k;
-        x[k >> 3][k & 7] = e < len ? to_f32(src[r * row_stride + e * elem_stride]) : 0.f;
-        amax = max(amax, __float_as_uint(x[k >> 3][k & 7]) & 0x7FFFFFFFu);
-      }
-      byte = gtp::mx4::scale_byte<STOCH>(amax);
-      const float inv = gtp::mx4::inv_scale(byte);
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (byte != gtp::mx4::kNanScale) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 d = make_uint4(0, 0, 0, 0);
-          if (STOCH)
-            d = gtp::philox(rng.k0, rng.k1, uint32_t(2 * b + h) | (stream << 30), uint32_t(r), uint32_t(offset),
-                            uint32_t(offset >> 32));
-          w[2 * h] = STOCH ? gtp::mx4::encode8_stochastic(x[2 * h], inv, d.x, d.y) : gtp::mx4::encode8(x[2 * h], inv);
-          w[2 * h + 1] =
-              STOCH ? gtp::mx4::encode8_stochastic(x[2 * h + 1], inv, d.z, d.w) : gtp::mx4::encode8(x[2 * h + 1], inv);
-        }
-      }
-      *reinterpret_cast<uint4 *>(codes + (r * blocks + b) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    scales[((r >> 7) * words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)] = uint8_t(byte);
+  for (int i = 0; i < N / 4; ++i) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
   }
 }
 
-// One thread per block of a view, back to values: exact in bf16 and fp32 (one mantissa bit; the
-// smallest magnitude, 2^-128, is a bf16 subnormal).
+// The word of up to two elements, element by element, for a ragged or unaligned source.
+__device__ __forceinline__ uint32_t word_of(const float *p, int n) { return n > 0 ? __float_as_uint(*p) : 0u; }
+__device__ __forceinline__ uint32_t word_of(const __nv_bfloat16 *p, int n) {
+  const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+  return (n > 0 ? uint32_t(q[0]) : 0u) | (n > 1 ? uint32_t(q[1]) << 16 : 0u);
+}
+
+// The largest magnitude of a word's elements so far: fp32 one 32-bit maximum, bf16 two 16-bit ones.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    mx4_values_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t len,
-                      T *__restrict__ out, int64_t blocks, int64_t words, int64_t total) {
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t max_magnitude<float>(uint32_t m, uint32_t w) {
+  return max(m, w & 0x7FFFFFFFu);
+}
+template <>
+__device__ __forceinline__ uint32_t max_magnitude<__nv_bfloat16>(uint32_t m, uint32_t w) {
+  return __vmaxu2(m, w & 0x7FFF7FFFu);
+}
+
+__device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// One block of 32 values under `byte` to 16 bytes of codes; view row r, block b (for the draws).
+template <bool STOCH, int N>
+__device__ __forceinline__ void encode_run(const float (&x)[N], uint32_t byte, uint32_t (&w)[N / 8], uint32_t stream,
+                                           uint32_t r, uint32_t first_group, const gtp::RngArgs &rng, uint64_t offset) {
+  const float inv = gtp::mx4::inv_scale(byte);
+  const uint32_t keep = byte == gtp::mx4::kNanScale ? 0u : 0xFFFFFFFFu;  // a bad block's codes are 0
+#pragma unroll
+  for (int h = 0; h < N / 16; ++h) {
+    uint4 d = make_uint4(0, 0, 0, 0);
+    if (STOCH)
+      d = gtp::philox(rng.k0, rng.k1, (first_group + h) | (stream << 30), r, uint32_t(offset), uint32_t(offset >> 32));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = x[16 * h + 8 * q + k];
+      w[2 * h + q] = keep & (STOCH ? gtp::mx4::encode8_stochastic(v, inv, q ? d.z : d.x, q ? d.w : d.y)
+                                   : gtp::mx4::encode8(v, inv));
+    }
+  }
+}
+
+struct ViewArgs {
+  uint8_t *codes, *scales;
+  int64_t pitch;  // bytes of a row of codes
+  int64_t words;  // atoms of a 128-row tile
+};
+
+struct TileArgs {
+  const void *src;
+  int64_t rows, cols, ld;
+  int64_t tiles_n;
+  ViewArgs row, col;
+  int32_t vec;  // rows on 16 bytes
+  gtp::RngArgs rng;
+};
+
+template <typename T, bool STOCH, bool ROW, bool COL>
+__global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
+  using F = Tile<T>;
+  constexpr int TW = F::THREAD_WORDS;
+  extern __shared__ __align__(16) uint32_t tile[];  // COL: [128][WORDS]
+  __shared__ __align__(16) uint8_t atom[2][512];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  const int64_t stride = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / blocks, b = i - r * blocks;
-    const uint32_t byte = scales[((r >> 7) * words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
+  const uint64_t offset = STOCH ? gtp::rng_offset(a.rng) : 0;
+  const int tid = threadIdx.x;
+  const int64_t tm = blockIdx.x / a.tiles_n, tn = blockIdx.x - tm * a.tiles_n;
+  const int seg = tid & 7, r32 = tid >> 3;  // this thread's 16 columns, and its row of every 32
+  const int64_t c0 = kTile * tn + 16 * seg;
+  const int nc = int(max(int64_t(0), min(int64_t(16), a.cols - c0)));  // its columns inside the matrix
+  uint32_t w[4][TW];
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int64_t r = kTile * tm + 32 * it + r32;
+    const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
+    if (r >= a.rows) {
+#pragma unroll
+      for (int i = 0; i < TW; ++i) w[it][i] = 0;
+    } else if (a.vec && nc == 16) {
+      load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
+    }
+  }
+  if (COL) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      uint32_t *t = tile + (32 * it + r32) * F::WORDS;
+#pragma unroll
+      for (int i = 0; i < TW / 4; ++i)
+        *reinterpret_cast<uint4 *>(t + ((seg * TW + 4 * i + 8 * it) & (F::WORDS - 1))) =
+            make_uint4(w[it][4 * i], w[it][4 * i + 1], w[it][4 * i + 2], w[it][4 * i + 3]);
+    }
+  }
+  if (ROW) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int64_t r = kTile * tm + 32 * it + r32;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < TW; ++i) m = max_magnitude<T>(m, w[it][i]);
+      if (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16) << 16;
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      const uint32_t byte = gtp::mx4::scale_byte<STOCH>(m);
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        x[k] = sizeof(T) == 4 ? __uint_as_float(w[it][k % TW])
+                              : (k & 1 ? high_f32(w[it][k >> 1]) : low_f32(w[it][k >> 1]));
+      uint32_t codes[2];
+      encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundRow, uint32_t(r), uint32_t(8 * tn + seg), a.rng, offset);
+      const bool in = r < a.rows && c0 < 2 * a.row.pitch;  // the block exists (two codes a byte)
+      if (in) *reinterpret_cast<uint2 *>(a.row.codes + r * a.row.pitch + c0 / 2) = make_uint2(codes[0], codes[1]);
+      if ((seg & 1) == 0) atom[0][16 * r32 + 4 * it + (seg >> 1)] = uint8_t(byte);
+    }
+  }
+  __syncthreads();
+  if (COL) {
+    // lanes 4 p + rb: column pair (bf16) or column (fp32) p of the warp's eight, row block rb
+    const int rb = tid & 3;
+#pragma unroll
+    for (int u = 0; u < 2 / F::PER; ++u) {
+      const int p = (tid >> 2) + 64 * u;  // word of the tile row
+      const uint32_t *t = tile + 32 * rb * F::WORDS + ((p + 8 * rb) & (F::WORDS - 1));
+      uint32_t v[32], m = 0;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        v[k] = t[k * F::WORDS];
+        m = max_magnitude<T>(m, v[k]);
+      }
+#pragma unroll
+      for (int e = 0; e < F::PER; ++e) {
+        const int c = F::PER * p + e;
+        const int64_t gc = kTile * tn + c;
+        const uint32_t byte = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : e ? m & 0xFFFF0000u : m << 16);
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = F::PER == 1 ? __uint_as_float(v[k]) : e ? high_f32(v[k]) : low_f32(v[k]);
+        uint32_t codes[4];
+        encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundCol, uint32_t(gc), uint32_t(8 * tm + 2 * rb), a.rng, offset);
+        const int64_t b = 4 * tm + rb;
+        if (gc < a.cols && 16 * b < a.col.pitch)
+          *reinterpret_cast<uint4 *>(a.col.codes + gc * a.col.pitch + 16 * b) =
+              make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        atom[1][16 * (c & 31) + 4 * (c >> 5) + rb] = uint8_t(byte);
+      }
+    }
+    __syncthreads();
+  }
+  // the atoms whole: rows, columns and blocks outside the matrix hold zeros, whose byte is 0
+  if (ROW && tid < 32)
+    reinterpret_cast<uint4 *>(a.row.scales + (tm * a.row.words + tn) * 512)[tid] = reinterpret_cast<uint4 *>(atom[0])[tid];
+  if (COL && tid >= 32 && tid < 64)
+    reinterpret_cast<uint4 *>(a.col.scales + (tn * a.col.words + tm) * 512)[tid - 32] =
+        reinterpret_cast<uint4 *>(atom[1])[tid - 32];
+}
+
+// Eight values a thread, back from a view: exact in bf16 and fp32 below 2^128 (one mantissa bit; the
+// smallest magnitude, 2^-128, is a bf16 subnormal).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    mx4_values_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t len,
+                      T *__restrict__ out, int64_t blocks, int64_t words) {
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const int64_t g = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, b = g >> 2;
+  const int64_t left = len - 8 * g;
+  if (left <= 0) return;
+  const uint8_t *sf = scales + (b >> 2) * 512 + (b & 3);
+  for (int64_t r = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r < rows; r += int64_t(gridDim.y) * blockDim.y) {
+    const uint32_t byte = __ldg(sf + (r >> 7) * words * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
     const float scale = byte == gtp::mx4::kNanScale ? __uint_as_float(0x7FC00000u)
                         : byte == 0                 ? 0x1p-127f
                                                     : __uint_as_float(byte << 23);
-    const uint4 v = *reinterpret_cast<const uint4 *>(codes + (r * blocks + b) * 16);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(codes + r * blocks * 16) + g);
+    float x[8];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const uint32_t c = (w[k >> 3] >> (4 * (k & 7))) & 15u, m = c & 7u;
-      const float mag = m < 4 ? 0.5f * float(m) : m < 6 ? float(m) - 2.f : 2.f * float(m) - 8.f;
-      const float y = (c & 8u ? -mag : mag) * scale;
-      if (32 * b + k < len) out[r * len + 32 * b + k] = T(y);
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((w >> (8 * i)) & 0xFFu), __NV_E2M1);
+      const float2 f = __half22float2(__half2(h));
+      x[2 * i] = f.x * scale;
+      x[2 * i + 1] = f.y * scale;
+    }
+    T *o = out + r * len + 8 * g;
+    if constexpr (VEC && sizeof(T) == 4) {
+      __stcs(reinterpret_cast<float4 *>(o), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4 *>(o) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    } else if constexpr (VEC) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        v[i] = *reinterpret_cast<const uint32_t *>(&p);
+      }
+      __stcs(reinterpret_cast<uint4 *>(o), make_uint4(v[0], v[1], v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) o[k] = T(x[k]);
     }
   }
 }
@@ -108,34 +270,27 @@ struct View {
   int64_t scale_bytes() const { return (rows + 127) / 128 * words() * 512; }
 };
 
-int grid_for(int64_t threads, int sm_count) {
-  return int(std::max<int64_t>(1, std::min<int64_t>((threads + kThreads - 1) / kThreads, int64_t(sm_count) * 8)));
+template <typename T, bool STOCH, bool ROW, bool COL>
+gtp_status launch_tiles(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  constexpr int smem = COL ? Tile<T>::BYTES : 0;
+  constexpr auto kernel = mx4_tile_kernel<T, STOCH, ROW, COL>;
+  if (smem > 48 * 1024) {
+    static std::atomic<uint64_t> configured{0};
+    const uint64_t bit = uint64_t(1) << (dev.device & 63);
+    if (!(configured.load() & bit)) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      configured.fetch_or(bit);
+    }
+  }
+  return gtp::launch_overlapped(kernel, dim3(unsigned(tiles)), kThreads, smem, st, "mxfp4_quantize", a);
 }
 
-template <typename T>
-gtp_status launch_view(const T *src, int64_t row_stride, int64_t elem_stride, const View &v, uint32_t stream_id,
-                       const gtp_rng *rng, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  const int64_t total = (v.rows + 127) / 128 * 128 * v.words() * 4;
-  const int grid = grid_for(total, dev.sm_count);
-  const gtp::RngArgs a = gtp::rng_args(rng);
-  if (rng)
-    return gtp::launch_overlapped(mx4_view_kernel<T, true>, grid, kThreads, 0, st, "mxfp4_quantize", src, row_stride,
-                                  elem_stride, v.rows, v.len, v.codes, v.scales, v.blocks(), v.words(), total,
-                                  stream_id, a);
-  return gtp::launch_overlapped(mx4_view_kernel<T, false>, grid, kThreads, 0, st, "mxfp4_quantize", src, row_stride,
-                                elem_stride, v.rows, v.len, v.codes, v.scales, v.blocks(), v.words(), total,
-                                stream_id, a);
-}
-
-template <typename T>
-gtp_status launch_views(const void *src, int64_t ld, const View &row, const View &col, const gtp_rng *rng,
-                        const gtp::DeviceInfo &dev, cudaStream_t st) {
-  auto *s = static_cast<const T *>(src);
-  if (row.codes)
-    if (gtp_status r = launch_view(s, ld, int64_t(1), row, gtp::kStreamRoundRow, rng, dev, st)) return r;
-  if (col.codes)
-    if (gtp_status r = launch_view(s, int64_t(1), ld, col, gtp::kStreamRoundCol, rng, dev, st)) return r;
-  return GTP_OK;
+template <typename T, bool STOCH>
+gtp_status launch_views(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  if (!a.col.codes) return launch_tiles<T, STOCH, true, false>(a, tiles, dev, st);
+  if (!a.row.codes) return launch_tiles<T, STOCH, false, true>(a, tiles, dev, st);
+  return launch_tiles<T, STOCH, true, true>(a, tiles, dev, st);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
@@ -183,8 +338,18 @@ extern "C" gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int6
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
   cudaStream_t st = gtp::as_stream(stream);
-  return src_dt == GTP_F32 ? launch_views<float>(src, src_ld, row, col, rng, dev, st)
-                           : launch_views<__nv_bfloat16>(src, src_ld, row, col, rng, dev, st);
+  TileArgs a = {};
+  a.src = src;
+  a.rows = rows, a.cols = cols, a.ld = rows > 1 ? src_ld : 0;
+  a.tiles_n = (cols + kTile - 1) / kTile;
+  a.row = {row_codes, row_scales, row.blocks() * 16, row.words()};
+  a.col = {col_codes, col_scales, col.blocks() * 16, col.words()};
+  a.vec = gtp::aligned16(src) && a.ld * es % 16 == 0;
+  a.rng = gtp::rng_args(rng);
+  const int64_t tiles = (rows + kTile - 1) / kTile * a.tiles_n;
+  if (tiles > INT32_MAX) return gtp::fail(GTP_E_SHAPE, "more than 2^31 - 1 tiles of 128 x 128");
+  if (src_dt == GTP_F32) return rng ? launch_views<float, true>(a, tiles, dev, st) : launch_views<float, false>(a, tiles, dev, st);
+  return rng ? launch_views<__nv_bfloat16, true>(a, tiles, dev, st) : launch_views<__nv_bfloat16, false>(a, tiles, dev, st);
 }
 
 extern "C" gtp_status gtp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
@@ -208,12 +373,22 @@ extern "C" gtp_status gtp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *
     return gtp::fail(GTP_E_ARG, "out overlaps the codes or the scales");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
-  const int64_t total = rows * v.blocks();
-  const int grid = grid_for(total, dev.sm_count);
   cudaStream_t st = gtp::as_stream(stream);
+  const int64_t groups = (cols + 7) / 8;
+  int tx = 4;  // a block's four words of codes side by side
+  while (tx < kThreads && tx < groups) tx *= 2;
+  const dim3 block(tx, kThreads / tx);
+  const int64_t gx = (groups + tx - 1) / tx, want = (rows + block.y - 1) / block.y;
+  const int64_t fill = (int64_t(dev.sm_count) * 16 + gx - 1) / gx;
+  const dim3 grid(unsigned(gx), unsigned(std::max<int64_t>(1, std::min<int64_t>({want, fill, 65535}))));
+  const bool vec = cols % 8 == 0 && gtp::aligned16(out);
+  const auto go = [&](auto *kernel, auto *o) {
+    return gtp::launch_overlapped(kernel, grid, block, 0, st, "mxfp4_dequantize", codes, scales, rows, cols, o,
+                                  v.blocks(), v.words());
+  };
   if (out_dt == GTP_F32)
-    return gtp::launch_overlapped(mx4_values_kernel<float>, grid, kThreads, 0, st, "mxfp4_dequantize", codes, scales,
-                                  rows, cols, static_cast<float *>(out), v.blocks(), v.words(), total);
-  return gtp::launch_overlapped(mx4_values_kernel<__nv_bfloat16>, grid, kThreads, 0, st, "mxfp4_dequantize", codes,
-                                scales, rows, cols, static_cast<__nv_bfloat16 *>(out), v.blocks(), v.words(), total);
+    return vec ? go(mx4_values_kernel<float, true>, static_cast<float *>(out))
+               : go(mx4_values_kernel<float, false>, static_cast<float *>(out));
+  return vec ? go(mx4_values_kernel<__nv_bfloat16, true>, static_cast<__nv_bfloat16 *>(out))
+             : go(mx4_values_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16 *>(out));
 }

@@ -38,7 +38,7 @@ struct RotaryArgs {
   int64_t src_token, src_group, src_head, dst_token, dst_group, dst_head;
   int64_t pos0, tokens_per_position, positions_per_sequence;
   int32_t heads, group_heads, head_dim, half;  // heads: over all groups
-  int32_t interleaved, inverse, positions64;
+  int32_t inverse, positions64, block_tokens, copy;  // copy: the part that keeps its values is written
   float scale;
 };
 
@@ -59,38 +59,157 @@ __device__ __forceinline__ void turn(uint64_t turns, int64_t pos, const RotaryAr
   s *= a.inverse ? -a.scale : a.scale;
 }
 
+// A chunk of a head is 8 pairs: two runs of 8 elements half a rotation apart, or 16 in a row.  With
+// rows on 16 bytes (VEC) a chunk moves in 16-byte vectors, else element by element, a pair a chunk.
+template <typename T>
+struct Run;
+template <>
+struct Run<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float *p) {
+    v[0] = __ldcs(reinterpret_cast<const float4 *>(p));
+    v[1] = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    __stcs(reinterpret_cast<float4 *>(p), v[0]);
+    __stcs(reinterpret_cast<float4 *>(p) + 1, v[1]);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = v[0].x, x[1] = v[0].y, x[2] = v[0].z, x[3] = v[0].w;
+    x[4] = v[1].x, x[5] = v[1].y, x[6] = v[1].z, x[7] = v[1].w;
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    v[0] = make_float4(x[0], x[1], x[2], x[3]);
+    v[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+template <>
+struct Run<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), v); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);  // bf16 -> fp32 is exact
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
 __device__ __forceinline__ float load_f32(const float *p) { return *p; }
 __device__ __forceinline__ float load_f32(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_f32(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// One thread per pair, or per two elements of the part that keeps its values.
-template <typename T>
+struct Head {
+  int64_t src, dst;
+};
+
+__device__ __forceinline__ Head head_of(const RotaryArgs &a, int64_t t, int h) {
+  const int g = h / a.group_heads, gh = h - g * a.group_heads;
+  return {t * a.src_token + g * a.src_group + gh * a.src_head, t * a.dst_token + g * a.dst_group + gh * a.dst_head};
+}
+
+// A block owns a.block_tokens tokens: it forms each (token, pair)'s cosine and sine once, in shared
+// memory, and every head of the token uses them.
+template <typename T, bool VEC, bool IL>
 __global__ void __launch_bounds__(kThreads)
-    rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Turns turns, int64_t total) {
+    rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Turns turns) {
+  extern __shared__ float2 cs[];  // [block_tokens][half]
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  const int slots = (a.head_dim + 1) / 2;
-  const int64_t stride = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t th = i / slots;
-    const int k = int(i - th * slots);
-    const int64_t t = th / a.heads;
-    const int h = int(th - t * a.heads), g = h / a.group_heads, gh = h - g * a.group_heads;
-    const T *s = static_cast<const T *>(a.src) + t * a.src_token + g * a.src_group + gh * a.src_head;
-    T *d = static_cast<T *>(a.dst) + t * a.dst_token + g * a.dst_group + gh * a.dst_head;
-    if (k < a.half) {
-      const int ia = a.interleaved ? 2 * k : k, ib = a.interleaved ? 2 * k + 1 : k + a.half;
-      float c, sn;
-      turn(turns.t[k], position_of(a, t), a, c, sn);
-      const float x = load_f32(s + ia), y = load_f32(s + ib);
-      store_f32(d + ia, x * c - y * sn);
-      store_f32(d + ib, x * sn + y * c);
-    } else if (s != d) {
-      d[2 * k] = s[2 * k];
-      if (2 * k + 1 < a.head_dim) d[2 * k + 1] = s[2 * k + 1];
+  const int64_t t0 = int64_t(blockIdx.x) * a.block_tokens;
+  const int nt = int(min(int64_t(a.block_tokens), a.tokens - t0));
+  for (int i = threadIdx.x; i < nt * a.half; i += kThreads) {
+    const int t = i / a.half, k = i - t * a.half;
+    turn(turns.t[k], position_of(a, t0 + t), a, cs[i].x, cs[i].y);
+  }
+  const T *src = static_cast<const T *>(a.src);
+  T *dst = static_cast<T *>(a.dst);
+  __syncthreads();
+  constexpr int P = VEC ? 8 : 1;
+  const int chunks = a.half / P, units = chunks * a.heads;
+  for (int i = threadIdx.x; i < nt * units; i += kThreads) {
+    const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
+    const Head at = head_of(a, t0 + t, h);
+    const float2 *w = cs + t * a.half + P * c;
+    const int ia = IL ? 2 * P * c : P * c, ib = IL ? ia + P : ia + a.half;
+    if constexpr (VEC) {
+      Run<T> u, v;
+      u.load(src + at.src + ia);
+      v.load(src + at.src + ib);
+      float x[8], y[8];
+      u.get(x);
+      v.get(y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // interleaved: pairs 0-3 of the chunk lie in the first run, 4-7 in the second
+        float &p = IL ? (k < 4 ? x[2 * k] : y[2 * k - 8]) : x[k];
+        float &q = IL ? (k < 4 ? x[2 * k + 1] : y[2 * k - 7]) : y[k];
+        const float2 m = w[k];
+        const float np = p * m.x - q * m.y, nq = p * m.y + q * m.x;
+        p = np;
+        q = nq;
+      }
+      u.set(x);
+      v.set(y);
+      u.store(dst + at.dst + ia);
+      v.store(dst + at.dst + ib);
+    } else {
+      const int ja = IL ? 2 * c : c, jb = IL ? 2 * c + 1 : c + a.half;
+      const float x = load_f32(src + at.src + ja), y = load_f32(src + at.src + jb);
+      const float2 m = w[0];
+      store_f32(dst + at.dst + ja, x * m.x - y * m.y);
+      store_f32(dst + at.dst + jb, x * m.y + y * m.x);
     }
   }
+  // the part of a head that keeps its values; in place there is nothing to do
+  const int rest = a.head_dim - 2 * a.half;
+  if (rest && a.copy) {
+    const int per = VEC ? rest / 8 : rest, all = per * a.heads;
+    for (int i = threadIdx.x; i < nt * all; i += kThreads) {
+      const int t = i / all, r = i - t * all, h = r / per, c = 2 * a.half + P * (r - h * per);
+      const Head at = head_of(a, t0 + t, h);
+      if constexpr (VEC) {
+        Run<T> u;
+        u.load(src + at.src + c);
+        u.store(dst + at.dst + c);
+      } else {
+        dst[at.dst + c] = src[at.src + c];
+      }
+    }
+  }
+}
+
+template <typename T, bool VEC>
+gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStream_t st) {
+  // about two chunks a thread: enough tokens to a block to fill it, few enough to spread a short batch
+  const int64_t units = int64_t(a.heads) * (a.half / (VEC ? 8 : 1));
+  a.block_tokens = int32_t(std::max<int64_t>(1, std::min<int64_t>({2 * kThreads / units, 16, a.tokens})));
+  const unsigned grid = unsigned((a.tokens + a.block_tokens - 1) / a.block_tokens);
+  const size_t smem = size_t(a.block_tokens) * a.half * sizeof(float2);
+  return interleaved ? gtp::launch_overlapped(rotary_kernel<T, VEC, true>, grid, kThreads, smem, st, "rotary", a, turns)
+                     : gtp::launch_overlapped(rotary_kernel<T, VEC, false>, grid, kThreads, smem, st, "rotary", a, turns);
+}
+
+template <typename T>
+gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStream_t st) {
+  // 16-byte vectors where every head starts on 16 bytes and whole runs of 8 elements turn or stay
+  const int64_t es = sizeof(T);
+  bool vec = gtp::aligned16(a.src) && gtp::aligned16(a.dst) && a.half % 8 == 0 && a.head_dim % 8 == 0;
+  for (int64_t s : {a.src_token, a.src_group, a.src_head, a.dst_token, a.dst_group, a.dst_head}) vec = vec && s * es % 16 == 0;
+  return vec ? launch<T, true>(a, turns, interleaved, st) : launch<T, false>(a, turns, interleaved, st);
 }
 
 }  // namespace
@@ -156,8 +275,8 @@ extern "C" gtp_status gtp_rotary(const gtp_rotary_desc *d, gtp_stream stream) {
   if (d->head_dim < 1 || d->head_dim > 65536) return gtp::fail(GTP_E_SHAPE, "head_dim must be 1 to 65536");
   if (d->rot_dim < 2 || d->rot_dim % 2 || d->rot_dim > 2 * kMaxPairs || d->rot_dim > d->head_dim)
     return gtp::fail(GTP_E_SHAPE, "rot_dim must be even, 2 to %d and at most head_dim", 2 * kMaxPairs);
-  if (d->tokens > (int64_t(1) << 32) || int64_t(d->groups) * d->heads > (1 << 20))
-    return gtp::fail(GTP_E_SHAPE, "more than 2^32 tokens or 2^20 heads");
+  if (d->tokens > INT32_MAX || int64_t(d->groups) * d->heads > (1 << 20))
+    return gtp::fail(GTP_E_SHAPE, "more than 2^31 - 1 tokens or 2^20 heads");
   if (!d->turns) return gtp::fail(GTP_E_ARG, "null turns");
   if (!std::isfinite(d->scale)) return gtp::fail(GTP_E_ARG, "scale must be finite");
   if (d->tokens_per_position < 1 || d->positions_per_sequence < 0)
@@ -211,13 +330,15 @@ extern "C" gtp_status gtp_rotary(const gtp_rotary_desc *d, gtp_stream stream) {
   a.heads = d->groups * d->heads;
   a.head_dim = d->head_dim;
   a.half = d->rot_dim / 2;
-  a.interleaved = d->interleaved, a.inverse = d->inverse, a.positions64 = d->positions64;
+  a.inverse = d->inverse, a.positions64 = d->positions64, a.copy = !in_place;
+  // a stride that no second head uses says nothing about alignment
+  if (d->tokens == 1) a.src_token = a.dst_token = 0;
+  if (d->groups == 1) a.src_group = a.dst_group = 0;
+  if (d->heads == 1) a.src_head = a.dst_head = 0;
   a.scale = d->scale;
   Turns turns = {};
   std::copy(d->turns, d->turns + a.half, turns.t);
-  const int64_t total = d->tokens * a.heads * ((d->head_dim + 1) / 2);
-  const int grid = int(std::min<int64_t>((total + kThreads - 1) / kThreads, int64_t(dev.sm_count) * 8));
   cudaStream_t st = gtp::as_stream(stream);
-  if (d->dtype == GTP_F32) return gtp::launch_overlapped(rotary_kernel<float>, grid, kThreads, 0, st, "rotary", a, turns, total);
-  return gtp::launch_overlapped(rotary_kernel<__nv_bfloat16>, grid, kThreads, 0, st, "rotary", a, turns, total);
+  return d->dtype == GTP_F32 ? launch<float>(a, turns, d->interleaved, st)
+                             : launch<__nv_bfloat16>(a, turns, d->interleaved, st);
 }
