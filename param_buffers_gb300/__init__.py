@@ -53,7 +53,8 @@ def _check(status: int, fn: str) -> None:
 def _stream(stream) -> int:
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building the Stream object that current_stream() returns costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -816,37 +817,63 @@ def _rng(rng):
     return C.byref(abi.gtp_rng(seed, offset, _ptr(word)))
 
 
+# The checks below look at each property of a tensor once: a small call is bound by them and the launch.
+
+_FLOATS: dict = {}
+
+
 def _float_dtype(t, name: str) -> int:
+    import torch
+    if not _FLOATS:
+        _FLOATS.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16})
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def _matrix(t, name: str):
+    """(dtype, shape, row stride) of a 2-D float matrix whose rows are contiguous."""
+    dt = _float_dtype(t, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dims, got {len(shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return dt, shape, ld if shape[0] > 1 else shape[1]
+
+
+def _bytes(t, name: str) -> int:
+    """The length of a contiguous uint8 tensor."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype == torch.bfloat16:
-        return abi.GTP_BF16
-    if t.dtype == torch.float32:
-        return abi.GTP_F32
-    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be {torch.uint8}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel()
 
 
-def _rows(t, name: str):
-    """(dtype, row stride) of a 2-D float matrix whose rows are contiguous."""
-    dt = _float_dtype(t, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return dt, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _scales(t, rows: int, blocks: int, name: str) -> int:
+    n = -(-rows // 128) * -(-blocks // 4) * 512
+    if _bytes(t, name) != n:
+        raise ValueError(f"{name} must hold gtp_sf_tiled_bytes({rows}, {blocks}) = {n} bytes")
+    return t.data_ptr()
 
 
 def _mxfp4_view(view, rows: int, cols: int, name: str):
-    import torch
     if view is None:
         return 0, 0
     codes, scales = view
-    _require(codes, torch.uint8, f"{name} codes", 2)
-    if tuple(codes.shape) != (rows, 16 * -(-cols // 32)):
-        raise ValueError(f"{name} codes must be [{rows}, {16 * -(-cols // 32)}]")
-    _require_tiled(scales, rows, -(-cols // 32), f"{name} scales")
-    return codes.data_ptr(), scales.data_ptr()
+    blocks = -(-cols // 32)
+    _bytes(codes, name)
+    if codes.shape != (rows, 16 * blocks):
+        raise ValueError(f"{name} codes must be [{rows}, {16 * blocks}]")
+    return codes.data_ptr(), _scales(scales, rows, blocks, name)
 
 
 def gtp_mxfp4_views(rows: int, cols: int, device="cuda"):
@@ -864,8 +891,7 @@ def gtp_mxfp4_quantize(src, row=None, col=None, rng=None, stream=None) -> None:
     """src[R,C] (fp32 or bf16, contiguous rows of any stride) -> its rowwise and / or columnwise MXFP4
     view, each a (codes, scales) pair as gtp_mxfp4_views makes them.  rng None rounds to nearest, an
     Rng stochastically."""
-    dt, ld = _rows(src, "src")
-    R, Cc = src.shape
+    dt, (R, Cc), ld = _matrix(src, "src")
     rc, rs = _mxfp4_view(row, R, Cc, "rowwise")
     cc, cs = _mxfp4_view(col, Cc, R, "columnwise")
     _check(lib().gtp_mxfp4_quantize(src.data_ptr(), dt, R, Cc, ld, rc, rs, cc, cs, _rng(rng), _stream(stream)),
@@ -882,48 +908,49 @@ def gtp_mxfp4_dequantize(codes, scales, out, stream=None) -> None:
 
 
 def _mxfp4_product(Aq, As, Bq, Bs, names: str):
-    """Pointers of two views contracted over their rows, and that length (padded to whole blocks)."""
+    """Pointers of two views contracted over their rows, their row counts and the contraction's length
+    (padded to whole blocks)."""
+    _bytes(Aq, names)
+    _bytes(Bq, names)
+    a, b = Aq.shape, Bq.shape
+    if len(a) != 2 or len(b) != 2 or a[1] != b[1] or a[1] % 16:
+        raise ValueError(f"shape mismatch: {names} are 2-D and hold the contraction's whole blocks")
+    blocks = a[1] // 16
+    return (Aq.data_ptr(), _scales(As, a[0], blocks, names), Bq.data_ptr(), _scales(Bs, b[0], blocks, names),
+            a[0], b[0], 32 * blocks)
+
+
+def _bf16_out(t, rows: int, cols: int, name: str) -> int:
     import torch
-    for t, n in zip((Aq, Bq), names.split()):
-        _require(t, torch.uint8, n, 2)
-    K = 2 * Aq.shape[1]
-    if Bq.shape[1] != Aq.shape[1] or K % 32:
-        raise ValueError("shape mismatch: both views hold the contraction's whole blocks")
-    for t, q, n in ((As, Aq, "scales of " + names.split()[0]), (Bs, Bq, "scales of " + names.split()[1])):
-        _require_tiled(t, q.shape[0], K // 32, n)
-    return Aq.data_ptr(), As.data_ptr(), Bq.data_ptr(), Bs.data_ptr(), K
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{rows}, {cols}]")
+    return t.data_ptr()
 
 
 def gtp_linear_fprop_mxfp4(Xq, Xs, Wq, Ws, Y, stream=None) -> None:
     """Y[M,N] (bf16) = dq(Xq, Xs) dq(Wq, Ws)^T, the rowwise MXFP4 views of X[M,K] and W[N,K]."""
-    import torch
-    *ptrs, K = _mxfp4_product(Xq, Xs, Wq, Ws, "Xq Wq")
-    _require(Y, torch.bfloat16, "Y", 2)
-    M, N = Xq.shape[0], Wq.shape[0]
-    if tuple(Y.shape) != (M, N):
-        raise ValueError("shape mismatch: Y [M,N]")
-    _check(lib().gtp_linear_fprop_mxfp4(*ptrs, Y.data_ptr(), M, N, K, _stream(stream)), "gtp_linear_fprop_mxfp4")
+    a, sa, b, sb, M, N, K = _mxfp4_product(Xq, Xs, Wq, Ws, "Xq and Wq")
+    _check(lib().gtp_linear_fprop_mxfp4(a, sa, b, sb, _bf16_out(Y, M, N, "Y"), M, N, K, _stream(stream)),
+           "gtp_linear_fprop_mxfp4")
 
 
 def gtp_linear_dgrad_mxfp4(dYq, dYs, Wtq, Wts, dX, stream=None) -> None:
     """dX[M,K] (bf16) = dq(dYq, dYs) dq(Wtq, Wts)^T: dY[M,N] rowwise, W[N,K] columnwise."""
-    import torch
-    *ptrs, N = _mxfp4_product(dYq, dYs, Wtq, Wts, "dYq Wtq")
-    _require(dX, torch.bfloat16, "dX", 2)
-    M, K = dYq.shape[0], Wtq.shape[0]
-    if tuple(dX.shape) != (M, K):
-        raise ValueError("shape mismatch: dX [M,K]")
-    _check(lib().gtp_linear_dgrad_mxfp4(*ptrs, dX.data_ptr(), M, N, K, _stream(stream)), "gtp_linear_dgrad_mxfp4")
+    a, sa, b, sb, M, K, N = _mxfp4_product(dYq, dYs, Wtq, Wts, "dYq and Wtq")
+    _check(lib().gtp_linear_dgrad_mxfp4(a, sa, b, sb, _bf16_out(dX, M, K, "dX"), M, N, K, _stream(stream)),
+           "gtp_linear_dgrad_mxfp4")
 
 
 def gtp_linear_wgrad_accum_mxfp4(dYtq, dYts, Xtq, Xts, grad_data, grad_offset: int, stream=None) -> None:
     """grad_data[grad_offset:+N*K].view(N,K) += dq(dYtq, dYts) dq(Xtq, Xts)^T (fp32), the columnwise MXFP4
     views of dY[M,N] and X[M,K]."""
     import torch
-    *ptrs, M = _mxfp4_product(dYtq, dYts, Xtq, Xts, "dYtq Xtq")
+    a, sa, b, sb, N, K, M = _mxfp4_product(dYtq, dYts, Xtq, Xts, "dYtq and Xtq")
     _require(grad_data, torch.float32, "grad_data")
-    _check(lib().gtp_linear_wgrad_accum_mxfp4(*ptrs, grad_data.data_ptr(), int(grad_offset), grad_data.numel(), M,
-                                              dYtq.shape[0], Xtq.shape[0], _stream(stream)),
+    _check(lib().gtp_linear_wgrad_accum_mxfp4(a, sa, b, sb, grad_data.data_ptr(), int(grad_offset), grad_data.numel(),
+                                              M, N, K, _stream(stream)),
            "gtp_linear_wgrad_accum_mxfp4")
 
 
@@ -968,19 +995,21 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
     (i, i + rot_dim/2), "interleaved" (2i, 2i+1).  inverse=True is the gradient."""
     import torch
     dt = _float_dtype(src, "src")
-    if dst.dtype != src.dtype or dst.shape != src.shape:
+    shape = src.shape
+    if _float_dtype(dst, "dst") != dt or dst.shape != shape:
         raise ValueError("dst must have src's dtype and shape")
-    if src.dim() not in (3, 4):
+    if len(shape) not in (3, 4):
         raise ValueError("src must be [tokens, heads, head_dim] or [tokens, groups, heads, head_dim]")
-    D = src.shape[-1]
-    if D > 1 and (src.stride(-1) != 1 or dst.stride(-1) != 1):
+    D, ss, ds = shape[-1], src.stride(), dst.stride()
+    if D > 1 and (ss[-1] != 1 or ds[-1] != 1):
         raise ValueError("heads must be contiguous")
     if layout not in ("half", "interleaved"):
         raise ValueError("layout must be 'half' or 'interleaved'")
-    T, G, H = (src.shape[0], 1, src.shape[1]) if src.dim() == 3 else src.shape[:3]
-    ss, ds = src.stride(), dst.stride()
-    if src.dim() == 3:
+    if len(shape) == 3:
+        T, G, H = shape[0], 1, shape[1]
         ss, ds = (ss[0], 0, ss[1]), (ds[0], 0, ds[1])
+    else:
+        T, G, H = shape[:3]
     wide = 0
     if positions is not None:
         if positions.dtype not in (torch.int32, torch.int64):
@@ -991,11 +1020,11 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
             raise ValueError("one position a token")
     if not isinstance(turns, C.Array):
         turns = (C.c_uint64 * len(turns))(*turns)
-    d = abi.gtp_rotary_desc(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
-                            positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
-                            C.addressof(turns), G, H, D, 2 * len(turns), dt, wide, int(layout == "interleaved"),
-                            int(bool(inverse)), scale, 0)
-    _check(lib().gtp_rotary(C.byref(d), _stream(stream)), "gtp_rotary")
+    d = abi.ROTARY_DESC_PACK(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
+                             positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
+                             C.addressof(turns), G, H, D, 2 * len(turns), dt, wide, layout == "interleaved",
+                             bool(inverse), scale, 0)
+    _check(lib().gtp_rotary(d, _stream(stream)), "gtp_rotary")
 
 
 # ----------------------------------------------------------------------------- dropout
@@ -1003,26 +1032,27 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
 def gtp_dropout_add(x, residual, out, p: float, rng, stream=None) -> None:
     """out = residual + dropout(x) (residual None: no add), [R,C] fp32 or bf16 with contiguous rows of any
     stride; residual has out's dtype.  out may be x or residual.  rng: an Rng, the gradient's too."""
-    xd, xl = _rows(x, "x")
-    od, ol = _rows(out, "out")
-    rl = 0
+    xd, xs, xl = _matrix(x, "x")
+    od, os, ol = _matrix(out, "out")
+    rp = rl = 0
     if residual is not None:
-        rd, rl = _rows(residual, "residual")
-        if rd != od or residual.shape != out.shape:
+        rd, rs, rl = _matrix(residual, "residual")
+        if rd != od or rs != os:
             raise ValueError("residual must have out's dtype and shape")
-    if x.shape != out.shape:
+        rp = residual.data_ptr()
+    if xs != os:
         raise ValueError("x and out must have the same shape")
-    _check(lib().gtp_dropout_add(x.data_ptr(), xd, xl, _ptr(residual), rl, out.data_ptr(), od, ol, x.shape[0],
-                                 x.shape[1], p, _rng(rng), _stream(stream)),
+    _check(lib().gtp_dropout_add(x.data_ptr(), xd, xl, rp, rl, out.data_ptr(), od, ol, xs[0], xs[1], p, _rng(rng),
+                                 _stream(stream)),
            "gtp_dropout_add")
 
 
 def gtp_dropout_grad(dout, dx, p: float, rng, stream=None) -> None:
     """dx = the gradient of dropout(x) from dout under the forward's p and rng; dx may be dout."""
-    gd, gl = _rows(dout, "dout")
-    xd, xl = _rows(dx, "dx")
-    if dout.shape != dx.shape:
+    gd, gs, gl = _matrix(dout, "dout")
+    xd, xs, xl = _matrix(dx, "dx")
+    if gs != xs:
         raise ValueError("dout and dx must have the same shape")
-    _check(lib().gtp_dropout_grad(dout.data_ptr(), gd, gl, dx.data_ptr(), xd, xl, dx.shape[0], dx.shape[1], p,
-                                  _rng(rng), _stream(stream)),
+    _check(lib().gtp_dropout_grad(dout.data_ptr(), gd, gl, dx.data_ptr(), xd, xl, xs[0], xs[1], p, _rng(rng),
+                                  _stream(stream)),
            "gtp_dropout_grad")

@@ -7,6 +7,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "libgtp.so"
@@ -105,6 +106,10 @@ class gtp_rotary_desc(C.Structure):
                 ("scale", C.c_float), ("reserved", C.c_int32)]
 
 
+# The same bytes as a gtp_rotary_desc, in one call: filling the 24 fields of the structure one by one costs
+# more than the launch.
+ROTARY_DESC_PACK = struct.Struct("<3Q10qQ8ifi").pack
+
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
@@ -156,7 +161,7 @@ PROTOTYPES = {
     "gtp_linear_dgrad_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
     "gtp_linear_wgrad_accum_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, I64, I64, VP]),
     "gtp_rotary_turns": (I32, [P(gtp_rotary_config), P(C.c_uint64), P(C.c_float)]),
-    "gtp_rotary": (I32, [P(gtp_rotary_desc), VP]),
+    "gtp_rotary": (I32, [VP, VP]),  # a gtp_rotary_desc, by reference or packed
     "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
     "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
     "gtp_wait_timeouts": (I32, [P(C.c_uint32), I32]),
