@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "device.h"
+#include "fastdiv.cuh"
 #include "philox.cuh"
 #include "sm100_ptx.cuh"
 
@@ -31,54 +32,44 @@ struct DropArgs {
   const void *x, *residual;
   void *out;
   int64_t rows, cols, x_ld, residual_ld, out_ld;
+  int64_t row0;  // rows before these in the call (a later launch of one call)
   uint32_t threshold;
   float scale;
   gtp::RngArgs rng;
 };
 
-// Eight consecutive elements as fp32, by 16-byte vectors or, up to `n` of them, one by one.
-template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int n, float (&x)[8]) {
-  if (VEC) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k] : 0.f;
+// Eight consecutive elements on 16 bytes, as they lie in memory: loads in flight hold no more registers
+// than bytes.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldcs(reinterpret_cast<const float4 *>(p));
+    b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
   }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, float (&x)[8]) {
-  if (VEC) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);  // bf16 -> fp32 is exact
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k]) : 0.f;
   }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(float *p, int n, const float (&x)[8]) {
-  if (VEC) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = x[k];
-  }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, int n, const float (&x)[8]) {
-  if (VEC) {
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -86,79 +77,245 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, int n, const float (&x)
       w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = __float2bfloat16_rn(x[k]);
   }
-}
+};
+
+// Element k of a group is kept where its 16 bits reach the threshold: the upper half of a word compares
+// as the whole word against threshold << 16 (what lies below cannot carry), the lower one shifted up.
+// threshold 65536 (p = 1) has no such word and is handled as `none`.
+struct Mask {
+  uint32_t w[4], cut;
+  bool none;
+  __device__ __forceinline__ Mask(const DropArgs &a, uint64_t offset, int64_t g, int64_t row) {
+    const uint4 d = gtp::philox(a.rng.k0, a.rng.k1, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
+                                uint32_t(offset), uint32_t(offset >> 32));
+    w[0] = d.x, w[1] = d.y, w[2] = d.z, w[3] = d.w;
+    cut = a.threshold << 16;
+    none = a.threshold > 65535u;
+  }
+  __device__ __forceinline__ bool keep(int k) const {
+    return (k & 1 ? w[k >> 1] : w[k >> 1] << 16) >= cut && !none;
+  }
+};
+
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // A thread owns one group of eight columns (one generator call) in ROWS rows at a time, whose loads
-// are in flight together; blocks are blockDim.x groups wide and step down the rows.
-constexpr int kRows = 2;
+// are in flight together; blocks are blockDim.x groups wide and step down the rows.  Every row of every
+// array starts on 16 bytes and holds whole groups.
+//
+// How many rows and blocks: measured on 2048 columns, bf16 onto a bf16 residual (8192 rows) 17.7 us with
+// 1 row and 8 blocks an SM against 20-23 with 2 or 4 rows; bf16 alone (32768 rows) 47.7 us with 4 rows
+// and 3 blocks against 49-57; where an array is fp32, 26.3 (bf16 onto fp32) and 62.5 us (fp32 to bf16)
+// with 2 rows and as many blocks as there are rows for, up to 16 an SM, against 28-39 and 65-72.
+template <typename TI, typename TO, bool RES>
+struct Shape {
+  static constexpr bool NARROW = sizeof(TI) == 2 && sizeof(TO) == 2;
+  static constexpr int ROWS = !NARROW ? 2 : RES ? 1 : 4;
+  static constexpr int MIN_BLOCKS = NARROW && RES ? 8 : 1;
+  static constexpr int BLOCKS = !NARROW ? 16 : RES ? 8 : 3;
+};
 
-template <typename TI, typename TO, bool RES, bool VEC>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
+template <typename TI, typename TO, bool RES>
+__global__ void __launch_bounds__(kThreads, Shape<TI, TO, RES>::MIN_BLOCKS)
+    dropout_kernel(const __grid_constant__ DropArgs a) {
+  constexpr int N = Shape<TI, TO, RES>::ROWS;
   gtp::ptx::allow_dependents();
   const int64_t g = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t left = a.cols - 8 * g;
   gtp::ptx::wait_prior_grid();
-  if (left <= 0) return;
-  const int n = VEC ? 8 : int(min(left, int64_t(8)));
+  if (8 * g >= a.cols) return;
   const uint64_t offset = gtp::rng_offset(a.rng);
   const int64_t step = int64_t(gridDim.y) * blockDim.y;
-  for (int64_t r0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r0 < a.rows; r0 += kRows * step) {
-    float x[kRows][8], res[kRows][8];
+  for (int64_t r0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r0 < a.rows; r0 += N * step) {
+    Eight<TI> x[N];
+    Eight<TO> res[RES ? N : 1];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int64_t row = r0 + i * step;
       if (row < a.rows) {
-        load8<VEC>(static_cast<const TI *>(a.x) + row * a.x_ld + 8 * g, n, x[i]);
-        if (RES) load8<VEC>(static_cast<const TO *>(a.residual) + row * a.residual_ld + 8 * g, n, res[i]);
+        x[i].load(static_cast<const TI *>(a.x) + row * a.x_ld + 8 * g);
+        if (RES) res[i].load(static_cast<const TO *>(a.residual) + row * a.residual_ld + 8 * g);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int64_t row = r0 + i * step;
       if (row < a.rows) {
-        const uint4 d = gtp::philox(a.rng.k0, a.rng.k1, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
-                                    uint32_t(offset), uint32_t(offset >> 32));
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-        float y[8];
+        const Mask m(a, offset, g, row);
+        float v[8], y[8];
+        x[i].get(v);
+        if (RES) res[i].get(y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t r = k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu;
-          y[k] = r >= a.threshold ? x[i][k] * a.scale : 0.f;
-          if (RES) y[k] += res[i][k];
+          if (!RES) y[k] = 0.f;
+          if (m.keep(k)) y[k] = RES ? fmaf(v[k], a.scale, y[k]) : v[k] * a.scale;
         }
-        store8<VEC>(static_cast<TO *>(a.out) + row * a.out_ld + 8 * g, n, y);
+        Eight<TO>::store(static_cast<TO *>(a.out) + row * a.out_ld + 8 * g, y);
       }
+    }
+  }
+}
+
+// Rows that start anywhere (odd lengths, strides and bases).  A lane still makes one generator call, for
+// group v of a row, and keeps its mask as eight bits; but the eight elements it moves are those from
+// column head + 8 v on, where head columns lie before the row's first 16-byte place: its own last
+// 8 - head and the first `head` of group v + 1, whose mask the lane above holds.  Items (row, v) run
+// over each row's groups one after the other, narrow rows side by side in a warp; the last lane of a
+// warp only draws (1/32 of the calls).  The up to 7 columns before and after a row's vectors go element
+// by element, a thread each, in the blocks after the others.
+//
+// That needs one `head` for all arrays of a row, i.e. rows of like length one after another: the
+// ordinary odd case.  Arrays that lie differently take dropout_elements_kernel.
+struct Shifted {
+  int32_t items;        // groups of all rows
+  int32_t vector_blocks;
+  gtp::FastDiv by_groups;
+  int32_t groups;       // of a row, one more than it has whole vectors at most
+};
+
+template <typename TI, typename TO, bool RES>
+__device__ __forceinline__ void one_element(const DropArgs &a, uint64_t offset, int64_t row, int64_t j) {
+  const Mask m(a, offset, j >> 3, row + a.row0);
+  const int k = int(j & 7);
+  const uint32_t word = k < 2 ? m.w[0] : k < 4 ? m.w[1] : k < 6 ? m.w[2] : m.w[3];
+  const bool keep = (k & 1 ? word : word << 16) >= m.cut && !m.none;
+  const float x = load1(static_cast<const TI *>(a.x) + row * a.x_ld + j);
+  float y = RES ? load1(static_cast<const TO *>(a.residual) + row * a.residual_ld + j) : 0.f;
+  if (keep) y = RES ? fmaf(x, a.scale, y) : x * a.scale;
+  store1(static_cast<TO *>(a.out) + row * a.out_ld + j, y);
+}
+
+template <typename TO>
+__device__ __forceinline__ int head_of(const DropArgs &a, int64_t row) {
+  return int((0u - uint32_t((reinterpret_cast<uintptr_t>(static_cast<const TO *>(a.out) + row * a.out_ld)) / sizeof(TO))) & 7u);
+}
+
+template <typename TI, typename TO, bool RES>
+__global__ void __launch_bounds__(kThreads)
+    dropout_shifted_kernel(const __grid_constant__ DropArgs a, const __grid_constant__ Shifted s) {
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const uint64_t offset = gtp::rng_offset(a.rng);
+  if (int(blockIdx.x) >= s.vector_blocks) {  // the ends: 16 threads a row
+    const int64_t i = int64_t(blockIdx.x - s.vector_blocks) * kThreads + threadIdx.x, row = i >> 4;
+    if (row >= a.rows) return;
+    const int e = int(i & 15);
+    const int64_t head = min(int64_t(head_of<TO>(a, row)), a.cols), tail = head + (a.cols - head) / 8 * 8;
+    const int64_t j = e < 8 ? e : tail + e - 8;
+    if (e < 8 ? j < head : j < a.cols) one_element<TI, TO, RES>(a, offset, row, j);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int item = (int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5)) * 31 + lane;
+  const int row32 = gtp::fast_div(min(item, s.items - 1), s.by_groups), v = min(item, s.items - 1) - row32 * s.groups;
+  const int64_t row = row32;
+  const int head = head_of<TO>(a, row);
+  const int64_t j = head + 8 * int64_t(v);
+  const bool whole = lane < 31 && item < s.items && j + 8 <= a.cols;
+  Eight<TI> x;
+  Eight<TO> res;
+  if (whole) {
+    x.load(static_cast<const TI *>(a.x) + row * a.x_ld + j);
+    if (RES) res.load(static_cast<const TO *>(a.residual) + row * a.residual_ld + j);
+  }
+  const Mask m(a, offset, v, row + a.row0);
+  uint32_t keep = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) keep |= (m.keep(k) ? 1u : 0u) << k;
+  // where head > 0 the vector reaches into group v + 1 of the same row, which exists
+  keep = (keep | __shfl_down_sync(0xFFFFFFFFu, keep, 1) << 8) >> head;
+  if (!whole) return;
+  float f[8], y[8];
+  x.get(f);
+  if (RES) res.get(y);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (!RES) y[k] = 0.f;
+    if (keep >> k & 1) y[k] = RES ? fmaf(f[k], a.scale, y[k]) : f[k] * a.scale;
+  }
+  Eight<TO>::store(static_cast<TO *>(a.out) + row * a.out_ld + j, y);
+}
+
+// Arrays that lie differently: a thread a group, element by element.
+template <typename TI, typename TO, bool RES>
+__global__ void __launch_bounds__(kThreads)
+    dropout_elements_kernel(const __grid_constant__ DropArgs a, const __grid_constant__ Shifted s) {
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const uint64_t offset = gtp::rng_offset(a.rng);
+  const int64_t item = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (item >= s.items) return;
+  const int row32 = gtp::fast_div(int(item), s.by_groups), v = int(item) - row32 * s.groups;
+  const int64_t row = row32;
+  const Mask m(a, offset, v, row + a.row0);
+  const TI *x = static_cast<const TI *>(a.x) + row * a.x_ld;
+  const TO *res = static_cast<const TO *>(a.residual) + (RES ? row * a.residual_ld : 0);
+  TO *out = static_cast<TO *>(a.out) + row * a.out_ld;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t j = 8 * int64_t(v) + k;
+    if (j < a.cols) {
+      float y = RES ? load1(res + j) : 0.f;
+      if (m.keep(k)) y = RES ? fmaf(load1(x + j), a.scale, y) : load1(x + j) * a.scale;
+      store1(out + j, y);
     }
   }
 }
 
 template <typename TI, typename TO, bool RES>
-gtp_status launch(const DropArgs &a, bool vec, const gtp::DeviceInfo &dev, cudaStream_t st) {
+gtp_status launch(DropArgs a, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  // the arrays' rows start the same number of elements past 16 bytes: their strides agree modulo 8
+  // elements and their first elements do
+  const auto at = [](const void *p, size_t es) { return (reinterpret_cast<uintptr_t>(p) / es) & 7u; };
+  const auto like_out = [&](const void *p, int64_t ld, size_t es) {
+    return at(p, es) == at(a.out, sizeof(TO)) && (a.rows == 1 || (ld - a.out_ld) % 8 == 0);
+  };
+  const bool same = like_out(a.x, a.x_ld, sizeof(TI)) && (!RES || like_out(a.residual, a.residual_ld, sizeof(TO)));
+  const bool aligned = same && at(a.out, sizeof(TO)) == 0 && (a.rows == 1 || a.out_ld % 8 == 0) && a.cols % 8 == 0;
   const int64_t groups = (a.cols + 7) / 8;
-  int tx = 1;
-  while (tx < kThreads && tx < groups) tx *= 2;
-  const dim3 block(tx, kThreads / tx);
-  const int64_t gx = (groups + tx - 1) / tx, want = (a.rows + block.y * kRows - 1) / (block.y * kRows);
-  const int64_t fill = (int64_t(dev.sm_count) * 8 + gx - 1) / gx;  // a grid that fills the SMs
-  const dim3 grid(unsigned(gx), unsigned(std::max<int64_t>(1, std::min<int64_t>({want, fill, 65535}))));
-  return vec ? gtp::launch_overlapped(dropout_kernel<TI, TO, RES, true>, grid, block, 0, st, "dropout", a)
-             : gtp::launch_overlapped(dropout_kernel<TI, TO, RES, false>, grid, block, 0, st, "dropout", a);
+  if (aligned) {
+    using S = Shape<TI, TO, RES>;
+    int tx = 1;
+    while (tx < kThreads && tx < groups) tx *= 2;
+    const dim3 block(tx, kThreads / tx);
+    const int64_t per = block.y * S::ROWS, gx = (groups + tx - 1) / tx;
+    const int64_t fill = std::max<int64_t>(1, (int64_t(dev.sm_count) * S::BLOCKS + gx / 2) / gx);
+    const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>({(a.rows + per - 1) / per, fill, 65535})));
+    return gtp::launch_overlapped(dropout_kernel<TI, TO, RES>, grid, block, 0, st, "dropout", a);
+  }
+  // items are counted in 31 bits: more than 2^30 groups go in several launches
+  const int64_t rows = a.rows, most = std::max<int64_t>(1, (int64_t(1) << 30) / groups);
+  const char *x = static_cast<const char *>(a.x), *res = static_cast<const char *>(a.residual);
+  char *out = static_cast<char *>(a.out);
+  for (int64_t r = 0; r < rows; r += most) {
+    a.row0 = r;
+    a.rows = std::min(most, rows - r);
+    a.x = x + r * a.x_ld * int64_t(sizeof(TI));
+    a.residual = RES ? res + r * a.residual_ld * int64_t(sizeof(TO)) : nullptr;
+    a.out = out + r * a.out_ld * int64_t(sizeof(TO));
+    Shifted s;
+    s.groups = int32_t(groups);
+    s.by_groups = gtp::make_fastdiv(s.groups);
+    s.items = int32_t(a.rows * groups);
+    const int64_t a_block = 31 * (kThreads / 32);
+    s.vector_blocks = int32_t((s.items + a_block - 1) / a_block);
+    const int64_t end_blocks = (a.rows * 16 + kThreads - 1) / kThreads;
+    const gtp_status e =
+        same ? gtp::launch_overlapped(dropout_shifted_kernel<TI, TO, RES>, unsigned(s.vector_blocks + end_blocks), kThreads,
+                                      0, st, "dropout", a, s)
+             : gtp::launch_overlapped(dropout_elements_kernel<TI, TO, RES>, unsigned((s.items + kThreads - 1) / kThreads),
+                                      kThreads, 0, st, "dropout", a, s);
+    if (e) return e;
+  }
+  return GTP_OK;
 }
 
 template <typename TI, typename TO>
 gtp_status launch(const DropArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  // vectors where every row of every array starts on 16 bytes and holds whole groups
-  const auto whole = [&](const void *p, int64_t ld, size_t es) {
-    return gtp::aligned16(p) && (a.rows == 1 || ld * int64_t(es) % 16 == 0);
-  };
-  const bool vec = a.cols % 8 == 0 && whole(a.x, a.x_ld, sizeof(TI)) && whole(a.out, a.out_ld, sizeof(TO)) &&
-                   (!a.residual || whole(a.residual, a.residual_ld, sizeof(TO)));
-  return a.residual ? launch<TI, TO, true>(a, vec, dev, st) : launch<TI, TO, false>(a, vec, dev, st);
+  return a.residual ? launch<TI, TO, true>(a, dev, st) : launch<TI, TO, false>(a, dev, st);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;

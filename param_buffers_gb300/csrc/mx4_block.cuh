@@ -9,8 +9,6 @@
 // Both clamp at byte 0.  A block holding NaN or Inf gets byte 0xFF (E8M0 NaN) and codes 0.
 #pragma once
 
-#include <cuda_fp4.h>
-
 #include <cstdint>
 
 namespace gtp {
@@ -33,34 +31,59 @@ __device__ __forceinline__ float inv_scale(uint32_t byte) {
   return byte == kNanScale ? 0.f : __uint_as_float((254u - byte) << 23);
 }
 
-// Eight codes of eight values to nearest, the first in the low nibble.
-__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float inv) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_E2M1,
-                                           cudaRoundNearest))
-         << (8 * i);
+// Two fp32 values in a register pair, multiplied together: half the multiply instructions.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Eight codes to nearest of eight scaled values (in pairs), the first in the low nibble.
+__device__ __forceinline__ uint32_t codes8(const uint64_t (&y)[4]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .f32 l0, h0, l1, h1, l2, h2, l3, h3;\n\t"
+      "mov.b64 {l0, h0}, %1;\n\tmov.b64 {l1, h1}, %2;\n\tmov.b64 {l2, h2}, %3;\n\tmov.b64 {l3, h3}, %4;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, h0, l0;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, h1, l1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, h2, l2;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, h3, l3;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "l"(y[0]), "l"(y[1]), "l"(y[2]), "l"(y[3]));
   return w;
 }
 
-// One stochastically rounded code.  |x| / scale times 2^-126 is a float whose top bits are the E2M1
-// code itself: exponents 1, 2, 3 for [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the
-// product keeps 23 fractional bits (round to nearest).  The 22 bits below the code are the fraction
-// of the step to the next point, so adding the random byte in their place, centred, carries into
-// the code with the right probability.  At most 6 stays at most 6: its fraction is 0.
-__device__ __forceinline__ uint32_t encode1_stochastic(float x, float inv, uint32_t r) {
-  const float y = fabsf(x * inv) * 0x1p-126f;
-  return ((__float_as_uint(y) + (r << 14) + (1u << 13)) >> 22) | ((__float_as_uint(x) >> 28) & 8u);
+// Eight values (in pairs) to nearest; inv2 holds 1 / scale twice.
+__device__ __forceinline__ uint32_t encode8(const uint64_t (&x)[4], uint64_t inv2) {
+  const uint64_t y[4] = {mul2(x[0], inv2), mul2(x[1], inv2), mul2(x[2], inv2), mul2(x[3], inv2)};
+  return codes8(y);
 }
 
-// Eight of them, with the random bytes of r0 (first four) and r1.
-__device__ __forceinline__ uint32_t encode8_stochastic(const float (&x)[8], float inv, uint32_t r0, uint32_t r1) {
-  uint32_t w = 0;
+// Eight values stochastically, with the random bytes of r0 (first four) and r1.  x / scale times 2^-126
+// is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
+// [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23 fractional bits
+// (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
+// the random byte in their place, centred (byte << 14 | 1 << 13, one byte permute and one
+// multiply-add), carries into the code with the right probability; cleared and scaled back, the value
+// is on the grid and the conversion to a code exact.  At most 6 stays at most 6: its fraction is 0.
+__device__ __forceinline__ uint32_t encode8_stochastic(const uint64_t (&x)[4], uint64_t inv2, uint32_t r0,
+                                                       uint32_t r1) {
+  const uint64_t down = pack2(0x1p-126f, 0x1p-126f), up = pack2(0x1p126f, 0x1p126f);
+  uint64_t y[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w |= encode1_stochastic(x[i], inv, ((i < 4 ? r0 : r1) >> (8 * (i & 3))) & 0xFFu) << (4 * i);
-  return w;
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = mul2(mul2(x[i], inv2), down);
+    const uint32_t r = i < 2 ? r0 : r1;
+    // byte b of r over 0x80: (byte << 8 | 0x80) << 6
+    const uint32_t a = __byte_perm(r, 0x80u, (i & 1) ? 0x5524u : 0x5504u);
+    const uint32_t b = __byte_perm(r, 0x80u, (i & 1) ? 0x5534u : 0x5514u);
+    const uint32_t lo = (uint32_t(t) + a * 64u) & 0xFFC00000u, hi = (uint32_t(t >> 32) + b * 64u) & 0xFFC00000u;
+    y[i] = mul2(pack2(__uint_as_float(lo), __uint_as_float(hi)), up);
+  }
+  return codes8(y);
 }
 
 }  // namespace mx4

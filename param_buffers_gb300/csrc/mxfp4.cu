@@ -15,6 +15,7 @@
 #include <atomic>
 
 #include "device.h"
+#include "fastdiv.cuh"
 #include "mx4_block.cuh"
 #include "philox.cuh"
 #include "sm100_ptx.cuh"
@@ -32,9 +33,17 @@ constexpr int kThreads = 256;
 //
 // Rows: a thread takes 16 consecutive elements of 4 rows (32 apart), two lanes a block of 32.  On the
 // way the tile goes to shared memory; then a thread takes 32 rows of two adjacent columns (bf16, one
-// 32-bit word a row) or of one column twice (fp32), so a column's block needs no shuffle.  The words
-// of a row are rotated by 8 per 32 rows: the four row blocks of a column, which neighbouring lanes
-// hold so that they write its 64 bytes together, then lie in different banks.
+// 32-bit word a row) or of one column twice (fp32), so a column's block needs no shuffle.
+//
+// Where a word of a tile row lies (in groups of four words, 16 bytes): lanes that store their segments
+// are THREAD_WORDS apart, so the low bits of a group are swapped by the bits above them; and the words
+// of a row are rotated by 8 per 32 rows, so that the four row blocks of a column, which neighbouring
+// lanes hold to write its 64 bytes together, lie in different banks.  Both directions then run without
+// bank conflicts.
+//
+// A source whose rows do not all start on 16 bytes (RAGGED: any odd row length) is read a row a warp, in
+// 32-bit words or, where those straddle, in elements, neighbouring lanes on neighbouring addresses, and
+// both passes take it from shared memory.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -54,11 +63,20 @@ __device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) 
   }
 }
 
-// The word of up to two elements, element by element, for a ragged or unaligned source.
+// The word of up to two elements, for a ragged or unaligned source.
 __device__ __forceinline__ uint32_t word_of(const float *p, int n) { return n > 0 ? __float_as_uint(*p) : 0u; }
 __device__ __forceinline__ uint32_t word_of(const __nv_bfloat16 *p, int n) {
   const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+  if (n > 1 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) return *reinterpret_cast<const uint32_t *>(p);
   return (n > 0 ? uint32_t(q[0]) : 0u) | (n > 1 ? uint32_t(q[1]) << 16 : 0u);
+}
+
+// Index of word `w` of row `r` in the tile.
+template <typename T>
+__device__ __forceinline__ int word_at(int r, int w) {
+  constexpr int WORDS = Tile<T>::WORDS, SPAN = Tile<T>::THREAD_WORDS / 4;
+  const int g = w >> 2, s = g ^ ((g >> 3) & (SPAN - 1));
+  return r * WORDS + ((4 * s + (w & 3) + 8 * (r >> 5)) & (WORDS - 1));
 }
 
 // The largest magnitude of a word's elements so far: fp32 one 32-bit maximum, bf16 two 16-bit ones.
@@ -76,25 +94,27 @@ __device__ __forceinline__ uint32_t max_magnitude<__nv_bfloat16>(uint32_t m, uin
 __device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// One block of 32 values under `byte` to 16 bytes of codes; view row r, block b (for the draws).
+// 2 N values in pairs, of one block under `byte`, to codes; view row r and its first group of draws.
 template <bool STOCH, int N>
-__device__ __forceinline__ void encode_run(const float (&x)[N], uint32_t byte, uint32_t (&w)[N / 8], uint32_t stream,
+__device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte, uint32_t (&w)[N / 4], uint32_t stream,
                                            uint32_t r, uint32_t first_group, const gtp::RngArgs &rng, uint64_t offset) {
   const float inv = gtp::mx4::inv_scale(byte);
-  const uint32_t keep = byte == gtp::mx4::kNanScale ? 0u : 0xFFFFFFFFu;  // a bad block's codes are 0
+  const uint64_t inv2 = gtp::mx4::pack2(inv, inv);
 #pragma unroll
-  for (int h = 0; h < N / 16; ++h) {
+  for (int h = 0; h < N / 8; ++h) {
     uint4 d = make_uint4(0, 0, 0, 0);
     if (STOCH)
       d = gtp::philox(rng.k0, rng.k1, (first_group + h) | (stream << 30), r, uint32_t(offset), uint32_t(offset >> 32));
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = x[16 * h + 8 * q + k];
-      w[2 * h + q] = keep & (STOCH ? gtp::mx4::encode8_stochastic(v, inv, q ? d.z : d.x, q ? d.w : d.y)
-                                   : gtp::mx4::encode8(v, inv));
+      const uint64_t v[4] = {x[8 * h + 4 * q], x[8 * h + 4 * q + 1], x[8 * h + 4 * q + 2], x[8 * h + 4 * q + 3]};
+      w[2 * h + q] = STOCH ? gtp::mx4::encode8_stochastic(v, inv2, q ? d.z : d.x, q ? d.w : d.y)
+                           : gtp::mx4::encode8(v, inv2);
     }
+  }
+  if (byte == gtp::mx4::kNanScale) {  // a bad block's codes are 0
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = 0;
   }
 }
 
@@ -109,15 +129,14 @@ struct TileArgs {
   int64_t rows, cols, ld;
   int64_t tiles_n;
   ViewArgs row, col;
-  int32_t vec;  // rows on 16 bytes
   gtp::RngArgs rng;
 };
 
-template <typename T, bool STOCH, bool ROW, bool COL>
+template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
 __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
   using F = Tile<T>;
   constexpr int TW = F::THREAD_WORDS;
-  extern __shared__ __align__(16) uint32_t tile[];  // COL: [128][WORDS]
+  extern __shared__ __align__(16) uint32_t tile[];  // COL or RAGGED: [128][WORDS]
   __shared__ __align__(16) uint8_t atom[2][512];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
@@ -128,28 +147,57 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
   const int64_t c0 = kTile * tn + 16 * seg;
   const int nc = int(max(int64_t(0), min(int64_t(16), a.cols - c0)));  // its columns inside the matrix
   uint32_t w[4][TW];
+  if constexpr (RAGGED) {
+    const int warp = tid >> 5, lane = tid & 31;
+    constexpr int LW = F::WORDS / 32;  // words a lane takes of a row
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int64_t r = kTile * tm + 32 * it + r32;
-    const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
-    if (r >= a.rows) {
+    for (int b = 0; b < 16; b += 8) {  // a warp's 16 rows, 8 in flight
+      uint32_t v[8][LW];
 #pragma unroll
-      for (int i = 0; i < TW; ++i) w[it][i] = 0;
-    } else if (a.vec && nc == 16) {
-      load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
-    } else {
+      for (int k = 0; k < 8; ++k) {
+        const int64_t r = kTile * tm + 16 * warp + b + k;
+        const T *p = static_cast<const T *>(a.src) + r * a.ld + kTile * tn;
+        const int n = r < a.rows ? int(min(int64_t(kTile), a.cols - kTile * tn)) : 0;
 #pragma unroll
-      for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
+        for (int i = 0; i < LW; ++i) v[k][i] = word_of(p + F::PER * (lane + 32 * i), n - F::PER * (lane + 32 * i));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < LW; ++i) tile[word_at<T>(16 * warp + b + k, lane + 32 * i)] = v[k][i];
     }
-  }
-  if (COL) {
+    __syncthreads();
+    if (ROW) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i < TW / 4; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(tile + word_at<T>(32 * it + r32, seg * TW + 4 * i));
+          w[it][4 * i] = v.x, w[it][4 * i + 1] = v.y, w[it][4 * i + 2] = v.z, w[it][4 * i + 3] = v.w;
+        }
+    }
+  } else {
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      uint32_t *t = tile + (32 * it + r32) * F::WORDS;
+      const int64_t r = kTile * tm + 32 * it + r32;
+      const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
+      if (r >= a.rows) {
 #pragma unroll
-      for (int i = 0; i < TW / 4; ++i)
-        *reinterpret_cast<uint4 *>(t + ((seg * TW + 4 * i + 8 * it) & (F::WORDS - 1))) =
-            make_uint4(w[it][4 * i], w[it][4 * i + 1], w[it][4 * i + 2], w[it][4 * i + 3]);
+        for (int i = 0; i < TW; ++i) w[it][i] = 0;
+      } else if (nc == 16) {
+        load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
+      }
+    }
+    if (COL) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i < TW / 4; ++i)
+          *reinterpret_cast<uint4 *>(tile + word_at<T>(32 * it + r32, seg * TW + 4 * i)) =
+              make_uint4(w[it][4 * i], w[it][4 * i + 1], w[it][4 * i + 2], w[it][4 * i + 3]);
     }
   }
   if (ROW) {
@@ -162,11 +210,11 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
       if (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16) << 16;
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       const uint32_t byte = gtp::mx4::scale_byte<STOCH>(m);
-      float x[16];
+      uint64_t x[8];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        x[k] = sizeof(T) == 4 ? __uint_as_float(w[it][k % TW])
-                              : (k & 1 ? high_f32(w[it][k >> 1]) : low_f32(w[it][k >> 1]));
+      for (int k = 0; k < 8; ++k)
+        x[k] = sizeof(T) == 4 ? gtp::mx4::pack2(__uint_as_float(w[it][2 * k % TW]), __uint_as_float(w[it][(2 * k + 1) % TW]))
+                              : gtp::mx4::pack2(low_f32(w[it][k]), high_f32(w[it][k]));
       uint32_t codes[2];
       encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundRow, uint32_t(r), uint32_t(8 * tn + seg), a.rng, offset);
       const bool in = r < a.rows && c0 < 2 * a.row.pitch;  // the block exists (two codes a byte)
@@ -181,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
 #pragma unroll
     for (int u = 0; u < 2 / F::PER; ++u) {
       const int p = (tid >> 2) + 64 * u;  // word of the tile row
-      const uint32_t *t = tile + 32 * rb * F::WORDS + ((p + 8 * rb) & (F::WORDS - 1));
+      const uint32_t *t = tile + word_at<T>(32 * rb, p);  // the rows of a block share the word's place
       uint32_t v[32], m = 0;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
@@ -193,9 +241,12 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
         const int c = F::PER * p + e;
         const int64_t gc = kTile * tn + c;
         const uint32_t byte = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : e ? m & 0xFFFF0000u : m << 16);
-        float x[32];
+        uint64_t x[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = F::PER == 1 ? __uint_as_float(v[k]) : e ? high_f32(v[k]) : low_f32(v[k]);
+        for (int k = 0; k < 16; ++k)
+          x[k] = F::PER == 1 ? gtp::mx4::pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]))
+                 : e         ? gtp::mx4::pack2(high_f32(v[2 * k]), high_f32(v[2 * k + 1]))
+                             : gtp::mx4::pack2(low_f32(v[2 * k]), low_f32(v[2 * k + 1]));
         uint32_t codes[4];
         encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundCol, uint32_t(gc), uint32_t(8 * tm + 2 * rb), a.rng, offset);
         const int64_t b = 4 * tm + rb;
@@ -215,50 +266,142 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
         reinterpret_cast<uint4 *>(atom[1])[tid - 32];
 }
 
-// Eight values a thread, back from a view: exact in bf16 and fp32 below 2^128 (one mantissa bit; the
-// smallest magnitude, 2^-128, is a bf16 subnormal).
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    mx4_values_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t len,
-                      T *__restrict__ out, int64_t blocks, int64_t words) {
+// Values back from a view, exact in bf16 and fp32 below 2^128 (one mantissa bit; the smallest
+// magnitude, 2^-128, is a bf16 subnormal).  A code's bf16 magnitude comes from a table of 8 in two
+// byte permutes for four codes, its sign by a multiply that moves two sign bits at once, and the scale
+// by a bf16 product, exact because it is a power of two.
+//
+// A thread writes eight elements where they lie on 16 bytes of the output.  Where rows start anywhere
+// (SHIFTED: an odd length), those are the elements from `head` + 8 v on, head the row's elements before
+// its first such place: eight nibbles out of words v and v + 1, the second held by the lane above (the
+// last lane of a warp only reads), under up to two scale bytes.  Items (row, v) run over all rows' words,
+// narrow rows side by side in a warp; the up to 7 elements at either end of a shifted row go one by one,
+// a thread each, in the blocks after the others.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) {
+  return byte == gtp::mx4::kNanScale ? 0x7FC0u : byte == 0 ? 0x0040u : byte << 7;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two codes in the low byte of w to two bf16 values; mag: their magnitudes.
+__device__ __forceinline__ uint32_t with_signs(uint32_t mag, uint32_t w) {
+  return mag | (((w & 0x88u) * 0x1001000u) & 0x80008000u);  // bits 3 and 7 to 15 and 31
+}
+
+struct ValueArgs {
+  const uint8_t *codes, *scales;
+  void *out;
+  int64_t rows, len, blocks, words;
+  int64_t row0;           // rows before these in the view (a later launch of one call)
+  int32_t items, groups;  // words of all rows and of a row that hold elements
+  int32_t vector_blocks;
+  gtp::FastDiv by_groups;
+};
+
+__device__ __forceinline__ uint32_t scale_byte_at(const ValueArgs &a, int64_t row, int64_t b) {
+  const int64_t r = row + a.row0;
+  return __ldg(a.scales + ((r >> 7) * a.words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3));
+}
+
+constexpr int kValueItems = 4;  // items a thread has in flight
+
+template <typename T, bool SHIFTED>
+__global__ void __launch_bounds__(kThreads) mx4_values_kernel(const __grid_constant__ ValueArgs a) {
+  constexpr int N = kValueItems, PER = SHIFTED ? 31 : 32;
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  const int64_t g = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, b = g >> 2;
-  const int64_t left = len - 8 * g;
-  if (left <= 0) return;
-  const uint8_t *sf = scales + (b >> 2) * 512 + (b & 3);
-  for (int64_t r = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r < rows; r += int64_t(gridDim.y) * blockDim.y) {
-    const uint32_t byte = __ldg(sf + (r >> 7) * words * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
-    const float scale = byte == gtp::mx4::kNanScale ? __uint_as_float(0x7FC00000u)
-                        : byte == 0                 ? 0x1p-127f
-                                                    : __uint_as_float(byte << 23);
-    const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(codes + r * blocks * 16) + g);
-    float x[8];
+  T *out = static_cast<T *>(a.out);
+  const auto head_of = [&](int64_t row) {
+    return int((0u - uint32_t(reinterpret_cast<uintptr_t>(out + row * a.len) / sizeof(T))) & 7u);
+  };
+  if (SHIFTED && int(blockIdx.x) >= a.vector_blocks) {  // the ends: 16 threads a row
+    const int64_t i = int64_t(blockIdx.x - a.vector_blocks) * kThreads + threadIdx.x, row = i >> 4;
+    if (row >= a.rows) return;
+    const int e = int(i & 15);
+    const int64_t head = min(int64_t(head_of(row)), a.len), tail = head + (a.len - head) / 8 * 8;
+    const int64_t j = e < 8 ? e : tail + e - 8;
+    if (e < 8 ? j >= head : j >= a.len) return;
+    const uint32_t c = uint32_t(a.codes[row * a.blocks * 16 + (j >> 1)]) >> (4 * (j & 1)), m = c & 7u;
+    const uint32_t mag = (__byte_perm(0xC0800000u, 0xC0804000u, m) & 0xFFu) | (__byte_perm(0x3F3F3F00u, 0x40404040u, m) & 0xFFu) << 8;
+    const uint32_t v = mul_bf16x2(mag | (c & 8u) << 12, scale_bf16(scale_byte_at(a, row, j >> 5)));
+    out[row * a.len + j] = T(low_f32(v));
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int first = (int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5)) * N * PER + lane;
+  uint32_t w[N], s[N];
+  int row[N], g[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-      const float2 f = __half22float2(__half2(h));
-      x[2 * i] = f.x * scale;
-      x[2 * i + 1] = f.y * scale;
+  for (int i = 0; i < N; ++i) {
+    const int item = min(first + i * PER, a.items - 1);
+    row[i] = gtp::fast_div(item, a.by_groups);
+    g[i] = item - row[i] * a.groups;
+    w[i] = __ldcs(reinterpret_cast<const uint32_t *>(a.codes + int64_t(row[i]) * a.blocks * 16) + g[i]);
+    s[i] = scale_byte_at(a, row[i], g[i] >> 2);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t c = w[i], ab = scale_bf16(s[i]), head = 0;
+    if (SHIFTED) {
+      // where head > 0 the vector reaches into word g + 1 of the same row, which exists
+      head = uint32_t(head_of(row[i]));
+      c = __funnelshift_r(c, __shfl_down_sync(0xFFFFFFFFu, c, 1), 4 * head);
+      ab |= __shfl_down_sync(0xFFFFFFFFu, ab, 1) << 16;
     }
-    T *o = out + r * len + 8 * g;
-    if constexpr (VEC && sizeof(T) == 4) {
-      __stcs(reinterpret_cast<float4 *>(o), make_float4(x[0], x[1], x[2], x[3]));
-      __stcs(reinterpret_cast<float4 *>(o) + 1, make_float4(x[4], x[5], x[6], x[7]));
-    } else if constexpr (VEC) {
-      uint32_t v[4];
+    const int64_t j = int64_t(head) + 8 * int64_t(g[i]);
+    if (first + i * PER >= a.items || (SHIFTED && lane == 31) || j + 8 > a.len) continue;
+    uint32_t v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        v[i] = *reinterpret_cast<const uint32_t *>(&p);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = (c >> (16 * h)) & 0x7777u;
+      const uint32_t top = __byte_perm(0x3F3F3F00u, 0x40404040u, sel), low = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+      v[2 * h] = with_signs(__byte_perm(low, top, 0x5140), c >> (16 * h));
+      v[2 * h + 1] = with_signs(__byte_perm(low, top, 0x7362), c >> (16 * h + 8));
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {  // elements from 8 - head on are the upper word's block's
+      const uint32_t sel = !SHIFTED || 2 * p + 1 < 8 - int(head) ? 0x1010u : 2 * p < 8 - int(head) ? 0x3210u : 0x3232u;
+      v[p] = mul_bf16x2(v[p], __byte_perm(ab, 0, sel));
+    }
+    T *o = out + int64_t(row[i]) * a.len + j;
+    if constexpr (sizeof(T) == 2) {
       __stcs(reinterpret_cast<uint4 *>(o), make_uint4(v[0], v[1], v[2], v[3]));
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < left) o[k] = T(x[k]);
+      __stcs(reinterpret_cast<float4 *>(o), make_float4(low_f32(v[0]), high_f32(v[0]), low_f32(v[1]), high_f32(v[1])));
+      __stcs(reinterpret_cast<float4 *>(o) + 1, make_float4(low_f32(v[2]), high_f32(v[2]), low_f32(v[3]), high_f32(v[3])));
     }
   }
+}
+
+template <typename T>
+gtp_status launch_values(ValueArgs a, cudaStream_t st) {
+  const bool shifted = !gtp::aligned16(a.out) || a.len % 8 != 0;
+  a.groups = int32_t((a.len + 7) / 8);
+  a.by_groups = gtp::make_fastdiv(a.groups);
+  // items are counted in 31 bits: more than 2^30 words go in several launches
+  const int64_t rows = a.rows, most = std::max<int64_t>(1, (int64_t(1) << 30) / a.groups);
+  const uint8_t *codes = a.codes;
+  T *out = static_cast<T *>(a.out);
+  for (int64_t r = 0; r < rows; r += most) {
+    a.row0 = r;
+    a.rows = std::min(most, rows - r);
+    a.codes = codes + r * a.blocks * 16;
+    a.out = out + r * a.len;
+    a.items = int32_t(a.rows * a.groups);
+    const int64_t a_block = (kThreads / 32) * kValueItems * (shifted ? 31 : 32);
+    a.vector_blocks = int32_t((a.items + a_block - 1) / a_block);
+    const int64_t ends = shifted ? (a.rows * 16 + kThreads - 1) / kThreads : 0;
+    const unsigned grid = unsigned(a.vector_blocks + ends);
+    const gtp_status e =
+        shifted ? gtp::launch_overlapped(mx4_values_kernel<T, true>, grid, kThreads, 0, st, "mxfp4_dequantize", a)
+                : gtp::launch_overlapped(mx4_values_kernel<T, false>, grid, kThreads, 0, st, "mxfp4_dequantize", a);
+    if (e) return e;
+  }
+  return GTP_OK;
 }
 
 struct View {
@@ -270,10 +413,10 @@ struct View {
   int64_t scale_bytes() const { return (rows + 127) / 128 * words() * 512; }
 };
 
-template <typename T, bool STOCH, bool ROW, bool COL>
+template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
 gtp_status launch_tiles(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  constexpr int smem = COL ? Tile<T>::BYTES : 0;
-  constexpr auto kernel = mx4_tile_kernel<T, STOCH, ROW, COL>;
+  constexpr int smem = COL || RAGGED ? Tile<T>::BYTES : 0;
+  constexpr auto kernel = mx4_tile_kernel<T, STOCH, ROW, COL, RAGGED>;
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> configured{0};
     const uint64_t bit = uint64_t(1) << (dev.device & 63);
@@ -286,11 +429,18 @@ gtp_status launch_tiles(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo 
   return gtp::launch_overlapped(kernel, dim3(unsigned(tiles)), kThreads, smem, st, "mxfp4_quantize", a);
 }
 
-template <typename T, bool STOCH>
+template <typename T, bool STOCH, bool RAGGED>
 gtp_status launch_views(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  if (!a.col.codes) return launch_tiles<T, STOCH, true, false>(a, tiles, dev, st);
-  if (!a.row.codes) return launch_tiles<T, STOCH, false, true>(a, tiles, dev, st);
-  return launch_tiles<T, STOCH, true, true>(a, tiles, dev, st);
+  if (!a.col.codes) return launch_tiles<T, STOCH, true, false, RAGGED>(a, tiles, dev, st);
+  if (!a.row.codes) return launch_tiles<T, STOCH, false, true, RAGGED>(a, tiles, dev, st);
+  return launch_tiles<T, STOCH, true, true, RAGGED>(a, tiles, dev, st);
+}
+
+template <typename T>
+gtp_status launch_views(const TileArgs &a, bool stochastic, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  const bool ragged = !gtp::aligned16(a.src) || a.ld * int64_t(sizeof(T)) % 16 != 0;
+  if (stochastic) return ragged ? launch_views<T, true, true>(a, tiles, dev, st) : launch_views<T, true, false>(a, tiles, dev, st);
+  return ragged ? launch_views<T, false, true>(a, tiles, dev, st) : launch_views<T, false, false>(a, tiles, dev, st);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
@@ -344,12 +494,11 @@ extern "C" gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int6
   a.tiles_n = (cols + kTile - 1) / kTile;
   a.row = {row_codes, row_scales, row.blocks() * 16, row.words()};
   a.col = {col_codes, col_scales, col.blocks() * 16, col.words()};
-  a.vec = gtp::aligned16(src) && a.ld * es % 16 == 0;
   a.rng = gtp::rng_args(rng);
   const int64_t tiles = (rows + kTile - 1) / kTile * a.tiles_n;
   if (tiles > INT32_MAX) return gtp::fail(GTP_E_SHAPE, "more than 2^31 - 1 tiles of 128 x 128");
-  if (src_dt == GTP_F32) return rng ? launch_views<float, true>(a, tiles, dev, st) : launch_views<float, false>(a, tiles, dev, st);
-  return rng ? launch_views<__nv_bfloat16, true>(a, tiles, dev, st) : launch_views<__nv_bfloat16, false>(a, tiles, dev, st);
+  return src_dt == GTP_F32 ? launch_views<float>(a, rng != nullptr, tiles, dev, st)
+                           : launch_views<__nv_bfloat16>(a, rng != nullptr, tiles, dev, st);
 }
 
 extern "C" gtp_status gtp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
@@ -374,21 +523,8 @@ extern "C" gtp_status gtp_mxfp4_dequantize(const uint8_t *codes, const uint8_t *
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
   cudaStream_t st = gtp::as_stream(stream);
-  const int64_t groups = (cols + 7) / 8;
-  int tx = 4;  // a block's four words of codes side by side
-  while (tx < kThreads && tx < groups) tx *= 2;
-  const dim3 block(tx, kThreads / tx);
-  const int64_t gx = (groups + tx - 1) / tx, want = (rows + block.y - 1) / block.y;
-  const int64_t fill = (int64_t(dev.sm_count) * 16 + gx - 1) / gx;
-  const dim3 grid(unsigned(gx), unsigned(std::max<int64_t>(1, std::min<int64_t>({want, fill, 65535}))));
-  const bool vec = cols % 8 == 0 && gtp::aligned16(out);
-  const auto go = [&](auto *kernel, auto *o) {
-    return gtp::launch_overlapped(kernel, grid, block, 0, st, "mxfp4_dequantize", codes, scales, rows, cols, o,
-                                  v.blocks(), v.words());
-  };
-  if (out_dt == GTP_F32)
-    return vec ? go(mx4_values_kernel<float, true>, static_cast<float *>(out))
-               : go(mx4_values_kernel<float, false>, static_cast<float *>(out));
-  return vec ? go(mx4_values_kernel<__nv_bfloat16, true>, static_cast<__nv_bfloat16 *>(out))
-             : go(mx4_values_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16 *>(out));
+  ValueArgs a = {};
+  a.codes = codes, a.scales = scales, a.out = out;
+  a.rows = rows, a.len = cols, a.blocks = v.blocks(), a.words = v.words();
+  return out_dt == GTP_F32 ? launch_values<float>(a, st) : launch_values<__nv_bfloat16>(a, st);
 }

@@ -121,8 +121,49 @@ __device__ __forceinline__ Head head_of(const RotaryArgs &a, int64_t t, int h) {
   return {t * a.src_token + g * a.src_group + gh * a.src_head, t * a.dst_token + g * a.dst_group + gh * a.dst_head};
 }
 
+// One chunk of a head: its two runs, loaded, turned by 8 (cosine, sine) pairs, stored.
+template <typename T, bool IL>
+struct Chunk {
+  Run<T> u, v;
+  T *a, *b;
+  const float2 *w;
+  __device__ __forceinline__ void load(const RotaryArgs &g, const float2 *cs, int64_t t0, int i, int units, int chunks) {
+    const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
+    const Head at = head_of(g, t0 + t, h);
+    const int ia = IL ? 16 * c : 8 * c, ib = IL ? ia + 8 : ia + g.half;
+    const T *src = static_cast<const T *>(g.src) + at.src;
+    u.load(src + ia);
+    v.load(src + ib);
+    a = static_cast<T *>(g.dst) + at.dst + ia;
+    b = static_cast<T *>(g.dst) + at.dst + ib;
+    w = cs + t * g.half + 8 * c;
+  }
+  __device__ __forceinline__ void turn_and_store() {
+    float x[8], y[8];
+    u.get(x);
+    v.get(y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // interleaved: pairs 0-3 of the chunk lie in the first run, 4-7 in the second
+      float &p = IL ? (k < 4 ? x[2 * k] : y[2 * k - 8]) : x[k];
+      float &q = IL ? (k < 4 ? x[2 * k + 1] : y[2 * k - 7]) : y[k];
+      const float2 m = w[k];
+      const float np = p * m.x - q * m.y, nq = p * m.y + q * m.x;
+      p = np;
+      q = nq;
+    }
+    u.set(x);
+    v.set(y);
+    u.store(a);
+    v.store(b);
+  }
+};
+
 // A block owns a.block_tokens tokens: it forms each (token, pair)'s cosine and sine once, in shared
-// memory, and every head of the token uses them.
+// memory, and every head of the token uses them.  The first chunks' loads go out before that, so the
+// sines run under their latency.
+constexpr int kAhead = 2;
+
 template <typename T, bool VEC, bool IL>
 __global__ void __launch_bounds__(kThreads)
     rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Turns turns) {
@@ -131,6 +172,15 @@ __global__ void __launch_bounds__(kThreads)
   gtp::ptx::wait_prior_grid();
   const int64_t t0 = int64_t(blockIdx.x) * a.block_tokens;
   const int nt = int(min(int64_t(a.block_tokens), a.tokens - t0));
+  constexpr int P = VEC ? 8 : 1;
+  const int chunks = a.half / P, units = chunks * a.heads;
+  Chunk<T, IL> ahead[kAhead];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (int(threadIdx.x) + k * kThreads < nt * units)
+        ahead[k].load(a, cs, t0, threadIdx.x + k * kThreads, units, chunks);
+  }
   for (int i = threadIdx.x; i < nt * a.half; i += kThreads) {
     const int t = i / a.half, k = i - t * a.half;
     turn(turns.t[k], position_of(a, t0 + t), a, cs[i].x, cs[i].y);
@@ -138,38 +188,22 @@ __global__ void __launch_bounds__(kThreads)
   const T *src = static_cast<const T *>(a.src);
   T *dst = static_cast<T *>(a.dst);
   __syncthreads();
-  constexpr int P = VEC ? 8 : 1;
-  const int chunks = a.half / P, units = chunks * a.heads;
-  for (int i = threadIdx.x; i < nt * units; i += kThreads) {
-    const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
-    const Head at = head_of(a, t0 + t, h);
-    const float2 *w = cs + t * a.half + P * c;
-    const int ia = IL ? 2 * P * c : P * c, ib = IL ? ia + P : ia + a.half;
-    if constexpr (VEC) {
-      Run<T> u, v;
-      u.load(src + at.src + ia);
-      v.load(src + at.src + ib);
-      float x[8], y[8];
-      u.get(x);
-      v.get(y);
+  if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // interleaved: pairs 0-3 of the chunk lie in the first run, 4-7 in the second
-        float &p = IL ? (k < 4 ? x[2 * k] : y[2 * k - 8]) : x[k];
-        float &q = IL ? (k < 4 ? x[2 * k + 1] : y[2 * k - 7]) : y[k];
-        const float2 m = w[k];
-        const float np = p * m.x - q * m.y, nq = p * m.y + q * m.x;
-        p = np;
-        q = nq;
-      }
-      u.set(x);
-      v.set(y);
-      u.store(dst + at.dst + ia);
-      v.store(dst + at.dst + ib);
-    } else {
+    for (int k = 0; k < kAhead; ++k)
+      if (int(threadIdx.x) + k * kThreads < nt * units) ahead[k].turn_and_store();
+    for (int i = threadIdx.x + kAhead * kThreads; i < nt * units; i += kThreads) {
+      Chunk<T, IL> c;
+      c.load(a, cs, t0, i, units, chunks);
+      c.turn_and_store();
+    }
+  } else {
+    for (int i = threadIdx.x; i < nt * units; i += kThreads) {
+      const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
+      const Head at = head_of(a, t0 + t, h);
       const int ja = IL ? 2 * c : c, jb = IL ? 2 * c + 1 : c + a.half;
       const float x = load_f32(src + at.src + ja), y = load_f32(src + at.src + jb);
-      const float2 m = w[0];
+      const float2 m = cs[t * a.half + c];
       store_f32(dst + at.dst + ja, x * m.x - y * m.y);
       store_f32(dst + at.dst + jb, x * m.y + y * m.x);
     }
