@@ -10,6 +10,7 @@ fallback.  ``gtp_buffer_layout`` is host-only and needs no GPU.
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 from dataclasses import dataclass
 from typing import NamedTuple, Sequence
 
@@ -819,17 +820,24 @@ def _rng(rng):
 
 # The checks below look at each property of a tensor once: a small call is bound by them and the launch.
 
-_FLOATS: dict = {}
+_DTYPES: dict = {}  # torch dtype -> gtp_dtype; filled at the first call (torch is imported late)
+
+
+def _dtype_of(t, name: str):
+    """The gtp_dtype of a tensor: the slow way, which fills the table or says what is wrong."""
+    import torch
+    _DTYPES.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16, torch.uint8: abi.GTP_U8})
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _DTYPES.get(t.dtype)
 
 
 def _float_dtype(t, name: str) -> int:
-    import torch
-    if not _FLOATS:
-        _FLOATS.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16})
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dt = _FLOATS.get(t.dtype)
-    if dt is None:
+    try:
+        dt = _DTYPES[t.dtype]
+    except (AttributeError, KeyError, TypeError):
+        dt = _dtype_of(t, name)
+    if dt != abi.GTP_F32 and dt != abi.GTP_BF16:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     return dt
 
@@ -848,11 +856,12 @@ def _matrix(t, name: str):
 
 def _bytes(t, name: str) -> int:
     """The length of a contiguous uint8 tensor."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.uint8:
-        raise TypeError(f"{name} must be {torch.uint8}, got {t.dtype}")
+    try:
+        dt = _DTYPES[t.dtype]
+    except (AttributeError, KeyError, TypeError):
+        dt = _dtype_of(t, name)
+    if dt != abi.GTP_U8:
+        raise TypeError(f"{name} must be uint8, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.numel()
@@ -921,9 +930,8 @@ def _mxfp4_product(Aq, As, Bq, Bs, names: str):
 
 
 def _bf16_out(t, rows: int, cols: int, name: str) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if _float_dtype(t, name) != abi.GTP_BF16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.shape != (rows, cols) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{rows}, {cols}]")
     return t.data_ptr()
@@ -993,7 +1001,6 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
     CUDA tensor of the tokens' positions, or None for
     pos0 + (t // tokens_per_position) % positions_per_sequence (0: no modulus).  layout: "half" pairs
     (i, i + rot_dim/2), "interleaved" (2i, 2i+1).  inverse=True is the gradient."""
-    import torch
     dt = _float_dtype(src, "src")
     shape = src.shape
     if _float_dtype(dst, "dst") != dt or dst.shape != shape:
@@ -1012,17 +1019,22 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
         T, G, H = shape[:3]
     wide = 0
     if positions is not None:
+        import torch
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
         wide = int(positions.dtype == torch.int64)
         _require(positions, positions.dtype, "positions", 1)
         if positions.numel() != T:
             raise ValueError("one position a token")
-    if not isinstance(turns, C.Array):
-        turns = (C.c_uint64 * len(turns))(*turns)
+    pairs = len(turns)
+    if isinstance(turns, C.Array):
+        at = C.addressof(turns)
+    else:  # any sequence of integers
+        turns = array("Q", turns)
+        at = turns.buffer_info()[0]
     d = abi.ROTARY_DESC_PACK(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
                              positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
-                             C.addressof(turns), G, H, D, 2 * len(turns), dt, wide, layout == "interleaved",
+                             at, G, H, D, 2 * pairs, dt, wide, layout == "interleaved",
                              bool(inverse), scale, 0)
     _check(lib().gtp_rotary(d, _stream(stream)), "gtp_rotary")
 

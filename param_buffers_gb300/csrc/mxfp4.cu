@@ -41,9 +41,9 @@ constexpr int kThreads = 256;
 // lanes hold to write its 64 bytes together, lie in different banks.  Both directions then run without
 // bank conflicts.
 //
-// A source whose rows do not all start on 16 bytes (RAGGED: any odd row length) is read a row a warp, in
-// 32-bit words or, where those straddle, in elements, neighbouring lanes on neighbouring addresses, and
-// both passes take it from shared memory.
+// A source whose rows do not all start on 16 bytes (RAGGED: any odd row length) is read in the 16-byte
+// vectors that cover a thread's elements, one more than they fill, and shifted into place in registers;
+// the first and last elements of the source, whose vectors would reach outside it, go one by one.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -69,6 +69,42 @@ __device__ __forceinline__ uint32_t word_of(const __nv_bfloat16 *p, int n) {
   const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
   if (n > 1 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) return *reinterpret_cast<const uint32_t *>(p);
   return (n > 0 ? uint32_t(q[0]) : 0u) | (n > 1 ? uint32_t(q[1]) << 16 : 0u);
+}
+
+struct ViewArgs {
+  uint8_t *codes, *scales;
+  int64_t pitch;  // bytes of a row of codes
+  int64_t words;  // atoms of a 128-row tile
+};
+
+struct TileArgs {
+  const void *src;
+  int64_t rows, cols, ld, src_bytes;
+  int64_t tiles_n;
+  ViewArgs row, col;
+  gtp::RngArgs rng;
+};
+
+// The 16-byte vectors around the 16 elements at p lie inside the source.
+template <typename T>
+__device__ __forceinline__ bool window_inside(const T *p, const TileArgs &a) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15), begin = reinterpret_cast<uintptr_t>(a.src);
+  return b >= begin && b + 16 * (Tile<T>::THREAD_WORDS / 4 + 1) <= begin + uintptr_t(a.src_bytes);
+}
+
+// 16 elements at an element-aligned address, out of the vectors around them: whole words by two rounds of
+// selects on the address's bits, a half word by funnel shifts.
+template <typename T, int N>
+__device__ __forceinline__ void load_shifted(const T *p, uint32_t (&w)[N]) {
+  const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+  uint32_t t[N + 4];
+  load_words(reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)), t);
+#pragma unroll
+  for (int k = 0; k < N + 2; ++k) t[k] = s & 8u ? t[k + 2] : t[k];
+#pragma unroll
+  for (int k = 0; k < N + 1; ++k) t[k] = s & 4u ? t[k + 1] : t[k];
+#pragma unroll
+  for (int k = 0; k < N; ++k) w[k] = sizeof(T) == 2 ? __funnelshift_r(t[k], t[k + 1], 8 * (s & 2u)) : t[k];
 }
 
 // Index of word `w` of row `r` in the tile.
@@ -118,25 +154,17 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
   }
 }
 
-struct ViewArgs {
-  uint8_t *codes, *scales;
-  int64_t pitch;  // bytes of a row of codes
-  int64_t words;  // atoms of a 128-row tile
-};
-
-struct TileArgs {
-  const void *src;
-  int64_t rows, cols, ld;
-  int64_t tiles_n;
-  ViewArgs row, col;
-  gtp::RngArgs rng;
-};
+// Blocks an SM that the registers are held to: latency against spills.  On [8192, 8192], both views, 2 / 3 / 4
+// blocks: bf16 45.8 / 39.5 / 37.3 us to nearest and 71.6 / 71.2 / 66.5 stochastically; fp32 66.7 / 80.3 / 106
+// (its 64 registers of tile words spill from 3 on), but the rowwise view alone 47.7 / 46.3 / 52.9.
+template <typename T, bool COL>
+constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL ? 2 : 3;
 
 template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
-__global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
   using F = Tile<T>;
   constexpr int TW = F::THREAD_WORDS;
-  extern __shared__ __align__(16) uint32_t tile[];  // COL or RAGGED: [128][WORDS]
+  extern __shared__ __align__(16) uint32_t tile[];  // COL: [128][WORDS]
   __shared__ __align__(16) uint8_t atom[2][512];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
@@ -147,58 +175,30 @@ __global__ void __launch_bounds__(kThreads) mx4_tile_kernel(const __grid_constan
   const int64_t c0 = kTile * tn + 16 * seg;
   const int nc = int(max(int64_t(0), min(int64_t(16), a.cols - c0)));  // its columns inside the matrix
   uint32_t w[4][TW];
-  if constexpr (RAGGED) {
-    const int warp = tid >> 5, lane = tid & 31;
-    constexpr int LW = F::WORDS / 32;  // words a lane takes of a row
 #pragma unroll
-    for (int b = 0; b < 16; b += 8) {  // a warp's 16 rows, 8 in flight
-      uint32_t v[8][LW];
+  for (int it = 0; it < 4; ++it) {
+    const int64_t r = kTile * tm + 32 * it + r32;
+    const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
+    if (r >= a.rows) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t r = kTile * tm + 16 * warp + b + k;
-        const T *p = static_cast<const T *>(a.src) + r * a.ld + kTile * tn;
-        const int n = r < a.rows ? int(min(int64_t(kTile), a.cols - kTile * tn)) : 0;
-#pragma unroll
-        for (int i = 0; i < LW; ++i) v[k][i] = word_of(p + F::PER * (lane + 32 * i), n - F::PER * (lane + 32 * i));
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < LW; ++i) tile[word_at<T>(16 * warp + b + k, lane + 32 * i)] = v[k][i];
-    }
-    __syncthreads();
-    if (ROW) {
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int i = 0; i < TW / 4; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(tile + word_at<T>(32 * it + r32, seg * TW + 4 * i));
-          w[it][4 * i] = v.x, w[it][4 * i + 1] = v.y, w[it][4 * i + 2] = v.z, w[it][4 * i + 3] = v.w;
-        }
-    }
-  } else {
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int64_t r = kTile * tm + 32 * it + r32;
-      const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
-      if (r >= a.rows) {
-#pragma unroll
-        for (int i = 0; i < TW; ++i) w[it][i] = 0;
-      } else if (nc == 16) {
+      for (int i = 0; i < TW; ++i) w[it][i] = 0;
+    } else if (nc == 16 && (!RAGGED || window_inside(p, a))) {
+      if (RAGGED)
+        load_shifted(p, w[it]);
+      else
         load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
-      } else {
+    } else {
 #pragma unroll
-        for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
-      }
+      for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
     }
-    if (COL) {
+  }
+  if (COL) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int i = 0; i < TW / 4; ++i)
-          *reinterpret_cast<uint4 *>(tile + word_at<T>(32 * it + r32, seg * TW + 4 * i)) =
-              make_uint4(w[it][4 * i], w[it][4 * i + 1], w[it][4 * i + 2], w[it][4 * i + 3]);
-    }
+      for (int i = 0; i < TW / 4; ++i)
+        *reinterpret_cast<uint4 *>(tile + word_at<T>(32 * it + r32, seg * TW + 4 * i)) =
+            make_uint4(w[it][4 * i], w[it][4 * i + 1], w[it][4 * i + 2], w[it][4 * i + 3]);
   }
   if (ROW) {
 #pragma unroll
@@ -415,7 +415,7 @@ struct View {
 
 template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
 gtp_status launch_tiles(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  constexpr int smem = COL || RAGGED ? Tile<T>::BYTES : 0;
+  constexpr int smem = COL ? Tile<T>::BYTES : 0;
   constexpr auto kernel = mx4_tile_kernel<T, STOCH, ROW, COL, RAGGED>;
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> configured{0};
@@ -491,6 +491,7 @@ extern "C" gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int6
   TileArgs a = {};
   a.src = src;
   a.rows = rows, a.cols = cols, a.ld = rows > 1 ? src_ld : 0;
+  a.src_bytes = ((rows - 1) * a.ld + cols) * es;
   a.tiles_n = (cols + kTile - 1) / kTile;
   a.row = {row_codes, row_scales, row.blocks() * 16, row.words()};
   a.col = {col_codes, col_scales, col.blocks() * 16, col.words()};

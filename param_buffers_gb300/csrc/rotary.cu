@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "device.h"
+#include "fastdiv.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gtp {
@@ -39,6 +40,8 @@ struct RotaryArgs {
   int64_t pos0, tokens_per_position, positions_per_sequence;
   int32_t heads, group_heads, head_dim, half;  // heads: over all groups
   int32_t inverse, positions64, block_tokens, copy;  // copy: the part that keeps its values is written
+  int32_t chunks, units;                             // chunks of a head and of a token
+  gtp::FastDiv by_half, by_units, by_chunks, by_group;
   float scale;
 };
 
@@ -117,7 +120,7 @@ struct Head {
 };
 
 __device__ __forceinline__ Head head_of(const RotaryArgs &a, int64_t t, int h) {
-  const int g = h / a.group_heads, gh = h - g * a.group_heads;
+  const int g = gtp::fast_div(h, a.by_group), gh = h - g * a.group_heads;
   return {t * a.src_token + g * a.src_group + gh * a.src_head, t * a.dst_token + g * a.dst_group + gh * a.dst_head};
 }
 
@@ -127,8 +130,10 @@ struct Chunk {
   Run<T> u, v;
   T *a, *b;
   const float2 *w;
-  __device__ __forceinline__ void load(const RotaryArgs &g, const float2 *cs, int64_t t0, int i, int units, int chunks) {
-    const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
+  int pitch;
+  __device__ __forceinline__ void load(const RotaryArgs &g, const float2 *cs, int64_t t0, int i) {
+    const int t = gtp::fast_div(i, g.by_units), r = i - t * g.units;
+    const int h = gtp::fast_div(r, g.by_chunks), c = r - h * g.chunks;
     const Head at = head_of(g, t0 + t, h);
     const int ia = IL ? 16 * c : 8 * c, ib = IL ? ia + 8 : ia + g.half;
     const T *src = static_cast<const T *>(g.src) + at.src;
@@ -136,18 +141,21 @@ struct Chunk {
     v.load(src + ib);
     a = static_cast<T *>(g.dst) + at.dst + ia;
     b = static_cast<T *>(g.dst) + at.dst + ib;
-    w = cs + t * g.half + 8 * c;
+    w = cs + t * g.half + 2 * c;
+    pitch = 2 * g.chunks;
   }
   __device__ __forceinline__ void turn_and_store() {
     float x[8], y[8];
     u.get(x);
     v.get(y);
+    float4 m2;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      if ((k & 1) == 0) m2 = *reinterpret_cast<const float4 *>(w + (k >> 1) * pitch);
       // interleaved: pairs 0-3 of the chunk lie in the first run, 4-7 in the second
       float &p = IL ? (k < 4 ? x[2 * k] : y[2 * k - 8]) : x[k];
       float &q = IL ? (k < 4 ? x[2 * k + 1] : y[2 * k - 7]) : y[k];
-      const float2 m = w[k];
+      const float2 m = k & 1 ? make_float2(m2.z, m2.w) : make_float2(m2.x, m2.y);
       const float np = p * m.x - q * m.y, nq = p * m.y + q * m.x;
       p = np;
       q = nq;
@@ -162,44 +170,56 @@ struct Chunk {
 // A block owns a.block_tokens tokens: it forms each (token, pair)'s cosine and sine once, in shared
 // memory, and every head of the token uses them.  The first chunks' loads go out before that, so the
 // sines run under their latency.
-constexpr int kAhead = 2;
+//
+// Chunks a thread (all loaded ahead) and blocks an SM, measured: bf16 (32768 tokens of 20 heads of 128) 49.3 us
+// with 2 and 5 against 56.7 (2, unbounded registers), 51.9 (1 ahead, 6) and 63.1 (1 and 6); fp32 (32769
+// tokens of 20 heads, 64 of 128 elements turned) 101.7 us with 1 and 6 against 110.2 (2 and 5).
+template <typename T>
+struct Shape {
+  static constexpr int CHUNKS = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int MIN_BLOCKS = sizeof(T) == 2 ? 5 : 6;
+};
+
 
 template <typename T, bool VEC, bool IL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, Shape<T>::MIN_BLOCKS)
     rotary_kernel(const __grid_constant__ RotaryArgs a, const __grid_constant__ Turns turns) {
-  extern __shared__ float2 cs[];  // [block_tokens][half]
+  extern __shared__ __align__(16) float2 cs[];  // [block_tokens][half]
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int64_t t0 = int64_t(blockIdx.x) * a.block_tokens;
   const int nt = int(min(int64_t(a.block_tokens), a.tokens - t0));
-  constexpr int P = VEC ? 8 : 1;
-  const int chunks = a.half / P, units = chunks * a.heads;
-  Chunk<T, IL> ahead[kAhead];
+  constexpr int P = VEC ? 8 : 1, N = Shape<T>::CHUNKS;
+  const int all = nt * a.units;
+  Chunk<T, IL> ahead[N];
   if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (int(threadIdx.x) + k * kThreads < nt * units)
-        ahead[k].load(a, cs, t0, threadIdx.x + k * kThreads, units, chunks);
+    for (int k = 0; k < N; ++k)
+      if (int(threadIdx.x) + k * kThreads < all) ahead[k].load(a, cs, t0, threadIdx.x + k * kThreads);
   }
   for (int i = threadIdx.x; i < nt * a.half; i += kThreads) {
-    const int t = i / a.half, k = i - t * a.half;
-    turn(turns.t[k], position_of(a, t0 + t), a, cs[i].x, cs[i].y);
+    const int t = gtp::fast_div(i, a.by_half), k = i - t * a.half;
+    // a chunk's eight pairs, two by two, one run of all chunks after the other: lanes on neighbouring
+    // chunks then read neighbouring 16 bytes
+    const int at = VEC ? t * a.half + 2 * ((k & 7) >> 1) * a.chunks + 2 * (k >> 3) + (k & 1) : i;
+    turn(turns.t[k], position_of(a, t0 + t), a, cs[at].x, cs[at].y);
   }
   const T *src = static_cast<const T *>(a.src);
   T *dst = static_cast<T *>(a.dst);
   __syncthreads();
   if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (int(threadIdx.x) + k * kThreads < nt * units) ahead[k].turn_and_store();
-    for (int i = threadIdx.x + kAhead * kThreads; i < nt * units; i += kThreads) {
+    for (int k = 0; k < N; ++k)
+      if (int(threadIdx.x) + k * kThreads < all) ahead[k].turn_and_store();
+    for (int i = threadIdx.x + N * kThreads; i < all; i += kThreads) {
       Chunk<T, IL> c;
-      c.load(a, cs, t0, i, units, chunks);
+      c.load(a, cs, t0, i);
       c.turn_and_store();
     }
   } else {
-    for (int i = threadIdx.x; i < nt * units; i += kThreads) {
-      const int t = i / units, r = i - t * units, h = r / chunks, c = r - h * chunks;
+    for (int i = threadIdx.x; i < all; i += kThreads) {
+      const int t = gtp::fast_div(i, a.by_units), r = i - t * a.units;
+      const int h = gtp::fast_div(r, a.by_chunks), c = r - h * a.chunks;
       const Head at = head_of(a, t0 + t, h);
       const int ja = IL ? 2 * c : c, jb = IL ? 2 * c + 1 : c + a.half;
       const float x = load_f32(src + at.src + ja), y = load_f32(src + at.src + jb);
@@ -211,9 +231,9 @@ __global__ void __launch_bounds__(kThreads)
   // the part of a head that keeps its values; in place there is nothing to do
   const int rest = a.head_dim - 2 * a.half;
   if (rest && a.copy) {
-    const int per = VEC ? rest / 8 : rest, all = per * a.heads;
-    for (int i = threadIdx.x; i < nt * all; i += kThreads) {
-      const int t = i / all, r = i - t * all, h = r / per, c = 2 * a.half + P * (r - h * per);
+    const int per = VEC ? rest / 8 : rest, kept = per * a.heads;
+    for (int i = threadIdx.x; i < nt * kept; i += kThreads) {
+      const int t = i / kept, r = i - t * kept, h = r / per, c = 2 * a.half + P * (r - h * per);
       const Head at = head_of(a, t0 + t, h);
       if constexpr (VEC) {
         Run<T> u;
@@ -228,9 +248,14 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool VEC>
 gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStream_t st) {
-  // about two chunks a thread: enough tokens to a block to fill it, few enough to spread a short batch
-  const int64_t units = int64_t(a.heads) * (a.half / (VEC ? 8 : 1));
-  a.block_tokens = int32_t(std::max<int64_t>(1, std::min<int64_t>({2 * kThreads / units, 16, a.tokens})));
+  // as many tokens to a block as fill its threads' chunks, and no more, so that a short batch spreads
+  a.chunks = a.half / (VEC ? 8 : 1);
+  a.units = a.heads * a.chunks;
+  a.by_half = gtp::make_fastdiv(a.half);
+  a.by_units = gtp::make_fastdiv(a.units);
+  a.by_chunks = gtp::make_fastdiv(a.chunks);
+  a.by_group = gtp::make_fastdiv(a.group_heads);
+  a.block_tokens = int32_t(std::max<int64_t>(1, std::min<int64_t>({Shape<T>::CHUNKS * kThreads / a.units, 16, a.tokens})));
   const unsigned grid = unsigned((a.tokens + a.block_tokens - 1) / a.block_tokens);
   const size_t smem = size_t(a.block_tokens) * a.half * sizeof(float2);
   return interleaved ? gtp::launch_overlapped(rotary_kernel<T, VEC, true>, grid, kThreads, smem, st, "rotary", a, turns)
