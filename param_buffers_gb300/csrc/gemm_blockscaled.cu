@@ -437,7 +437,10 @@ struct BlockScaledPair {
   static_assert(!SF_INPLACE || SF_SLOT == LAND_BYTES, "in-place slots");
   static constexpr int THREADS = kBsThreads + 32 * SCALE_WARPS;
   static constexpr int SMEM_EPI = kBsEpiWarps * kBsEpiBuf;
-  static constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SF + SMEM_LAND + SMEM_EPI + SMEM_CTRL + 1024;
+  // the dynamic shared memory is declared 1024-byte aligned; MXFP4 counts on that, since its sixth stage leaves no
+  // room for a kernel-side alignment (and gives up, with the wait flag set, where it does not hold)
+  static constexpr int SLACK = FMT == kMxfp4 ? 0 : 1024;
+  static constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SF + SMEM_LAND + SMEM_EPI + SMEM_CTRL + SLACK;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t SFA_COL = BN;
   static constexpr uint32_t SFB_COL = BN + 4 * WORDS * STAGES;
@@ -447,16 +450,29 @@ struct BlockScaledPair {
   static_assert((2 * STAGES + 3 + LFULL) * 8 + 8 <= SMEM_CTRL, "barriers");
 };
 
+// A unit's tile and k-range; `part` is -1 for a whole tile, or which 128-column half of it a half-width
+// tail unit covers (MXFP4; see run_mxfp4).
+template <int FMT>
+__device__ __forceinline__ void decode_bs_unit(const Problem &p, int u, int &tm, int &tn, int &kb0, int &kb1, int &part) {
+  if constexpr (FMT == kMxfp4) {
+    decode_unit_half(p, u, tm, tn, kb0, kb1, part);
+  } else {
+    decode_unit(p, u, tm, tn, kb0, kb1);
+    part = -1;
+  }
+}
+
 template <int FMT, int EPI, int S, bool TSF, bool TILED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT, S, TSF, TILED>::THREADS, 1)
     gemm_blockscaled_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSA,
-                                 const __grid_constant__ CUtensorMap tmSB, const uint8_t *__restrict__ sfa_g,
+                                 const __grid_constant__ CUtensorMap tmSB,
+                                 const __grid_constant__ CUtensorMap tmBh, const uint8_t *__restrict__ sfa_g,
                                  const uint8_t *__restrict__ sfb_g, const float *__restrict__ a_amax,
                                  const float *__restrict__ b_amax, const Problem p) {
   using F = BlockScaledPair<FMT, S, TSF, TILED>;
   constexpr int STAGES = F::STAGES;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sA = smem;
   uint8_t *sB = sA + STAGES * F::A_STAGE;
@@ -476,6 +492,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  if (F::SLACK == 0 && smem != smem_raw) {  // the same in every CTA: all of them leave
+    if (threadIdx.x == 0) atomicOr(&g_gtp_wait_timeouts, 0x4u);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       // the even CTA's expect_tx arrival (both CTAs' operand bytes) and one arrival from
@@ -528,8 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
       for (int s = 0; s < STAGES; ++s) armed[s] = armed_l[s] = -1;
       const uint32_t full0 = mapa_shared(&full[0], 0);
       for (int u = pair_id; u < p.num_units; u += npairs) {
-        int tm, tn, kb0, kb1;
-        decode_unit(p, u, tm, tn, kb0, kb1);
+        int tm, tn, kb0, kb1, part;
+        decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
           // the operands go as soon as the stage is free: the scale warps signal the full
@@ -549,11 +569,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
             armed_l[stage] = int(phase);
           }
           if (rank == 0) {  // the even CTA's barrier counts both CTAs' bytes
-            mbar_arrive_expect_tx(&full[stage], 2 * (F::STAGE_TX + (F::SF_TILED ? F::SF_SLOT : 0)));
+            const uint32_t whole = 2 * (F::STAGE_TX + (F::SF_TILED ? F::SF_SLOT : 0));
+            mbar_arrive_expect_tx(&full[stage], part < 0 ? whole : whole - (F::B_STAGE + F::SFB_STAGE));
             armed[stage] = int(phase);
           }
           tma_load_2d_pair(&tmA, bar, sA + stage * F::A_STAGE, kb * F::BK, tm * F::BMP + F::BMC * int(rank));
-          tma_load_2d_pair(&tmB, bar, sB + stage * F::B_STAGE, kb * F::BK, tn * BN + F::BNC * int(rank));
+          if (FMT != kMxfp4 || part < 0)
+            tma_load_2d_pair(&tmB, bar, sB + stage * F::B_STAGE, kb * F::BK, tn * BN + F::BNC * int(rank));
+          else
+            tma_load_2d_pair(&tmBh, bar, sB + stage * F::B_STAGE, kb * F::BK,
+                             tn * BN + F::BNC * part + F::BNC / 2 * int(rank));
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -582,8 +607,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
         uint32_t phase = 0;
         bool ok = true;
         for (int u = pair_id; ok && u < p.num_units; u += npairs) {
-          int tm, tn, kb0, kb1;
-          decode_unit(p, u, tm, tn, kb0, kb1);
+          int tm, tn, kb0, kb1, part;
+          decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u)) {
               ok = false;
@@ -594,8 +619,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
             const int w0 = kb * F::WORDS;
             if constexpr (FMT == kMxfp4) {
               tma_load_3d_pair(&tmSA, bar, slot, 0, w0, 2 * tm + int(rank));
-              tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, w0, 2 * tn);
-              tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, w0, 2 * tn + 1);
+              tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, w0, 2 * tn + (part > 0 ? 1 : 0));
+              if (part < 0)
+                tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, w0, 2 * tn + 1);
             } else {
               tma_load_2d_pair(&tmSA, bar, slot, 0, (2 * tm + int(rank)) * wrow + w0);
               tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, 2 * tn * wrow + w0);
@@ -865,7 +891,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
     }
   } else if (warp == 1) {  // -------- MMA issuer (even CTA only): the whole warp waits, one elected lane issues
     if (rank == 0) {
-      auto copy_scales = [&](int s) {
+      auto copy_scales = [&](int s, bool both) {
         const uint32_t sfa_t = tmem_base + F::SFA_COL + 4 * F::WORDS * s;
         const uint32_t sfb_t = tmem_base + F::SFB_COL + 8 * F::WORDS * s;
         const uint32_t *fa = sfa_of(s);
@@ -876,20 +902,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           // B rows 0-127 and 128-255 of word w: atoms [w][half], or [half][w] when tiled
           const int b0 = F::SF_TILED ? w : 2 * w, b1 = F::SF_TILED ? F::WORDS + w : 2 * w + 1;
           tmem_cp_32x128b_warpx4_pair(sfb_t + 8 * w, sdesc_noswizzle_rows16(smem_u32(fb + 128 * b0)));
-          tmem_cp_32x128b_warpx4_pair(sfb_t + 8 * w + 4, sdesc_noswizzle_rows16(smem_u32(fb + 128 * b1)));
+          if (both) tmem_cp_32x128b_warpx4_pair(sfb_t + 8 * w + 4, sdesc_noswizzle_rows16(smem_u32(fb + 128 * b1)));
         }
       };
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = pair_id; ok && u < p.num_units; u += npairs) {
-        int tm, tn, kb0, kb1;
-        decode_unit(p, u, tm, tn, kb0, kb1);
+        int tm, tn, kb0, kb1, part;
+        decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
+        const int width = part < 0 ? BN : BN / 2;
         // the tile's first scale copies need only their stage, not the accumulator: issued
         // before the epilogue releases it, they run while the previous tile drains
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, abort_flag, err, 0x4u))) break;
         tc_fence_after();
-        if (elect_one_sync()) copy_scales(stage);
+        if (elect_one_sync()) copy_scales(stage, part < 0);
         __syncwarp();
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty, acc_phase ^ 1u, abort_flag, err, 0x2u))) break;
         tc_fence_after();
@@ -904,7 +931,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           if (elect_one_sync()) {
             // each later stage's scale copy goes right before its own MMAs: issuing it a
             // stage early (when that stage had already landed) measured slower
-            if (kb > kb0) copy_scales(stage);
+            if (kb > kb0) copy_scales(stage, part < 0);
             const uint32_t sfa_t = tmem_base + F::SFA_COL + 4 * F::WORDS * stage;
             const uint32_t sfb_t = tmem_base + F::SFB_COL + 8 * F::WORDS * stage;
             const uint32_t a0 = smem_u32(sA + stage * F::A_STAGE);
@@ -918,7 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
                 mma_mxf8_block_scale_pair(tmem_base, ad, bd, idesc_mxf8_e4m3(F::BMP, BN, uint32_t(k)), sfa_t, sfb_t,
                                           acc);
               else if (FMT == kMxfp4)
-                mma_mxf4_block_scale_pair(tmem_base, ad, bd, idesc_mxf4_e2m1(F::BMP, BN, 2u * uint32_t(k & 1)),
+                mma_mxf4_block_scale_pair(tmem_base, ad, bd, idesc_mxf4_e2m1(F::BMP, width, 2u * uint32_t(k & 1)),
                                           sfa_t + 4 * (k >> 1), sfb_t + 8 * (k >> 1), acc);
               else
                 mma_nvf4_block_scale_pair(tmem_base, ad, bd, idesc_nvf4_e2m1(F::BMP, BN), sfa_t + 4 * k,
@@ -956,12 +983,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
     if (FMT == kNvfp4)
       alpha = float(1.0 / (double(gtp::nv::tensor_scale(__ldg(a_amax))) * double(gtp::nv::tensor_scale(__ldg(b_amax)))));
     for (int u = pair_id; u < p.num_units; u += npairs) {
-      int tm, tn, kb0, kb1;
-      decode_unit(p, u, tm, tn, kb0, kb1);
+      int tm, tn, kb0, kb1, part;
+      decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
       const bool ok = mbar_wait(tfull, acc_phase, abort_flag, err, 0x8u);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const int row = tm * F::BMP + F::BMC * int(rank) + 32 * quarter;
+      // nothing of this warp's to write: a half-width tile's other half, or rows past the output
+      if (FMT == kMxfp4 && ((part >= 0 && half == 1) || row >= p.m_dim)) {
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0);
+        acc_phase ^= 1u;
+        continue;
+      }
       const uint32_t tbase = tmem_base + (uint32_t(32 * quarter) << 16) + uint32_t(half * (BN / 2));
       uint32_t r[4][32];
 #pragma unroll
@@ -989,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           stage_rows64<EPI>(buf, lane, r[q >> 1], 16 * (q & 1));
         fence_proxy_async_smem();
         __syncwarp();
-        const int col = tn * BN + half * (BN / 2) + q * CW;
+        const int col = tn * BN + (part > 0 ? BN / 2 : 0) + half * (BN / 2) + q * CW;
         if (lane == 0) {
           if (row < p.m_dim && col < p.n_dim) {
             if (EPI == kStoreBf16)
@@ -1031,9 +1064,9 @@ gtp_status launch_blockscaled(const CUtensorMap &a, const CUtensorMap &b, const 
 
 template <int FMT, int EPI, int S, bool TSF, bool TILED = false>
 gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &d,
-                                   const CUtensorMap &sa, const CUtensorMap &sb, const uint8_t *As, const uint8_t *Bs,
-                                   const float *a_amax, const float *b_amax, const Problem &p, int grid,
-                                   const gtp::DeviceInfo &dev, cudaStream_t st) {
+                                   const CUtensorMap &sa, const CUtensorMap &sb, const CUtensorMap &bh,
+                                   const uint8_t *As, const uint8_t *Bs, const float *a_amax, const float *b_amax,
+                                   const Problem &p, int grid, const gtp::DeviceInfo &dev, cudaStream_t st) {
   using F = BlockScaledPair<FMT, S, TSF, TILED>;
   constexpr auto kernel = gemm_blockscaled_pair_kernel<FMT, EPI, S, TSF, TILED>;
   static std::atomic<uint64_t> configured{0};
@@ -1042,7 +1075,7 @@ gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, c
                                 FMT == kMxfp8   ? "gemm_mxfp8_pair"
                                 : FMT == kMxfp4 ? "gemm_mxfp4_pair"
                                                 : "gemm_nvfp4_pair",
-                                a, b, d, sa, sb, As, Bs, a_amax, b_amax, p);
+                                a, b, d, sa, sb, bh, As, Bs, a_amax, b_amax, p);
 }
 
 // The CTA pair unless the output has at most 128 rows (half of every pair tile would be
@@ -1122,16 +1155,16 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
     // for 5 stages with one)
     if constexpr (FMT == kMxfp8) {
       if (tiled)
-        return launch_blockscaled_pair<FMT, EPI, 6, true, true>(a, b, d, sa, sb, As, Bs, a_amax, b_amax, p, grid, dev,
+        return launch_blockscaled_pair<FMT, EPI, 6, true, true>(a, b, d, sa, sb, b, As, Bs, a_amax, b_amax, p, grid, dev,
                                                                 st);
       if (sf_tma)
-        return launch_blockscaled_pair<FMT, EPI, 6, true>(a, b, d, sa, sb, As, Bs, a_amax, b_amax, p, grid, dev, st);
-      return launch_blockscaled_pair<FMT, EPI, 6, false>(a, b, d, sa, sb, As, Bs, a_amax, b_amax, p, grid, dev, st);
+        return launch_blockscaled_pair<FMT, EPI, 6, true>(a, b, d, sa, sb, b, As, Bs, a_amax, b_amax, p, grid, dev, st);
+      return launch_blockscaled_pair<FMT, EPI, 6, false>(a, b, d, sa, sb, b, As, Bs, a_amax, b_amax, p, grid, dev, st);
     } else {  // NVFP4 scale arrays are always 16-byte aligned with 16-byte multiple rows
       if (tiled)
-        return launch_blockscaled_pair<FMT, EPI, 5, true, true>(a, b, d, sa, sb, As, Bs, a_amax, b_amax, p, grid, dev,
+        return launch_blockscaled_pair<FMT, EPI, 5, true, true>(a, b, d, sa, sb, b, As, Bs, a_amax, b_amax, p, grid, dev,
                                                                 st);
-      return launch_blockscaled_pair<FMT, EPI, 5, true>(a, b, d, sa, sb, As, Bs, a_amax, b_amax, p, grid, dev, st);
+      return launch_blockscaled_pair<FMT, EPI, 5, true>(a, b, d, sa, sb, b, As, Bs, a_amax, b_amax, p, grid, dev, st);
     }
   }
   p.tiles_m = int((m_dim + BM - 1) / BM);
@@ -1151,18 +1184,23 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
   return launch_blockscaled<FMT, EPI, 3>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
 }
 
+// Stages measured, PFLOP/s for 4 / 5 / 6: fc1 fprop 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 /
+// 5.30.  MXFP4's scale words take half of NVFP4's room, which is what makes the sixth fit.
+constexpr int kMx4Stages = 6;
+
 // The MXFP4 products: any contraction length (code rows hold whole blocks of 32, zero past the end;
 // TMA reads zeros beyond them, codes and scales alike, up to the stage's 256).
 template <int EPI>
 gtp_status run_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, const uint8_t *Bs, void *D, int64_t m_dim,
                      int64_t n_dim, int64_t k_dim, bool allow_split, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  using F = BlockScaledPair<kMxfp4, 5, true, true>;
+  using F = BlockScaledPair<kMxfp4, kMx4Stages, true, true>;
   constexpr CU kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, kU32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   constexpr CUtensorMapSwizzle kSW64 = CU_TENSOR_MAP_SWIZZLE_64B;
   const int64_t blocks = (k_dim + 31) / 32, row_bytes = 16 * blocks, words = (blocks + 3) / 4;
-  CUtensorMap a, b, d, sa, sb;
+  CUtensorMap a, b, bh, d, sa, sb;
   if (gtp_status s = gtp::encode_tmap_2d(&a, kU8, Aq, row_bytes, m_dim, row_bytes, F::BK, F::BMC, kSW128)) return s;
   if (gtp_status s = gtp::encode_tmap_2d(&b, kU8, Bq, row_bytes, n_dim, row_bytes, F::BK, F::BNC, kSW128)) return s;
+  if (gtp_status s = gtp::encode_tmap_2d(&bh, kU8, Bq, row_bytes, n_dim, row_bytes, F::BK, F::BNC / 2, kSW128)) return s;
   if (gtp_status s = gtp::encode_tmap_3d(&sa, kU32, As, 128, words, (m_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
     return s;
   if (gtp_status s = gtp::encode_tmap_3d(&sb, kU32, Bs, 128, words, (n_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
@@ -1178,12 +1216,28 @@ gtp_status run_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, co
   p.tiles_n = int((n_dim + BN - 1) / BN);
   p.k_blocks = int((k_dim + F::K_STAGE - 1) / F::K_STAGE);
   const int tiles = p.tiles_m * p.tiles_n, pairs = dev.sm_count / 2;
+  // A last wave of T tiles over at least 2 T pairs runs as 2 T half-width tiles (N = 128 MMAs on the two
+  // 128-row halves of B, each with its own scale atoms), so it takes half a wave: fc1 dgrad, 256 tiles on 76
+  // pairs, 3.5 waves instead of 4.  A split contraction counts its units in whole waves and pays one more
+  // fp32 copy of the output a split (0.06 of a wave's worth each, as choose_splits has it).
+  const int last = tiles % pairs;
+  const bool halves = last > 0 && 2 * last <= pairs;
+  const double unsplit = double(tiles) / pairs / (tiles / pairs + (last == 0 ? 0.0 : halves ? 0.5 : 1.0));
   p.splits = allow_split ? choose_splits(tiles, p.k_blocks, pairs) : 1;
+  if (p.splits > 1) {
+    const int64_t units = int64_t(tiles) * p.splits;
+    if (unsplit >= double(units) / double((units + pairs - 1) / pairs * pairs) - 0.06 * (p.splits - 1)) p.splits = 1;
+  }
   p.num_units = tiles * p.splits;
   p.group_m = 2;
   finalize_problem(p);
+  if (p.splits == 1 && halves) {
+    p.tail_half = 1;
+    p.tail_first = tiles - last;
+    p.num_units = tiles + last;
+  }
   const int grid = 2 * std::min(p.num_units, pairs);
-  return launch_blockscaled_pair<kMxfp4, EPI, 5, true, true>(a, b, d, sa, sb, As, Bs, nullptr, nullptr, p, grid, dev,
+  return launch_blockscaled_pair<kMxfp4, EPI, kMx4Stages, true, true>(a, b, d, sa, sb, bh, As, Bs, nullptr, nullptr, p, grid, dev,
                                                              st);
 }
 
