@@ -540,38 +540,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
   // operand copies of a stage go as soon as the MMAs have freed it; each CTA's scale warp
   // arrives on the even CTA's full barrier once that CTA's words of the stage are in place.
   constexpr int kScaleWarp = 2 + kBsEpiWarps;
-  if (warp == 0) {  // ------------------------------------------ operand producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int armed[STAGES], armed_l[STAGES];  // parities of copies in flight (full, landing)
-      for (int s = 0; s < STAGES; ++s) armed[s] = armed_l[s] = -1;
-      const uint32_t full0 = mapa_shared(&full[0], 0);
-      for (int u = pair_id; u < p.num_units; u += npairs) {
-        int tm, tn, kb0, kb1, part;
-        decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
-        bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          // the operands go as soon as the stage is free: the scale warps signal the full
-          // barrier themselves (waiting for them here cost the copies 400-1000 cycles of
-          // their lead a stage)
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = full0 + uint32_t(stage) * 8u;
+  if (warp == 0) {  // ---- operand producer (both CTAs): the whole warp waits, one elected lane issues
+    int stage = 0;
+    uint32_t phase = 0;
+    int armed[STAGES], armed_l[STAGES];  // parities of copies in flight (full, landing)
+    for (int s = 0; s < STAGES; ++s) armed[s] = armed_l[s] = -1;
+    const uint32_t full0 = mapa_shared(&full[0], 0);
+    bool ok = true;
+    for (int u = pair_id; ok && u < p.num_units; u += npairs) {
+      int tm, tn, kb0, kb1, part;
+      decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        // the operands go as soon as the stage is free: the scale warps signal the full
+        // barrier themselves (waiting for them here cost the copies 400-1000 cycles of
+        // their lead a stage)
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u))) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = full0 + uint32_t(stage) * 8u;
+        if (elect_one_sync()) {
           if constexpr (F::SF_INPLACE) {  // this CTA's scale rows of the stage, into its slot
             uint8_t *slot = sSF + stage * F::SF_SLOT;
             mbar_arrive_expect_tx_relaxed(&lfull[stage], F::SF_SLOT);
             // this CTA's A rows are rows 128 * (2 tm + rank) ..; B rows are the whole tile's
             tma_load_2d(&tmSA, &lfull[stage], slot, 16 * kb, (2 * tm + int(rank)) * BM);
             tma_load_2d(&tmSB, &lfull[stage], slot + F::SFA_STAGE, 16 * kb, tn * BN);
-            armed_l[stage] = int(phase);
           }
           if (rank == 0) {  // the even CTA's barrier counts both CTAs' bytes
             const uint32_t whole = 2 * (F::STAGE_TX + (F::SF_TILED ? F::SF_SLOT : 0));
-            mbar_arrive_expect_tx(&full[stage], part < 0 ? whole : whole - (F::B_STAGE + F::SFB_STAGE));
-            armed[stage] = int(phase);
+            mbar_arrive_expect_tx(&full[stage], part < 0 ? whole : whole - F::B_STAGE);
           }
           tma_load_2d_pair(&tmA, bar, sA + stage * F::A_STAGE, kb * F::BK, tm * F::BMP + F::BMC * int(rank));
           if (FMT != kMxfp4 || part < 0)
@@ -579,58 +577,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           else
             tma_load_2d_pair(&tmBh, bar, sB + stage * F::B_STAGE, kb * F::BK,
                              tn * BN + F::BNC * part + F::BNC / 2 * int(rank));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
+        __syncwarp();
+        if (F::SF_INPLACE) armed_l[stage] = int(phase);
+        if (rank == 0) armed[stage] = int(phase);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+    }
+    if (lane == 0)
       for (int s = 0; s < STAGES; ++s) {
         if (armed[s] >= 0) drain_wait(&full[s], uint32_t(armed[s]));
         if (armed_l[s] >= 0) drain_wait(&lfull[s], uint32_t(armed_l[s]));
       }
-    }
   } else if (warp >= kScaleWarp) {  // --------------------------------- scale warps (both CTAs)
     if constexpr (F::SF_TILED) {
       // The scale atoms arrive in the copy layout, on the stage's full barrier, which the
       // even CTA's operand producer arms for them too: this warp only issues the three
       // copies a stage (this CTA's A rows, both B halves) beside the operand producer's two.
       // One thread issuing all five fell behind the MMAs.
-      if (lane == 0) {
-        const uint32_t full0 = mapa_shared(&full[0], 0);
-        // atoms per 128-row tile.  MXFP4's atoms are planes of a 3-D tensor instead, one per row
-        // tile: a contraction that ends inside a stage then reads zeros, not the next tile's scales
-        // (whose 0xFF would make NaN of the zero codes past the end)
-        const int wrow = FMT == kMxfp4 ? 0 : p.k_dim / (4 * F::SF_BLOCK);
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = pair_id; ok && u < p.num_units; u += npairs) {
-          int tm, tn, kb0, kb1, part;
-          decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u)) {
-              ok = false;
-              break;
-            }
+      const uint32_t full0 = mapa_shared(&full[0], 0);
+      const int wrow = p.k_dim / (4 * F::SF_BLOCK);  // atoms per 128-row tile
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair_id; ok && u < p.num_units; u += npairs) {
+        int tm, tn, kb0, kb1, part;
+        decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u))) {
+            ok = false;
+            break;
+          }
+          if (elect_one_sync()) {
             const uint32_t bar = full0 + uint32_t(stage) * 8u;
             uint8_t *slot = sSF + stage * F::SF_SLOT;
             const int w0 = kb * F::WORDS;
             if constexpr (FMT == kMxfp4) {
+              // MXFP4's atoms are planes of a 3-D tensor, one per row tile: a contraction that ends inside a
+              // stage then reads zeros, not the next tile's scales (whose 0xFF would make NaN of the zero codes
+              // past the end), and the tile's two B atoms a word come in one copy (a half-width tile needs
+              // the first of the two)
               tma_load_3d_pair(&tmSA, bar, slot, 0, w0, 2 * tm + int(rank));
               tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, w0, 2 * tn + (part > 0 ? 1 : 0));
-              if (part < 0)
-                tma_load_3d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, w0, 2 * tn + 1);
             } else {
               tma_load_2d_pair(&tmSA, bar, slot, 0, (2 * tm + int(rank)) * wrow + w0);
               tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE, 0, 2 * tn * wrow + w0);
               tma_load_2d_pair(&tmSB, bar, slot + F::SFA_STAGE + 512 * F::WORDS, 0, (2 * tn + 1) * wrow + w0);
             }
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
       }
@@ -1201,9 +1202,9 @@ gtp_status run_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, co
   if (gtp_status s = gtp::encode_tmap_2d(&a, kU8, Aq, row_bytes, m_dim, row_bytes, F::BK, F::BMC, kSW128)) return s;
   if (gtp_status s = gtp::encode_tmap_2d(&b, kU8, Bq, row_bytes, n_dim, row_bytes, F::BK, F::BNC, kSW128)) return s;
   if (gtp_status s = gtp::encode_tmap_2d(&bh, kU8, Bq, row_bytes, n_dim, row_bytes, F::BK, F::BNC / 2, kSW128)) return s;
-  if (gtp_status s = gtp::encode_tmap_3d(&sa, kU32, As, 128, words, (m_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
+  if (gtp_status s = gtp::encode_tmap_3d(&sa, kU32, As, 128, words, (m_dim + 127) / 128, 512, 512 * words, 128, F::WORDS, 1))
     return s;
-  if (gtp_status s = gtp::encode_tmap_3d(&sb, kU32, Bs, 128, words, (n_dim + 127) / 128, 512, 512 * words, 128, F::WORDS))
+  if (gtp_status s = gtp::encode_tmap_3d(&sb, kU32, Bs, 128, words, (n_dim + 127) / 128, 512, 512 * words, 128, F::WORDS, 2))
     return s;
   if (gtp_status s = EPI == kStoreBf16 ? gtp::encode_tmap_2d(&d, kBF16, D, n_dim, m_dim, n_dim * 2, 32, 32, kSW64)
                                        : gtp::encode_tmap_2d(&d, kF32, D, n_dim, m_dim, n_dim * 4, 16, 32, kSW64))

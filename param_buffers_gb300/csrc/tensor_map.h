@@ -17,9 +17,9 @@ gtp_status encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const voi
                           CUtensorMapSwizzle swizzle);
 
 // A 3-D tensor of `inner` contiguous elements, `middle` rows and `outer` planes (strides in bytes,
-// multiples of 16); the box spans box_inner x box_middle x 1 elements, unswizzled.
+// multiples of 16); the box spans box_inner x box_middle x box_outer elements, unswizzled.
 gtp_status encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
                           uint64_t middle, uint64_t outer, uint64_t row_stride_bytes, uint64_t plane_stride_bytes,
-                          uint32_t box_inner, uint32_t box_middle);
+                          uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
 
 }  // namespace gtp
