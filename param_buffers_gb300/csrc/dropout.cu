@@ -87,7 +87,7 @@ struct Mask {
   uint32_t w[4], cut;
   bool none;
   __device__ __forceinline__ Mask(const DropArgs &a, uint64_t offset, int64_t g, int64_t row) {
-    const uint4 d = gtp::philox(a.rng.k0, a.rng.k1, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
+    const uint4 d = gtp::philox(a.rng, uint32_t(g) | (gtp::kStreamDropout << 30), uint32_t(row),
                                 uint32_t(offset), uint32_t(offset >> 32));
     w[0] = d.x, w[1] = d.y, w[2] = d.z, w[3] = d.w;
     cut = a.threshold << 16;

@@ -56,6 +56,18 @@ __device__ __forceinline__ uint32_t codes8(const uint64_t (&y)[4]) {
   return w;
 }
 
+// Eight codes rounded towards zero.
+__device__ __forceinline__ uint32_t codes8_cut(const uint64_t (&y)[4]) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 l0, h0, l1, h1, l2, h2, l3, h3;\n\t"
+      "mov.b64 {l0, h0}, %1;\n\tmov.b64 {l1, h1}, %2;\n\tmov.b64 {l2, h2}, %3;\n\tmov.b64 {l3, h3}, %4;\n\t"
+      "cvt.rs.satfinite.e2m1x4.f32 lo, {h1, l1, h0, l0}, %5;\n\tcvt.rs.satfinite.e2m1x4.f32 hi, {h3, l3, h2, l2}, %5;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "l"(y[0]), "l"(y[1]), "l"(y[2]), "l"(y[3]), "r"(0));
+  return w;
+}
+
 // Eight values (in pairs) to nearest; inv2 holds 1 / scale twice.
 __device__ __forceinline__ uint32_t encode8(const uint64_t (&x)[4], uint64_t inv2) {
   const uint64_t y[4] = {mul2(x[0], inv2), mul2(x[1], inv2), mul2(x[2], inv2), mul2(x[3], inv2)};
@@ -67,8 +79,9 @@ __device__ __forceinline__ uint32_t encode8(const uint64_t (&x)[4], uint64_t inv
 // [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23 fractional bits
 // (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
 // the random byte in their place, centred (byte << 14 | 1 << 13, one byte permute and one
-// multiply-add), carries into the code with the right probability; cleared and scaled back, the value
-// is on the grid and the conversion to a code exact.  At most 6 stays at most 6: its fraction is 0.
+// multiply-add), carries into the code with the right probability; what is left of the fraction is cut off
+// by a conversion that rounds stochastically with no random bits.  At most 6 stays at most 6: its
+// fraction is 0.
 __device__ __forceinline__ uint32_t encode8_stochastic(const uint64_t (&x)[4], uint64_t inv2, uint32_t r0,
                                                        uint32_t r1) {
   const uint64_t down = pack2(0x1p-126f, 0x1p-126f), up = pack2(0x1p126f, 0x1p126f);
@@ -80,10 +93,9 @@ __device__ __forceinline__ uint32_t encode8_stochastic(const uint64_t (&x)[4], u
     // byte b of r over 0x80: (byte << 8 | 0x80) << 6
     const uint32_t a = __byte_perm(r, 0x80u, (i & 1) ? 0x5524u : 0x5504u);
     const uint32_t b = __byte_perm(r, 0x80u, (i & 1) ? 0x5534u : 0x5514u);
-    const uint32_t lo = (uint32_t(t) + a * 64u) & 0xFFC00000u, hi = (uint32_t(t >> 32) + b * 64u) & 0xFFC00000u;
-    y[i] = mul2(pack2(__uint_as_float(lo), __uint_as_float(hi)), up);
+    y[i] = mul2(pack2(__uint_as_float(uint32_t(t) + a * 64u), __uint_as_float(uint32_t(t >> 32) + b * 64u)), up);
   }
-  return codes8(y);
+  return codes8_cut(y);
 }
 
 }  // namespace mx4

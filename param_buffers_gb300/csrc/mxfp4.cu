@@ -140,7 +140,7 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
   for (int h = 0; h < N / 8; ++h) {
     uint4 d = make_uint4(0, 0, 0, 0);
     if (STOCH)
-      d = gtp::philox(rng.k0, rng.k1, (first_group + h) | (stream << 30), r, uint32_t(offset), uint32_t(offset >> 32));
+      d = gtp::philox(rng, (first_group + h) | (stream << 30), r, uint32_t(offset), uint32_t(offset >> 32));
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint64_t v[4] = {x[8 * h + 4 * q], x[8 * h + 4 * q + 1], x[8 * h + 4 * q + 2], x[8 * h + 4 * q + 3]};

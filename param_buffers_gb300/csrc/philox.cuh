@@ -17,8 +17,12 @@ namespace gtp {
 
 enum : uint32_t { kStreamDropout = 0, kStreamRoundRow = 1, kStreamRoundCol = 2 };
 
+// The rounds' keys are formed on the host: they are the same for every draw of a call, and read from the
+// kernel's parameters they cost the rounds nothing.
+constexpr int kPhiloxRounds = 10;
+
 struct RngArgs {
-  uint32_t k0, k1;
+  uint32_t keys[kPhiloxRounds][2];
   uint64_t offset;
   const uint64_t *device_offset;
 };
@@ -26,8 +30,10 @@ struct RngArgs {
 inline RngArgs rng_args(const gtp_rng *r) {
   RngArgs a = {};
   if (r) {
-    a.k0 = uint32_t(r->seed);
-    a.k1 = uint32_t(r->seed >> 32);
+    for (int i = 0; i < kPhiloxRounds; ++i) {
+      a.keys[i][0] = uint32_t(r->seed) + uint32_t(i) * 0x9E3779B9u;
+      a.keys[i][1] = uint32_t(r->seed >> 32) + uint32_t(i) * 0xBB67AE85u;
+    }
     a.offset = r->offset;
     a.device_offset = r->device_offset;
   }
@@ -40,16 +46,14 @@ __device__ __forceinline__ uint64_t rng_offset(const RngArgs &r) {
   return r.device_offset ? r.offset + __ldg(r.device_offset) : r.offset;
 }
 
-__device__ __forceinline__ uint4 philox(uint32_t k0, uint32_t k1, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+__device__ __forceinline__ uint4 philox(const RngArgs &r, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
 #pragma unroll
-  for (int i = 0; i < 10; ++i) {
+  for (int i = 0; i < kPhiloxRounds; ++i) {
     const uint64_t p = uint64_t(0xD2511F53u) * c0, q = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(q >> 32) ^ c1 ^ k0;
+    c0 = uint32_t(q >> 32) ^ c1 ^ r.keys[i][0];
     c1 = uint32_t(q);
-    c2 = uint32_t(p >> 32) ^ c3 ^ k1;
+    c2 = uint32_t(p >> 32) ^ c3 ^ r.keys[i][1];
     c3 = uint32_t(p);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
