@@ -19,6 +19,7 @@
 #include "fastdiv.cuh"
 #include "philox.cuh"
 #include "sm100_ptx.cuh"
+#include "wide.cuh"
 
 namespace gtp {
 void clear_error();
@@ -38,23 +39,23 @@ struct DropArgs {
   gtp::RngArgs rng;
 };
 
-// Eight consecutive elements on 16 bytes, as they lie in memory: loads in flight hold no more registers
+// Eight consecutive elements on 16 bytes (bf16) or 32 (fp32), as they lie in memory: loads in flight hold no more registers
 // than bytes.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = __ldcs(reinterpret_cast<const float4 *>(p));
-    b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-  }
+  uint32_t a[8];
+  __device__ __forceinline__ void load(const float *p) { gtp::load_32b(p, a); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(a[i]);
   }
   static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    gtp::store_32b(p, w);
   }
 };
 template <>
@@ -98,6 +99,14 @@ struct Mask {
   }
 };
 
+__device__ __forceinline__ uint64_t mul2(float a, float b, float s) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmul.rn.f32x2 %0, x, y;\n\t}"
+      : "=l"(r)
+      : "f"(a), "f"(b), "f"(s));
+  return r;
+}
+
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
@@ -107,16 +116,18 @@ __device__ __forceinline__ void store1(__nv_bfloat16 *p, float v) { *p = __float
 // are in flight together; blocks are blockDim.x groups wide and step down the rows.  Every row of every
 // array starts on 16 bytes and holds whole groups.
 //
-// How many rows and blocks: measured on 2048 columns, bf16 onto a bf16 residual (8192 rows) 17.7 us with
-// 1 row and 8 blocks an SM against 20-23 with 2 or 4 rows; bf16 alone (32768 rows) 47.7 us with 4 rows
-// and 3 blocks against 49-57; where an array is fp32, 26.3 (bf16 onto fp32) and 62.5 us (fp32 to bf16)
-// with 2 rows and as many blocks as there are rows for, up to 16 an SM, against 28-39 and 65-72.
+// How many rows, and blocks an SM (the grid, and what the registers are held to), measured on 2048 columns:
+// bf16 onto a bf16 residual (8192 rows) 17.1 us with 1 row and 8 blocks against 18.3 with 6 and 20-23 with
+// 2 or 4 rows; bf16 alone (32768 rows), which the generator bounds, 44.9 us with 4 rows and 4 blocks against
+// 45.5-47.7; fp32 to bf16 59.6 us with 2 rows and 4 blocks against 62-74; bf16 onto fp32 (8192 rows) 26.7 us
+// with 2 rows and 3 blocks against 30 with the 2 that unbounded registers leave.  Where fp32 moves, a grid of
+// up to 16 blocks an SM (26.3 us against 28-30 with 3 to 5): the hardware balances it.
 template <typename TI, typename TO, bool RES>
 struct Shape {
   static constexpr bool NARROW = sizeof(TI) == 2 && sizeof(TO) == 2;
   static constexpr int ROWS = !NARROW ? 2 : RES ? 1 : 4;
-  static constexpr int MIN_BLOCKS = NARROW && RES ? 8 : 1;
-  static constexpr int BLOCKS = !NARROW ? 16 : RES ? 8 : 3;
+  static constexpr int MIN_BLOCKS = !RES ? 4 : NARROW ? 8 : 3;
+  static constexpr int BLOCKS = !NARROW ? 16 : MIN_BLOCKS;
 };
 
 template <typename TI, typename TO, bool RES>
@@ -147,11 +158,18 @@ __global__ void __launch_bounds__(kThreads, Shape<TI, TO, RES>::MIN_BLOCKS)
         const Mask m(a, offset, g, row);
         float v[8], y[8];
         x[i].get(v);
-        if (RES) res[i].get(y);
+        if (RES) {
+          res[i].get(y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (!RES) y[k] = 0.f;
-          if (m.keep(k)) y[k] = RES ? fmaf(v[k], a.scale, y[k]) : v[k] * a.scale;
+          for (int k = 0; k < 8; ++k)
+            if (m.keep(k)) y[k] = fmaf(v[k], a.scale, y[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {  // two products an instruction
+            const uint64_t z = mul2(v[k], v[k + 1], a.scale);
+            y[k] = m.keep(k) ? __uint_as_float(uint32_t(z)) : 0.f;
+            y[k + 1] = m.keep(k + 1) ? __uint_as_float(uint32_t(z >> 32)) : 0.f;
+          }
         }
         Eight<TO>::store(static_cast<TO *>(a.out) + row * a.out_ld + 8 * g, y);
       }

@@ -19,6 +19,7 @@
 #include "mx4_block.cuh"
 #include "philox.cuh"
 #include "sm100_ptx.cuh"
+#include "wide.cuh"
 
 namespace gtp {
 void clear_error();
@@ -271,12 +272,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
 // byte permutes for four codes, its sign by a multiply that moves two sign bits at once, and the scale
 // by a bf16 product, exact because it is a power of two.
 //
-// A thread writes eight elements where they lie on 16 bytes of the output.  Where rows start anywhere
-// (SHIFTED: an odd length), those are the elements from `head` + 8 v on, head the row's elements before
-// its first such place: eight nibbles out of words v and v + 1, the second held by the lane above (the
-// last lane of a warp only reads), under up to two scale bytes.  Items (row, v) run over all rows' words,
-// narrow rows side by side in a warp; the up to 7 elements at either end of a shifted row go one by one,
-// a thread each, in the blocks after the others.
+// A thread writes sixteen elements, half a block, where they lie on whole 32-byte sectors of the output.
+// Where rows start anywhere (SHIFTED: an odd length), those are the elements from `head` + 16 v on, head
+// the row's elements before its first such place: out of its own two words and those of the lane above
+// (the last lane of a warp only reads), under up to two scale bytes.  Items (row, v) run over all rows'
+// half blocks, narrow rows side by side in a warp; the up to 15 elements at either end of a shifted row
+// go one by one, a thread each, in the blocks after the others.
 __device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) {
   return byte == gtp::mx4::kNanScale ? 0x7FC0u : byte == 0 ? 0x0040u : byte << 7;
 }
@@ -297,7 +298,7 @@ struct ValueArgs {
   void *out;
   int64_t rows, len, blocks, words;
   int64_t row0;           // rows before these in the view (a later launch of one call)
-  int32_t items, groups;  // words of all rows and of a row that hold elements
+  int32_t items, groups;  // half blocks of all rows and of a row that hold elements
   int32_t vector_blocks;
   gtp::FastDiv by_groups;
 };
@@ -307,7 +308,7 @@ __device__ __forceinline__ uint32_t scale_byte_at(const ValueArgs &a, int64_t ro
   return __ldg(a.scales + ((r >> 7) * a.words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3));
 }
 
-constexpr int kValueItems = 4;  // items a thread has in flight
+constexpr int kValueItems = 2;  // items a thread has in flight
 
 template <typename T, bool SHIFTED>
 __global__ void __launch_bounds__(kThreads) mx4_values_kernel(const __grid_constant__ ValueArgs a) {
@@ -316,15 +317,15 @@ __global__ void __launch_bounds__(kThreads) mx4_values_kernel(const __grid_const
   gtp::ptx::wait_prior_grid();
   T *out = static_cast<T *>(a.out);
   const auto head_of = [&](int64_t row) {
-    return int((0u - uint32_t(reinterpret_cast<uintptr_t>(out + row * a.len) / sizeof(T))) & 7u);
+    return int((0u - uint32_t(reinterpret_cast<uintptr_t>(out + row * a.len) / sizeof(T))) & 15u);
   };
-  if (SHIFTED && int(blockIdx.x) >= a.vector_blocks) {  // the ends: 16 threads a row
-    const int64_t i = int64_t(blockIdx.x - a.vector_blocks) * kThreads + threadIdx.x, row = i >> 4;
+  if (SHIFTED && int(blockIdx.x) >= a.vector_blocks) {  // the ends: 32 threads a row
+    const int64_t i = int64_t(blockIdx.x - a.vector_blocks) * kThreads + threadIdx.x, row = i >> 5;
     if (row >= a.rows) return;
-    const int e = int(i & 15);
-    const int64_t head = min(int64_t(head_of(row)), a.len), tail = head + (a.len - head) / 8 * 8;
-    const int64_t j = e < 8 ? e : tail + e - 8;
-    if (e < 8 ? j >= head : j >= a.len) return;
+    const int e = int(i & 31);
+    const int64_t head = min(int64_t(head_of(row)), a.len), tail = head + (a.len - head) / 16 * 16;
+    const int64_t j = e < 16 ? e : tail + e - 16;
+    if (e < 16 ? j >= head : j >= a.len) return;
     const uint32_t c = uint32_t(a.codes[row * a.blocks * 16 + (j >> 1)]) >> (4 * (j & 1)), m = c & 7u;
     const uint32_t mag = (__byte_perm(0xC0800000u, 0xC0804000u, m) & 0xFFu) | (__byte_perm(0x3F3F3F00u, 0x40404040u, m) & 0xFFu) << 8;
     const uint32_t v = mul_bf16x2(mag | (c & 8u) << 12, scale_bf16(scale_byte_at(a, row, j >> 5)));
@@ -333,56 +334,67 @@ __global__ void __launch_bounds__(kThreads) mx4_values_kernel(const __grid_const
   }
   const int lane = threadIdx.x & 31;
   const int first = (int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5)) * N * PER + lane;
-  uint32_t w[N], s[N];
+  uint2 w[N];
+  uint32_t s[N];
   int row[N], g[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int item = min(first + i * PER, a.items - 1);
     row[i] = gtp::fast_div(item, a.by_groups);
     g[i] = item - row[i] * a.groups;
-    w[i] = __ldcs(reinterpret_cast<const uint32_t *>(a.codes + int64_t(row[i]) * a.blocks * 16) + g[i]);
-    s[i] = scale_byte_at(a, row[i], g[i] >> 2);
+    w[i] = __ldcs(reinterpret_cast<const uint2 *>(a.codes + int64_t(row[i]) * a.blocks * 16) + g[i]);
+    s[i] = scale_byte_at(a, row[i], g[i] >> 1);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    uint32_t c = w[i], ab = scale_bf16(s[i]), head = 0;
+    uint32_t c[2] = {w[i].x, w[i].y}, ab = scale_bf16(s[i]);
+    int head = 0;
     if (SHIFTED) {
-      // where head > 0 the vector reaches into word g + 1 of the same row, which exists
-      head = uint32_t(head_of(row[i]));
-      c = __funnelshift_r(c, __shfl_down_sync(0xFFFFFFFFu, c, 1), 4 * head);
+      // where head > 0 the vector reaches into half block g + 1 of the same row, which exists
+      head = head_of(row[i]);
+      const uint32_t n0 = __shfl_down_sync(0xFFFFFFFFu, c[0], 1), n1 = __shfl_down_sync(0xFFFFFFFFu, c[1], 1);
       ab |= __shfl_down_sync(0xFFFFFFFFu, ab, 1) << 16;
+      const bool far = head >= 8;
+      const uint32_t x = far ? c[1] : c[0], y = far ? n0 : c[1], z = far ? n1 : n0;
+      c[0] = __funnelshift_r(x, y, 4 * (head & 7));
+      c[1] = __funnelshift_r(y, z, 4 * (head & 7));
     }
-    const int64_t j = int64_t(head) + 8 * int64_t(g[i]);
-    if (first + i * PER >= a.items || (SHIFTED && lane == 31) || j + 8 > a.len) continue;
-    uint32_t v[4];
+    const int64_t j = int64_t(head) + 16 * int64_t(g[i]);
+    if (first + i * PER >= a.items || (SHIFTED && (lane == 31 || j + 16 > a.len))) continue;
+    uint32_t v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t sel = (c >> (16 * h)) & 0x7777u;
+    for (int h = 0; h < 4; ++h) {  // four codes a round
+      const uint32_t q = c[h >> 1] >> (16 * (h & 1)), sel = q & 0x7777u;
       const uint32_t top = __byte_perm(0x3F3F3F00u, 0x40404040u, sel), low = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-      v[2 * h] = with_signs(__byte_perm(low, top, 0x5140), c >> (16 * h));
-      v[2 * h + 1] = with_signs(__byte_perm(low, top, 0x7362), c >> (16 * h + 8));
+      v[2 * h] = with_signs(__byte_perm(low, top, 0x5140), q);
+      v[2 * h + 1] = with_signs(__byte_perm(low, top, 0x7362), q >> 8);
     }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {  // elements from 8 - head on are the upper word's block's
-      const uint32_t sel = !SHIFTED || 2 * p + 1 < 8 - int(head) ? 0x1010u : 2 * p < 8 - int(head) ? 0x3210u : 0x3232u;
+    for (int p = 0; p < 8; ++p) {  // elements from 16 - head on are the next half block's
+      const uint32_t sel = !SHIFTED || 2 * p + 1 < 16 - head ? 0x1010u : 2 * p < 16 - head ? 0x3210u : 0x3232u;
       v[p] = mul_bf16x2(v[p], __byte_perm(ab, 0, sel));
     }
     T *o = out + int64_t(row[i]) * a.len + j;
     if constexpr (sizeof(T) == 2) {
-      __stcs(reinterpret_cast<uint4 *>(o), make_uint4(v[0], v[1], v[2], v[3]));
+      gtp::store_32b(o, v);
     } else {
-      __stcs(reinterpret_cast<float4 *>(o), make_float4(low_f32(v[0]), high_f32(v[0]), low_f32(v[1]), high_f32(v[1])));
-      __stcs(reinterpret_cast<float4 *>(o) + 1, make_float4(low_f32(v[2]), high_f32(v[2]), low_f32(v[3]), high_f32(v[3])));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t f[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) f[2 * p] = v[4 * h + p] << 16, f[2 * p + 1] = v[4 * h + p] & 0xFFFF0000u;
+        gtp::store_32b(o + 8 * h, f);
+      }
     }
   }
 }
 
 template <typename T>
 gtp_status launch_values(ValueArgs a, cudaStream_t st) {
-  const bool shifted = !gtp::aligned16(a.out) || a.len % 8 != 0;
-  a.groups = int32_t((a.len + 7) / 8);
+  const bool shifted = reinterpret_cast<uintptr_t>(a.out) % (16 * sizeof(T)) || a.len % 16 != 0;
+  a.groups = int32_t((a.len + 15) / 16);
   a.by_groups = gtp::make_fastdiv(a.groups);
-  // items are counted in 31 bits: more than 2^30 words go in several launches
+  // items are counted in 31 bits: more than 2^30 half blocks go in several launches
   const int64_t rows = a.rows, most = std::max<int64_t>(1, (int64_t(1) << 30) / a.groups);
   const uint8_t *codes = a.codes;
   T *out = static_cast<T *>(a.out);
@@ -394,7 +406,7 @@ gtp_status launch_values(ValueArgs a, cudaStream_t st) {
     a.items = int32_t(a.rows * a.groups);
     const int64_t a_block = (kThreads / 32) * kValueItems * (shifted ? 31 : 32);
     a.vector_blocks = int32_t((a.items + a_block - 1) / a_block);
-    const int64_t ends = shifted ? (a.rows * 16 + kThreads - 1) / kThreads : 0;
+    const int64_t ends = shifted ? (a.rows * 32 + kThreads - 1) / kThreads : 0;
     const unsigned grid = unsigned(a.vector_blocks + ends);
     const gtp_status e =
         shifted ? gtp::launch_overlapped(mx4_values_kernel<T, true>, grid, kThreads, 0, st, "mxfp4_dequantize", a)

@@ -17,6 +17,7 @@
 #include "device.h"
 #include "fastdiv.cuh"
 #include "sm100_ptx.cuh"
+#include "wide.cuh"
 
 namespace gtp {
 void clear_error();
@@ -63,27 +64,21 @@ __device__ __forceinline__ void turn(uint64_t turns, int64_t pos, const RotaryAr
 }
 
 // A chunk of a head is 8 pairs: two runs of 8 elements half a rotation apart, or 16 in a row.  With
-// rows on 16 bytes (VEC) a chunk moves in 16-byte vectors, else element by element, a pair a chunk.
+// heads on whole vectors of 8 elements (VEC; 16 bytes, fp32 32) a chunk moves in those, else element by element, a pair a chunk.
 template <typename T>
 struct Run;
 template <>
 struct Run<float> {
-  float4 v[2];
-  __device__ __forceinline__ void load(const float *p) {
-    v[0] = __ldcs(reinterpret_cast<const float4 *>(p));
-    v[1] = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-  }
-  __device__ __forceinline__ void store(float *p) const {
-    __stcs(reinterpret_cast<float4 *>(p), v[0]);
-    __stcs(reinterpret_cast<float4 *>(p) + 1, v[1]);
-  }
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const float *p) { gtp::load_32b(p, v); }
+  __device__ __forceinline__ void store(float *p) const { gtp::store_32b(p, v); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = v[0].x, x[1] = v[0].y, x[2] = v[0].z, x[3] = v[0].w;
-    x[4] = v[1].x, x[5] = v[1].y, x[6] = v[1].z, x[7] = v[1].w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
   }
   __device__ __forceinline__ void set(const float (&x)[8]) {
-    v[0] = make_float4(x[0], x[1], x[2], x[3]);
-    v[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(x[i]);
   }
 };
 template <>
@@ -264,10 +259,11 @@ gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStrea
 
 template <typename T>
 gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStream_t st) {
-  // 16-byte vectors where every head starts on 16 bytes and whole runs of 8 elements turn or stay
-  const int64_t es = sizeof(T);
-  bool vec = gtp::aligned16(a.src) && gtp::aligned16(a.dst) && a.half % 8 == 0 && a.head_dim % 8 == 0;
-  for (int64_t s : {a.src_token, a.src_group, a.src_head, a.dst_token, a.dst_group, a.dst_head}) vec = vec && s * es % 16 == 0;
+  // vectors of 8 elements where every head starts on one (16 bytes, fp32 32) and whole ones turn or stay
+  const uintptr_t mask = 8 * sizeof(T) - 1;
+  bool vec = !((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst)) & mask) && a.half % 8 == 0 &&
+             a.head_dim % 8 == 0;
+  for (int64_t s : {a.src_token, a.src_group, a.src_head, a.dst_token, a.dst_group, a.dst_head}) vec = vec && s % 8 == 0;
   return vec ? launch<T, true>(a, turns, interleaved, st) : launch<T, false>(a, turns, interleaved, st);
 }
 
