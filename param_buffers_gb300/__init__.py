@@ -820,21 +820,21 @@ def _rng(rng):
 
 # The checks below look at each property of a tensor once: a small call is bound by them and the launch.
 
-_DTYPES: dict = {}  # torch dtype -> gtp_dtype; filled at the first call (torch is imported late)
+_TORCH_DTYPES: dict = {}  # torch dtype -> gtp_dtype; filled at the first call (torch is imported late)
 
 
 def _dtype_of(t, name: str):
     """The gtp_dtype of a tensor: the slow way, which fills the table or says what is wrong."""
     import torch
-    _DTYPES.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16, torch.uint8: abi.GTP_U8})
+    _TORCH_DTYPES.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16, torch.uint8: abi.GTP_U8})
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    return _DTYPES.get(t.dtype)
+    return _TORCH_DTYPES.get(t.dtype)
 
 
 def _float_dtype(t, name: str) -> int:
     try:
-        dt = _DTYPES[t.dtype]
+        dt = _TORCH_DTYPES[t.dtype]
     except (AttributeError, KeyError, TypeError):
         dt = _dtype_of(t, name)
     if dt != abi.GTP_F32 and dt != abi.GTP_BF16:
@@ -857,7 +857,7 @@ def _matrix(t, name: str):
 def _bytes(t, name: str) -> int:
     """The length of a contiguous uint8 tensor."""
     try:
-        dt = _DTYPES[t.dtype]
+        dt = _TORCH_DTYPES[t.dtype]
     except (AttributeError, KeyError, TypeError):
         dt = _dtype_of(t, name)
     if dt != abi.GTP_U8:

@@ -16,20 +16,6 @@ inline cudaStream_t as_stream(gtp_stream s) { return reinterpret_cast<cudaStream
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The bytes of one argument, for the checks that outputs share none with inputs or each other.
-struct ByteRange {
-  uintptr_t begin, end;
-};
-
-inline ByteRange byte_range(const void *p, int64_t bytes) {
-  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-  return {b, b + uintptr_t(bytes)};
-}
-
-inline bool overlap(const ByteRange &a, const ByteRange &b) {
-  return a.begin < a.end && b.begin < b.end && a.begin < b.end && b.begin < a.end;
-}
-
 struct DeviceInfo {
   int device = -1;
   int sm_count = 0;

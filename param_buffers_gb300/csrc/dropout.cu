@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "byte_range.h"
 #include "device.h"
 #include "fastdiv.cuh"
 #include "philox.cuh"

@@ -1,4 +1,5 @@
-// Division by a number fixed on the host, in kernels that split an index once per item.
+// Division by a number fixed on the host, in the elementwise kernels that split an index once per item (the
+// GEMMs have their own in gemm_common.cuh).
 #pragma once
 #include <cstdint>
 

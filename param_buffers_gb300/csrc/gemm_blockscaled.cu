@@ -5,7 +5,9 @@
 // (native MXFP8 / NVFP4 weights, blocks of 32 / 16 elements with one scale each) on top of
 // the linear layer's three products ("01 · ColumnParallelLinear / RowParallelLinear and the
 // core autograd" (llm-infra-atlas), §4.1, §4.2).
+#include "byte_range.h"
 #include "gemm_common.cuh"
+#include "mxf4_ptx.cuh"
 #include "nv_block.cuh"
 
 namespace {

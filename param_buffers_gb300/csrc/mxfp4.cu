@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "byte_range.h"
 #include "device.h"
 #include "fastdiv.cuh"
 #include "mx4_block.cuh"
@@ -82,9 +83,23 @@ struct TileArgs {
   const void *src;
   int64_t rows, cols, ld, src_bytes;
   int64_t tiles_n;
+  int32_t wide;  // every row starts on 32 bytes
   ViewArgs row, col;
   gtp::RngArgs rng;
 };
+
+// The same in whole sectors.  fp32 takes them where rows allow (both views of [8192, 8192] 66.6 -> 57.7 us);
+// bf16, one sector a thread, lost by it (stochastically 60.8 -> 62.0, the rowwise view alone 27.2 -> 28.0).
+template <typename T, int N>
+__device__ __forceinline__ void load_sectors(const T *p, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) {
+    uint32_t v[8];
+    gtp::load_32b(p + 8 * Tile<T>::PER * i, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[8 * i + k] = v[k];
+  }
+}
 
 // The 16-byte vectors around the 16 elements at p lie inside the source.
 template <typename T>
@@ -155,9 +170,9 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
   }
 }
 
-// Blocks an SM that the registers are held to: latency against spills.  On [8192, 8192], both views, 2 / 3 / 4
-// blocks: bf16 45.8 / 39.5 / 37.3 us to nearest and 71.6 / 71.2 / 66.5 stochastically; fp32 66.7 / 80.3 / 106
-// (its 64 registers of tile words spill from 3 on), but the rowwise view alone 47.7 / 46.3 / 52.9.
+// Blocks an SM that the registers are held to: latency against spills.  On [8192, 8192], 2 / 3 / 4 blocks: bf16
+// both views 45.8 / 39.4 / 37.2 us to nearest and 67.8 / 62.0 / 61.8 stochastically; fp32 both views 57.6 / 66.6 /
+// 92.2 (its 64 registers of tile words spill from 3 on), but the rowwise view alone 46.7 / 44.6 / 48.8.
 template <typename T, bool COL>
 constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL ? 2 : 3;
 
@@ -186,6 +201,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
     } else if (nc == 16 && (!RAGGED || window_inside(p, a))) {
       if (RAGGED)
         load_shifted(p, w[it]);
+      else if (sizeof(T) == 4 && a.wide)
+        load_sectors(p, w[it]);
       else
         load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
     } else {
@@ -507,6 +524,7 @@ extern "C" gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int6
   a.tiles_n = (cols + kTile - 1) / kTile;
   a.row = {row_codes, row_scales, row.blocks() * 16, row.words()};
   a.col = {col_codes, col_scales, col.blocks() * 16, col.words()};
+  a.wide = ((reinterpret_cast<uintptr_t>(src) | uintptr_t(a.ld * es)) & 31u) == 0;
   a.rng = gtp::rng_args(rng);
   const int64_t tiles = (rows + kTile - 1) / kTile * a.tiles_n;
   if (tiles > INT32_MAX) return gtp::fail(GTP_E_SHAPE, "more than 2^31 - 1 tiles of 128 x 128");

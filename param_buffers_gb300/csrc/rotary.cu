@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "byte_range.h"
 #include "device.h"
 #include "fastdiv.cuh"
 #include "sm100_ptx.cuh"

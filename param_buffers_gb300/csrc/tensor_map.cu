@@ -15,8 +15,9 @@ std::once_flag g_once;
 cudaError_t g_lookup_err = cudaSuccess;
 }  // namespace
 
-namespace {
-gtp_status look_up_encoder() {
+gtp_status encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+                          uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
+                          CUtensorMapSwizzle swizzle) {
   std::call_once(g_once, [] {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -25,14 +26,6 @@ gtp_status look_up_encoder() {
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!g_encode) return fail(GTP_E_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(g_lookup_err));
-  return GTP_OK;
-}
-}  // namespace
-
-gtp_status encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
-                          uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
-                          CUtensorMapSwizzle swizzle) {
-  if (gtp_status s = look_up_encoder()) return s;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_stride_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
@@ -44,24 +37,6 @@ gtp_status encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const voi
     return fail(GTP_E_CUDA, "cuTensorMapEncodeTiled failed (%d): dims %llu x %llu, stride %llu, box %u x %u", int(r),
                 (unsigned long long)inner, (unsigned long long)outer, (unsigned long long)row_stride_bytes, box_inner,
                 box_outer);
-  return GTP_OK;
-}
-
-gtp_status encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner,
-                          uint64_t middle, uint64_t outer, uint64_t row_stride_bytes, uint64_t plane_stride_bytes,
-                          uint32_t box_inner, uint32_t box_middle, uint32_t box_outer) {
-  if (gtp_status s = look_up_encoder()) return s;
-  const cuuint64_t dims[3] = {inner, middle, outer};
-  const cuuint64_t strides[2] = {row_stride_bytes, plane_stride_bytes};
-  const cuuint32_t box[3] = {box_inner, box_middle, box_outer};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(map, dtype, 3, const_cast<void *>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(GTP_E_CUDA, "cuTensorMapEncodeTiled failed (%d): dims %llu x %llu x %llu, box %u x %u x %u", int(r),
-                (unsigned long long)inner, (unsigned long long)middle, (unsigned long long)outer, box_inner,
-                box_middle, box_outer);
   return GTP_OK;
 }
 
