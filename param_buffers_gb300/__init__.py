@@ -839,6 +839,8 @@ def _float_dtype(t, name: str) -> int:
         dt = _dtype_of(t, name)
     if dt != abi.GTP_F32 and dt != abi.GTP_BF16:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
     return dt
 
 
@@ -862,6 +864,8 @@ def _bytes(t, name: str) -> int:
         dt = _dtype_of(t, name)
     if dt != abi.GTP_U8:
         raise TypeError(f"{name} must be uint8, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.numel()
@@ -910,7 +914,8 @@ def gtp_mxfp4_quantize(src, row=None, col=None, rng=None, stream=None) -> None:
 def gtp_mxfp4_dequantize(codes, scales, out, stream=None) -> None:
     """The values of an MXFP4 view, out[R,C] (fp32 or bf16, contiguous)."""
     dt = _float_dtype(out, "out")
-    _require(out, out.dtype, "out", 2)
+    if len(out.shape) != 2 or not out.is_contiguous():
+        raise ValueError("out must be contiguous with 2 dims")
     R, Cc = out.shape
     c, s = _mxfp4_view((codes, scales), R, Cc, "view")
     _check(lib().gtp_mxfp4_dequantize(c, s, R, Cc, out.data_ptr(), dt, _stream(stream)), "gtp_mxfp4_dequantize")
@@ -954,9 +959,11 @@ def gtp_linear_dgrad_mxfp4(dYq, dYs, Wtq, Wts, dX, stream=None) -> None:
 def gtp_linear_wgrad_accum_mxfp4(dYtq, dYts, Xtq, Xts, grad_data, grad_offset: int, stream=None) -> None:
     """grad_data[grad_offset:+N*K].view(N,K) += dq(dYtq, dYts) dq(Xtq, Xts)^T (fp32), the columnwise MXFP4
     views of dY[M,N] and X[M,K]."""
-    import torch
     a, sa, b, sb, N, K, M = _mxfp4_product(dYtq, dYts, Xtq, Xts, "dYtq and Xtq")
-    _require(grad_data, torch.float32, "grad_data")
+    if _float_dtype(grad_data, "grad_data") != abi.GTP_F32:
+        raise TypeError(f"grad_data must be float32, got {grad_data.dtype}")
+    if not grad_data.is_contiguous():
+        raise ValueError("grad_data must be contiguous")
     _check(lib().gtp_linear_wgrad_accum_mxfp4(a, sa, b, sb, grad_data.data_ptr(), int(grad_offset), grad_data.numel(),
                                               M, N, K, _stream(stream)),
            "gtp_linear_wgrad_accum_mxfp4")
@@ -1023,9 +1030,8 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
         wide = int(positions.dtype == torch.int64)
-        _require(positions, positions.dtype, "positions", 1)
-        if positions.numel() != T:
-            raise ValueError("one position a token")
+        if positions.shape != (T,) or not positions.is_contiguous() or not positions.is_cuda:
+            raise ValueError("positions must be one position a token, contiguous, on the GPU")
     pairs = len(turns)
     if isinstance(turns, C.Array):
         at = C.addressof(turns)
