@@ -51,11 +51,18 @@ def _check(status: int, fn: str) -> None:
         raise GtpError(status, fn, (lib().gtp_last_error() or b"").decode(errors="replace"))
 
 
+_current: list = []  # torch's getters of the current device and of its current stream's handle
+
+
 def _stream(stream) -> int:
-    import torch
+    """The handle of `stream`, or of the current stream: read by itself, because building the Stream object that
+    torch.cuda.current_stream() returns costs 3 us a call."""
     if stream is None:
-        # the handle alone: building the Stream object that current_stream() returns costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if not _current:
+            import torch
+            torch.cuda.current_device()  # initialises CUDA
+            _current.extend((torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream))
+        return _current[1](_current[0]())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -856,26 +863,31 @@ def _matrix(t, name: str):
     return dt, shape, ld if shape[0] > 1 else shape[1]
 
 
-def _bytes(t, name: str) -> int:
-    """The length of a contiguous uint8 tensor."""
-    try:
-        dt = _TORCH_DTYPES[t.dtype]
-    except (AttributeError, KeyError, TypeError):
-        dt = _dtype_of(t, name)
-    if dt != abi.GTP_U8:
-        raise TypeError(f"{name} must be uint8, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.numel()
+def _is_bytes(t) -> bool:
+    """A contiguous uint8 tensor on the GPU."""
+    return _TORCH_DTYPES.get(t.dtype) == abi.GTP_U8 and t.is_cuda and t.is_contiguous()
 
 
-def _scales(t, rows: int, blocks: int, name: str) -> int:
-    n = -(-rows // 128) * -(-blocks // 4) * 512
-    if _bytes(t, name) != n:
-        raise ValueError(f"{name} must hold gtp_sf_tiled_bytes({rows}, {blocks}) = {n} bytes")
-    return t.data_ptr()
+def _scale_bytes(rows: int, blocks: int) -> int:
+    return ((rows + 127) >> 7) * ((blocks + 3) >> 2) << 9
+
+
+def _refuse_view(codes, scales, rows: int, cols: int, name: str):
+    """Says what is wrong with a view that failed its check."""
+    blocks = -(-cols // 32)
+    for t, what in ((codes, f"{name} codes"), (scales, f"{name} scales")):
+        dt = _TORCH_DTYPES.get(getattr(t, "dtype", None))
+        if (_dtype_of(t, what) if dt is None else dt) != abi.GTP_U8:
+            raise TypeError(f"{what} must be uint8, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be on the GPU")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    if codes.shape != (rows, 16 * blocks):
+        raise ValueError(f"{name} codes must be [{rows}, {16 * blocks}]")
+    n = _scale_bytes(rows, blocks)
+    if scales.numel() != n:
+        raise ValueError(f"{name} scales must hold gtp_sf_tiled_bytes({rows}, {blocks}) = {n} bytes")
 
 
 def _mxfp4_view(view, rows: int, cols: int, name: str):
@@ -883,10 +895,14 @@ def _mxfp4_view(view, rows: int, cols: int, name: str):
         return 0, 0
     codes, scales = view
     blocks = -(-cols // 32)
-    _bytes(codes, name)
-    if codes.shape != (rows, 16 * blocks):
-        raise ValueError(f"{name} codes must be [{rows}, {16 * blocks}]")
-    return codes.data_ptr(), _scales(scales, rows, blocks, name)
+    try:
+        good = _is_bytes(codes) and _is_bytes(scales) and codes.shape == (rows, 16 * blocks) \
+            and scales.numel() == _scale_bytes(rows, blocks)
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse_view(codes, scales, rows, cols, name)
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def gtp_mxfp4_views(rows: int, cols: int, device="cuda"):
@@ -924,14 +940,14 @@ def gtp_mxfp4_dequantize(codes, scales, out, stream=None) -> None:
 def _mxfp4_product(Aq, As, Bq, Bs, names: str):
     """Pointers of two views contracted over their rows, their row counts and the contraction's length
     (padded to whole blocks)."""
-    _bytes(Aq, names)
-    _bytes(Bq, names)
-    a, b = Aq.shape, Bq.shape
-    if len(a) != 2 or len(b) != 2 or a[1] != b[1] or a[1] % 16:
-        raise ValueError(f"shape mismatch: {names} are 2-D and hold the contraction's whole blocks")
-    blocks = a[1] // 16
-    return (Aq.data_ptr(), _scales(As, a[0], blocks, names), Bq.data_ptr(), _scales(Bs, b[0], blocks, names),
-            a[0], b[0], 32 * blocks)
+    try:
+        (m, width), (n, other) = Aq.shape, Bq.shape
+    except (AttributeError, ValueError):
+        raise ValueError(f"{names} must be tensors of 2 dims") from None
+    if width != other or width & 15:
+        raise ValueError(f"shape mismatch: {names} hold the same contraction's whole blocks")
+    K = 2 * width
+    return (*_mxfp4_view((Aq, As), m, K, names), *_mxfp4_view((Bq, Bs), n, K, names), m, n, K)
 
 
 def _bf16_out(t, rows: int, cols: int, name: str) -> int:
