@@ -8,6 +8,7 @@
 #include "byte_range.h"
 #include "gemm_common.cuh"
 #include "mxf4_ptx.cuh"
+#include "mxf4_rows.h"
 #include "nv_block.cuh"
 
 namespace {
@@ -1437,6 +1438,7 @@ gtp_status store_mxfp4(const uint8_t *Aq, const uint8_t *As, const uint8_t *Bq, 
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
   cudaStream_t st = gtp::as_stream(stream);
   if (k_dim == 0) return gtp::launch_zero_bytes(D, m_dim * n_dim * 2, st, dev.sm_count);
+  if (gtp::few_rows(m_dim, n_dim, dev.sm_count)) return gtp::run_mxfp4_rows(Aq, As, Bq, Bs, D, m_dim, n_dim, k_dim, st);
   return run_mxfp4<kStoreBf16>(Aq, As, Bq, Bs, D, m_dim, n_dim, k_dim, false, dev, st);
 }
 }  // namespace

@@ -101,6 +101,25 @@ def test_ties_saturation_and_both_scale_rules():
         check_view(col, MX.quantize_columnwise(x, rng=rng))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rng", [None, (31, 5)], ids=["nearest", "stochastic"])
+def test_blocks_of_every_exponent(rng, dtype):
+    """One row, and one block of a column, for each power of two that a block's amax can have."""
+    exps = np.arange(-149, 128)
+    g = np.random.default_rng(12)
+    m = (g.uniform(-1, 1, size=(exps.size, 64)) * np.exp2(-g.integers(0, 30, size=(exps.size, 64)))).astype(np.float32)
+    m[:, ::32] = 1.75
+    rows = torch.from_numpy(np.ldexp(m, exps[:, None]).astype(np.float32))
+    cols = torch.from_numpy(np.ldexp(m.T[:32], exps[None]).astype(np.float32)).contiguous()
+    for x in (rows, cols):
+        x = x.to(torch.bfloat16) if dtype == "bf16" else x
+        a, bf = oracle_in(x)
+        row, col = buffers(*x.shape)
+        gtp.gtp_mxfp4_quantize(x.to(DEV), row=row, col=col, rng=rng)
+        check_view(row, MX.quantize_rowwise(a, bf, rng))
+        check_view(col, MX.quantize_columnwise(a, bf, rng))
+
+
 def test_stochastic_mean_and_device_offset():
     """The mean over many offsets approaches the source; an offset on the device adds to the host's."""
     x = source(64, 96, 8, "f32").nan_to_num(0, 0, 0)
@@ -171,6 +190,43 @@ def test_forward_and_dgrad(M, N, K):
         dX = torch.full((M, K), float("nan"), dtype=torch.bfloat16, device=DEV)
         gtp.gtp_linear_dgrad_mxfp4(*dYq, *Wtq, dX)
         check_bf16(dX, dY, Wt)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9])
+@pytest.mark.parametrize("N,K", [(8, 8), (40, 40), (136, 104), (264, 1064), (1288, 4200), (128, 9000)])
+def test_few_rows(M, N, K):
+    """Single tokens and a few, around the size at which they take their own kernel: lengths that end inside a
+    block, an atom of scales and a warp's step, rows that end inside a tile of 128."""
+    (Xq, X), (Wq, W) = operand(M, K, 11), operand(N, K, 12)
+    Y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    gtp.gtp_linear_fprop_mxfp4(*Xq, *Wq, Y)
+    check_bf16(Y, X, W)
+    (dYq, dY), (Wtq, Wt) = operand(M, N, 13), operand(K, N, 14)
+    dX = torch.full((M, K), float("nan"), dtype=torch.bfloat16, device=DEV)
+    gtp.gtp_linear_dgrad_mxfp4(*dYq, *Wtq, dX)
+    check_bf16(dX, dY, Wt)
+
+
+def test_few_rows_extreme_scales_and_nan():
+    """Exponents of the two blocks that meet inside the range although one alone is at its end; NaN scales."""
+    M, N, K = 2, 16, 64
+    g = np.random.default_rng(15)
+    xc, wc = (g.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    xs, ws = np.full((M, 2), 254, np.uint8), np.full((N, 2), 3, np.uint8)
+    xs[1] = 0
+    ws[1::2] = 252
+    A, W = MX.dequantize(xc, xs, K), MX.dequantize(wc, ws, K)
+    dev = lambda c, s: (torch.from_numpy(c).to(DEV), torch.from_numpy(tile_scales(s)).to(DEV))
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    gtp.gtp_linear_fprop_mxfp4(*dev(xc, xs), *dev(wc, ws), Y)
+    keep = np.array([[n % 2 == (0 if m == 0 else 1) for n in range(N)] for m in range(M)])  # the others pass 2^127 or vanish
+    got, ref, mass = F.bf16_bits_to_f64(bits(Y)), A @ W.T, np.abs(A) @ np.abs(W).T
+    bound = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -7) + K * 2.0 ** -23 * mass + 2.0 ** -133
+    assert np.all(np.abs(got - ref)[keep] <= bound[keep])
+    assert not np.isnan(got[keep]).any()  # the others may hold Inf - Inf of two blocks
+    ws[3, 1] = 0xFF
+    gtp.gtp_linear_fprop_mxfp4(*dev(xc, xs), *dev(wc, ws), Y)
+    assert torch.isnan(Y[:, 3]).all() and torch.isnan(Y).cpu().numpy()[keep].sum() == 1
 
 
 @pytest.mark.parametrize("M,N,K,off", [(1, 4, 4, 0), (32, 128, 64, 64), (33, 129, 68, 4), (1111, 160, 96, 128),
