@@ -131,16 +131,22 @@ __device__ __forceinline__ int word_at(int r, int w) {
   return r * WORDS + ((4 * s + (w & 3) + 8 * (r >> 5)) & (WORDS - 1));
 }
 
-// The largest magnitude of a word's elements so far: fp32 one 32-bit maximum, bf16 two 16-bit ones.
+// The largest magnitude of a word's elements so far, as floats (fp32 one, bf16 two); NaN stays.
 template <typename T>
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w);
 template <>
 __device__ __forceinline__ uint32_t max_magnitude<float>(uint32_t m, uint32_t w) {
-  return max(m, w & 0x7FFFFFFFu);
+  float r;
+  asm("{\n\t.reg .f32 a;\n\tabs.f32 a, %2;\n\tmax.NaN.f32 %0, %1, a;\n\t}"
+      : "=f"(r)
+      : "f"(__uint_as_float(m)), "f"(__uint_as_float(w)));
+  return __float_as_uint(r);
 }
 template <>
 __device__ __forceinline__ uint32_t max_magnitude<__nv_bfloat16>(uint32_t m, uint32_t w) {
-  return __vmaxu2(m, w & 0x7FFF7FFFu);
+  uint32_t r;
+  asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  return r;
 }
 
 __device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
