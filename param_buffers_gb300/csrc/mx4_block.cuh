@@ -68,27 +68,20 @@ __device__ __forceinline__ uint32_t codes8_cut(const uint64_t (&y)[4]) {
   return w;
 }
 
-// Eight values (in pairs) to nearest; inv2 holds 1 / scale twice.
-__device__ __forceinline__ uint32_t encode8(const uint64_t (&x)[4], uint64_t inv2) {
-  const uint64_t y[4] = {mul2(x[0], inv2), mul2(x[1], inv2), mul2(x[2], inv2), mul2(x[3], inv2)};
-  return codes8(y);
-}
-
-// Eight values stochastically, with the random bytes of r0 (first four) and r1.  x / scale times 2^-126
-// is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
+// Eight codes of eight scaled values (in pairs) stochastically, with the random bytes of r0 (first four) and
+// r1.  A value times 2^-126 is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
 // [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23 fractional bits
 // (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
 // the random byte in their place, centred (byte << 14 | 1 << 13, one byte permute and one
 // multiply-add), carries into the code with the right probability; what is left of the fraction is cut off
 // by a conversion that rounds stochastically with no random bits.  At most 6 stays at most 6: its
 // fraction is 0.
-__device__ __forceinline__ uint32_t encode8_stochastic(const uint64_t (&x)[4], uint64_t inv2, uint32_t r0,
-                                                       uint32_t r1) {
+__device__ __forceinline__ uint32_t codes8_stochastic(const uint64_t (&x)[4], uint32_t r0, uint32_t r1) {
   const uint64_t down = pack2(0x1p-126f, 0x1p-126f), up = pack2(0x1p126f, 0x1p126f);
   uint64_t y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t t = mul2(mul2(x[i], inv2), down);
+    const uint64_t t = mul2(x[i], down);
     const uint32_t r = i < 2 ? r0 : r1;
     // byte b of r over 0x80: (byte << 8 | 0x80) << 6
     const uint32_t a = __byte_perm(r, 0x80u, (i & 1) ? 0x5524u : 0x5504u);

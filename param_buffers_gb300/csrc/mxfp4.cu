@@ -150,14 +150,35 @@ __device__ __forceinline__ uint32_t max_magnitude<__nv_bfloat16>(uint32_t m, uin
 }
 
 __device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// 2 N values in pairs, of one block under `byte`, to codes; view row r and its first group of draws.
+// Two values in a pair, divided by the block's scale.  bf16 elements, the low or the high halves of two words, are
+// multiplied as they lie by a product of halves added to -0, which keeps the sign of zero: half of the unpacking
+// gone (both views of [8192, 8192] bf16 36.7 -> 36.2 us, stochastically 60.1 -> 57.7).
+__device__ __forceinline__ uint64_t scaled(float a, float b, float inv) {
+  return gtp::mx4::mul2(gtp::mx4::pack2(a, b), gtp::mx4::pack2(inv, inv));
+}
+__device__ __forceinline__ float scaled_half(uint32_t w, bool high, float inv) {
+  float r;
+  if (high)
+    asm("{\n\t.reg .b16 l, h, z, s;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {z, s}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, h, s, %3;\n\t}"
+        : "=f"(r)
+        : "r"(w), "f"(inv), "f"(-0.f));
+  else
+    asm("{\n\t.reg .b16 l, h, z, s;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {z, s}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, l, s, %3;\n\t}"
+        : "=f"(r)
+        : "r"(w), "f"(inv), "f"(-0.f));
+  return r;
+}
+__device__ __forceinline__ uint64_t scaled_halves(uint32_t a, bool a_high, uint32_t b, bool b_high, float inv) {
+  return gtp::mx4::pack2(scaled_half(a, a_high, inv), scaled_half(b, b_high, inv));
+}
+
+// 2 N values in pairs, divided by the scale of their block's `byte`, to codes; view row r and its first group of draws.
 template <bool STOCH, int N>
 __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte, uint32_t (&w)[N / 4], uint32_t stream,
                                            uint32_t r, uint32_t first_group, const gtp::RngArgs &rng, uint64_t offset) {
-  const float inv = gtp::mx4::inv_scale(byte);
-  const uint64_t inv2 = gtp::mx4::pack2(inv, inv);
 #pragma unroll
   for (int h = 0; h < N / 8; ++h) {
     uint4 d = make_uint4(0, 0, 0, 0);
@@ -166,8 +187,7 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint64_t v[4] = {x[8 * h + 4 * q], x[8 * h + 4 * q + 1], x[8 * h + 4 * q + 2], x[8 * h + 4 * q + 3]};
-      w[2 * h + q] = STOCH ? gtp::mx4::encode8_stochastic(v, inv2, q ? d.z : d.x, q ? d.w : d.y)
-                           : gtp::mx4::encode8(v, inv2);
+      w[2 * h + q] = STOCH ? gtp::mx4::codes8_stochastic(v, q ? d.z : d.x, q ? d.w : d.y) : gtp::mx4::codes8(v);
     }
   }
   if (byte == gtp::mx4::kNanScale) {  // a bad block's codes are 0
@@ -234,11 +254,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
       if (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16) << 16;
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       const uint32_t byte = gtp::mx4::scale_byte<STOCH>(m);
+      const float inv = gtp::mx4::inv_scale(byte);
       uint64_t x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        x[k] = sizeof(T) == 4 ? gtp::mx4::pack2(__uint_as_float(w[it][2 * k % TW]), __uint_as_float(w[it][(2 * k + 1) % TW]))
-                              : gtp::mx4::pack2(low_f32(w[it][k]), high_f32(w[it][k]));
+        x[k] = sizeof(T) == 4
+                   ? scaled(__uint_as_float(w[it][2 * k % TW]), __uint_as_float(w[it][(2 * k + 1) % TW]), inv)
+                   : scaled_halves(w[it][k % TW], false, w[it][k % TW], true, inv);
       uint32_t codes[2];
       encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundRow, uint32_t(r), uint32_t(8 * tn + seg), a.rng, offset);
       const bool in = r < a.rows && c0 < 2 * a.row.pitch;  // the block exists (two codes a byte)
@@ -265,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
         const int c = F::PER * p + e;
         const int64_t gc = kTile * tn + c;
         const uint32_t byte = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : e ? m & 0xFFFF0000u : m << 16);
+        const float inv = gtp::mx4::inv_scale(byte);
         uint64_t x[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          x[k] = F::PER == 1 ? gtp::mx4::pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]))
-                 : e         ? gtp::mx4::pack2(high_f32(v[2 * k]), high_f32(v[2 * k + 1]))
-                             : gtp::mx4::pack2(low_f32(v[2 * k]), low_f32(v[2 * k + 1]));
+          x[k] = F::PER == 1 ? scaled(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), inv)
+                             : scaled_halves(v[2 * k], e, v[2 * k + 1], e, inv);
         uint32_t codes[4];
         encode_run<STOCH>(x, byte, codes, gtp::kStreamRoundCol, uint32_t(gc), uint32_t(8 * tm + 2 * rb), a.rng, offset);
         const int64_t b = 4 * tm + rb;
