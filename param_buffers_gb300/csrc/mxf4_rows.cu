@@ -13,17 +13,18 @@
 // blocks' powers of two and added up, lanes and warps in a fixed order.
 //
 // Measured, one token (two, four; the tensor-core kernel, whose time hardly depends on them), B of
-//   [8192, 2048]    4.3 - 5.0 us  (6.2,  8.2;  8.1)      [8192, 4096]    6.6  ( 8.9, 13.5; 10.6 - 12.4)
-//   [2048, 8192]    4.3 - 4.8     (6.2,  8.3; 13.1)      [4096, 16384]  10.1  (13.6, 21.8; 22 - 28)
-//   [2048, 4096]    3.9           (4.3,  4.8;  8.8)      [28672, 8192]  31.4  (44.3, 76.8; 38 - 41)
-//   [1536, 2048]    2.7           (3.4,  4.3;  6.2)      [8192, 28672]  27.4  (38.4, 67.0; 55 - 58)
-//   [2048, 1024]    2.5           (3.0,  3.6;  5.1)      [128256, 2048] 35.2  (49.7, 86.2; 36)
-// About 2.5 us of each is launch, first loads and the way out.  On large matrices the conversions and
-// the multiply-adds bound it, at 4.0 - 4.6 TB/s of codes for one token and in proportion to the tokens beyond:
-// a ring of asynchronous copies 100 KB an SM deep, which keeps the memory busy through the arithmetic, did
-// not move it (30.6 us on [28672, 8192], 33.9 on [8192, 28672]).  The same loads feeding legacy 16-bit matrix
-// instructions cost more in unpacking to bf16 than they saved (one to eight tokens 6.5 us on [8192, 2048], 15 on
-// [2048, 8192]); asking for B's lines in L2 before the previous kernel ends gave 0.1 us.
+//   [8192, 2048]    4.5 us  (6.5,  8.2;  8.1)      [8192, 4096]    6.6  ( 8.9, 13.5; 10.6 - 12.4)
+//   [2048, 8192]    4.5     (6.6,  8.3; 13.1)      [4096, 16384]  10.1  (13.6, 21.8; 22 - 28)
+//   [2048, 4096]    3.9     (4.3,  4.8;  8.8)      [28672, 8192]  31.4  (44.3, 76.8; 38 - 41)
+//   [1536, 2048]    2.7     (3.4,  4.3;  6.2)      [8192, 28672]  27.5  (38.4, 67.0; 55 - 58)
+//   [2048, 1024]    2.5     (3.0,  3.6;  5.1)      [128256, 2048] 35.2  (49.7, 86.2; 36)
+// About 2.5 us of each is launch, first loads and the way out.  On large matrices it runs at 3.9 - 4.6 TB/s of the
+// copy's 6.8: blocks come and go, and while one multiplies and adds up its sums it loads nothing.  A persistent form
+// with a ring of asynchronous copies 100 KB an SM deep is bound by instructions instead (73 % of the issue slots; 26.3 us
+// on [28672, 8192]) and costs the small matrices 0.5 - 1 us; the same loads feeding legacy 16-bit matrix
+// instructions cost more in unpacking to bf16 than they saved (6.5 us on [8192, 2048], 15 on
+// [2048, 8192]); asking for B's lines in L2 before the previous kernel ends gave 0.1 us; unpacking by shifts and
+// masks instead of the conversion takes 5.5 us on [8192, 2048].
 //
 // Hence the rule in few_rows(): one token always; up to four while they and B's rows are few, where the tensor-core
 // kernel's tiles of 256 columns leave SMs idle and each waits for its own chain of loads.
@@ -78,8 +79,14 @@ __device__ __forceinline__ float block_dot(const uint32_t (&x)[16], const uint32
     s0 = __hfma2(half2_of(x[i]), half2_of(y[i]), s0);
     s1 = __hfma2(half2_of(x[8 + i]), half2_of(y[8 + i]), s1);
   }
-  const float2 f0 = __half22float2(s0), f1 = __half22float2(s1);
-  return (f0.x + f0.y) + (f1.x + f1.y);
+  // the four lanes' sums into fp32, each half taken as it lies
+  float r;
+  asm("{\n\t.reg .b16 a, b, c, d, one;\n\t.reg .f32 f;\n\tmov.b32 {a, b}, %1;\n\tmov.b32 {c, d}, %2;\n\t"
+      "mov.b16 one, 0x3C00;\n\tfma.rn.f32.f16 f, a, one, 0f00000000;\n\tfma.rn.f32.f16 f, b, one, f;\n\t"
+      "fma.rn.f32.f16 f, c, one, f;\n\tfma.rn.f32.f16 %0, d, one, f;\n\t}"
+      : "=f"(r)
+      : "r"(*reinterpret_cast<const uint32_t *>(&s0)), "r"(*reinterpret_cast<const uint32_t *>(&s1)));
+  return r;
 }
 
 // 2^(byte - 127), NaN for 0xFF.
