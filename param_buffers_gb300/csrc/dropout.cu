@@ -188,6 +188,9 @@ __global__ void __launch_bounds__(kThreads, Shape<TI, TO, RES>::MIN_BLOCKS)
 //
 // That needs one `head` for all arrays of a row, i.e. rows of like length one after another: the
 // ordinary odd case.  Arrays that lie differently take dropout_elements_kernel.
+//
+// [4000, 3001] fp32 onto fp32 22.3 us (96 % of a copy's rate), bf16 alone 13.2 (54 %: the calls, a lane in 32 of
+// which is lost, and one vector a thread in flight), [16384, 1001] bf16 onto bf16 19.1 (76 %).
 struct Shifted {
   int32_t items;        // groups of all rows
   int32_t vector_blocks;

@@ -13,7 +13,7 @@
 
 namespace {
 
-// ------------------------------------------------------------ block-scaled (MXFP8, NVFP4)
+// ------------------------------------------------------------ block-scaled (MXFP8, NVFP4, MXFP4)
 //
 // Y[M,N] (bf16) = dq(Xq, Xs) dq(Wq, Ws)^T on the block-scaled tensor-core path, operands
 // K-major with 128-byte rows per stage, scales read from tensor memory:
@@ -1188,8 +1188,22 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
   return launch_blockscaled<FMT, EPI, 3>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
 }
 
-// Stages measured, PFLOP/s for 4 / 5 / 6: fc1 fprop 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 /
-// 5.30.  MXFP4's scale words take half of NVFP4's room, which is what makes the sixth fit.
+// MXFP4 on the fc1 shape (8192 tokens, 2048 -> 8192): forward 45.9 us, 5.99 PFLOP/s, 0.80 of the 7.5 that the
+// fp4 instruction issues at (four times bf16's measured rate); dgrad 42.5 us, 6.46; wgrad 50.6 us, 5.43.
+//
+// A stage of 256 contraction elements is 512 tensor cycles; measured, the dgrad (32 stages a tile) takes 581 and
+// the forward (8) 685 with its tile's boundary, about 430 cycles of waiting for the one accumulator and 130 for the
+// first operands.  What a stage moves through an SM's shared memory explains most of the 581: 35 KB written
+// by the copies, 32 KB read by the instructions, 3 KB of scales, at 128 B a cycle 547 cycles.  Taken away one by
+// one in copies of the kernel (times only): the output's stores 43.4 us of the forward's 46, the scale copies
+// 44.6, the accumulate's read-modify-write 45.6 of the wgrad's 50.6; about 5 us of a launch lie outside
+// the first and last instruction.
+//
+// Stages, PFLOP/s for 4 / 5 / 6: forward 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 / 5.30
+// (before the copies were issued by whole warps).  MXFP4's scale words take half of NVFP4's room, which is what
+// makes the sixth fit.  Tried and slower: asking for operands in L2 ahead (55 us), outputs from registers in
+// 16-byte (58) and 32-byte stores (50.5), the wgrad's sums as vector reductions from registers (52.1), more
+// staging buffers for it (53), its old sums asked for ahead (54.7); tile groups of 1 to 16 rows within 1 %.
 constexpr int kMx4Stages = 6;
 
 // The MXFP4 products: any contraction length (code rows hold whole blocks of 32, zero past the end;

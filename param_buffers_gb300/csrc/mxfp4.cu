@@ -46,6 +46,14 @@ constexpr int kThreads = 256;
 // A source whose rows do not all start on 16 bytes (RAGGED: any odd row length) is read in the 16-byte
 // vectors that cover a thread's elements, one more than they fill, and shifted into place in registers;
 // the first and last elements of the source, whose vectors would reach outside it, go one by one.
+//
+// What bounds it, on [8192, 8192] (share of a copy's rate of the bytes that have to move): to nearest the
+// memory, nearly: bf16 both views 36.2 us (84 %), rowwise 26.8 (94 %), columnwise 30.1 (83 %); fp32 56.2 (89 %),
+// 44.5 (101 %), 49.5 (91 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply pipes 58 %): bf16
+// both views 57.7 us (53 %), rowwise 35.3, columnwise 35.0; fp32 72.1 (70 %).  Ten rounds of the generator, one
+// call for 16 elements of a view, are 17 us of those 57.7 (with two rounds, for the time only, 48.0 of
+// 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 57 us to nearest and 77
+// stochastically: selecting shifted words costs two integer instructions an element.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -198,7 +206,8 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
 
 // Blocks an SM that the registers are held to: latency against spills.  On [8192, 8192], 2 / 3 / 4 blocks: bf16
 // both views 45.8 / 39.4 / 37.2 us to nearest and 67.8 / 62.0 / 61.8 stochastically; fp32 both views 57.6 / 66.6 /
-// 92.2 (its 64 registers of tile words spill from 3 on), but the rowwise view alone 46.7 / 44.6 / 48.8.
+// 92.2 (its 64 registers of tile words spill from 3 on), but the rowwise view alone 46.7 / 44.6 / 48.8 (all before
+// the maxima and the scaling took fewer instructions).
 template <typename T, bool COL>
 constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL ? 2 : 3;
 
@@ -323,6 +332,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
 // (the last lane of a warp only reads), under up to two scale bytes.  Items (row, v) run over all rows'
 // half blocks, narrow rows side by side in a warp; the up to 15 elements at either end of a shifted row
 // go one by one, a thread each, in the blocks after the others.
+//
+// The bytes bound it: [8192, 8192] bf16 26.2 us (96 % of a copy's rate), fp32 45.0 (100 %); [8192, 8001] bf16,
+// shifted, 34.2 (72 %: the integer work of the shifts).
 __device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) {
   return byte == gtp::mx4::kNanScale ? 0x7FC0u : byte == 0 ? 0x0040u : byte << 7;
 }

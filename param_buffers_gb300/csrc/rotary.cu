@@ -170,12 +170,15 @@ struct Chunk {
 // Chunks a thread (all loaded ahead) and blocks an SM, measured: bf16 (32768 tokens of 20 heads of 128) 49.3 us
 // with 2 and 5 against 56.7 (2, unbounded registers), 51.9 (1 ahead, 6) and 63.1 (1 and 6); fp32 (32769
 // tokens of 20 heads, 64 of 128 elements turned) 101.7 us with 1 and 6 against 110.2 (2 and 5).
+//
+// The bytes bound it: 6.8 TB/s on both of these (49.3 and 97.7 us since rows of 32 bytes), the rate of a copy.
+// 8192 tokens of 20 heads of 64 (the packed QKV product of a microbatch) take 9.1 us, 4.6 TB/s: the ramp and the
+// drain of one wave.  Blocks that stay and load ahead of the sines were slower there.
 template <typename T>
 struct Shape {
   static constexpr int CHUNKS = sizeof(T) == 2 ? 2 : 1;
   static constexpr int MIN_BLOCKS = sizeof(T) == 2 ? 5 : 6;
 };
-
 
 template <typename T, bool VEC, bool IL>
 __global__ void __launch_bounds__(kThreads, Shape<T>::MIN_BLOCKS)
@@ -244,7 +247,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::MIN_BLOCKS)
 
 template <typename T, bool VEC>
 gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStream_t st) {
-  // as many tokens to a block as fill its threads' chunks, and no more, so that a short batch spreads
+  // As many tokens to a block as fill its threads' chunks, and no more, so that a short batch spreads.  On 8192
+  // tokens of 20 heads of 64, 2 / 3 / 4 / 5 / 6 (the rule's) / 8 / 11 / 16: 11.5 / 10.1 / 9.6 / 9.5 / 9.1 / 10.0 /
+  // 10.1 / 11.7 us.
   a.chunks = a.half / (VEC ? 8 : 1);
   a.units = a.heads * a.chunks;
   a.by_half = gtp::make_fastdiv(a.half);

@@ -115,3 +115,28 @@ def test_large_rows_and_empty():
     # 0.1 of an ulp-sized x could round away: bf16 keeps x + 1.11 x apart from x always
     assert np.array_equal(moved, keep | (x[rows].cpu().float().numpy() == 0))
     gtp.gtp_dropout_add(x[:0], x[:0], out[:0], 0.1, (2, 3))
+
+
+def test_side_stream_and_captured_offset():
+    """On a stream of its own, captured once: each replay draws at the device's offset, both ways."""
+    x, r = torch.randn(40, 100, device=DEV), torch.randn(40, 100, device=DEV)
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    word = torch.zeros(1, dtype=torch.int64, device=DEV)
+    rng = gtp.Rng(6, 1 << 33, word)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gtp.gtp_dropout_add(x, r, out, 0.3, rng, stream=side)
+    gtp.gtp_dropout_grad(x, dx, 0.3, rng, stream=side)
+    side.synchronize()
+    check(out, x, 0.3, (6, 1 << 33), r)
+    check(dx, x, 0.3, (6, 1 << 33))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        gtp.gtp_dropout_add(x, r, out, 0.3, rng)
+        gtp.gtp_dropout_grad(x, dx, 0.3, rng)
+    for step in (3, 4):
+        word.fill_(step)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, x, 0.3, (6, (1 << 33) + step), r)
+        check(dx, x, 0.3, (6, (1 << 33) + step))

@@ -127,3 +127,24 @@ def test_long_batch_and_empty():
     rows = [0, 1, 8191, 8192, 20000]
     check(out[rows], x[rows], rows, turns, "half")
     gtp.gtp_rotary(x[:0], out[:0], turns)
+
+
+def test_side_stream_and_captured_positions():
+    """On a stream of its own, captured once: each replay turns by the positions on the device then."""
+    x = torch.randn(9, 3, 64, device=DEV)
+    out = torch.empty_like(x)
+    pos = torch.arange(9, dtype=torch.int32, device=DEV)
+    turns, _ = gtp.gtp_rotary_turns(gtp.RotaryConfig(64))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gtp.gtp_rotary(x, out, turns, positions=pos, stream=side)
+    side.synchronize()
+    check(out, x, pos.tolist(), turns, "half")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        gtp.gtp_rotary(x, out, turns, positions=pos)
+    for step in (1, 2):
+        pos.add_(1000)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, x, pos.tolist(), turns, "half")
