@@ -44,16 +44,19 @@ constexpr int kThreads = 256;
 // bank conflicts.
 //
 // A source whose rows do not all start on 16 bytes (RAGGED: any odd row length) is read in the 16-byte
-// vectors that cover a thread's elements, one more than they fill, and shifted into place in registers;
-// the first and last elements of the source, whose vectors would reach outside it, go one by one.
+// vectors that cover a thread's elements, one more than they fill, and shifted into place in registers.
+// Rows 8 apart start at the same place in a vector, so a warp takes such rows and shifts by whole words that are
+// known when it is compiled (selecting them by the address took 57 us on [8001, 8191] bf16 against 45).
+// Rows' and columns' ends are read past, inside the source, and masked; only the source's own corners, whose
+// vectors would reach outside it, go element by element ([1111, 1535]: 7.5 us against 12.4 when every end did).
 //
 // What bounds it, on [8192, 8192] (share of a copy's rate of the bytes that have to move): to nearest the
-// memory, nearly: bf16 both views 36.2 us (84 %), rowwise 26.8 (94 %), columnwise 30.1 (83 %); fp32 56.2 (89 %),
-// 44.5 (101 %), 49.5 (91 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply pipes 58 %): bf16
-// both views 57.7 us (53 %), rowwise 35.3, columnwise 35.0; fp32 72.1 (70 %).  Ten rounds of the generator, one
-// call for 16 elements of a view, are 17 us of those 57.7 (with two rounds, for the time only, 48.0 of
-// 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 57 us to nearest and 77
-// stochastically: selecting shifted words costs two integer instructions an element.
+// memory, nearly: bf16 both views 35.5 us (86 %), rowwise 26.6 (95 %), columnwise 29.2 (86 %); fp32 55.3 (91 %),
+// 44.4 (101 %), 48.0 (94 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply pipes 58 %): bf16
+// both views 57.4 us (53 %), rowwise 32.4, columnwise 34.9; fp32 70.4 (71 %).  Ten rounds of the generator, one
+// call for 16 elements of a view, are 17 us of those 57.4 (with two rounds, for the time only, 48.0 of
+// 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 44.7 us to nearest and 61.6
+// stochastically, fp32 76.6 and 87.9: a third more loads, whose vectors hold the registers.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -109,26 +112,40 @@ __device__ __forceinline__ void load_sectors(const T *p, uint32_t (&w)[N]) {
   }
 }
 
-// The 16-byte vectors around the 16 elements at p lie inside the source.
-template <typename T>
+// The 16-byte vectors around the 16 elements at p, one more than they fill where rows start anywhere, lie inside
+// the source.
+template <typename T, bool RAGGED>
 __device__ __forceinline__ bool window_inside(const T *p, const TileArgs &a) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15), begin = reinterpret_cast<uintptr_t>(a.src);
-  return b >= begin && b + 16 * (Tile<T>::THREAD_WORDS / 4 + 1) <= begin + uintptr_t(a.src_bytes);
+  return b >= begin && b + 16 * (Tile<T>::THREAD_WORDS / 4 + (RAGGED ? 1 : 0)) <= begin + uintptr_t(a.src_bytes);
 }
 
-// 16 elements at an element-aligned address, out of the vectors around them: whole words by two rounds of
-// selects on the address's bits, a half word by funnel shifts.
-template <typename T, int N>
+// 16 elements at an element-aligned address, out of the vectors around them, which start J words and (HALF) one
+// bf16 before them.
+template <typename T, int J, bool HALF, int N>
 __device__ __forceinline__ void load_shifted(const T *p, uint32_t (&w)[N]) {
-  const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
-  uint32_t t[N + 4];
-  load_words(reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)), t);
+  constexpr int V = (J + N + (HALF ? 1 : 0) + 3) / 4;  // vectors that hold any of them
+  const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+  uint32_t t[4 * V];
 #pragma unroll
-  for (int k = 0; k < N + 2; ++k) t[k] = s & 8u ? t[k + 2] : t[k];
+  for (int i = 0; i < V; ++i) {
+    const uint4 v = __ldcs(q + i);
+    t[4 * i] = v.x, t[4 * i + 1] = v.y, t[4 * i + 2] = v.z, t[4 * i + 3] = v.w;
+  }
 #pragma unroll
-  for (int k = 0; k < N + 1; ++k) t[k] = s & 4u ? t[k + 1] : t[k];
+  for (int k = 0; k < N; ++k) w[k] = HALF ? __funnelshift_r(t[k + J], t[(k + J + 1) % (4 * V)], 16) : t[k + J];
+}
+
+// The same of four rows, at these offsets.
+template <typename T, int J, int N>
+__device__ __forceinline__ void load_rows(const T *p, const int64_t (&off)[4], bool half, uint32_t (&w)[4][N]) {
+  if (sizeof(T) == 2 && half) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) w[k] = sizeof(T) == 2 ? __funnelshift_r(t[k], t[k + 1], 8 * (s & 2u)) : t[k];
+    for (int it = 0; it < 4; ++it) load_shifted<T, J, sizeof(T) == 2>(p + off[it], w[it]);
+  } else {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) load_shifted<T, J, false>(p + off[it], w[it]);
+  }
 }
 
 // Index of word `w` of row `r` in the tile.
@@ -207,12 +224,12 @@ __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte
 // Blocks an SM that the registers are held to: latency against spills.  On [8192, 8192], 2 / 3 / 4 blocks: bf16
 // both views 45.8 / 39.4 / 37.2 us to nearest and 67.8 / 62.0 / 61.8 stochastically; fp32 both views 57.6 / 66.6 /
 // 92.2 (its 64 registers of tile words spill from 3 on), but the rowwise view alone 46.7 / 44.6 / 48.8 (all before
-// the maxima and the scaling took fewer instructions).
-template <typename T, bool COL>
-constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL ? 2 : 3;
+// the maxima and the scaling took fewer instructions).  A ragged fp32 rowwise view 49.7 with 2, 67.6 with 3.
+template <typename T, bool COL, bool RAGGED>
+constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL || RAGGED ? 2 : 3;
 
 template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
-__global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
   using F = Tile<T>;
   constexpr int TW = F::THREAD_WORDS;
   extern __shared__ __align__(16) uint32_t tile[];  // COL: [128][WORDS]
@@ -222,27 +239,60 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL>) mx4_tile_kernel(
   const uint64_t offset = STOCH ? gtp::rng_offset(a.rng) : 0;
   const int tid = threadIdx.x;
   const int64_t tm = blockIdx.x / a.tiles_n, tn = blockIdx.x - tm * a.tiles_n;
-  const int seg = tid & 7, r32 = tid >> 3;  // this thread's 16 columns, and its row of every 32
+  // this thread's 16 columns, and its row of every 32; a warp's rows are 8 apart where rows start anywhere, so that
+  // they all start at the same place in a vector
+  const int seg = tid & 7, r32 = RAGGED ? (tid >> 5) + 8 * ((tid >> 3) & 3) : tid >> 3;
   const int64_t c0 = kTile * tn + 16 * seg;
   const int nc = int(max(int64_t(0), min(int64_t(16), a.cols - c0)));  // its columns inside the matrix
   uint32_t w[4][TW];
+  const int64_t r0 = kTile * tm + r32;
+  const int nr = int(max(int64_t(0), min(int64_t(4), (a.rows - r0 + 31) >> 5)));  // its rows inside
+  const T *p = static_cast<const T *>(a.src) + r0 * a.ld + c0;
+  const auto load = [&](const T *q, uint32_t(&v)[TW]) {
+    if (sizeof(T) == 4 && a.wide)
+      load_sectors(q, v);
+    else
+      load_words(reinterpret_cast<const uint32_t *>(q), v);
+  };
+  if (!RAGGED && nr == 4 && nc == 16) {
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int64_t r = kTile * tm + 32 * it + r32;
-    const T *p = static_cast<const T *>(a.src) + r * a.ld + c0;
-    if (r >= a.rows) {
+    for (int it = 0; it < 4; ++it) load(p + 32 * it * a.ld, w[it]);
+  } else {
+    int64_t off[4];  // rows past the end read the first one again
 #pragma unroll
-      for (int i = 0; i < TW; ++i) w[it][i] = 0;
-    } else if (nc == 16 && (!RAGGED || window_inside(p, a))) {
-      if (RAGGED)
-        load_shifted(p, w[it]);
-      else if (sizeof(T) == 4 && a.wide)
-        load_sectors(p, w[it]);
-      else
-        load_words(reinterpret_cast<const uint32_t *>(p), w[it]);
+    for (int it = 0; it < 4; ++it) off[it] = it < nr ? 32 * it * a.ld : 0;
+    const bool some = nr > 0 && nc > 0;
+    // vectors where they lie inside the source, even past a row's end; the elements one by one at its corners
+    if (some && window_inside<T, RAGGED>(p, a) && window_inside<T, RAGGED>(p + 32 * (nr - 1) * a.ld, a)) {
+      if constexpr (RAGGED) {
+        const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+        const bool half = (s & 2u) != 0;
+        if (s < 4)
+          load_rows<T, 0>(p, off, half, w);
+        else if (s < 8)
+          load_rows<T, 1>(p, off, half, w);
+        else if (s < 12)
+          load_rows<T, 2>(p, off, half, w);
+        else
+          load_rows<T, 3>(p, off, half, w);
+      } else {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) load(p + off[it], w[it]);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + F::PER * i, nc - F::PER * i);
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i < TW; ++i) w[it][i] = some ? word_of(p + off[it] + F::PER * i, nc - F::PER * i) : 0u;
+    }
+    if (nr < 4 || nc < 16) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+          const int n = it < nr ? nc - F::PER * i : 0;  // elements of the word inside
+          w[it][i] = n >= F::PER ? w[it][i] : n > 0 ? w[it][i] & 0xFFFFu : 0u;
+        }
     }
   }
   if (COL) {
