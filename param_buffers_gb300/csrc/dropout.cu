@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TI, TO, RES>::MIN_BLOCKS)
 // That needs one `head` for all arrays of a row, i.e. rows of like length one after another: the
 // ordinary odd case.  Arrays that lie differently take dropout_elements_kernel.
 //
-// [4000, 3001] fp32 onto fp32 22.3 us (96 % of a copy's rate), bf16 alone 13.2 (54 %: the calls, a lane in 32 of
-// which is lost, and one vector a thread in flight), [16384, 1001] bf16 onto bf16 19.1 (76 %).
+// [4000, 3001] fp32 onto fp32 22.2 us (96 % of a copy's rate), bf16 alone 12.2 (58 %: the calls, a lane in 32 of
+// which is lost, and the mask's way through bits), [16384, 1001] bf16 onto bf16 18.4 (79 %).
 struct Shifted {
   int32_t items;        // groups of all rows
   int32_t vector_blocks;
@@ -215,6 +215,12 @@ __device__ __forceinline__ int head_of(const DropArgs &a, int64_t row) {
   return int((0u - uint32_t((reinterpret_cast<uintptr_t>(static_cast<const TO *>(a.out) + row * a.out_ld)) / sizeof(TO))) & 7u);
 }
 
+// Items a thread, loaded together; with 1 / 2 / 3: bf16 alone [16384, 3001] 48.1 / 45.8 / 43.2 us, bf16 onto bf16
+// [16384, 1001] 19.3 / 18.4 / 18.7, fp32 to bf16 [8001, 3001] 24.4 / 23.3 / 23.9, bf16 onto fp32 [8001, 3001] 36.1 / 36.2 /
+// 36.7 (98 % of a copy's rate).
+template <typename TI, typename TO, bool RES>
+constexpr int kShiftedItems = sizeof(TI) + sizeof(TO) > 4 ? (RES ? 1 : 2) : RES ? 2 : 3;
+
 template <typename TI, typename TO, bool RES>
 __global__ void __launch_bounds__(kThreads)
     dropout_shifted_kernel(const __grid_constant__ DropArgs a, const __grid_constant__ Shifted s) {
@@ -230,35 +236,45 @@ __global__ void __launch_bounds__(kThreads)
     if (e < 8 ? j < head : j < a.cols) one_element<TI, TO, RES>(a, offset, row, j);
     return;
   }
+  constexpr int N = kShiftedItems<TI, TO, RES>;
   const int lane = threadIdx.x & 31;
-  const int item = (int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5)) * 31 + lane;
-  const int row32 = gtp::fast_div(min(item, s.items - 1), s.by_groups), v = min(item, s.items - 1) - row32 * s.groups;
-  const int64_t row = row32;
-  const int head = head_of<TO>(a, row);
-  const int64_t j = head + 8 * int64_t(v);
-  const bool whole = lane < 31 && item < s.items && j + 8 <= a.cols;
-  Eight<TI> x;
-  Eight<TO> res;
-  if (whole) {
-    x.load(static_cast<const TI *>(a.x) + row * a.x_ld + j);
-    if (RES) res.load(static_cast<const TO *>(a.residual) + row * a.residual_ld + j);
-  }
-  const Mask m(a, offset, v, row + a.row0);
-  uint32_t keep = 0;
+  const int first = (int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5)) * N * 31 + lane;
+  Eight<TI> x[N];
+  Eight<TO> res[RES ? N : 1];
+  int row[N], v[N], head[N];
+  bool whole[N];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) keep |= (m.keep(k) ? 1u : 0u) << k;
-  // where head > 0 the vector reaches into group v + 1 of the same row, which exists
-  keep = (keep | __shfl_down_sync(0xFFFFFFFFu, keep, 1) << 8) >> head;
-  if (!whole) return;
-  float f[8], y[8];
-  x.get(f);
-  if (RES) res.get(y);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (!RES) y[k] = 0.f;
-    if (keep >> k & 1) y[k] = RES ? fmaf(f[k], a.scale, y[k]) : f[k] * a.scale;
+  for (int i = 0; i < N; ++i) {
+    const int item = min(first + 31 * i, s.items - 1);
+    row[i] = gtp::fast_div(item, s.by_groups);
+    v[i] = item - row[i] * s.groups;
+    head[i] = head_of<TO>(a, row[i]);
+    const int64_t j = head[i] + 8 * int64_t(v[i]);
+    whole[i] = lane < 31 && first + 31 * i < s.items && j + 8 <= a.cols;
+    if (whole[i]) {
+      x[i].load(static_cast<const TI *>(a.x) + row[i] * a.x_ld + j);
+      if (RES) res[i].load(static_cast<const TO *>(a.residual) + row[i] * a.residual_ld + j);
+    }
   }
-  Eight<TO>::store(static_cast<TO *>(a.out) + row * a.out_ld + j, y);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Mask m(a, offset, v[i], row[i] + a.row0);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) keep |= (m.keep(k) ? 1u : 0u) << k;
+    // where head > 0 the vector reaches into group v + 1 of the same row, which exists
+    keep = (keep | __shfl_down_sync(0xFFFFFFFFu, keep, 1) << 8) >> head[i];
+    if (!whole[i]) continue;
+    float f[8], y[8];
+    x[i].get(f);
+    if (RES) res[i].get(y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (!RES) y[k] = 0.f;
+      if (keep >> k & 1) y[k] = RES ? fmaf(f[k], a.scale, y[k]) : f[k] * a.scale;
+    }
+    Eight<TO>::store(static_cast<TO *>(a.out) + row[i] * a.out_ld + head[i] + 8 * int64_t(v[i]), y);
+  }
 }
 
 // Arrays that lie differently: a thread a group, element by element.
@@ -322,7 +338,7 @@ gtp_status launch(DropArgs a, const gtp::DeviceInfo &dev, cudaStream_t st) {
     s.groups = int32_t(groups);
     s.by_groups = gtp::make_fastdiv(s.groups);
     s.items = int32_t(a.rows * groups);
-    const int64_t a_block = 31 * (kThreads / 32);
+    const int64_t a_block = 31 * (kThreads / 32) * kShiftedItems<TI, TO, RES>;
     s.vector_blocks = int32_t((s.items + a_block - 1) / a_block);
     const int64_t end_blocks = (a.rows * 16 + kThreads - 1) / kThreads;
     const gtp_status e =
