@@ -812,21 +812,26 @@ class Rng(NamedTuple):
 
 
 def _rng(rng):
+    """The bytes of a gtp_rng, or None."""
     if rng is None:
         return None
     seed, offset, *device = rng
-    word = device[0] if device else None
-    if word is not None:
+    word = 0
+    if device and device[0] is not None:
         import torch
-        if word.dtype != torch.int64 or word.numel() != 1 or not word.is_cuda:
+        t = device[0]
+        if t.dtype != torch.int64 or t.numel() != 1 or not t.is_cuda:
             raise TypeError("device_offset must be a one-element int64 CUDA tensor")
-    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
-        raise ValueError("seed and offset are unsigned 64-bit numbers")
-    return C.byref(abi.gtp_rng(seed, offset, _ptr(word)))
+        word = t.data_ptr()
+    try:
+        return abi.RNG_PACK(seed, offset, word)
+    except abi.struct.error:
+        raise ValueError("seed and offset are unsigned 64-bit numbers") from None
 
 
 # The checks below look at each property of a tensor once: a small call is bound by them and the launch.
 
+_F32, _BF16, _U8 = abi.GTP_F32, abi.GTP_BF16, abi.GTP_U8
 _TORCH_DTYPES: dict = {}  # torch dtype -> gtp_dtype; filled at the first call (torch is imported late)
 
 
@@ -844,7 +849,7 @@ def _float_dtype(t, name: str) -> int:
         dt = _TORCH_DTYPES[t.dtype]
     except (AttributeError, KeyError, TypeError):
         dt = _dtype_of(t, name)
-    if dt != abi.GTP_F32 and dt != abi.GTP_BF16:
+    if dt != _F32 and dt != _BF16:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
@@ -861,11 +866,6 @@ def _matrix(t, name: str):
     if inner != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     return dt, shape, ld if shape[0] > 1 else shape[1]
-
-
-def _is_bytes(t) -> bool:
-    """A contiguous uint8 tensor on the GPU."""
-    return _TORCH_DTYPES.get(t.dtype) == abi.GTP_U8 and t.is_cuda and t.is_contiguous()
 
 
 def _scale_bytes(rows: int, blocks: int) -> int:
@@ -894,14 +894,16 @@ def _mxfp4_view(view, rows: int, cols: int, name: str):
     if view is None:
         return 0, 0
     codes, scales = view
-    blocks = -(-cols // 32)
-    try:
-        good = _is_bytes(codes) and _is_bytes(scales) and codes.shape == (rows, 16 * blocks) \
-            and scales.numel() == _scale_bytes(rows, blocks)
-    except AttributeError:
-        good = False
-    if not good:
-        _refuse_view(codes, scales, rows, cols, name)
+    blocks = (cols + 31) >> 5
+    table = _TORCH_DTYPES
+    try:  # contiguous bytes on the GPU, of the right sizes
+        if (table[codes.dtype] == table[scales.dtype] == _U8 and codes.is_cuda and scales.is_cuda
+                and codes.is_contiguous() and scales.is_contiguous() and codes.shape == (rows, blocks << 4)
+                and scales.numel() == ((rows + 127) >> 7) * ((blocks + 3) >> 2) << 9):
+            return codes.data_ptr(), scales.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    _refuse_view(codes, scales, rows, cols, name)
     return codes.data_ptr(), scales.data_ptr()
 
 

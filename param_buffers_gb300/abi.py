@@ -87,6 +87,9 @@ class gtp_rng(C.Structure):
     _fields_ = [("seed", C.c_uint64), ("offset", C.c_uint64), ("device_offset", C.c_void_p)]
 
 
+# The same bytes in one call: building the structure and a reference to it costs three times as much.
+RNG_PACK = struct.Struct("<3Q").pack
+
 # gtp_rotary_scaling
 GTP_ROTARY_UNSCALED, GTP_ROTARY_LINEAR, GTP_ROTARY_BASE, GTP_ROTARY_BANDS, GTP_ROTARY_RAMP = range(5)
 
@@ -113,6 +116,7 @@ ROTARY_DESC_PACK = struct.Struct("<3Q10qQ8ifi").pack
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
+# A gtp_rng or a gtp_rotary_desc goes by reference or packed (VP takes both).
 # name -> (restype, argtypes); every entry point declared in include/gtp.h
 PROTOTYPES = {
     "gtp_last_error": (C.c_char_p, []),
@@ -155,15 +159,15 @@ PROTOTYPES = {
     "gtp_linear_dgrad_mxfp8_tiled": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
     "gtp_linear_wgrad_accum_mxfp8_tiled": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, I64, I64, VP]),
     "gtp_linear_fprop_nvfp4_tiled": (I32, [VP, VP, VP, VP, VP, VP, VP, I64, I64, I64, VP]),
-    "gtp_mxfp4_quantize": (I32, [VP, I32, I64, I64, I64, VP, VP, VP, VP, P(gtp_rng), VP]),
+    "gtp_mxfp4_quantize": (I32, [VP, I32, I64, I64, I64, VP, VP, VP, VP, VP, VP]),
     "gtp_mxfp4_dequantize": (I32, [VP, VP, I64, I64, VP, I32, VP]),
     "gtp_linear_fprop_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
     "gtp_linear_dgrad_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, VP]),
     "gtp_linear_wgrad_accum_mxfp4": (I32, [VP, VP, VP, VP, VP, I64, I64, I64, I64, I64, VP]),
     "gtp_rotary_turns": (I32, [P(gtp_rotary_config), P(C.c_uint64), P(C.c_float)]),
-    "gtp_rotary": (I32, [VP, VP]),  # a gtp_rotary_desc, by reference or packed
-    "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
-    "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, P(gtp_rng), VP]),
+    "gtp_rotary": (I32, [VP, VP]),
+    "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
+    "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
     "gtp_wait_timeouts": (I32, [P(C.c_uint32), I32]),
     "gtp_selftest_wait_timeout": (I32, [I64, VP]),
     "gtp_grad_norm_workspace_bytes": (C.c_size_t, [P(gtp_bucket_desc), I32]),
