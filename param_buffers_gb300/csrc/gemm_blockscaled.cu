@@ -1016,23 +1016,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           for (int i = 0; i < 32; ++i) r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) * alpha);
       }
       constexpr int CW = (EPI == kStoreBf16) ? 32 : 16;  // columns per 64-byte staged row
+      constexpr int CHUNKS = (BN / 2) / CW;
+      // MXFP4: the last tile's chunks are staged in the operand ring, which its MMAs have left and nothing refills, so
+      // that none waits for another's copy out: on one-wave launches most of what follows the MMAs
+      const bool spare = FMT == kMxfp4 && u + npairs >= p.num_units;
+      static_assert(kBsEpiWarps * CHUNKS * kBsEpiBuf <= F::SMEM_OPS, "staging in the operand ring");
 #pragma unroll
-      for (int q = 0; q < (BN / 2) / CW; ++q) {
-        if (lane == 0) bulk_wait_group_read<0>();
+      for (int q = 0; q < CHUNKS; ++q) {
+        uint8_t *const to = spare ? smem + (ew * CHUNKS + q) * kBsEpiBuf : buf;
+        if (!spare && lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
         if (EPI == kStoreBf16)
-          stage_rows64<EPI>(buf, lane, r[q], 0);
+          stage_rows64<EPI>(to, lane, r[q], 0);
         else
-          stage_rows64<EPI>(buf, lane, r[q >> 1], 16 * (q & 1));
+          stage_rows64<EPI>(to, lane, r[q >> 1], 16 * (q & 1));
         fence_proxy_async_smem();
         __syncwarp();
         const int col = tn * BN + (part > 0 ? BN / 2 : 0) + half * (BN / 2) + q * CW;
         if (lane == 0) {
           if (row < p.m_dim && col < p.n_dim) {
             if (EPI == kStoreBf16)
-              tma_store_2d_hint(&tmD, buf, col, row, pol_out);
+              tma_store_2d_hint(&tmD, to, col, row, pol_out);
             else
-              tma_reduce_add_2d(&tmD, buf, col, row);
+              tma_reduce_add_2d(&tmD, to, col, row);
           }
           bulk_commit_group();
         }
