@@ -1219,16 +1219,16 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
   return launch_blockscaled<FMT, EPI, 3>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
 }
 
-// MXFP4 on the fc1 shape (8192 tokens, 2048 -> 8192): forward 45.9 us, 5.99 PFLOP/s, 0.80 of the 7.5 that the
-// fp4 instruction issues at (four times bf16's measured rate); dgrad 42.5 us, 6.46; wgrad 50.6 us, 5.43.
+// MXFP4 on the fc1 shape (8192 tokens, 2048 -> 8192): forward 45.3 us, 6.07 PFLOP/s, 0.81 of the 7.5 that the
+// fp4 instruction issues at (four times bf16's measured rate); dgrad 42.4 us, 6.48; wgrad 50.1 us, 5.49.
 //
 // A stage of 256 contraction elements is 512 tensor cycles; measured, the dgrad (32 stages a tile) takes 581 and
 // the forward (8) 685 with its tile's boundary, about 430 cycles of waiting for the one accumulator and 130 for the
 // first operands.  What a stage moves through an SM's shared memory explains most of the 581: 35 KB written
 // by the copies, 32 KB read by the instructions, 3 KB of scales, at 128 B a cycle 547 cycles.  Taken away one by
 // one in copies of the kernel (times only): the output's stores 43.4 us of the forward's 46, the scale copies
-// 44.6, the accumulate's read-modify-write 45.6 of the wgrad's 50.6; about 5 us of a launch lie outside
-// the first and last instruction.
+// 44.6, the accumulate's read-modify-write 45.6 of the wgrad's 50.6; about 5 us of a launch lay outside
+// the first and last instruction (4.5 since the last tile leaves through the operand ring).
 //
 // Stages, PFLOP/s for 4 / 5 / 6: forward 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 / 5.30
 // (before the copies were issued by whole warps).  MXFP4's scale words take half of NVFP4's room, which is what
