@@ -1228,7 +1228,7 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
 // by the copies, 32 KB read by the instructions, 3 KB of scales, at 128 B a cycle 547 cycles.  Taken away one by
 // one in copies of the kernel (times only): the output's stores 43.4 us of the forward's 46, the scale copies
 // 44.6, the accumulate's read-modify-write 45.6 of the wgrad's 50.6; about 5 us of a launch lay outside
-// the first and last instruction (4.5 since the last tile leaves through the operand ring).
+// the first and last instruction, 0.4 less since the last tile leaves through the operand ring.
 //
 // Stages, PFLOP/s for 4 / 5 / 6: forward 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 / 5.30
 // (before the copies were issued by whole warps).  MXFP4's scale words take half of NVFP4's room, which is what
