@@ -68,8 +68,19 @@ __device__ __forceinline__ uint32_t codes8_cut(const uint64_t (&y)[4]) {
   return w;
 }
 
-// Eight codes of eight scaled values (in pairs) stochastically, with the random bytes of r0 (first four) and
-// r1.  A value times 2^-126 is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
+// What codes8_stochastic takes is x / scale times 2^-126, one product of x with 2^(1 - byte).  Above byte 134
+// (values of 2^8 and more) that is no bf16; such a block's values are first multiplied by 2^(120 - byte), which takes
+// them to 2^-7 of their share of the scale (exact in bf16 down to 2^-119 of it), and then by 2^-119.
+__device__ __forceinline__ bool is_far(uint32_t byte) { return byte > 134u && byte != kNanScale; }
+__device__ __forceinline__ float near_factor(uint32_t byte) {  // 2^(120 - byte) of a far block, else 1
+  return is_far(byte) ? inv_scale(byte) * 0x1p-7f : 1.f;
+}
+__device__ __forceinline__ float down_factor(uint32_t byte) {
+  return is_far(byte) ? 0x1p-119f : inv_scale(byte) * 0x1p-126f;
+}
+
+// Eight codes of eight values (in pairs), scaled and times 2^-126, stochastically, with the random bytes of
+// r0 (first four) and r1.  Such a value is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
 // [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23 fractional bits
 // (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
 // the random byte in their place, centred (byte << 14 | 1 << 13, one byte permute and one
@@ -77,11 +88,11 @@ __device__ __forceinline__ uint32_t codes8_cut(const uint64_t (&y)[4]) {
 // by a conversion that rounds stochastically with no random bits.  At most 6 stays at most 6: its
 // fraction is 0.
 __device__ __forceinline__ uint32_t codes8_stochastic(const uint64_t (&x)[4], uint32_t r0, uint32_t r1) {
-  const uint64_t down = pack2(0x1p-126f, 0x1p-126f), up = pack2(0x1p126f, 0x1p126f);
+  const uint64_t up = pack2(0x1p126f, 0x1p126f);
   uint64_t y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t t = mul2(x[i], down);
+    const uint64_t t = x[i];
     const uint32_t r = i < 2 ? r0 : r1;
     // byte b of r over 0x80: (byte << 8 | 0x80) << 6
     const uint32_t a = __byte_perm(r, 0x80u, (i & 1) ? 0x5524u : 0x5504u);

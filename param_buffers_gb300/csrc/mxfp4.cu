@@ -53,8 +53,8 @@ constexpr int kThreads = 256;
 // What bounds it, on [8192, 8192] (share of a copy's rate of the bytes that have to move): to nearest the
 // memory, nearly: bf16 both views 35.5 us (86 %), rowwise 26.6 (95 %), columnwise 29.2 (86 %); fp32 55.3 (91 %),
 // 44.4 (101 %), 48.0 (94 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply pipes 58 %): bf16
-// both views 57.4 us (53 %), rowwise 32.4, columnwise 34.9; fp32 70.4 (71 %).  Ten rounds of the generator, one
-// call for 16 elements of a view, are 17 us of those 57.4 (with two rounds, for the time only, 48.0 of
+// both views 55.9 us (54 %), rowwise 33.3, columnwise 34.0; fp32 69.7 (72 %).  Ten rounds of the generator, one
+// call for 16 elements of a view, are 17 us of those 55.9 (with two rounds, for the time only, 48.0 of
 // 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 44.7 us to nearest and 61.6
 // stochastically, fp32 76.6 and 87.9: a third more loads, whose vectors hold the registers.
 constexpr int kTile = 128;
@@ -200,6 +200,25 @@ __device__ __forceinline__ uint64_t scaled_halves(uint32_t a, bool a_high, uint3
   return gtp::mx4::pack2(scaled_half(a, a_high, inv), scaled_half(b, b_high, inv));
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Far blocks' values brought near (mx4::near_factor; one product an element fewer for all the others, both views of
+// [8192, 8192] bf16 57.4 -> 55.9 us), on the words as they lie, so that the branch, which
+// real data hardly takes, holds no registers of its own: one block's, or (bf16) those of the low and the high halves.
+template <typename T, int N>
+__device__ __forceinline__ void bring_near(uint32_t (&w)[N], uint32_t low, uint32_t high) {
+  if (!(gtp::mx4::is_far(low) || gtp::mx4::is_far(high))) return;
+  const uint32_t f0 = __float_as_uint(gtp::mx4::near_factor(low)), f1 = __float_as_uint(gtp::mx4::near_factor(high));
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    w[i] = sizeof(T) == 2 ? mul_bf16x2(w[i], f0 >> 16 | (f1 & 0xFFFF0000u))
+                          : __float_as_uint(__uint_as_float(w[i]) * __uint_as_float(f0));
+}
+
 // 2 N values in pairs, divided by the scale of their block's `byte`, to codes; view row r and its first group of draws.
 template <bool STOCH, int N>
 __device__ __forceinline__ void encode_run(const uint64_t (&x)[N], uint32_t byte, uint32_t (&w)[N / 4], uint32_t stream,
@@ -313,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile
       if (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16) << 16;
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       const uint32_t byte = gtp::mx4::scale_byte<STOCH>(m);
-      const float inv = gtp::mx4::inv_scale(byte);
+      const float inv = STOCH ? gtp::mx4::down_factor(byte) : gtp::mx4::inv_scale(byte);
+      if (STOCH) bring_near<T>(w[it], byte, byte);
       uint64_t x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -341,12 +361,15 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile
         v[k] = t[k * F::WORDS];
         m = max_magnitude<T>(m, v[k]);
       }
+      const uint32_t b0 = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : m << 16);
+      const uint32_t b1 = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : m & 0xFFFF0000u);
+      if (STOCH) bring_near<T>(v, b0, b1);
 #pragma unroll
       for (int e = 0; e < F::PER; ++e) {
         const int c = F::PER * p + e;
         const int64_t gc = kTile * tn + c;
-        const uint32_t byte = gtp::mx4::scale_byte<STOCH>(F::PER == 1 ? m : e ? m & 0xFFFF0000u : m << 16);
-        const float inv = gtp::mx4::inv_scale(byte);
+        const uint32_t byte = e ? b1 : b0;
+        const float inv = STOCH ? gtp::mx4::down_factor(byte) : gtp::mx4::inv_scale(byte);
         uint64_t x[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -387,12 +410,6 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile
 // shifted, 34.2 (72 %: the integer work of the shifts).
 __device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) {
   return byte == gtp::mx4::kNanScale ? 0x7FC0u : byte == 0 ? 0x0040u : byte << 7;
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // Two codes in the low byte of w to two bf16 values; mag: their magnitudes.
