@@ -713,7 +713,8 @@ gtp_status gtp_rotary_turns(const gtp_rotary_config *cfg, uint64_t *turns, float
  * h src_head (element strides; a head's elements are contiguous), likewise dst: the packed QKV
  * product [tokens, groups, queries + key + value, head_dim] rotates its queries and keys as
  * groups x (queries + 1) heads of a group stride of queries + 2.  dst may be src exactly (in place)
- * and otherwise may not overlap it; the heads of dst may not overlap each other (GTP_E_ARG). */
+ * and otherwise may not overlap it; the heads of dst may not overlap each other (GTP_E_ARG).  At most
+ * 2^20 heads and 2^30 elements a token (GTP_E_SHAPE). */
 typedef struct {
   const void *src;
   void *dst;

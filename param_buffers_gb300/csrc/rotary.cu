@@ -338,6 +338,9 @@ extern "C" gtp_status gtp_rotary(const gtp_rotary_desc *d, gtp_stream stream) {
     return gtp::fail(GTP_E_SHAPE, "rot_dim must be even, 2 to %d and at most head_dim", 2 * kMaxPairs);
   if (d->tokens > INT32_MAX || int64_t(d->groups) * d->heads > (1 << 20))
     return gtp::fail(GTP_E_SHAPE, "more than 2^31 - 1 tokens or 2^20 heads");
+  // a block walks its tokens' elements in 32 bits
+  if (int64_t(d->groups) * d->heads > (int64_t(1) << 30) / d->head_dim)
+    return gtp::fail(GTP_E_SHAPE, "more than 2^30 elements in a token's heads");
   if (!d->turns) return gtp::fail(GTP_E_ARG, "null turns");
   if (!std::isfinite(d->scale)) return gtp::fail(GTP_E_ARG, "scale must be finite");
   if (d->tokens_per_position < 1 || d->positions_per_sequence < 0)

@@ -73,7 +73,8 @@ def test_rotary_argument_errors():
                 dict(positions=a[1] + 64)):
         assert r(**bad) == abi.GTP_E_ARG, bad
     for bad in (dict(rot_dim=63), dict(rot_dim=66), dict(rot_dim=0), dict(head_dim=0),
-                dict(head_dim=512, rot_dim=258), dict(tokens=(1 << 32) + 1), dict(heads=1 << 21)):
+                dict(head_dim=512, rot_dim=258), dict(tokens=(1 << 32) + 1), dict(heads=1 << 21),
+                dict(heads=1 << 15, head_dim=1 << 16)):              # 2^31 elements in a token's heads
         assert r(**bad) == abi.GTP_E_SHAPE, bad
     assert r(src=a[0] + 1) == abi.GTP_E_ALIGN and r(positions=a[2] + 2) == abi.GTP_E_ALIGN
     assert r(positions=a[2] + 4, positions64=1) == abi.GTP_E_ALIGN
