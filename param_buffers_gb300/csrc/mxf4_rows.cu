@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks<MT>) mx4_rows_kernel(c
       for (int i = 0; i < kGroupRows; ++i) {
         c[i] = make_uint4(0, 0, 0, 0);
         if (n0 + 32 * i < p.n_dim)
-          c[i] = __ldg(reinterpret_cast<const uint4 *>(p.b) + (n0 + 32 * i) * p.blocks + k);
+          c[i] = *(reinterpret_cast<const uint4 *>(p.b) + (n0 + 32 * i) * p.blocks + k);
       }
-      const uint4 s = __ldg(reinterpret_cast<const uint4 *>(p.bs + (tile * p.words + (k >> 2)) * 512) + r0);
+      const uint4 s = *(reinterpret_cast<const uint4 *>(p.bs + (tile * p.words + (k >> 2)) * 512) + r0);
       uint4 x[MT];
       uint32_t sx[MT];
 #pragma unroll
@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks<MT>) mx4_rows_kernel(c
         x[m] = make_uint4(0, 0, 0, 0);
         sx[m] = 0;
         if (m < p.m_dim) {
-          x[m] = __ldg(reinterpret_cast<const uint4 *>(p.a) + m * p.blocks + k);
-          sx[m] = __ldg(p.as + (k >> 2) * 512 + 16 * m + (k & 3));
+          x[m] = *(reinterpret_cast<const uint4 *>(p.a) + m * p.blocks + k);
+          sx[m] = p.as[(k >> 2) * 512 + 16 * m + (k & 3)];
         }
       }
       const uint32_t sw[kGroupRows] = {s.x, s.y, s.z, s.w};

@@ -429,7 +429,7 @@ struct ValueArgs {
 
 __device__ __forceinline__ uint32_t scale_byte_at(const ValueArgs &a, int64_t row, int64_t b) {
   const int64_t r = row + a.row0;
-  return __ldg(a.scales + ((r >> 7) * a.words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3));
+  return a.scales[((r >> 7) * a.words + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)];
 }
 
 constexpr int kValueItems = 2;  // items a thread has in flight

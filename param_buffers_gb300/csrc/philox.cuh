@@ -41,9 +41,11 @@ inline RngArgs rng_args(const gtp_rng *r) {
 }
 
 #ifdef __CUDACC__
-// The call's offset; the device word (a captured graph's step count) is added when the kernel runs.
+// The call's offset; the device word (a captured graph's step count) is added when the kernel runs.  It is read, like
+// everything that a kernel before this one may have written, by an ordinary load: loads through the read-only path
+// need not stay behind the wait for that kernel.
 __device__ __forceinline__ uint64_t rng_offset(const RngArgs &r) {
-  return r.device_offset ? r.offset + __ldg(r.device_offset) : r.offset;
+  return r.device_offset ? r.offset + *r.device_offset : r.offset;
 }
 
 __device__ __forceinline__ uint4 philox(const RngArgs &r, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {

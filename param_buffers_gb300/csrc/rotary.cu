@@ -47,10 +47,11 @@ struct RotaryArgs {
   float scale;
 };
 
+// Positions are read by ordinary loads: the kernel before this one may have written them.
 __device__ __forceinline__ int64_t position_of(const RotaryArgs &a, int64_t t) {
   if (a.positions)
-    return a.positions64 ? __ldg(static_cast<const int64_t *>(a.positions) + t)
-                         : int64_t(__ldg(static_cast<const int32_t *>(a.positions) + t));
+    return a.positions64 ? __ldca(static_cast<const long long *>(a.positions) + t)
+                         : int64_t(__ldca(static_cast<const int32_t *>(a.positions) + t));
   int64_t p = t / a.tokens_per_position;
   if (a.positions_per_sequence) p %= a.positions_per_sequence;
   return a.pos0 + p;
