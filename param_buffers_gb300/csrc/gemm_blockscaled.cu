@@ -530,7 +530,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before any remote arrive or multicast
+  // both CTAs' barriers exist before any remote arrive or multicast
+  if (FMT == kMxfp4)
+    cluster_sync_relaxed();
+  else
+    cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   unsigned int *err = &g_gtp_wait_timeouts;
@@ -994,9 +998,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const int row = tm * F::BMP + F::BMC * int(rank) + 32 * quarter;
+      const bool more = FMT != kMxfp4 || u + npairs < p.num_units;  // another tile waits for the accumulator
       // nothing of this warp's to write: a half-width tile's other half, or rows past the output
       if (FMT == kMxfp4 && ((part >= 0 && half == 1) || row >= p.m_dim)) {
-        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0);
+        if (more && lane == 0) mbar_arrive_cluster_relaxed(tempty0);
         acc_phase ^= 1u;
         continue;
       }
@@ -1009,7 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
       __syncwarp();
       // the next tile's MMAs may overwrite it: the loads above have completed (wait::ld), and
       // a release here would also wait for this warp's earlier stores in flight
-      if (lane == 0) mbar_arrive_cluster_relaxed(tempty0);
+      if (more && lane == 0) mbar_arrive_cluster_relaxed(tempty0);
       if (FMT == kNvfp4) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -1022,7 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
       // chunk waits for another's copy out.  Sums go out in rows of 128 bytes, whole lines of the output (QKV
       // wgrad 15.3 -> 14.7 us, 1111 tokens 9.4 -> 8.9); bf16 in the usual 64, which leave sooner (QKV forward
       // 14.0 us against 14.2).
-      if (FMT == kMxfp4 && u + npairs >= p.num_units) {
+      if (!more) {
         constexpr int COLS = (EPI == kStoreBf16) ? CW : 2 * CW, CHUNKS = (BN / 2) / COLS, BUF = 32 * (EPI == kStoreBf16 ? 64 : 128);
         static_assert(kBsEpiWarps * CHUNKS * BUF <= F::SMEM_OPS, "staging in the operand ring");
 #pragma unroll
@@ -1074,7 +1079,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // neither CTA leaves while the other may still reach its shared memory
+  // neither CTA leaves while the other may still reach its shared memory: MXFP4's last tile signals nobody, and every
+  // arrival before it was waited for
+  if (FMT == kMxfp4)
+    cluster_sync_relaxed();
+  else
+    cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, F::TMEM_COLS);
@@ -1219,8 +1229,8 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
   return launch_blockscaled<FMT, EPI, 3>(a, b, d, As, Bs, a_amax, b_amax, p, grid, dev, st);
 }
 
-// MXFP4 on the fc1 shape (8192 tokens, 2048 -> 8192): forward 45.3 us, 6.07 PFLOP/s, 0.81 of the 7.5 that the
-// fp4 instruction issues at (four times bf16's measured rate); dgrad 42.4 us, 6.48; wgrad 50.1 us, 5.49.
+// MXFP4 on the fc1 shape (8192 tokens, 2048 -> 8192): forward 45.1 us, 6.10 PFLOP/s, 0.81 of the 7.5 that the
+// fp4 instruction issues at (four times bf16's measured rate); dgrad 42.0 us, 6.54; wgrad 49.6 us, 5.54.
 //
 // A stage of 256 contraction elements is 512 tensor cycles; measured, the dgrad (32 stages a tile) takes 581 and
 // the forward (8) 685 with its tile's boundary, about 430 cycles of waiting for the one accumulator and 130 for the
@@ -1228,7 +1238,8 @@ gtp_status run_blockscaled(const uint8_t *Aq, const uint8_t *As, const uint8_t *
 // by the copies, 32 KB read by the instructions, 3 KB of scales, at 128 B a cycle 547 cycles.  Taken away one by
 // one in copies of the kernel (times only): the output's stores 43.4 us of the forward's 46, the scale copies
 // 44.6, the accumulate's read-modify-write 45.6 of the wgrad's 50.6; about 5 us of a launch lay outside
-// the first and last instruction, 0.4 less since the last tile leaves through the operand ring.
+// the first and last instruction, 0.4 less since the last tile leaves through the operand ring and 0.45 less since the
+// cluster's barriers at both ends wait for no memory fence.
 //
 // Stages, PFLOP/s for 4 / 5 / 6: forward 5.49 / 5.80 / 5.97, dgrad 5.40 / 6.08 / 6.29, wgrad 4.95 / 5.16 / 5.30
 // (before the copies were issued by whole warps).  MXFP4's scale words take half of NVFP4's room, which is what

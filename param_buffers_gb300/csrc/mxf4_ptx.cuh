@@ -6,6 +6,13 @@
 namespace gtp {
 namespace ptx {
 
+// The cluster's barrier without the release of its arrival, which waits for a memory fence (about 600 cycles even when
+// nothing is outstanding).  It orders execution alone: barrier inits have their own fence (fence_barrier_init), and
+// whoever uses it at the end of a kernel has seen every remote operation complete by other means.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // tma_load_2d_pair of a 3-D tensor.
 __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap *map, uint32_t bar_cluster_addr, void *dst,
                                                  int32_t c0, int32_t c1, int32_t c2) {
