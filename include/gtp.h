@@ -646,7 +646,8 @@ typedef struct {
 
 /* src[rows, cols] (F32 or BF16, row stride src_ld elements, element-aligned) -> the rowwise view
  * (row_codes, row_scales) and / or the columnwise view (col_codes, col_scales: the rowwise view of
- * src^T, [cols, ceil(rows / 32) * 16 bytes]), which dgrad and wgrad contract over.  A NULL pair is
+ * src^T, [cols, ceil(rows / 32) * 16 bytes]), which dgrad and wgrad contract over.  What lies between
+ * the rows of a strided src may be read (it is not used).  A NULL pair is
  * not written; both views of one source cost one read of it.  rng: host pointer, NULL rounds to
  * nearest.  No output may overlap src or another output (GTP_E_ARG). */
 gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int64_t rows, int64_t cols,

@@ -40,8 +40,8 @@ struct DropArgs {
   gtp::RngArgs rng;
 };
 
-// Eight consecutive elements on 16 bytes (bf16) or 32 (fp32), as they lie in memory: loads in flight hold no more registers
-// than bytes.
+// Eight consecutive elements on 16 bytes (bf16) or 32 (fp32), as they lie in memory: loads in flight hold no
+// more registers than bytes.
 template <typename T>
 struct Eight;
 template <>
@@ -212,12 +212,13 @@ __device__ __forceinline__ void one_element(const DropArgs &a, uint64_t offset, 
 
 template <typename TO>
 __device__ __forceinline__ int head_of(const DropArgs &a, int64_t row) {
-  return int((0u - uint32_t((reinterpret_cast<uintptr_t>(static_cast<const TO *>(a.out) + row * a.out_ld)) / sizeof(TO))) & 7u);
+  const uintptr_t first = reinterpret_cast<uintptr_t>(static_cast<const TO *>(a.out) + row * a.out_ld);
+  return int((0u - uint32_t(first / sizeof(TO))) & 7u);
 }
 
-// Items a thread, loaded together; with 1 / 2 / 3: bf16 alone [16384, 3001] 48.1 / 45.8 / 43.2 us, bf16 onto bf16
-// [16384, 1001] 19.3 / 18.4 / 18.7, fp32 to bf16 [8001, 3001] 24.4 / 23.3 / 23.9, bf16 onto fp32 [8001, 3001] 36.1 / 36.2 /
-// 36.7 (98 % of a copy's rate).
+// Items a thread, loaded together; with 1 / 2 / 3: bf16 alone [16384, 3001] 48.1 / 45.8 / 43.2 us, bf16 onto
+// bf16 [16384, 1001] 19.3 / 18.4 / 18.7, fp32 to bf16 [8001, 3001] 24.4 / 23.3 / 23.9, bf16 onto fp32
+// [8001, 3001] 36.1 / 36.2 / 36.7 (98 % of a copy's rate).
 template <typename TI, typename TO, bool RES>
 constexpr int kShiftedItems = sizeof(TI) + sizeof(TO) > 4 ? (RES ? 1 : 2) : RES ? 2 : 3;
 

@@ -80,9 +80,9 @@ __device__ __forceinline__ float down_factor(uint32_t byte) {
 }
 
 // Eight codes of eight values (in pairs), scaled and times 2^-126, stochastically, with the random bytes of
-// r0 (first four) and r1.  Such a value is a float whose bits below the sign are the E2M1 code itself from bit 22 up: exponents 1, 2, 3 for
-// [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23 fractional bits
-// (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
+// r0 (first four) and r1.  Such a value is a float whose bits below the sign are the E2M1 code itself from bit
+// 22 up: exponents 1, 2, 3 for [1, 2), [2, 4), [4, 8) and the subnormals for [0, 1), where the product keeps 23
+// fractional bits (round to nearest).  The 22 bits below are the fraction of the step to the next point, so adding
 // the random byte in their place, centred (byte << 14 | 1 << 13, one byte permute and one
 // multiply-add), carries into the code with the right probability; what is left of the fraction is cut off
 // by a conversion that rounds stochastically with no random bits.  At most 6 stays at most 6: its

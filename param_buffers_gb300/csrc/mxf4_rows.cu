@@ -20,8 +20,8 @@
 //   [2048, 1024]    2.5     (3.0,  3.6;  5.1)      [128256, 2048] 35.2  (49.7, 86.2; 36)
 // About 2.5 us of each is launch, first loads and the way out.  On large matrices it runs at 3.9 - 4.6 TB/s of the
 // copy's 6.8: blocks come and go, and while one multiplies and adds up its sums it loads nothing.  A persistent form
-// with a ring of asynchronous copies 100 KB an SM deep is bound by instructions instead (73 % of the issue slots; 26.3 us
-// on [28672, 8192]) and costs the small matrices 0.5 - 1 us; the same loads feeding legacy 16-bit matrix
+// with a ring of asynchronous copies 100 KB an SM deep is bound by instructions instead (73 % of the issue
+// slots; 26.3 us on [28672, 8192]) and costs the small matrices 0.5 - 1 us; the same loads feeding legacy 16-bit matrix
 // instructions cost more in unpacking to bf16 than they saved (6.5 us on [8192, 2048], 15 on
 // [2048, 8192]); asking for B's lines in L2 before the previous kernel ends gave 0.1 us; unpacking by shifts and
 // masks instead of the conversion takes 5.5 us on [8192, 2048].

@@ -52,11 +52,11 @@ constexpr int kThreads = 256;
 //
 // What bounds it, on [8192, 8192] (share of a copy's rate of the bytes that have to move): to nearest the
 // memory, nearly: bf16 both views 35.5 us (86 %), rowwise 26.6 (95 %), columnwise 29.2 (86 %); fp32 55.3 (91 %),
-// 44.4 (101 %), 48.0 (94 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply pipes 58 %): bf16
-// both views 55.9 us (54 %), rowwise 33.3, columnwise 34.0; fp32 69.7 (72 %).  Ten rounds of the generator, one
-// call for 16 elements of a view, are 17 us of those 55.9 (with two rounds, for the time only, 48.0 of
-// 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 44.7 us to nearest and 61.6
-// stochastically, fp32 76.6 and 87.9: a third more loads, whose vectors hold the registers.
+// 44.4 (101 %), 48.0 (94 %).  Stochastically the instructions (74 % of the issue slots, integer and multiply
+// pipes 58 %): bf16 both views 55.9 us (54 %), rowwise 33.3, columnwise 34.0; fp32 69.7 (72 %).  Ten rounds of the
+// generator, one call for 16 elements of a view, are 17 us of those 55.9 (with two rounds, for the time only,
+// 48.0 of 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 44.7 us to nearest and
+// 61.4 stochastically, fp32 76.6 and 88.3: a third more loads, whose vectors hold the registers.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -248,7 +248,8 @@ template <typename T, bool COL, bool RAGGED>
 constexpr int kMinBlocks = sizeof(T) == 2 ? 4 : COL || RAGGED ? 2 : 3;
 
 template <typename T, bool STOCH, bool ROW, bool COL, bool RAGGED>
-__global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>)
+    mx4_tile_kernel(const __grid_constant__ TileArgs a) {
   using F = Tile<T>;
   constexpr int TW = F::THREAD_WORDS;
   extern __shared__ __align__(16) uint32_t tile[];  // COL: [128][WORDS]
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>) mx4_tile
   }
   // the atoms whole: rows, columns and blocks outside the matrix hold zeros, whose byte is 0
   if (ROW && tid < 32)
-    reinterpret_cast<uint4 *>(a.row.scales + (tm * a.row.words + tn) * 512)[tid] = reinterpret_cast<uint4 *>(atom[0])[tid];
+    reinterpret_cast<uint4 *>(a.row.scales + (tm * a.row.words + tn) * 512)[tid] =
+        reinterpret_cast<uint4 *>(atom[0])[tid];
   if (COL && tid >= 32 && tid < 64)
     reinterpret_cast<uint4 *>(a.col.scales + (tn * a.col.words + tm) * 512)[tid - 32] =
         reinterpret_cast<uint4 *>(atom[1])[tid - 32];
@@ -451,7 +453,8 @@ __global__ void __launch_bounds__(kThreads) mx4_values_kernel(const __grid_const
     const int64_t j = e < 16 ? e : tail + e - 16;
     if (e < 16 ? j >= head : j >= a.len) return;
     const uint32_t c = uint32_t(a.codes[row * a.blocks * 16 + (j >> 1)]) >> (4 * (j & 1)), m = c & 7u;
-    const uint32_t mag = (__byte_perm(0xC0800000u, 0xC0804000u, m) & 0xFFu) | (__byte_perm(0x3F3F3F00u, 0x40404040u, m) & 0xFFu) << 8;
+    const uint32_t mag = (__byte_perm(0xC0800000u, 0xC0804000u, m) & 0xFFu) |
+                         (__byte_perm(0x3F3F3F00u, 0x40404040u, m) & 0xFFu) << 8;
     const uint32_t v = mul_bf16x2(mag | (c & 8u) << 12, scale_bf16(scale_byte_at(a, row, j >> 5)));
     out[row * a.len + j] = T(low_f32(v));
     return;
@@ -573,9 +576,11 @@ gtp_status launch_views(const TileArgs &a, int64_t tiles, const gtp::DeviceInfo 
 }
 
 template <typename T>
-gtp_status launch_views(const TileArgs &a, bool stochastic, int64_t tiles, const gtp::DeviceInfo &dev, cudaStream_t st) {
+gtp_status launch_views(const TileArgs &a, bool stochastic, int64_t tiles, const gtp::DeviceInfo &dev,
+                        cudaStream_t st) {
   const bool ragged = !gtp::aligned16(a.src) || a.ld * int64_t(sizeof(T)) % 16 != 0;
-  if (stochastic) return ragged ? launch_views<T, true, true>(a, tiles, dev, st) : launch_views<T, true, false>(a, tiles, dev, st);
+  if (stochastic)
+    return ragged ? launch_views<T, true, true>(a, tiles, dev, st) : launch_views<T, true, false>(a, tiles, dev, st);
   return ragged ? launch_views<T, false, true>(a, tiles, dev, st) : launch_views<T, false, false>(a, tiles, dev, st);
 }
 

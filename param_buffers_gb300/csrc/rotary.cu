@@ -66,7 +66,8 @@ __device__ __forceinline__ void turn(uint64_t turns, int64_t pos, const RotaryAr
 }
 
 // A chunk of a head is 8 pairs: two runs of 8 elements half a rotation apart, or 16 in a row.  With
-// heads on whole vectors of 8 elements (VEC; 16 bytes, fp32 32) a chunk moves in those, else element by element, a pair a chunk.
+// heads on whole vectors of 8 elements (VEC; 16 bytes, fp32 32) a chunk moves in those, else element by
+// element, a pair a chunk.
 template <typename T>
 struct Run;
 template <>
@@ -257,7 +258,8 @@ gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStrea
   a.by_units = gtp::make_fastdiv(a.units);
   a.by_chunks = gtp::make_fastdiv(a.chunks);
   a.by_group = gtp::make_fastdiv(a.group_heads);
-  a.block_tokens = int32_t(std::max<int64_t>(1, std::min<int64_t>({Shape<T>::CHUNKS * kThreads / a.units, 16, a.tokens})));
+  a.block_tokens =
+      int32_t(std::max<int64_t>(1, std::min<int64_t>({Shape<T>::CHUNKS * kThreads / a.units, 16, a.tokens})));
   const unsigned grid = unsigned((a.tokens + a.block_tokens - 1) / a.block_tokens);
   const size_t smem = size_t(a.block_tokens) * a.half * sizeof(float2);
   return interleaved ? gtp::launch_overlapped(rotary_kernel<T, VEC, true>, grid, kThreads, smem, st, "rotary", a, turns)
@@ -270,7 +272,8 @@ gtp_status launch(RotaryArgs &a, const Turns &turns, bool interleaved, cudaStrea
   const uintptr_t mask = 8 * sizeof(T) - 1;
   bool vec = !((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst)) & mask) && a.half % 8 == 0 &&
              a.head_dim % 8 == 0;
-  for (int64_t s : {a.src_token, a.src_group, a.src_head, a.dst_token, a.dst_group, a.dst_head}) vec = vec && s % 8 == 0;
+  for (int64_t s : {a.src_token, a.src_group, a.src_head, a.dst_token, a.dst_group, a.dst_head})
+    vec = vec && s % 8 == 0;
   return vec ? launch<T, true>(a, turns, interleaved, st) : launch<T, false>(a, turns, interleaved, st);
 }
 
