@@ -56,7 +56,8 @@ constexpr int kThreads = 256;
 // pipes 58 %): bf16 both views 55.9 us (54 %), rowwise 33.3, columnwise 34.0; fp32 69.7 (72 %).  Ten rounds of the
 // generator, one call for 16 elements of a view, are 17 us of those 55.9 (with two rounds, for the time only,
 // 48.0 of 61.9 then), the rounding itself 5.  A ragged source ([8001, 8191] bf16) takes 44.7 us to nearest and
-// 61.4 stochastically, fp32 76.6 and 88.3: a third more loads, whose vectors hold the registers.
+// 61.4 stochastically, fp32 76.6 and 88.3: a third more loads, whose vectors hold the registers.  Blocks that stay
+// and copy their next tile into shared memory meanwhile have room for fewer warps: 38.4 and 66.5 us on both bf16 views.
 constexpr int kTile = 128;
 
 template <typename T>
@@ -277,13 +278,17 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>)
   if (!RAGGED && nr == 4 && nc == 16) {
 #pragma unroll
     for (int it = 0; it < 4; ++it) load(p + 32 * it * a.ld, w[it]);
+  } else if (nr == 0 || nc == 0) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int i = 0; i < TW; ++i) w[it][i] = 0;
   } else {
     int64_t off[4];  // rows past the end read the first one again
 #pragma unroll
     for (int it = 0; it < 4; ++it) off[it] = it < nr ? 32 * it * a.ld : 0;
-    const bool some = nr > 0 && nc > 0;
     // vectors where they lie inside the source, even past a row's end; the elements one by one at its corners
-    if (some && window_inside<T, RAGGED>(p, a) && window_inside<T, RAGGED>(p + 32 * (nr - 1) * a.ld, a)) {
+    if (window_inside<T, RAGGED>(p, a) && window_inside<T, RAGGED>(p + 32 * (nr - 1) * a.ld, a)) {
       if constexpr (RAGGED) {
         const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
         const bool half = (s & 2u) != 0;
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, COL, RAGGED>)
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int i = 0; i < TW; ++i) w[it][i] = some ? word_of(p + off[it] + F::PER * i, nc - F::PER * i) : 0u;
+        for (int i = 0; i < TW; ++i) w[it][i] = word_of(p + off[it] + F::PER * i, nc - F::PER * i);
     }
     if (nr < 4 || nc < 16) {
 #pragma unroll
