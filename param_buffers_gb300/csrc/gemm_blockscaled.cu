@@ -10,6 +10,7 @@
 #include "mxf4_ptx.cuh"
 #include "mxf4_rows.h"
 #include "nv_block.cuh"
+#include "smem_base.h"
 
 namespace {
 
@@ -441,7 +442,7 @@ struct BlockScaledPair {
   static constexpr int THREADS = kBsThreads + 32 * SCALE_WARPS;
   static constexpr int SMEM_EPI = kBsEpiWarps * kBsEpiBuf;
   // the dynamic shared memory is declared 1024-byte aligned; MXFP4 counts on that, since its sixth stage leaves no
-  // room for a kernel-side alignment (and gives up, with the wait flag set, where it does not hold)
+  // room for a kernel-side alignment: the host refuses the launch where it would not hold (configure_unpadded)
   static constexpr int SLACK = FMT == kMxfp4 ? 0 : 1024;
   static constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SF + SMEM_LAND + SMEM_EPI + SMEM_CTRL + SLACK;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -496,7 +497,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  if (F::SLACK == 0 && smem != smem_raw) {  // the same in every CTA: all of them leave
+  // the host has checked what this rests on; an overrun here would fault, so all CTAs would leave, the same in each
+  if (F::SLACK == 0 && smem != smem_raw) {
     if (threadIdx.x == 0) atomicOr(&g_gtp_wait_timeouts, 0x4u);
     return;
   }
@@ -1107,6 +1109,21 @@ gtp_status launch_blockscaled(const CUtensorMap &a, const CUtensorMap &b, const 
                                 FMT == kMxfp8 ? "gemm_mxfp8" : "gemm_nvfp4", a, b, d, As, Bs, a_amax, b_amax, p);
 }
 
+// configure() of a kernel without room to align its dynamic shared memory: refuses one that would not start on 1024
+// bytes, once per kernel and device.
+template <typename K>
+gtp_status configure_unpadded(K kernel, const char *what, int smem, std::atomic<uint64_t> &configured, int device) {
+  if (!(configured.load() & uint64_t(1) << (device & 63))) {
+    cudaFuncAttributes f;
+    int reserved = 0;
+    cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, device);
+    if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "%s: shared memory attributes: %s", what, cudaGetErrorString(e));
+    if (gtp_status s = gtp::check_dynamic_base(what, size_t(reserved), f.sharedSizeBytes, 1024)) return s;
+  }
+  return configure(kernel, smem, configured, device);
+}
+
 template <int FMT, int EPI, int S, bool TSF, bool TILED = false>
 gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &d,
                                    const CUtensorMap &sa, const CUtensorMap &sb, const CUtensorMap &bh, const CUtensorMap &dw,
@@ -1114,13 +1131,12 @@ gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, c
                                    const Problem &p, int grid, const gtp::DeviceInfo &dev, cudaStream_t st) {
   using F = BlockScaledPair<FMT, S, TSF, TILED>;
   constexpr auto kernel = gemm_blockscaled_pair_kernel<FMT, EPI, S, TSF, TILED>;
+  constexpr const char *what = FMT == kMxfp8 ? "gemm_mxfp8_pair" : FMT == kMxfp4 ? "gemm_mxfp4_pair" : "gemm_nvfp4_pair";
   static std::atomic<uint64_t> configured{0};
-  if (gtp_status e = configure(kernel, F::SMEM_TOTAL, configured, dev.device)) return e;
-  return gtp::launch_overlapped(kernel, grid, F::THREADS, F::SMEM_TOTAL, st,
-                                FMT == kMxfp8   ? "gemm_mxfp8_pair"
-                                : FMT == kMxfp4 ? "gemm_mxfp4_pair"
-                                                : "gemm_nvfp4_pair",
-                                a, b, d, sa, sb, bh, dw, As, Bs, a_amax, b_amax, p);
+  if (gtp_status e = F::SLACK == 0 ? configure_unpadded(kernel, what, F::SMEM_TOTAL, configured, dev.device)
+                                   : configure(kernel, F::SMEM_TOTAL, configured, dev.device))
+    return e;
+  return gtp::launch_overlapped(kernel, grid, F::THREADS, F::SMEM_TOTAL, st, what, a, b, d, sa, sb, bh, dw, As, Bs, a_amax, b_amax, p);
 }
 
 // The CTA pair unless the output has at most 128 rows (half of every pair tile would be
