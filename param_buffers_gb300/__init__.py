@@ -1056,10 +1056,14 @@ def gtp_rotary(src, dst, turns, positions=None, layout: str = "half", scale: flo
     else:  # any sequence of integers
         turns = array("Q", turns)
         at = turns.buffer_info()[0]
-    d = abi.ROTARY_DESC_PACK(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
-                             positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
-                             at, G, H, D, 2 * pairs, dt, wide, layout == "interleaved",
-                             bool(inverse), scale, 0)
+    try:
+        d = abi.ROTARY_DESC_PACK(src.data_ptr(), dst.data_ptr(), _ptr(positions), pos0, tokens_per_position,
+                                 positions_per_sequence, T, ss[0], ss[1], ss[2], ds[0], ds[1], ds[2],
+                                 at, G, H, D, 2 * pairs, dt, wide, layout == "interleaved",
+                                 bool(inverse), scale, 0)
+    except abi.struct.error:
+        raise ValueError("pos0, tokens_per_position and positions_per_sequence are 64-bit integers, scale a number; "
+                         "groups, heads, head_dim and the rotated elements fit in 32 bits") from None
     _check(lib().gtp_rotary(d, _stream(stream)), "gtp_rotary")
 
 
