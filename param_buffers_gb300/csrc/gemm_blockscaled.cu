@@ -1024,7 +1024,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
           for (int i = 0; i < 32; ++i) r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) * alpha);
       }
       constexpr int CW = (EPI == kStoreBf16) ? 32 : 16;  // columns per 64-byte staged row
-      constexpr int CHUNKS = (BN / 2) / CW;
       // MXFP4: the last tile is staged in the operand ring, which its MMAs have left and nothing refills, so that no
       // chunk waits for another's copy out.  Sums go out in rows of 128 bytes, whole lines of the output (QKV
       // wgrad 15.3 -> 14.7 us, 1111 tokens 9.4 -> 8.9); bf16 in the usual 64, which leave sooner (QKV forward
