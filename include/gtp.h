@@ -695,6 +695,11 @@ typedef enum {
   GTP_ROTARY_RAMP = 4      /* the same blend, linear in i between the pairs that make high_turns   */
                            /*   and low_turns; scale 0.1 ln(factor) + 1                            */
 } gtp_rotary_scaling;
+/* The published rules behind them: LINEAR is position interpolation (Chen et al., "Extending Context Window of Large
+ * Language Models via Positional Interpolation", 2023); BASE, BANDS and RAMP are the "NTK-aware" base, the
+ * "NTK-by-parts" blend over turns (the one that Llama 3.2's configuration scales its context by) and YaRN of Peng et al.,
+ * "YaRN: Efficient Context Window Extension of Large Language Models", 2023, sections 3.1 to 3.4, RAMP with the blend over
+ * pair indices, their rounding to whole pairs and the 0.001 between equal ends as its authors released it. */
 
 typedef struct {
   double base;           /* > 1                                                           */

@@ -11,7 +11,9 @@ import numpy as np
 
 
 def frequencies(rot_dim, base=10000.0, scaling="unscaled", factor=1.0, low_turns=1.0, high_turns=4.0, context=8192):
-    """(frequencies in radians per position, scale of the rotated values)."""
+    """(frequencies in radians per position, scale of the rotated values).  "linear": position interpolation (Chen et al.
+    2023); "base", "bands" and "ramp": the NTK-aware base, NTK-by-parts and YaRN (Peng et al. 2023), the last as its
+    authors released it."""
     i = np.arange(rot_dim // 2, dtype=np.float64)
     if scaling == "base":
         base = base * factor ** (rot_dim / (rot_dim - 2))

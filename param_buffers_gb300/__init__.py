@@ -991,8 +991,8 @@ def gtp_linear_wgrad_accum_mxfp4(dYtq, dYts, Xtq, Xts, grad_data, grad_offset: i
 
 @dataclass(frozen=True)
 class RotaryConfig:
-    """Frequencies of the rotated pairs; scaling: "unscaled", "linear", "base", "bands" or "ramp" (the
-    rules of gtp_rotary_scaling)."""
+    """Frequencies of the rotated pairs; scaling: "unscaled", "linear" (position interpolation), "base" (NTK-aware),
+    "bands" (NTK-by-parts, blended over turns) or "ramp" (YaRN): the rules of gtp_rotary_scaling."""
     rot_dim: int
     base: float = 10000.0
     scaling: str = "unscaled"

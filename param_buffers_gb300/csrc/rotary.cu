@@ -300,8 +300,9 @@ extern "C" gtp_status gtp_rotary_turns(const gtp_rotary_config *cfg, uint64_t *t
   constexpr double kTwoPi = 6.283185307179586476925286766559;
   double base = cfg->base;
   if (cfg->scaling == GTP_ROTARY_BASE) base *= std::pow(cfg->factor, double(rot) / double(rot - 2));
-  // GTP_ROTARY_RAMP blends over pair indices, between the (fractional) indices whose frequencies make
-  // high_turns and low_turns turns over the context, rounded outwards to whole pairs
+  // GTP_ROTARY_RAMP (YaRN, Peng et al. 2023) blends over pair indices, between the (fractional) indices whose
+  // frequencies make high_turns and low_turns turns over the context, rounded outwards to whole pairs; the far end is
+  // held to rot - 1 and equal ends are set 0.001 apart as its authors released it
   double first = 0, last = 0;
   if (cfg->scaling == GTP_ROTARY_RAMP) {
     const auto index = [&](double n) {
