@@ -718,8 +718,9 @@ gtp_status gtp_rotary_turns(const gtp_rotary_config *cfg, uint64_t *turns, float
 /* Heads (t, g, h), t < tokens, g < groups, h < heads, at src + t src_token + g src_group +
  * h src_head (element strides; a head's elements are contiguous), likewise dst: the packed QKV
  * product [tokens, groups, queries + key + value, head_dim] rotates its queries and keys as
- * groups x (queries + 1) heads of a group stride of queries + 2.  dst may be src exactly (in place)
- * and otherwise may not overlap it; the heads of dst may not overlap each other (GTP_E_ARG).  At most
+ * groups x (queries + 1) heads of a group stride of queries + 2.  dst may be src exactly (in place);
+ * otherwise no head of it may overlap one of src nor, where the strides differ, may what the two
+ * span; the heads of dst may not overlap each other (GTP_E_ARG).  At most
  * 2^20 heads and 2^30 elements a token (GTP_E_SHAPE). */
 typedef struct {
   const void *src;
@@ -749,7 +750,8 @@ gtp_status gtp_rotary(const gtp_rotary_desc *desc, gtp_stream stream);
  * gradient is dout.  fp32 arithmetic, one rounding.
  * x, residual and out are [rows, cols] with row strides x_ld, residual_ld, out_ld (elements, >=
  * cols), each F32 or BF16 and element-aligned; residual has out's type and may be NULL (no add).
- * out may be x or residual exactly (same start, stride and type), else it may not overlap them. */
+ * out may be x or residual exactly (same start, stride and type), else no row of it may overlap one of
+ * theirs; where the row strides differ in bytes, nor may what the arrays span. */
 gtp_status gtp_dropout_add(const void *x, gtp_dtype x_dt, int64_t x_ld, const void *residual,
                            int64_t residual_ld, void *out, gtp_dtype out_dt, int64_t out_ld,
                            int64_t rows, int64_t cols, float p, const gtp_rng *rng,

@@ -382,13 +382,15 @@ gtp_status run(const void *x, gtp_dtype x_dt, int64_t x_ld, const void *residual
       ((reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(out)) & uintptr_t(os - 1)))
     return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
   if (rows == 1) x_ld = residual_ld = out_ld = cols;
-  const gtp::ByteRange o = gtp::byte_range(out, ((rows - 1) * out_ld + cols) * os);
-  // in place is fine where every element is read and written by one thread: same start, stride, type
-  if (gtp::overlap(o, gtp::byte_range(x, ((rows - 1) * x_ld + cols) * xs)) &&
-      !(x == out && x_dt == out_dt && x_ld == out_ld))
+  const auto runs = [&](const void *p, int64_t ld, int64_t es) {
+    return gtp::Runs{reinterpret_cast<uintptr_t>(p), cols * es, {{ld * es, rows}, {0, 1}, {0, 1}}};
+  };
+  const gtp::Runs o = runs(out, out_ld, os);
+  // in place is fine where every element is read and written by one thread: same start, stride, type; no thread
+  // touches anything between the rows, so columns of one buffer may stand side by side
+  if (!(x == out && x_dt == out_dt && x_ld == out_ld) && gtp::overlap(o, runs(x, x_ld, xs)))
     return gtp::fail(GTP_E_ARG, "out overlaps the input and is not it");
-  if (residual && gtp::overlap(o, gtp::byte_range(residual, ((rows - 1) * residual_ld + cols) * os)) &&
-      !(residual == out && residual_ld == out_ld))
+  if (residual && !(residual == out && residual_ld == out_ld) && gtp::overlap(o, runs(residual, residual_ld, os)))
     return gtp::fail(GTP_E_ARG, "out overlaps the residual and is not it");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;

@@ -373,15 +373,17 @@ extern "C" gtp_status gtp_rotary(const gtp_rotary_desc *d, gtp_stream stream) {
     span += (m.n - 1) * m.stride;
   }
   if (d->src_token > (int64_t(1) << 50) / d->tokens) return gtp::fail(GTP_E_SHAPE, "src spans more than 2^50 elements");
-  const int64_t src_span =
-      (d->tokens - 1) * d->src_token + (d->groups - 1) * d->src_group + (d->heads - 1) * d->src_head + d->head_dim;
-  const gtp::ByteRange in = gtp::byte_range(d->src, src_span * es), out = gtp::byte_range(d->dst, span * es);
+  const gtp::Runs in = {reinterpret_cast<uintptr_t>(d->src), d->head_dim * es,
+                        {{d->src_token * es, d->tokens}, {d->src_group * es, d->groups}, {d->src_head * es, d->heads}}};
+  const gtp::Runs out = {reinterpret_cast<uintptr_t>(d->dst), d->head_dim * es,
+                         {{d->dst_token * es, d->tokens}, {d->dst_group * es, d->groups}, {d->dst_head * es, d->heads}}};
   const bool in_place = d->src == d->dst && (d->tokens == 1 || d->src_token == d->dst_token) &&
                         (d->groups == 1 || d->src_group == d->dst_group) &&
                         (d->heads == 1 || d->src_head == d->dst_head);
-  if (!in_place && gtp::overlap(in, out))
+  if (!in_place && gtp::overlap(out, in))
     return gtp::fail(GTP_E_ARG, "src and dst overlap and are not the same heads in place");
-  if (d->positions && gtp::overlap(out, gtp::byte_range(d->positions, d->tokens * (d->positions64 ? 8 : 4))))
+  if (d->positions && gtp::overlap(gtp::byte_range(d->dst, span * es),
+                                    gtp::byte_range(d->positions, d->tokens * (d->positions64 ? 8 : 4))))
     return gtp::fail(GTP_E_ARG, "dst overlaps positions");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
