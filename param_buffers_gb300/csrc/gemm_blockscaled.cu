@@ -115,13 +115,13 @@ __device__ __forceinline__ void load_row_words(uint32_t (&w)[WORDS], const uint8
                                                int rows, int kb) {
   const uint8_t *row = sf + int64_t(r) * row_bytes;
   if (WORDS == 4) {  // 16 bytes per row and stage: one vector load (16-byte aligned rows)
-    const uint4 v = r < rows ? __ldg(reinterpret_cast<const uint4 *>(row) + kb) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 v = r < rows ? reinterpret_cast<const uint4 *>(row)[kb] : make_uint4(0u, 0u, 0u, 0u);
     w[0] = v.x;
     w[1 % WORDS] = v.y;
     w[2 % WORDS] = v.z;
     w[3 % WORDS] = v.w;
   } else {
-    w[0] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(row) + kb) : 0u;
+    w[0] = r < rows ? reinterpret_cast<const uint32_t *>(row)[kb] : 0u;
   }
 }
 
@@ -154,9 +154,9 @@ __device__ __forceinline__ void store_scales(const ScaleRegs<WORDS> &R, uint32_t
 template <int FMT, int EPI, int S>
 __global__ void __launch_bounds__(kBsThreads, 1)
     gemm_blockscaled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                            const __grid_constant__ CUtensorMap tmD, const uint8_t *__restrict__ sfa_g,
-                            const uint8_t *__restrict__ sfb_g, const float *__restrict__ a_amax,
-                            const float *__restrict__ b_amax, const Problem p) {
+                            const __grid_constant__ CUtensorMap tmD, const uint8_t *sfa_g,
+                            const uint8_t *sfb_g, const float *a_amax,
+                            const float *b_amax, const Problem p) {
   using F = BlockScaled<FMT, S>;
   constexpr int STAGES = F::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     // NVFP4: the MMA applied the block scales; the per-tensor ones leave as 1 / (S_A S_B)
     float alpha = 1.f;
     if (FMT == kNvfp4)
-      alpha = float(1.0 / (double(gtp::nv::tensor_scale(__ldg(a_amax))) * double(gtp::nv::tensor_scale(__ldg(b_amax)))));
+      alpha = float(1.0 / (double(gtp::nv::tensor_scale(*a_amax)) * double(gtp::nv::tensor_scale(*b_amax))));
     for (int u = blockIdx.x; u < p.num_units; u += gridDim.x) {
       int tm, tn, kb0, kb1;
       decode_unit(p, u, tm, tn, kb0, kb1);
@@ -472,9 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
                                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSA,
                                  const __grid_constant__ CUtensorMap tmSB,
                                  const __grid_constant__ CUtensorMap tmBh,
-                                 const __grid_constant__ CUtensorMap tmDw, const uint8_t *__restrict__ sfa_g,
-                                 const uint8_t *__restrict__ sfb_g, const float *__restrict__ a_amax,
-                                 const float *__restrict__ b_amax, const Problem p) {
+                                 const __grid_constant__ CUtensorMap tmDw, const uint8_t *sfa_g,
+                                 const uint8_t *sfb_g, const float *a_amax,
+                                 const float *b_amax, const Problem p) {
   using F = BlockScaledPair<FMT, S, TSF, TILED>;
   constexpr int STAGES = F::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -992,7 +992,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockScaledPair<FMT,
     const uint64_t pol_out = l2_policy(1);
     float alpha = 1.f;
     if (FMT == kNvfp4)
-      alpha = float(1.0 / (double(gtp::nv::tensor_scale(__ldg(a_amax))) * double(gtp::nv::tensor_scale(__ldg(b_amax)))));
+      alpha = float(1.0 / (double(gtp::nv::tensor_scale(*a_amax)) * double(gtp::nv::tensor_scale(*b_amax))));
     for (int u = pair_id; u < p.num_units; u += npairs) {
       int tm, tn, kb0, kb1, part;
       decode_bs_unit<FMT>(p, u, tm, tn, kb0, kb1, part);

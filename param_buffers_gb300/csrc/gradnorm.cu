@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t block_sum_u32(uint32_t v, uint32_t *red) {
   return s;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_partials_kernel(const float *__restrict__ grad,
+__global__ void __launch_bounds__(kThreads) grad_norm_partials_kernel(const float *grad,
                                                                       Partial *__restrict__ partials,
                                                                       const __grid_constant__ NormTable t) {
   __shared__ double red_d[kThreads / 32];
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_partials_kernel(const floa
 }
 
 __global__ void __launch_bounds__(kFinThreads) grad_norm_finalize_kernel(
-    const Partial *__restrict__ partials, double *__restrict__ sumsq, uint32_t *__restrict__ nonfinite,
+    const Partial *partials, double *__restrict__ sumsq, uint32_t *__restrict__ nonfinite,
     float *__restrict__ total_norm, float *__restrict__ clip_coef, float max_norm, const __grid_constant__ NormTable t) {
   __shared__ double red_d[kFinThreads / 32];
   __shared__ uint32_t red_u[kFinThreads / 32];

@@ -64,7 +64,7 @@ __device__ __forceinline__ int64_t scale_index_rc(int64_t r, int64_t j, int64_t 
 // its codes, and the block's scale byte from the first of the block's four lanes.  The
 // four lanes of a block (lanes 4 k .. 4 k + 3) must take part together.
 template <typename T>
-__device__ __forceinline__ void row_vec(const T *__restrict__ src, int64_t v, uint8_t *__restrict__ q,
+__device__ __forceinline__ void row_vec(const T *src, int64_t v, uint8_t *__restrict__ q,
                                         uint8_t *__restrict__ scale, int64_t C, int64_t words, int lane) {
   const unsigned group = 0xFu << (lane & ~3);   // the 4 lanes that share a 32-element block
   float x[8];
@@ -92,7 +92,7 @@ __device__ __forceinline__ void row_vec(const T *__restrict__ src, int64_t v, ui
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const T *__restrict__ src, int64_t nvec,
+__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const T *src, int64_t nvec,
                                                                uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
                                                                int64_t C, int64_t words) {
   gtp::ptx::allow_dependents();
@@ -172,7 +172,7 @@ __device__ __forceinline__ void loadv<__nv_bfloat16, 2>(const __nv_bfloat16 *src
 }
 
 template <typename T, int V, int S>
-__global__ void __launch_bounds__(kColThreads) mx_quantize_col_kernel(const T *__restrict__ src, int64_t rows,
+__global__ void __launch_bounds__(kColThreads) mx_quantize_col_kernel(const T *src, int64_t rows,
                                                                       int64_t cols, uint8_t *__restrict__ qt,
                                                                       uint8_t *__restrict__ st, int pack,
                                                                       int64_t words) {
@@ -410,7 +410,7 @@ __device__ __forceinline__ void col_unit(const uint4 (&w)[8], uint8_t *__restric
 }
 
 template <typename T>
-__device__ __forceinline__ void col_load(const T *__restrict__ src, int64_t cols, int64_t c, int64_t r0, bool live,
+__device__ __forceinline__ void col_load(const T *src, int64_t cols, int64_t c, int64_t r0, bool live,
                                          int g, uint4 (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -442,7 +442,7 @@ struct ColArgs {
 template <typename T, int S>
 __device__ __forceinline__ void col_tile_block(const ColItem &it, int bx, int by) {
   constexpr int VE = ColTile<T>::VE, NQ = VE / 4;
-  const T *__restrict__ src = static_cast<const T *>(it.src);
+  const T *src = static_cast<const T *>(it.src);
   const int64_t rows = it.rows, cols = it.cols;
   const int lane = threadIdx.x & 31, g = lane >> 3, q = lane & 7;
   const int64_t c = (int64_t(bx) * (kColTileThreads / 32) + (threadIdx.x >> 5)) * (8 * VE) + VE * q;

@@ -44,7 +44,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *src, int64_t v, float
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) nv_amax_kernel(const T *__restrict__ src, int64_t nvec,
+__global__ void __launch_bounds__(kThreads) nv_amax_kernel(const T *src, int64_t nvec,
                                                            unsigned int *__restrict__ amax_bits) {
   __shared__ float red[kThreads / 32];
   gtp::ptx::allow_dependents();
@@ -78,14 +78,14 @@ __device__ __forceinline__ int64_t scale_index(int64_t b, int64_t C, int64_t wor
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) nv_quantize_kernel(const T *__restrict__ src, int64_t nvec,
-                                                               const float *__restrict__ amax,
+__global__ void __launch_bounds__(kThreads) nv_quantize_kernel(const T *src, int64_t nvec,
+                                                               const float *amax,
                                                                uint8_t *__restrict__ packed,
                                                                uint8_t *__restrict__ scale, int64_t C,
                                                                int64_t words) {
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  const float S = gtp::nv::tensor_scale(__ldg(amax));
+  const float S = gtp::nv::tensor_scale(*amax);
   const int lane = threadIdx.x & 31;
   const unsigned pair = 0x3u << (lane & ~1);  // the 2 lanes that share a 16-element block
   const int64_t stride = int64_t(gridDim.x) * blockDim.x;

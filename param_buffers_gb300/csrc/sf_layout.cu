@@ -26,7 +26,7 @@ constexpr int kThreads = 256;
 
 // One thread per 32-bit word of the tiled array; consecutive threads write consecutive
 // words, and the 4 bytes of a word come from one row.
-__global__ void __launch_bounds__(kThreads) sf_tile_kernel(const uint8_t *__restrict__ sf, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(kThreads) sf_tile_kernel(const uint8_t *sf, int64_t rows, int64_t cols,
                                                            int64_t words, int64_t total, uint32_t *__restrict__ out) {
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();

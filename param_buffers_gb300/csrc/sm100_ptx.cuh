@@ -29,6 +29,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // blocks the calling thread until that kernel has completed and its memory is visible, so
 // stream order holds for every access made after it; allow_dependents() lets the next
 // kernel start launching (it still waits for this one before touching memory).
+// What an earlier kernel may have written is read after the wait by ordinary loads: the read-only path (__ldg, and what the
+// compiler makes of a `const T *__restrict__` parameter) is for data that nobody writes while the kernel lives, and this
+// one lives before its predecessor has ended.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

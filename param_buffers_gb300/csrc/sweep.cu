@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) adam_flat_kernel(
   allow_dependents();
   wait_prior_grid();
   const bool clip = s.grad_scale != nullptr;
-  const float cs = clip ? __ldg(s.grad_scale) : 1.f;
+  const float cs = clip ? *s.grad_scale : 1.f;
   const int64_t nvec = numel >> 2;
   const int64_t stride = int64_t(gridDim.x) * blockDim.x;
   const int64_t tid = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) adam_flat_mx_kernel(
   allow_dependents();
   wait_prior_grid();
   const bool clip = s.grad_scale != nullptr;
-  const float cs = clip ? __ldg(s.grad_scale) : 1.f;
+  const float cs = clip ? *s.grad_scale : 1.f;
   const int lane = threadIdx.x & 31;
   const int64_t nvec = numel >> 2;
   const int64_t stride = int64_t(gridDim.x) * blockDim.x;
