@@ -1,5 +1,5 @@
-// Division by a number fixed on the host, in the elementwise kernels that split an index once per item (the
-// GEMMs have their own in gemm_common.cuh).
+// Division by a number fixed on the host: the GEMMs' unit decode, and the elementwise kernels that split an index
+// once per item.
 #pragma once
 #include <cstdint>
 

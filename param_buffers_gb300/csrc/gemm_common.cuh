@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "device.h"
+#include "fastdiv.cuh"
 #include "sm100_ptx.cuh"
 #include "tensor_map.h"
 
@@ -51,25 +52,11 @@ enum { kStoreBf16 = 0, kReduceAddF32 = 1, kReduceAddF32Direct = 2, kAccumBf16 = 
 
 __host__ __device__ constexpr bool epi_by_tma(int epi) { return epi == kStoreBf16 || epi == kReduceAddF32; }
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1 as one multiply and a shift (the round-up
-// method of Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994): with l = ceil(log2 d) and m = ceil(2^(31+l) / d) < 2^32,
-// floor(n / d) = (n m) >> (31 + l).  The unit decode below runs once per tile in every
-// warp role; with hardware division (two of them 64-bit) it cost about 1000 cycles.
-struct FastDiv {
-  uint32_t m, s;
-};
-
-inline FastDiv make_fastdiv(int d) {
-  uint32_t l = 0;
-  while ((uint64_t(1) << l) < uint64_t(d)) ++l;
-  const uint64_t num = uint64_t(1) << (31 + l);
-  return {uint32_t((num + uint64_t(d) - 1) / uint64_t(d)), 31 + l};
-}
-
-__device__ __forceinline__ int fast_div(int n, FastDiv f) {
-  return int((uint64_t(uint32_t(n)) * f.m) >> f.s);
-}
+// The unit decode below runs once per tile in every warp role; with hardware division (two of them 64-bit) it cost
+// about 1000 cycles.
+using gtp::FastDiv;
+using gtp::fast_div;
+using gtp::make_fastdiv;
 
 struct Problem {
   int32_t m_dim, n_dim, k_dim;  // D rows, D columns, contraction length
@@ -78,7 +65,7 @@ struct Problem {
   // (which may hold fewer tile rows) and its height, and the divisions the decode needs
   int32_t per_group, last_group, gm_last;
   FastDiv f_splits, f_per_group, f_gm, f_gm_last;
-  // half-width tail (CTA-pair bf16 GEMM only): units from tail_first on are the 128-column
+  // half-width tail (the CTA-pair bf16 GEMM and the MXFP4 products): units from tail_first on are the 128-column
   // halves of tiles tail_first, tail_first + 1, ... (two units a tile)
   int32_t tail_first, tail_half;
   // L2 cache policy of the A and B operand loads (CTA-pair bf16 GEMM): 0 normal,
