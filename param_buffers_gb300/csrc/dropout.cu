@@ -376,6 +376,8 @@ gtp_status run(const void *x, gtp_dtype x_dt, int64_t x_ld, const void *residual
     return gtp::fail(GTP_E_ARG, "a row stride below cols");
   if (x_ld > max_ld || out_ld > max_ld || residual_ld > max_ld) return gtp::fail(GTP_E_SHAPE, "a row stride above 2^40");
   if (rows == 0 || cols == 0) return GTP_OK;
+  if (rows > 1 && std::max({x_ld, out_ld, residual ? residual_ld : 0}) > (int64_t(1) << 50) / rows)
+    return gtp::fail(GTP_E_SHAPE, "an array spans more than 2^50 elements");
   if (!x || !out) return gtp::fail(GTP_E_ARG, "null pointer");
   const int64_t xs = x_dt == GTP_F32 ? 4 : 2, os = out_dt == GTP_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(x) & uintptr_t(xs - 1)) ||

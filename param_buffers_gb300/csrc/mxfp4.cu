@@ -619,6 +619,7 @@ extern "C" gtp_status gtp_mxfp4_quantize(const void *src, gtp_dtype src_dt, int6
   if (rows == 0 || cols == 0) return GTP_OK;
   if (!row_codes && !col_codes) return gtp::fail(GTP_E_ARG, "no view to write");
   if (!src) return gtp::fail(GTP_E_ARG, "null src");
+  if (rows > 1 && src_ld > (int64_t(1) << 50) / rows) return gtp::fail(GTP_E_SHAPE, "src spans more than 2^50 elements");
   const int64_t es = src_dt == GTP_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(src) & uintptr_t(es - 1))
     return gtp::fail(GTP_E_ALIGN, "src must be aligned to its elements");
