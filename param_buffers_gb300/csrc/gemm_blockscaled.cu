@@ -46,8 +46,8 @@ __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap *map, const 
                : "memory");
 }
 
-// The block-scaled kernel keeps one accumulator (the scale columns take the rest of tensor
-// memory), so its epilogue runs 8 warps, two per 32-lane quarter, each holding half of its
+// The block-scaled kernel keeps one accumulator (a second of 256 columns does not fit beside the scale
+// columns in tensor memory), so its epilogue runs 8 warps, two per 32-lane quarter, each holding half of its
 // rows' 256 columns in registers: the accumulator is released as soon as it has been read,
 // and the conversion and stores of one tile overlap the main loop of the next.
 constexpr int kBsEpiWarps = 8;

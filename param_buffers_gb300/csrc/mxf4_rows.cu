@@ -13,11 +13,12 @@
 // blocks' powers of two and added up, lanes and warps in a fixed order.
 //
 // Measured, one token (two, four; the tensor-core kernel, whose time hardly depends on them), B of
-//   [8192, 2048]    4.5 us  (6.5,  8.2;  8.1)      [8192, 4096]    6.6  ( 8.9, 13.5; 10.6 - 12.4)
-//   [2048, 8192]    4.5     (6.6,  8.3; 13.1)      [4096, 16384]  10.1  (13.6, 21.8; 22 - 28)
-//   [2048, 4096]    3.9     (4.3,  4.8;  8.8)      [28672, 8192]  31.4  (44.3, 76.8; 38 - 41)
-//   [1536, 2048]    2.7     (3.4,  4.3;  6.2)      [8192, 28672]  27.5  (38.4, 67.0; 55 - 58)
-//   [2048, 1024]    2.5     (3.0,  3.6;  5.1)      [128256, 2048] 35.2  (49.7, 86.2; 36)
+//   [8192, 2048]    4.6 us  (6.6,  7.9;  7.2 - 7.5)   [8192, 4096]    6.8  (10.1, 13.4;  9.7 - 11.7)
+//   [2048, 8192]    4.5     (6.6,  7.9; 12.3)         [4096, 16384]  10.0  (14.5, 21.5; 21 - 24)
+//   [2048, 4096]    4.0     (4.8,  4.8;  8.1)         [28672, 8192]  31.3  (48.3, 77;   37 - 39)
+//   [1536, 2048]    2.8     (3.8,  4.3;  5.4)         [8192, 28672]  27.5  (39.8, 65.6; 52 - 57)
+//   [2048, 1024]    2.5     (3.1,  3.7;  4.4)         [64128, 2048]  19.0  (28.5, 44.7; 21 - 23)
+//                                                     [128256, 2048] 35.1  (52.9, 87;   35)
 // About 2.5 us of each is launch, first loads and the way out.  On large matrices it runs at 3.9 - 4.6 TB/s of the
 // copy's 6.8: blocks come and go, and while one multiplies and adds up its sums it loads nothing.  A persistent form
 // with a ring of asynchronous copies 100 KB an SM deep is bound by instructions instead (73 % of the issue
