@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Arrays that lie differently: a thread a group, element by element.
+// Arrays that lie differently: a thread a group, element by element.  [8192, 2048] bf16 42.3 us (23 % of a copy's rate),
+// fp32 66.7 (30 %): neighbouring threads' elements are 16 or 32 bytes apart, eight accesses for each vector of the others.
 template <typename TI, typename TO, bool RES>
 __global__ void __launch_bounds__(kThreads)
     dropout_elements_kernel(const __grid_constant__ DropArgs a, const __grid_constant__ Shifted s) {

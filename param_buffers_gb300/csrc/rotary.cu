@@ -175,7 +175,8 @@ struct Chunk {
 //
 // The bytes bound it: 6.8 TB/s on both of these (49.3 and 97.7 us since rows of 32 bytes), the rate of a copy.
 // 8192 tokens of 20 heads of 64 (the packed QKV product of a microbatch) take 9.1 us, 4.6 TB/s: the ramp and the
-// drain of one wave.  Blocks that stay and load ahead of the sines were slower there.
+// drain of one wave.  Blocks that stay and load ahead of the sines were slower there.  Heads off whole vectors (8192
+// tokens of 20 heads of 65, 64 turned), element by element, take 30.5 us in bf16 (21 % of a copy's rate) and 32.4 in fp32 (39 %).
 template <typename T>
 struct Shape {
   static constexpr int CHUNKS = sizeof(T) == 2 ? 2 : 1;
