@@ -1135,7 +1135,8 @@ gtp_status launch_blockscaled_pair(const CUtensorMap &a, const CUtensorMap &b, c
   if (gtp_status e = F::SLACK == 0 ? configure_unpadded(kernel, what, F::SMEM_TOTAL, configured, dev.device)
                                    : configure(kernel, F::SMEM_TOTAL, configured, dev.device))
     return e;
-  return gtp::launch_overlapped(kernel, grid, F::THREADS, F::SMEM_TOTAL, st, what, a, b, d, sa, sb, bh, dw, As, Bs, a_amax, b_amax, p);
+  return gtp::launch_overlapped(kernel, grid, F::THREADS, F::SMEM_TOTAL, st, what, a, b, d, sa, sb, bh, dw, As, Bs, a_amax,
+                                b_amax, p);
 }
 
 // The CTA pair unless the output has at most 128 rows (half of every pair tile would be
