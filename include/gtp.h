@@ -760,6 +760,137 @@ gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld
                             gtp_dtype dx_dt, int64_t dx_ld, int64_t rows, int64_t cols, float p,
                             const gtp_rng *rng, gtp_stream stream);
 
+/* ------------------------------------------------------------------------ token embedding
+ * The embedding before the first layer, of one vocabulary shard ([MLM] §1; [BUF] §4.2 its bucket):
+ *   out[t] = scale * table[ids[t] - first_row]  where that row is in [0, rows), else 0 (another shard's
+ *   token, or none's: any id is allowed),  one rounding to out's type;
+ *   grad_data[grad_offset : +rows*cols].view(rows, cols)[ids[t] - first_row] += scale * dout[t].
+ * A row's tokens are sorted and summed in fp32 in an order that depends on the ids alone, and added to the
+ * buffer (F32 or BF16, any view offset) in one rounding: equal calls give equal bits.  Rows without a token
+ * are neither read nor written.
+ * ids: device [tokens], int32 (ids64 = 0) or int64, aligned to their size.  table [rows, cols], out and dout
+ * [tokens, cols]: F32 or BF16, row strides table_ld, out_ld, dout_ld (elements, >= cols), element-aligned.
+ * No output overlaps an input (GTP_E_ARG).  workspace: device, 16-byte aligned, at least
+ * gtp_embedding_grad_workspace_bytes (-1 for sizes that the call refuses; GTP_E_CAPACITY where it is
+ * smaller); its contents are not needed afterwards, and calls that may overlap on the GPU need one each.
+ * Sizes up to 2^30 a dimension and 2^40 elements (GTP_E_SHAPE). */
+gtp_status gtp_embedding(const void *ids, int32_t ids64, int64_t tokens, const void *table,
+                         gtp_dtype table_dt, int64_t table_ld, int64_t first_row, int64_t rows,
+                         int64_t cols, float scale, void *out, gtp_dtype out_dt, int64_t out_ld,
+                         gtp_stream stream);
+int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
+gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, int64_t tokens, const void *dout,
+                                    gtp_dtype dout_dt, int64_t dout_ld, int64_t first_row,
+                                    int64_t rows, int64_t cols, float scale, void *grad_data,
+                                    gtp_dtype grad_dt, int64_t grad_offset, int64_t grad_numel_total,
+                                    void *workspace, int64_t workspace_bytes, gtp_stream stream);
+
+/* ------------------------------------------------------------------------ root-mean-square norm
+ * The norm before the attention block and before the MLP, on the residual stream ([MLM] §1):
+ *   sum = x + residual, rounded to the residual's type (without a residual sum is x);
+ *   rstd = 1 / sqrt(mean over the row of sum^2 + eps);   y = (sum * rstd) * weight.
+ * y is written as F32 or BF16 and / or as its MXFP8 views, quantized from the fp32 y in one rounding by the
+ * rule of gtp_mxfp8_quantize_rowwise: row_codes [rows, cols] with row_scales [rows, cols / 32], and the
+ * columnwise view col_codes [cols, rows] with col_scales [cols, rows / 32]; tiled_scales = 1: both scale
+ * arrays in gtp_sf_tile's order (padding bytes not written).  One read of x and residual serves all outputs.
+ * Equal calls give equal bits; a call that asks for other outputs may sum a row's squares in another order.
+ * Outputs that are NULL are not written; residual and sum are given together, a view's two arrays as well,
+ * and with a columnwise view rstd too.  sum may be x or residual exactly (same start, stride and type), y may
+ * be x exactly (but not with a columnwise view and no residual); otherwise no output overlaps an input or
+ * another output (GTP_E_ARG).  Row strides in elements, >= cols; arrays element-aligned; with a view, the
+ * rows of every matrix, the weight and the codes on 16 bytes (GTP_E_ALIGN), cols % 32 == 0 and, columnwise,
+ * rows % 32 == 0 and rows <= 32 * 65535 (GTP_E_SHAPE).  cols <= 16384, rows <= 2^30 (GTP_E_SHAPE). */
+typedef struct {
+  const void *x;            /* [rows, cols]                                                     */
+  const void *residual;     /* [rows, cols] or NULL                                             */
+  const void *weight;       /* [cols]                                                           */
+  void *sum;                /* [rows, cols], the residual's type; NULL without one              */
+  void *y;                  /* [rows, cols] or NULL                                             */
+  float *rstd;              /* [rows] or NULL                                                   */
+  uint8_t *row_codes, *row_scales, *col_codes, *col_scales;
+  int64_t rows, cols, x_ld, residual_ld, sum_ld, y_ld;
+  float eps;                /* >= 0                                                             */
+  int32_t x_dtype, residual_dtype, weight_dtype, y_dtype; /* GTP_F32 or GTP_BF16                */
+  int32_t tiled_scales;     /* 0 or 1                                                           */
+  int32_t reserved;         /* 0                                                                */
+} gtp_rmsnorm_desc;
+
+gtp_status gtp_rmsnorm(const gtp_rmsnorm_desc *desc, gtp_stream stream);
+
+/* Its gradient.  With n = sum * rstd and g = dy * weight:
+ *   dx = rstd (g - n mean(g n)) + dsum,   the gradient of x and of residual alike, in sum's type; dsum, the
+ *        gradient that reaches sum past the norm, may be NULL;
+ *   grad_data[grad_offset : +cols] += sum over rows of dy * n   (F32 or BF16 buffer, one rounding a call).
+ * sum and rstd are the forward's.  fp32 sums in a fixed order: equal calls give equal bits.  dx may be dy, sum
+ * or dsum exactly; otherwise no output overlaps an input.  workspace as gtp_embedding_grad_accum's. */
+typedef struct {
+  const void *dy, *sum, *weight, *dsum;
+  const float *rstd;
+  void *dx;
+  void *grad_data;
+  int64_t rows, cols, dy_ld, sum_ld, dsum_ld, dx_ld, grad_offset, grad_numel_total;
+  int32_t dy_dtype, sum_dtype, weight_dtype, grad_dtype; /* dsum and dx have sum's type */
+  int64_t reserved; /* 0 */
+} gtp_rmsnorm_grad_desc;
+
+int64_t gtp_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+gtp_status gtp_rmsnorm_grad(const gtp_rmsnorm_grad_desc *desc, void *workspace,
+                            int64_t workspace_bytes, gtp_stream stream);
+
+/* The values of an MXFP8 view, out[rows, cols] (F32 or BF16, contiguous, element-aligned): codes times scales,
+ * exact where the type holds them; a block of scale 0xFF reads as NaN.  e4m3: 16-byte aligned; tiled_scales
+ * as above; cols % 32 == 0. */
+gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_t tiled_scales,
+                                int64_t rows, int64_t cols, void *out, gtp_dtype out_dt,
+                                gtp_stream stream);
+
+/* ------------------------------------------------------------------------ orthogonalised update
+ * The update of parameters that a layer-wise optimizer manages (gtp_param_desc.is_layer_wise; [BUF] §3): the
+ * matrix of a weight's momentum is replaced by the nearest semi-orthogonal one, by Newton-Schulz iterations
+ * (Jordan et al., "Muon: an optimizer for hidden layers in neural networks", 2024):
+ *   X = G / |G|_F (0 for a matrix of zeros);   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X,
+ * (a, b, c) = coefficients[0..2], with the smaller Gram matrix (X^T X on the other side for rows > cols).
+ * fp16 tensor-core products with fp32 accumulation, the diagonals of A and of b A + c A^2 in fp32 and the X of the
+ * linear term in 22 bits: relative error 3e-4 to 1.5e-3 before the result's own rounding.  The sum of squares is taken in fp32 by
+ * fours and in fp64 across: where it is not finite, the result is NaN.  A fixed order: equal calls give equal
+ * bits.
+ * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane
+ * (elements), element-aligned; dst likewise, and may be src or overlap it (src is read before dst is
+ * written).  1 <= steps <= 16; coefficients (host) that let a singular value of [0, 1] grow past 2 are
+ * refused (GTP_E_ARG).  count <= 64 (GTP_E_CAPACITY), rows and cols <= 65536, rows * cols < 2^31
+ * (GTP_E_SHAPE).  workspace: device, 256-byte aligned, gtp_orthogonalize_workspace_bytes(count, rows, cols)
+ * bytes (-1 for sizes that the call refuses), apart from src and dst; its contents are not needed afterwards,
+ * and calls that may overlap on the GPU need one each. */
+int64_t gtp_orthogonalize_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
+gtp_status gtp_orthogonalize(const void *src, gtp_dtype src_dt, int64_t src_ld, int64_t src_plane,
+                             void *dst, gtp_dtype dst_dt, int64_t dst_ld, int64_t dst_plane,
+                             int64_t count, int64_t rows, int64_t cols, const float *coefficients,
+                             int32_t steps, void *workspace, int64_t workspace_bytes,
+                             gtp_stream stream);
+
+typedef struct {
+  float lr, momentum, weight_decay;  /* lr, weight_decay >= 0; 0 <= momentum < 1                    */
+  float scale;                       /* of the update, say 0.2 sqrt(max(rows, cols))                */
+  float grad_factor;                 /* host factor of the gradient (a bucket's scaling)            */
+  float coefficients[3];
+  int32_t steps;
+  int32_t nesterov, zero_grad_after; /* 0 or 1                                                      */
+  int32_t reserved;                  /* 0                                                           */
+  const float *grad_scale;           /* device pointer to one float (the clip coefficient); NULL = 1 */
+} gtp_muon_hparams;
+
+/* One step of `count` weights of the same [rows, cols], the views [offsets[k], offsets[k] + rows*cols) of flat
+ * buffers of numel elements each (offsets: host; any, but views apart: GTP_E_RANGE):
+ *   g = grad * grad_factor * *grad_scale;   m <- mu m + (1 - mu) g;
+ *   u = nesterov ? mu m + (1 - mu) g : m;   O = the orthogonalised u;
+ *   p <- p (1 - lr wd) - lr scale O;   param = bf16_rne(p);   grad = 0 if zero_grad_after.
+ * grad_data: F32 or BF16; momentum (m) and master (p): fp32; param_data: bf16 or NULL.  No two of the arrays
+ * and the workspace share a byte (GTP_E_ARG).  The workspace and the limits are gtp_orthogonalize's. */
+gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *momentum, float *master,
+                         void *param_data, int64_t numel, const int64_t *offsets, int64_t count,
+                         int64_t rows, int64_t cols, const gtp_muon_hparams *h, void *workspace,
+                         int64_t workspace_bytes, gtp_stream stream);
+
 /* ------------------------------------------------------------------ diagnostics
  * Every wait inside the tensor-core kernels has a time limit.  A wait that runs out sets
  * a bit in a per-device word and the kernel unwinds (its results are then invalid):

@@ -36,6 +36,9 @@ Modules:
   mxfp4         MXFP4 quantize (block 32, two roundings), the products (pinned)
   rotary        rotary positions and their frequencies                 (pinned)
   dropout       dropout with the residual add, and its gradient        (pinned)
+  embedding     a vocabulary shard's lookup and its gradient           (pinned)
+  rmsnorm       root-mean-square norm and its gradient                 (pinned)
+  orthogonalize Newton-Schulz products and the step on them            (pinned)
 
 Every function is pinned by a ``-m "not gpu"`` test against something other than
 itself (page-printed values under tests/golden/, closed forms, library special cases,

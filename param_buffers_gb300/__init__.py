@@ -32,6 +32,9 @@ __all__ = [
     "Rng", "gtp_mxfp4_views", "gtp_mxfp4_quantize", "gtp_mxfp4_dequantize", "gtp_linear_fprop_mxfp4",
     "gtp_linear_dgrad_mxfp4", "gtp_linear_wgrad_accum_mxfp4", "RotaryConfig", "gtp_rotary_turns", "gtp_rotary",
     "gtp_dropout_add", "gtp_dropout_grad",
+    "gtp_embedding", "gtp_embedding_grad_accum", "gtp_embedding_grad_workspace_bytes", "gtp_rmsnorm", "gtp_rmsnorm_grad",
+    "gtp_rmsnorm_grad_workspace_bytes", "gtp_mxfp8_dequantize", "MuonHparams", "gtp_orthogonalize", "gtp_muon_step",
+    "gtp_orthogonalize_workspace_bytes",
     "gtp_wait_timeouts", "gtp_selftest_wait_timeout",
 ]
 
@@ -1096,3 +1099,270 @@ def gtp_dropout_grad(dout, dx, p: float, rng, stream=None) -> None:
     _check(lib().gtp_dropout_grad(dout.data_ptr(), gd, gl, dx.data_ptr(), xd, xl, xs[0], xs[1], p, _rng(rng),
                                   _stream(stream)),
            "gtp_dropout_grad")
+
+
+# ----------------------------------------------------------------------------- token embedding
+
+def _ids(ids):
+    """(64-bit or not, count) of a vector of token ids."""
+    import torch
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    if len(ids.shape) != 1 or not ids.is_contiguous() or not ids.is_cuda:
+        raise ValueError("ids must be contiguous with 1 dim, on the GPU")
+    return ids.dtype == torch.int64, ids.shape[0]
+
+
+def _bytes(t, name: str) -> int:
+    """The bytes of a workspace on the GPU."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, on the GPU")
+    return t.numel() * t.element_size()
+
+
+def _grad_buffer(t) -> int:
+    dt = _float_dtype(t, "grad_data")
+    if not t.is_contiguous():
+        raise ValueError("grad_data must be contiguous")
+    return dt
+
+
+def _size(n: int, fn: str) -> int:
+    if n < 0:
+        raise ValueError(f"{fn}: sizes out of range")
+    return n
+
+
+def gtp_embedding(ids, table, out, first_row: int = 0, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[ids[t] - first_row] where that is a row of the shard's table, else 0.  ids[T] int32 or
+    int64 (any values), table[rows,C] and out[T,C] fp32 or bf16 with contiguous rows of any stride."""
+    wide, T = _ids(ids)
+    td, ts, tl = _matrix(table, "table")
+    od, os, ol = _matrix(out, "out")
+    if os != (T, ts[1]):
+        raise ValueError(f"out must be [{T}, {ts[1]}]")
+    _check(lib().gtp_embedding(ids.data_ptr(), wide, T, table.data_ptr(), td, tl, first_row, ts[0], ts[1], scale,
+                               out.data_ptr(), od, ol, _stream(stream)),
+           "gtp_embedding")
+
+
+def gtp_embedding_grad_workspace_bytes(tokens: int, rows: int, cols: int) -> int:
+    return _size(lib().gtp_embedding_grad_workspace_bytes(tokens, rows, cols), "gtp_embedding_grad_workspace_bytes")
+
+
+def gtp_embedding_grad_accum(dout, ids, grad_data, grad_offset: int, rows: int, workspace, first_row: int = 0,
+                             scale: float = 1.0, stream=None) -> None:
+    """grad_data[grad_offset : +rows*C].view(rows, C)[ids[t] - first_row] += scale * dout[t] for the shard's tokens;
+    dout[T,C] fp32 or bf16, grad_data the flat fp32 or bf16 buffer.  The same bits for the same inputs.  workspace:
+    gtp_embedding_grad_workspace_bytes(T, rows, C) bytes."""
+    wide, T = _ids(ids)
+    dd, ds, dl = _matrix(dout, "dout")
+    if ds[0] != T:
+        raise ValueError(f"dout must have {T} rows")
+    gd = _grad_buffer(grad_data)
+    _check(lib().gtp_embedding_grad_accum(ids.data_ptr(), wide, T, dout.data_ptr(), dd, dl, first_row, rows, ds[1], scale,
+                                          grad_data.data_ptr(), gd, grad_offset, grad_data.numel(), workspace.data_ptr(),
+                                          _bytes(workspace, "workspace"), _stream(stream)),
+           "gtp_embedding_grad_accum")
+
+
+# ----------------------------------------------------------------------------- root-mean-square norm
+
+def _vector(t, n: int, name: str) -> int:
+    dt = _float_dtype(t, name)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{n}]")
+    return dt
+
+
+def _rstd(t, rows: int) -> int:
+    if _float_dtype(t, "rstd") != _F32:
+        raise TypeError(f"rstd must be float32, got {t.dtype}")
+    if t.shape != (rows,) or not t.is_contiguous():
+        raise ValueError(f"rstd must be contiguous [{rows}]")
+    return t.data_ptr()
+
+
+def _mxfp8_view(view, rows: int, cols: int, name: str):
+    """(codes, scales, whether the scales are tiled) of an MXFP8 view: 2-D scales [rows, cols/32], or 1-D tiled ones."""
+    codes, scales = view
+    for t, what in ((codes, f"{name} codes"), (scales, f"{name} scales")):
+        dt = _TORCH_DTYPES.get(getattr(t, "dtype", None))
+        if (_dtype_of(t, what) if dt is None else dt) != _U8:
+            raise TypeError(f"{what} must be uint8")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous, on the GPU")
+    if codes.shape != (rows, cols):
+        raise ValueError(f"{name} codes must be [{rows}, {cols}]")
+    tiled = len(scales.shape) == 1
+    if scales.numel() != _scale_bytes(rows, cols >> 5) if tiled else scales.shape != (rows, cols >> 5):
+        raise ValueError(f"{name} scales must be [{rows}, {cols >> 5}], or "
+                         f"gtp_sf_tiled_bytes({rows}, {cols >> 5}) bytes in one dimension")
+    return codes.data_ptr(), scales.data_ptr(), tiled
+
+
+def gtp_rmsnorm(x, weight, eps: float, residual=None, sum=None, y=None, rstd=None, row=None, col=None,
+                stream=None) -> None:
+    """s = x + residual, written to sum in the residual's type (s = x without one); rstd = 1/sqrt(mean s^2 + eps) of
+    each row; y = s * rstd * weight, written to y[R,C] (fp32 or bf16) and / or as MXFP8 views: row = (codes [R,C],
+    scales), col = (codes [C,R], scales), scales [.., /32] or in one dimension tiled (gtp_sf_tile's order; both views
+    alike).  Matrices fp32 or bf16 with contiguous rows of any stride; outputs left None are not written; col needs
+    rstd."""
+    xd, xs, xl = _matrix(x, "x")
+    R, Cc = xs
+    wd = _vector(weight, Cc, "weight")
+    rp = rd = rl = sp = sl = yp = yd = yl = rc = rsc = cc = csc = tiled = 0
+    if residual is not None:
+        rd, rs, rl = _matrix(residual, "residual")
+        if sum is None:
+            raise ValueError("residual and sum are given together")
+        sd, ss, sl = _matrix(sum, "sum")
+        if rs != xs or ss != xs or sd != rd:
+            raise ValueError("residual and sum must have x's shape and one type")
+        rp, sp = residual.data_ptr(), sum.data_ptr()
+    elif sum is not None:
+        raise ValueError("residual and sum are given together")
+    if y is not None:
+        yd, ys, yl = _matrix(y, "y")
+        if ys != xs:
+            raise ValueError("y must have x's shape")
+        yp = y.data_ptr()
+    if row is not None:
+        rc, rsc, tiled = _mxfp8_view(row, R, Cc, "rowwise")
+    if col is not None:
+        cc, csc, t = _mxfp8_view(col, Cc, R, "columnwise")
+        if row is not None and t != tiled:
+            raise ValueError("both views' scales must be tiled, or neither's")
+        tiled = t
+    try:
+        d = abi.RMSNORM_DESC_PACK(x.data_ptr(), rp, weight.data_ptr(), sp, yp, 0 if rstd is None else _rstd(rstd, R), rc,
+                                  rsc, cc, csc, R, Cc, xl, rl, sl, yl, eps, xd, rd, wd, yd, tiled, 0)
+    except (abi.struct.error, OverflowError):
+        raise ValueError("eps must be a number that fits fp32") from None
+    _check(lib().gtp_rmsnorm(d, _stream(stream)), "gtp_rmsnorm")
+
+
+def gtp_rmsnorm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return _size(lib().gtp_rmsnorm_grad_workspace_bytes(rows, cols), "gtp_rmsnorm_grad_workspace_bytes")
+
+
+def gtp_rmsnorm_grad(dy, sum, rstd, weight, dx, grad_data, grad_offset: int, workspace, dsum=None, stream=None) -> None:
+    """The norm's gradient: dx (in sum's type) of x and residual alike, with dsum, the gradient that reaches sum past the
+    norm, added; grad_data[grad_offset : +C] (flat fp32 or bf16 buffer) += the weight's.  sum and rstd are the forward's
+    (sum is x where there was no residual).  dx may be dy, sum or dsum.  workspace:
+    gtp_rmsnorm_grad_workspace_bytes(R, C) bytes."""
+    yd, ys, yl = _matrix(dy, "dy")
+    R, Cc = ys
+    sd, ss, sl = _matrix(sum, "sum")
+    xd, xs, xl = _matrix(dx, "dx")
+    wd = _vector(weight, Cc, "weight")
+    rp = _rstd(rstd, R)
+    if ss != ys or xs != ys or xd != sd:
+        raise ValueError("sum and dx must have dy's shape and one type")
+    dp = dl = 0
+    if dsum is not None:
+        dd, ds, dl = _matrix(dsum, "dsum")
+        if ds != ys or dd != sd:
+            raise ValueError("dsum must have sum's shape and type")
+        dp = dsum.data_ptr()
+    gd = _grad_buffer(grad_data)
+    try:
+        d = abi.RMSNORM_GRAD_DESC_PACK(dy.data_ptr(), sum.data_ptr(), weight.data_ptr(), dp, rp, dx.data_ptr(),
+                                       grad_data.data_ptr(), R, Cc, yl, sl, dl, xl, grad_offset, grad_data.numel(), yd, sd,
+                                       wd, gd, 0)
+    except abi.struct.error:
+        raise ValueError("grad_offset must be a 64-bit integer") from None
+    _check(lib().gtp_rmsnorm_grad(d, workspace.data_ptr(), _bytes(workspace, "workspace"), _stream(stream)),
+           "gtp_rmsnorm_grad")
+
+
+def gtp_mxfp8_dequantize(codes, scales, out, stream=None) -> None:
+    """The values of an MXFP8 view, out[R,C] (fp32 or bf16, contiguous); scales [R,C/32], or in one dimension tiled."""
+    dt, (R, Cc), _ = _matrix(out, "out")
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    c, s, tiled = _mxfp8_view((codes, scales), R, Cc, "view")
+    _check(lib().gtp_mxfp8_dequantize(c, s, tiled, R, Cc, out.data_ptr(), dt, _stream(stream)), "gtp_mxfp8_dequantize")
+
+
+# ----------------------------------------------------------------------------- orthogonalised update
+
+@dataclass(frozen=True)
+class MuonHparams:
+    """The orthogonalised step's; scale multiplies the update (say 0.2 sqrt(max(rows, cols))), grad_factor the gradient
+    (a bucket's scaling)."""
+    lr: float = 3e-4
+    momentum: float = 0.95
+    weight_decay: float = 0.1
+    scale: float = 1.0
+    grad_factor: float = 1.0
+    nesterov: bool = True
+    steps: int = 5
+    coefficients: tuple = (3.4445, -4.7750, 2.0315)
+    zero_grad_after: bool = True
+
+
+def gtp_orthogonalize_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    return _size(lib().gtp_orthogonalize_workspace_bytes(count, rows, cols), "gtp_orthogonalize_workspace_bytes")
+
+
+def _planes(t, name: str):
+    """(dtype, (count, rows, cols), row stride, matrix stride) of one matrix or of a stack of them."""
+    dt = _float_dtype(t, name)
+    shape, stride = tuple(t.shape), t.stride()
+    if len(shape) == 2:
+        shape, stride = (1, *shape), (0, *stride)
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 2 or 3 dims, got {len(shape)}")
+    if stride[2] != 1 and shape[2] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return dt, shape, stride[1] if shape[1] > 1 else shape[2], stride[0] if shape[0] > 1 else 0
+
+
+def gtp_orthogonalize(src, out, workspace, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), stream=None) -> None:
+    """out = src orthogonalised by `steps` Newton-Schulz iterations X <- a X + (b A + c A^2) X, A = X X^T, from
+    X = src / |src|.  src, out: [rows,cols] or a stack [count,rows,cols], fp32 or bf16, contiguous rows of any stride; out
+    may be src.  workspace: gtp_orthogonalize_workspace_bytes(count, rows, cols) bytes, on 256 bytes."""
+    sd, ss, sl, sp = _planes(src, "src")
+    od, os, ol, op = _planes(out, "out")
+    if os != ss:
+        raise ValueError("src and out must have the same shape")
+    try:
+        abc = abi.COEFFICIENTS_PACK(*coefficients)
+    except (abi.struct.error, OverflowError):
+        raise ValueError("coefficients are three numbers") from None
+    _check(lib().gtp_orthogonalize(src.data_ptr(), sd, sl, sp, out.data_ptr(), od, ol, op, *ss, abc, steps,
+                                   workspace.data_ptr(), _bytes(workspace, "workspace"), _stream(stream)),
+           "gtp_orthogonalize")
+
+
+def gtp_muon_step(grad_data, momentum, master, param_data, offsets: Sequence[int], rows: int, cols: int, h: MuonHparams,
+                  workspace, stream=None, grad_scale=None) -> None:
+    """One orthogonalised step of the weights [rows,cols] at `offsets` of the flat buffers: grad_data (fp32 or bf16),
+    momentum and master (fp32), param_data (bf16, or None).  grad_scale: optional one-element float32 device tensor (the
+    clip coefficient).  workspace: gtp_orthogonalize_workspace_bytes(len(offsets), rows, cols) bytes, on 256 bytes."""
+    gd = _grad_buffer(grad_data)
+    n = grad_data.numel()
+    for t, name in ((momentum, "momentum"), (master, "master"), (param_data, "param_data")):
+        if t is None and name == "param_data":
+            continue
+        want = _BF16 if name == "param_data" else _F32
+        if _float_dtype(t, name) != want:
+            raise TypeError(f"{name} must be {'bfloat16' if want == _BF16 else 'float32'}, got {t.dtype}")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with {n} elements")
+    if grad_scale is not None and (_float_dtype(grad_scale, "grad_scale") != _F32 or grad_scale.numel() != 1):
+        raise TypeError("grad_scale must be a one-element float32 CUDA tensor")
+    try:
+        at = array("q", offsets)
+    except (TypeError, OverflowError):
+        raise ValueError("offsets are 64-bit integers") from None
+    try:
+        hp = abi.MUON_HPARAMS_PACK(h.lr, h.momentum, h.weight_decay, h.scale, h.grad_factor, *h.coefficients, h.steps,
+                                   bool(h.nesterov), bool(h.zero_grad_after), 0, _ptr(grad_scale))
+    except (abi.struct.error, OverflowError):
+        raise ValueError("hyper-parameters are numbers, the coefficients three of them") from None
+    _check(lib().gtp_muon_step(grad_data.data_ptr(), gd, momentum.data_ptr(), master.data_ptr(), _ptr(param_data), n,
+                               at.buffer_info()[0], len(at), rows, cols, hp, workspace.data_ptr(),
+                               _bytes(workspace, "workspace"), _stream(stream)),
+           "gtp_muon_step")

@@ -113,10 +113,43 @@ class gtp_rotary_desc(C.Structure):
 # more than the launch.
 ROTARY_DESC_PACK = struct.Struct("<3Q10qQ8ifi").pack
 
+
+class gtp_rmsnorm_desc(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("residual", C.c_void_p), ("weight", C.c_void_p), ("sum", C.c_void_p),
+                ("y", C.c_void_p), ("rstd", C.c_void_p), ("row_codes", C.c_void_p), ("row_scales", C.c_void_p),
+                ("col_codes", C.c_void_p), ("col_scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("x_ld", C.c_int64), ("residual_ld", C.c_int64), ("sum_ld", C.c_int64), ("y_ld", C.c_int64),
+                ("eps", C.c_float), ("x_dtype", C.c_int32), ("residual_dtype", C.c_int32), ("weight_dtype", C.c_int32),
+                ("y_dtype", C.c_int32), ("tiled_scales", C.c_int32), ("reserved", C.c_int32)]
+
+
+class gtp_rmsnorm_grad_desc(C.Structure):
+    _fields_ = [("dy", C.c_void_p), ("sum", C.c_void_p), ("weight", C.c_void_p), ("dsum", C.c_void_p),
+                ("rstd", C.c_void_p), ("dx", C.c_void_p), ("grad_data", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("dy_ld", C.c_int64), ("sum_ld", C.c_int64), ("dsum_ld", C.c_int64),
+                ("dx_ld", C.c_int64), ("grad_offset", C.c_int64), ("grad_numel_total", C.c_int64),
+                ("dy_dtype", C.c_int32), ("sum_dtype", C.c_int32), ("weight_dtype", C.c_int32),
+                ("grad_dtype", C.c_int32), ("reserved", C.c_int64)]
+
+
+class gtp_muon_hparams(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("scale", C.c_float),
+                ("grad_factor", C.c_float), ("coefficients", C.c_float * 3), ("steps", C.c_int32),
+                ("nesterov", C.c_int32), ("zero_grad_after", C.c_int32), ("reserved", C.c_int32),
+                ("grad_scale", C.c_void_p)]
+
+
+# Packed likewise: gtp_rmsnorm_desc (padded to 8 bytes at its end), gtp_rmsnorm_grad_desc and gtp_muon_hparams.
+RMSNORM_DESC_PACK = struct.Struct("<10Q6qf6i4x").pack
+RMSNORM_GRAD_DESC_PACK = struct.Struct("<7Q8q4iq").pack
+MUON_HPARAMS_PACK = struct.Struct("<8f4iQ").pack
+COEFFICIENTS_PACK = struct.Struct("<3f").pack
+
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
-# A gtp_rng or a gtp_rotary_desc goes by reference or packed (VP takes both).
+# A gtp_rng, gtp_rotary_desc, gtp_rmsnorm_desc, gtp_rmsnorm_grad_desc or gtp_muon_hparams goes by reference or packed
+# (VP takes both).
 # name -> (restype, argtypes); every entry point declared in include/gtp.h
 PROTOTYPES = {
     "gtp_last_error": (C.c_char_p, []),
@@ -168,6 +201,17 @@ PROTOTYPES = {
     "gtp_rotary": (I32, [VP, VP]),
     "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
     "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
+    "gtp_embedding": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, I64, C.c_float, VP, I32, I64, VP]),
+    "gtp_embedding_grad_workspace_bytes": (I64, [I64, I64, I64]),
+    "gtp_embedding_grad_accum": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, I64, C.c_float, VP, I32, I64, I64, VP, I64,
+                                       VP]),
+    "gtp_rmsnorm": (I32, [VP, VP]),
+    "gtp_rmsnorm_grad_workspace_bytes": (I64, [I64, I64]),
+    "gtp_rmsnorm_grad": (I32, [VP, VP, I64, VP]),
+    "gtp_mxfp8_dequantize": (I32, [VP, VP, I32, I64, I64, VP, I32, VP]),
+    "gtp_orthogonalize_workspace_bytes": (I64, [I64, I64, I64]),
+    "gtp_orthogonalize": (I32, [VP, I32, I64, I64, VP, I32, I64, I64, I64, I64, I64, VP, I32, VP, I64, VP]),
+    "gtp_muon_step": (I32, [VP, I32, VP, VP, VP, I64, VP, I64, I64, I64, VP, VP, I64, VP]),
     "gtp_wait_timeouts": (I32, [P(C.c_uint32), I32]),
     "gtp_selftest_wait_timeout": (I32, [I64, VP]),
     "gtp_grad_norm_workspace_bytes": (C.c_size_t, [P(gtp_bucket_desc), I32]),

@@ -1,0 +1,669 @@
+// Token embedding of a vocabulary shard, and its gradient accumulated into the flat gradient buffer by sorted tokens.
+//
+// Pages: "Megatron-LM architecture and source guide" (arganzheng.life), §1 (the embedding before the first layer) and
+// "05 · grad/param buffer ..." (llm-infra-atlas), §4.2 and §5 (the embedding's bucket, main_grad as a view).
+//
+//   out[t] = scale * table[ids[t] - first_row]  where that row is in the shard, else 0
+//   grad[r] += scale * sum of dout[t] over the tokens t of row r
+// The gradient's sum over a row's tokens is formed in fp32 in an order that depends on the ids alone: tokens are sorted
+// by row (ties in token order), the sorted list is cut into tiles of equal length, a row inside a tile is summed and
+// added at once, a row that crosses tiles leaves one partial a tile, joined in order by a second kernel.  No atomic's
+// order takes part, so equal calls give equal bits.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "byte_range.h"
+#include "device.h"
+#include "sm100_ptx.cuh"
+
+namespace gtp {
+void clear_error();
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t id_at(const void *ids, int wide, int64_t t) {
+  return wide ? static_cast<const int64_t *>(ids)[t] : int64_t(static_cast<const int32_t *>(ids)[t]);
+}
+
+// The shard's row of a token, or `rows` for one of another shard (or of none).  Unsigned: no id wraps into the range.
+__device__ __forceinline__ int64_t row_of(const void *ids, int wide, int64_t t, int64_t first_row, int64_t rows) {
+  const uint64_t r = uint64_t(id_at(ids, wide, t)) - uint64_t(first_row);
+  return r < uint64_t(rows) ? int64_t(r) : rows;
+}
+
+// Eight elements of a row that one thread moves: consecutive ones on 16 bytes (VEC), or every step-th from its own on,
+// so that a warp's accesses stay side by side whatever the row's alignment.
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int step, int n, float (&x)[8]) {
+  if (VEC) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);  // bf16 -> fp32 is exact
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k * step]) : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int step, int n, float (&x)[8]) {
+  if (VEC) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k * step] : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, int step, int n, const float (&x)[8]) {
+  if (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k * step] = __float2bfloat16_rn(x[k]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float *p, int step, int n, const float (&x)[8]) {
+  if (VEC) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k * step] = x[k];
+  }
+}
+
+// A block is tx threads wide, eight columns a thread; this thread's first column and how many of its eight exist.
+template <bool VEC>
+__device__ __forceinline__ bool columns(int64_t cols, int64_t &c, int &n) {
+  const int tx = blockDim.x;
+  const int64_t c0 = int64_t(blockIdx.x) * 8 * tx;
+  c = c0 + (VEC ? 8 * threadIdx.x : threadIdx.x);
+  if (c >= cols) return false;
+  n = VEC ? 8 : int(min(int64_t(8), (cols - c + tx - 1) / tx));
+  return true;
+}
+
+// --------------------------------------------------------------------------- lookup
+
+struct LookupArgs {
+  const void *ids, *table;
+  void *out;
+  int64_t tokens, table_ld, out_ld, first_row, rows, cols;
+  float scale;
+  int wide;
+};
+
+template <typename TI, typename TO, bool VEC>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ LookupArgs a) {
+  constexpr int N = 4;  // tokens of a thread in flight
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  int64_t c;
+  int n;
+  if (!columns<VEC>(a.cols, c, n)) return;
+  const int tx = blockDim.x;
+  const int64_t step = int64_t(gridDim.y) * blockDim.y;
+  for (int64_t t0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; t0 < a.tokens; t0 += N * step) {
+    int64_t row[N];
+    float x[N][8];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t t = t0 + i * step;
+      row[i] = t < a.tokens ? row_of(a.ids, a.wide, t, a.first_row, a.rows) : a.rows;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (row[i] < a.rows) {
+        load8<VEC>(static_cast<const TI *>(a.table) + row[i] * a.table_ld + c, tx, n, x[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t t = t0 + i * step;
+      if (t < a.tokens) {
+        if (row[i] < a.rows) {  // not the zeros of other shards' tokens: a scale of Inf or NaN leaves them 0
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] *= a.scale;
+        }
+        store8<VEC>(static_cast<TO *>(a.out) + t * a.out_ld + c, tx, n, x[i]);
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------- sorting the tokens
+
+// Sorted lists: key[p] the row, token[p] the token of sorted place p; places behind the shard's tokens hold key `rows`.
+struct SortArgs {
+  const void *ids;
+  int64_t first_row, rows;
+  int32_t tokens, wide;
+  int32_t *key, *token;  // the result
+  int32_t *key2, *token2;
+  int32_t *counts;  // radix: [256][tiles]
+  int32_t tiles;
+};
+
+// Few tokens: the place of a token is the number of tokens that sort before it, counted outright.  A block owns
+// kOwn tokens, keeps every token of the shard as one 32-bit number row * tokens + t in shared memory (any order: the
+// numbers differ), and its warps count, 32 owned tokens a warp, each over a part of the list.  tokens^2 comparisons
+// but one launch and no exchange between blocks.
+constexpr int kOwn = 64, kRankThreads = 512, kRankMost = 16384;
+
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ __align__(16) uint32_t list[];  // tokens rounded up to 4, padded with the largest number
+  __shared__ uint32_t own[kOwn], place[kOwn];
+  __shared__ int listed, owned;
+  gtp::ptx::allow_dependents();
+  if (threadIdx.x == 0) listed = owned = 0;
+  if (threadIdx.x < kOwn) place[threadIdx.x] = 0;
+  gtp::ptx::wait_prior_grid();
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = blockIdx.x * kOwn;
+  for (int t0 = 32 * warp; t0 < a.tokens; t0 += kRankThreads) {
+    const int t = t0 + lane;
+    const int64_t row = t < a.tokens ? row_of(a.ids, a.wide, t, a.first_row, a.rows) : a.rows;
+    const bool mine = row < a.rows;
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, mine);
+    int base = 0;
+    if (lane == 0 && m) base = atomicAdd(&listed, __popc(m));
+    base = __shfl_sync(0xFFFFFFFFu, base, 0);
+    if (mine) {
+      const uint32_t k = uint32_t(row) * uint32_t(a.tokens) + uint32_t(t);
+      list[base + __popc(m & ((1u << lane) - 1))] = k;
+      if (t >= first && t < first + kOwn) own[atomicAdd(&owned, 1)] = k;
+    }
+  }
+  __syncthreads();
+  const int n = listed, mine = owned;
+  if (threadIdx.x < 4 && n + threadIdx.x < ((n + 3) & ~3)) list[n + threadIdx.x] = 0xFFFFFFFFu;
+  __syncthreads();
+  const int sets = (mine + 31) >> 5;  // of 32 owned tokens
+  if (sets > 0) {
+    const int parts = (kRankThreads / 32) / sets, set = warp % sets, part = warp / sets;
+    if (part < parts) {
+      const int i = 32 * set + lane;
+      const uint32_t k = i < mine ? own[i] : 0u;
+      const int quads = (n + 3) >> 2, q0 = int(int64_t(quads) * part / parts), q1 = int(int64_t(quads) * (part + 1) / parts);
+      uint32_t before = 0;
+#pragma unroll 4
+      for (int q = q0; q < q1; ++q) {
+        const uint4 v = reinterpret_cast<const uint4 *>(list)[q];
+        before += (v.x < k) + (v.y < k) + (v.z < k) + (v.w < k);
+      }
+      if (i < mine) atomicAdd(&place[i], before);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < mine) {
+    const uint32_t k = own[threadIdx.x], p = place[threadIdx.x];
+    a.key[p] = int32_t(k / uint32_t(a.tokens));
+    a.token[p] = int32_t(k % uint32_t(a.tokens));
+  }
+  if (threadIdx.x < kOwn) {  // the places behind the shard's tokens
+    const int p = first + int(threadIdx.x);
+    if (p >= n && p < a.tokens) a.key[p] = int32_t(a.rows);
+  }
+}
+
+// Many tokens: a radix sort from the low digit up, eight bits a pass, each pass three launches: digits counted by tiles
+// of 4096 tokens, the counts summed up in (digit, tile) order, and each tile's tokens written to their places in
+// order.  The first pass reads the ids themselves.
+constexpr int kTile = 4096, kTileThreads = 256, kRounds = kTile / kTileThreads;
+
+__device__ __forceinline__ void radix_load(const SortArgs &a, const int32_t *key, const int32_t *token, int64_t p,
+                                           int32_t &k, int32_t &t) {
+  if (key) {
+    k = key[p];
+    t = token[p];
+  } else {
+    k = int32_t(row_of(a.ids, a.wide, p, a.first_row, a.rows));
+    t = int32_t(p);
+  }
+}
+
+__global__ void __launch_bounds__(kTileThreads)
+    radix_count_kernel(const __grid_constant__ SortArgs a, const int32_t *key, int shift) {
+  __shared__ int32_t count[256];
+  gtp::ptx::allow_dependents();
+  count[threadIdx.x] = 0;
+  gtp::ptx::wait_prior_grid();
+  __syncthreads();
+  for (int i = 0; i < kRounds; ++i) {
+    const int64_t p = int64_t(blockIdx.x) * kTile + i * kTileThreads + threadIdx.x;
+    if (p < a.tokens) {
+      const int32_t k = key ? key[p] : int32_t(row_of(a.ids, a.wide, p, a.first_row, a.rows));
+      atomicAdd(&count[(k >> shift) & 255], 1);
+    }
+  }
+  __syncthreads();
+  a.counts[int64_t(threadIdx.x) * a.tiles + blockIdx.x] = count[threadIdx.x];
+}
+
+// counts -> what stands before each, in place, by one block.
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) radix_scan_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int32_t sums[32];
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n = int64_t(256) * a.tiles;
+  int32_t carry = 0;
+  for (int64_t i0 = 0; i0 < n; i0 += 4 * kScanThreads) {
+    int32_t v[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = i0 + 4 * threadIdx.x + k;
+      v[k] = i < n ? a.counts[i] : 0;
+      sum += v[k];
+    }
+    int32_t run = sum;  // inclusive over the warp
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int32_t o = __shfl_up_sync(0xFFFFFFFFu, run, d);
+      if (lane >= d) run += o;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    if (warp == 0) {
+      int32_t s = sums[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += o;
+      }
+      sums[lane] = s;
+    }
+    __syncthreads();
+    int32_t before = carry + (warp ? sums[warp - 1] : 0) + run - sum;
+    carry += sums[31];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = i0 + 4 * threadIdx.x + k;
+      if (i < n) a.counts[i] = before;
+      before += v[k];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kTileThreads)
+    radix_scatter_kernel(const __grid_constant__ SortArgs a, const int32_t *key, const int32_t *token, int32_t *key_out,
+                         int32_t *token_out, int shift) {
+  __shared__ int32_t at[kTileThreads / 32][256];  // a warp's next place of each digit
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int w = 0; w < kTileThreads / 32; ++w) at[w][threadIdx.x] = 0;
+  __syncthreads();
+  // a warp takes kTile / 8 tokens in a row, 32 at a time
+  const int64_t p0 = int64_t(blockIdx.x) * kTile + warp * (kTile / (kTileThreads / 32)) + lane;
+  int32_t k[kRounds], t[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int64_t p = p0 + 32 * i;
+    k[i] = t[i] = 0;
+    if (p < a.tokens) {
+      radix_load(a, key, token, p, k[i], t[i]);
+      atomicAdd(&at[warp][(k[i] >> shift) & 255], 1);
+    }
+  }
+  __syncthreads();
+  {  // thread d: digit d's place for each warp in turn
+    int32_t before = a.counts[int64_t(threadIdx.x) * a.tiles + blockIdx.x];
+    for (int w = 0; w < kTileThreads / 32; ++w) {
+      const int32_t c = at[w][threadIdx.x];
+      at[w][threadIdx.x] = before;
+      before += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const bool live = p0 + 32 * i < a.tokens;
+    const int d = live ? (k[i] >> shift) & 255 : 256 + lane;  // no one's digit
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int32_t base = 0;
+    if (live) base = at[warp][d];
+    __syncwarp();
+    if (live && rank == 0) at[warp][d] = base + __popc(same);
+    __syncwarp();
+    if (live) {
+      key_out[base + rank] = k[i];
+      token_out[base + rank] = t[i];
+    }
+  }
+}
+
+// --------------------------------------------------------------------------- the rows' sums
+
+struct SumArgs {
+  const int32_t *key, *token;
+  const void *dout;
+  void *grad;
+  float *part;  // [tiles][2][cols]: the row that comes in from the tile before, and the one that goes on
+  int64_t dout_ld, rows, cols;
+  int32_t tokens, tile, tiles;
+  float scale;
+};
+
+// grad[row] += scale * x at this thread's eight columns: one rounding of the sum in the buffer's type.  fp32 by the
+// memory's own additions: nobody else adds to these elements in this call, so the result does not depend on their order.
+template <bool VEC>
+__device__ __forceinline__ void add8(float *p, int step, int n, float scale, const float (&x)[8]) {
+  if (VEC) {
+    atomicAdd(reinterpret_cast<float4 *>(p), make_float4(scale * x[0], scale * x[1], scale * x[2], scale * x[3]));
+    atomicAdd(reinterpret_cast<float4 *>(p) + 1, make_float4(scale * x[4], scale * x[5], scale * x[6], scale * x[7]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) atomicAdd(p + k * step, scale * x[k]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void add8(__nv_bfloat16 *p, int step, int n, float scale, const float (&x)[8]) {
+  float g[8];
+  load8<VEC>(p, step, n, g);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = fmaf(scale, x[k], g[k]);
+  store8<VEC>(p, step, n, g);
+}
+
+template <typename TD, typename TG, bool VEC>
+__global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int N = 4;  // tokens in flight
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  int64_t c;
+  int n;
+  const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y;
+  if (tile >= a.tiles || !columns<VEC>(a.cols, c, n)) return;
+  const int tx = blockDim.x, rows = int(a.rows);
+  const int p0 = tile * a.tile, p1 = min(p0 + a.tile, a.tokens);
+  int row = a.key[p0];
+  if (row >= rows) return;
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+  bool open = p0 > 0 && a.key[p0 - 1] == row;  // this row's first tokens are in the tile before
+  float *const part = a.part + int64_t(tile) * 2 * a.cols + c;
+  for (int p = p0; p < p1; p += N) {
+    float x[N][8];
+    int key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = p + i < p1 ? a.key[p + i] : rows;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] < rows) load8<VEC>(static_cast<const TD *>(a.dout) + int64_t(a.token[p + i]) * a.dout_ld + c, tx, n, x[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (key[i] < rows) {
+        if (key[i] != row) {
+          if (open) store8<false>(part, VEC ? 1 : tx, n, acc);
+          else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+          open = false;
+          row = key[i];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += x[i][k];
+      }
+    }
+  }
+  if (open) store8<false>(part, VEC ? 1 : tx, n, acc);
+  else if (p1 < a.tokens && a.key[p1] == row) store8<false>(part + a.cols, VEC ? 1 : tx, n, acc);
+  else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+}
+
+// The rows that cross tiles: the tile in which such a row begins adds up its parts.
+template <typename TG, bool VEC>
+__global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a) {
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  int64_t c;
+  int n;
+  const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y;
+  if (tile >= a.tiles || !columns<VEC>(a.cols, c, n)) return;
+  const int p0 = tile * a.tile, p1 = p0 + a.tile;
+  if (p1 >= a.tokens) return;
+  const int row = a.key[p1];
+  if (row >= a.rows || a.key[p1 - 1] != row || (p0 > 0 && a.key[p0 - 1] == row)) return;
+  const int tx = blockDim.x, step = VEC ? 1 : tx;
+  float acc[8];
+  load8<false>(a.part + (int64_t(tile) * 2 + 1) * a.cols + c, step, n, acc);
+  for (int t = tile + 1; t < a.tiles && a.key[t * a.tile] == row; ++t) {
+    float x[8];
+    load8<false>(a.part + int64_t(t) * 2 * a.cols + c, step, n, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += x[k];
+  }
+  add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+}
+
+// --------------------------------------------------------------------------- host
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+
+// Threads a block across a row's groups of eight, and rows of such threads.
+dim3 block_of(int64_t cols) {
+  int tx = 1;
+  while (tx < kThreads && 8 * tx < cols) tx *= 2;
+  return dim3(tx, kThreads / tx);
+}
+
+bool on16(const void *p, int64_t ld, int64_t es) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es & 15) == 0;
+}
+
+int64_t size_of(gtp_dtype dt) { return dt == GTP_F32 ? 4 : 2; }
+
+gtp_status check_sizes(int64_t tokens, int64_t first_row, int64_t rows, int64_t cols, int32_t ids64) {
+  if (tokens < 0 || rows < 0 || cols < 0 || first_row < 0) return gtp::fail(GTP_E_ARG, "negative size");
+  if (ids64 != 0 && ids64 != 1) return gtp::fail(GTP_E_ARG, "ids64 must be 0 or 1");
+  if (tokens > kMaxDim || rows > kMaxDim || cols > kMaxDim) return gtp::fail(GTP_E_SHAPE, "a dimension above 2^30");
+  const int64_t c = std::max<int64_t>(cols, 1);
+  if (tokens > (int64_t(1) << 40) / c || rows > (int64_t(1) << 40) / c)
+    return gtp::fail(GTP_E_SHAPE, "more than 2^40 elements");
+  return GTP_OK;
+}
+
+gtp_status check_ld(const char *name, int64_t ld, int64_t n, int64_t cols) {
+  if (n > 1 && ld < cols) return gtp::fail(GTP_E_ARG, "a row stride of %s below cols", name);
+  if (n > 1 && ld > (int64_t(1) << 50) / n) return gtp::fail(GTP_E_SHAPE, "%s spans more than 2^50 elements", name);
+  return GTP_OK;
+}
+
+gtp::ByteRange span_of(const void *p, int64_t n, int64_t ld, int64_t cols, int64_t es) {
+  return gtp::byte_range(p, n && cols ? ((n - 1) * ld + cols) * es : 0);
+}
+
+template <typename TI, typename TO>
+gtp_status launch_lookup(const LookupArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
+  const bool vec = a.cols % 8 == 0 && on16(a.table, a.table_ld, sizeof(TI)) && on16(a.out, a.out_ld, sizeof(TO));
+  const dim3 block = block_of(a.cols);
+  const int64_t gx = (a.cols + 8 * block.x - 1) / (8 * block.x);
+  const int64_t fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / gx);
+  const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>({(a.tokens + block.y - 1) / block.y, fill, 65535})));
+  return gtp::launch_overlapped(vec ? embedding_kernel<TI, TO, true> : embedding_kernel<TI, TO, false>, grid, block, 0, st,
+                                "embedding", a);
+}
+
+struct GradPlan {
+  int32_t tile, tiles, sort_tiles;
+  bool radix;
+  int64_t key, token, key2, token2, counts, part, bytes;  // places in the workspace
+};
+
+GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
+  GradPlan p = {};
+  p.radix = tokens > kRankMost || rows * tokens >= (int64_t(1) << 32) - 1;
+  // tiles: short ones spread few tokens over the machine; above 2^16 of them longer ones keep the partials few
+  p.tile = int32_t(std::max<int64_t>(16, (tokens + 65534) / 65535));
+  p.tiles = int32_t((tokens + p.tile - 1) / p.tile);
+  p.sort_tiles = int32_t((tokens + kTile - 1) / kTile);
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) & ~int64_t(255);
+    return here;
+  };
+  p.key = take(4 * tokens);
+  p.token = take(4 * tokens);
+  if (p.radix) {
+    p.key2 = take(4 * tokens);
+    p.token2 = take(4 * tokens);
+    p.counts = take(int64_t(4) * 256 * p.sort_tiles);
+  }
+  p.part = take(int64_t(8) * p.tiles * cols);
+  p.bytes = at;
+  return p;
+}
+
+gtp_status sort_tokens(SortArgs &a, const GradPlan &plan, cudaStream_t st) {
+  if (!plan.radix) {
+    const size_t smem = size_t((a.tokens + 3) & ~3) * 4;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankMost * 4);
+      if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    }
+    return gtp::launch_overlapped(rank_kernel, unsigned((a.tokens + kOwn - 1) / kOwn), kRankThreads, smem, st, "embedding_grad",
+                                  a);
+  }
+  int bits = 1;  // of the keys 0 .. rows
+  while (bits < 31 && (int64_t(1) << bits) <= a.rows) ++bits;
+  const int passes = (bits + 7) / 8;
+  const int32_t *key = nullptr, *token = nullptr;
+  for (int i = 0; i < passes; ++i) {  // the last pass writes the result
+    const bool into_first = (passes - 1 - i) % 2 == 0;
+    int32_t *key_out = into_first ? a.key : a.key2, *token_out = into_first ? a.token : a.token2;
+    gtp_status s = gtp::launch_overlapped(radix_count_kernel, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key,
+                                          8 * i);
+    if (!s) s = gtp::launch_overlapped(radix_scan_kernel, 1, kScanThreads, 0, st, "embedding_grad", a);
+    if (!s)
+      s = gtp::launch_overlapped(radix_scatter_kernel, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key, token,
+                                 key_out, token_out, 8 * i);
+    if (s) return s;
+    key = key_out, token = token_out;
+  }
+  return GTP_OK;
+}
+
+template <typename TD, typename TG>
+gtp_status launch_sums(const SumArgs &a, cudaStream_t st) {
+  const bool vec = a.cols % 8 == 0 && on16(a.dout, a.dout_ld, sizeof(TD)) && on16(a.grad, a.cols, sizeof(TG));
+  const dim3 block = block_of(a.cols);
+  const dim3 grid(unsigned((a.cols + 8 * block.x - 1) / (8 * block.x)), (a.tiles + block.y - 1) / block.y);
+  if (gtp_status s = gtp::launch_overlapped(vec ? embedding_sum_kernel<TD, TG, true> : embedding_sum_kernel<TD, TG, false>, grid,
+                                            block, 0, st, "embedding_grad", a))
+    return s;
+  if (a.tiles == 1) return GTP_OK;
+  return gtp::launch_overlapped(vec ? embedding_join_kernel<TG, true> : embedding_join_kernel<TG, false>, grid, block, 0, st,
+                                "embedding_grad", a);
+}
+
+}  // namespace
+
+extern "C" gtp_status gtp_embedding(const void *ids, int32_t ids64, int64_t tokens, const void *table, gtp_dtype table_dt,
+                                    int64_t table_ld, int64_t first_row, int64_t rows, int64_t cols, float scale, void *out,
+                                    gtp_dtype out_dt, int64_t out_ld, gtp_stream stream) {
+  gtp::clear_error();
+  if ((table_dt != GTP_F32 && table_dt != GTP_BF16) || (out_dt != GTP_F32 && out_dt != GTP_BF16))
+    return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
+  if (gtp_status s = check_sizes(tokens, first_row, rows, cols, ids64)) return s;
+  if (gtp_status s = check_ld("table", table_ld, rows, cols)) return s;
+  if (gtp_status s = check_ld("out", out_ld, tokens, cols)) return s;
+  if (tokens == 0 || cols == 0) return GTP_OK;
+  if (!ids || !out || (!table && rows)) return gtp::fail(GTP_E_ARG, "null pointer");
+  const int64_t ts = size_of(table_dt), os = size_of(out_dt), is = ids64 ? 8 : 4;
+  if ((reinterpret_cast<uintptr_t>(ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(table) & uintptr_t(ts - 1)) ||
+      (reinterpret_cast<uintptr_t>(out) & uintptr_t(os - 1)))
+    return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
+  if (rows <= 1) table_ld = cols;
+  if (tokens == 1) out_ld = cols;
+  const gtp::ByteRange o = span_of(out, tokens, out_ld, cols, os);
+  if (gtp::overlap(o, span_of(table, rows, table_ld, cols, ts)) || gtp::overlap(o, gtp::byte_range(ids, tokens * is)))
+    return gtp::fail(GTP_E_ARG, "out overlaps an input");
+  gtp::DeviceInfo dev;
+  if (gtp_status s = gtp::require_sm103(&dev)) return s;
+  const LookupArgs a = {ids, table, out, tokens, table_ld, out_ld, first_row, rows, cols, scale, ids64};
+  cudaStream_t st = gtp::as_stream(stream);
+  if (table_dt == GTP_F32)
+    return out_dt == GTP_F32 ? launch_lookup<float, float>(a, dev, st) : launch_lookup<float, __nv_bfloat16>(a, dev, st);
+  return out_dt == GTP_F32 ? launch_lookup<__nv_bfloat16, float>(a, dev, st)
+                           : launch_lookup<__nv_bfloat16, __nv_bfloat16>(a, dev, st);
+}
+
+extern "C" int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols) {
+  if (tokens < 0 || rows < 0 || cols < 0 || tokens > kMaxDim || rows > kMaxDim || cols > kMaxDim) return -1;
+  if (tokens == 0 || rows == 0 || cols == 0) return 0;
+  return grad_plan(tokens, rows, cols).bytes;
+}
+
+extern "C" gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, int64_t tokens, const void *dout,
+                                               gtp_dtype dout_dt, int64_t dout_ld, int64_t first_row, int64_t rows,
+                                               int64_t cols, float scale, void *grad_data, gtp_dtype grad_dt,
+                                               int64_t grad_offset, int64_t grad_numel_total, void *workspace,
+                                               int64_t workspace_bytes, gtp_stream stream) {
+  gtp::clear_error();
+  if ((dout_dt != GTP_F32 && dout_dt != GTP_BF16) || (grad_dt != GTP_F32 && grad_dt != GTP_BF16))
+    return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
+  if (gtp_status s = check_sizes(tokens, first_row, rows, cols, ids64)) return s;
+  if (gtp_status s = check_ld("dout", dout_ld, tokens, cols)) return s;
+  if (grad_offset < 0 || grad_numel_total < 0 || grad_numel_total > (int64_t(1) << 50) || grad_offset > grad_numel_total ||
+      rows * cols > grad_numel_total - grad_offset)
+    return gtp::fail(GTP_E_RANGE, "the view of %lld elements at %lld leaves a buffer of %lld", (long long)(rows * cols),
+                     (long long)grad_offset, (long long)grad_numel_total);
+  if (tokens == 0 || rows == 0 || cols == 0) return GTP_OK;
+  if (!ids || !dout || !grad_data || !workspace) return gtp::fail(GTP_E_ARG, "null pointer");
+  const int64_t ds = size_of(dout_dt), gs = size_of(grad_dt), is = ids64 ? 8 : 4;
+  if ((reinterpret_cast<uintptr_t>(ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(dout) & uintptr_t(ds - 1)) ||
+      (reinterpret_cast<uintptr_t>(grad_data) & uintptr_t(gs - 1)))
+    return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
+  if (!gtp::aligned16(workspace)) return gtp::fail(GTP_E_ALIGN, "workspace must be 16-byte aligned");
+  const GradPlan plan = grad_plan(tokens, rows, cols);
+  if (workspace_bytes < plan.bytes)
+    return gtp::fail(GTP_E_CAPACITY, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)plan.bytes);
+  if (tokens == 1) dout_ld = cols;
+  char *const grad = static_cast<char *>(grad_data) + grad_offset * gs, *const ws = static_cast<char *>(workspace);
+  const gtp::ByteRange g = gtp::byte_range(grad, rows * cols * gs), w = gtp::byte_range(ws, plan.bytes),
+                       d = span_of(dout, tokens, dout_ld, cols, ds), i = gtp::byte_range(ids, tokens * is);
+  if (gtp::overlap(g, d) || gtp::overlap(g, i) || gtp::overlap(w, d) || gtp::overlap(w, i) || gtp::overlap(w, g))
+    return gtp::fail(GTP_E_ARG, "the gradient view or the workspace overlaps an input or the other");
+  gtp::DeviceInfo dev;
+  if (gtp_status s = gtp::require_sm103(&dev)) return s;
+  const auto at = [&](int64_t place) { return reinterpret_cast<int32_t *>(ws + place); };
+  SortArgs sort = {ids, first_row, rows, int32_t(tokens), ids64, at(plan.key), at(plan.token), at(plan.key2),
+                   at(plan.token2), at(plan.counts), plan.sort_tiles};
+  cudaStream_t st = gtp::as_stream(stream);
+  if (gtp_status s = sort_tokens(sort, plan, st)) return s;
+  const SumArgs a = {at(plan.key), at(plan.token), dout, grad, reinterpret_cast<float *>(ws + plan.part), dout_ld, rows, cols,
+                     int32_t(tokens), plan.tile, plan.tiles, scale};
+  if (dout_dt == GTP_F32)
+    return grad_dt == GTP_F32 ? launch_sums<float, float>(a, st) : launch_sums<float, __nv_bfloat16>(a, st);
+  return grad_dt == GTP_F32 ? launch_sums<__nv_bfloat16, float>(a, st) : launch_sums<__nv_bfloat16, __nv_bfloat16>(a, st);
+}

@@ -1553,6 +1553,8 @@ extern "C" gtp_status gtp_linear_wgrad_accum_mxfp4(const uint8_t *dYtq, const ui
 }
 
 namespace gtp {
+// The word of the orthogonalised update's unit (orthogonalize.cu), read along with this one's.
+gtp_status orthogonalize_wait_word(unsigned int *v, bool reset);
 gtp_status blockscaled_wait_word(unsigned int *v, bool reset) {
   cudaError_t e = cudaMemcpyFromSymbol(v, g_gtp_wait_timeouts, sizeof(*v));
   if (e == cudaSuccess && reset) {
@@ -1560,6 +1562,9 @@ gtp_status blockscaled_wait_word(unsigned int *v, bool reset) {
     e = cudaMemcpyToSymbol(g_gtp_wait_timeouts, &z, sizeof(z));
   }
   if (e != cudaSuccess) return fail(GTP_E_CUDA, "reading the wait-timeout word: %s", cudaGetErrorString(e));
+  unsigned int o = 0;
+  if (gtp_status s = orthogonalize_wait_word(&o, reset)) return s;
+  *v |= o;
   return GTP_OK;
 }
 }  // namespace gtp
