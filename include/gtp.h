@@ -851,7 +851,7 @@ gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_
  *   X = G / |G|_F (0 for a matrix of zeros);   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X,
  * (a, b, c) = coefficients[0..2], with the smaller Gram matrix (X^T X on the other side for rows > cols).
  * fp16 tensor-core products with fp32 accumulation, the diagonals of A and of b A + c A^2 in fp32 and the X of the
- * linear term in 22 bits: relative error 3e-4 to 1.5e-3 before the result's own rounding.  The sum of squares is taken in fp32 by
+ * linear term in 22 bits: relative error 2e-4 to 1e-3 before the result's own rounding.  The sum of squares is taken in fp32 by
  * fours and in fp64 across: where it is not finite, the result is NaN.  A fixed order: equal calls give equal
  * bits.
  * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane

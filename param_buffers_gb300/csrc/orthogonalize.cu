@@ -17,9 +17,13 @@
 // polynomial's terms cancel (a + b + c = 0.7 out of terms up to 4.8):
 //   - the diagonals of A and B never become fp16: d = diag(A) and e = a + diag(B) stay fp32 vectors, with A = d + A'
 //     the square is d^2 + (d_i + d_j) A' + A'^2, and X <- e X + B' X;
-//   - the X of the linear term is fp16 high part + fp16 low part (22 bits); the products read the high part alone.
-// Against fp64, relative error of the result: 3e-4 to 1.4e-3 over Gaussian, row-scaled and low-rank matrices; without
-// these two 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.
+//   - the X of the linear term is fp16 high part + fp16 low part (22 bits); the products read the high part alone.  The
+//     low part is scaled by e where X is nearly orthogonal (B' is small there: what its product leaves out is small),
+//     but by a alone in the first two iterations, where small singular values, on which a + diag(B) acts as far more
+//     than a + B does, still grow threefold each;
+//   - A' enters B' with a low part of its own (the square reads the high part).
+// Against fp64, relative error of the result: 2e-4 to 1e-3 over Gaussian, row-scaled and low-rank matrices; without the
+// first two 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -232,7 +236,7 @@ struct Product {
   int symmetric, n_fast; // tiles on and above the diagonal only; which index of the tiles runs first
   int m_dim, n_dim;      // of the output
   // kGram, kPoly
-  __half *gram, *poly;   // A' and B'
+  __half *gram, *gram_lo, *poly;  // A' (high and low part) and B'
   int64_t ldg, planeg;
   float *diag, *e;       // [count][m]
   int m;
@@ -240,7 +244,7 @@ struct Product {
   const __half *hi;
   __half *hi_out, *lo;
   int64_t ldx, planex;
-  int tall;
+  int tall, early;       // early: one of the first two iterations
   // powers of two: what makes the accumulator, A', B' and X true values and the reverse
   float alpha, gram_scale, gram_inv, poly_scale, x_scale, x_inv;
   float a, b, c;
@@ -328,18 +332,20 @@ template <int EPI>
 __device__ __forceinline__ void finish(const Product &p, int k, int row, int col, const uint32_t (&acc)[32]) {
   if (row >= p.m_dim || col >= p.n_dim) return;
   if constexpr (EPI == kGram || EPI == kPoly) {
-    uint32_t w[16], g[16];
+    uint32_t w[16], g[16], l[16];
     float di = 0.f;
     const float *const d = p.diag + int64_t(k) * p.m;
-    __half *const gram = p.gram + k * p.planeg;
+    __half *const gram = p.gram + k * p.planeg, *const gram_lo = p.gram_lo + k * p.planeg;
     if (EPI == kPoly) {
       load_row(gram + row * p.ldg + col, g);
+      load_row(gram_lo + row * p.ldg + col, l);
       di = d[row];
     }
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       float v[2];
       const float2 old = EPI == kPoly ? unpack2(g[j >> 1]) : make_float2(0.f, 0.f);
+      const float2 low = EPI == kPoly ? unpack2(l[j >> 1]) : make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float s = __uint_as_float(acc[j + i]) * p.alpha;
@@ -350,12 +356,17 @@ __device__ __forceinline__ void finish(const Product &p, int k, int row, int col
         } else {
           if (on_diagonal) p.e[int64_t(k) * p.m + row] = fmaf(p.c, fmaf(di, di, s), fmaf(p.b, di, p.a));
           const float dj = col + j + i < p.m ? d[col + j + i] : 0.f;
-          const float a = (i ? old.y : old.x) * p.gram_inv;
+          const float a = (i ? old.y + low.y : old.x + low.x) * p.gram_inv;
           v[i] = on_diagonal ? 0.f : (p.b * a + p.c * fmaf(di + dj, a, s)) * p.poly_scale;
         }
       }
       w[j >> 1] = pack2(v[0], v[1]);
+      if (EPI == kGram) {
+        const float2 high = unpack2(w[j >> 1]);
+        l[j >> 1] = pack2(v[0] - high.x, v[1] - high.y);
+      }
     }
+    if (EPI == kGram) store_row(gram_lo + row * p.ldg + col, l);  // where kPoly's own tiles are
     store_symmetric(EPI == kGram ? gram : p.poly + k * p.planeg, p.ldg, p.m, row, col, w);
   } else {
     const int64_t at = k * p.planex + row * p.ldx + col;
@@ -371,8 +382,10 @@ __device__ __forceinline__ void finish(const Product &p, int k, int row, int col
       const float e0 = p.tall ? (col + j < p.m ? e[col + j] : 0.f) : er;
       const float e1 = p.tall ? (col + j + 1 < p.m ? e[col + j + 1] : 0.f) : er;
       // x_inv times the stored X, alpha times the accumulator: true values
-      x[j] = fmaf(e0, (a.x + b.x) * p.x_inv, __uint_as_float(acc[j]) * p.alpha);
-      x[j + 1] = fmaf(e1, (a.y + b.y) * p.x_inv, __uint_as_float(acc[j + 1]) * p.alpha);
+      const float x0 = p.early ? fmaf(e0, a.x, p.a * b.x) : e0 * (a.x + b.x);
+      const float x1 = p.early ? fmaf(e1, a.y, p.a * b.y) : e1 * (a.y + b.y);
+      x[j] = fmaf(x0, p.x_inv, __uint_as_float(acc[j]) * p.alpha);
+      x[j + 1] = fmaf(x1, p.x_inv, __uint_as_float(acc[j + 1]) * p.alpha);
     }
     if constexpr (EPI == kUpdate) {
 #pragma unroll
@@ -664,7 +677,7 @@ constexpr int kMostSteps = 16, kMostParts = 256;
 
 struct Plan {
   int64_t m, n, rows, ldx, planex, ldg, planeg;  // rows: of X with the zeros that fill a contraction's last block
-  int64_t hi[2], lo, gram, poly, diag, e, part, bytes;  // places in the workspace
+  int64_t hi[2], lo, gram, gram_lo, poly, diag, e, part, bytes;  // places in the workspace
 };
 
 Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
@@ -685,6 +698,7 @@ Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
   p.hi[1] = take(2 * count * p.planex);
   p.lo = take(2 * count * p.planex);
   p.gram = take(2 * count * p.planeg);
+  p.gram_lo = take(2 * count * p.planeg);
   p.poly = take(2 * count * p.planeg);
   p.diag = take(4 * count * p.m);
   p.e = take(4 * count * p.m);
@@ -796,7 +810,8 @@ gtp_status iterate(Product p, const Schedule &s, const Plan &plan, char *ws, int
   const int ps = std::min(14, 15 - int(std::ceil(std::log2(std::max(poly_top, 1.0)))));
   const auto pow2 = [](int e) { return std::ldexp(1.f, e); };
   p.m = int(plan.m), p.tall = rows > cols;
-  p.gram = reinterpret_cast<__half *>(ws + plan.gram), p.poly = reinterpret_cast<__half *>(ws + plan.poly);
+  p.gram = reinterpret_cast<__half *>(ws + plan.gram), p.gram_lo = reinterpret_cast<__half *>(ws + plan.gram_lo);
+  p.poly = reinterpret_cast<__half *>(ws + plan.poly);
   p.diag = reinterpret_cast<float *>(ws + plan.diag), p.e = reinterpret_cast<float *>(ws + plan.e);
   p.lo = reinterpret_cast<__half *>(ws + plan.lo);
   p.ldg = plan.ldg, p.planeg = plan.planeg, p.ldx = plan.ldx, p.planex = plan.planex;
@@ -813,7 +828,7 @@ gtp_status iterate(Product p, const Schedule &s, const Plan &plan, char *ws, int
     p.alpha = pow2(-2 * gs);
     if (gtp_status e = run_product<false, false, kPoly>(p, gram, gram, count, plan.m, dev, st)) return e;
     p.symmetric = 0, p.n_fast = p.tall, p.m_dim = int(rows), p.n_dim = int(cols);
-    p.alpha = pow2(-ps - xs);
+    p.alpha = pow2(-ps - xs), p.early = k < 2;
     p.hi = reinterpret_cast<const __half *>(x.base), p.hi_out = reinterpret_cast<__half *>(ws + plan.hi[~k & 1]);
     if (gtp_status e = k + 1 < s.steps ? run_update<kUpdate>(p, x, poly, count, plan, dev, st)
                                        : run_update<EPI>(p, x, poly, count, plan, dev, st))
