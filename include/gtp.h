@@ -896,7 +896,8 @@ gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *momentum, fl
  * a bit in a per-device word and the kernel unwinds (its results are then invalid):
  * bit 0 operand ring (producer side), bit 1 accumulator hand-off, bit 2 operand ring
  * (MMA side), bit 3 epilogue, bit 5/6 the dynamic schedule's ring, bit 7 a drain of the
- * kernel's own copies at exit, bit 8 the self-test below.
+ * kernel's own copies at exit, bit 8 the self-test below; of the orthogonalised update bit 4
+ * a phase inside a CTA, bit 9 the CTAs of the phase before, bit 10 a chunk's old values.
  * Reads the word into *flags (host pointer) and clears it if reset != 0.  Synchronous
  * with respect to the current device.  The pages' failure detection ("05 · grad/param
  * buffer ...", §6.3: NaN / large-gradient checks before the collective) is a check of the

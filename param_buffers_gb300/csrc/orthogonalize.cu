@@ -9,8 +9,8 @@
 //   X = G / |G|_F;   steps times:   A = X X^T,  B = b A + c A^2,  X <- a X + B X
 // with the smaller Gram matrix: for more rows than columns A = X^T X and X <- a X + X B.
 //
-// Three products an iteration, each one launch of a CTA-pair kernel.  A and A^2 are symmetric: only tiles on and above
-// the diagonal are computed, each is written twice.
+// Three products an iteration.  A and A^2 are symmetric: only tiles on and above the diagonal are computed, and written
+// twice.
 //
 // Precision.  The operands are fp16, whose 11 bits err an eighth of bf16's at the same rate; all values here are bounded
 // (|X|_2 stays near 1), so powers of two hold them in fp16's range.  Three choices keep rounding away from where the
@@ -48,7 +48,7 @@ using namespace gtp::ptx;
 
 __device__ unsigned int g_ortho_wait_timeouts;  // this unit's part of gtp_wait_timeouts' word
 
-constexpr int kMostMatrices = 64;
+constexpr int kMostMatrices = 64, kMostSteps = 16, kMostPhases = 3 * kMostSteps;
 
 // --------------------------------------------------------------------------- the norm, the momentum, the first X
 
@@ -73,6 +73,7 @@ struct FirstX {
   int64_t ldx, planex;
   float xscale;
   int parts, rows;  // rows: of X, those behind the matrix's zero
+  unsigned int *arrived;  // the products' counters, cleared here
 };
 
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kPassThreads)
   for (int p = threadIdx.x; p < f.parts; p += kPassThreads) total += f.part[blockIdx.y * f.parts + p];
   total = block_sum(total);
   const float r = total == 0 ? 0.f : isfinite(total) ? float(double(f.xscale) / sqrt(total)) : nanf("");
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kMostPhases) f.arrived[threadIdx.x] = 0;
   const int step = int(gridDim.x) * kPassThreads, me = int(blockIdx.x) * kPassThreads + int(threadIdx.x);
   const int64_t zeros = (f.rows - s.rows) * f.ldx / 8;  // in both buffers that take turns as the products' X
   for (int64_t i = me; i < zeros; i += step) {
@@ -212,74 +214,89 @@ __global__ void __launch_bounds__(kPassThreads)
 
 // --------------------------------------------------------------------------- the products
 
-constexpr int BK = 64, UK = 16, BMC = 128, BMP = 256;
-constexpr int A_STAGE = BMC * BK * 2;
-constexpr int MN_CHUNK = 64 * BK * 2;  // one 64-wide MN-major box
-constexpr int SMEM_OPS = 192 * 1024, SMEM_CTRL = 512;
-constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_CTRL + 1024;
-// warps: 0 A producer, 1 MMA, 2 B producer, 4-11 epilogue (two a quarter of the accumulator's lanes)
-constexpr int kThreads = 384, kEpilogueWarps = 8;
+// All products of a call in one cooperative launch of CTA pairs.  A phase is one product of one iteration over all
+// matrices; its pair tiles go round the pairs, and a phase starts on a CTA when every CTA that had a tile of the one
+// before has counted itself off (arrived[phase], one word each, cleared by first_x_kernel).
+//
+// Inside a CTA: warp 0 and warp 2 copy A and B tiles to a ring of shared-memory stages, warp 1 of the even CTA issues the
+// M = 256 MMAs of the pair into one of two accumulators, warp 3 waits for phases, warps 4-11 finish the tiles: 32 x 32
+// chunks of the accumulator meet the old values (A', or X's two parts) that a tensor copy brought to the warp's own
+// staging slot one chunk ahead, and the new ones leave through the same slot.
+constexpr int BK = 64, UK = 16, BMC = 128, BMP = 256, BN = 256;
+constexpr int BOX = 64 * 64 * 2;  // one tensor copy: 64 rows of 128 bytes, either majorness
+constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 5;
+constexpr int kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
+constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART;  // a chunk of fp16; high and low part of one
+constexpr int SMEM_OPS = STAGES * STAGE, SMEM_SLOTS = kEpilogueWarps * 2 * SLOT;
+constexpr int SMEM_VEC = kEpilogueWarps * 32 * 4 + 16, SMEM_CTRL = 512;
+// dynamic shared memory is on 1024 bytes only after an offset of up to 1008
+constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SLOTS + SMEM_CTRL + 1024;
+static_assert(SMEM_TOTAL + SMEM_VEC <= 232448, "shared memory per block");
 
-template <int BN>
-struct Ring {
-  static constexpr int B_STAGE = BN / 2 * BK * 2;
-  static constexpr int STAGE = A_STAGE + B_STAGE;
-  static constexpr int STAGES = SMEM_OPS / STAGE;
+enum Kind { kGram, kPoly, kUpdate };
+
+struct Phase {
+  int units, full;       // tiles, the last ones (from `full` on) as two half-wide units each
+  int each, tiles_m, tiles_n, k_blocks;
+  int a_rows, b_rows;    // a matrix's rows in either operand
+  int m_dim, n_dim, out_rows;  // of the output; its rows in memory
 };
 
-enum Epilogue { kGram, kPoly, kUpdate, kOut, kStep };
+struct Maps {
+  CUtensorMap x[2], gram, poly;                                   // operands: 64 x 64 boxes
+  CUtensorMap c_hi[2], c_lo, c_gram, c_gram_lo, c_poly;           // 32 x 32 chunks
+};
 
-struct Product {
-  int tiles_m, tiles_n, k_blocks;
-  int each, units;       // units of a matrix, of all
-  int a_rows, b_rows;    // a matrix's rows in either operand
-  int symmetric, n_fast; // tiles on and above the diagonal only; which index of the tiles runs first
-  int m_dim, n_dim;      // of the output
-  // kGram, kPoly
-  __half *gram, *gram_lo, *poly;  // A' (high and low part) and B'
-  int64_t ldg, planeg;
+struct Args {
+  Phase phase[3];
+  int steps, m, step;  // step: the last product moves the master instead of writing dst
+  unsigned int *arrived;
   float *diag, *e;       // [count][m]
-  int m;
-  // kUpdate and the last product
-  const __half *hi;
-  __half *hi_out, *lo;
-  int64_t ldx, planex;
-  int tall, early;       // early: one of the first two iterations
-  // powers of two: what makes the accumulator, A', B' and X true values and the reverse
-  float alpha, gram_scale, gram_inv, poly_scale, x_scale, x_inv;
+  // powers of two: what makes the accumulators, A', B' and X true values and the reverse
+  float x_scale, x_inv, gram_scale, gram_inv, poly_scale, poly_inv;
   float a, b, c;
-  // kOut
   void *dst;
   int64_t ld, plane;
   int dst_f32;
-  // kStep
   float *master;
   __nv_bfloat16 *param;
   float keep, rate;      // 1 - lr wd, lr scale
   int64_t offset[kMostMatrices];
 };
 
-template <int BN>
-__device__ __forceinline__ void decode(const Product &p, int u, int &k, int &tm, int &tn) {
-  k = u / p.each;
-  int t = u - k * p.each;
-  if (p.symmetric) {
+// A unit's matrix, its first row of 256 and first column, and whether it is half as wide; false where it lies beside the
+// output (the second half of a narrow last tile).
+template <bool SYMMETRIC, bool N_FAST>
+__device__ __forceinline__ bool decode(const Phase &p, int u, int &k, int &row, int &col, bool &half) {
+  int t = u;
+  int h = 0;
+  half = u >= p.full;
+  if (half) {
+    t = p.full + ((u - p.full) >> 1);
+    h = (u - p.full) & 1;
+  }
+  k = t / p.each;
+  t -= k * p.each;
+  int tm, tn;
+  if (SYMMETRIC) {  // row tm of the tiles on and above the diagonal has tiles_n - tm of them
     tm = 0;
-    for (;;) {
-      tn = tm * (BMP / BN);
-      const int n = p.tiles_n - tn;
-      if (t < n) break;
-      t -= n;
-      ++tm;
-    }
-    tn += t;
-  } else if (p.n_fast) {
+    while (t >= p.tiles_n - tm) t -= p.tiles_n - tm++;
+    tn = tm + t;
+  } else if (N_FAST) {
     tm = t / p.tiles_n;
     tn = t - tm * p.tiles_n;
   } else {
     tn = t / p.tiles_m;
     tm = t - tn * p.tiles_m;
   }
+  row = tm * BMP;
+  col = tn * BN + h * (BN / 2);
+  return col < p.n_dim;
+}
+
+template <bool TALL>
+__device__ __forceinline__ bool decode(const Phase &p, int kind, int u, int &k, int &row, int &col, bool &half) {
+  return kind == kUpdate ? decode<false, TALL>(p, u, k, row, col, half) : decode<true, false>(p, u, k, row, col, half);
 }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
@@ -296,217 +313,185 @@ __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
   }
 }
 
+__device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(unsigned int *p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Waits until this CTA may start `phase` (warp 3 says so); false when the CTA gives up.
+__device__ __forceinline__ bool wait_ready(volatile int *ready, int phase, volatile int *abort_flag, unsigned int *err) {
+  if (*ready < phase) {
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t spins = 0;
+    while (*ready < phase) {
+      if ((++spins & 63u) == 0) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicOr(err, 0x10u);
+          return false;
+        }
+      }
+    }
+  }
+  __threadfence_block();
+  return true;
+}
+
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// 32 fp16 of one row, on 64 bytes.
-__device__ __forceinline__ void load_row(const __half *p, uint32_t (&w)[16]) {
+// A lane's row of a 32 x 32 chunk of fp16 in a slot, in the copies' 64-byte swizzle: 16-byte piece j of row r at
+// j ^ (r / 2 % 4).
+__device__ __forceinline__ void load_row(const uint8_t *part, int lane, uint32_t (&w)[16]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 v = reinterpret_cast<const uint4 *>(p)[q];
-    w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(part + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
   }
 }
-__device__ __forceinline__ void store_row(__half *p, const uint32_t (&w)[16]) {
+__device__ __forceinline__ void store_row(uint8_t *part, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    reinterpret_cast<uint4 *>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4 *>(part + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+// The same chunk transposed: this lane's row becomes column `lane`.
+__device__ __forceinline__ void store_column(uint8_t *part, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    *reinterpret_cast<uint16_t *>(part + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + 2 * (lane & 7)) =
+        uint16_t(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
 }
 
-// A row's 32 fp16 of a symmetric matrix, and the same below the diagonal where no tile computes them.
-__device__ __forceinline__ void store_symmetric(__half *out, int64_t ld, int m, int row, int col, const uint32_t (&w)[16]) {
-  store_row(out + row * ld + col, w);
-  if (col / BMP > row / BMP) {
+// The last product's values of a chunk (x, true values, this lane's row), through the slot so that a warp writes whole
+// row segments: eight lanes a row of 32, four values a lane.
+__device__ __forceinline__ void write_out(const Args &a, const Phase &p, uint8_t *slot, int lane, int k, int row0, int col,
+                                          const float (&x)[32]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col + j < m)
-        reinterpret_cast<uint16_t *>(out)[(col + j) * ld + row] = uint16_t(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
-  }
-}
-
-// What becomes of 32 columns of one row of the accumulator.
-template <int EPI>
-__device__ __forceinline__ void finish(const Product &p, int k, int row, int col, const uint32_t (&acc)[32]) {
-  if (row >= p.m_dim || col >= p.n_dim) return;
-  if constexpr (EPI == kGram || EPI == kPoly) {
-    uint32_t w[16], g[16], l[16];
-    float di = 0.f;
-    const float *const d = p.diag + int64_t(k) * p.m;
-    __half *const gram = p.gram + k * p.planeg, *const gram_lo = p.gram_lo + k * p.planeg;
-    if (EPI == kPoly) {
-      load_row(gram + row * p.ldg + col, g);
-      load_row(gram_lo + row * p.ldg + col, l);
-      di = d[row];
-    }
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4 *>(slot + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 7, c = col + 4 * j;
+  const int n = min(4, p.n_dim - c);
+  if (!a.step) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      float v[2];
-      const float2 old = EPI == kPoly ? unpack2(g[j >> 1]) : make_float2(0.f, 0.f);
-      const float2 low = EPI == kPoly ? unpack2(l[j >> 1]) : make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float s = __uint_as_float(acc[j + i]) * p.alpha;
-        const bool on_diagonal = col + j + i == row;
-        if (EPI == kGram) {
-          if (on_diagonal) p.diag[int64_t(k) * p.m + row] = s;
-          v[i] = on_diagonal ? 0.f : s * p.gram_scale;
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), row = row0 + r;
+      const float4 v = *reinterpret_cast<const float4 *>(slot + r * 128 + ((j ^ (r & 7)) << 4));
+      if (row >= p.m_dim || n <= 0) continue;
+      const float y[4] = {v.x, v.y, v.z, v.w};
+      const int64_t at = k * a.plane + row * a.ld + c;
+      if (a.dst_f32) {
+        float *const o = static_cast<float *>(a.dst) + at;
+        if (n == 4 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+          *reinterpret_cast<float4 *>(o) = v;
         } else {
-          if (on_diagonal) p.e[int64_t(k) * p.m + row] = fmaf(p.c, fmaf(di, di, s), fmaf(p.b, di, p.a));
-          const float dj = col + j + i < p.m ? d[col + j + i] : 0.f;
-          const float a = (i ? old.y + low.y : old.x + low.x) * p.gram_inv;
-          v[i] = on_diagonal ? 0.f : (p.b * a + p.c * fmaf(di + dj, a, s)) * p.poly_scale;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < n) o[q] = y[q];
+        }
+      } else {
+        __nv_bfloat16 *const o = static_cast<__nv_bfloat16 *>(a.dst) + at;
+        if (n == 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+          const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+          *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(w);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < n) o[q] = __float2bfloat16_rn(y[q]);
         }
       }
-      w[j >> 1] = pack2(v[0], v[1]);
-      if (EPI == kGram) {
-        const float2 high = unpack2(w[j >> 1]);
-        l[j >> 1] = pack2(v[0] - high.x, v[1] - high.y);
-      }
     }
-    if (EPI == kGram) store_row(gram_lo + row * p.ldg + col, l);  // where kPoly's own tiles are
-    store_symmetric(EPI == kGram ? gram : p.poly + k * p.planeg, p.ldg, p.m, row, col, w);
   } else {
-    const int64_t at = k * p.planex + row * p.ldx + col;
-    uint32_t h[16], l[16];
-    load_row(p.hi + at, h);
-    load_row(p.lo + at, l);
-    float x[32];
-    const float *const e = p.e + int64_t(k) * p.m;
-    const float er = p.tall ? 0.f : e[row];
+    const int64_t base = a.offset[k] + int64_t(row0 + (lane >> 3)) * p.n_dim + c;
+    const int64_t step = 4 * int64_t(p.n_dim);
+    const bool wide = n == 4 && p.n_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.master + base) & 15) == 0;
+    float4 m[8];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 a = unpack2(h[j >> 1]), b = unpack2(l[j >> 1]);
-      const float e0 = p.tall ? (col + j < p.m ? e[col + j] : 0.f) : er;
-      const float e1 = p.tall ? (col + j + 1 < p.m ? e[col + j + 1] : 0.f) : er;
-      // x_inv times the stored X, alpha times the accumulator: true values
-      const float x0 = p.early ? fmaf(e0, a.x, p.a * b.x) : e0 * (a.x + b.x);
-      const float x1 = p.early ? fmaf(e1, a.y, p.a * b.y) : e1 * (a.y + b.y);
-      x[j] = fmaf(x0, p.x_inv, __uint_as_float(acc[j]) * p.alpha);
-      x[j + 1] = fmaf(x1, p.x_inv, __uint_as_float(acc[j + 1]) * p.alpha);
+    for (int i = 0; i < 8; ++i) {
+      if (row0 + 4 * i + (lane >> 3) >= p.m_dim || n <= 0) continue;
+      const float *const o = a.master + base + i * step;
+      if (wide) m[i] = *reinterpret_cast<const float4 *>(o);
+      else m[i] = make_float4(o[0], n > 1 ? o[1] : 0.f, n > 2 ? o[2] : 0.f, n > 3 ? o[3] : 0.f);
     }
-    if constexpr (EPI == kUpdate) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float x0 = x[j] * p.x_scale, x1 = x[j + 1] * p.x_scale;
-        h[j >> 1] = pack2(x0, x1);
-        const float2 r = unpack2(h[j >> 1]);
-        l[j >> 1] = pack2(x0 - r.x, x1 - r.y);
-      }
-      store_row(p.hi_out + at, h);
-      store_row(p.lo + at, l);
-    } else if constexpr (EPI == kOut) {
-      const int n = min(32, p.n_dim - col);
-      const int64_t to = k * p.plane + row * p.ld + col;
-      if (p.dst_f32) {
-        float *const o = static_cast<float *>(p.dst) + to;
-        if (n == 32 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            reinterpret_cast<float4 *>(o)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < n) o[j] = x[j];
-        }
-      } else {
-        __nv_bfloat16 *const o = static_cast<__nv_bfloat16 *>(p.dst) + to;
-        __nv_bfloat162 w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        if (n == 32 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) reinterpret_cast<uint4 *>(o)[q] = reinterpret_cast<const uint4 *>(w)[q];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < n) o[j] = j & 1 ? __high2bfloat16(w[j >> 1]) : __low2bfloat16(w[j >> 1]);
-        }
-      }
-    } else {
-      const int n = min(32, p.n_dim - col);
-      const int64_t to = p.offset[k] + int64_t(row) * p.n_dim + col;
-      float *const o = p.master + to;
-      const bool wide = n == 32 && (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const float4 v = *reinterpret_cast<const float4 *>(slot + r * 128 + ((j ^ (r & 7)) << 4));
+      if (row0 + r >= p.m_dim || n <= 0) continue;
+      const float y[4] = {fmaf(a.keep, m[i].x, -a.rate * v.x), fmaf(a.keep, m[i].y, -a.rate * v.y),
+                          fmaf(a.keep, m[i].z, -a.rate * v.z), fmaf(a.keep, m[i].w, -a.rate * v.w)};
+      float *const o = a.master + base + i * step;
       if (wide) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 v = reinterpret_cast<const float4 *>(o)[q];
-          x[4 * q] = fmaf(p.keep, v.x, -p.rate * x[4 * q]);
-          x[4 * q + 1] = fmaf(p.keep, v.y, -p.rate * x[4 * q + 1]);
-          x[4 * q + 2] = fmaf(p.keep, v.z, -p.rate * x[4 * q + 2]);
-          x[4 * q + 3] = fmaf(p.keep, v.w, -p.rate * x[4 * q + 3]);
-          reinterpret_cast<float4 *>(o)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        }
+        *reinterpret_cast<float4 *>(o) = make_float4(y[0], y[1], y[2], y[3]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < n) {
-            x[j] = fmaf(p.keep, o[j], -p.rate * x[j]);
-            o[j] = x[j];
-          }
+        for (int q = 0; q < 4; ++q)
+          if (q < n) o[q] = y[q];
       }
-      if (p.param) {
-        __nv_bfloat16 *const q = p.param + to;
-        __nv_bfloat162 w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        if (wide && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(q)[i] = reinterpret_cast<const uint4 *>(w)[i];
+      if (a.param) {
+        __nv_bfloat16 *const w = a.param + base + i * step;
+        if (wide && (reinterpret_cast<uintptr_t>(w) & 7) == 0) {
+          const __nv_bfloat162 b[2] = {__floats2bfloat162_rn(y[0], y[1]), __floats2bfloat162_rn(y[2], y[3])};
+          *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(b);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < n) q[j] = j & 1 ? __high2bfloat16(w[j >> 1]) : __low2bfloat16(w[j >> 1]);
+          for (int q = 0; q < 4; ++q)
+            if (q < n) w[q] = __float2bfloat16_rn(y[q]);
         }
       }
     }
   }
 }
 
-// D = A B^T of one pair tile of 256 x BN after another, over a CTA pair (a cluster of two SMs sharing M = 256 MMAs):
-// each CTA stages 128 rows of A and BN / 2 rows of B a k-block and holds its 128 x BN of D in tensor memory, twice, so
-// that a tile's epilogue runs under the next one's products.  The hand-offs are those of the bf16 pair GEMM: both CTAs'
-// copies complete on the even CTA's full[], which that CTA arms; its commits go to both CTAs' empty[] and tfull[]; the
-// epilogue warps of both release an accumulator on its tempty[]; at exit it drains every stage that it armed.
-template <int BN, bool A_MN, bool B_MN, int EPI>
+template <bool TALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    newton_schulz_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                         const __grid_constant__ Product p) {
-  using R = Ring<BN>;
+    newton_schulz_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int finished;  // warps that have finished their part of a phase, over all phases
+  __shared__ __align__(16) float vec[kEpilogueWarps][32];  // d or e of a chunk's columns
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sA = smem, *sB = smem + R::STAGES * A_STAGE;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + SMEM_OPS);
-  uint64_t *empty = full + R::STAGES;
-  uint64_t *tfull = empty + R::STAGES;
+  uint8_t *sA = smem, *sB = smem + STAGES * A_STAGE, *slots = smem + SMEM_OPS;
+  uint64_t *full = reinterpret_cast<uint64_t *>(slots + SMEM_SLOTS);
+  uint64_t *empty = full + STAGES;
+  uint64_t *tfull = empty + STAGES;
   uint64_t *tempty = tfull + 2;
   uint64_t *drained = tempty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+  uint64_t *cfull = drained + 1;  // [warp][slot]: a chunk's old values have landed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + 2 * kEpilogueWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * R::STAGES + 5) * 8 + 8 <= SMEM_CTRL, "control block");
+  volatile int *ready = abort_flag + 1;
+  static_assert((2 * STAGES + 5 + 2 * kEpilogueWarps) * 8 + 12 <= SMEM_CTRL, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int first = int(blockIdx.x >> 1), step = int(gridDim.x >> 1);
+  const int first = int(blockIdx.x >> 1), step = int(gridDim.x >> 1), phases = 3 * a.steps;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < R::STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpilogueWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpilogueWarps);
     }
     mbar_init(drained, 1);
+    for (int i = 0; i < 2 * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
     *abort_flag = 0;
+    *ready = 0;
+    finished = 0;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 2 * BN);
@@ -518,147 +503,363 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   unsigned int *err = &g_ortho_wait_timeouts;
-  allow_dependents();
-  wait_prior_grid();
 
-  if (warp == 0) {
-    if (lane == 0) {  // -------------------------------------------------- A producer (both CTAs)
+  if (warp == 0 || warp == 2) {
+    if (lane == 0) {  // ------------------------------------ producers (both CTAs): warp 0 A, warp 2 B
+      const bool is_a = warp == 0;
       int stage = 0;
-      uint32_t phase = 0;
-      int armed[R::STAGES];
-      for (int s = 0; s < R::STAGES; ++s) armed[s] = -1;
+      uint32_t parity = 0;
+      int armed[STAGES];
+      for (int s = 0; s < STAGES; ++s) armed[s] = -1;
       bool ok = true;
-      for (int u = first; ok && u < p.units; u += step) {
-        int k, tm, tn;
-        decode<BN>(p, u, k, tm, tn);
-        const int m0 = tm * BMP + BMC * int(rank);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&full[stage], 2u * uint32_t(R::STAGE));
-            armed[stage] = int(phase);
-          }
-          const uint32_t bar = mapa_shared(&full[stage], 0);
-          uint8_t *a = sA + stage * A_STAGE;
-          if (A_MN) {
-            tma_load_2d_pair(&tmA, bar, a, m0, k * p.a_rows + kb * BK);
-            tma_load_2d_pair(&tmA, bar, a + MN_CHUNK, m0 + 64, k * p.a_rows + kb * BK);
-          } else {
-            tma_load_2d_pair(&tmA, bar, a, kb * BK, k * p.a_rows + m0);
-          }
-          if (++stage == R::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+      for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+        const Phase &p = a.phase[kind];
+        if (first >= p.units) continue;
+        if (!wait_ready(ready, ph, abort_flag, err)) break;
+        fence_proxy_async();
+        const CUtensorMap *x = &maps.x[(ph / 3) & 1];
+        const bool mn = kind == kGram ? TALL : kind == kUpdate && !is_a && !TALL;  // rows of the box run along K
+        const CUtensorMap *map = kind == kGram ? x : kind == kPoly ? &maps.gram : is_a == TALL ? x : &maps.poly;
+        const int rows = is_a ? p.a_rows : p.b_rows;
+        for (int u = first; ok && u < p.units; u += step) {
+          int k, row, col;
+          bool half;
+          if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
+          // this CTA's 128 rows of A, 128 or 64 of B
+          const int i0 = is_a ? row + BMC * int(rank) : col + (half ? 64 : 128) * int(rank);
+          const int boxes = is_a || !half ? 2 : 1;
+          for (int kb = 0; kb < p.k_blocks; ++kb) {
+            if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) {
+              ok = false;
+              break;
+            }
+            if (is_a && rank == 0) {  // the even CTA's barrier counts both CTAs' bytes
+              mbar_arrive_expect_tx(&full[stage], half ? 2u * (A_STAGE + BOX) : 2u * STAGE);
+              armed[stage] = int(parity);
+            }
+            const uint32_t bar = mapa_shared(&full[stage], 0);
+            uint8_t *to = (is_a ? sA : sB) + stage * A_STAGE;
+            for (int i = 0; i < boxes; ++i) {
+              const int at = i0 + 64 * i;
+              if (mn) tma_load_2d_pair(map, bar, to + i * BOX, at, k * rows + kb * BK);
+              else tma_load_2d_pair(map, bar, to + i * BOX, kb * BK, k * rows + at);
+            }
+            if (++stage == STAGES) {
+              stage = 0;
+              parity ^= 1u;
+            }
           }
         }
       }
-      for (int s = 0; s < R::STAGES; ++s)
+      for (int s = 0; s < STAGES; ++s)  // every armed copy has landed before the pair leaves
         if (armed[s] >= 0) drain(&full[s], uint32_t(armed[s]));
-    }
-  } else if (warp == 2) {
-    if (lane == 0) {  // -------------------------------------------------- B producer (both CTAs)
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = first; ok && u < p.units; u += step) {
-        int k, tm, tn;
-        decode<BN>(p, u, k, tm, tn);
-        const int n0 = tn * BN + (BN / 2) * int(rank);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 0x1u)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = mapa_shared(&full[stage], 0);
-          uint8_t *b = sB + stage * R::B_STAGE;
-          if (B_MN) {
-#pragma unroll
-            for (int j = 0; j < BN / 128; ++j)
-              tma_load_2d_pair(&tmB, bar, b + j * MN_CHUNK, n0 + 64 * j, k * p.b_rows + kb * BK);
-          } else {
-            tma_load_2d_pair(&tmB, bar, b, kb * BK, k * p.b_rows + n0);
-          }
-          if (++stage == R::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
     }
   } else if (warp == 1) {  // ---------------------------------------------- MMA (the even CTA)
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(BMP, BN, A_MN, B_MN);
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t parity = 0, acc_parity = 0;
       bool ok = true;
-      for (int u = first; ok && u < p.units; u += step) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, err, 0x2u))) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + uint32_t(acc * BN);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, abort_flag, err, 0x4u))) {
+      for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+        const Phase &p = a.phase[kind];
+        const bool a_mn = kind == kGram && TALL, b_mn = a_mn || (kind == kUpdate && !TALL);
+        for (int u = first; ok && u < p.units; u += step) {
+          int k, row, col;
+          bool half;
+          if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_parity ^ 1u, abort_flag, err, 0x2u))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (elect_one_sync()) {
-            const uint32_t a0 = smem_u32(sA + stage * A_STAGE), b0 = smem_u32(sB + stage * R::B_STAGE);
-#pragma unroll
-            for (int i = 0; i < BK / UK; ++i) {
-              const uint64_t ad = A_MN ? sdesc_sw128(a0 + i * (UK * 128), MN_CHUNK, 1024) : sdesc_sw128(a0 + i * (UK * 2), 16, 1024);
-              const uint64_t bd = B_MN ? sdesc_sw128(b0 + i * (UK * 128), MN_CHUNK, 1024) : sdesc_sw128(b0 + i * (UK * 2), 16, 1024);
-              mma_f16_pair(d, ad, bd, idesc, (kb > 0 || i > 0) ? 1u : 0u);
+          const uint32_t d = tmem_base + uint32_t(acc * BN);
+          const uint32_t idesc = idesc_f16_f32(BMP, half ? BN / 2 : BN, a_mn, b_mn);
+          // from one K = 16 slice of a stage to the next: 16 rows of 128 bytes, or 32 bytes of each row
+          const uint32_t da = a_mn ? UK * 128 : UK * 2, db = b_mn ? UK * 128 : UK * 2;
+          for (int kb = 0; kb < p.k_blocks; ++kb) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], parity, abort_flag, err, 0x4u))) {
+              ok = false;
+              break;
             }
-            mma_commit_pair(&empty[stage], 0x3);
+            tc_fence_after();
+            if (elect_one_sync()) {
+              const uint32_t a0 = smem_u32(sA + stage * A_STAGE), b0 = smem_u32(sB + stage * A_STAGE);
+#pragma unroll
+              for (int i = 0; i < BK / UK; ++i) {
+                const uint64_t ad = sdesc_sw128(a0 + i * da, a_mn ? BOX : 16, 1024);
+                const uint64_t bd = sdesc_sw128(b0 + i * db, b_mn ? BOX : 16, 1024);
+                mma_f16_pair(d, ad, bd, idesc, (kb > 0 || i > 0) ? 1u : 0u);
+              }
+              mma_commit_pair(&empty[stage], 0x3);
+            }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              parity ^= 1u;
+            }
           }
+          if (!ok) break;
+          if (elect_one_sync()) mma_commit_pair(&tfull[acc], 0x3);
           __syncwarp();
-          if (++stage == R::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          if (++acc == 2) {
+            acc = 0;
+            acc_parity ^= 1u;
           }
-        }
-        if (!ok) break;
-        if (elect_one_sync()) mma_commit_pair(&tfull[acc], 0x3);
-        __syncwarp();
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
         }
       }
       if (elect_one_sync()) mma_commit_pair(drained, 0x3);  // both CTAs learn when every MMA has finished
       __syncwarp();
     }
     if (lane == 0) drain(drained, 0);
-  } else if (warp >= 4) {  // ---------------------------------------------- epilogue (both CTAs)
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int u = first; u < p.units; u += step) {
-      int k, tm, tn;
-      decode<BN>(p, u, k, tm, tn);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, abort_flag, err, 0x8u))) break;
-      tc_fence_after();
-      const int row = tm * BMP + BMC * int(rank) + 32 * quarter + lane;
-      const int c0 = half * (BN / 2);
-      const uint32_t base = tmem_base + (uint32_t(32 * quarter) << 16) + uint32_t(acc * BN + c0);
+  } else if (warp == 3) {
+    if (lane == 0) {  // ---------------------------------------------------- the phases' order
+      for (int ph = 1; ph < phases; ++ph) {
+        if (first >= a.phase[ph % 3].units) continue;
+        const unsigned int all = 2u * unsigned(min(a.phase[(ph - 1) % 3].units, step));
+        const uint64_t t0 = globaltimer_ns();
+        bool ok = true;
+        while (load_acquire(&a.arrived[ph - 1]) < all) {
+          if (*abort_flag) ok = false;
+          if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, 0x200u);
+            ok = false;
+          }
+          if (!ok) break;
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          break;
+        }
+        fence_proxy_async();
+        __threadfence_block();
+        *ready = ph;
+      }
+    }
+  } else {  // -------------------------------------------------------------- finishing the tiles (both CTAs)
+    const int ew = warp - 4, quarter = warp & 3, side = ew >> 2;
+    uint8_t *const mine = slots + ew * 2 * SLOT;
+    uint64_t *const cbar = cfull + 2 * ew;
+    float *const v = vec[ew];
+    int acc = 0, slot = 0;
+    uint32_t acc_parity = 0, cparity = 0;  // bit s: the parity that slot s's next copy completes
+    int flying = 0;                        // bit s: a copy into slot s that nobody has waited for
+    bool ok = true;
+    for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+      const Phase &p = a.phase[kind];
+      if (first >= p.units) continue;
+      const bool last = ph + 1 == phases, early = ph < 6;
+      {
+        bool r = true;
+        if (lane == 0) r = wait_ready(ready, ph, abort_flag, err);
+        ok = __all_sync(0xFFFFFFFFu, r);
+        if (!ok) break;
+        if (lane == 0) fence_proxy_async();
+      }
+      const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
+      const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
+      // The chunk behind (u, c): fetched into the other slot while this one is worked on.
+      const auto fetch = [&](int s, int k, int row0, int col) {  // lane 0
+        mbar_arrive_expect_tx(&cbar[s], 2 * PART);
+        tma_load_2d(from_hi, &cbar[s], mine + s * SLOT, col, k * p.out_rows + row0);
+        tma_load_2d(from_lo, &cbar[s], mine + s * SLOT + PART, col, k * p.out_rows + row0);
+      };
+      const auto exists = [&](int row0, int col) { return row0 < p.out_rows && col < p.n_dim; };
+      bool fetched = false;  // the coming chunk's copy is under way
+      for (int u = first; ok && u < p.units; u += step) {
+        int k, row, col;
+        bool half;
+        if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
+        const int wide = half ? BN / 4 : BN / 2;  // this warp's columns
+        const int row0 = row + BMC * int(rank) + 32 * quarter, c0 = col + side * wide, me = row0 + lane;
+        if (kind != kGram && !fetched && exists(row0, c0)) {
+          if (lane == 0) {
+            bulk_wait_group_read<0>();
+            fetch(slot, k, row0, c0);
+          }
+          flying |= 1 << slot;
+          fetched = true;
+        }
+        // d or e of this lane's row and of the columns
+        float own = 0.f, t[4] = {0.f, 0.f, 0.f, 0.f};
+        if (kind != kGram) {
+          const float *const d = (kind == kPoly ? a.diag : a.e) + int64_t(k) * a.m;
+          if ((kind == kPoly || !TALL) && me < a.m) own = __ldcg(d + me);
+          if (kind == kPoly || TALL) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c0 + 32 * i + lane < a.m) t[i] = __ldcg(d + c0 + 32 * i + lane);
+          }
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_parity, abort_flag, err, 0x8u))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = tmem_base + (uint32_t(32 * quarter) << 16) + uint32_t(acc * BN + side * wide);
 #pragma unroll 1
-      for (int c = 0; c < BN / 2; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(base + uint32_t(c), r);
-        tmem_ld_wait();
-        finish<EPI>(p, k, row, tn * BN + c0 + c, r);
+        for (int c = 0; c < wide; c += 32) {
+          const int at = c0 + c;
+          if (!exists(row0, at)) break;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(base + uint32_t(c), r);
+          uint8_t *const buf = mine + slot * SLOT, *const other = mine + (slot ^ 1) * SLOT;
+          if (kind != kGram) {
+            // the coming chunk: the next of this unit, or the next unit's first
+            int nk = k, nrow = row0, ncol = at + 32;
+            bool more = c + 32 < wide && exists(nrow, ncol);
+            for (int nu = u + step; !more && nu < p.units; nu += step) {
+              int rr, cc;
+              bool hh;
+              if (!decode<TALL>(p, kind, nu, nk, rr, cc, hh)) continue;
+              nrow = rr + BMC * int(rank) + 32 * quarter, ncol = cc + side * (hh ? BN / 4 : BN / 2);
+              more = exists(nrow, ncol);
+              break;  // a unit without a chunk for this warp starts its own fetch after it
+            }
+            if (more) {
+              if (lane == 0) {
+                bulk_wait_group_read<0>();  // the other slot's store has read it
+                fetch(slot ^ 1, nk, nrow, ncol);
+              }
+              flying |= 1 << (slot ^ 1);
+            }
+            fetched = more;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u))) {
+              tmem_ld_wait();
+              ok = false;
+              break;
+            }
+            cparity ^= 1u << slot;
+            flying &= ~(1 << slot);
+            v[lane] = c == 0 ? t[0] : c == 32 ? t[1] : c == 64 ? t[2] : t[3];
+            __syncwarp();
+          } else {
+            if (lane == 0) bulk_wait_group_read<0>();  // both slots' stores have read them
+            __syncwarp();
+          }
+          tmem_ld_wait();
+          if (kind == kUpdate) {
+            uint32_t h[16], l[16];
+            load_row(buf, lane, h);
+            load_row(buf + PART, lane, l);
+            float x[32];
+            const float alpha = a.poly_inv * a.x_inv;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              float e[4] = {own, own, own, own};
+              if (TALL) {
+                const float4 t = *reinterpret_cast<const float4 *>(&v[j]);
+                e[0] = t.x, e[1] = t.y, e[2] = t.z, e[3] = t.w;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                const float2 hi = unpack2(h[(j + i) >> 1]), lo = unpack2(l[(j + i) >> 1]);
+                // x_inv times the stored X, alpha times the accumulator: true values
+                const float x0 = early ? fmaf(e[i], hi.x, a.a * lo.x) : e[i] * (hi.x + lo.x);
+                const float x1 = early ? fmaf(e[i + 1], hi.y, a.a * lo.y) : e[i + 1] * (hi.y + lo.y);
+                x[j + i] = fmaf(x0, a.x_inv, __uint_as_float(r[j + i]) * alpha);
+                x[j + i + 1] = fmaf(x1, a.x_inv, __uint_as_float(r[j + i + 1]) * alpha);
+              }
+            }
+            if (!last) {
+              const bool inside = me < p.m_dim;  // the rows that fill a contraction's last block stay zero
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float x0 = inside ? x[j] * a.x_scale : 0.f, x1 = inside ? x[j + 1] * a.x_scale : 0.f;
+                h[j >> 1] = pack2(x0, x1);
+                const float2 t = unpack2(h[j >> 1]);
+                l[j >> 1] = pack2(x0 - t.x, x1 - t.y);
+              }
+              store_row(buf, lane, h);
+              store_row(buf + PART, lane, l);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int to = k * p.out_rows + row0;
+                tma_store_2d(&maps.c_hi[~(ph / 3) & 1], buf, at, to);
+                tma_store_2d(&maps.c_lo, buf + PART, at, to);
+                bulk_commit_group();
+              }
+            } else {
+              __syncwarp();  // every lane has read its row of the slot
+              write_out(a, p, buf, lane, k, row0, at, x);
+              fence_proxy_async_smem();
+              __syncwarp();  // and the slot's values, before a copy overwrites them
+            }
+          } else {
+            uint32_t w[16], l[16];
+            if (kind == kPoly) {
+              load_row(buf, lane, w);
+              load_row(buf + PART, lane, l);
+            }
+            const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float out[2];
+              const float2 hi = unpack2(w[j >> 1]), lo = unpack2(l[j >> 1]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float s = __uint_as_float(r[j + i]) * alpha;
+                const bool on_diagonal = at + j + i == me;
+                if (kind == kGram) {
+                  if (on_diagonal && me < a.m) a.diag[int64_t(k) * a.m + me] = s;
+                  out[i] = on_diagonal ? 0.f : s * a.gram_scale;
+                } else {
+                  if (on_diagonal && me < a.m) a.e[int64_t(k) * a.m + me] = fmaf(a.c, fmaf(own, own, s), fmaf(a.b, own, a.a));
+                  const float g = (i ? hi.y + lo.y : hi.x + lo.x) * a.gram_inv;
+                  out[i] = on_diagonal ? 0.f : (a.b * g + a.c * fmaf(own + v[j + i], g, s)) * a.poly_scale;
+                }
+              }
+              w[j >> 1] = pack2(out[0], out[1]);
+              if (kind == kGram) {
+                const float2 high = unpack2(w[j >> 1]);
+                l[j >> 1] = pack2(out[0] - high.x, out[1] - high.y);
+              }
+            }
+            // the chunk, its low part (A'; where the next phase's own tiles are), and its mirror image where no tile
+            // computes it
+            const bool mirror = at / BMP > row0 / BMP;
+            uint8_t *const image = kind == kGram ? other : buf + PART;
+            store_row(buf, lane, w);
+            if (kind == kGram) store_row(buf + PART, lane, l);
+            __syncwarp();  // kPoly: the image lies where the low part was read
+            if (mirror) store_column(image, lane, w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int to = k * p.out_rows + row0, across = k * p.out_rows + at;
+              const CUtensorMap *const out = kind == kGram ? &maps.c_gram : &maps.c_poly;
+              tma_store_2d(out, buf, at, to);
+              if (kind == kGram) tma_store_2d(&maps.c_gram_lo, buf + PART, at, to);
+              if (mirror) tma_store_2d(out, image, row0, across);
+              bulk_commit_group();
+            }
+          }
+          if (kind != kGram) slot ^= 1;
+        }
+        if (!ok) break;
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[acc], 0));
+        if (++acc == 2) {
+          acc = 0;
+          acc_parity ^= 1u;
+        }
       }
-      tc_fence_before();
+      if (!ok || last) break;
+      // this CTA's part of the phase is in memory: copies out have been written, d and e by every lane
+      if (lane == 0) bulk_wait_all();
+      fence_proxy_async();
+      __threadfence();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[acc], 0));
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+      if (lane == 0 && (atomicAdd(&finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {  // the last of the warps
+        __threadfence();
+        add_release(&a.arrived[ph]);
       }
+    }
+    if (!ok) *abort_flag = 1;
+    if (lane == 0) {
+      bulk_wait_group_read<0>();  // the slots outlive the stores' reads of them
+      for (int s = 0; s < 2; ++s)
+        if (flying >> s & 1) drain(&cbar[s], (cparity >> s) & 1u);
     }
   }
   tc_fence_before();
@@ -673,21 +874,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // --------------------------------------------------------------------------- host
 
 constexpr int64_t kMostElements = (int64_t(1) << 31) - 1, kMostSide = 65536;
-constexpr int kMostSteps = 16, kMostParts = 256;
+constexpr int kMostParts = 1024;
 
 struct Plan {
-  int64_t m, n, rows, ldx, planex, ldg, planeg;  // rows: of X with the zeros that fill a contraction's last block
-  int64_t hi[2], lo, gram, gram_lo, poly, diag, e, part, bytes;  // places in the workspace
+  int64_t m, n, rows, ldx, planex, grows, ldg, planeg;  // rows, grows: of X and of A with what fills the last block of 64
+  int64_t hi[2], lo, gram, gram_lo, poly, diag, e, part, arrived, bytes;  // places in the workspace
 };
 
 Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
   Plan p = {};
   p.m = std::min(rows, cols), p.n = std::max(rows, cols);
-  // whole 32-column chunks a row, whatever the matrix's own width: the epilogue needs no bounds inside a chunk, and
-  // the copies stop at the true width
-  p.rows = (rows + BK - 1) / BK * BK;
+  // matrices stand on whole blocks of 64 rows: chunks and boxes of one stay within it
+  p.rows = (rows + BK - 1) / BK * BK, p.grows = (p.m + BK - 1) / BK * BK;
   p.ldx = (cols + 63) / 64 * 64, p.planex = p.rows * p.ldx;
-  p.ldg = (p.m + 63) / 64 * 64, p.planeg = p.m * p.ldg;
+  p.ldg = p.grows, p.planeg = p.grows * p.ldg;
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -703,6 +903,7 @@ Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
   p.diag = take(4 * count * p.m);
   p.e = take(4 * count * p.m);
   p.part = take(8 * count * kMostParts);
+  p.arrived = take(4 * kMostPhases);
   p.bytes = at;
   return p;
 }
@@ -710,7 +911,7 @@ Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
 struct Schedule {
   float a, b, c;
   int steps;
-  float bound;  // on |X|_2 over all iterations, from 1
+  float bound;  // on |X|_2 over the operands, from 1
 };
 
 // The largest singular value that the iteration can make of one in [0, 1], step by step, on a grid whose spacing the
@@ -736,105 +937,106 @@ gtp_status schedule_of(const float *abc, int32_t steps, Schedule *s) {
   return GTP_OK;
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
-gtp_status launch_product(const CUtensorMap &ta, const CUtensorMap &tb, const Product &p, const gtp::DeviceInfo &dev,
-                          cudaStream_t st) {
-  static std::atomic<uint64_t> configured{0};
-  const auto kernel = newton_schulz_kernel<BN, A_MN, B_MN, EPI>;
-  const uint64_t bit = uint64_t(1) << (dev.device & 63);
-  if (!(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
-    if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    configured.fetch_or(bit);
-  }
-  const unsigned grid = 2 * unsigned(std::min(p.units, dev.sm_count / 2));
-  return gtp::launch_overlapped(kernel, grid, kThreads, SMEM_TOTAL, st, "orthogonalize", ta, tb, p);
+// How many CTA pairs of the kernel the device holds at once (a cooperative launch's limit); 0 on an error.
+template <bool TALL>
+gtp_status pairs_of(const gtp::DeviceInfo &dev, int *pairs) {
+  static std::atomic<int> known[64];
+  std::atomic<int> &slot = known[dev.device & 63];
+  if ((*pairs = slot.load()) > 0) return GTP_OK;
+  cudaError_t e = cudaFuncSetAttribute(newton_schulz_kernel<TALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(dev.sm_count / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SMEM_TOTAL;
+  e = cudaOccupancyMaxActiveClusters(pairs, newton_schulz_kernel<TALL>, &cfg);
+  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+  if (*pairs < 1) return gtp::fail(GTP_E_CUDA, "no room for a CTA pair");
+  *pairs = std::min(*pairs, dev.sm_count / 2);
+  slot.store(*pairs);
+  return GTP_OK;
 }
 
-// An operand: matrices of rows x inner fp16 at `base`, one after another.  A copy that passes a matrix's last row reads
-// the next one's: harmless where rows are the product's rows or columns (nobody takes those), and where they are the
-// contraction the last block's rows are zeros of the matrix's own (Plan::rows).
-struct Operand {
-  const void *base;
-  int64_t inner, rows, ld;
-};
-
-gtp_status map_of(CUtensorMap *map, const Operand &o, int64_t count, bool mn, int box_rows) {
-  return gtp::encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, o.base, uint64_t(o.inner), uint64_t(count * o.rows),
-                             uint64_t(2 * o.ld), BK, mn ? 64 : uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// The product D = A B^T (m_dim x n_dim, contraction k) of every matrix, in tiles 256 columns wide or 128: whichever
-// needs less time in whole waves of the machine's CTA pairs.  A half-wide tile takes 0.55 of a whole one's time.
-template <bool A_MN, bool B_MN, int EPI>
-gtp_status run_product(Product p, const Operand &a, const Operand &b, int64_t count, int64_t k, const gtp::DeviceInfo &dev,
-                       cudaStream_t st) {
-  const int pairs = dev.sm_count / 2;
-  const auto shape = [&](int BN) {
-    p.tiles_m = (p.m_dim + BMP - 1) / BMP;
-    p.tiles_n = (p.n_dim + BN - 1) / BN;
-    p.each = p.tiles_m * p.tiles_n;
-    if (p.symmetric) {
-      p.each = 0;
-      for (int tm = 0; tm < p.tiles_m; ++tm) p.each += std::max(0, p.tiles_n - tm * (BMP / BN));
-    }
-    p.units = int(count) * p.each;
-    return (p.units + pairs - 1) / pairs;
-  };
+// Tiles of 256 x 256 in whole waves of the pairs, the rest as halves where those fit one wave or less time: a half-wide
+// unit takes 0.55 of a whole one's time.
+void shape(Phase &p, int64_t count, bool symmetric, int64_t k, int pairs) {
+  p.tiles_m = (p.m_dim + BMP - 1) / BMP, p.tiles_n = (p.n_dim + BN - 1) / BN;
+  p.each = symmetric ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
   p.k_blocks = int((k + BK - 1) / BK);
-  p.a_rows = int(a.rows), p.b_rows = int(b.rows);
-  const bool narrow = 0.55 * shape(128) < shape(256);
-  CUtensorMap ta, tb;
-  if (gtp_status s = map_of(&ta, a, count, A_MN, BMC)) return s;
-  if (gtp_status s = map_of(&tb, b, count, B_MN, narrow ? 64 : 128)) return s;
-  if (narrow) {
-    shape(128);
-    return launch_product<128, A_MN, B_MN, EPI>(ta, tb, p, dev, st);
-  }
-  return launch_product<256, A_MN, B_MN, EPI>(ta, tb, p, dev, st);
+  const int tiles = int(count) * p.each;
+  const auto waves = [&](int units) { return (units + pairs - 1) / pairs; };
+  const int whole = tiles / pairs * pairs;
+  const double all = waves(tiles), tail = whole / pairs + 0.55 * waves(2 * (tiles - whole)), none = 0.55 * waves(2 * tiles);
+  p.full = all <= tail && all <= none ? tiles : tail <= none ? whole : 0;
+  p.units = p.full + 2 * (tiles - p.full);
 }
 
-template <int EPI>
-gtp_status run_update(const Product &p, const Operand &x, const Operand &poly, int64_t count, const Plan &plan,
-                      const gtp::DeviceInfo &dev, cudaStream_t st) {
-  if (p.tall) return run_product<false, false, EPI>(p, x, poly, count, plan.m, dev, st);
-  return run_product<false, true, EPI>(p, poly, x, count, plan.m, dev, st);
+// Matrices of rows x inner fp16, one after another on `stand` rows each.  A box that passes a matrix's last row stays
+// in it or reads the next one's: harmless where rows are the product's rows or columns (nobody takes those), and where
+// they are the contraction they are zeros.
+gtp_status map_of(CUtensorMap *map, const void *base, int64_t inner, int64_t stand, int64_t ld, int64_t count, bool chunk) {
+  return gtp::encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, uint64_t(inner), uint64_t(count * stand),
+                             uint64_t(2 * ld), chunk ? 32 : 64, chunk ? 32 : 64,
+                             chunk ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The iterations, from X in hi[0] and lo to the last product's epilogue.
-template <int EPI>
-gtp_status iterate(Product p, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
+// The iterations, from X in hi[0] and lo to the last product's output.
+template <bool TALL>
+gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
                    const gtp::DeviceInfo &dev, cudaStream_t st) {
+  int pairs = 0;
+  if (gtp_status e = pairs_of<TALL>(dev, &pairs)) return e;
   const int xs = 12, gs = 12;
   const double top2 = double(s.bound) * s.bound, poly_top = std::fabs(s.b) * top2 + std::fabs(s.c) * top2 * top2;
   const int ps = std::min(14, 15 - int(std::ceil(std::log2(std::max(poly_top, 1.0)))));
   const auto pow2 = [](int e) { return std::ldexp(1.f, e); };
-  p.m = int(plan.m), p.tall = rows > cols;
-  p.gram = reinterpret_cast<__half *>(ws + plan.gram), p.gram_lo = reinterpret_cast<__half *>(ws + plan.gram_lo);
-  p.poly = reinterpret_cast<__half *>(ws + plan.poly);
-  p.diag = reinterpret_cast<float *>(ws + plan.diag), p.e = reinterpret_cast<float *>(ws + plan.e);
-  p.lo = reinterpret_cast<__half *>(ws + plan.lo);
-  p.ldg = plan.ldg, p.planeg = plan.planeg, p.ldx = plan.ldx, p.planex = plan.planex;
-  p.gram_scale = pow2(gs), p.gram_inv = pow2(-gs), p.poly_scale = pow2(ps), p.x_scale = pow2(xs), p.x_inv = pow2(-xs);
-  p.a = s.a, p.b = s.b, p.c = s.c;
-  const Operand gram = {ws + plan.gram, plan.m, plan.m, plan.ldg}, poly = {ws + plan.poly, plan.m, plan.m, plan.ldg};
-  for (int k = 0; k < s.steps; ++k) {
-    const Operand x = {ws + plan.hi[k & 1], cols, plan.rows, plan.ldx};
-    p.symmetric = 1, p.m_dim = p.n_dim = int(plan.m);
-    p.alpha = pow2(-2 * xs);
-    if (gtp_status e = p.tall ? run_product<true, true, kGram>(p, x, x, count, rows, dev, st)
-                              : run_product<false, false, kGram>(p, x, x, count, cols, dev, st))
-      return e;
-    p.alpha = pow2(-2 * gs);
-    if (gtp_status e = run_product<false, false, kPoly>(p, gram, gram, count, plan.m, dev, st)) return e;
-    p.symmetric = 0, p.n_fast = p.tall, p.m_dim = int(rows), p.n_dim = int(cols);
-    p.alpha = pow2(-ps - xs), p.early = k < 2;
-    p.hi = reinterpret_cast<const __half *>(x.base), p.hi_out = reinterpret_cast<__half *>(ws + plan.hi[~k & 1]);
-    if (gtp_status e = k + 1 < s.steps ? run_update<kUpdate>(p, x, poly, count, plan, dev, st)
-                                       : run_update<EPI>(p, x, poly, count, plan, dev, st))
-      return e;
+  a.x_scale = pow2(xs), a.x_inv = pow2(-xs), a.gram_scale = pow2(gs), a.gram_inv = pow2(-gs);
+  a.poly_scale = pow2(ps), a.poly_inv = pow2(-ps);
+  a.a = s.a, a.b = s.b, a.c = s.c, a.steps = s.steps, a.m = int(plan.m);
+  a.diag = reinterpret_cast<float *>(ws + plan.diag), a.e = reinterpret_cast<float *>(ws + plan.e);
+  a.arrived = reinterpret_cast<unsigned int *>(ws + plan.arrived);
+  for (int kind = 0; kind < 3; ++kind) {
+    Phase &p = a.phase[kind];
+    const bool update = kind == kUpdate;
+    p.m_dim = int(update ? rows : plan.m), p.n_dim = int(update ? cols : plan.m);
+    p.out_rows = int(update ? plan.rows : plan.grows);
+    p.a_rows = int(kind == kGram || (update && TALL) ? plan.rows : plan.grows);
+    p.b_rows = int(kind == kGram || (update && !TALL) ? plan.rows : plan.grows);
+    shape(p, count, !update, kind == kGram ? plan.n : plan.m, pairs);
   }
-  return GTP_OK;
+  Maps maps;
+  const auto x_map = [&](CUtensorMap *m, int64_t at, bool chunk) {
+    return map_of(m, ws + at, cols, plan.rows, plan.ldx, count, chunk);
+  };
+  const auto g_map = [&](CUtensorMap *m, int64_t at, bool chunk) {
+    return map_of(m, ws + at, plan.m, plan.grows, plan.ldg, count, chunk);
+  };
+  for (const gtp_status e : {x_map(&maps.x[0], plan.hi[0], false), x_map(&maps.x[1], plan.hi[1], false),
+                             g_map(&maps.gram, plan.gram, false), g_map(&maps.poly, plan.poly, false),
+                             x_map(&maps.c_hi[0], plan.hi[0], true), x_map(&maps.c_hi[1], plan.hi[1], true),
+                             x_map(&maps.c_lo, plan.lo, true), g_map(&maps.c_gram, plan.gram, true),
+                             g_map(&maps.c_gram_lo, plan.gram_lo, true), g_map(&maps.c_poly, plan.poly, true)})
+    if (e) return e;
+  const int used = std::min(pairs, std::max({a.phase[0].units, a.phase[1].units, a.phase[2].units}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * unsigned(used));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SMEM_TOTAL;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all of them run at the same time
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, newton_schulz_kernel<TALL>, maps, a);
+  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "orthogonalize: %s", cudaGetErrorString(e));
+  return gtp::check_launch("orthogonalize");
+}
+
+gtp_status iterate(const Args &a, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
+                   const gtp::DeviceInfo &dev, cudaStream_t st) {
+  return rows > cols ? iterate<true>(a, s, plan, ws, count, rows, cols, dev, st)
+                     : iterate<false>(a, s, plan, ws, count, rows, cols, dev, st);
 }
 
 template <typename T, bool VEC, bool STEP>
@@ -885,6 +1087,7 @@ FirstX first_x(const Plan &plan, char *ws) {
   f.part = reinterpret_cast<double *>(ws + plan.part);
   f.hi = reinterpret_cast<__half *>(ws + plan.hi[0]), f.lo = reinterpret_cast<__half *>(ws + plan.lo);
   f.hi_next = reinterpret_cast<__half *>(ws + plan.hi[1]), f.rows = int(plan.rows);
+  f.arrived = reinterpret_cast<unsigned int *>(ws + plan.arrived);
   f.ldx = plan.ldx, f.planex = plan.planex, f.xscale = std::ldexp(1.f, 12);
   return f;
 }
@@ -945,9 +1148,9 @@ extern "C" gtp_status gtp_orthogonalize(const void *src, gtp_dtype src_dt, int64
   source.src = src, source.ld = src_ld, source.plane = src_plane;
   const bool vec = cols % 4 == 0 && aligned(src, 4 * ss) && src_ld % 4 == 0 && src_plane % 4 == 0;
   if (gtp_status s = first<false>(source, src_dt == GTP_F32, vec, first_x(plan, ws), count, rows, cols, dev, st)) return s;
-  Product p = {};
-  p.dst = dst, p.ld = dst_ld, p.plane = dst_plane, p.dst_f32 = dst_dt == GTP_F32;
-  return iterate<kOut>(p, schedule, plan, ws, count, rows, cols, dev, st);
+  Args a = {};
+  a.dst = dst, a.ld = dst_ld, a.plane = dst_plane, a.dst_f32 = dst_dt == GTP_F32;
+  return iterate(a, schedule, plan, ws, count, rows, cols, dev, st);
 }
 
 extern "C" gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *momentum, float *master, void *param_data,
@@ -999,11 +1202,11 @@ extern "C" gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *m
   Source source = {};
   source.grad = grad_data, source.momentum = momentum, source.grad_scale = h->grad_scale;
   source.mu = h->momentum, source.factor = h->grad_factor, source.nesterov = h->nesterov, source.zero_grad = h->zero_grad_after;
-  Product p = {};
-  p.master = master, p.param = static_cast<__nv_bfloat16 *>(param_data);
-  p.keep = float(1.0 - double(h->lr) * double(h->weight_decay)), p.rate = float(double(h->lr) * double(h->scale));
-  for (int64_t k = 0; k < count; ++k) source.offset[k] = p.offset[k] = offsets[k];
+  Args a = {};
+  a.step = 1, a.master = master, a.param = static_cast<__nv_bfloat16 *>(param_data);
+  a.keep = float(1.0 - double(h->lr) * double(h->weight_decay)), a.rate = float(double(h->lr) * double(h->scale));
+  for (int64_t k = 0; k < count; ++k) source.offset[k] = a.offset[k] = offsets[k];
   vec = vec && aligned(grad_data, 4 * gs) && aligned(momentum, 16);
   if (gtp_status s = first<true>(source, grad_dt == GTP_F32, vec, first_x(plan, ws), count, rows, cols, dev, st)) return s;
-  return iterate<kStep>(p, schedule, plan, ws, count, rows, cols, dev, st);
+  return iterate(a, schedule, plan, ws, count, rows, cols, dev, st);
 }
