@@ -246,6 +246,7 @@ struct Maps {
   CUtensorMap x[2], gram, poly;                                   // operands: 64 x 64 boxes
   CUtensorMap c_hi[2], c_lo, c_gram, c_gram_lo, c_poly;           // 32 x 32 chunks
 };
+static_assert(sizeof(Maps) == 10 * sizeof(CUtensorMap), "prefetched one by one");
 
 struct Args {
   Phase phase[3];
@@ -321,7 +322,7 @@ __device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
 __device__ __forceinline__ void add_release(unsigned int *p) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Waits until this CTA may start `phase` (warp 3 says so); false when the CTA gives up.
@@ -493,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     finished = 0;
     fence_barrier_init();
   }
+  if (warp == 0 && lane < 10) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 2 * BN);
     tmem_relinquish_pair();
@@ -515,12 +517,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
         const Phase &p = a.phase[kind];
         if (first >= p.units) continue;
-        if (!wait_ready(ready, ph, abort_flag, err)) break;
-        fence_proxy_async();
         const CUtensorMap *x = &maps.x[(ph / 3) & 1];
         const bool mn = kind == kGram ? TALL : kind == kUpdate && !is_a && !TALL;  // rows of the box run along K
         const CUtensorMap *map = kind == kGram ? x : kind == kPoly ? &maps.gram : is_a == TALL ? x : &maps.poly;
         const int rows = is_a ? p.a_rows : p.b_rows;
+        bool waited = false;
         for (int u = first; ok && u < p.units; u += step) {
           int k, row, col;
           bool half;
@@ -528,6 +529,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // this CTA's 128 rows of A, 128 or 64 of B
           const int i0 = is_a ? row + BMC * int(rank) : col + (half ? 64 : 128) * int(rank);
           const int boxes = is_a || !half ? 2 : 1;
+          if (!waited && !(ok = wait_ready(ready, ph, abort_flag, err))) break;
+          waited = true;
           for (int kb = 0; kb < p.k_blocks; ++kb) {
             if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) {
               ok = false;
@@ -629,7 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           *abort_flag = 1;
           break;
         }
-        fence_proxy_async();
+        // what the other CTAs' copies wrote, before this CTA's copies read it
+        fence_proxy_async_global();
         __threadfence_block();
         *ready = ph;
       }
@@ -652,7 +656,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) r = wait_ready(ready, ph, abort_flag, err);
         ok = __all_sync(0xFFFFFFFFu, r);
         if (!ok) break;
-        if (lane == 0) fence_proxy_async();
       }
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
@@ -791,6 +794,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               load_row(buf + PART, lane, l);
             }
             const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
+            const int diagonal = me - at;  // this lane's diagonal element, where the chunk holds it
+            float at_diagonal = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               float out[2];
@@ -798,14 +803,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const float s = __uint_as_float(r[j + i]) * alpha;
-                const bool on_diagonal = at + j + i == me;
                 if (kind == kGram) {
-                  if (on_diagonal && me < a.m) a.diag[int64_t(k) * a.m + me] = s;
-                  out[i] = on_diagonal ? 0.f : s * a.gram_scale;
+                  out[i] = s * a.gram_scale;
                 } else {
-                  if (on_diagonal && me < a.m) a.e[int64_t(k) * a.m + me] = fmaf(a.c, fmaf(own, own, s), fmaf(a.b, own, a.a));
                   const float g = (i ? hi.y + lo.y : hi.x + lo.x) * a.gram_inv;
-                  out[i] = on_diagonal ? 0.f : (a.b * g + a.c * fmaf(own + v[j + i], g, s)) * a.poly_scale;
+                  out[i] = (a.b * g + a.c * fmaf(own + v[j + i], g, s)) * a.poly_scale;
+                }
+                if (j + i == diagonal) {
+                  at_diagonal = s;
+                  out[i] = 0.f;
                 }
               }
               w[j >> 1] = pack2(out[0], out[1]);
@@ -813,6 +819,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float2 high = unpack2(w[j >> 1]);
                 l[j >> 1] = pack2(out[0] - high.x, out[1] - high.y);
               }
+            }
+            if (diagonal >= 0 && diagonal < 32 && me < a.m) {
+              if (kind == kGram) a.diag[int64_t(k) * a.m + me] = at_diagonal;
+              else a.e[int64_t(k) * a.m + me] = fmaf(a.c, fmaf(own, own, at_diagonal), fmaf(a.b, own, a.a));
             }
             // the chunk, its low part (A'; where the next phase's own tiles are), and its mirror image where no tile
             // computes it
@@ -845,14 +855,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok || last) break;
-      // this CTA's part of the phase is in memory: copies out have been written, d and e by every lane
+      // This warp's part of the phase is in memory: its copies out have been written, d and e by its lanes before the
+      // warp's barrier.  The last of the warps releases what it and, through `finished`, the others have written.
       if (lane == 0) bulk_wait_all();
-      fence_proxy_async();
-      __threadfence();
       __syncwarp();
-      if (lane == 0 && (atomicAdd(&finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {  // the last of the warps
-        __threadfence();
-        add_release(&a.arrived[ph]);
+      if (lane == 0) {
+        __threadfence_block();
+        if ((atomicAdd(&finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
+          __threadfence_block();
+          add_release(&a.arrived[ph]);
+        }
       }
     }
     if (!ok) *abort_flag = 1;
