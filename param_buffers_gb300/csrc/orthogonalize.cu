@@ -224,10 +224,10 @@ __global__ void __launch_bounds__(kPassThreads)
 // staging slot one chunk ahead, and the new ones leave through the same slot.
 constexpr int BK = 64, UK = 16, BMC = 128, BMP = 256, BN = 256;
 constexpr int BOX = 64 * 64 * 2;  // one tensor copy: 64 rows of 128 bytes, either majorness
-constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 5;
+constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 4;
 constexpr int kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART;  // a chunk of fp16; high and low part of one
-constexpr int SMEM_OPS = STAGES * STAGE, SMEM_SLOTS = kEpilogueWarps * 2 * SLOT;
+constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART, SLOTS = 3;  // a chunk of fp16; high and low part of one; a warp's
+constexpr int SMEM_OPS = STAGES * STAGE, SMEM_SLOTS = kEpilogueWarps * SLOTS * SLOT;
 constexpr int SMEM_VEC = kEpilogueWarps * 32 * 4 + 16, SMEM_CTRL = 512;
 // dynamic shared memory is on 1024 bytes only after an offset of up to 1008
 constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SLOTS + SMEM_CTRL + 1024;
@@ -351,105 +351,83 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// A lane's row of a 32 x 32 chunk of fp16 in a slot, in the copies' 64-byte swizzle: 16-byte piece j of row r at
-// j ^ (r / 2 % 4).
-__device__ __forceinline__ void load_row(const uint8_t *part, int lane, uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(part + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
-}
-__device__ __forceinline__ void store_row(uint8_t *part, int lane, const uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4 *>(part + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-}
-// The same chunk transposed: this lane's row becomes column `lane`.
-__device__ __forceinline__ void store_column(uint8_t *part, int lane, const uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    *reinterpret_cast<uint16_t *>(part + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + 2 * (lane & 7)) =
-        uint16_t(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
+// 32 lanes x 8 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
-// The last product's values of a chunk (x, true values, this lane's row), through the slot so that a warp writes whole
-// row segments: eight lanes a row of 32, four values a lane.
-__device__ __forceinline__ void write_out(const Args &a, const Phase &p, uint8_t *slot, int lane, int k, int row0, int col,
-                                          const float (&x)[32]) {
+// A 32 x 32 chunk of fp16 lies as the copies' 64-byte swizzle has it: the 16-byte piece j (eight columns) of row r at
+// r * 64 + 16 (j ^ (r / 2 % 4)).
+__device__ __forceinline__ int piece_at(int row, int j) { return row * 64 + ((j ^ ((row >> 1) & 3)) << 4); }
+
+// The chunk in `from` transposed into `to`: this lane's row becomes column `lane`.
+__device__ __forceinline__ void transpose_chunk(const uint8_t *from, uint8_t *to, int lane) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(from + piece_at(lane, j));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<float4 *>(slot + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-  __syncwarp();
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint16_t *>(to + piece_at(8 * j + i, lane >> 3) + 2 * (lane & 7)) =
+          uint16_t(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+  }
+}
+
+// The last product's values of a chunk, true values in fp32 at `staged` (row r's 16-byte piece j at r * 128 + 16 (j ^ r
+// % 8)), out in whole row segments: eight lanes a row of 32, four values a lane.
+__device__ __forceinline__ void write_out(const Args &a, const Phase &p, const uint8_t *staged, int lane, int k, int row0,
+                                          int col) {
   const int j = lane & 7, c = col + 4 * j;
   const int n = min(4, p.n_dim - c);
-  if (!a.step) {
+  if (n <= 0) return;
+  const int64_t ld = a.step ? p.n_dim : a.ld;
+  const int64_t base = (a.step ? a.offset[k] : k * a.plane) + (row0 + (lane >> 3)) * ld + c;
+  const bool in4 = n == 4 && ld % 4 == 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8; i0 += 4) {
+    float4 m[4];
+    if (a.step) {
+      const bool wide = in4 && (reinterpret_cast<uintptr_t>(a.master + base) & 15) == 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3), row = row0 + r;
-      const float4 v = *reinterpret_cast<const float4 *>(slot + r * 128 + ((j ^ (r & 7)) << 4));
-      if (row >= p.m_dim || n <= 0) continue;
+      for (int i = 0; i < 4; ++i) {
+        const float *const o = a.master + base + 4 * (i0 + i) * ld;
+        if (row0 + 4 * (i0 + i) + (lane >> 3) >= p.m_dim) continue;
+        if (wide) m[i] = *reinterpret_cast<const float4 *>(o);
+        else m[i] = make_float4(o[0], n > 1 ? o[1] : 0.f, n > 2 ? o[2] : 0.f, n > 3 ? o[3] : 0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * (i0 + i) + (lane >> 3);
+      if (row0 + r >= p.m_dim) continue;
+      const int64_t at = base + 4 * (i0 + i) * ld;
+      float4 v = *reinterpret_cast<const float4 *>(staged + r * 128 + ((j ^ (r & 7)) << 4));
+      if (a.step)
+        v = make_float4(fmaf(a.keep, m[i].x, -a.rate * v.x), fmaf(a.keep, m[i].y, -a.rate * v.y),
+                        fmaf(a.keep, m[i].z, -a.rate * v.z), fmaf(a.keep, m[i].w, -a.rate * v.w));
       const float y[4] = {v.x, v.y, v.z, v.w};
-      const int64_t at = k * a.plane + row * a.ld + c;
-      if (a.dst_f32) {
-        float *const o = static_cast<float *>(a.dst) + at;
-        if (n == 4 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+      float *const o = a.step ? a.master + at : a.dst_f32 ? static_cast<float *>(a.dst) + at : nullptr;
+      if (o) {
+        if (in4 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
           *reinterpret_cast<float4 *>(o) = v;
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (q < n) o[q] = y[q];
         }
-      } else {
-        __nv_bfloat16 *const o = static_cast<__nv_bfloat16 *>(a.dst) + at;
-        if (n == 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+      }
+      __nv_bfloat16 *const b = a.step ? (a.param ? a.param + at : nullptr)
+                                      : a.dst_f32 ? nullptr : static_cast<__nv_bfloat16 *>(a.dst) + at;
+      if (b) {
+        if (in4 && (reinterpret_cast<uintptr_t>(b) & 7) == 0) {
           const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
-          *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(w);
+          *reinterpret_cast<uint2 *>(b) = *reinterpret_cast<const uint2 *>(w);
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (q < n) o[q] = __float2bfloat16_rn(y[q]);
-        }
-      }
-    }
-  } else {
-    const int64_t base = a.offset[k] + int64_t(row0 + (lane >> 3)) * p.n_dim + c;
-    const int64_t step = 4 * int64_t(p.n_dim);
-    const bool wide = n == 4 && p.n_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(a.master + base) & 15) == 0;
-    float4 m[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (row0 + 4 * i + (lane >> 3) >= p.m_dim || n <= 0) continue;
-      const float *const o = a.master + base + i * step;
-      if (wide) m[i] = *reinterpret_cast<const float4 *>(o);
-      else m[i] = make_float4(o[0], n > 1 ? o[1] : 0.f, n > 2 ? o[2] : 0.f, n > 3 ? o[3] : 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      const float4 v = *reinterpret_cast<const float4 *>(slot + r * 128 + ((j ^ (r & 7)) << 4));
-      if (row0 + r >= p.m_dim || n <= 0) continue;
-      const float y[4] = {fmaf(a.keep, m[i].x, -a.rate * v.x), fmaf(a.keep, m[i].y, -a.rate * v.y),
-                          fmaf(a.keep, m[i].z, -a.rate * v.z), fmaf(a.keep, m[i].w, -a.rate * v.w)};
-      float *const o = a.master + base + i * step;
-      if (wide) {
-        *reinterpret_cast<float4 *>(o) = make_float4(y[0], y[1], y[2], y[3]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < n) o[q] = y[q];
-      }
-      if (a.param) {
-        __nv_bfloat16 *const w = a.param + base + i * step;
-        if (wide && (reinterpret_cast<uintptr_t>(w) & 7) == 0) {
-          const __nv_bfloat162 b[2] = {__floats2bfloat162_rn(y[0], y[1]), __floats2bfloat162_rn(y[2], y[3])};
-          *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(b);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < n) w[q] = __float2bfloat16_rn(y[q]);
+            if (q < n) b[q] = __float2bfloat16_rn(y[q]);
         }
       }
     }
@@ -470,10 +448,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *tempty = tfull + 2;
   uint64_t *drained = tempty + 2;
   uint64_t *cfull = drained + 1;  // [warp][slot]: a chunk's old values have landed
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + 2 * kEpilogueWarps);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + SLOTS * kEpilogueWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *ready = abort_flag + 1;
-  static_assert((2 * STAGES + 5 + 2 * kEpilogueWarps) * 8 + 12 <= SMEM_CTRL, "control block");
+  static_assert((2 * STAGES + 5 + SLOTS * kEpilogueWarps) * 8 + 12 <= SMEM_CTRL, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -488,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[i], 2 * kEpilogueWarps);
     }
     mbar_init(drained, 1);
-    for (int i = 0; i < 2 * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
+    for (int i = 0; i < SLOTS * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
     *abort_flag = 0;
     *ready = 0;
     finished = 0;
@@ -640,10 +618,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {  // -------------------------------------------------------------- finishing the tiles (both CTAs)
     const int ew = warp - 4, quarter = warp & 3, side = ew >> 2;
-    uint8_t *const mine = slots + ew * 2 * SLOT;
-    uint64_t *const cbar = cfull + 2 * ew;
+    uint8_t *const mine = slots + ew * SLOTS * SLOT;
+    uint64_t *const cbar = cfull + SLOTS * ew;
     float *const v = vec[ew];
-    int acc = 0, slot = 0;
+    int acc = 0, slot = 0, set = 0;        // set: which half of the slots a chunk of A' leaves by
     uint32_t acc_parity = 0, cparity = 0;  // bit s: the parity that slot s's next copy completes
     int flying = 0;                        // bit s: a copy into slot s that nobody has waited for
     bool ok = true;
@@ -659,7 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
-      // The chunk behind (u, c): fetched into the other slot while this one is worked on.
+      // Old values of a chunk into slot s.  The next chunk's go into the next slot while this one is worked on, which the
+      // chunk before the last one left: all stores but the latest have read their slots.
       const auto fetch = [&](int s, int k, int row0, int col) {  // lane 0
         mbar_arrive_expect_tx(&cbar[s], 2 * PART);
         tma_load_2d(from_hi, &cbar[s], mine + s * SLOT, col, k * p.out_rows + row0);
@@ -675,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row0 = row + BMC * int(rank) + 32 * quarter, c0 = col + side * wide, me = row0 + lane;
         if (kind != kGram && !fetched && exists(row0, c0)) {
           if (lane == 0) {
-            bulk_wait_group_read<0>();
+            bulk_wait_group_read<1>();
             fetch(slot, k, row0, c0);
           }
           flying |= 1 << slot;
@@ -702,9 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < wide; c += 32) {
           const int at = c0 + c;
           if (!exists(row0, at)) break;
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(base + uint32_t(c), r);
-          uint8_t *const buf = mine + slot * SLOT, *const other = mine + (slot ^ 1) * SLOT;
+          const int next = slot == SLOTS - 1 ? 0 : slot + 1;
           if (kind != kGram) {
             // the coming chunk: the next of this unit, or the next unit's first
             int nk = k, nrow = row0, ncol = at + 32;
@@ -715,135 +692,134 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!decode<TALL>(p, kind, nu, nk, rr, cc, hh)) continue;
               nrow = rr + BMC * int(rank) + 32 * quarter, ncol = cc + side * (hh ? BN / 4 : BN / 2);
               more = exists(nrow, ncol);
-              break;  // a unit without a chunk for this warp starts its own fetch after it
+              break;  // a unit without a chunk for this warp: the one after it starts its own fetch
             }
             if (more) {
               if (lane == 0) {
-                bulk_wait_group_read<0>();  // the other slot's store has read it
-                fetch(slot ^ 1, nk, nrow, ncol);
+                bulk_wait_group_read<1>();
+                fetch(next, nk, nrow, ncol);
               }
-              flying |= 1 << (slot ^ 1);
+              flying |= 1 << next;
             }
             fetched = more;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u))) {
-              tmem_ld_wait();
               ok = false;
               break;
             }
             cparity ^= 1u << slot;
             flying &= ~(1 << slot);
             v[lane] = c == 0 ? t[0] : c == 32 ? t[1] : c == 64 ? t[2] : t[3];
-            __syncwarp();
-          } else {
-            if (lane == 0) bulk_wait_group_read<0>();  // both slots' stores have read them
-            __syncwarp();
+          } else if (lane == 0) {
+            bulk_wait_group_read<1>();  // the chunk before the last has left this half of the slots
           }
-          tmem_ld_wait();
-          if (kind == kUpdate) {
-            uint32_t h[16], l[16];
-            load_row(buf, lane, h);
-            load_row(buf + PART, lane, l);
-            float x[32];
-            const float alpha = a.poly_inv * a.x_inv;
+          __syncwarp();
+          uint8_t *const hi_part = mine + (kind == kGram ? set * 3 * PART : slot * SLOT), *const lo_part = hi_part + PART;
+          uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
+          const int diagonal = me - at;  // this lane's diagonal element, where the chunk holds it
+          float at_diagonal = 0.f;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {  // eight columns at a time: the code of a phase stays small
+            uint32_t r[8];
+            tmem_ld_32x32b_x8(base + uint32_t(c + 8 * j), r);
+            const int piece = piece_at(lane, j);
+            uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
+            float cols[8];
+            if (kind != kGram) {
+              const uint4 hv = *reinterpret_cast<const uint4 *>(hi_part + piece), lv = *reinterpret_cast<const uint4 *>(lo_part + piece);
+              h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
+              l[0] = lv.x, l[1] = lv.y, l[2] = lv.z, l[3] = lv.w;
+              const float4 c0 = *reinterpret_cast<const float4 *>(&v[8 * j]), c1 = *reinterpret_cast<const float4 *>(&v[8 * j + 4]);
+              cols[0] = c0.x, cols[1] = c0.y, cols[2] = c0.z, cols[3] = c0.w;
+              cols[4] = c1.x, cols[5] = c1.y, cols[6] = c1.z, cols[7] = c1.w;
+            }
+            tmem_ld_wait();
+            float x[8];
+            if (kind == kUpdate) {
+              const float alpha = a.poly_inv * a.x_inv;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float e[4] = {own, own, own, own};
-              if (TALL) {
-                const float4 t = *reinterpret_cast<const float4 *>(&v[j]);
-                e[0] = t.x, e[1] = t.y, e[2] = t.z, e[3] = t.w;
+              for (int i = 0; i < 8; ++i) {
+                const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
+                const float hx = i & 1 ? hf.y : hf.x, lx = i & 1 ? lf.y : lf.x, e = TALL ? cols[i] : own;
+                // x_inv times the stored X, alpha times the accumulator: true values
+                x[i] = fmaf(early ? fmaf(e, hx, a.a * lx) : e * (hx + lx), a.x_inv, __uint_as_float(r[i]) * alpha);
+              }
+              if (last) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  *reinterpret_cast<float4 *>(const_cast<uint8_t *>(staged) + lane * 128 + (((2 * j + i) ^ (lane & 7)) << 4)) =
+                      make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                continue;
               }
 #pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                const float2 hi = unpack2(h[(j + i) >> 1]), lo = unpack2(l[(j + i) >> 1]);
-                // x_inv times the stored X, alpha times the accumulator: true values
-                const float x0 = early ? fmaf(e[i], hi.x, a.a * lo.x) : e[i] * (hi.x + lo.x);
-                const float x1 = early ? fmaf(e[i + 1], hi.y, a.a * lo.y) : e[i + 1] * (hi.y + lo.y);
-                x[j + i] = fmaf(x0, a.x_inv, __uint_as_float(r[j + i]) * alpha);
-                x[j + i + 1] = fmaf(x1, a.x_inv, __uint_as_float(r[j + i + 1]) * alpha);
+              for (int i = 0; i < 8; ++i) x[i] = me < p.m_dim ? x[i] * a.x_scale : 0.f;  // rows that fill the last block stay zero
+            } else {
+              const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float s = __uint_as_float(r[i]) * alpha;
+                if (kind == kGram) {
+                  x[i] = s * a.gram_scale;
+                } else {
+                  const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
+                  const float g = (i & 1 ? hf.y + lf.y : hf.x + lf.x) * a.gram_inv;
+                  x[i] = (a.b * g + a.c * fmaf(own + cols[i], g, s)) * a.poly_scale;
+                }
+                if (8 * j + i == diagonal) {
+                  at_diagonal = s;
+                  x[i] = 0.f;
+                }
               }
             }
-            if (!last) {
-              const bool inside = me < p.m_dim;  // the rows that fill a contraction's last block stay zero
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float x0 = inside ? x[j] * a.x_scale : 0.f, x1 = inside ? x[j + 1] * a.x_scale : 0.f;
-                h[j >> 1] = pack2(x0, x1);
-                const float2 t = unpack2(h[j >> 1]);
-                l[j >> 1] = pack2(x0 - t.x, x1 - t.y);
-              }
-              store_row(buf, lane, h);
-              store_row(buf + PART, lane, l);
+            for (int i = 0; i < 4; ++i) {
+              h[i] = pack2(x[2 * i], x[2 * i + 1]);
+              const float2 t = unpack2(h[i]);
+              l[i] = pack2(x[2 * i] - t.x, x[2 * i + 1] - t.y);
+            }
+            *reinterpret_cast<uint4 *>(hi_part + piece) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (kind != kPoly) *reinterpret_cast<uint4 *>(lo_part + piece) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+          const int to = k * p.out_rows + row0;
+          if (kind == kUpdate) {
+            if (!last) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                const int to = k * p.out_rows + row0;
-                tma_store_2d(&maps.c_hi[~(ph / 3) & 1], buf, at, to);
-                tma_store_2d(&maps.c_lo, buf + PART, at, to);
+                tma_store_2d(&maps.c_hi[~(ph / 3) & 1], hi_part, at, to);
+                tma_store_2d(&maps.c_lo, lo_part, at, to);
                 bulk_commit_group();
               }
             } else {
-              __syncwarp();  // every lane has read its row of the slot
-              write_out(a, p, buf, lane, k, row0, at, x);
-              fence_proxy_async_smem();
-              __syncwarp();  // and the slot's values, before a copy overwrites them
+              __syncwarp();
+              write_out(a, p, staged, lane, k, row0, at);
+              fence_proxy_async_smem();  // before a copy lands where this was
+              __syncwarp();
             }
           } else {
-            uint32_t w[16], l[16];
-            if (kind == kPoly) {
-              load_row(buf, lane, w);
-              load_row(buf + PART, lane, l);
-            }
-            const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
-            const int diagonal = me - at;  // this lane's diagonal element, where the chunk holds it
-            float at_diagonal = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float out[2];
-              const float2 hi = unpack2(w[j >> 1]), lo = unpack2(l[j >> 1]);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float s = __uint_as_float(r[j + i]) * alpha;
-                if (kind == kGram) {
-                  out[i] = s * a.gram_scale;
-                } else {
-                  const float g = (i ? hi.y + lo.y : hi.x + lo.x) * a.gram_inv;
-                  out[i] = (a.b * g + a.c * fmaf(own + v[j + i], g, s)) * a.poly_scale;
-                }
-                if (j + i == diagonal) {
-                  at_diagonal = s;
-                  out[i] = 0.f;
-                }
-              }
-              w[j >> 1] = pack2(out[0], out[1]);
-              if (kind == kGram) {
-                const float2 high = unpack2(w[j >> 1]);
-                l[j >> 1] = pack2(out[0] - high.x, out[1] - high.y);
-              }
-            }
             if (diagonal >= 0 && diagonal < 32 && me < a.m) {
               if (kind == kGram) a.diag[int64_t(k) * a.m + me] = at_diagonal;
               else a.e[int64_t(k) * a.m + me] = fmaf(a.c, fmaf(own, own, at_diagonal), fmaf(a.b, own, a.a));
             }
             // the chunk, its low part (A'; where the next phase's own tiles are), and its mirror image where no tile
-            // computes it
+            // computes it: B' leaves that where the low part of A' was
             const bool mirror = at / BMP > row0 / BMP;
-            uint8_t *const image = kind == kGram ? other : buf + PART;
-            store_row(buf, lane, w);
-            if (kind == kGram) store_row(buf + PART, lane, l);
-            __syncwarp();  // kPoly: the image lies where the low part was read
-            if (mirror) store_column(image, lane, w);
+            uint8_t *const image = kind == kGram ? lo_part + PART : lo_part;
+            if (mirror) {
+              __syncwarp();  // every lane has read its low part
+              transpose_chunk(hi_part, image, lane);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              const int to = k * p.out_rows + row0, across = k * p.out_rows + at;
               const CUtensorMap *const out = kind == kGram ? &maps.c_gram : &maps.c_poly;
-              tma_store_2d(out, buf, at, to);
-              if (kind == kGram) tma_store_2d(&maps.c_gram_lo, buf + PART, at, to);
-              if (mirror) tma_store_2d(out, image, row0, across);
+              tma_store_2d(out, hi_part, at, to);
+              if (kind == kGram) tma_store_2d(&maps.c_gram_lo, lo_part, at, to);
+              if (mirror) tma_store_2d(out, image, row0, k * p.out_rows + at);
               bulk_commit_group();
             }
           }
-          if (kind != kGram) slot ^= 1;
+          if (kind == kGram) set ^= 1;
+          else slot = next;
         }
         if (!ok) break;
         tc_fence_before();
@@ -870,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok) *abort_flag = 1;
     if (lane == 0) {
       bulk_wait_group_read<0>();  // the slots outlive the stores' reads of them
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < SLOTS; ++s)
         if (flying >> s & 1) drain(&cbar[s], (cparity >> s) & 1u);
     }
   }
