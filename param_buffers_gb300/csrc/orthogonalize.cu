@@ -36,6 +36,7 @@
 #include "device.h"
 #include "fastdiv.cuh"
 #include "sm100_ptx.cuh"
+#include "smem_base.h"
 #include "tensor_map.h"
 
 namespace gtp {
@@ -48,7 +49,9 @@ using namespace gtp::ptx;
 
 __device__ unsigned int g_ortho_wait_timeouts;  // this unit's part of gtp_wait_timeouts' word
 
-constexpr int kMostMatrices = 64, kMostSteps = 16, kMostPhases = 3 * kMostSteps;
+constexpr int kMostMatrices = 64, kMostSteps = 16;
+constexpr int kCounters = kMostMatrices * kMostSteps;  // of a launch's CTAs: one a phase, or one a matrix and iteration
+static_assert(3 * kMostSteps <= kCounters, "");
 
 // --------------------------------------------------------------------------- the norm, the momentum, the first X
 
@@ -182,7 +185,8 @@ __global__ void __launch_bounds__(kPassThreads)
   for (int p = threadIdx.x; p < f.parts; p += kPassThreads) total += f.part[blockIdx.y * f.parts + p];
   total = block_sum(total);
   const float r = total == 0 ? 0.f : isfinite(total) ? float(double(f.xscale) / sqrt(total)) : nanf("");
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kMostPhases) f.arrived[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < kCounters; i += kPassThreads) f.arrived[i] = 0;
   const int step = int(gridDim.x) * kPassThreads, me = int(blockIdx.x) * kPassThreads + int(threadIdx.x);
   const int64_t zeros = (f.rows - s.rows) * f.ldx / 8;  // in both buffers that take turns as the products' X
   for (int64_t i = me; i < zeros; i += step) {
@@ -228,10 +232,9 @@ constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 4;
 constexpr int kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART, SLOTS = 3;  // a chunk of fp16; high and low part of one; a warp's
 constexpr int SMEM_OPS = STAGES * STAGE, SMEM_SLOTS = kEpilogueWarps * SLOTS * SLOT;
-constexpr int SMEM_VEC = kEpilogueWarps * 32 * 4 + 16, SMEM_CTRL = 512;
-// dynamic shared memory is on 1024 bytes only after an offset of up to 1008
-constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SLOTS + SMEM_CTRL + 1024;
-static_assert(SMEM_TOTAL + SMEM_VEC <= 232448, "shared memory per block");
+constexpr int SMEM_VEC = kEpilogueWarps * 32 * 4, SMEM_CTRL = 512;
+constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SLOTS + SMEM_VEC + SMEM_CTRL;
+static_assert(SMEM_TOTAL <= 232448, "shared memory per block");
 
 enum Kind { kGram, kPoly, kUpdate };
 
@@ -351,11 +354,14 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// 32 lanes x 8 consecutive 32-bit columns of tensor memory.
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+// 32 lanes x 16 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 // A 32 x 32 chunk of fp16 lies as the copies' 64-byte swizzle has it: the 16-byte piece j (eight columns) of row r at
@@ -377,12 +383,12 @@ __device__ __forceinline__ void transpose_chunk(const uint8_t *from, uint8_t *to
 
 // The last product's values of a chunk, true values in fp32 at `staged` (row r's 16-byte piece j at r * 128 + 16 (j ^ r
 // % 8)), out in whole row segments: eight lanes a row of 32, four values a lane.
-__device__ __forceinline__ void write_out(const Args &a, const Phase &p, const uint8_t *staged, int lane, int k, int row0,
-                                          int col) {
+__device__ __forceinline__ void write_out(const Args &a, int m_dim, int n_dim, const uint8_t *staged, int lane, int k,
+                                          int row0, int col) {
   const int j = lane & 7, c = col + 4 * j;
-  const int n = min(4, p.n_dim - c);
+  const int n = min(4, n_dim - c);
   if (n <= 0) return;
-  const int64_t ld = a.step ? p.n_dim : a.ld;
+  const int64_t ld = a.step ? n_dim : a.ld;
   const int64_t base = (a.step ? a.offset[k] : k * a.plane) + (row0 + (lane >> 3)) * ld + c;
   const bool in4 = n == 4 && ld % 4 == 0;
 #pragma unroll 1
@@ -393,7 +399,7 @@ __device__ __forceinline__ void write_out(const Args &a, const Phase &p, const u
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float *const o = a.master + base + 4 * (i0 + i) * ld;
-        if (row0 + 4 * (i0 + i) + (lane >> 3) >= p.m_dim) continue;
+        if (row0 + 4 * (i0 + i) + (lane >> 3) >= m_dim) continue;
         if (wide) m[i] = *reinterpret_cast<const float4 *>(o);
         else m[i] = make_float4(o[0], n > 1 ? o[1] : 0.f, n > 2 ? o[2] : 0.f, n > 3 ? o[3] : 0.f);
       }
@@ -401,7 +407,7 @@ __device__ __forceinline__ void write_out(const Args &a, const Phase &p, const u
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * (i0 + i) + (lane >> 3);
-      if (row0 + r >= p.m_dim) continue;
+      if (row0 + r >= m_dim) continue;
       const int64_t at = base + 4 * (i0 + i) * ld;
       float4 v = *reinterpret_cast<const float4 *>(staged + r * 128 + ((j ^ (r & 7)) << 4));
       if (a.step)
@@ -434,15 +440,97 @@ __device__ __forceinline__ void write_out(const Args &a, const Phase &p, const u
   }
 }
 
+// A chunk of the update, from the accumulator at `taddr` and the old X in hi and lo: the new X in their place, or (last)
+// true values in `staged`.  v: e of the chunk's columns (TALL), own: e of this lane's row; inside: that row exists (rows
+// that fill a contraction's last block stay zero).  Sixteen columns at a time: the code of a phase stays small.
+template <bool TALL>
+__device__ __forceinline__ void update_chunk(const Args &a, uint32_t taddr, uint8_t *hi, uint8_t *lo, uint8_t *staged,
+                                             const float *v, float own, bool inside, bool early, bool last, int lane) {
+  const float alpha = a.poly_inv * a.x_inv;
+#pragma unroll 1
+  for (int j = 0; j < 4; j += 2) {
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(taddr + uint32_t(8 * j), r);
+    uint4 h4[2], l4[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      h4[q] = *reinterpret_cast<const uint4 *>(hi + piece_at(lane, j + q));
+      l4[q] = *reinterpret_cast<const uint4 *>(lo + piece_at(lane, j + q));
+    }
+    float e[TALL ? 16 : 1];
+    if (TALL) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = *reinterpret_cast<const float4 *>(&v[8 * j + 4 * q]);
+        e[4 * q] = f.x, e[4 * q + 1] = f.y, e[4 * q + 2] = f.z, e[4 * q + 3] = f.w;
+      }
+    } else {
+      e[0] = own;
+    }
+    tmem_ld_wait();
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t h[4] = {h4[q].x, h4[q].y, h4[q].z, h4[q].w}, l[4] = {l4[q].x, l4[q].y, l4[q].z, l4[q].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
+        const float hx = i & 1 ? hf.y : hf.x, lx = i & 1 ? lf.y : lf.x, f = TALL ? e[8 * q + i] : e[0];
+        // x_inv times the stored X, alpha times the accumulator: true values
+        x[8 * q + i] = fmaf(early ? fmaf(f, hx, a.a * lx) : f * (hx + lx), a.x_inv, __uint_as_float(r[8 * q + i]) * alpha);
+      }
+    }
+    if (last) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(staged + lane * 128 + (((2 * j + i) ^ (lane & 7)) << 4)) =
+            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      continue;
+    }
+    const float scale = inside ? a.x_scale : 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = inside ? x[8 * q + 2 * i] * scale : 0.f, x1 = inside ? x[8 * q + 2 * i + 1] * scale : 0.f;
+        h[i] = pack2(x0, x1);
+        const float2 f = unpack2(h[i]);
+        l[i] = pack2(x0 - f.x, x1 - f.y);
+      }
+      *reinterpret_cast<uint4 *>(hi + piece_at(lane, j + q)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4 *>(lo + piece_at(lane, j + q)) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+}
+
+// The same chunk on its way: a copy of both parts to X's next buffers, or the result written out.  The whole warp.
+__device__ __forceinline__ void send_chunk(const Args &a, const CUtensorMap *to_hi, const CUtensorMap *to_lo, uint8_t *hi,
+                                           uint8_t *lo, const uint8_t *staged, bool last, int lane, int k, int m_dim, int n_dim,
+                                           int stand, int row0, int col) {
+  if (!last) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(to_hi, hi, col, k * stand + row0);
+      tma_store_2d(to_lo, lo, col, k * stand + row0);
+      bulk_commit_group();
+    }
+  } else {
+    __syncwarp();
+    write_out(a, m_dim, n_dim, staged, lane, k, row0, col);
+    fence_proxy_async_smem();  // before a copy lands where this was
+    __syncwarp();
+  }
+}
+
 template <bool TALL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     newton_schulz_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int finished;  // warps that have finished their part of a phase, over all phases
-  __shared__ __align__(16) float vec[kEpilogueWarps][32];  // d or e of a chunk's columns
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sA = smem, *sB = smem + STAGES * A_STAGE, *slots = smem + SMEM_OPS;
-  uint64_t *full = reinterpret_cast<uint64_t *>(slots + SMEM_SLOTS);
+  extern __shared__ __align__(1024) uint8_t smem_at_1024[];  // the host checks that it starts there
+  uint8_t *sA = smem_at_1024, *sB = sA + STAGES * A_STAGE, *slots = sA + SMEM_OPS;
+  float(*const vec)[32] = reinterpret_cast<float(*)[32]>(slots + SMEM_SLOTS);  // d or e of a chunk's columns, a warp each
+  uint64_t *full = reinterpret_cast<uint64_t *>(vec + kEpilogueWarps);
   uint64_t *empty = full + STAGES;
   uint64_t *tfull = empty + STAGES;
   uint64_t *tempty = tfull + 2;
@@ -451,7 +539,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + SLOTS * kEpilogueWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *ready = abort_flag + 1;
-  static_assert((2 * STAGES + 5 + SLOTS * kEpilogueWarps) * 8 + 12 <= SMEM_CTRL, "control block");
+  int *finished = const_cast<int *>(ready + 1);  // warps that have finished their part of a phase, over all phases
+  static_assert((2 * STAGES + 5 + SLOTS * kEpilogueWarps) * 8 + 16 <= SMEM_CTRL, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -469,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < SLOTS * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
     *abort_flag = 0;
     *ready = 0;
-    finished = 0;
+    *finished = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < 10) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
@@ -717,45 +806,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
           const int diagonal = me - at;  // this lane's diagonal element, where the chunk holds it
           float at_diagonal = 0.f;
+          if (kind == kUpdate) {
+            update_chunk<TALL>(a, base + uint32_t(c), hi_part, lo_part, staged, v, own, me < p.m_dim, early, last, lane);
+            send_chunk(a, &maps.c_hi[~(ph / 3) & 1], &maps.c_lo, hi_part, lo_part, staged, last, lane, k, p.m_dim, p.n_dim,
+                       p.out_rows, row0, at);
+          } else {
+            const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {  // eight columns at a time: the code of a phase stays small
-            uint32_t r[8];
-            tmem_ld_32x32b_x8(base + uint32_t(c + 8 * j), r);
-            const int piece = piece_at(lane, j);
-            uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
-            float cols[8];
-            if (kind != kGram) {
-              const uint4 hv = *reinterpret_cast<const uint4 *>(hi_part + piece), lv = *reinterpret_cast<const uint4 *>(lo_part + piece);
-              h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
-              l[0] = lv.x, l[1] = lv.y, l[2] = lv.z, l[3] = lv.w;
-              const float4 c0 = *reinterpret_cast<const float4 *>(&v[8 * j]), c1 = *reinterpret_cast<const float4 *>(&v[8 * j + 4]);
-              cols[0] = c0.x, cols[1] = c0.y, cols[2] = c0.z, cols[3] = c0.w;
-              cols[4] = c1.x, cols[5] = c1.y, cols[6] = c1.z, cols[7] = c1.w;
-            }
-            tmem_ld_wait();
-            float x[8];
-            if (kind == kUpdate) {
-              const float alpha = a.poly_inv * a.x_inv;
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(base + uint32_t(c + 8 * j), r);
+              uint32_t h[8], l[8];
+              float cols[16];
+              if (kind == kPoly) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
-                const float hx = i & 1 ? hf.y : hf.x, lx = i & 1 ? lf.y : lf.x, e = TALL ? cols[i] : own;
-                // x_inv times the stored X, alpha times the accumulator: true values
-                x[i] = fmaf(early ? fmaf(e, hx, a.a * lx) : e * (hx + lx), a.x_inv, __uint_as_float(r[i]) * alpha);
+                for (int q = 0; q < 2; ++q) {
+                  const uint4 hv = *reinterpret_cast<const uint4 *>(hi_part + piece_at(lane, j + q));
+                  const uint4 lv = *reinterpret_cast<const uint4 *>(lo_part + piece_at(lane, j + q));
+                  h[4 * q] = hv.x, h[4 * q + 1] = hv.y, h[4 * q + 2] = hv.z, h[4 * q + 3] = hv.w;
+                  l[4 * q] = lv.x, l[4 * q + 1] = lv.y, l[4 * q + 2] = lv.z, l[4 * q + 3] = lv.w;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float4 f = *reinterpret_cast<const float4 *>(&v[8 * j + 4 * q]);
+                  cols[4 * q] = f.x, cols[4 * q + 1] = f.y, cols[4 * q + 2] = f.z, cols[4 * q + 3] = f.w;
+                }
               }
-              if (last) {
+              tmem_ld_wait();
+              float x[16];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  *reinterpret_cast<float4 *>(const_cast<uint8_t *>(staged) + lane * 128 + (((2 * j + i) ^ (lane & 7)) << 4)) =
-                      make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                continue;
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = me < p.m_dim ? x[i] * a.x_scale : 0.f;  // rows that fill the last block stay zero
-            } else {
-              const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 16; ++i) {
                 const float s = __uint_as_float(r[i]) * alpha;
                 if (kind == kGram) {
                   x[i] = s * a.gram_scale;
@@ -769,33 +849,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   x[i] = 0.f;
                 }
               }
-            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              h[i] = pack2(x[2 * i], x[2 * i + 1]);
-              const float2 t = unpack2(h[i]);
-              l[i] = pack2(x[2 * i] - t.x, x[2 * i + 1] - t.y);
-            }
-            *reinterpret_cast<uint4 *>(hi_part + piece) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (kind != kPoly) *reinterpret_cast<uint4 *>(lo_part + piece) = make_uint4(l[0], l[1], l[2], l[3]);
-          }
-          const int to = k * p.out_rows + row0;
-          if (kind == kUpdate) {
-            if (!last) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(&maps.c_hi[~(ph / 3) & 1], hi_part, at, to);
-                tma_store_2d(&maps.c_lo, lo_part, at, to);
-                bulk_commit_group();
+              for (int i = 0; i < 8; ++i) {
+                h[i] = pack2(x[2 * i], x[2 * i + 1]);
+                const float2 f = unpack2(h[i]);
+                l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
               }
-            } else {
-              __syncwarp();
-              write_out(a, p, staged, lane, k, row0, at);
-              fence_proxy_async_smem();  // before a copy lands where this was
-              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                *reinterpret_cast<uint4 *>(hi_part + piece_at(lane, j + q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+                if (kind == kGram)
+                  *reinterpret_cast<uint4 *>(lo_part + piece_at(lane, j + q)) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+              }
             }
-          } else {
             if (diagonal >= 0 && diagonal < 32 && me < a.m) {
               if (kind == kGram) a.diag[int64_t(k) * a.m + me] = at_diagonal;
               else a.e[int64_t(k) * a.m + me] = fmaf(a.c, fmaf(own, own, at_diagonal), fmaf(a.b, own, a.a));
@@ -811,6 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
+              const int to = k * p.out_rows + row0;
               const CUtensorMap *const out = kind == kGram ? &maps.c_gram : &maps.c_poly;
               tma_store_2d(out, hi_part, at, to);
               if (kind == kGram) tma_store_2d(&maps.c_gram_lo, lo_part, at, to);
@@ -837,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         __threadfence_block();
-        if ((atomicAdd(&finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
+        if ((atomicAdd(finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
           __threadfence_block();
           add_release(&a.arrived[ph]);
         }
@@ -856,6 +923,455 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * BN);
+  }
+}
+
+// --------------------------------------------------------------------------- small Gram matrices
+
+// Matrices whose smaller side fits one tile (128 G: a CTA, or a pair of them): every CTA or pair that shares a matrix
+// computes all of A and A^2 by itself, so that A' and B' go from the accumulator to the next product's operand through
+// its own shared memory, and an iteration has one exchange, X's, in place of three.
+//   GRAM    X's rows (columns, TALL) stream through the ring; one tile in shared memory is both operands, A staying in
+//           the accumulator, exact, until B is formed;
+//   POLY    A' as the first epilogue left it: each CTA of a pair holds its 128 rows, which are its rows of either operand;
+//   UPDATE  B' likewise, against X's tiles: those of this group, `parts` groups a matrix.
+// d and e of all rows are traded between the CTAs of a pair.
+constexpr int R_STAGE = 128 * BK * 2;  // 128 rows of 64 (or 64 of 128)
+
+struct SmallArgs {
+  int count, rows, cols, stand;          // X: its rows in memory
+  int parts, groups;                     // CTAs or pairs a matrix, matrices at a time
+  int tiles, gram_blocks, poly_blocks;   // X's tiles; blocks of 64 of the contractions
+};
+
+struct SmallMaps {
+  CUtensorMap x[2], c_hi[2], c_lo;
+};
+
+template <int G>
+struct Small {
+  static constexpr int N = 128 * G, OP = 2 * G * R_STAGE;  // B' or A': 2 G panels of 64 columns
+  static constexpr int STAGES = G == 1 ? 6 : 4;
+  static constexpr int VECS = 2 * N * 4;
+  static constexpr int SMEM = OP + STAGES * R_STAGE + SMEM_SLOTS + VECS + SMEM_CTRL;  // no room to align it again
+};
+static_assert(Small<1>::SMEM <= 232448 && Small<2>::SMEM <= 232448, "shared memory per block");
+
+// Where column c (a multiple of 8) of row r of A' or B' lies in the operand: panels of 64 columns in the 128-byte swizzle.
+__device__ __forceinline__ int operand_at(int r, int c) { return (c >> 6) * R_STAGE + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4); }
+
+// Waits for a phase of `bar` with the writes of the cluster's other CTA before its arrivals made visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err,
+                                                  unsigned int bit) {
+  const bool ok = mbar_wait(bar, parity, abort_flag, err, bit);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+template <int G, bool TALL>
+__global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
+    newton_schulz_small_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ Args a,
+                               const __grid_constant__ SmallArgs s) {
+  using S = Small<G>;
+  constexpr int N = S::N;
+  extern __shared__ __align__(1024) uint8_t smem_at_1024[];  // the host checks that it starts there
+  uint8_t *op = smem_at_1024, *ring = op + S::OP, *slots = ring + S::STAGES * R_STAGE;
+  float *dvec = reinterpret_cast<float *>(slots + SMEM_SLOTS), *evec = dvec + N;
+  uint64_t *full = reinterpret_cast<uint64_t *>(evec + N);
+  uint64_t *empty = full + S::STAGES;
+  uint64_t *tfull = empty + S::STAGES;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *op_ready = tempty + 2;   // the even CTA's: A' or B' is in shared memory
+  uint64_t *traded = op_ready + 1;   // d or e of all rows is in this CTA
+  uint64_t *drained = traded + 1;
+  uint64_t *cfull = drained + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + SLOTS * kEpilogueWarps);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  volatile int *ready = abort_flag + 1;
+  int *finished = const_cast<int *>(ready + 1);  // warps that have finished their part of an iteration, over all of them
+  static_assert((2 * S::STAGES + 7 + SLOTS * kEpilogueWarps) * 8 + 16 <= SMEM_CTRL, "control block");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = G == 2 ? cluster_ctarank() : 0;
+  const int cluster = int(blockIdx.x) / G, group = cluster / s.parts, part = cluster - group * s.parts;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], G * kEpilogueWarps);
+    }
+    mbar_init(op_ready, G * kEpilogueWarps);
+    mbar_init(traded, G * kEpilogueWarps);
+    mbar_init(drained, 1);
+    for (int i = 0; i < SLOTS * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
+    *abort_flag = 0;
+    *ready = 0;
+    *finished = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane < 5) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
+  if (warp == 1) {
+    if (G == 2) {
+      tmem_alloc_pair(tmem_slot, 2 * N);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 2 * N);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (G == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  unsigned int *err = &g_ortho_wait_timeouts;
+  // seq counts this CTA's iterations over all its matrices; `ready` holds the last one that may start
+  if (warp == 0) {
+    if (lane == 0) {  // -------------------------------------------------- producer: X's tiles, GRAM's then UPDATE's
+      int stage = 0;
+      uint32_t parity = 0;
+      int armed[S::STAGES];
+      for (int i = 0; i < S::STAGES; ++i) armed[i] = -1;
+      bool ok = true;
+      int seq = 0;
+      for (int k = group; ok && k < s.count; k += s.groups) {
+        const int r0 = k * s.stand;
+        for (int it = 0; ok && it < a.steps; ++it, ++seq) {
+          const CUtensorMap *x = &maps.x[it & 1];
+          if (it > 0 && !(ok = wait_ready(ready, seq, abort_flag, err))) break;
+          // one block: 128 indices of a tile from i0 on, 64 of the contraction from c0 on; along: the contraction runs
+          // along X's rows
+          const auto block = [&](bool along, int i0, int c0) {
+            if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) return false;
+            if (rank == 0) {
+              mbar_arrive_expect_tx(&full[stage], G * R_STAGE);
+              armed[stage] = int(parity);
+            }
+            uint8_t *to = ring + stage * R_STAGE;
+            for (int i = 0; i < 2; ++i) {
+              const int cx = along ? c0 : i0 + 64 * i, cy = r0 + (along ? i0 + 64 * i : c0);
+              if (G == 2) tma_load_2d_pair(x, mapa_shared(&full[stage], 0), to + i * BOX, cx, cy);
+              else tma_load_2d(x, &full[stage], to + i * BOX, cx, cy);
+            }
+            if (++stage == S::STAGES) {
+              stage = 0;
+              parity ^= 1u;
+            }
+            return true;
+          };
+          for (int b = 0; ok && b < s.gram_blocks; ++b) ok = block(!TALL, 128 * int(rank), b * BK);
+          for (int t = part; ok && t < s.tiles; t += s.parts)
+            for (int b = 0; ok && b < s.poly_blocks; ++b) ok = block(TALL, t * N + 128 * int(rank), b * BK);
+        }
+      }
+      for (int i = 0; i < S::STAGES; ++i)
+        if (armed[i] >= 0) drain(&full[i], uint32_t(armed[i]));
+    }
+  } else if (warp == 1) {  // ---------------------------------------------- MMA (the even CTA)
+    if (rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t parity = 0, acc_parity = 0, op_parity = 0;
+      bool ok = true;
+      const auto issue = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool more) {
+        if (G == 2) mma_f16_pair(d, ad, bd, idesc, more);
+        else mma_f16(d, ad, bd, idesc, more);
+      };
+      const auto commit = [&](uint64_t *bar) {
+        if (G == 2) mma_commit_pair(bar, 0x3);
+        else mma_commit(bar);
+      };
+      // One product: `kind`'s contraction into the next accumulator.
+      const auto product = [&](int kind, int blocks) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_parity ^ 1u, abort_flag, err, 0x2u))) return false;
+        tc_fence_after();
+        const uint32_t d = tmem_base + uint32_t(acc * N);
+        const bool a_mn = kind == kGram && TALL, b_mn = a_mn || (kind == kUpdate && !TALL);
+        const uint32_t idesc = idesc_f16_f32(N, N, a_mn, b_mn);
+        const uint32_t da = a_mn ? UK * 128 : UK * 2, db = b_mn ? UK * 128 : UK * 2;
+        for (int b = 0; b < blocks; ++b) {
+          if (kind != kPoly && !__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], parity, abort_flag, err, 0x4u))) return false;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint32_t x0 = smem_u32(ring + stage * R_STAGE), o0 = smem_u32(op + b * R_STAGE);
+            const uint32_t a0 = kind == kGram || (kind == kUpdate && TALL) ? x0 : o0;
+            const uint32_t b0 = kind == kGram || (kind == kUpdate && !TALL) ? x0 : o0;
+#pragma unroll
+            for (int i = 0; i < BK / UK; ++i)
+              issue(d, sdesc_sw128(a0 + i * da, a_mn ? BOX : 16, 1024), sdesc_sw128(b0 + i * db, b_mn ? BOX : 16, 1024), idesc,
+                    b > 0 || i > 0);
+            if (kind != kPoly) commit(&empty[stage]);
+          }
+          __syncwarp();
+          if (kind != kPoly && ++stage == S::STAGES) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
+        if (elect_one_sync()) commit(&tfull[acc]);
+        __syncwarp();
+        if (++acc == 2) {
+          acc = 0;
+          acc_parity ^= 1u;
+        }
+        return true;
+      };
+      const auto operand = [&] {  // A' or B' is in place
+        const bool there = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(op_ready, op_parity, abort_flag, err, 0x800u));
+        op_parity ^= 1u;
+        tc_fence_after();
+        return there;
+      };
+      for (int k = group; ok && k < s.count; k += s.groups)
+        for (int it = 0; ok && it < a.steps; ++it) {
+          ok = product(kGram, s.gram_blocks) && operand() && product(kPoly, s.poly_blocks) && operand();
+          for (int t = part; ok && t < s.tiles; t += s.parts) ok = product(kUpdate, s.poly_blocks);
+        }
+      if (elect_one_sync()) commit(drained);
+      __syncwarp();
+    }
+    if (lane == 0) drain(drained, 0);
+  } else if (warp == 3) {
+    if (lane == 0) {  // ---------------------------------------------------- X of the iteration before, from all parts
+      int seq = 0;
+      bool ok = true;
+      for (int k = group; ok && k < s.count; k += s.groups)
+        for (int it = 0; ok && it < a.steps; ++it, ++seq) {
+          if (it == 0) continue;
+          const unsigned int all = unsigned(G * s.parts);
+          const uint64_t t0 = globaltimer_ns();
+          uint32_t spins = 0;
+          while (load_acquire(&a.arrived[k * kMostSteps + it - 1]) < all) {
+            if (*abort_flag) ok = false;
+            if ((++spins & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+              atomicOr(err, 0x200u);
+              ok = false;
+            }
+            if (!ok) break;
+          }
+          if (!ok) {
+            *abort_flag = 1;
+            break;
+          }
+          fence_proxy_async_global();
+          __threadfence_block();
+          *ready = seq;
+        }
+    }
+  } else if (warp >= 4) {  // ----------------------------------------------- epilogues (both CTAs)
+    const int ew = warp - 4, quarter = warp & 3, side = ew >> 2;
+    const int lrow = 32 * quarter + lane, me = 128 * int(rank) + lrow;  // this lane's row of A and B
+    uint8_t *const mine = slots + ew * SLOTS * SLOT;
+    uint64_t *const cbar = cfull + SLOTS * ew;
+    const uint32_t lanes = uint32_t(32 * quarter) << 16;
+    const int m_dim = s.rows, n_dim = s.cols;
+    int acc = 0, slot = 0, seq = 0;
+    uint32_t acc_parity = 0, cparity = 0, t_parity = 0;
+    int flying = 0;
+    bool ok = true;
+    const auto result = [&] {  // the next accumulator holds its product
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_parity, abort_flag, err, 0x8u))) return false;
+      tc_fence_after();
+      return true;
+    };
+    const auto advance = [&] {
+      if (++acc == 2) {
+        acc = 0;
+        acc_parity ^= 1u;
+      }
+    };
+    const auto release = [&](int which) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[which], 0));
+    };
+    // A value of this lane's row for every row's reader in the pair; `put`: it has one.
+    const auto trade = [&](float *vec, bool put, float value) {
+      if (put) {
+        vec[me] = value;
+        if (G == 2) {
+          const uint32_t to = mapa_shared(&vec[me], rank ^ 1u);
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(value) : "memory");
+        }
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (uint32_t q = 0; q < G; ++q) mbar_arrive_cluster(mapa_shared(traded, q));
+    };
+    const auto wait_trade = [&] {
+      const bool there = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(traded, t_parity, abort_flag, err, 0x1000u));
+      t_parity ^= 1u;
+      return there;
+    };
+    const auto hand_over = [&] {  // the operand that this warp has written
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(op_ready, 0));
+    };
+    for (int k = group; ok && k < s.count; k += s.groups) {
+      for (int it = 0; ok && it < a.steps; ++it, ++seq) {
+        const bool early = it < 2, last = it + 1 == a.steps;
+        const CUtensorMap *const from = &maps.c_hi[it & 1], *const to = &maps.c_hi[~it & 1];
+        // ---- A: the diagonal to d, the rest as fp16
+        if (!(ok = result())) break;
+        const int gram_acc = acc;
+        advance();
+        const uint32_t gram = tmem_base + lanes + uint32_t(gram_acc * N + side * (N / 2));
+        const float g_alpha = a.x_inv * a.x_inv;
+        float at_diagonal = 0.f;
+        const int diagonal = me - side * (N / 2);  // of this warp's columns
+#pragma unroll 1
+        for (int c = 0; c < N / 2; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(gram + uint32_t(c), r);
+          tmem_ld_wait();
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float x[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float v = __uint_as_float(r[i + q]) * g_alpha;
+              const bool on = c + i + q == diagonal;
+              if (on) at_diagonal = v;
+              x[q] = !on && me < a.m && side * (N / 2) + c + i + q < a.m ? v * a.gram_scale : 0.f;
+            }
+            w[i >> 1] = pack2(x[0], x[1]);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4 *>(op + operand_at(lrow, side * (N / 2) + c + 8 * q)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+        hand_over();
+        trade(dvec, diagonal >= 0 && diagonal < N / 2, at_diagonal);
+        // ---- B from A, still exact in its accumulator, and A'^2
+        if (!(ok = result() && wait_trade())) break;
+        const uint32_t poly = tmem_base + lanes + uint32_t(acc * N + side * (N / 2));
+        const float s_alpha = a.gram_inv * a.gram_inv, di = dvec[me];
+#pragma unroll 1
+        for (int c = 0; c < N / 2; c += 16) {
+          uint32_t r[16], g[16];
+          tmem_ld_32x32b_x16(poly + uint32_t(c), r);
+          tmem_ld_32x32b_x16(gram + uint32_t(c), g);
+          float dj[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 f = *reinterpret_cast<const float4 *>(&dvec[side * (N / 2) + c + 4 * q]);
+            dj[4 * q] = f.x, dj[4 * q + 1] = f.y, dj[4 * q + 2] = f.z, dj[4 * q + 3] = f.w;
+          }
+          tmem_ld_wait();
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float x[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float sq = __uint_as_float(r[i + q]) * s_alpha, v = __uint_as_float(g[i + q]) * g_alpha;
+              const bool on = c + i + q == diagonal;
+              if (on) at_diagonal = sq;
+              x[q] = !on && me < a.m && side * (N / 2) + c + i + q < a.m
+                         ? (a.b * v + a.c * fmaf(di + dj[i + q], v, sq)) * a.poly_scale
+                         : 0.f;
+            }
+            w[i >> 1] = pack2(x[0], x[1]);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4 *>(op + operand_at(lrow, side * (N / 2) + c + 8 * q)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+        release(gram_acc);
+        release(acc);
+        advance();
+        hand_over();
+        trade(evec, diagonal >= 0 && diagonal < N / 2, fmaf(a.c, fmaf(di, di, at_diagonal), fmaf(a.b, di, a.a)));
+        if (!(ok = wait_trade())) break;
+        // ---- X of this group's tiles
+        if (it > 0) {
+          bool r = true;
+          if (lane == 0) r = wait_ready(ready, seq, abort_flag, err);
+          if (!(ok = __all_sync(0xFFFFFFFFu, r))) break;
+        }
+        const float own = evec[me];
+        const auto place = [&](int t, int &row0, int &col) {
+          row0 = (TALL ? t * N : 0) + 128 * int(rank) + 32 * quarter;
+          col = (TALL ? 0 : t * N) + side * (N / 2);
+        };
+        const auto exists = [&](int row0, int col) { return row0 < s.stand && col < n_dim; };
+        const auto fetch = [&](int q, int row0, int col) {
+          if (lane == 0) {
+            bulk_wait_group_read<1>();
+            mbar_arrive_expect_tx(&cbar[q], 2 * PART);
+            tma_load_2d(from, &cbar[q], mine + q * SLOT, col, k * s.stand + row0);
+            tma_load_2d(&maps.c_lo, &cbar[q], mine + q * SLOT + PART, col, k * s.stand + row0);
+          }
+          flying |= 1 << q;
+        };
+        bool fetched = false;
+        for (int t = part; ok && t < s.tiles; t += s.parts) {
+          int row0, col;
+          place(t, row0, col);
+          if (!fetched && exists(row0, col)) fetch(slot, row0, col);
+          if (!(ok = result())) break;
+          const uint32_t base = tmem_base + lanes + uint32_t(acc * N + side * (N / 2));
+          fetched = false;
+#pragma unroll 1
+          for (int c = 0; c < N / 2 && exists(row0, col + c); c += 32) {
+            const int next = slot == SLOTS - 1 ? 0 : slot + 1;
+            int nrow = row0, ncol = col + c + 32;
+            bool more = c + 32 < N / 2 && exists(nrow, ncol);
+            if (!more && t + s.parts < s.tiles) {
+              place(t + s.parts, nrow, ncol);
+              more = exists(nrow, ncol);
+            }
+            if (more) fetch(next, nrow, ncol);
+            fetched = more;
+            if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u)))) break;
+            cparity ^= 1u << slot;
+            flying &= ~(1 << slot);
+            __syncwarp();
+            uint8_t *const hi = mine + slot * SLOT, *const lo = hi + PART;
+            uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
+            update_chunk<TALL>(a, base + uint32_t(c), hi, lo, staged, &evec[TALL ? col + c : 0], own, row0 + lane < m_dim, early,
+                               last, lane);
+            send_chunk(a, to, &maps.c_lo, hi, lo, staged, last, lane, k, m_dim, n_dim, s.stand, row0, col + c);
+            slot = next;
+          }
+          if (!ok) break;
+          release(acc);
+          advance();
+        }
+        if (!ok) break;
+        if (!last) {
+          if (lane == 0) bulk_wait_all();
+          __syncwarp();
+          if (lane == 0) {
+            __threadfence_block();
+            if ((atomicAdd(finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
+              __threadfence_block();
+              add_release(&a.arrived[k * kMostSteps + it]);
+            }
+          }
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (lane == 0) {
+      bulk_wait_group_read<0>();
+      for (int i = 0; i < SLOTS; ++i)
+        if (flying >> i & 1) drain(&cbar[i], (cparity >> i) & 1u);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (G == 2) cluster_sync();  // neither CTA leaves while the other may still reach its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    if (G == 2) tmem_dealloc_pair(tmem_base, 2 * N);
+    else tmem_dealloc(tmem_base, 2 * N);
   }
 }
 
@@ -891,7 +1407,7 @@ Plan plan_of(int64_t count, int64_t rows, int64_t cols) {
   p.diag = take(4 * count * p.m);
   p.e = take(4 * count * p.m);
   p.part = take(8 * count * kMostParts);
-  p.arrived = take(4 * kMostPhases);
+  p.arrived = take(4 * kCounters);
   p.bytes = at;
   return p;
 }
@@ -925,24 +1441,49 @@ gtp_status schedule_of(const float *abc, int32_t steps, Schedule *s) {
   return GTP_OK;
 }
 
-// How many CTA pairs of the kernel the device holds at once (a cooperative launch's limit); 0 on an error.
-template <bool TALL>
-gtp_status pairs_of(const gtp::DeviceInfo &dev, int *pairs) {
-  static std::atomic<int> known[64];
+// How many clusters of the kernel the device holds at once (a cooperative launch's limit).
+template <typename K>
+gtp_status clusters_of(K kernel, int size, int smem, std::atomic<int> (&known)[64], const gtp::DeviceInfo &dev,
+                       int *clusters) {
   std::atomic<int> &slot = known[dev.device & 63];
-  if ((*pairs = slot.load()) > 0) return GTP_OK;
-  cudaError_t e = cudaFuncSetAttribute(newton_schulz_kernel<TALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+  if ((*clusters = slot.load()) > 0) return GTP_OK;
+  cudaFuncAttributes f;
+  int reserved = 0;
+  cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev.device);
+  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "shared memory attributes: %s", cudaGetErrorString(e));
+  if (gtp_status s = gtp::check_dynamic_base("orthogonalize", size_t(reserved), f.sharedSizeBytes, 1024))
+    return s;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(dev.sm_count / 2 * 2));
+  cfg.gridDim = dim3(unsigned(dev.sm_count / size * size));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = SMEM_TOTAL;
-  e = cudaOccupancyMaxActiveClusters(pairs, newton_schulz_kernel<TALL>, &cfg);
+  cfg.dynamicSmemBytes = size_t(smem);
+  e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
   if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
-  if (*pairs < 1) return gtp::fail(GTP_E_CUDA, "no room for a CTA pair");
-  *pairs = std::min(*pairs, dev.sm_count / 2);
-  slot.store(*pairs);
+  if (*clusters < 1) return gtp::fail(GTP_E_CUDA, "no room for a cluster of %d CTAs", size);
+  *clusters = std::min(*clusters, dev.sm_count / size);
+  slot.store(*clusters);
   return GTP_OK;
+}
+
+// A cooperative launch: the CTAs wait for one another, so all of them run at the same time.
+template <typename... KArgs, typename... As>
+gtp_status launch_together(void (*kernel)(KArgs...), int ctas, int smem, cudaStream_t st, const As &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "orthogonalize: %s", cudaGetErrorString(e));
+  return gtp::check_launch("orthogonalize");
 }
 
 // Tiles of 256 x 256 in whole waves of the pairs, the rest as halves where those fit one wave or less time: a half-wide
@@ -968,12 +1509,8 @@ gtp_status map_of(CUtensorMap *map, const void *base, int64_t inner, int64_t sta
                              chunk ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The iterations, from X in hi[0] and lo to the last product's output.
-template <bool TALL>
-gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
-                   const gtp::DeviceInfo &dev, cudaStream_t st) {
-  int pairs = 0;
-  if (gtp_status e = pairs_of<TALL>(dev, &pairs)) return e;
+// What both kernels need: the iteration's constants and the powers of two that keep every fp16 value in range.
+void fill(Args &a, const Schedule &s, const Plan &plan, char *ws) {
   const int xs = 12, gs = 12;
   const double top2 = double(s.bound) * s.bound, poly_top = std::fabs(s.b) * top2 + std::fabs(s.c) * top2 * top2;
   const int ps = std::min(14, 15 - int(std::ceil(std::log2(std::max(poly_top, 1.0)))));
@@ -983,6 +1520,15 @@ gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_
   a.a = s.a, a.b = s.b, a.c = s.c, a.steps = s.steps, a.m = int(plan.m);
   a.diag = reinterpret_cast<float *>(ws + plan.diag), a.e = reinterpret_cast<float *>(ws + plan.e);
   a.arrived = reinterpret_cast<unsigned int *>(ws + plan.arrived);
+}
+
+// The iterations, from X in hi[0] and lo to the last product's output.
+template <bool TALL>
+gtp_status iterate(Args a, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols, const gtp::DeviceInfo &dev,
+                   cudaStream_t st) {
+  static std::atomic<int> known[64];
+  int pairs = 0;
+  if (gtp_status e = clusters_of(newton_schulz_kernel<TALL>, 2, SMEM_TOTAL, known, dev, &pairs)) return e;
   for (int kind = 0; kind < 3; ++kind) {
     Phase &p = a.phase[kind];
     const bool update = kind == kUpdate;
@@ -1006,25 +1552,41 @@ gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_
                              g_map(&maps.c_gram_lo, plan.gram_lo, true), g_map(&maps.c_poly, plan.poly, true)})
     if (e) return e;
   const int used = std::min(pairs, std::max({a.phase[0].units, a.phase[1].units, a.phase[2].units}));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * unsigned(used));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = SMEM_TOTAL;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all of them run at the same time
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, newton_schulz_kernel<TALL>, maps, a);
-  if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "orthogonalize: %s", cudaGetErrorString(e));
-  return gtp::check_launch("orthogonalize");
+  return launch_together(newton_schulz_kernel<TALL>, 2 * used, SMEM_TOTAL, st, maps, a);
 }
 
-gtp_status iterate(const Args &a, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
+template <int G, bool TALL>
+gtp_status iterate_small(const Args &a, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
+                         const gtp::DeviceInfo &dev, cudaStream_t st) {
+  static std::atomic<int> known[64];
+  int clusters = 0;
+  if (gtp_status e = clusters_of(newton_schulz_small_kernel<G, TALL>, G, Small<G>::SMEM, known, dev, &clusters)) return e;
+  SmallArgs s = {};
+  s.count = int(count), s.rows = int(rows), s.cols = int(cols), s.stand = int(plan.rows);
+  s.tiles = int((plan.n + Small<G>::N - 1) / Small<G>::N);
+  s.gram_blocks = int((plan.n + BK - 1) / BK), s.poly_blocks = int((plan.m + BK - 1) / BK);
+  s.parts = std::max(1, std::min(s.tiles, clusters / s.count));
+  s.groups = std::min(s.count, clusters / s.parts);
+  SmallMaps maps;
+  for (int i = 0; i < 5; ++i) {
+    const int64_t at = i == 4 ? plan.lo : plan.hi[i & 1];
+    CUtensorMap *m = i < 2 ? &maps.x[i] : i < 4 ? &maps.c_hi[i - 2] : &maps.c_lo;
+    if (gtp_status e = map_of(m, ws + at, cols, plan.rows, plan.ldx, count, i >= 2)) return e;
+  }
+  return launch_together(newton_schulz_small_kernel<G, TALL>, G * s.parts * s.groups, Small<G>::SMEM, st, maps, a, s);
+}
+
+gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_t count, int64_t rows, int64_t cols,
                    const gtp::DeviceInfo &dev, cudaStream_t st) {
-  return rows > cols ? iterate<true>(a, s, plan, ws, count, rows, cols, dev, st)
-                     : iterate<false>(a, s, plan, ws, count, rows, cols, dev, st);
+  fill(a, s, plan, ws);
+  const bool tall = rows > cols;
+  if (plan.m <= 128)
+    return tall ? iterate_small<1, true>(a, plan, ws, count, rows, cols, dev, st)
+                : iterate_small<1, false>(a, plan, ws, count, rows, cols, dev, st);
+  if (plan.m <= 256)
+    return tall ? iterate_small<2, true>(a, plan, ws, count, rows, cols, dev, st)
+                : iterate_small<2, false>(a, plan, ws, count, rows, cols, dev, st);
+  return tall ? iterate<true>(a, plan, ws, count, rows, cols, dev, st) : iterate<false>(a, plan, ws, count, rows, cols, dev, st);
 }
 
 template <typename T, bool VEC, bool STEP>
