@@ -898,7 +898,7 @@ gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *momentum, fl
  * (MMA side), bit 3 epilogue, bit 5/6 the dynamic schedule's ring, bit 7 a drain of the
  * kernel's own copies at exit, bit 8 the self-test below; of the orthogonalised update bit 4
  * a phase inside a CTA, bit 9 the CTAs of the phase before, bit 10 a chunk's old values, bit 11
- * an operand formed in shared memory, bit 12 the diagonals traded in a CTA pair.
+ * an operand formed in shared memory.
  * Reads the word into *flags (host pointer) and clears it if reset != 0.  Synchronous
  * with respect to the current device.  The pages' failure detection ("05 · grad/param
  * buffer ...", §6.3: NaN / large-gradient checks before the collective) is a check of the

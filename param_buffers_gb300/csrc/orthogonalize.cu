@@ -440,66 +440,107 @@ __device__ __forceinline__ void write_out(const Args &a, int m_dim, int n_dim, c
   }
 }
 
+// Sixteen elements of a row of A' out of its accumulator, times `scale`.  EDGE: element `diagonal` of them is on the
+// diagonal, which is kept apart (true value) and left out, and so are elements from `limit` on.
+template <bool EDGE>
+__device__ __forceinline__ void gram_row(const uint32_t (&r)[16], float scale, float alpha, int diagonal, int limit,
+                                         float &at_diagonal, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = __uint_as_float(r[i]) * scale;
+    if (EDGE) {
+      if (i == diagonal) at_diagonal = __uint_as_float(r[i]) * alpha;
+      if (i == diagonal || i >= limit) x[i] = 0.f;
+    }
+  }
+}
+
+// The same of B' = b A' + c ((d_i + d_j) A' + A'^2): g holds A' and r its square, in their own scales;
+// k = {(b + c d_i), c, c}, each with the powers of two that make the sum B' in its scale.
+template <bool EDGE>
+__device__ __forceinline__ void poly_row(const uint32_t (&r)[16], const float (&g)[16], const float (&dj)[16], const float (&k)[3],
+                                         float alpha, int diagonal, int limit, float &at_diagonal, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = fmaf(g[i], fmaf(k[1], dj[i], k[0]), __uint_as_float(r[i]) * k[2]);
+    if (EDGE) {
+      if (i == diagonal) at_diagonal = __uint_as_float(r[i]) * alpha;
+      if (i == diagonal || i >= limit) x[i] = 0.f;
+    }
+  }
+}
+
+__device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 f = *reinterpret_cast<const float4 *>(p + 4 * q);
+    x[4 * q] = f.x, x[4 * q + 1] = f.y, x[4 * q + 2] = f.z, x[4 * q + 3] = f.w;
+  }
+}
+
 // A chunk of the update, from the accumulator at `taddr` and the old X in hi and lo: the new X in their place, or (last)
-// true values in `staged`.  v: e of the chunk's columns (TALL), own: e of this lane's row; inside: that row exists (rows
-// that fill a contraction's last block stay zero).  Sixteen columns at a time: the code of a phase stays small.
+// true values in `staged`.  v: e of the chunk's columns (TALL), own: e of this lane's row; inside: that row exists (those
+// that fill a contraction's last block keep the zeros that came).  Sixteen columns at a time: the code of a phase stays
+// small.
 template <bool TALL>
 __device__ __forceinline__ void update_chunk(const Args &a, uint32_t taddr, uint8_t *hi, uint8_t *lo, uint8_t *staged,
                                              const float *v, float own, bool inside, bool early, bool last, int lane) {
-  const float alpha = a.poly_inv * a.x_inv;
+  const float alpha = a.poly_inv;  // the accumulator in X's scale
 #pragma unroll 1
   for (int j = 0; j < 4; j += 2) {
     uint32_t r[16];
     tmem_ld_32x32b_x16(taddr + uint32_t(8 * j), r);
-    uint4 h4[2], l4[2];
+    uint32_t h[8], l[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      h4[q] = *reinterpret_cast<const uint4 *>(hi + piece_at(lane, j + q));
-      l4[q] = *reinterpret_cast<const uint4 *>(lo + piece_at(lane, j + q));
+      const uint4 hv = *reinterpret_cast<const uint4 *>(hi + piece_at(lane, j + q));
+      const uint4 lv = *reinterpret_cast<const uint4 *>(lo + piece_at(lane, j + q));
+      h[4 * q] = hv.x, h[4 * q + 1] = hv.y, h[4 * q + 2] = hv.z, h[4 * q + 3] = hv.w;
+      l[4 * q] = lv.x, l[4 * q + 1] = lv.y, l[4 * q + 2] = lv.z, l[4 * q + 3] = lv.w;
     }
-    float e[TALL ? 16 : 1];
+    float e[16];
     if (TALL) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 f = *reinterpret_cast<const float4 *>(&v[8 * j + 4 * q]);
-        e[4 * q] = f.x, e[4 * q + 1] = f.y, e[4 * q + 2] = f.z, e[4 * q + 3] = f.w;
-      }
+      load16(v + 8 * j, e);
     } else {
-      e[0] = own;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) e[i] = own;
     }
     tmem_ld_wait();
     float x[16];
+    if (early) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t h[4] = {h4[q].x, h4[q].y, h4[q].z, h4[q].w}, l[4] = {l4[q].x, l4[q].y, l4[q].z, l4[q].w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; i += 2) {
         const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
-        const float hx = i & 1 ? hf.y : hf.x, lx = i & 1 ? lf.y : lf.x, f = TALL ? e[8 * q + i] : e[0];
-        // x_inv times the stored X, alpha times the accumulator: true values
-        x[8 * q + i] = fmaf(early ? fmaf(f, hx, a.a * lx) : f * (hx + lx), a.x_inv, __uint_as_float(r[8 * q + i]) * alpha);
+        x[i] = fmaf(e[i], hf.x, fmaf(a.a, lf.x, __uint_as_float(r[i]) * alpha));
+        x[i + 1] = fmaf(e[i + 1], hf.y, fmaf(a.a, lf.y, __uint_as_float(r[i + 1]) * alpha));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
+        x[i] = fmaf(e[i], hf.x + lf.x, __uint_as_float(r[i]) * alpha);
+        x[i + 1] = fmaf(e[i + 1], hf.y + lf.y, __uint_as_float(r[i + 1]) * alpha);
       }
     }
     if (last) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4 *>(staged + lane * 128 + (((2 * j + i) ^ (lane & 7)) << 4)) =
-            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            make_float4(x[4 * i] * a.x_inv, x[4 * i + 1] * a.x_inv, x[4 * i + 2] * a.x_inv, x[4 * i + 3] * a.x_inv);
       continue;
     }
-    const float scale = inside ? a.x_scale : 0.f;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t h[4], l[4];
+    for (int i = 0; i < 8; ++i) {
+      h[i] = pack2(x[2 * i], x[2 * i + 1]);
+      const float2 f = unpack2(h[i]);
+      l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+    }
+    if (inside) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = inside ? x[8 * q + 2 * i] * scale : 0.f, x1 = inside ? x[8 * q + 2 * i + 1] * scale : 0.f;
-        h[i] = pack2(x0, x1);
-        const float2 f = unpack2(h[i]);
-        l[i] = pack2(x0 - f.x, x1 - f.y);
+      for (int q = 0; q < 2; ++q) {
+        *reinterpret_cast<uint4 *>(hi + piece_at(lane, j + q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+        *reinterpret_cast<uint4 *>(lo + piece_at(lane, j + q)) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
       }
-      *reinterpret_cast<uint4 *>(hi + piece_at(lane, j + q)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4 *>(lo + piece_at(lane, j + q)) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -812,13 +853,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        p.out_rows, row0, at);
           } else {
             const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
+            const float poly[3] = {fmaf(a.c, own, a.b) * a.gram_inv * a.poly_scale, a.c * a.gram_inv * a.poly_scale,
+                                   a.c * alpha * a.poly_scale};
+            const bool edge = at == row0;  // the chunk holds a piece of the diagonal
 #pragma unroll 1
             for (int j = 0; j < 4; j += 2) {
               uint32_t r[16];
               tmem_ld_32x32b_x16(base + uint32_t(c + 8 * j), r);
               uint32_t h[8], l[8];
-              float cols[16];
-              if (kind == kPoly) {
+              float x[16];
+              if (kind == kGram) {
+                tmem_ld_wait();
+                if (edge) gram_row<true>(r, alpha * a.gram_scale, alpha, diagonal - 8 * j, 16, at_diagonal, x);
+                else gram_row<false>(r, alpha * a.gram_scale, alpha, 0, 0, at_diagonal, x);
+              } else {
+                float g[16], dj[16];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   const uint4 hv = *reinterpret_cast<const uint4 *>(hi_part + piece_at(lane, j + q));
@@ -826,34 +875,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   h[4 * q] = hv.x, h[4 * q + 1] = hv.y, h[4 * q + 2] = hv.z, h[4 * q + 3] = hv.w;
                   l[4 * q] = lv.x, l[4 * q + 1] = lv.y, l[4 * q + 2] = lv.z, l[4 * q + 3] = lv.w;
                 }
+                load16(v + 8 * j, dj);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float4 f = *reinterpret_cast<const float4 *>(&v[8 * j + 4 * q]);
-                  cols[4 * q] = f.x, cols[4 * q + 1] = f.y, cols[4 * q + 2] = f.z, cols[4 * q + 3] = f.w;
+                for (int i = 0; i < 8; ++i) {
+                  const float2 hf = unpack2(h[i]), lf = unpack2(l[i]);
+                  g[2 * i] = hf.x + lf.x, g[2 * i + 1] = hf.y + lf.y;
                 }
-              }
-              tmem_ld_wait();
-              float x[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float s = __uint_as_float(r[i]) * alpha;
-                if (kind == kGram) {
-                  x[i] = s * a.gram_scale;
-                } else {
-                  const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
-                  const float g = (i & 1 ? hf.y + lf.y : hf.x + lf.x) * a.gram_inv;
-                  x[i] = (a.b * g + a.c * fmaf(own + cols[i], g, s)) * a.poly_scale;
-                }
-                if (8 * j + i == diagonal) {
-                  at_diagonal = s;
-                  x[i] = 0.f;
-                }
+                tmem_ld_wait();
+                if (edge) poly_row<true>(r, g, dj, poly, alpha, diagonal - 8 * j, 16, at_diagonal, x);
+                else poly_row<false>(r, g, dj, poly, alpha, 0, 0, at_diagonal, x);
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                h[i] = pack2(x[2 * i], x[2 * i + 1]);
-                const float2 f = unpack2(h[i]);
-                l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+              for (int i = 0; i < 8; ++i) h[i] = pack2(x[2 * i], x[2 * i + 1]);
+              if (kind == kGram) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float2 f = unpack2(h[i]);
+                  l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+                }
               }
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
@@ -960,11 +999,12 @@ static_assert(Small<1>::SMEM <= 232448 && Small<2>::SMEM <= 232448, "shared memo
 // Where column c (a multiple of 8) of row r of A' or B' lies in the operand: panels of 64 columns in the 128-byte swizzle.
 __device__ __forceinline__ int operand_at(int r, int c) { return (c >> 6) * R_STAGE + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4); }
 
-// Waits for a phase of `bar` with the writes of the cluster's other CTA before its arrivals made visible.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err,
-                                                  unsigned int bit) {
+// Waits for a phase of `bar`, with what the other CTA of the pair wrote before its arrivals made visible.
+template <int G>
+__device__ __forceinline__ bool mbar_wait_group(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err,
+                                                unsigned int bit) {
   const bool ok = mbar_wait(bar, parity, abort_flag, err, bit);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  if (G == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
   return ok;
 }
 
@@ -982,14 +1022,13 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *tfull = empty + S::STAGES;
   uint64_t *tempty = tfull + 2;
   uint64_t *op_ready = tempty + 2;   // the even CTA's: A' or B' is in shared memory
-  uint64_t *traded = op_ready + 1;   // d or e of all rows is in this CTA
-  uint64_t *drained = traded + 1;
+  uint64_t *drained = op_ready + 1;
   uint64_t *cfull = drained + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + SLOTS * kEpilogueWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *ready = abort_flag + 1;
   int *finished = const_cast<int *>(ready + 1);  // warps that have finished their part of an iteration, over all of them
-  static_assert((2 * S::STAGES + 7 + SLOTS * kEpilogueWarps) * 8 + 16 <= SMEM_CTRL, "control block");
+  static_assert((2 * S::STAGES + 6 + SLOTS * kEpilogueWarps) * 8 + 16 <= SMEM_CTRL, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = G == 2 ? cluster_ctarank() : 0;
@@ -1004,7 +1043,6 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[i], G * kEpilogueWarps);
     }
     mbar_init(op_ready, G * kEpilogueWarps);
-    mbar_init(traded, G * kEpilogueWarps);
     mbar_init(drained, 1);
     for (int i = 0; i < SLOTS * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
     *abort_flag = 0;
@@ -1012,6 +1050,9 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
     *finished = 0;
     fence_barrier_init();
   }
+  for (int i = threadIdx.x; i < S::OP / 16; i += kThreads)  // what lies beside A' and B' stays zero
+    reinterpret_cast<uint4 *>(op)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == 0 && lane < 5) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
   if (warp == 1) {
     if (G == 2) {
@@ -1119,7 +1160,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
         return true;
       };
       const auto operand = [&] {  // A' or B' is in place
-        const bool there = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(op_ready, op_parity, abort_flag, err, 0x800u));
+        const bool there = __all_sync(0xFFFFFFFFu, mbar_wait_group<G>(op_ready, op_parity, abort_flag, err, 0x800u));
         op_parity ^= 1u;
         tc_fence_after();
         return there;
@@ -1168,7 +1209,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const int m_dim = s.rows, n_dim = s.cols;
     int acc = 0, slot = 0, seq = 0;
-    uint32_t acc_parity = 0, cparity = 0, t_parity = 0;
+    uint32_t acc_parity = 0, cparity = 0;
     int flying = 0;
     bool ok = true;
     const auto result = [&] {  // the next accumulator holds its product
@@ -1187,28 +1228,33 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[which], 0));
     };
-    // A value of this lane's row for every row's reader in the pair; `put`: it has one.
-    const auto trade = [&](float *vec, bool put, float value) {
+    // What this warp has written of an operand, and the value of a row's diagonal element for every row's reader in the
+    // pair (put: this lane has it).  Who waits for the product of that operand has waited for both.
+    const auto hand_over = [&](float *vec, bool put, float value) {
       if (put) {
         vec[me] = value;
-        if (G == 2) {
-          const uint32_t to = mapa_shared(&vec[me], rank ^ 1u);
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(value) : "memory");
-        }
+        if (G == 2)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(&vec[me], rank ^ 1u)), "f"(value) : "memory");
       }
-      __syncwarp();
-      if (lane == 0)
-        for (uint32_t q = 0; q < G; ++q) mbar_arrive_cluster(mapa_shared(traded, q));
-    };
-    const auto wait_trade = [&] {
-      const bool there = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(traded, t_parity, abort_flag, err, 0x1000u));
-      t_parity ^= 1u;
-      return there;
-    };
-    const auto hand_over = [&] {  // the operand that this warp has written
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(op_ready, 0));
+      if (lane == 0) {
+        if (G == 2) mbar_arrive_cluster(mapa_shared(op_ready, 0));
+        else mbar_arrive(op_ready);
+      }
+    };
+    const int first_col = side * (N / 2), first_row = 128 * int(rank) + 32 * quarter;
+    const bool exists_row = me < a.m;
+    // Whether sixteen columns from c on need more than arithmetic: a piece of the diagonal, the matrix's end.
+    const auto edge_at = [&](int c) { return c + 16 > a.m || (c < first_row + 32 && c + 16 > first_row); };
+    const auto put_row = [&](int c, const float (&x)[16]) {
+      if (exists_row) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<uint4 *>(op + operand_at(lrow, c + 8 * q)) =
+              make_uint4(pack2(x[8 * q], x[8 * q + 1]), pack2(x[8 * q + 2], x[8 * q + 3]), pack2(x[8 * q + 4], x[8 * q + 5]),
+                         pack2(x[8 * q + 6], x[8 * q + 7]));
+      }
     };
     for (int k = group; ok && k < s.count; k += s.groups) {
       for (int it = 0; ok && it < a.steps; ++it, ++seq) {
@@ -1218,84 +1264,54 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(ok = result())) break;
         const int gram_acc = acc;
         advance();
-        const uint32_t gram = tmem_base + lanes + uint32_t(gram_acc * N + side * (N / 2));
+        const uint32_t gram = tmem_base + lanes + uint32_t(gram_acc * N + first_col);
         const float g_alpha = a.x_inv * a.x_inv;
         float at_diagonal = 0.f;
-        const int diagonal = me - side * (N / 2);  // of this warp's columns
+        const bool on_diagonal = me >= first_col && me < first_col + N / 2;
+        const int cols_here = min(N / 2, a.m - first_col);
 #pragma unroll 1
-        for (int c = 0; c < N / 2; c += 16) {
+        for (int c = 0; c < cols_here; c += 16) {
+          const int at = first_col + c;
           uint32_t r[16];
           tmem_ld_32x32b_x16(gram + uint32_t(c), r);
           tmem_ld_wait();
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float v = __uint_as_float(r[i + q]) * g_alpha;
-              const bool on = c + i + q == diagonal;
-              if (on) at_diagonal = v;
-              x[q] = !on && me < a.m && side * (N / 2) + c + i + q < a.m ? v * a.gram_scale : 0.f;
-            }
-            w[i >> 1] = pack2(x[0], x[1]);
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4 *>(op + operand_at(lrow, side * (N / 2) + c + 8 * q)) =
-                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          float x[16];
+          if (edge_at(at)) gram_row<true>(r, g_alpha * a.gram_scale, g_alpha, me - at, a.m - at, at_diagonal, x);
+          else gram_row<false>(r, g_alpha * a.gram_scale, g_alpha, 0, 0, at_diagonal, x);
+          put_row(at, x);
         }
-        hand_over();
-        trade(dvec, diagonal >= 0 && diagonal < N / 2, at_diagonal);
+        hand_over(dvec, on_diagonal, at_diagonal);
         // ---- B from A, still exact in its accumulator, and A'^2
-        if (!(ok = result() && wait_trade())) break;
-        const uint32_t poly = tmem_base + lanes + uint32_t(acc * N + side * (N / 2));
+        if (!(ok = result())) break;
+        const uint32_t square = tmem_base + lanes + uint32_t(acc * N + first_col);
         const float s_alpha = a.gram_inv * a.gram_inv, di = dvec[me];
+        const float poly[3] = {fmaf(a.c, di, a.b) * g_alpha * a.poly_scale, a.c * g_alpha * a.poly_scale,
+                               a.c * s_alpha * a.poly_scale};
 #pragma unroll 1
-        for (int c = 0; c < N / 2; c += 16) {
+        for (int c = 0; c < cols_here; c += 16) {
+          const int at = first_col + c;
           uint32_t r[16], g[16];
-          tmem_ld_32x32b_x16(poly + uint32_t(c), r);
+          tmem_ld_32x32b_x16(square + uint32_t(c), r);
           tmem_ld_32x32b_x16(gram + uint32_t(c), g);
-          float dj[16];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 f = *reinterpret_cast<const float4 *>(&dvec[side * (N / 2) + c + 4 * q]);
-            dj[4 * q] = f.x, dj[4 * q + 1] = f.y, dj[4 * q + 2] = f.z, dj[4 * q + 3] = f.w;
-          }
+          float dj[16], gf[16], x[16];
+          load16(dvec + at, dj);
           tmem_ld_wait();
-          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float sq = __uint_as_float(r[i + q]) * s_alpha, v = __uint_as_float(g[i + q]) * g_alpha;
-              const bool on = c + i + q == diagonal;
-              if (on) at_diagonal = sq;
-              x[q] = !on && me < a.m && side * (N / 2) + c + i + q < a.m
-                         ? (a.b * v + a.c * fmaf(di + dj[i + q], v, sq)) * a.poly_scale
-                         : 0.f;
-            }
-            w[i >> 1] = pack2(x[0], x[1]);
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<uint4 *>(op + operand_at(lrow, side * (N / 2) + c + 8 * q)) =
-                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          for (int i = 0; i < 16; ++i) gf[i] = __uint_as_float(g[i]);
+          if (edge_at(at)) poly_row<true>(r, gf, dj, poly, s_alpha, me - at, a.m - at, at_diagonal, x);
+          else poly_row<false>(r, gf, dj, poly, s_alpha, 0, 0, at_diagonal, x);
+          put_row(at, x);
         }
         release(gram_acc);
         release(acc);
         advance();
-        hand_over();
-        trade(evec, diagonal >= 0 && diagonal < N / 2, fmaf(a.c, fmaf(di, di, at_diagonal), fmaf(a.b, di, a.a)));
-        if (!(ok = wait_trade())) break;
+        hand_over(evec, on_diagonal, fmaf(a.c, fmaf(di, di, at_diagonal), fmaf(a.b, di, a.a)));
         // ---- X of this group's tiles
         if (it > 0) {
           bool r = true;
           if (lane == 0) r = wait_ready(ready, seq, abort_flag, err);
           if (!(ok = __all_sync(0xFFFFFFFFu, r))) break;
         }
-        const float own = evec[me];
         const auto place = [&](int t, int &row0, int &col) {
           row0 = (TALL ? t * N : 0) + 128 * int(rank) + 32 * quarter;
           col = (TALL ? 0 : t * N) + side * (N / 2);
@@ -1316,7 +1332,8 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           place(t, row0, col);
           if (!fetched && exists(row0, col)) fetch(slot, row0, col);
           if (!(ok = result())) break;
-          const uint32_t base = tmem_base + lanes + uint32_t(acc * N + side * (N / 2));
+          const uint32_t base = tmem_base + lanes + uint32_t(acc * N + first_col);
+          const float own = evec[me];
           fetched = false;
 #pragma unroll 1
           for (int c = 0; c < N / 2 && exists(row0, col + c); c += 32) {
