@@ -354,6 +354,32 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t bits2(float2 v) { return uint64_t(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 float2_of(uint64_t v) { return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32))); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// The low part of a pair whose high part is `high`: what fp16 left over.
+__device__ __forceinline__ uint32_t low2(float2 v, uint32_t high) {
+  const float2 h = unpack2(high), l = add2(v, make_float2(-h.x, -h.y));
+  return pack2(l.x, l.y);
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t (&r)[16], int i) { return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); }
+
 // 32 lanes x 16 consecutive 32-bit columns of tensor memory.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -440,41 +466,44 @@ __device__ __forceinline__ void write_out(const Args &a, int m_dim, int n_dim, c
   }
 }
 
-// Sixteen elements of a row of A' out of its accumulator, times `scale`.  EDGE: element `diagonal` of them is on the
-// diagonal, which is kept apart (true value) and left out, and so are elements from `limit` on.
+// EDGE: element `diagonal` of the sixteen is on the diagonal, which is kept apart (true value) and left out, and so are
+// elements from `limit` on.
 template <bool EDGE>
-__device__ __forceinline__ void gram_row(const uint32_t (&r)[16], float scale, float alpha, int diagonal, int limit,
-                                         float &at_diagonal, float (&x)[16]) {
+__device__ __forceinline__ void leave_out(const uint32_t (&r)[16], float alpha, int diagonal, int limit, float &at_diagonal,
+                                      float2 (&x)[8]) {
+  if constexpr (EDGE) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = __uint_as_float(r[i]) * scale;
-    if (EDGE) {
+    for (int i = 0; i < 16; ++i) {
       if (i == diagonal) at_diagonal = __uint_as_float(r[i]) * alpha;
-      if (i == diagonal || i >= limit) x[i] = 0.f;
+      if (i == diagonal || i >= limit) (i & 1 ? x[i >> 1].y : x[i >> 1].x) = 0.f;
     }
   }
+}
+// Sixteen elements of a row of A' out of its accumulator, times `scale`.
+template <bool EDGE>
+__device__ __forceinline__ void gram_row(const uint32_t (&r)[16], float scale, float alpha, int diagonal, int limit,
+                                         float &at_diagonal, float2 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = mul2(pair_of(r, 2 * i), both(scale));
+  leave_out<EDGE>(r, alpha, diagonal, limit, at_diagonal, x);
 }
 
 // The same of B' = b A' + c ((d_i + d_j) A' + A'^2): g holds A' and r its square, in their own scales;
-// k = {(b + c d_i), c, c}, each with the powers of two that make the sum B' in its scale.
+// k = {b + c d_i, c, c}, each with the powers of two that make the sum B' in its scale.
 template <bool EDGE>
-__device__ __forceinline__ void poly_row(const uint32_t (&r)[16], const float (&g)[16], const float (&dj)[16], const float (&k)[3],
-                                         float alpha, int diagonal, int limit, float &at_diagonal, float (&x)[16]) {
+__device__ __forceinline__ void poly_row(const uint32_t (&r)[16], const float2 (&g)[8], const float2 (&dj)[8], const float (&k)[3],
+                                         float alpha, int diagonal, int limit, float &at_diagonal, float2 (&x)[8]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = fmaf(g[i], fmaf(k[1], dj[i], k[0]), __uint_as_float(r[i]) * k[2]);
-    if (EDGE) {
-      if (i == diagonal) at_diagonal = __uint_as_float(r[i]) * alpha;
-      if (i == diagonal || i >= limit) x[i] = 0.f;
-    }
-  }
+  for (int i = 0; i < 8; ++i)
+    x[i] = fma2(g[i], fma2(both(k[1]), dj[i], both(k[0])), mul2(pair_of(r, 2 * i), both(k[2])));
+  leave_out<EDGE>(r, alpha, diagonal, limit, at_diagonal, x);
 }
 
-__device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
+__device__ __forceinline__ void load16(const float *p, float2 (&x)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float4 f = *reinterpret_cast<const float4 *>(p + 4 * q);
-    x[4 * q] = f.x, x[4 * q + 1] = f.y, x[4 * q + 2] = f.z, x[4 * q + 3] = f.w;
+    x[2 * q] = make_float2(f.x, f.y), x[2 * q + 1] = make_float2(f.z, f.w);
   }
 }
 
@@ -498,42 +527,34 @@ __device__ __forceinline__ void update_chunk(const Args &a, uint32_t taddr, uint
       h[4 * q] = hv.x, h[4 * q + 1] = hv.y, h[4 * q + 2] = hv.z, h[4 * q + 3] = hv.w;
       l[4 * q] = lv.x, l[4 * q + 1] = lv.y, l[4 * q + 2] = lv.z, l[4 * q + 3] = lv.w;
     }
-    float e[16];
+    float2 e[8], x[8];
     if (TALL) {
       load16(v + 8 * j, e);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) e[i] = own;
+      for (int i = 0; i < 8; ++i) e[i] = both(own);
     }
     tmem_ld_wait();
-    float x[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mul2(pair_of(r, 2 * i), both(alpha));
     if (early) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
-        x[i] = fmaf(e[i], hf.x, fmaf(a.a, lf.x, __uint_as_float(r[i]) * alpha));
-        x[i + 1] = fmaf(e[i + 1], hf.y, fmaf(a.a, lf.y, __uint_as_float(r[i + 1]) * alpha));
-      }
+      for (int i = 0; i < 8; ++i) x[i] = fma2(e[i], unpack2(h[i]), fma2(both(a.a), unpack2(l[i]), x[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float2 hf = unpack2(h[i >> 1]), lf = unpack2(l[i >> 1]);
-        x[i] = fmaf(e[i], hf.x + lf.x, __uint_as_float(r[i]) * alpha);
-        x[i + 1] = fmaf(e[i + 1], hf.y + lf.y, __uint_as_float(r[i + 1]) * alpha);
-      }
+      for (int i = 0; i < 8; ++i) x[i] = fma2(e[i], add2(unpack2(h[i]), unpack2(l[i])), x[i]);
     }
     if (last) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4 *>(staged + lane * 128 + (((2 * j + i) ^ (lane & 7)) << 4)) =
-            make_float4(x[4 * i] * a.x_inv, x[4 * i + 1] * a.x_inv, x[4 * i + 2] * a.x_inv, x[4 * i + 3] * a.x_inv);
+            make_float4(x[2 * i].x * a.x_inv, x[2 * i].y * a.x_inv, x[2 * i + 1].x * a.x_inv, x[2 * i + 1].y * a.x_inv);
       continue;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      h[i] = pack2(x[2 * i], x[2 * i + 1]);
-      const float2 f = unpack2(h[i]);
-      l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+      h[i] = pack2(x[i].x, x[i].y);
+      l[i] = low2(x[i], h[i]);
     }
     if (inside) {
 #pragma unroll
@@ -645,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               break;
             }
             if (is_a && rank == 0) {  // the even CTA's barrier counts both CTAs' bytes
-              mbar_arrive_expect_tx(&full[stage], half ? 2u * (A_STAGE + BOX) : 2u * STAGE);
+              mbar_arrive_expect_tx_relaxed(&full[stage], half ? 2u * (A_STAGE + BOX) : 2u * STAGE);
               armed[stage] = int(parity);
             }
             const uint32_t bar = mapa_shared(&full[stage], 0);
@@ -752,6 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *const cbar = cfull + SLOTS * ew;
     float *const v = vec[ew];
     int acc = 0, slot = 0, set = 0;        // set: which half of the slots a chunk of A' leaves by
+    int ahead = 0;                         // chunks fetched and not yet worked on, from `slot` on
     uint32_t acc_parity = 0, cparity = 0;  // bit s: the parity that slot s's next copy completes
     int flying = 0;                        // bit s: a copy into slot s that nobody has waited for
     bool ok = true;
@@ -767,29 +789,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
-      // Old values of a chunk into slot s.  The next chunk's go into the next slot while this one is worked on, which the
-      // chunk before the last one left: all stores but the latest have read their slots.
-      const auto fetch = [&](int s, int k, int row0, int col) {  // lane 0
-        mbar_arrive_expect_tx(&cbar[s], 2 * PART);
-        tma_load_2d(from_hi, &cbar[s], mine + s * SLOT, col, k * p.out_rows + row0);
-        tma_load_2d(from_lo, &cbar[s], mine + s * SLOT + PART, col, k * p.out_rows + row0);
-      };
+      // Old values are fetched in the order in which chunks are worked on, up to three chunks at a time (two where the
+      // chunk before leaves its slot to the result).
       const auto exists = [&](int row0, int col) { return row0 < p.out_rows && col < p.n_dim; };
-      bool fetched = false;  // the coming chunk's copy is under way
+      int fu = first, fc = 0, fk = 0, frow = 0, fcol = 0, fwide = 0;  // the next to fetch: unit and column in it
+      bool funit = false;                                            // fk .. fwide are of unit fu
+      const auto fetch_next = [&] {
+        for (; fu < p.units; fu += step, fc = 0, funit = false) {
+          if (!funit) {
+            int row, col;
+            bool half;
+            if (!decode<TALL>(p, kind, fu, fk, row, col, half)) continue;
+            fwide = half ? BN / 4 : BN / 2;
+            frow = row + BMC * int(rank) + 32 * quarter, fcol = col + side * fwide;
+            funit = true;
+          }
+          if (fc < fwide && exists(frow, fcol + fc)) break;
+        }
+        if (fu >= p.units) return;
+        const int q = slot + ahead < SLOTS ? slot + ahead : slot + ahead - SLOTS;
+        if (lane == 0) {
+          mbar_arrive_expect_tx_relaxed(&cbar[q], 2 * PART);
+          tma_load_2d(from_hi, &cbar[q], mine + q * SLOT, fcol + fc, fk * p.out_rows + frow);
+          tma_load_2d(from_lo, &cbar[q], mine + q * SLOT + PART, fcol + fc, fk * p.out_rows + frow);
+        }
+        flying |= 1 << q;
+        ++ahead;
+        fc += 32;
+      };
+      if (kind != kGram)
+        for (int i = 0; i < (last ? SLOTS - 1 : SLOTS); ++i) fetch_next();
       for (int u = first; ok && u < p.units; u += step) {
         int k, row, col;
         bool half;
         if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
         const int wide = half ? BN / 4 : BN / 2;  // this warp's columns
         const int row0 = row + BMC * int(rank) + 32 * quarter, c0 = col + side * wide, me = row0 + lane;
-        if (kind != kGram && !fetched && exists(row0, c0)) {
-          if (lane == 0) {
-            bulk_wait_group_read<1>();
-            fetch(slot, k, row0, c0);
-          }
-          flying |= 1 << slot;
-          fetched = true;
-        }
         // d or e of this lane's row and of the columns
         float own = 0.f, t[4] = {0.f, 0.f, 0.f, 0.f};
         if (kind != kGram) {
@@ -811,27 +846,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < wide; c += 32) {
           const int at = c0 + c;
           if (!exists(row0, at)) break;
-          const int next = slot == SLOTS - 1 ? 0 : slot + 1;
+          // the slot that the chunk before left: its store has read it by now
+          const auto refill = [&] {
+            if (ahead < SLOTS) {
+              if (lane == 0) bulk_wait_group_read<0>();
+              fetch_next();
+            }
+          };
           if (kind != kGram) {
-            // the coming chunk: the next of this unit, or the next unit's first
-            int nk = k, nrow = row0, ncol = at + 32;
-            bool more = c + 32 < wide && exists(nrow, ncol);
-            for (int nu = u + step; !more && nu < p.units; nu += step) {
-              int rr, cc;
-              bool hh;
-              if (!decode<TALL>(p, kind, nu, nk, rr, cc, hh)) continue;
-              nrow = rr + BMC * int(rank) + 32 * quarter, ncol = cc + side * (hh ? BN / 4 : BN / 2);
-              more = exists(nrow, ncol);
-              break;  // a unit without a chunk for this warp: the one after it starts its own fetch
-            }
-            if (more) {
-              if (lane == 0) {
-                bulk_wait_group_read<1>();
-                fetch(next, nk, nrow, ncol);
-              }
-              flying |= 1 << next;
-            }
-            fetched = more;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u))) {
               ok = false;
               break;
@@ -849,8 +871,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float at_diagonal = 0.f;
           if (kind == kUpdate) {
             update_chunk<TALL>(a, base + uint32_t(c), hi_part, lo_part, staged, v, own, me < p.m_dim, early, last, lane);
+            if (!last) refill();
             send_chunk(a, &maps.c_hi[~(ph / 3) & 1], &maps.c_lo, hi_part, lo_part, staged, last, lane, k, p.m_dim, p.n_dim,
                        p.out_rows, row0, at);
+            if (last) refill();
           } else {
             const float alpha = kind == kGram ? a.x_inv * a.x_inv : a.gram_inv * a.gram_inv;
             const float poly[3] = {fmaf(a.c, own, a.b) * a.gram_inv * a.poly_scale, a.c * a.gram_inv * a.poly_scale,
@@ -861,13 +885,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t r[16];
               tmem_ld_32x32b_x16(base + uint32_t(c + 8 * j), r);
               uint32_t h[8], l[8];
-              float x[16];
+              float2 x[8];
               if (kind == kGram) {
                 tmem_ld_wait();
                 if (edge) gram_row<true>(r, alpha * a.gram_scale, alpha, diagonal - 8 * j, 16, at_diagonal, x);
                 else gram_row<false>(r, alpha * a.gram_scale, alpha, 0, 0, at_diagonal, x);
               } else {
-                float g[16], dj[16];
+                float2 g[8], dj[8];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   const uint4 hv = *reinterpret_cast<const uint4 *>(hi_part + piece_at(lane, j + q));
@@ -877,22 +901,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 load16(v + 8 * j, dj);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float2 hf = unpack2(h[i]), lf = unpack2(l[i]);
-                  g[2 * i] = hf.x + lf.x, g[2 * i + 1] = hf.y + lf.y;
-                }
+                for (int i = 0; i < 8; ++i) g[i] = add2(unpack2(h[i]), unpack2(l[i]));
                 tmem_ld_wait();
                 if (edge) poly_row<true>(r, g, dj, poly, alpha, diagonal - 8 * j, 16, at_diagonal, x);
                 else poly_row<false>(r, g, dj, poly, alpha, 0, 0, at_diagonal, x);
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) h[i] = pack2(x[2 * i], x[2 * i + 1]);
-              if (kind == kGram) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float2 f = unpack2(h[i]);
-                  l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
-                }
+              for (int i = 0; i < 8; ++i) {
+                h[i] = pack2(x[i].x, x[i].y);
+                if (kind == kGram) l[i] = low2(x[i], h[i]);
               }
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
@@ -913,6 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               __syncwarp();  // every lane has read its low part
               transpose_chunk(hi_part, image, lane);
             }
+            if (kind == kPoly) refill();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -924,8 +942,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               bulk_commit_group();
             }
           }
-          if (kind == kGram) set ^= 1;
-          else slot = next;
+          if (kind == kGram) {
+            set ^= 1;
+          } else {
+            slot = slot == SLOTS - 1 ? 0 : slot + 1;
+            --ahead;
+          }
         }
         if (!ok) break;
         tc_fence_before();
@@ -1088,7 +1110,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           const auto block = [&](bool along, int i0, int c0) {
             if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) return false;
             if (rank == 0) {
-              mbar_arrive_expect_tx(&full[stage], G * R_STAGE);
+              mbar_arrive_expect_tx_relaxed(&full[stage], G * R_STAGE);
               armed[stage] = int(parity);
             }
             uint8_t *to = ring + stage * R_STAGE;
@@ -1208,7 +1230,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *const cbar = cfull + SLOTS * ew;
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const int m_dim = s.rows, n_dim = s.cols;
-    int acc = 0, slot = 0, seq = 0;
+    int acc = 0, slot = 0, ahead = 0, seq = 0;
     uint32_t acc_parity = 0, cparity = 0;
     int flying = 0;
     bool ok = true;
@@ -1247,19 +1269,55 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
     const bool exists_row = me < a.m;
     // Whether sixteen columns from c on need more than arithmetic: a piece of the diagonal, the matrix's end.
     const auto edge_at = [&](int c) { return c + 16 > a.m || (c < first_row + 32 && c + 16 > first_row); };
-    const auto put_row = [&](int c, const float (&x)[16]) {
+    const auto put_row = [&](int c, const float2 (&x)[8]) {
       if (exists_row) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           *reinterpret_cast<uint4 *>(op + operand_at(lrow, c + 8 * q)) =
-              make_uint4(pack2(x[8 * q], x[8 * q + 1]), pack2(x[8 * q + 2], x[8 * q + 3]), pack2(x[8 * q + 4], x[8 * q + 5]),
-                         pack2(x[8 * q + 6], x[8 * q + 7]));
+              make_uint4(pack2(x[4 * q].x, x[4 * q].y), pack2(x[4 * q + 1].x, x[4 * q + 1].y),
+                         pack2(x[4 * q + 2].x, x[4 * q + 2].y), pack2(x[4 * q + 3].x, x[4 * q + 3].y));
       }
     };
     for (int k = group; ok && k < s.count; k += s.groups) {
       for (int it = 0; ok && it < a.steps; ++it, ++seq) {
         const bool early = it < 2, last = it + 1 == a.steps;
         const CUtensorMap *const from = &maps.c_hi[it & 1], *const to = &maps.c_hi[~it & 1];
+        // ---- the old X of this group's first chunks, under way while A and B are formed
+        if (it > 0) {
+          bool r = true;
+          if (lane == 0) r = wait_ready(ready, seq, abort_flag, err);
+          if (!(ok = __all_sync(0xFFFFFFFFu, r))) break;
+        }
+        const auto place = [&](int t, int &row0, int &col) {
+          row0 = (TALL ? t * N : 0) + 128 * int(rank) + 32 * quarter;
+          col = (TALL ? 0 : t * N) + side * (N / 2);
+        };
+        const auto exists = [&](int row0, int col) { return row0 < s.stand && col < n_dim; };
+        int ft = part, fc = 0;  // the next chunk to fetch
+        const auto fetch_next = [&] {
+          int row0 = 0, col = 0;
+          for (; ft < s.tiles; ft += s.parts, fc = 0) {
+            place(ft, row0, col);
+            if (fc < N / 2 && exists(row0, col + fc)) break;
+          }
+          if (ft >= s.tiles) return;
+          const int q = slot + ahead < SLOTS ? slot + ahead : slot + ahead - SLOTS;
+          if (lane == 0) {
+            mbar_arrive_expect_tx_relaxed(&cbar[q], 2 * PART);
+            tma_load_2d(from, &cbar[q], mine + q * SLOT, col + fc, k * s.stand + row0);
+            tma_load_2d(&maps.c_lo, &cbar[q], mine + q * SLOT + PART, col + fc, k * s.stand + row0);
+          }
+          flying |= 1 << q;
+          ++ahead;
+          fc += 32;
+        };
+        const auto refill = [&] {  // the slot that the chunk before left: its store has read it by now
+          if (ahead < SLOTS) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            fetch_next();
+          }
+        };
+        for (int i = 0; i < (last ? SLOTS - 1 : SLOTS); ++i) fetch_next();
         // ---- A: the diagonal to d, the rest as fp16
         if (!(ok = result())) break;
         const int gram_acc = acc;
@@ -1275,7 +1333,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t r[16];
           tmem_ld_32x32b_x16(gram + uint32_t(c), r);
           tmem_ld_wait();
-          float x[16];
+          float2 x[8];
           if (edge_at(at)) gram_row<true>(r, g_alpha * a.gram_scale, g_alpha, me - at, a.m - at, at_diagonal, x);
           else gram_row<false>(r, g_alpha * a.gram_scale, g_alpha, 0, 0, at_diagonal, x);
           put_row(at, x);
@@ -1293,11 +1351,11 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t r[16], g[16];
           tmem_ld_32x32b_x16(square + uint32_t(c), r);
           tmem_ld_32x32b_x16(gram + uint32_t(c), g);
-          float dj[16], gf[16], x[16];
+          float2 dj[8], gf[8], x[8];
           load16(dvec + at, dj);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) gf[i] = __uint_as_float(g[i]);
+          for (int i = 0; i < 8; ++i) gf[i] = pair_of(g, 2 * i);
           if (edge_at(at)) poly_row<true>(r, gf, dj, poly, s_alpha, me - at, a.m - at, at_diagonal, x);
           else poly_row<false>(r, gf, dj, poly, s_alpha, 0, 0, at_diagonal, x);
           put_row(at, x);
@@ -1307,45 +1365,14 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
         advance();
         hand_over(evec, on_diagonal, fmaf(a.c, fmaf(di, di, at_diagonal), fmaf(a.b, di, a.a)));
         // ---- X of this group's tiles
-        if (it > 0) {
-          bool r = true;
-          if (lane == 0) r = wait_ready(ready, seq, abort_flag, err);
-          if (!(ok = __all_sync(0xFFFFFFFFu, r))) break;
-        }
-        const auto place = [&](int t, int &row0, int &col) {
-          row0 = (TALL ? t * N : 0) + 128 * int(rank) + 32 * quarter;
-          col = (TALL ? 0 : t * N) + side * (N / 2);
-        };
-        const auto exists = [&](int row0, int col) { return row0 < s.stand && col < n_dim; };
-        const auto fetch = [&](int q, int row0, int col) {
-          if (lane == 0) {
-            bulk_wait_group_read<1>();
-            mbar_arrive_expect_tx(&cbar[q], 2 * PART);
-            tma_load_2d(from, &cbar[q], mine + q * SLOT, col, k * s.stand + row0);
-            tma_load_2d(&maps.c_lo, &cbar[q], mine + q * SLOT + PART, col, k * s.stand + row0);
-          }
-          flying |= 1 << q;
-        };
-        bool fetched = false;
         for (int t = part; ok && t < s.tiles; t += s.parts) {
           int row0, col;
           place(t, row0, col);
-          if (!fetched && exists(row0, col)) fetch(slot, row0, col);
           if (!(ok = result())) break;
           const uint32_t base = tmem_base + lanes + uint32_t(acc * N + first_col);
           const float own = evec[me];
-          fetched = false;
 #pragma unroll 1
           for (int c = 0; c < N / 2 && exists(row0, col + c); c += 32) {
-            const int next = slot == SLOTS - 1 ? 0 : slot + 1;
-            int nrow = row0, ncol = col + c + 32;
-            bool more = c + 32 < N / 2 && exists(nrow, ncol);
-            if (!more && t + s.parts < s.tiles) {
-              place(t + s.parts, nrow, ncol);
-              more = exists(nrow, ncol);
-            }
-            if (more) fetch(next, nrow, ncol);
-            fetched = more;
             if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u)))) break;
             cparity ^= 1u << slot;
             flying &= ~(1 << slot);
@@ -1354,8 +1381,11 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
             update_chunk<TALL>(a, base + uint32_t(c), hi, lo, staged, &evec[TALL ? col + c : 0], own, row0 + lane < m_dim, early,
                                last, lane);
+            if (!last) refill();
             send_chunk(a, to, &maps.c_lo, hi, lo, staged, last, lane, k, m_dim, n_dim, s.stand, row0, col + c);
-            slot = next;
+            if (last) refill();
+            slot = slot == SLOTS - 1 ? 0 : slot + 1;
+            --ahead;
           }
           if (!ok) break;
           release(acc);
