@@ -246,10 +246,11 @@ struct Phase {
 };
 
 struct Maps {
-  CUtensorMap x[2], gram, poly;                                   // operands: 64 x 64 boxes
+  CUtensorMap x[2], gram, poly;                                   // operands: boxes of 64 rows of 64 elements
+  CUtensorMap x_tall[2], gram_tall, poly_tall;                    // and of 128 rows
   CUtensorMap c_hi[2], c_lo, c_gram, c_gram_lo, c_poly;           // 32 x 32 chunks
 };
-static_assert(sizeof(Maps) == 10 * sizeof(CUtensorMap), "prefetched one by one");
+static_assert(sizeof(Maps) == 14 * sizeof(CUtensorMap), "prefetched one by one");
 
 struct Args {
   Phase phase[3];
@@ -623,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     *finished = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane < 10) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
+  if (warp == 0 && lane < 14) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 2 * BN);
     tmem_relinquish_pair();
@@ -637,18 +638,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 2) {
     if (lane == 0) {  // ------------------------------------ producers (both CTAs): warp 0 A, warp 2 B
+      // A block's copies are one or two a thread and little else: the threads' issuing bounds the kernel where the loop is
+      // longer (two 64-row boxes in place of one of 128 rows, and the arming kept in an array: 590 cycles a block for the
+      // 256 that its MMAs take).
       const bool is_a = warp == 0;
       int stage = 0;
-      uint32_t parity = 0;
-      int armed[STAGES];
-      for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+      uint32_t parity = 0, armed = 0, armed_parity = 0;  // bit s: stage s has been armed, and for which phase
+      const uint32_t bars = mapa_shared(full, 0);
       bool ok = true;
       for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
         const Phase &p = a.phase[kind];
         if (first >= p.units) continue;
-        const CUtensorMap *x = &maps.x[(ph / 3) & 1];
+        const int xi = (ph / 3) & 1;
         const bool mn = kind == kGram ? TALL : kind == kUpdate && !is_a && !TALL;  // rows of the box run along K
-        const CUtensorMap *map = kind == kGram ? x : kind == kPoly ? &maps.gram : is_a == TALL ? x : &maps.poly;
+        const bool of_x = kind == kGram || (kind == kUpdate && is_a == TALL);
+        const CUtensorMap *map = of_x ? &maps.x[xi] : kind == kPoly ? &maps.gram : &maps.poly;
+        const CUtensorMap *tall_map = of_x ? &maps.x_tall[xi] : kind == kPoly ? &maps.gram_tall : &maps.poly_tall;
         const int rows = is_a ? p.a_rows : p.b_rows;
         bool waited = false;
         for (int u = first; ok && u < p.units; u += step) {
@@ -656,26 +661,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bool half;
           if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
           // this CTA's 128 rows of A, 128 or 64 of B
-          const int i0 = is_a ? row + BMC * int(rank) : col + (half ? 64 : 128) * int(rank);
-          const int boxes = is_a || !half ? 2 : 1;
+          const bool whole = is_a || !half;
+          const int i0 = is_a ? row + BMC * int(rank) : col + (half ? 64 : 128) * int(rank), r0 = k * rows;
+          const uint32_t bytes = half ? 2u * (A_STAGE + BOX) : 2u * STAGE;
+          const CUtensorMap *const use = whole && !mn ? tall_map : map;
           if (!waited && !(ok = wait_ready(ready, ph, abort_flag, err))) break;
           waited = true;
+          int cx = mn ? i0 : 0, cy = mn ? r0 : r0 + i0;
+          const int dx = mn ? 0 : BK, dy = mn ? BK : 0;
+          uint8_t *const base = is_a ? sA : sB;
           for (int kb = 0; kb < p.k_blocks; ++kb) {
             if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) {
               ok = false;
               break;
             }
             if (is_a && rank == 0) {  // the even CTA's barrier counts both CTAs' bytes
-              mbar_arrive_expect_tx_relaxed(&full[stage], half ? 2u * (A_STAGE + BOX) : 2u * STAGE);
-              armed[stage] = int(parity);
+              mbar_arrive_expect_tx_relaxed(&full[stage], bytes);
+              armed |= 1u << stage;
+              armed_parity = (armed_parity & ~(1u << stage)) | parity << stage;
             }
-            const uint32_t bar = mapa_shared(&full[stage], 0);
-            uint8_t *to = (is_a ? sA : sB) + stage * A_STAGE;
-            for (int i = 0; i < boxes; ++i) {
-              const int at = i0 + 64 * i;
-              if (mn) tma_load_2d_pair(map, bar, to + i * BOX, at, k * rows + kb * BK);
-              else tma_load_2d_pair(map, bar, to + i * BOX, kb * BK, k * rows + at);
-            }
+            uint8_t *const to = base + stage * A_STAGE;
+            tma_load_2d_pair(use, bars + 8 * stage, to, cx, cy);
+            if (mn && whole) tma_load_2d_pair(use, bars + 8 * stage, to + BOX, cx + 64, cy);
+            cx += dx, cy += dy;
             if (++stage == STAGES) {
               stage = 0;
               parity ^= 1u;
@@ -684,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       for (int s = 0; s < STAGES; ++s)  // every armed copy has landed before the pair leaves
-        if (armed[s] >= 0) drain(&full[s], uint32_t(armed[s]));
+        if (armed >> s & 1) drain(&full[s], armed_parity >> s & 1);
     }
   } else if (warp == 1) {  // ---------------------------------------------- MMA (the even CTA)
     if (rank == 0) {
@@ -1006,7 +1014,7 @@ struct SmallArgs {
 };
 
 struct SmallMaps {
-  CUtensorMap x[2], c_hi[2], c_lo;
+  CUtensorMap x[2], x_tall[2], c_hi[2], c_lo;
 };
 
 template <int G>
@@ -1075,7 +1083,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
   for (int i = threadIdx.x; i < S::OP / 16; i += kThreads)  // what lies beside A' and B' stays zero
     reinterpret_cast<uint4 *>(op)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (warp == 0 && lane < 5) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
+  if (warp == 0 && lane < 7) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
   if (warp == 1) {
     if (G == 2) {
       tmem_alloc_pair(tmem_slot, 2 * N);
@@ -1095,43 +1103,45 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {  // -------------------------------------------------- producer: X's tiles, GRAM's then UPDATE's
       int stage = 0;
-      uint32_t parity = 0;
-      int armed[S::STAGES];
-      for (int i = 0; i < S::STAGES; ++i) armed[i] = -1;
+      uint32_t parity = 0, armed = 0, armed_parity = 0;  // bit s: stage s has been armed, and for which phase
+      const uint32_t bars = mapa_shared(full, 0);
       bool ok = true;
       int seq = 0;
       for (int k = group; ok && k < s.count; k += s.groups) {
         const int r0 = k * s.stand;
         for (int it = 0; ok && it < a.steps; ++it, ++seq) {
-          const CUtensorMap *x = &maps.x[it & 1];
           if (it > 0 && !(ok = wait_ready(ready, seq, abort_flag, err))) break;
-          // one block: 128 indices of a tile from i0 on, 64 of the contraction from c0 on; along: the contraction runs
-          // along X's rows
-          const auto block = [&](bool along, int i0, int c0) {
-            if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) return false;
-            if (rank == 0) {
-              mbar_arrive_expect_tx_relaxed(&full[stage], G * R_STAGE);
-              armed[stage] = int(parity);
-            }
-            uint8_t *to = ring + stage * R_STAGE;
-            for (int i = 0; i < 2; ++i) {
-              const int cx = along ? c0 : i0 + 64 * i, cy = r0 + (along ? i0 + 64 * i : c0);
-              if (G == 2) tma_load_2d_pair(x, mapa_shared(&full[stage], 0), to + i * BOX, cx, cy);
-              else tma_load_2d(x, &full[stage], to + i * BOX, cx, cy);
-            }
-            if (++stage == S::STAGES) {
-              stage = 0;
-              parity ^= 1u;
+          // blocks of 128 indices of a tile from i0 on, 64 of the contraction each; along: it runs along X's rows
+          const auto blocks = [&](bool along, int i0, int n) {
+            const CUtensorMap *const x = along ? &maps.x_tall[it & 1] : &maps.x[it & 1];
+            int cx = along ? 0 : i0, cy = along ? r0 + i0 : r0;
+            for (int b = 0; b < n; ++b) {
+              if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) return false;
+              if (rank == 0) {
+                mbar_arrive_expect_tx_relaxed(&full[stage], G * R_STAGE);
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | parity << stage;
+              }
+              uint8_t *const to = ring + stage * R_STAGE;
+              for (int i = 0; i < (along ? 1 : 2); ++i) {
+                if (G == 2) tma_load_2d_pair(x, bars + 8 * stage, to + i * BOX, cx + 64 * i, cy);
+                else tma_load_2d(x, &full[stage], to + i * BOX, cx + 64 * i, cy);
+              }
+              if (along) cx += BK;
+              else cy += BK;
+              if (++stage == S::STAGES) {
+                stage = 0;
+                parity ^= 1u;
+              }
             }
             return true;
           };
-          for (int b = 0; ok && b < s.gram_blocks; ++b) ok = block(!TALL, 128 * int(rank), b * BK);
-          for (int t = part; ok && t < s.tiles; t += s.parts)
-            for (int b = 0; ok && b < s.poly_blocks; ++b) ok = block(TALL, t * N + 128 * int(rank), b * BK);
+          ok = blocks(!TALL, 128 * int(rank), s.gram_blocks);
+          for (int t = part; ok && t < s.tiles; t += s.parts) ok = blocks(TALL, t * N + 128 * int(rank), s.poly_blocks);
         }
       }
       for (int i = 0; i < S::STAGES; ++i)
-        if (armed[i] >= 0) drain(&full[i], uint32_t(armed[i]));
+        if (armed >> i & 1) drain(&full[i], armed_parity >> i & 1);
     }
   } else if (warp == 1) {  // ---------------------------------------------- MMA (the even CTA)
     if (rank == 0) {
@@ -1550,10 +1560,11 @@ void shape(Phase &p, int64_t count, bool symmetric, int64_t k, int pairs) {
 // Matrices of rows x inner fp16, one after another on `stand` rows each.  A box that passes a matrix's last row stays
 // in it or reads the next one's: harmless where rows are the product's rows or columns (nobody takes those), and where
 // they are the contraction they are zeros.
-gtp_status map_of(CUtensorMap *map, const void *base, int64_t inner, int64_t stand, int64_t ld, int64_t count, bool chunk) {
+// box: 32, a chunk of 32 x 32; 64 or 128, as many rows of 64 elements.
+gtp_status map_of(CUtensorMap *map, const void *base, int64_t inner, int64_t stand, int64_t ld, int64_t count, uint32_t box) {
   return gtp::encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, uint64_t(inner), uint64_t(count * stand),
-                             uint64_t(2 * ld), chunk ? 32 : 64, chunk ? 32 : 64,
-                             chunk ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                             uint64_t(2 * ld), box == 32 ? 32 : 64, box,
+                             box == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // What both kernels need: the iteration's constants and the powers of two that keep every fp16 value in range.
@@ -1586,17 +1597,18 @@ gtp_status iterate(Args a, const Plan &plan, char *ws, int64_t count, int64_t ro
     shape(p, count, !update, kind == kGram ? plan.n : plan.m, pairs);
   }
   Maps maps;
-  const auto x_map = [&](CUtensorMap *m, int64_t at, bool chunk) {
-    return map_of(m, ws + at, cols, plan.rows, plan.ldx, count, chunk);
+  const auto x_map = [&](CUtensorMap *m, int64_t at, uint32_t box) {
+    return map_of(m, ws + at, cols, plan.rows, plan.ldx, count, box);
   };
-  const auto g_map = [&](CUtensorMap *m, int64_t at, bool chunk) {
-    return map_of(m, ws + at, plan.m, plan.grows, plan.ldg, count, chunk);
+  const auto g_map = [&](CUtensorMap *m, int64_t at, uint32_t box) {
+    return map_of(m, ws + at, plan.m, plan.grows, plan.ldg, count, box);
   };
-  for (const gtp_status e : {x_map(&maps.x[0], plan.hi[0], false), x_map(&maps.x[1], plan.hi[1], false),
-                             g_map(&maps.gram, plan.gram, false), g_map(&maps.poly, plan.poly, false),
-                             x_map(&maps.c_hi[0], plan.hi[0], true), x_map(&maps.c_hi[1], plan.hi[1], true),
-                             x_map(&maps.c_lo, plan.lo, true), g_map(&maps.c_gram, plan.gram, true),
-                             g_map(&maps.c_gram_lo, plan.gram_lo, true), g_map(&maps.c_poly, plan.poly, true)})
+  for (const gtp_status e :
+       {x_map(&maps.x[0], plan.hi[0], 64), x_map(&maps.x[1], plan.hi[1], 64), x_map(&maps.x_tall[0], plan.hi[0], 128),
+        x_map(&maps.x_tall[1], plan.hi[1], 128), g_map(&maps.gram, plan.gram, 64), g_map(&maps.poly, plan.poly, 64),
+        g_map(&maps.gram_tall, plan.gram, 128), g_map(&maps.poly_tall, plan.poly, 128), x_map(&maps.c_hi[0], plan.hi[0], 32),
+        x_map(&maps.c_hi[1], plan.hi[1], 32), x_map(&maps.c_lo, plan.lo, 32), g_map(&maps.c_gram, plan.gram, 32),
+        g_map(&maps.c_gram_lo, plan.gram_lo, 32), g_map(&maps.c_poly, plan.poly, 32)})
     if (e) return e;
   const int used = std::min(pairs, std::max({a.phase[0].units, a.phase[1].units, a.phase[2].units}));
   return launch_together(newton_schulz_kernel<TALL>, 2 * used, SMEM_TOTAL, st, maps, a);
@@ -1615,11 +1627,14 @@ gtp_status iterate_small(const Args &a, const Plan &plan, char *ws, int64_t coun
   s.parts = std::max(1, std::min(s.tiles, clusters / s.count));
   s.groups = std::min(s.count, clusters / s.parts);
   SmallMaps maps;
-  for (int i = 0; i < 5; ++i) {
-    const int64_t at = i == 4 ? plan.lo : plan.hi[i & 1];
-    CUtensorMap *m = i < 2 ? &maps.x[i] : i < 4 ? &maps.c_hi[i - 2] : &maps.c_lo;
-    if (gtp_status e = map_of(m, ws + at, cols, plan.rows, plan.ldx, count, i >= 2)) return e;
-  }
+  const auto x_map = [&](CUtensorMap *m, int64_t at, uint32_t box) {
+    return map_of(m, ws + at, cols, plan.rows, plan.ldx, count, box);
+  };
+  for (const gtp_status e :
+       {x_map(&maps.x[0], plan.hi[0], 64), x_map(&maps.x[1], plan.hi[1], 64), x_map(&maps.x_tall[0], plan.hi[0], 128),
+        x_map(&maps.x_tall[1], plan.hi[1], 128), x_map(&maps.c_hi[0], plan.hi[0], 32), x_map(&maps.c_hi[1], plan.hi[1], 32),
+        x_map(&maps.c_lo, plan.lo, 32)})
+    if (e) return e;
   return launch_together(newton_schulz_small_kernel<G, TALL>, G * s.parts * s.groups, Small<G>::SMEM, st, maps, a, s);
 }
 
