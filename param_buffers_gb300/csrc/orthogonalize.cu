@@ -91,46 +91,50 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
-// The elements of item i of matrix k (four consecutive ones of a row with VEC, else one): the matrix's own, or the
-// step's u.  FIRST: the pass that writes the momentum; the second finds it written and clears the gradient.
-template <typename T, bool VEC, bool STEP, bool FIRST>
-__device__ __forceinline__ void source_at(const Source &s, int k, int i, float g_scale, int &row, int &col,
-                                          float (&x)[VEC ? 4 : 1]) {
-  constexpr int E = VEC ? 4 : 1;
-  row = gtp::fast_div(i, s.by_cols);
-  col = (i - row * (s.cols / E)) * E;
-  if (!STEP) {
-    const T *p = static_cast<const T *>(s.src) + k * s.plane + row * s.ld + col;
-    if constexpr (VEC) load4(p, x);
-    else x[0] = load1(p);
-    return;
+// Item i of matrix k, four consecutive elements of a row with VEC, else one: the matrix's own, or the gradient and the
+// momentum that the step's u comes from.
+template <typename T, bool VEC, bool STEP>
+struct Item {
+  static constexpr int E = VEC ? 4 : 1;
+  float g[E], m[STEP ? E : 1];
+  int row, col;
+
+  __device__ __forceinline__ int64_t at(const Source &s, int k) const { return s.offset[k] + int64_t(row) * s.cols + col; }
+  __device__ __forceinline__ void load(const Source &s, int k, int i) {
+    row = gtp::fast_div(i, s.by_cols);
+    col = (i - row * (s.cols / E)) * E;
+    const T *const p = STEP ? static_cast<const T *>(s.grad) + at(s, k) : static_cast<const T *>(s.src) + k * s.plane + row * s.ld + col;
+    if constexpr (VEC) load4(p, g);
+    else g[0] = load1(p);
+    if constexpr (STEP) {
+      if constexpr (VEC) load4(s.momentum + at(s, k), m);
+      else m[0] = s.momentum[at(s, k)];
+    }
   }
-  const int64_t at = s.offset[k] + int64_t(row) * s.cols + col;
-  T *const gp = static_cast<T *>(s.grad) + at;
-  float *const mp = s.momentum + at;
-  float g[E], m[E];
-  if constexpr (VEC) {
-    load4(gp, g);
-    load4(mp, m);
-  } else {
-    g[0] = load1(gp);
-    m[0] = *mp;
-  }
+  // The values to orthogonalise, in g.  FIRST: the pass that writes the momentum; the second one finds it written and
+  // clears the gradient.
+  template <bool FIRST>
+  __device__ __forceinline__ void finish(const Source &s, int k, float g_scale) {
+    if constexpr (STEP) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    g[e] *= g_scale;
-    if (FIRST) m[e] = fmaf(s.mu, m[e], (1.f - s.mu) * g[e]);
-    x[e] = s.nesterov ? fmaf(s.mu, m[e], (1.f - s.mu) * g[e]) : m[e];
+      for (int e = 0; e < E; ++e) {
+        g[e] *= g_scale;
+        if (FIRST) m[e] = fmaf(s.mu, m[e], (1.f - s.mu) * g[e]);
+        g[e] = s.nesterov ? fmaf(s.mu, m[e], (1.f - s.mu) * g[e]) : m[e];
+      }
+      if (FIRST) {
+        float *const mp = s.momentum + at(s, k);
+        if constexpr (VEC) *reinterpret_cast<float4 *>(mp) = make_float4(m[0], m[1], m[2], m[3]);
+        else *mp = m[0];
+      } else if (s.zero_grad) {
+        T *const gp = static_cast<T *>(s.grad) + at(s, k);
+        if constexpr (!VEC) gp[0] = T(0.f);
+        else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(gp) = make_float4(0.f, 0.f, 0.f, 0.f);
+        else *reinterpret_cast<uint2 *>(gp) = make_uint2(0u, 0u);
+      }
+    }
   }
-  if (FIRST) {
-    if constexpr (VEC) *reinterpret_cast<float4 *>(mp) = make_float4(m[0], m[1], m[2], m[3]);
-    else *mp = m[0];
-  } else if (s.zero_grad) {
-    if constexpr (!VEC) gp[0] = T(0.f);
-    else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(gp) = make_float4(0.f, 0.f, 0.f, 0.f);
-    else *reinterpret_cast<uint2 *>(gp) = make_uint2(0u, 0u);
-  }
-}
+};
 
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double sums[32];
@@ -144,7 +148,7 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-constexpr int kPassThreads = 256;
+constexpr int kPassThreads = 256, kFlight = 4;  // items of a thread whose loads are under way together
 
 // Sums of squares, a block's part each (and the new momentum).
 template <typename T, bool VEC, bool STEP>
@@ -154,17 +158,19 @@ __global__ void __launch_bounds__(kPassThreads)
   wait_prior_grid();
   const float g_scale = STEP ? s.factor * (s.grad_scale ? *s.grad_scale : 1.f) : 1.f;
   double total = 0;
-  for (int64_t i0 = int64_t(blockIdx.x) * kPassThreads; i0 < s.items; i0 += 4 * int64_t(gridDim.x) * kPassThreads) {
+  const int64_t step = int64_t(gridDim.x) * kPassThreads;
+  for (int64_t i0 = int64_t(blockIdx.x) * kPassThreads + threadIdx.x; i0 < s.items; i0 += kFlight * step) {
+    Item<T, VEC, STEP> x[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j)
+      if (i0 + j * step < s.items) x[j].load(s, blockIdx.y, int(i0 + j * step));
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t i = i0 + int64_t(j) * gridDim.x * kPassThreads + threadIdx.x;
-      if (i < s.items) {
-        int row, col;
-        float x[VEC ? 4 : 1];
-        source_at<T, VEC, STEP, true>(s, blockIdx.y, int(i), g_scale, row, col, x);
+    for (int j = 0; j < kFlight; ++j) {
+      if (i0 + j * step < s.items) {
+        x[j].template finish<true>(s, blockIdx.y, g_scale);
 #pragma unroll
-        for (int e = 0; e < (VEC ? 4 : 1); ++e) sum = fmaf(x[e], x[e], sum);
+        for (int e = 0; e < Item<T, VEC, STEP>::E; ++e) sum = fmaf(x[j].g[e], x[j].g[e], sum);
       }
     }
     total += double(sum);
@@ -194,24 +200,31 @@ __global__ void __launch_bounds__(kPassThreads)
     *reinterpret_cast<uint4 *>(f.hi + at) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4 *>(f.hi_next + at) = make_uint4(0, 0, 0, 0);
   }
-  for (int64_t i = me; i < s.items; i += step) {
-    int row, col;
-    float x[VEC ? 4 : 1];
-    source_at<T, VEC, STEP, false>(s, blockIdx.y, int(i), g_scale, row, col, x);
-    const int64_t at = blockIdx.y * f.planex + row * f.ldx + col;
-    __half hi[VEC ? 4 : 1], lo[VEC ? 4 : 1];
+  for (int64_t i0 = me; i0 < s.items; i0 += int64_t(kFlight) * step) {
+    Item<T, VEC, STEP> x[kFlight];
 #pragma unroll
-    for (int e = 0; e < (VEC ? 4 : 1); ++e) {
-      const float v = x[e] * r;
-      hi[e] = __float2half_rn(v);
-      lo[e] = __float2half_rn(v - __half2float(hi[e]));
-    }
-    if constexpr (VEC) {
-      *reinterpret_cast<uint2 *>(f.hi + at) = *reinterpret_cast<const uint2 *>(hi);
-      *reinterpret_cast<uint2 *>(f.lo + at) = *reinterpret_cast<const uint2 *>(lo);
-    } else {
-      f.hi[at] = hi[0];
-      f.lo[at] = lo[0];
+    for (int j = 0; j < kFlight; ++j)
+      if (i0 + int64_t(j) * step < s.items) x[j].load(s, blockIdx.y, int(i0 + int64_t(j) * step));
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      if (i0 + int64_t(j) * step >= s.items) continue;
+      x[j].template finish<false>(s, blockIdx.y, g_scale);
+      const int64_t at = blockIdx.y * f.planex + x[j].row * f.ldx + x[j].col;
+      constexpr int E = Item<T, VEC, STEP>::E;
+      __half hi[E], lo[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float v = x[j].g[e] * r;
+        hi[e] = __float2half_rn(v);
+        lo[e] = __float2half_rn(v - __half2float(hi[e]));
+      }
+      if constexpr (VEC) {
+        *reinterpret_cast<uint2 *>(f.hi + at) = *reinterpret_cast<const uint2 *>(hi);
+        *reinterpret_cast<uint2 *>(f.lo + at) = *reinterpret_cast<const uint2 *>(lo);
+      } else {
+        f.hi[at] = hi[0];
+        f.lo[at] = lo[0];
+      }
     }
   }
 }
@@ -228,9 +241,9 @@ __global__ void __launch_bounds__(kPassThreads)
 // staging slot one chunk ahead, and the new ones leave through the same slot.
 constexpr int BK = 64, UK = 16, BMC = 128, BMP = 256, BN = 256;
 constexpr int BOX = 64 * 64 * 2;  // one tensor copy: 64 rows of 128 bytes, either majorness
-constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 4;
+constexpr int A_STAGE = BMC * BK * 2, STAGE = 2 * A_STAGE, STAGES = 5;
 constexpr int kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART, SLOTS = 3;  // a chunk of fp16; high and low part of one; a warp's
+constexpr int PART = 32 * 32 * 2, SLOT = 2 * PART, SLOTS = 2;  // a chunk of fp16; high and low part of one; a warp's
 constexpr int SMEM_OPS = STAGES * STAGE, SMEM_SLOTS = kEpilogueWarps * SLOTS * SLOT;
 constexpr int SMEM_VEC = kEpilogueWarps * 32 * 4, SMEM_CTRL = 512;
 constexpr int SMEM_TOTAL = SMEM_OPS + SMEM_SLOTS + SMEM_VEC + SMEM_CTRL;
@@ -638,9 +651,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 2) {
     if (lane == 0) {  // ------------------------------------ producers (both CTAs): warp 0 A, warp 2 B
-      // A block's copies are one or two a thread and little else: the threads' issuing bounds the kernel where the loop is
-      // longer (two 64-row boxes in place of one of 128 rows, and the arming kept in an array: 590 cycles a block for the
-      // 256 that its MMAs take).
+      // One copy a block and thread, two where rows run along the contraction, and little else: the threads' issuing bounds
+      // the kernel where there is more (two boxes of 64 rows in place of one of 128, and the arming kept in an array: 590
+      // cycles a block for the 256 of a half-wide unit's MMAs, now 440).
       const bool is_a = warp == 0;
       int stage = 0;
       uint32_t parity = 0, armed = 0, armed_parity = 0;  // bit s: stage s has been armed, and for which phase
@@ -780,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t *const mine = slots + ew * SLOTS * SLOT;
     uint64_t *const cbar = cfull + SLOTS * ew;
     float *const v = vec[ew];
-    int acc = 0, slot = 0, set = 0;        // set: which half of the slots a chunk of A' leaves by
+    int acc = 0, slot = 0;
     int ahead = 0;                         // chunks fetched and not yet worked on, from `slot` on
     uint32_t acc_parity = 0, cparity = 0;  // bit s: the parity that slot s's next copy completes
     int flying = 0;                        // bit s: a copy into slot s that nobody has waited for
@@ -797,8 +810,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
-      // Old values are fetched in the order in which chunks are worked on, up to three chunks at a time (two where the
-      // chunk before leaves its slot to the result).
+      // Old values are fetched in the order in which chunks are worked on: the next chunk's before this one's new values
+      // leave (in the last product after it, which lends the other slot to the result).
       const auto exists = [&](int row0, int col) { return row0 < p.out_rows && col < p.n_dim; };
       int fu = first, fc = 0, fk = 0, frow = 0, fcol = 0, fwide = 0;  // the next to fetch: unit and column in it
       bool funit = false;                                            // fk .. fwide are of unit fu
@@ -815,7 +828,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (fc < fwide && exists(frow, fcol + fc)) break;
         }
         if (fu >= p.units) return;
-        const int q = slot + ahead < SLOTS ? slot + ahead : slot + ahead - SLOTS;
+        const int q = slot ^ ahead;  // ahead is 0 or 1
         if (lane == 0) {
           mbar_arrive_expect_tx_relaxed(&cbar[q], 2 * PART);
           tma_load_2d(from_hi, &cbar[q], mine + q * SLOT, fcol + fc, fk * p.out_rows + frow);
@@ -825,8 +838,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++ahead;
         fc += 32;
       };
-      if (kind != kGram)
-        for (int i = 0; i < (last ? SLOTS - 1 : SLOTS); ++i) fetch_next();
+      if (kind != kGram) {
+        fetch_next();
+        if (!last) fetch_next();
+      }
       for (int u = first; ok && u < p.units; u += step) {
         int k, row, col;
         bool half;
@@ -870,11 +885,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             flying &= ~(1 << slot);
             v[lane] = c == 0 ? t[0] : c == 32 ? t[1] : c == 64 ? t[2] : t[3];
           } else if (lane == 0) {
-            bulk_wait_group_read<1>();  // the chunk before the last has left this half of the slots
+            bulk_wait_group_read<0>();  // the chunk before has left the slots
           }
           __syncwarp();
-          uint8_t *const hi_part = mine + (kind == kGram ? set * 3 * PART : slot * SLOT), *const lo_part = hi_part + PART;
-          uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
+          uint8_t *const hi_part = mine + (kind == kGram ? 0 : slot * SLOT), *const lo_part = hi_part + PART;
+          uint8_t *const staged = mine + (slot ^ 1) * SLOT;  // the chunk before's, free
           const int diagonal = me - at;  // this lane's diagonal element, where the chunk holds it
           float at_diagonal = 0.f;
           if (kind == kUpdate) {
@@ -950,10 +965,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               bulk_commit_group();
             }
           }
-          if (kind == kGram) {
-            set ^= 1;
-          } else {
-            slot = slot == SLOTS - 1 ? 0 : slot + 1;
+          if (kind != kGram) {
+            slot ^= 1;
             --ahead;
           }
         }
@@ -1020,7 +1033,7 @@ struct SmallMaps {
 template <int G>
 struct Small {
   static constexpr int N = 128 * G, OP = 2 * G * R_STAGE;  // B' or A': 2 G panels of 64 columns
-  static constexpr int STAGES = G == 1 ? 6 : 4;
+  static constexpr int STAGES = G == 1 ? 8 : 6;
   static constexpr int VECS = 2 * N * 4;
   static constexpr int SMEM = OP + STAGES * R_STAGE + SMEM_SLOTS + VECS + SMEM_CTRL;  // no room to align it again
 };
@@ -1311,7 +1324,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             if (fc < N / 2 && exists(row0, col + fc)) break;
           }
           if (ft >= s.tiles) return;
-          const int q = slot + ahead < SLOTS ? slot + ahead : slot + ahead - SLOTS;
+          const int q = slot ^ ahead;  // ahead is 0 or 1
           if (lane == 0) {
             mbar_arrive_expect_tx_relaxed(&cbar[q], 2 * PART);
             tma_load_2d(from, &cbar[q], mine + q * SLOT, col + fc, k * s.stand + row0);
@@ -1327,7 +1340,8 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             fetch_next();
           }
         };
-        for (int i = 0; i < (last ? SLOTS - 1 : SLOTS); ++i) fetch_next();
+        fetch_next();
+        if (!last) fetch_next();
         // ---- A: the diagonal to d, the rest as fp16
         if (!(ok = result())) break;
         const int gram_acc = acc;
@@ -1388,13 +1402,13 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             flying &= ~(1 << slot);
             __syncwarp();
             uint8_t *const hi = mine + slot * SLOT, *const lo = hi + PART;
-            uint8_t *const staged = mine + (slot == 0 ? SLOTS - 1 : slot - 1) * SLOT;  // the chunk before's, free
+            uint8_t *const staged = mine + (slot ^ 1) * SLOT;  // the chunk before's, free
             update_chunk<TALL>(a, base + uint32_t(c), hi, lo, staged, &evec[TALL ? col + c : 0], own, row0 + lane < m_dim, early,
                                last, lane);
             if (!last) refill();
             send_chunk(a, to, &maps.c_lo, hi, lo, staged, last, lane, k, m_dim, n_dim, s.stand, row0, col + c);
             if (last) refill();
-            slot = slot == SLOTS - 1 ? 0 : slot + 1;
+            slot ^= 1;
             --ahead;
           }
           if (!ok) break;
@@ -1655,11 +1669,12 @@ template <typename T, bool VEC, bool STEP>
 gtp_status first_of(const Source &s, FirstX f, int64_t count, const gtp::DeviceInfo &dev, cudaStream_t st) {
   const int64_t blocks = (s.items + kPassThreads - 1) / kPassThreads;
   const int64_t fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / count);
-  const dim3 squares(unsigned(std::min<int64_t>({(blocks + 3) / 4, fill, kMostParts})), unsigned(count));
+  const int64_t most = (blocks + kFlight - 1) / kFlight;
+  const dim3 squares(unsigned(std::min<int64_t>({most, fill, kMostParts})), unsigned(count));
   f.parts = int(squares.x);
   if (gtp_status e = gtp::launch_overlapped(squares_kernel<T, VEC, STEP>, squares, kPassThreads, 0, st, "orthogonalize", s, f))
     return e;
-  return gtp::launch_overlapped(first_x_kernel<T, VEC, STEP>, dim3(unsigned(std::min(blocks, fill)), unsigned(count)),
+  return gtp::launch_overlapped(first_x_kernel<T, VEC, STEP>, dim3(unsigned(std::min(most, fill)), unsigned(count)),
                                 kPassThreads, 0, st, "orthogonalize", s, f);
 }
 
