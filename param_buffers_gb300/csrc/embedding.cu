@@ -16,6 +16,7 @@
 
 #include "byte_range.h"
 #include "device.h"
+#include "eight.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gtp {
@@ -36,60 +37,41 @@ __device__ __forceinline__ int64_t row_of(const void *ids, int wide, int64_t t, 
   return r < uint64_t(rows) ? int64_t(r) : rows;
 }
 
-// Eight elements of a row that one thread moves: consecutive ones on 16 bytes (VEC), or every step-th from its own on,
-// so that a warp's accesses stay side by side whatever the row's alignment.
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int step, int n, float (&x)[8]) {
-  if (VEC) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);  // bf16 -> fp32 is exact
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k * step]) : 0.f;
+// Eight elements of a row that one thread moves: consecutive ones on 16 bytes (VEC), as they lie in memory, or every
+// step-th from its own on, so that a warp's accesses stand side by side whatever the row's alignment; n of them exist.
+template <typename T, bool VEC>
+struct Group {
+  gtp::Eight<T> e;
+  __device__ __forceinline__ void load(const T *p, int, int) { e.load(p); }
+  __device__ __forceinline__ void clear() { e.clear(); }
+  __device__ __forceinline__ void get(float (&x)[8]) const { e.get(x); }
+  static __device__ __forceinline__ void store(T *p, int, int, const float (&x)[8]) {
+    gtp::Eight<T> v;
+    v.set(x);
+    v.store(p);
   }
-}
-template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int step, int n, float (&x)[8]) {
-  if (VEC) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+};
+template <typename T>
+struct Group<T, false> {
+  T v[8];
+  __device__ __forceinline__ void load(const T *p, int step, int n) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k * step] : 0.f;
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k * step] : T(0.f);
   }
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, int step, int n, const float (&x)[8]) {
-  if (VEC) {
-    uint32_t w[4];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
+    for (int k = 0; k < 8; ++k) v[k] = T(0.f);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = float(v[k]);
+  }
+  static __device__ __forceinline__ void store(T *p, int step, int n, const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) p[k * step] = __float2bfloat16_rn(x[k]);
+      if (k < n) p[k * step] = T(x[k]);
   }
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(float *p, int step, int n, const float (&x)[8]) {
-  if (VEC) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k * step] = x[k];
-  }
-}
+};
 
 // A block is tx threads wide, eight columns a thread; this thread's first column and how many of its eight exist.
 template <bool VEC>
@@ -112,9 +94,9 @@ struct LookupArgs {
   int wide;
 };
 
-template <typename TI, typename TO, bool VEC>
+// N tokens of a thread in flight: their ids, then their rows.
+template <typename TI, typename TO, bool VEC, int N>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ LookupArgs a) {
-  constexpr int N = 4;  // tokens of a thread in flight
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   int64_t c;
@@ -124,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
   const int64_t step = int64_t(gridDim.y) * blockDim.y;
   for (int64_t t0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; t0 < a.tokens; t0 += N * step) {
     int64_t row[N];
-    float x[N][8];
+    Group<TI, VEC> x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int64_t t = t0 + i * step;
@@ -132,23 +114,20 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (row[i] < a.rows) {
-        load8<VEC>(static_cast<const TI *>(a.table) + row[i] * a.table_ld + c, tx, n, x[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
-      }
+      x[i].clear();
+      if (row[i] < a.rows) x[i].load(static_cast<const TI *>(a.table) + row[i] * a.table_ld + c, tx, n);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int64_t t = t0 + i * step;
-      if (t < a.tokens) {
-        if (row[i] < a.rows) {  // not the zeros of other shards' tokens: a scale of Inf or NaN leaves them 0
+      if (t >= a.tokens) continue;
+      float y[8];
+      x[i].get(y);
+      if (row[i] < a.rows) {  // not the zeros of other shards' tokens: a scale of Inf or NaN leaves them 0
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[i][k] *= a.scale;
-        }
-        store8<VEC>(static_cast<TO *>(a.out) + t * a.out_ld + c, tx, n, x[i]);
+        for (int k = 0; k < 8; ++k) y[k] *= a.scale;
       }
+      Group<TO, VEC>::store(static_cast<TO *>(a.out) + t * a.out_ld + c, tx, n, y);
     }
   }
 }
@@ -183,18 +162,33 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constan
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = blockIdx.x * kOwn;
-  for (int t0 = 32 * warp; t0 < a.tokens; t0 += kRankThreads) {
-    const int t = t0 + lane;
-    const int64_t row = t < a.tokens ? row_of(a.ids, a.wide, t, a.first_row, a.rows) : a.rows;
-    const bool mine = row < a.rows;
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, mine);
+  constexpr int N = 8;  // ids of a thread in flight
+  for (int t0 = 32 * warp; t0 < a.tokens; t0 += N * kRankThreads) {
+    int64_t row[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = t0 + i * kRankThreads + lane;
+      row[i] = t < a.tokens ? row_of(a.ids, a.wide, t, a.first_row, a.rows) : a.rows;
+    }
+    unsigned m[N];
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      m[i] = __ballot_sync(0xFFFFFFFFu, row[i] < a.rows);
+      total += __popc(m[i]);
+    }
     int base = 0;
-    if (lane == 0 && m) base = atomicAdd(&listed, __popc(m));
+    if (lane == 0 && total) base = atomicAdd(&listed, total);
     base = __shfl_sync(0xFFFFFFFFu, base, 0);
-    if (mine) {
-      const uint32_t k = uint32_t(row) * uint32_t(a.tokens) + uint32_t(t);
-      list[base + __popc(m & ((1u << lane) - 1))] = k;
-      if (t >= first && t < first + kOwn) own[atomicAdd(&owned, 1)] = k;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = t0 + i * kRankThreads + lane;
+      if (row[i] < a.rows) {
+        const uint32_t k = uint32_t(row[i]) * uint32_t(a.tokens) + uint32_t(t);
+        list[base + __popc(m[i] & ((1u << lane) - 1))] = k;
+        if (t >= first && t < first + kOwn) own[atomicAdd(&owned, 1)] = k;
+      }
+      base += __popc(m[i]);
     }
   }
   __syncthreads();
@@ -386,92 +380,180 @@ __device__ __forceinline__ void add8(float *p, int step, int n, float scale, con
 }
 template <bool VEC>
 __device__ __forceinline__ void add8(__nv_bfloat16 *p, int step, int n, float scale, const float (&x)[8]) {
+  Group<__nv_bfloat16, VEC> v;
+  v.load(p, step, n);
   float g[8];
-  load8<VEC>(p, step, n, g);
+  v.get(g);
 #pragma unroll
   for (int k = 0; k < 8; ++k) g[k] = fmaf(scale, x[k], g[k]);
-  store8<VEC>(p, step, n, g);
+  Group<__nv_bfloat16, VEC>::store(p, step, n, g);
 }
+
+// A tile a thread row (whole warps, so that a warp's lanes read the keys of 32 places at once and hand them round), eight
+// columns a thread, kFlight tokens' rows in flight.
+constexpr int kFlight = 8;
 
 template <typename TD, typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ SumArgs a) {
-  constexpr int N = 4;  // tokens in flight
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   int64_t c;
-  int n;
-  const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y;
-  if (tile >= a.tiles || !columns<VEC>(a.cols, c, n)) return;
+  int n = 0;
+  const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y, lane = threadIdx.x & 31;
+  const bool mine = columns<VEC>(a.cols, c, n);
+  if (tile >= a.tiles) return;  // the whole warp
   const int tx = blockDim.x, rows = int(a.rows);
   const int p0 = tile * a.tile, p1 = min(p0 + a.tile, a.tokens);
-  int row = a.key[p0];
-  if (row >= rows) return;
+  const int after = p1 < a.tokens ? a.key[p1] : rows, before = p0 > 0 ? a.key[p0 - 1] : -1;
   float acc[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-  bool open = p0 > 0 && a.key[p0 - 1] == row;  // this row's first tokens are in the tile before
   float *const part = a.part + int64_t(tile) * 2 * a.cols + c;
-  for (int p = p0; p < p1; p += N) {
-    float x[N][8];
-    int key[N];
+  int row = rows;     // the row being summed
+  bool open = false;  // its first tokens are in the tile before
+  for (int q0 = p0; q0 < p1; q0 += 32) {
+    const int q = q0 + lane;
+    const int key = q < p1 ? a.key[q] : rows, token = q < p1 && key < rows ? a.token[q] : 0;
+    if (q0 == p0) {
+      row = __shfl_sync(0xFFFFFFFFu, key, 0);
+      if (row >= rows) return;  // behind the shard's tokens
+      open = before == row;
+    }
+    for (int i0 = 0; i0 < min(32, p1 - q0); i0 += kFlight) {
+      Group<TD, VEC> x[kFlight];
+      int k[kFlight];
 #pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = p + i < p1 ? a.key[p + i] : rows;
+      for (int i = 0; i < kFlight; ++i) {
+        k[i] = __shfl_sync(0xFFFFFFFFu, key, i0 + i);
+        const int t = __shfl_sync(0xFFFFFFFFu, token, i0 + i);
+        if (k[i] < rows && mine) x[i].load(static_cast<const TD *>(a.dout) + int64_t(t) * a.dout_ld + c, tx, n);
+      }
+      if (!mine) continue;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (key[i] < rows) load8<VEC>(static_cast<const TD *>(a.dout) + int64_t(a.token[p + i]) * a.dout_ld + c, tx, n, x[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (key[i] < rows) {
-        if (key[i] != row) {
-          if (open) store8<false>(part, VEC ? 1 : tx, n, acc);
+      for (int i = 0; i < kFlight; ++i) {
+        if (k[i] >= rows) continue;
+        if (k[i] != row) {
+          if (open) Group<float, VEC>::store(part, tx, n, acc);
           else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
           open = false;
-          row = key[i];
+          row = k[i];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
         }
+        float f[8];
+        x[i].get(f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += x[i][k];
+        for (int j = 0; j < 8; ++j) acc[j] += f[j];
       }
     }
   }
-  if (open) store8<false>(part, VEC ? 1 : tx, n, acc);
-  else if (p1 < a.tokens && a.key[p1] == row) store8<false>(part + a.cols, VEC ? 1 : tx, n, acc);
+  if (!mine) return;
+  if (open) Group<float, VEC>::store(part, tx, n, acc);
+  else if (after == row) Group<float, VEC>::store(part + a.cols, tx, n, acc);
   else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
 }
 
-// The rows that cross tiles: the tile in which such a row begins adds up its parts.
+// The rows that cross tiles.  A block has 32 tiles and 256 columns; its eight warps look at the tiles in which such a row
+// begins.  A row of up to kShort more tiles is one warp's, which adds its parts up in order; a longer one is everybody's:
+// warp w adds every eighth part from w on, and the eight sums are added up in order.
+constexpr int kJoinTiles = 32, kShort = 8;
+
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a) {
+  __shared__ float sums[8][256];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  int64_t c;
-  int n;
-  const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y;
-  if (tile >= a.tiles || !columns<VEC>(a.cols, c, n)) return;
-  const int p0 = tile * a.tile, p1 = p0 + a.tile;
-  if (p1 >= a.tokens) return;
-  const int row = a.key[p1];
-  if (row >= a.rows || a.key[p1 - 1] != row || (p0 > 0 && a.key[p0 - 1] == row)) return;
-  const int tx = blockDim.x, step = VEC ? 1 : tx;
-  float acc[8];
-  load8<false>(a.part + (int64_t(tile) * 2 + 1) * a.cols + c, step, n, acc);
-  for (int t = tile + 1; t < a.tiles && a.key[t * a.tile] == row; ++t) {
-    float x[8];
-    load8<false>(a.part + int64_t(t) * 2 * a.cols + c, step, n, x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = int(a.rows);
+  const int64_t c = int64_t(blockIdx.x) * 256 + (VEC ? 8 * lane : lane);
+  const int step = 32, n = c >= a.cols ? 0 : VEC ? 8 : int(min(int64_t(8), (a.cols - c + 31) / 32));
+  // this lane's tile: its last row goes on and does not come in
+  const int tile = int(blockIdx.y) * kJoinTiles + lane, p1 = (tile + 1) * a.tile;
+  const int row = tile < a.tiles && p1 < a.tokens ? a.key[p1] : rows;
+  bool begins = row < rows && a.key[p1 - 1] == row && (tile == 0 || a.key[p1 - 1 - a.tile] != row);
+  unsigned todo = __ballot_sync(0xFFFFFFFFu, begins), longer = 0;
+  const auto part_of = [&](int t, int which) { return a.part + (int64_t(t) * 2 + which) * a.cols + c; };
+  // how many tiles after t the row goes on into, at least (up to `most`): tiles t + 1, ... begin with it
+  const auto more_of = [&](int t, int r) {
+    int more = 0;
+    for (;;) {
+      const int u = t + 1 + more + lane;
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, u < a.tiles && a.key[u * a.tile] == r);
+      if (m != 0xFFFFFFFFu) return more + __ffs(~m) - 1;
+      more += 32;
+    }
+  };
+  int turn = 0;
+  for (; todo; todo &= todo - 1, ++turn) {
+    const int l = __ffs(todo) - 1;
+    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l);
+    const bool is_long = t + 1 + kShort < a.tiles && a.key[(t + 1 + kShort) * a.tile] == r;
+    if (is_long) longer |= 1u << l;
+    if (is_long || (turn & 7) != warp) continue;
+    const int more = more_of(t, r);
+    Group<float, VEC> x[kShort + 1];
+    if (n == 0) continue;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] += x[k];
+    for (int i = 0; i <= kShort; ++i) {
+      x[i].clear();
+      if (i <= more) x[i].load(part_of(t + i, i == 0), step, n);
+    }
+    float acc[8], f[8];
+    x[0].get(acc);
+#pragma unroll
+    for (int i = 1; i <= kShort; ++i) {
+      x[i].get(f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += f[k];
+    }
+    add8<VEC>(static_cast<TG *>(a.grad) + int64_t(r) * a.cols + c, step, n, a.scale, acc);
   }
-  add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+  for (; longer; longer &= longer - 1) {  // the same for every warp
+    const int l = __ffs(longer) - 1;
+    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l);
+    const int more = more_of(t, r);
+    float acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    if (n > 0) {
+      constexpr int N = 4;  // parts in flight
+      for (int i0 = warp; i0 <= more; i0 += 8 * N) {
+        Group<float, VEC> x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          x[i].clear();
+          if (i0 + 8 * i <= more) x[i].load(part_of(t + i0 + 8 * i, i0 + 8 * i == 0), step, n);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float f[8];
+          x[i].get(f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] += f[k];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[warp][VEC ? 8 * lane + k : lane + 32 * k] = acc[k];
+    __syncthreads();
+    const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;  // a column a thread
+    if (col < a.cols) {
+      float s = sums[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) s += sums[w][threadIdx.x];
+      TG *const g = static_cast<TG *>(a.grad) + int64_t(r) * a.cols + col;
+      gtp::store1(g, fmaf(a.scale, s, gtp::load1(g)));
+    }
+    __syncthreads();
+  }
 }
 
 // --------------------------------------------------------------------------- host
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 
-// Threads a block across a row's groups of eight, and rows of such threads.
-dim3 block_of(int64_t cols) {
-  int tx = 1;
+// Threads a block across a row's groups of eight (at least `least`), and rows of such threads.
+dim3 block_of(int64_t cols, int least) {
+  int tx = least;
   while (tx < kThreads && 8 * tx < cols) tx *= 2;
   return dim3(tx, kThreads / tx);
 }
@@ -505,12 +587,15 @@ gtp::ByteRange span_of(const void *p, int64_t n, int64_t ld, int64_t cols, int64
 template <typename TI, typename TO>
 gtp_status launch_lookup(const LookupArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && on16(a.table, a.table_ld, sizeof(TI)) && on16(a.out, a.out_ld, sizeof(TO));
-  const dim3 block = block_of(a.cols);
-  const int64_t gx = (a.cols + 8 * block.x - 1) / (8 * block.x);
-  const int64_t fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / gx);
-  const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>({(a.tokens + block.y - 1) / block.y, fill, 65535})));
-  return gtp::launch_overlapped(vec ? embedding_kernel<TI, TO, true> : embedding_kernel<TI, TO, false>, grid, block, 0, st,
-                                "embedding", a);
+  const dim3 block = block_of(a.cols, 1);
+  const int64_t gx = (a.cols + 8 * block.x - 1) / (8 * block.x), fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / gx);
+  const int64_t rows = (a.tokens + block.y - 1) / block.y;  // of blocks, at a token a thread
+  constexpr int N = 4;
+  const bool many = rows > fill;
+  const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>(many ? (rows + N - 1) / N : rows, 65535)));
+  const auto kernel = many ? (vec ? embedding_kernel<TI, TO, true, N> : embedding_kernel<TI, TO, false, N>)
+                           : (vec ? embedding_kernel<TI, TO, true, 1> : embedding_kernel<TI, TO, false, 1>);
+  return gtp::launch_overlapped(kernel, grid, block, 0, st, "embedding", a);
 }
 
 struct GradPlan {
@@ -522,8 +607,8 @@ struct GradPlan {
 GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
   GradPlan p = {};
   p.radix = tokens > kRankMost || rows * tokens >= (int64_t(1) << 32) - 1;
-  // tiles: short ones spread few tokens over the machine; above 2^16 of them longer ones keep the partials few
-  p.tile = int32_t(std::max<int64_t>(16, (tokens + 65534) / 65535));
+  // tiles: short ones spread few tokens over the machine; from 4096 of them on longer ones keep the parts few
+  p.tile = int32_t(std::max<int64_t>(8, (tokens + 4095) / 4096));
   p.tiles = int32_t((tokens + p.tile - 1) / p.tile);
   p.sort_tiles = int32_t((tokens + kTile - 1) / kTile);
   int64_t at = 0;
@@ -576,13 +661,14 @@ gtp_status sort_tokens(SortArgs &a, const GradPlan &plan, cudaStream_t st) {
 template <typename TD, typename TG>
 gtp_status launch_sums(const SumArgs &a, cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && on16(a.dout, a.dout_ld, sizeof(TD)) && on16(a.grad, a.cols, sizeof(TG));
-  const dim3 block = block_of(a.cols);
+  const dim3 block = block_of(a.cols, 32);
   const dim3 grid(unsigned((a.cols + 8 * block.x - 1) / (8 * block.x)), (a.tiles + block.y - 1) / block.y);
   if (gtp_status s = gtp::launch_overlapped(vec ? embedding_sum_kernel<TD, TG, true> : embedding_sum_kernel<TD, TG, false>, grid,
                                             block, 0, st, "embedding_grad", a))
     return s;
   if (a.tiles == 1) return GTP_OK;
-  return gtp::launch_overlapped(vec ? embedding_join_kernel<TG, true> : embedding_join_kernel<TG, false>, grid, block, 0, st,
+  const dim3 join(unsigned((a.cols + 255) / 256), unsigned((a.tiles + kJoinTiles - 1) / kJoinTiles));
+  return gtp::launch_overlapped(vec ? embedding_join_kernel<TG, true> : embedding_join_kernel<TG, false>, join, kThreads, 0, st,
                                 "embedding_grad", a);
 }
 
