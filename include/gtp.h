@@ -770,7 +770,7 @@ gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld
  * are neither read nor written.
  * ids: device [tokens], int32 (ids64 = 0) or int64, aligned to their size.  table [rows, cols], out and dout
  * [tokens, cols]: F32 or BF16, row strides table_ld, out_ld, dout_ld (elements, >= cols), element-aligned.
- * No output overlaps an input (GTP_E_ARG).  workspace: device, 16-byte aligned, at least
+ * No output overlaps an input (GTP_E_ARG).  workspace: device, 32-byte aligned, at least
  * gtp_embedding_grad_workspace_bytes (-1 for sizes that the call refuses; GTP_E_CAPACITY where it is
  * smaller); its contents are not needed afterwards, and calls that may overlap on the GPU need one each.
  * Sizes up to 2^30 a dimension and 2^40 elements (GTP_E_SHAPE). */
@@ -798,8 +798,8 @@ gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, int64_t toke
  * and with a columnwise view rstd too.  sum may be x or residual exactly (same start, stride and type), y may
  * be x exactly (but not with a columnwise view and no residual); otherwise no output overlaps an input or
  * another output (GTP_E_ARG).  Row strides in elements, >= cols; arrays element-aligned; with a view, the
- * rows of every matrix, the weight and the codes on 16 bytes (GTP_E_ALIGN), cols % 32 == 0 and, columnwise,
- * rows % 32 == 0 and rows <= 32 * 65535 (GTP_E_SHAPE).  cols <= 16384, rows <= 2^30 (GTP_E_SHAPE). */
+ * rows of every matrix on eight elements' size (16 bytes of BF16, 32 of F32), the weight and the codes on 16
+ * bytes (GTP_E_ALIGN), cols % 32 == 0 and, columnwise, rows % 32 == 0 and rows <= 32 * 65535 (GTP_E_SHAPE).  cols <= 16384, rows <= 2^30 (GTP_E_SHAPE). */
 typedef struct {
   const void *x;            /* [rows, cols]                                                     */
   const void *residual;     /* [rows, cols] or NULL                                             */

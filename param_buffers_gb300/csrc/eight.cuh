@@ -5,9 +5,12 @@
 
 #include <cstdint>
 
+#include "wide.cuh"
+
 namespace gtp {
 
-// Eight consecutive elements on 16 bytes: a load in flight holds no more registers than bytes.
+// Eight consecutive elements on their own size (16 bytes of bf16, 32 of fp32): one access, and a load in flight holds no
+// more registers than bytes.
 template <typename T>
 struct Eight;
 template <>
@@ -36,22 +39,21 @@ struct Eight<__nv_bfloat16> {
 };
 template <>
 struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = __ldcs(reinterpret_cast<const float4 *>(p));
-    b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  uint32_t a[8];
+  __device__ __forceinline__ void load(const float *p) { load_32b(p, a); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = 0;
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(a[i]);
   }
   __device__ __forceinline__ void set(const float (&x)[8]) {
-    a = make_float4(x[0], x[1], x[2], x[3]), b = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(x[i]);
   }
-  __device__ __forceinline__ void store(float *p) const {
-    reinterpret_cast<float4 *>(p)[0] = a;
-    reinterpret_cast<float4 *>(p)[1] = b;
-  }
+  __device__ __forceinline__ void store(float *p) const { store_32b(p, a); }
 };
 
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }

@@ -27,8 +27,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// As two 32-bit words (one of them twice where the ids are 32 bits wide): without a branch several ids' loads are under
+// way at once.
 __device__ __forceinline__ int64_t id_at(const void *ids, int wide, int64_t t) {
-  return wide ? static_cast<const int64_t *>(ids)[t] : int64_t(static_cast<const int32_t *>(ids)[t]);
+  const int32_t *const p = static_cast<const int32_t *>(ids) + (t << wide);
+  const int32_t low = p[0], high = p[wide];
+  return wide ? int64_t(uint64_t(uint32_t(high)) << 32 | uint32_t(low)) : int64_t(low);
 }
 
 // The shard's row of a token, or `rows` for one of another shard (or of none).  Unsigned: no id wraps into the range.
@@ -37,7 +41,7 @@ __device__ __forceinline__ int64_t row_of(const void *ids, int wide, int64_t t, 
   return r < uint64_t(rows) ? int64_t(r) : rows;
 }
 
-// Eight elements of a row that one thread moves: consecutive ones on 16 bytes (VEC), as they lie in memory, or every
+// Eight elements of a row that one thread moves: consecutive ones (VEC), as they lie in memory, or every
 // step-th from its own on, so that a warp's accesses stand side by side whatever the row's alignment; n of them exist.
 template <typename T, bool VEC>
 struct Group {
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
   bool open = false;  // its first tokens are in the tile before
   for (int q0 = p0; q0 < p1; q0 += 32) {
     const int q = q0 + lane;
-    const int key = q < p1 ? a.key[q] : rows, token = q < p1 && key < rows ? a.token[q] : 0;
+    const int key = q < p1 ? a.key[q] : rows, token = q < p1 ? a.token[q] : 0;  // not a token where key is rows
     if (q0 == p0) {
       row = __shfl_sync(0xFFFFFFFFu, key, 0);
       if (row >= rows) return;  // behind the shard's tokens
@@ -470,32 +474,23 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
   const int tile = int(blockIdx.y) * kJoinTiles + lane, p1 = (tile + 1) * a.tile;
   const int row = tile < a.tiles && p1 < a.tokens ? a.key[p1] : rows;
   bool begins = row < rows && a.key[p1 - 1] == row && (tile == 0 || a.key[p1 - 1 - a.tile] != row);
-  unsigned todo = __ballot_sync(0xFFFFFFFFu, begins), longer = 0;
+  // how many tiles more begin with it, counted up to kShort + 1
+  int more = 0;
+#pragma unroll
+  for (int i = 1; i <= kShort + 1; ++i) more += begins && tile + i < a.tiles && a.key[(tile + i) * a.tile] == row;
+  unsigned longer = __ballot_sync(0xFFFFFFFFu, begins && more > kShort);
+  unsigned todo = __ballot_sync(0xFFFFFFFFu, begins) & ~longer;
   const auto part_of = [&](int t, int which) { return a.part + (int64_t(t) * 2 + which) * a.cols + c; };
-  // how many tiles after t the row goes on into, at least (up to `most`): tiles t + 1, ... begin with it
-  const auto more_of = [&](int t, int r) {
-    int more = 0;
-    for (;;) {
-      const int u = t + 1 + more + lane;
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, u < a.tiles && a.key[u * a.tile] == r);
-      if (m != 0xFFFFFFFFu) return more + __ffs(~m) - 1;
-      more += 32;
-    }
-  };
   int turn = 0;
   for (; todo; todo &= todo - 1, ++turn) {
     const int l = __ffs(todo) - 1;
-    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l);
-    const bool is_long = t + 1 + kShort < a.tiles && a.key[(t + 1 + kShort) * a.tile] == r;
-    if (is_long) longer |= 1u << l;
-    if (is_long || (turn & 7) != warp) continue;
-    const int more = more_of(t, r);
+    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l), m = __shfl_sync(0xFFFFFFFFu, more, l);
+    if ((turn & 7) != warp || n == 0) continue;
     Group<float, VEC> x[kShort + 1];
-    if (n == 0) continue;
 #pragma unroll
     for (int i = 0; i <= kShort; ++i) {
       x[i].clear();
-      if (i <= more) x[i].load(part_of(t + i, i == 0), step, n);
+      if (i <= m) x[i].load(part_of(t + i, i == 0), step, n);
     }
     float acc[8], f[8];
     x[0].get(acc);
@@ -510,18 +505,24 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
   for (; longer; longer &= longer - 1) {  // the same for every warp
     const int l = __ffs(longer) - 1;
     const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l);
-    const int more = more_of(t, r);
+    int m = kShort + 1;  // tiles after t that begin with it: counted on, 32 at a time
+    for (;;) {
+      const int u = t + 1 + m + lane;
+      const unsigned same = __ballot_sync(0xFFFFFFFFu, u < a.tiles && a.key[u * a.tile] == r);
+      m += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
+      if (same != 0xFFFFFFFFu) break;
+    }
     float acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.f;
     if (n > 0) {
       constexpr int N = 4;  // parts in flight
-      for (int i0 = warp; i0 <= more; i0 += 8 * N) {
+      for (int i0 = warp; i0 <= m; i0 += 8 * N) {
         Group<float, VEC> x[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           x[i].clear();
-          if (i0 + 8 * i <= more) x[i].load(part_of(t + i0 + 8 * i, i0 + 8 * i == 0), step, n);
+          if (i0 + 8 * i <= m) x[i].load(part_of(t + i0 + 8 * i, i0 + 8 * i == 0), step, n);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -558,8 +559,9 @@ dim3 block_of(int64_t cols, int least) {
   return dim3(tx, kThreads / tx);
 }
 
-bool on16(const void *p, int64_t ld, int64_t es) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es & 15) == 0;
+// Whether every row starts on eight elements' own size.
+bool in_eights(const void *p, int64_t ld, int64_t es) {
+  return (reinterpret_cast<uintptr_t>(p) & uintptr_t(8 * es - 1)) == 0 && ld % 8 == 0;
 }
 
 int64_t size_of(gtp_dtype dt) { return dt == GTP_F32 ? 4 : 2; }
@@ -586,7 +588,7 @@ gtp::ByteRange span_of(const void *p, int64_t n, int64_t ld, int64_t cols, int64
 
 template <typename TI, typename TO>
 gtp_status launch_lookup(const LookupArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && on16(a.table, a.table_ld, sizeof(TI)) && on16(a.out, a.out_ld, sizeof(TO));
+  const bool vec = a.cols % 8 == 0 && in_eights(a.table, a.table_ld, sizeof(TI)) && in_eights(a.out, a.out_ld, sizeof(TO));
   const dim3 block = block_of(a.cols, 1);
   const int64_t gx = (a.cols + 8 * block.x - 1) / (8 * block.x), fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / gx);
   const int64_t rows = (a.tokens + block.y - 1) / block.y;  // of blocks, at a token a thread
@@ -660,7 +662,7 @@ gtp_status sort_tokens(SortArgs &a, const GradPlan &plan, cudaStream_t st) {
 
 template <typename TD, typename TG>
 gtp_status launch_sums(const SumArgs &a, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && on16(a.dout, a.dout_ld, sizeof(TD)) && on16(a.grad, a.cols, sizeof(TG));
+  const bool vec = a.cols % 8 == 0 && in_eights(a.dout, a.dout_ld, sizeof(TD)) && in_eights(a.grad, a.cols, sizeof(TG));
   const dim3 block = block_of(a.cols, 32);
   const dim3 grid(unsigned((a.cols + 8 * block.x - 1) / (8 * block.x)), (a.tiles + block.y - 1) / block.y);
   if (gtp_status s = gtp::launch_overlapped(vec ? embedding_sum_kernel<TD, TG, true> : embedding_sum_kernel<TD, TG, false>, grid,
@@ -730,7 +732,7 @@ extern "C" gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, i
   if ((reinterpret_cast<uintptr_t>(ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(dout) & uintptr_t(ds - 1)) ||
       (reinterpret_cast<uintptr_t>(grad_data) & uintptr_t(gs - 1)))
     return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
-  if (!gtp::aligned16(workspace)) return gtp::fail(GTP_E_ALIGN, "workspace must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) & 31u) return gtp::fail(GTP_E_ALIGN, "workspace must be 32-byte aligned");
   const GradPlan plan = grad_plan(tokens, rows, cols);
   if (workspace_bytes < plan.bytes)
     return gtp::fail(GTP_E_CAPACITY, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)plan.bytes);

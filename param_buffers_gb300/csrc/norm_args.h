@@ -39,8 +39,9 @@ bool same_place(const Matrix &out, const Matrix &in, int64_t rows) {
   return out.p == in.p && out.dt == in.dt && (rows == 1 || out.ld == in.ld);
 }
 
+// Whether every row starts on eight elements' own size.
 bool vector_rows(const Matrix &m, int64_t rows) {
-  return aligned(m.p, 16) && (rows == 1 || m.ld * size_of(m.dt) % 16 == 0);
+  return aligned(m.p, 8 * size_of(m.dt)) && (rows == 1 || m.ld % 8 == 0);
 }
 
 }  // namespace

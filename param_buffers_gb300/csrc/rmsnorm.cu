@@ -49,7 +49,7 @@ struct NormArgs {
   int64_t rows, cols, x_ld, residual_ld, sum_ld, y_ld;
   int64_t row_words, col_words;  // 0: scales in [rows, blocks] order
   float eps, inv_cols;
-  int weight_f32, y_f32;
+  int weight_f32, y_f32, codes_on_32;  // the last: col_codes starts on 32 bytes
 };
 
 using gtp::Eight;
@@ -209,15 +209,18 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_elements_kernel(cons
     const TS *const res = static_cast<const TS *>(a.residual) + (RES ? row * a.residual_ld + t : 0);
     TS *const sum = static_cast<TS *>(a.sum) + (RES ? row * a.sum_ld + t : 0);
     float h[K], squares[1] = {0.f};
+    TS old[RES ? K : 1];  // all loads before the first store
 #pragma unroll
-    for (int k = 0; k < K; ++k) h[k] = live && t + k * TX < cols ? gtp::load1(x + k * TX) : 0.f;
+    for (int k = 0; k < K; ++k) {
+      h[k] = live && t + k * TX < cols ? gtp::load1(x + k * TX) : 0.f;
+      if (RES) old[RES ? k : 0] = live && t + k * TX < cols ? res[k * TX] : TS(0.f);
+    }
     if (RES) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (live && t + k * TX < cols) {
-          h[k] = gtp::rounded<TS>(h[k] + gtp::load1(res + k * TX));
-          gtp::store1(sum + k * TX, h[k]);
-        }
+      for (int k = 0; k < K; ++k) {
+        h[k] = gtp::rounded<TS>(h[k] + float(old[RES ? k : 0]));
+        if (live && t + k * TX < cols) gtp::store1(sum + k * TX, h[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) squares[0] = fmaf(h[k], h[k], squares[0]);
@@ -226,10 +229,13 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_elements_kernel(cons
     if (a.rstd && live && t == 0) a.rstd[row] = r;
     if (!a.y || !live) continue;
     const int64_t at = row * a.y_ld + t;
+    float w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (t + k * TX < cols) {
-        const float y = h[k] * r * gtp::load1_of(a.weight, a.weight_f32, t + k * TX);
+        const float y = h[k] * r * w[k];
         if (a.y_f32) static_cast<float *>(a.y)[at + k * TX] = y;
         else static_cast<__nv_bfloat16 *>(a.y)[at + k * TX] = __float2bfloat16_rn(y);
       }
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_elements_kernel(cons
 constexpr int kTileThreads = 256, kTileRows = 32, kMostCluster = 8;
 
 template <typename TX, typename TS, bool RES, int VPL, bool STATS>
-__global__ void __launch_bounds__(kTileThreads) norm_tile_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kTileThreads, VPL == 1 ? 4 : 2) norm_tile_kernel(const __grid_constant__ NormArgs a) {
   constexpr int CW = 256 * VPL;
   using TH = typename std::conditional<RES, TS, TX>::type;
   __shared__ __align__(16) uint32_t plane[8][CW];  // columns' amax of each warp, then their codes of each warp's rows
@@ -384,45 +390,67 @@ __global__ void __launch_bounds__(kTileThreads) norm_tile_kernel(const __grid_co
   for (int v = 0; v < VPL; ++v) {
     const int j = 256 * v + threadIdx.x;
     if (c0 + j < a.cols) {
-      uint4 *dst = reinterpret_cast<uint4 *>(a.col_codes + (c0 + j) * a.rows + int64_t(blockIdx.y) * kTileRows);
-      dst[0] = make_uint4(plane[0][j], plane[1][j], plane[2][j], plane[3][j]);
-      dst[1] = make_uint4(plane[4][j], plane[5][j], plane[6][j], plane[7][j]);
+      uint8_t *const dst = a.col_codes + (c0 + j) * a.rows + int64_t(blockIdx.y) * kTileRows;
+      const uint32_t w[8] = {plane[0][j], plane[1][j], plane[2][j], plane[3][j],
+                             plane[4][j], plane[5][j], plane[6][j], plane[7][j]};
+      if (a.codes_on_32) {
+        gtp::store_32b(dst, w);
+      } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     }
   }
 }
 
 // --------------------------------------------------------------------------- MXFP8 values
 
+// A thread has eight columns, N rows at a time in flight.
 template <typename TO>
 __global__ void __launch_bounds__(256)
     mxfp8_dequantize_kernel(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int64_t words, TO *out,
                             int vec) {
+  constexpr int N = 4;
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
-  const int64_t blocks = cols >> 5, items = rows * (cols >> 3), step = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += step) {
-    const int64_t row = i / (cols >> 3), j = i - row * (cols >> 3);
-    const uint2 q = *reinterpret_cast<const uint2 *>(codes + 8 * i);
-    const uint32_t byte = scales[scale_at(row, j >> 2, blocks, words)];
-    // 2^(byte - 127); byte 0 is a subnormal of fp32, 255 NaN
-    const float s = byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7FC00000u)
-                                                                          : __uint_as_float(byte << 23);
-    float x[8];
+  const int64_t c = 8 * (int64_t(blockIdx.x) * blockDim.x + threadIdx.x), step = int64_t(gridDim.y) * blockDim.y;
+  if (c >= cols) return;
+  for (int64_t r0 = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r0 < rows; r0 += N * step) {
+    uint2 q[N];
+    uint32_t byte[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = k < 2 ? q.x : q.y;
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * (k & 1))), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      x[2 * k] = f.x * s;
-      x[2 * k + 1] = f.y * s;
+    for (int i = 0; i < N; ++i) {
+      const int64_t row = r0 + i * step;
+      if (row < rows) {
+        q[i] = *reinterpret_cast<const uint2 *>(codes + row * cols + c);
+        byte[i] = scales[scale_at(row, c >> 5, cols >> 5, words)];
+      }
     }
-    if (vec) {
-      Eight<TO> e;
-      e.set(x);
-      e.store(out + 8 * i);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) gtp::store1(out + 8 * i + k, x[k]);
+    for (int i = 0; i < N; ++i) {
+      const int64_t row = r0 + i * step;
+      if (row >= rows) continue;
+      // 2^(byte - 127); byte 0 is a subnormal of fp32, 255 NaN
+      const float s = byte[i] == 0 ? __uint_as_float(0x00400000u) : byte[i] == 255 ? __uint_as_float(0x7FC00000u)
+                                                                                  : __uint_as_float(byte[i] << 23);
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? q[i].x : q[i].y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * (k & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * k] = f.x * s;
+        x[2 * k + 1] = f.y * s;
+      }
+      TO *const to = out + row * cols + c;
+      if (vec) {
+        Eight<TO> e;
+        e.set(x);
+        e.store(to);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) gtp::store1(to + k, x[k]);
+      }
     }
   }
 }
@@ -552,7 +580,7 @@ extern "C" gtp_status gtp_rmsnorm(const gtp_rmsnorm_desc *d, gtp_stream stream) 
   if (res) vec = vec && vector_rows(r, R) && vector_rows(s, R);
   if (d->y) vec = vec && vector_rows(y, R);
   if ((row_view || col_view) && (!vec || !aligned(d->row_codes, 16) || !aligned(d->col_codes, 16)))
-    return gtp::fail(GTP_E_ALIGN, "with a view the rows of every matrix, the weight and the codes start on 16 bytes");
+    return gtp::fail(GTP_E_ALIGN, "with a view the rows of every matrix start on eight elements, the weight and the codes on 16 bytes");
   // no output shares a byte with an input or another output, but for the sum in place of x or of the residual, and y in
   // place of x
   gtp::Runs out[7];
@@ -592,7 +620,7 @@ extern "C" gtp_status gtp_rmsnorm(const gtp_rmsnorm_desc *d, gtp_stream stream) 
   a.sum_ld = R > 1 ? d->sum_ld : C, a.y_ld = R > 1 ? d->y_ld : C;
   a.row_words = d->tiled_scales ? (C / 32 + 3) / 4 : 0;
   a.col_words = d->tiled_scales ? (R / 32 + 3) / 4 : 0;
-  a.inv_cols = 1.f / float(C);
+  a.inv_cols = 1.f / float(C), a.codes_on_32 = aligned(d->col_codes, 32);
   a.eps = d->eps, a.weight_f32 = d->weight_dtype == GTP_F32, a.y_f32 = d->y_dtype == GTP_F32;
   cudaStream_t st = gtp::as_stream(stream);
   using B = __nv_bfloat16;
@@ -621,13 +649,17 @@ extern "C" gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e
     return gtp::fail(GTP_E_ARG, "out overlaps the view");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
-  const int64_t items = rows * (cols / 8), words = tiled_scales ? (cols / 32 + 3) / 4 : 0;
-  const unsigned grid = unsigned(std::min<int64_t>((items + 255) / 256, int64_t(dev.sm_count) * 16));
+  const int64_t words = tiled_scales ? (cols / 32 + 3) / 4 : 0;
+  int tx = 4;
+  while (tx < 256 && 8 * tx < cols) tx *= 2;
+  const dim3 block(tx, 256 / tx);
+  const int64_t gx = (cols + 8 * tx - 1) / (8 * tx);
+  const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>((rows + 4 * block.y - 1) / (4 * block.y), 65535)));
   cudaStream_t st = gtp::as_stream(stream);
-  const int vec = aligned(out, 16);
+  const int vec = aligned(out, 8 * size_of(out_dt));
   if (out_dt == GTP_F32)
-    return gtp::launch_overlapped(mxfp8_dequantize_kernel<float>, grid, 256, 0, st, "mxfp8_dequantize", e4m3, e8m0, rows, cols,
+    return gtp::launch_overlapped(mxfp8_dequantize_kernel<float>, grid, block, 0, st, "mxfp8_dequantize", e4m3, e8m0, rows, cols,
                                   words, static_cast<float *>(out), vec);
-  return gtp::launch_overlapped(mxfp8_dequantize_kernel<__nv_bfloat16>, grid, 256, 0, st, "mxfp8_dequantize", e4m3, e8m0, rows,
+  return gtp::launch_overlapped(mxfp8_dequantize_kernel<__nv_bfloat16>, grid, block, 0, st, "mxfp8_dequantize", e4m3, e8m0, rows,
                                 cols, words, static_cast<__nv_bfloat16 *>(out), vec);
 }

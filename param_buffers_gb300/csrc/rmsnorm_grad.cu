@@ -171,6 +171,9 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_grad_elements_kernel
     for (int k = 0; k < K; ++k) g[k] = live && t + k * TX < cols ? gtp::load1(dy + k * TX) : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) n[k] = live && t + k * TX < cols ? gtp::load1(s + k * TX) : 0.f;
+    TS d[K];  // with the others, not behind the stores
+#pragma unroll
+    for (int k = 0; k < K; ++k) d[k] = live && a.dsum && t + k * TX < cols ? ds[k * TX] : TS(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float wk = KEEP ? w[KEEP ? k : 0] : t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
@@ -185,10 +188,7 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_grad_elements_kernel
     TS *const dx = static_cast<TS *>(a.dx) + row * a.dx_ld + t;
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (t + k * TX < cols) {
-        const float d = a.dsum ? gtp::load1(ds + k * TX) : 0.f;
-        gtp::store1(dx + k * TX, fmaf(r, fmaf(-n[k], mean, g[k]), d));
-      }
+      if (t + k * TX < cols) gtp::store1(dx + k * TX, fmaf(r, fmaf(-n[k], mean, g[k]), gtp::load1(&d[k])));
   }
   float *const out = a.part + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * a.cols + t;
 #pragma unroll
@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *part, in
 
 // --------------------------------------------------------------------------- host
 
-// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four) and blocks: two of 512
-// threads an SM or as many threads in smaller ones.  One rule for the workspace's size and the launch.
+// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four) and blocks: those that run at
+// once, 512 threads an SM (128 registers each).  One rule for the workspace's size and the launch.
 struct GradShape {
   int tx, ty, V, grid;
 };
@@ -233,7 +233,7 @@ GradShape grad_shape(int64_t rows, int64_t cols, int sms) {
   const int64_t groups = (cols + 7) / 8;
   const int V = groups <= kRowThreads ? 1 : 4;
   const int tx = int((groups + 32 * V - 1) / (32 * V)) * 32, ty = tx == 32 ? 8 : 1;
-  const int64_t most = int64_t(sms) * std::max(1, 1024 / (tx * ty));
+  const int64_t most = int64_t(sms) * std::max(1, 512 / (tx * ty));
   return {tx, ty, V, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
 }
 
@@ -291,8 +291,8 @@ extern "C" gtp_status gtp_rmsnorm_grad(const gtp_rmsnorm_grad_desc *d, void *wor
     if (gtp_status e = check_matrix(ds, R, C)) return e;
   if (!d->rstd || !d->grad_data || !workspace) return gtp::fail(GTP_E_ARG, "null pointer");
   const int64_t gs = size_of(d->grad_dtype);
-  if (!aligned(d->rstd, 4) || !aligned(d->grad_data, gs) || !aligned(workspace, 16))
-    return gtp::fail(GTP_E_ALIGN, "rstd and grad_data must be aligned to their elements, the workspace to 16 bytes");
+  if (!aligned(d->rstd, 4) || !aligned(d->grad_data, gs) || !aligned(workspace, 32))
+    return gtp::fail(GTP_E_ALIGN, "rstd and grad_data must be aligned to their elements, the workspace to 32 bytes");
   const int64_t need = gtp_rmsnorm_grad_workspace_bytes(R, C);
   if (workspace_bytes < need)
     return gtp::fail(GTP_E_CAPACITY, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);

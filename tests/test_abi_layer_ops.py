@@ -49,7 +49,7 @@ GRAD = dict(ids=at(0), ids64=1, tokens=10, dout=at(1), dout_dt=BF16, dout_ld=64,
     (dict(total=1 << 62, offset=1 << 61), RANGE), (dict(workspace=None), ARG), (dict(grad=None), ARG), (dict(ids=None), ARG),
     (dict(dout=None), ARG), (dict(workspace=at(3) + 8), ALIGN), (dict(grad=at(2) + 2), ALIGN), (dict(dout=at(1) + 1), ALIGN),
     (dict(bytes=100), CAPACITY), (dict(grad=at(1)), ARG), (dict(workspace=at(2) + 1024), ARG), (dict(workspace=at(0)), ARG),
-    (dict(workspace=at(1) + 16), ARG), (dict(tokens=0), OK), (dict(rows=0), OK)])
+    (dict(workspace=at(1) + 32), ARG), (dict(workspace=at(3) + 16), ALIGN), (dict(tokens=0), OK), (dict(rows=0), OK)])
 def test_embedding_gradient(change, status):
     assert abi.load().gtp_embedding_grad_accum(*{**GRAD, **change}.values(), None) == status
 
