@@ -774,16 +774,28 @@ gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld
  * gtp_embedding_grad_workspace_bytes (-1 for sizes that the call refuses; GTP_E_CAPACITY where it is
  * smaller); its contents are not needed afterwards, and calls that may overlap on the GPU need one each.
  * Sizes up to 2^30 a dimension and 2^40 elements (GTP_E_SHAPE). */
-gtp_status gtp_embedding(const void *ids, int32_t ids64, int64_t tokens, const void *table,
-                         gtp_dtype table_dt, int64_t table_ld, int64_t first_row, int64_t rows,
-                         int64_t cols, float scale, void *out, gtp_dtype out_dt, int64_t out_ld,
-                         gtp_stream stream);
+typedef struct {
+  const void *ids, *table;
+  void *out;
+  int64_t tokens, first_row, rows, cols, table_ld, out_ld;
+  float scale;
+  int32_t ids64, table_dtype, out_dtype; /* 0 or 1; GTP_F32 or GTP_BF16 */
+  int64_t reserved;                      /* 0                           */
+} gtp_embedding_desc;
+
+typedef struct {
+  const void *ids, *dout;
+  void *grad_data;
+  int64_t tokens, first_row, rows, cols, dout_ld, grad_offset, grad_numel_total;
+  float scale;
+  int32_t ids64, dout_dtype, grad_dtype;
+  int64_t reserved;
+} gtp_embedding_grad_desc;
+
+gtp_status gtp_embedding(const gtp_embedding_desc *desc, gtp_stream stream);
 int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
-gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, int64_t tokens, const void *dout,
-                                    gtp_dtype dout_dt, int64_t dout_ld, int64_t first_row,
-                                    int64_t rows, int64_t cols, float scale, void *grad_data,
-                                    gtp_dtype grad_dt, int64_t grad_offset, int64_t grad_numel_total,
-                                    void *workspace, int64_t workspace_bytes, gtp_stream stream);
+gtp_status gtp_embedding_grad_accum(const gtp_embedding_grad_desc *desc, void *workspace,
+                                    int64_t workspace_bytes, gtp_stream stream);
 
 /* ------------------------------------------------------------------------ root-mean-square norm
  * The norm before the attention block and before the MLP, on the residual stream ([MLM] §1):

@@ -1103,14 +1103,21 @@ def gtp_dropout_grad(dout, dx, p: float, rng, stream=None) -> None:
 
 # ----------------------------------------------------------------------------- token embedding
 
+_ID_DTYPES: dict = {}  # torch's integer types -> whether of 64 bits; filled at the first call
+
+
 def _ids(ids):
     """(64-bit or not, count) of a vector of token ids."""
-    import torch
-    if ids.dtype not in (torch.int32, torch.int64):
+    if not _ID_DTYPES:
+        import torch
+        _ID_DTYPES.update({torch.int32: 0, torch.int64: 1})
+    wide = _ID_DTYPES.get(ids.dtype)
+    if wide is None:
         raise TypeError("ids must be int32 or int64")
-    if len(ids.shape) != 1 or not ids.is_contiguous() or not ids.is_cuda:
+    shape = ids.shape
+    if len(shape) != 1 or not ids.is_contiguous() or not ids.is_cuda:
         raise ValueError("ids must be contiguous with 1 dim, on the GPU")
-    return ids.dtype == torch.int64, ids.shape[0]
+    return wide, shape[0]
 
 
 def _bytes(t, name: str) -> int:
@@ -1141,9 +1148,12 @@ def gtp_embedding(ids, table, out, first_row: int = 0, scale: float = 1.0, strea
     od, os, ol = _matrix(out, "out")
     if os != (T, ts[1]):
         raise ValueError(f"out must be [{T}, {ts[1]}]")
-    _check(lib().gtp_embedding(ids.data_ptr(), wide, T, table.data_ptr(), td, tl, first_row, ts[0], ts[1], scale,
-                               out.data_ptr(), od, ol, _stream(stream)),
-           "gtp_embedding")
+    try:
+        d = abi.EMBEDDING_DESC_PACK(ids.data_ptr(), table.data_ptr(), out.data_ptr(), T, first_row, ts[0], ts[1], tl, ol,
+                                    scale, wide, td, od, 0)
+    except (abi.struct.error, OverflowError):
+        raise ValueError("first_row must be a 64-bit integer, scale a number that fits fp32") from None
+    _check(lib().gtp_embedding(d, _stream(stream)), "gtp_embedding")
 
 
 def gtp_embedding_grad_workspace_bytes(tokens: int, rows: int, cols: int) -> int:
@@ -1160,9 +1170,12 @@ def gtp_embedding_grad_accum(dout, ids, grad_data, grad_offset: int, rows: int, 
     if ds[0] != T:
         raise ValueError(f"dout must have {T} rows")
     gd = _grad_buffer(grad_data)
-    _check(lib().gtp_embedding_grad_accum(ids.data_ptr(), wide, T, dout.data_ptr(), dd, dl, first_row, rows, ds[1], scale,
-                                          grad_data.data_ptr(), gd, grad_offset, grad_data.numel(), workspace.data_ptr(),
-                                          _bytes(workspace, "workspace"), _stream(stream)),
+    try:
+        d = abi.EMBEDDING_GRAD_DESC_PACK(ids.data_ptr(), dout.data_ptr(), grad_data.data_ptr(), T, first_row, rows, ds[1], dl,
+                                         grad_offset, grad_data.numel(), scale, wide, dd, gd, 0)
+    except (abi.struct.error, OverflowError):
+        raise ValueError("first_row, rows and grad_offset must be 64-bit integers, scale a number that fits fp32") from None
+    _check(lib().gtp_embedding_grad_accum(d, workspace.data_ptr(), _bytes(workspace, "workspace"), _stream(stream)),
            "gtp_embedding_grad_accum")
 
 

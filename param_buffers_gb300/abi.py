@@ -114,6 +114,20 @@ class gtp_rotary_desc(C.Structure):
 ROTARY_DESC_PACK = struct.Struct("<3Q10qQ8ifi").pack
 
 
+class gtp_embedding_desc(C.Structure):
+    _fields_ = [("ids", C.c_void_p), ("table", C.c_void_p), ("out", C.c_void_p), ("tokens", C.c_int64),
+                ("first_row", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64), ("table_ld", C.c_int64),
+                ("out_ld", C.c_int64), ("scale", C.c_float), ("ids64", C.c_int32), ("table_dtype", C.c_int32),
+                ("out_dtype", C.c_int32), ("reserved", C.c_int64)]
+
+
+class gtp_embedding_grad_desc(C.Structure):
+    _fields_ = [("ids", C.c_void_p), ("dout", C.c_void_p), ("grad_data", C.c_void_p), ("tokens", C.c_int64),
+                ("first_row", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64), ("dout_ld", C.c_int64),
+                ("grad_offset", C.c_int64), ("grad_numel_total", C.c_int64), ("scale", C.c_float), ("ids64", C.c_int32),
+                ("dout_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("reserved", C.c_int64)]
+
+
 class gtp_rmsnorm_desc(C.Structure):
     _fields_ = [("x", C.c_void_p), ("residual", C.c_void_p), ("weight", C.c_void_p), ("sum", C.c_void_p),
                 ("y", C.c_void_p), ("rstd", C.c_void_p), ("row_codes", C.c_void_p), ("row_scales", C.c_void_p),
@@ -139,7 +153,10 @@ class gtp_muon_hparams(C.Structure):
                 ("grad_scale", C.c_void_p)]
 
 
-# Packed likewise: gtp_rmsnorm_desc (padded to 8 bytes at its end), gtp_rmsnorm_grad_desc and gtp_muon_hparams.
+# Packed likewise: gtp_embedding_desc, gtp_embedding_grad_desc, gtp_rmsnorm_desc (padded to 8 bytes at its end),
+# gtp_rmsnorm_grad_desc and gtp_muon_hparams.
+EMBEDDING_DESC_PACK = struct.Struct("<3Q6qf3iq").pack
+EMBEDDING_GRAD_DESC_PACK = struct.Struct("<3Q7qf3iq").pack
 RMSNORM_DESC_PACK = struct.Struct("<10Q6qf6i4x").pack
 RMSNORM_GRAD_DESC_PACK = struct.Struct("<7Q8q4iq").pack
 MUON_HPARAMS_PACK = struct.Struct("<8f4iQ").pack
@@ -148,7 +165,7 @@ COEFFICIENTS_PACK = struct.Struct("<3f").pack
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
-# A gtp_rng, gtp_rotary_desc, gtp_rmsnorm_desc, gtp_rmsnorm_grad_desc or gtp_muon_hparams goes by reference or packed
+# A gtp_rng, gtp_rotary_desc, gtp_embedding_desc, gtp_embedding_grad_desc, gtp_rmsnorm_desc, gtp_rmsnorm_grad_desc or gtp_muon_hparams goes by reference or packed
 # (VP takes both).
 # name -> (restype, argtypes); every entry point declared in include/gtp.h
 PROTOTYPES = {
@@ -201,10 +218,9 @@ PROTOTYPES = {
     "gtp_rotary": (I32, [VP, VP]),
     "gtp_dropout_add": (I32, [VP, I32, I64, VP, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
     "gtp_dropout_grad": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, C.c_float, VP, VP]),
-    "gtp_embedding": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, I64, C.c_float, VP, I32, I64, VP]),
+    "gtp_embedding": (I32, [VP, VP]),
     "gtp_embedding_grad_workspace_bytes": (I64, [I64, I64, I64]),
-    "gtp_embedding_grad_accum": (I32, [VP, I32, I64, VP, I32, I64, I64, I64, I64, C.c_float, VP, I32, I64, I64, VP, I64,
-                                       VP]),
+    "gtp_embedding_grad_accum": (I32, [VP, VP, I64, VP]),
     "gtp_rmsnorm": (I32, [VP, VP]),
     "gtp_rmsnorm_grad_workspace_bytes": (I64, [I64, I64]),
     "gtp_rmsnorm_grad": (I32, [VP, VP, I64, VP]),

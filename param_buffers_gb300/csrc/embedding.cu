@@ -7,8 +7,8 @@
 //   grad[r] += scale * sum of dout[t] over the tokens t of row r
 // The gradient's sum over a row's tokens is formed in fp32 in an order that depends on the ids alone: tokens are sorted
 // by row (ties in token order), the sorted list is cut into tiles of equal length, a row inside a tile is summed and
-// added at once, a row that crosses tiles leaves one partial a tile, joined in order by a second kernel.  No atomic's
-// order takes part, so equal calls give equal bits.
+// added at once, a row that crosses tiles leaves one part a tile, and whoever leaves the last part adds them all up in
+// their order.  No atomic's order takes part, so equal calls give equal bits.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -147,7 +147,14 @@ struct SortArgs {
   int32_t *key2, *token2;
   int32_t *counts;  // radix: [256][tiles]
   int32_t tiles;
+  int32_t *counters;  // of the sums, cleared here
+  int64_t counter_count;
 };
+
+__device__ __forceinline__ void clear_counters(const SortArgs &a) {
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < a.counter_count; i += int64_t(gridDim.x) * blockDim.x)
+    a.counters[i] = 0;
+}
 
 // Few tokens: the place of a token is the number of tokens that sort before it, counted outright.  A block owns
 // kOwn tokens, keeps every token of the shard as one 32-bit number row * tokens + t in shared memory (any order: the
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constan
   if (threadIdx.x == 0) listed = owned = 0;
   if (threadIdx.x < kOwn) place[threadIdx.x] = 0;
   gtp::ptx::wait_prior_grid();
+  clear_counters(a);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = blockIdx.x * kOwn;
@@ -249,6 +257,7 @@ __global__ void __launch_bounds__(kTileThreads)
   gtp::ptx::allow_dependents();
   count[threadIdx.x] = 0;
   gtp::ptx::wait_prior_grid();
+  if (shift == 0) clear_counters(a);
   __syncthreads();
   for (int i = 0; i < kRounds; ++i) {
     const int64_t p = int64_t(blockIdx.x) * kTile + i * kTileThreads + threadIdx.x;
@@ -364,8 +373,9 @@ struct SumArgs {
   const void *dout;
   void *grad;
   float *part;  // [tiles][2][cols]: the row that comes in from the tile before, and the one that goes on
+  int32_t *counters;  // [tiles][3][groups]
   int64_t dout_ld, rows, cols;
-  int32_t tokens, tile, tiles;
+  int32_t tokens, tile, tiles, groups;  // groups: warps across a row
   float scale;
 };
 
@@ -393,6 +403,113 @@ __device__ __forceinline__ void add8(__nv_bfloat16 *p, int step, int n, float sc
   Group<__nv_bfloat16, VEC>::store(p, step, n, g);
 }
 
+// A part, past the first-level cache: another block may have written it.
+template <bool VEC>
+__device__ __forceinline__ void load_part(const float *p, int step, int n, float (&x)[8]) {
+  if (VEC) {
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? __ldcg(p + k * step) : 0.f;
+  }
+}
+
+// A row that crosses tiles: its parts are those of tiles first .. last, the first one's second, the others' first.  Each
+// warp counts its tile off once its part is written; the one that counts the last off adds them up in their order, up to
+// kJoin of them.  Of a longer row the tiles of an aligned group of kJoin count among themselves, their sum takes the place
+// of the group's first part, and the groups count in turn.
+constexpr int kJoin = 16;
+
+// The tile in which the row that comes into `tile` begins: the last one before it that the row does not fill.  A lane
+// looks at one tile's first place, 32 tiles at a time, or far from here at steps that narrow by 32.
+__device__ __forceinline__ int begins_at(const SumArgs &a, int tile, int row) {
+  const int lane = threadIdx.x & 31;
+  // the row fills the tiles hi .. tile - 1 but for their last tokens' rows; it begins in lo .. hi
+  int hi = tile, lo = 0;
+  for (int step = 1;; step = max((hi - lo + 31) / 32, 1)) {
+    const int t = hi - 1 - lane * step;  // whether the row is there before its first place
+    const bool reaches = t >= 0 && t * a.tile > 0 && a.key[t * a.tile - 1] == row;
+    const unsigned no = __ballot_sync(0xFFFFFFFFu, !reaches);
+    const int first = __ffs(int(no)) - 1;  // -1: all 32 do
+    if (first >= 0) {
+      if (step == 1) return hi - 1 - first;
+      lo = max(lo, hi - 1 - first * step);
+      if (first > 0) hi = hi - 1 - (first - 1) * step;
+    } else {
+      hi = hi - 1 - 31 * step;
+    }
+  }
+}
+
+// The tile in which the row that goes on from `tile` ends.
+__device__ __forceinline__ int ends_at(const SumArgs &a, int tile, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = tile, hi = a.tiles - 1;  // it ends in lo .. hi
+  for (int step = 1;; step = max((hi - lo + 31) / 32, 1)) {
+    const int t = lo + 1 + lane * step;  // whether the row goes on behind its last place
+    const bool goes = t < a.tiles - 1 && a.key[(t + 1) * a.tile] == row;
+    const unsigned no = __ballot_sync(0xFFFFFFFFu, !goes);
+    const int first = __ffs(int(no)) - 1;
+    if (first >= 0) {
+      if (step == 1) return lo + 1 + first;
+      hi = min(hi, lo + 1 + first * step);
+      if (first > 0) lo = lo + 1 + (first - 1) * step;
+    } else {
+      lo = lo + 1 + 31 * step;
+    }
+  }
+}
+
+template <typename TG, bool VEC>
+__device__ __forceinline__ void join_row(const SumArgs &a, int tile, int first, int last, int row, int group, int64_t c, int step,
+                                         int n) {
+  const int lane = threadIdx.x & 31;
+  const auto place = [&](int t) { return a.part + (int64_t(t) * 2 + (t == first)) * a.cols + c; };
+  const auto last_of = [&](int t, int which, int of) {  // whether this warp counts the last of them off
+    __threadfence();
+    __syncwarp();
+    int before = 0;
+    if (lane == 0) before = atomicAdd(a.counters + (int64_t(t) * 3 + which) * a.groups + group, 1);
+    before = __shfl_sync(0xFFFFFFFFu, before, 0);
+    __threadfence();
+    return before == of - 1;
+  };
+  float acc[8];
+  const auto sum = [&](int from, int to, int by, bool groups) {  // parts from .. to, four in flight
+    constexpr int N = 4;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    for (int t0 = from; t0 <= to; t0 += N * by) {
+      float x[N][8];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+        const int t = t0 + i * by;
+        if (t <= to && n > 0) load_part<VEC>(place(groups ? max(t, first) : t), step, n, x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += x[i][k];
+    }
+  };
+  TG *const grad = static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c;
+  if (last - first < kJoin) {
+    if (!last_of(first, 1, last - first + 1)) return;
+    sum(first, last, 1, false);
+  } else {
+    const int g = tile & ~(kJoin - 1), t0 = max(first, g), t1 = min(last, g + kJoin - 1);
+    if (!last_of(t0, t0 == first, t1 - t0 + 1)) return;
+    sum(t0, t1, 1, false);
+    if (n > 0) Group<float, VEC>::store(place(t0), step, n, acc);
+    if (!last_of(first, 2, last / kJoin - first / kJoin + 1)) return;
+    sum(first & ~(kJoin - 1), last, kJoin, true);
+  }
+  if (n > 0) add8<VEC>(grad, step, n, a.scale, acc);
+}
+
 // A tile a thread row (whole warps, so that a warp's lanes read the keys of 32 places at once and hand them round), eight
 // columns a thread, kFlight tokens' rows in flight.
 constexpr int kFlight = 8;
@@ -405,6 +522,7 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
   int n = 0;
   const int tile = int(blockIdx.y) * blockDim.y + threadIdx.y, lane = threadIdx.x & 31;
   const bool mine = columns<VEC>(a.cols, c, n);
+  if (!mine) n = 0;
   if (tile >= a.tiles) return;  // the whole warp
   const int tx = blockDim.x, rows = int(a.rows);
   const int p0 = tile * a.tile, p1 = min(p0 + a.tile, a.tokens);
@@ -413,8 +531,9 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   float *const part = a.part + int64_t(tile) * 2 * a.cols + c;
-  int row = rows;     // the row being summed
-  bool open = false;  // its first tokens are in the tile before
+  const int group = int(blockIdx.x) * (tx >> 5) + (int(threadIdx.x) >> 5);
+  int row = rows, came = rows;  // the row being summed; the one that came in, once its part is written
+  bool open = false;            // the row being summed came in from the tile before
   for (int q0 = p0; q0 < p1; q0 += 32) {
     const int q = q0 + lane;
     const int key = q < p1 ? a.key[q] : rows, token = q < p1 ? a.token[q] : 0;  // not a token where key is rows
@@ -432,18 +551,22 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
         const int t = __shfl_sync(0xFFFFFFFFu, token, i0 + i);
         if (k[i] < rows && mine) x[i].load(static_cast<const TD *>(a.dout) + int64_t(t) * a.dout_ld + c, tx, n);
       }
-      if (!mine) continue;
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         if (k[i] >= rows) continue;
         if (k[i] != row) {
-          if (open) Group<float, VEC>::store(part, tx, n, acc);
-          else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+          if (open) {
+            if (mine) Group<float, VEC>::store(part, tx, n, acc);
+            came = row;
+          } else if (mine) {
+            add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+          }
           open = false;
           row = k[i];
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[j] = 0.f;
         }
+        if (!mine) continue;
         float f[8];
         x[i].get(f);
 #pragma unroll
@@ -451,101 +574,17 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
       }
     }
   }
-  if (!mine) return;
-  if (open) Group<float, VEC>::store(part, tx, n, acc);
-  else if (after == row) Group<float, VEC>::store(part + a.cols, tx, n, acc);
-  else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
-}
-
-// The rows that cross tiles.  A block has 32 tiles and 256 columns; its eight warps look at the tiles in which such a row
-// begins.  A row of up to kShort more tiles is one warp's, which adds its parts up in order; a longer one is everybody's:
-// warp w adds every eighth part from w on, and the eight sums are added up in order.
-constexpr int kJoinTiles = 32, kShort = 8;
-
-template <typename TG, bool VEC>
-__global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ float sums[8][256];
-  gtp::ptx::allow_dependents();
-  gtp::ptx::wait_prior_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = int(a.rows);
-  const int64_t c = int64_t(blockIdx.x) * 256 + (VEC ? 8 * lane : lane);
-  const int step = 32, n = c >= a.cols ? 0 : VEC ? 8 : int(min(int64_t(8), (a.cols - c + 31) / 32));
-  // this lane's tile: its last row goes on and does not come in
-  const int tile = int(blockIdx.y) * kJoinTiles + lane, p1 = (tile + 1) * a.tile;
-  const int row = tile < a.tiles && p1 < a.tokens ? a.key[p1] : rows;
-  bool begins = row < rows && a.key[p1 - 1] == row && (tile == 0 || a.key[p1 - 1 - a.tile] != row);
-  // how many tiles more begin with it, counted up to kShort + 1
-  int more = 0;
-#pragma unroll
-  for (int i = 1; i <= kShort + 1; ++i) more += begins && tile + i < a.tiles && a.key[(tile + i) * a.tile] == row;
-  unsigned longer = __ballot_sync(0xFFFFFFFFu, begins && more > kShort);
-  unsigned todo = __ballot_sync(0xFFFFFFFFu, begins) & ~longer;
-  const auto part_of = [&](int t, int which) { return a.part + (int64_t(t) * 2 + which) * a.cols + c; };
-  int turn = 0;
-  for (; todo; todo &= todo - 1, ++turn) {
-    const int l = __ffs(todo) - 1;
-    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l), m = __shfl_sync(0xFFFFFFFFu, more, l);
-    if ((turn & 7) != warp || n == 0) continue;
-    Group<float, VEC> x[kShort + 1];
-#pragma unroll
-    for (int i = 0; i <= kShort; ++i) {
-      x[i].clear();
-      if (i <= m) x[i].load(part_of(t + i, i == 0), step, n);
-    }
-    float acc[8], f[8];
-    x[0].get(acc);
-#pragma unroll
-    for (int i = 1; i <= kShort; ++i) {
-      x[i].get(f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += f[k];
-    }
-    add8<VEC>(static_cast<TG *>(a.grad) + int64_t(r) * a.cols + c, step, n, a.scale, acc);
+  const bool goes = after == row;
+  if (mine) {
+    if (open) Group<float, VEC>::store(part, tx, n, acc);
+    else if (goes) Group<float, VEC>::store(part + a.cols, tx, n, acc);
+    else add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
   }
-  for (; longer; longer &= longer - 1) {  // the same for every warp
-    const int l = __ffs(longer) - 1;
-    const int t = int(blockIdx.y) * kJoinTiles + l, r = __shfl_sync(0xFFFFFFFFu, row, l);
-    int m = kShort + 1;  // tiles after t that begin with it: counted on, 32 at a time
-    for (;;) {
-      const int u = t + 1 + m + lane;
-      const unsigned same = __ballot_sync(0xFFFFFFFFu, u < a.tiles && a.key[u * a.tile] == r);
-      m += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
-      if (same != 0xFFFFFFFFu) break;
-    }
-    float acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-    if (n > 0) {
-      constexpr int N = 4;  // parts in flight
-      for (int i0 = warp; i0 <= m; i0 += 8 * N) {
-        Group<float, VEC> x[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          x[i].clear();
-          if (i0 + 8 * i <= m) x[i].load(part_of(t + i0 + 8 * i, i0 + 8 * i == 0), step, n);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float f[8];
-          x[i].get(f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] += f[k];
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sums[warp][VEC ? 8 * lane + k : lane + 32 * k] = acc[k];
-    __syncthreads();
-    const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;  // a column a thread
-    if (col < a.cols) {
-      float s = sums[0][threadIdx.x];
-#pragma unroll
-      for (int w = 1; w < 8; ++w) s += sums[w][threadIdx.x];
-      TG *const g = static_cast<TG *>(a.grad) + int64_t(r) * a.cols + col;
-      gtp::store1(g, fmaf(a.scale, s, gtp::load1(g)));
-    }
-    __syncthreads();
-  }
+  const bool came_in = came < rows;
+  if (!came_in && !open && !goes) return;
+  const int begins = came_in || open ? begins_at(a, tile, came_in ? came : row) : tile, ends = goes ? ends_at(a, tile, row) : tile;
+  if (came_in) join_row<TG, VEC>(a, tile, begins, tile, came, group, c, tx, n);
+  if (open || goes) join_row<TG, VEC>(a, tile, open ? begins : tile, ends, row, group, c, tx, n);
 }
 
 // --------------------------------------------------------------------------- host
@@ -564,7 +603,8 @@ bool in_eights(const void *p, int64_t ld, int64_t es) {
   return (reinterpret_cast<uintptr_t>(p) & uintptr_t(8 * es - 1)) == 0 && ld % 8 == 0;
 }
 
-int64_t size_of(gtp_dtype dt) { return dt == GTP_F32 ? 4 : 2; }
+int64_t size_of(int dt) { return dt == GTP_F32 ? 4 : 2; }
+bool float_type(int dt) { return dt == GTP_F32 || dt == GTP_BF16; }
 
 gtp_status check_sizes(int64_t tokens, int64_t first_row, int64_t rows, int64_t cols, int32_t ids64) {
   if (tokens < 0 || rows < 0 || cols < 0 || first_row < 0) return gtp::fail(GTP_E_ARG, "negative size");
@@ -603,7 +643,8 @@ gtp_status launch_lookup(const LookupArgs &a, const gtp::DeviceInfo &dev, cudaSt
 struct GradPlan {
   int32_t tile, tiles, sort_tiles;
   bool radix;
-  int64_t key, token, key2, token2, counts, part, bytes;  // places in the workspace
+  int32_t groups;
+  int64_t key, token, key2, token2, counts, counters, part, bytes;  // places in the workspace
 };
 
 GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
@@ -626,6 +667,9 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
     p.token2 = take(4 * tokens);
     p.counts = take(int64_t(4) * 256 * p.sort_tiles);
   }
+  const dim3 block = block_of(cols, 32);
+  p.groups = int32_t((cols + 8 * block.x - 1) / (8 * block.x) * (block.x / 32));
+  p.counters = take(int64_t(12) * p.tiles * p.groups);
   p.part = take(int64_t(8) * p.tiles * cols);
   p.bytes = at;
   return p;
@@ -665,45 +709,39 @@ gtp_status launch_sums(const SumArgs &a, cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && in_eights(a.dout, a.dout_ld, sizeof(TD)) && in_eights(a.grad, a.cols, sizeof(TG));
   const dim3 block = block_of(a.cols, 32);
   const dim3 grid(unsigned((a.cols + 8 * block.x - 1) / (8 * block.x)), (a.tiles + block.y - 1) / block.y);
-  if (gtp_status s = gtp::launch_overlapped(vec ? embedding_sum_kernel<TD, TG, true> : embedding_sum_kernel<TD, TG, false>, grid,
-                                            block, 0, st, "embedding_grad", a))
-    return s;
-  if (a.tiles == 1) return GTP_OK;
-  const dim3 join(unsigned((a.cols + 255) / 256), unsigned((a.tiles + kJoinTiles - 1) / kJoinTiles));
-  return gtp::launch_overlapped(vec ? embedding_join_kernel<TG, true> : embedding_join_kernel<TG, false>, join, kThreads, 0, st,
+  return gtp::launch_overlapped(vec ? embedding_sum_kernel<TD, TG, true> : embedding_sum_kernel<TD, TG, false>, grid, block, 0, st,
                                 "embedding_grad", a);
 }
 
 }  // namespace
 
-extern "C" gtp_status gtp_embedding(const void *ids, int32_t ids64, int64_t tokens, const void *table, gtp_dtype table_dt,
-                                    int64_t table_ld, int64_t first_row, int64_t rows, int64_t cols, float scale, void *out,
-                                    gtp_dtype out_dt, int64_t out_ld, gtp_stream stream) {
+extern "C" gtp_status gtp_embedding(const gtp_embedding_desc *d, gtp_stream stream) {
   gtp::clear_error();
-  if ((table_dt != GTP_F32 && table_dt != GTP_BF16) || (out_dt != GTP_F32 && out_dt != GTP_BF16))
-    return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
-  if (gtp_status s = check_sizes(tokens, first_row, rows, cols, ids64)) return s;
-  if (gtp_status s = check_ld("table", table_ld, rows, cols)) return s;
-  if (gtp_status s = check_ld("out", out_ld, tokens, cols)) return s;
-  if (tokens == 0 || cols == 0) return GTP_OK;
-  if (!ids || !out || (!table && rows)) return gtp::fail(GTP_E_ARG, "null pointer");
-  const int64_t ts = size_of(table_dt), os = size_of(out_dt), is = ids64 ? 8 : 4;
-  if ((reinterpret_cast<uintptr_t>(ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(table) & uintptr_t(ts - 1)) ||
-      (reinterpret_cast<uintptr_t>(out) & uintptr_t(os - 1)))
+  if (!d) return gtp::fail(GTP_E_ARG, "null descriptor");
+  if (d->reserved) return gtp::fail(GTP_E_ARG, "reserved must be 0");
+  if (!float_type(d->table_dtype) || !float_type(d->out_dtype)) return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
+  const int64_t T = d->tokens, R = d->rows, C = d->cols;
+  if (gtp_status s = check_sizes(T, d->first_row, R, C, d->ids64)) return s;
+  if (gtp_status s = check_ld("table", d->table_ld, R, C)) return s;
+  if (gtp_status s = check_ld("out", d->out_ld, T, C)) return s;
+  if (T == 0 || C == 0) return GTP_OK;
+  if (!d->ids || !d->out || (!d->table && R)) return gtp::fail(GTP_E_ARG, "null pointer");
+  const int64_t ts = size_of(d->table_dtype), os = size_of(d->out_dtype), is = d->ids64 ? 8 : 4;
+  if ((reinterpret_cast<uintptr_t>(d->ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(d->table) & uintptr_t(ts - 1)) ||
+      (reinterpret_cast<uintptr_t>(d->out) & uintptr_t(os - 1)))
     return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
-  if (rows <= 1) table_ld = cols;
-  if (tokens == 1) out_ld = cols;
-  const gtp::ByteRange o = span_of(out, tokens, out_ld, cols, os);
-  if (gtp::overlap(o, span_of(table, rows, table_ld, cols, ts)) || gtp::overlap(o, gtp::byte_range(ids, tokens * is)))
+  const int64_t table_ld = R > 1 ? d->table_ld : C, out_ld = T > 1 ? d->out_ld : C;
+  const gtp::ByteRange o = span_of(d->out, T, out_ld, C, os);
+  if (gtp::overlap(o, span_of(d->table, R, table_ld, C, ts)) || gtp::overlap(o, gtp::byte_range(d->ids, T * is)))
     return gtp::fail(GTP_E_ARG, "out overlaps an input");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
-  const LookupArgs a = {ids, table, out, tokens, table_ld, out_ld, first_row, rows, cols, scale, ids64};
+  const LookupArgs a = {d->ids, d->table, d->out, T, table_ld, out_ld, d->first_row, R, C, d->scale, d->ids64};
   cudaStream_t st = gtp::as_stream(stream);
-  if (table_dt == GTP_F32)
-    return out_dt == GTP_F32 ? launch_lookup<float, float>(a, dev, st) : launch_lookup<float, __nv_bfloat16>(a, dev, st);
-  return out_dt == GTP_F32 ? launch_lookup<__nv_bfloat16, float>(a, dev, st)
-                           : launch_lookup<__nv_bfloat16, __nv_bfloat16>(a, dev, st);
+  using B = __nv_bfloat16;
+  if (d->table_dtype == GTP_F32)
+    return d->out_dtype == GTP_F32 ? launch_lookup<float, float>(a, dev, st) : launch_lookup<float, B>(a, dev, st);
+  return d->out_dtype == GTP_F32 ? launch_lookup<B, float>(a, dev, st) : launch_lookup<B, B>(a, dev, st);
 }
 
 extern "C" int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols) {
@@ -712,46 +750,50 @@ extern "C" int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t ro
   return grad_plan(tokens, rows, cols).bytes;
 }
 
-extern "C" gtp_status gtp_embedding_grad_accum(const void *ids, int32_t ids64, int64_t tokens, const void *dout,
-                                               gtp_dtype dout_dt, int64_t dout_ld, int64_t first_row, int64_t rows,
-                                               int64_t cols, float scale, void *grad_data, gtp_dtype grad_dt,
-                                               int64_t grad_offset, int64_t grad_numel_total, void *workspace,
-                                               int64_t workspace_bytes, gtp_stream stream) {
+extern "C" gtp_status gtp_embedding_grad_accum(const gtp_embedding_grad_desc *d, void *workspace, int64_t workspace_bytes,
+                                               gtp_stream stream) {
   gtp::clear_error();
-  if ((dout_dt != GTP_F32 && dout_dt != GTP_BF16) || (grad_dt != GTP_F32 && grad_dt != GTP_BF16))
-    return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
-  if (gtp_status s = check_sizes(tokens, first_row, rows, cols, ids64)) return s;
-  if (gtp_status s = check_ld("dout", dout_ld, tokens, cols)) return s;
-  if (grad_offset < 0 || grad_numel_total < 0 || grad_numel_total > (int64_t(1) << 50) || grad_offset > grad_numel_total ||
-      rows * cols > grad_numel_total - grad_offset)
-    return gtp::fail(GTP_E_RANGE, "the view of %lld elements at %lld leaves a buffer of %lld", (long long)(rows * cols),
-                     (long long)grad_offset, (long long)grad_numel_total);
-  if (tokens == 0 || rows == 0 || cols == 0) return GTP_OK;
-  if (!ids || !dout || !grad_data || !workspace) return gtp::fail(GTP_E_ARG, "null pointer");
-  const int64_t ds = size_of(dout_dt), gs = size_of(grad_dt), is = ids64 ? 8 : 4;
-  if ((reinterpret_cast<uintptr_t>(ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(dout) & uintptr_t(ds - 1)) ||
-      (reinterpret_cast<uintptr_t>(grad_data) & uintptr_t(gs - 1)))
+  if (!d) return gtp::fail(GTP_E_ARG, "null descriptor");
+  if (d->reserved) return gtp::fail(GTP_E_ARG, "reserved must be 0");
+  if (!float_type(d->dout_dtype) || !float_type(d->grad_dtype)) return gtp::fail(GTP_E_DTYPE, "dtypes must be F32 or BF16");
+  const int64_t T = d->tokens, R = d->rows, C = d->cols;
+  if (gtp_status s = check_sizes(T, d->first_row, R, C, d->ids64)) return s;
+  if (gtp_status s = check_ld("dout", d->dout_ld, T, C)) return s;
+  if (d->grad_offset < 0 || d->grad_numel_total < 0 || d->grad_numel_total > (int64_t(1) << 50) ||
+      d->grad_offset > d->grad_numel_total || R * C > d->grad_numel_total - d->grad_offset)
+    return gtp::fail(GTP_E_RANGE, "the view of %lld elements at %lld leaves a buffer of %lld", (long long)(R * C),
+                     (long long)d->grad_offset, (long long)d->grad_numel_total);
+  if (T == 0 || R == 0 || C == 0) return GTP_OK;
+  if (!d->ids || !d->dout || !d->grad_data || !workspace) return gtp::fail(GTP_E_ARG, "null pointer");
+  const int64_t ds = size_of(d->dout_dtype), gs = size_of(d->grad_dtype), is = d->ids64 ? 8 : 4;
+  if ((reinterpret_cast<uintptr_t>(d->ids) & uintptr_t(is - 1)) || (reinterpret_cast<uintptr_t>(d->dout) & uintptr_t(ds - 1)) ||
+      (reinterpret_cast<uintptr_t>(d->grad_data) & uintptr_t(gs - 1)))
     return gtp::fail(GTP_E_ALIGN, "arrays must be aligned to their elements");
   if (reinterpret_cast<uintptr_t>(workspace) & 31u) return gtp::fail(GTP_E_ALIGN, "workspace must be 32-byte aligned");
-  const GradPlan plan = grad_plan(tokens, rows, cols);
+  const GradPlan plan = grad_plan(T, R, C);
   if (workspace_bytes < plan.bytes)
     return gtp::fail(GTP_E_CAPACITY, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)plan.bytes);
-  if (tokens == 1) dout_ld = cols;
-  char *const grad = static_cast<char *>(grad_data) + grad_offset * gs, *const ws = static_cast<char *>(workspace);
-  const gtp::ByteRange g = gtp::byte_range(grad, rows * cols * gs), w = gtp::byte_range(ws, plan.bytes),
-                       d = span_of(dout, tokens, dout_ld, cols, ds), i = gtp::byte_range(ids, tokens * is);
-  if (gtp::overlap(g, d) || gtp::overlap(g, i) || gtp::overlap(w, d) || gtp::overlap(w, i) || gtp::overlap(w, g))
+  const int64_t dout_ld = T > 1 ? d->dout_ld : C;
+  char *const grad = static_cast<char *>(d->grad_data) + d->grad_offset * gs, *const ws = static_cast<char *>(workspace);
+  const gtp::ByteRange g = gtp::byte_range(grad, R * C * gs), w = gtp::byte_range(ws, plan.bytes),
+                       x = span_of(d->dout, T, dout_ld, C, ds), i = gtp::byte_range(d->ids, T * is);
+  if (gtp::overlap(g, x) || gtp::overlap(g, i) || gtp::overlap(w, x) || gtp::overlap(w, i) || gtp::overlap(w, g))
     return gtp::fail(GTP_E_ARG, "the gradient view or the workspace overlaps an input or the other");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
   const auto at = [&](int64_t place) { return reinterpret_cast<int32_t *>(ws + place); };
-  SortArgs sort = {ids, first_row, rows, int32_t(tokens), ids64, at(plan.key), at(plan.token), at(plan.key2),
-                   at(plan.token2), at(plan.counts), plan.sort_tiles};
+  SortArgs sort = {};
+  sort.ids = d->ids, sort.first_row = d->first_row, sort.rows = R, sort.tokens = int32_t(T), sort.wide = d->ids64;
+  sort.key = at(plan.key), sort.token = at(plan.token), sort.key2 = at(plan.key2), sort.token2 = at(plan.token2);
+  sort.counts = at(plan.counts), sort.tiles = plan.sort_tiles;
+  sort.counters = at(plan.counters), sort.counter_count = int64_t(3) * plan.tiles * plan.groups;
   cudaStream_t st = gtp::as_stream(stream);
   if (gtp_status s = sort_tokens(sort, plan, st)) return s;
-  const SumArgs a = {at(plan.key), at(plan.token), dout, grad, reinterpret_cast<float *>(ws + plan.part), dout_ld, rows, cols,
-                     int32_t(tokens), plan.tile, plan.tiles, scale};
-  if (dout_dt == GTP_F32)
-    return grad_dt == GTP_F32 ? launch_sums<float, float>(a, st) : launch_sums<float, __nv_bfloat16>(a, st);
-  return grad_dt == GTP_F32 ? launch_sums<__nv_bfloat16, float>(a, st) : launch_sums<__nv_bfloat16, __nv_bfloat16>(a, st);
+  SumArgs a = {};
+  a.key = sort.key, a.token = sort.token, a.dout = d->dout, a.grad = grad, a.part = reinterpret_cast<float *>(ws + plan.part);
+  a.counters = sort.counters, a.groups = plan.groups;
+  a.dout_ld = dout_ld, a.rows = R, a.cols = C, a.tokens = int32_t(T), a.tile = plan.tile, a.tiles = plan.tiles, a.scale = d->scale;
+  using B = __nv_bfloat16;
+  if (d->dout_dtype == GTP_F32) return d->grad_dtype == GTP_F32 ? launch_sums<float, float>(a, st) : launch_sums<float, B>(a, st);
+  return d->grad_dtype == GTP_F32 ? launch_sums<B, float>(a, st) : launch_sums<B, B>(a, st);
 }

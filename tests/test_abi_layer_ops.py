@@ -18,17 +18,22 @@ def at(k):
 
 
 def test_struct_sizes():
+    assert C.sizeof(abi.gtp_embedding_desc) == 96 == len(abi.EMBEDDING_DESC_PACK(*[0] * 9, 0.0, *[0] * 4))
+    assert C.sizeof(abi.gtp_embedding_grad_desc) == 104 == len(abi.EMBEDDING_GRAD_DESC_PACK(*[0] * 10, 0.0, *[0] * 4))
     assert C.sizeof(abi.gtp_rmsnorm_desc) == 160 == len(abi.RMSNORM_DESC_PACK(*[0] * 16, 0.0, *[0] * 6))
     assert C.sizeof(abi.gtp_rmsnorm_grad_desc) == 144 == len(abi.RMSNORM_GRAD_DESC_PACK(*[0] * 20))
     assert C.sizeof(abi.gtp_muon_hparams) == 56 == len(abi.MUON_HPARAMS_PACK(*[0] * 13))
 
 
-LOOKUP = dict(ids=at(0), ids64=1, tokens=10, table=at(1), table_dt=BF16, table_ld=64, first_row=0, rows=100, cols=64,
-              scale=1.0, out=at(2), out_dt=BF16, out_ld=64)
+def lookup(**change):
+    d = dict(ids=at(0), table=at(1), out=at(2), tokens=10, first_row=0, rows=100, cols=64, table_ld=64, out_ld=64, scale=1.0,
+             ids64=1, table_dtype=BF16, out_dtype=BF16, reserved=0)
+    assert set(change) <= set(d)
+    return abi.load().gtp_embedding(C.byref(abi.gtp_embedding_desc(**{**d, **change})), None)
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(table_dt=U8), DTYPE), (dict(out_dt=abi.GTP_F16), DTYPE), (dict(ids64=2), ARG), (dict(tokens=-1), ARG),
+    (dict(reserved=1), ARG), (dict(table_dtype=U8), DTYPE), (dict(out_dtype=abi.GTP_F16), DTYPE), (dict(ids64=2), ARG), (dict(tokens=-1), ARG),
     (dict(rows=-1), ARG), (dict(cols=-1), ARG), (dict(first_row=-1), ARG), (dict(tokens=(1 << 30) + 1), SHAPE),
     (dict(rows=1 << 30, cols=1 << 11, table_ld=1 << 11, out_ld=1 << 11), SHAPE), (dict(table_ld=63), ARG), (dict(out_ld=63), ARG),
     (dict(table_ld=1 << 45), SHAPE), (dict(ids=None), ARG), (dict(table=None), ARG), (dict(out=None), ARG),
@@ -36,22 +41,25 @@ LOOKUP = dict(ids=at(0), ids64=1, tokens=10, table=at(1), table_dt=BF16, table_l
     (dict(out=at(2) + 1), ALIGN), (dict(out=at(1) + 128), ARG), (dict(out=at(0) + 16), ARG),
     (dict(tokens=0, ids=None, out=None), OK), (dict(cols=0), OK)])
 def test_embedding(change, status):
-    assert abi.load().gtp_embedding(*{**LOOKUP, **change}.values(), None) == status
+    assert lookup(**change) == status, abi.load().gtp_last_error()
 
 
-GRAD = dict(ids=at(0), ids64=1, tokens=10, dout=at(1), dout_dt=BF16, dout_ld=64, first_row=0, rows=100, cols=64, scale=1.0,
-            grad=at(2), grad_dt=F32, offset=64, total=6464, workspace=at(3), bytes=1 << 20)
+def lookup_grad(workspace=at(3), bytes=1 << 20, **change):
+    d = dict(ids=at(0), dout=at(1), grad_data=at(2), tokens=10, first_row=0, rows=100, cols=64, dout_ld=64, grad_offset=64,
+             grad_numel_total=6464, scale=1.0, ids64=1, dout_dtype=BF16, grad_dtype=F32, reserved=0)
+    assert set(change) <= set(d)
+    return abi.load().gtp_embedding_grad_accum(C.byref(abi.gtp_embedding_grad_desc(**{**d, **change})), workspace, bytes, None)
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dout_dt=U8), DTYPE), (dict(grad_dt=U8), DTYPE), (dict(ids64=-1), ARG), (dict(rows=-1), ARG),
-    (dict(first_row=-5), ARG), (dict(dout_ld=3), ARG), (dict(offset=65), RANGE), (dict(offset=-1), RANGE), (dict(total=-1), RANGE),
-    (dict(total=1 << 62, offset=1 << 61), RANGE), (dict(workspace=None), ARG), (dict(grad=None), ARG), (dict(ids=None), ARG),
-    (dict(dout=None), ARG), (dict(workspace=at(3) + 8), ALIGN), (dict(grad=at(2) + 2), ALIGN), (dict(dout=at(1) + 1), ALIGN),
-    (dict(bytes=100), CAPACITY), (dict(grad=at(1)), ARG), (dict(workspace=at(2) + 1024), ARG), (dict(workspace=at(0)), ARG),
+    (dict(reserved=-1), ARG), (dict(dout_dtype=U8), DTYPE), (dict(grad_dtype=U8), DTYPE), (dict(ids64=-1), ARG), (dict(rows=-1), ARG),
+    (dict(first_row=-5), ARG), (dict(dout_ld=3), ARG), (dict(grad_offset=65), RANGE), (dict(grad_offset=-1), RANGE), (dict(grad_numel_total=-1), RANGE),
+    (dict(grad_numel_total=1 << 62, grad_offset=1 << 61), RANGE), (dict(workspace=None), ARG), (dict(grad_data=None), ARG), (dict(ids=None), ARG),
+    (dict(dout=None), ARG), (dict(workspace=at(3) + 8), ALIGN), (dict(grad_data=at(2) + 2), ALIGN), (dict(dout=at(1) + 1), ALIGN),
+    (dict(bytes=100), CAPACITY), (dict(grad_data=at(1)), ARG), (dict(workspace=at(2) + 1024), ARG), (dict(workspace=at(0)), ARG),
     (dict(workspace=at(1) + 32), ARG), (dict(workspace=at(3) + 16), ALIGN), (dict(tokens=0), OK), (dict(rows=0), OK)])
 def test_embedding_gradient(change, status):
-    assert abi.load().gtp_embedding_grad_accum(*{**GRAD, **change}.values(), None) == status
+    assert lookup_grad(**change) == status, abi.load().gtp_last_error()
 
 
 def test_workspace_sizes():
@@ -92,7 +100,8 @@ def test_norm(change, status):
     assert norm(**change) == status, abi.load().gtp_last_error()
 
 
-def test_norm_null_descriptors():
+def test_null_descriptors():
+    assert abi.load().gtp_embedding(None, None) == ARG and abi.load().gtp_embedding_grad_accum(None, at(1), 1 << 20, None) == ARG
     assert abi.load().gtp_rmsnorm(None, None) == ARG and abi.load().gtp_rmsnorm_grad(None, at(1), 1 << 20, None) == ARG
 
 
