@@ -145,8 +145,8 @@ struct SortArgs {
   int32_t tokens, wide;
   int32_t *key, *token;  // the result
   int32_t *key2, *token2;
-  int32_t *counts;  // radix: [256][tiles]
-  int32_t tiles;
+  int32_t *counts;  // radix: [256][tiles], or without scan [tiles][256]
+  int32_t tiles, scan;
   int32_t *counters;  // of the sums, cleared here
   int64_t counter_count;
 };
@@ -159,8 +159,9 @@ __device__ __forceinline__ void clear_counters(const SortArgs &a) {
 // Few tokens: the place of a token is the number of tokens that sort before it, counted outright.  A block owns
 // kOwn tokens, keeps every token of the shard as one 32-bit number row * tokens + t in shared memory (any order: the
 // numbers differ), and its warps count, 32 owned tokens a warp, each over a part of the list.  tokens^2 comparisons
-// but one launch and no exchange between blocks.
-constexpr int kOwn = 64, kRankThreads = 512, kRankMost = 16384;
+// but one launch and no exchange between blocks: the whole gradient of [2048, 256] takes 12.4 us, 15.7 with the radix
+// sort; at 4096 tokens 21.1 and 18.2.
+constexpr int kOwn = 64, kRankThreads = 512, kRankMost = 2560;
 
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ __align__(16) uint32_t list[];  // tokens rounded up to 4, padded with the largest number
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constan
 // Many tokens: a radix sort from the low digit up, eight bits a pass, each pass three launches: digits counted by tiles
 // of 4096 tokens, the counts summed up in (digit, tile) order, and each tile's tokens written to their places in
 // order.  The first pass reads the ids themselves.
-constexpr int kTile = 4096, kTileThreads = 256, kRounds = kTile / kTileThreads;
+constexpr int kTileThreads = 256;
 
 __device__ __forceinline__ void radix_load(const SortArgs &a, const int32_t *key, const int32_t *token, int64_t p,
                                            int32_t &k, int32_t &t) {
@@ -251,6 +252,7 @@ __device__ __forceinline__ void radix_load(const SortArgs &a, const int32_t *key
   }
 }
 
+template <int ROUNDS>
 __global__ void __launch_bounds__(kTileThreads)
     radix_count_kernel(const __grid_constant__ SortArgs a, const int32_t *key, int shift) {
   __shared__ int32_t count[256];
@@ -259,15 +261,16 @@ __global__ void __launch_bounds__(kTileThreads)
   gtp::ptx::wait_prior_grid();
   if (shift == 0) clear_counters(a);
   __syncthreads();
-  for (int i = 0; i < kRounds; ++i) {
-    const int64_t p = int64_t(blockIdx.x) * kTile + i * kTileThreads + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int64_t p = (int64_t(blockIdx.x) * ROUNDS + i) * kTileThreads + threadIdx.x;
     if (p < a.tokens) {
       const int32_t k = key ? key[p] : int32_t(row_of(a.ids, a.wide, p, a.first_row, a.rows));
       atomicAdd(&count[(k >> shift) & 255], 1);
     }
   }
   __syncthreads();
-  a.counts[int64_t(threadIdx.x) * a.tiles + blockIdx.x] = count[threadIdx.x];
+  a.counts[a.scan ? int64_t(threadIdx.x) * a.tiles + blockIdx.x : blockIdx.x * 256 + threadIdx.x] = count[threadIdx.x];
 }
 
 // counts -> what stands before each, in place, by one block.
@@ -317,20 +320,49 @@ __global__ void __launch_bounds__(kScanThreads) radix_scan_kernel(const __grid_c
   }
 }
 
+// Up to kFewTiles each block adds up the counts itself (not SCANNED): a launch less.
+constexpr int kFewTiles = 64;
+
+// Thread d: the tokens that stand before the tile's first one of digit d.  sums: 8 words.
+__device__ __forceinline__ int32_t before_digit(const SortArgs &a, int32_t *sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t total = 0, mine = 0;
+  for (int i0 = 0; i0 < a.tiles; i0 += 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int32_t c = i0 + i < a.tiles ? a.counts[(i0 + i) * 256 + threadIdx.x] : 0;
+      total += c;
+      mine += i0 + i < int(blockIdx.x) ? c : 0;
+    }
+  }
+  int32_t run = total;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int32_t o = __shfl_up_sync(0xFFFFFFFFu, run, d);
+    if (lane >= d) run += o;
+  }
+  if (lane == 31) sums[warp] = run;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) run += sums[w];
+  return run - total + mine;
+}
+
+template <int ROUNDS, bool SCANNED>
 __global__ void __launch_bounds__(kTileThreads)
     radix_scatter_kernel(const __grid_constant__ SortArgs a, const int32_t *key, const int32_t *token, int32_t *key_out,
                          int32_t *token_out, int shift) {
   __shared__ int32_t at[kTileThreads / 32][256];  // a warp's next place of each digit
+  __shared__ int32_t sums[kTileThreads / 32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int w = 0; w < kTileThreads / 32; ++w) at[w][threadIdx.x] = 0;
   __syncthreads();
-  // a warp takes kTile / 8 tokens in a row, 32 at a time
-  const int64_t p0 = int64_t(blockIdx.x) * kTile + warp * (kTile / (kTileThreads / 32)) + lane;
-  int32_t k[kRounds], t[kRounds];
+  // a warp takes an eighth of the tile's tokens in a row, 32 at a time
+  const int64_t p0 = (int64_t(blockIdx.x) * kTileThreads + warp * 32) * ROUNDS + lane;
+  int32_t k[ROUNDS], t[ROUNDS];
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
+  for (int i = 0; i < ROUNDS; ++i) {
     const int64_t p = p0 + 32 * i;
     k[i] = t[i] = 0;
     if (p < a.tokens) {
@@ -340,7 +372,7 @@ __global__ void __launch_bounds__(kTileThreads)
   }
   __syncthreads();
   {  // thread d: digit d's place for each warp in turn
-    int32_t before = a.counts[int64_t(threadIdx.x) * a.tiles + blockIdx.x];
+    int32_t before = SCANNED ? a.counts[int64_t(threadIdx.x) * a.tiles + blockIdx.x] : before_digit(a, sums);
     for (int w = 0; w < kTileThreads / 32; ++w) {
       const int32_t c = at[w][threadIdx.x];
       at[w][threadIdx.x] = before;
@@ -349,7 +381,7 @@ __global__ void __launch_bounds__(kTileThreads)
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
+  for (int i = 0; i < ROUNDS; ++i) {
     const bool live = p0 + 32 * i < a.tokens;
     const int d = live ? (k[i] >> shift) & 255 : 256 + lane;  // no one's digit
     const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
@@ -647,13 +679,18 @@ struct GradPlan {
   int64_t key, token, key2, token2, counts, counters, part, bytes;  // places in the workspace
 };
 
+// Tokens a thread of a sort tile: few where that keeps the tiles in kFewTiles (16384 tokens: 27 us with 2, 34 with 8), else
+// more, so that their counts stay few (65536: 72 us with 2, 58 with 4).
+int rounds_of(int64_t tokens) { return tokens <= 2 * kTileThreads * kFewTiles ? 2 : 8; }
+
 GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
   GradPlan p = {};
   p.radix = tokens > kRankMost || rows * tokens >= (int64_t(1) << 32) - 1;
   // tiles: short ones spread few tokens over the machine; from 4096 of them on longer ones keep the parts few
   p.tile = int32_t(std::max<int64_t>(8, (tokens + 4095) / 4096));
   p.tiles = int32_t((tokens + p.tile - 1) / p.tile);
-  p.sort_tiles = int32_t((tokens + kTile - 1) / kTile);
+  const int64_t each = kTileThreads * rounds_of(tokens);
+  p.sort_tiles = int32_t((tokens + each - 1) / each);
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -678,25 +715,23 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
 gtp_status sort_tokens(SortArgs &a, const GradPlan &plan, cudaStream_t st) {
   if (!plan.radix) {
     const size_t smem = size_t((a.tokens + 3) & ~3) * 4;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankMost * 4);
-      if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    }
     return gtp::launch_overlapped(rank_kernel, unsigned((a.tokens + kOwn - 1) / kOwn), kRankThreads, smem, st, "embedding_grad",
                                   a);
   }
   int bits = 1;  // of the keys 0 .. rows
   while (bits < 31 && (int64_t(1) << bits) <= a.rows) ++bits;
   const int passes = (bits + 7) / 8;
+  a.scan = a.tiles > kFewTiles;
+  const bool wide = rounds_of(a.tokens) == 8;
   const int32_t *key = nullptr, *token = nullptr;
   for (int i = 0; i < passes; ++i) {  // the last pass writes the result
     const bool into_first = (passes - 1 - i) % 2 == 0;
     int32_t *key_out = into_first ? a.key : a.key2, *token_out = into_first ? a.token : a.token2;
-    gtp_status s = gtp::launch_overlapped(radix_count_kernel, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key,
+    gtp_status s = gtp::launch_overlapped(wide ? radix_count_kernel<8> : radix_count_kernel<2>, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key,
                                           8 * i);
-    if (!s) s = gtp::launch_overlapped(radix_scan_kernel, 1, kScanThreads, 0, st, "embedding_grad", a);
+    if (!s && a.scan) s = gtp::launch_overlapped(radix_scan_kernel, 1, kScanThreads, 0, st, "embedding_grad", a);
     if (!s)
-      s = gtp::launch_overlapped(radix_scatter_kernel, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key, token,
+      s = gtp::launch_overlapped(a.scan ? radix_scatter_kernel<8, true> : wide ? radix_scatter_kernel<8, false> : radix_scatter_kernel<2, false>, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key, token,
                                  key_out, token_out, 8 * i);
     if (s) return s;
     key = key_out, token = token_out;

@@ -98,7 +98,7 @@ __device__ __forceinline__ void store_row_view(const NormArgs &a, int64_t row, i
 // Sums of N rows at a time over the blockDim.x threads of a row (whole warps; blockDim.y rows a block side by side where
 // one warp is a row's).  part: two arrays in turn, so that one barrier each time does.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][kRowThreads / 32], int flip) {
+__device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][32], int flip) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = warp_sum(s[i]);
@@ -116,7 +116,7 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][kRow
 // share a barrier.
 template <typename TX, typename TS, bool RES, int V, int N>
 __global__ void __launch_bounds__(kRowThreads) norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][N][kRowThreads / 32];
+  __shared__ float part[2][N][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int tx = blockDim.x;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(const __grid_constant
 // row's alignment.  One row a block of TX threads, K elements a thread, or (TX 32) eight rows.
 template <typename T, typename TS, bool RES, int TX, int K>
 __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_elements_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][1][kRowThreads / 32];
+  __shared__ float part[2][1][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int cols = int(a.cols), t = threadIdx.x;
@@ -475,8 +475,8 @@ gtp_status launch_rows(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream
   const dim3 block(s.tx, s.ty);
   const int64_t blocks = (a.rows + s.ty - 1) / s.ty, most = int64_t(dev.sm_count) * std::max(1, 2048 / (s.tx * s.ty));
   // rows a time: as many bytes in flight a thread as 64 registers leave; few rows: one, spread over the machine
-  constexpr int MANY = sizeof(TX) + (RES ? sizeof(TS) : 0) > 4 ? 2 : 4;
-  if (s.V == 1 && blocks > most)
+  constexpr int MANY = sizeof(TX) + (RES ? sizeof(TS) : 0) > 4 ? 1 : 4;
+  if (MANY > 1 && s.V == 1 && blocks > most)
     return gtp::launch_overlapped(norm_kernel<TX, TS, RES, 1, MANY>, unsigned((blocks + MANY - 1) / MANY), block, 0, st, "rmsnorm", a);
   return gtp::launch_overlapped(s.V == 1 ? norm_kernel<TX, TS, RES, 1, 1> : norm_kernel<TX, TS, RES, 4, 1>,
                                 unsigned(std::min(blocks, most)), block, 0, st, "rmsnorm", a);
@@ -494,7 +494,9 @@ template <typename TX, typename TS, bool RES>
 gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   if (a.cols <= 32 * 8) return launch_elements_of<TX, TS, RES, 32, 8>(a, dev, st);
   if (a.cols <= 256 * 8) return launch_elements_of<TX, TS, RES, 256, 8>(a, dev, st);
-  return launch_elements_of<TX, TS, RES, kRowThreads, 32>(a, dev, st);
+  if (a.cols <= 512 * 8) return launch_elements_of<TX, TS, RES, 512, 8>(a, dev, st);
+  if (a.cols <= 1024 * 8) return launch_elements_of<TX, TS, RES, 1024, 8>(a, dev, st);
+  return launch_elements_of<TX, TS, RES, 1024, 16>(a, dev, st);
 }
 
 template <typename TX, typename TS, bool RES, int VPL, bool STATS>

@@ -42,7 +42,7 @@ using gtp::warp_sum;
 
 // Sums of N rows at a time over a row's threads, as the forward's.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][kRowThreads / 32], int flip) {
+__device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][32], int flip) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = warp_sum(s[i]);
@@ -61,7 +61,7 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (&part)[2][N][kRow
 // memory, and share a barrier; what is between the loads and the outputs is computed twice rather than kept.
 template <typename TD, typename TS, int V, int N>
 __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-  __shared__ float part[2][N][kRowThreads / 32];
+  __shared__ float part[2][N][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int tx = blockDim.x;
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const __grid_con
 
 // Rows that start anywhere: the elements TX apart are a thread's (as the forward's).
 template <typename TD, typename TS, int TX, int K>
-__global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_grad_elements_kernel(const __grid_constant__ GradArgs a) {
-  __shared__ float part[2][1][kRowThreads / 32];
+__global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 4 : 1024 / TX) norm_grad_elements_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float part[2][1][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int cols = int(a.cols), t = threadIdx.x;
@@ -239,9 +239,9 @@ GradShape grad_shape(int64_t rows, int64_t cols, int sms) {
 
 // The same for rows that start anywhere.
 GradShape elements_shape(int64_t rows, int64_t cols, int sms) {
-  const int tx = cols <= 32 * 8 ? 32 : cols <= 256 * 8 ? 256 : kRowThreads, ty = tx == 32 ? 8 : 1;
+  const int tx = cols <= 32 * 8 ? 32 : cols <= 256 * 8 ? 256 : cols <= 512 * 8 ? 512 : 1024, ty = tx == 32 ? 8 : 1;
   const int64_t most = int64_t(sms) * (1024 / (tx * ty));
-  return {tx, ty, cols <= 256 * 8 ? 1 : 4, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
+  return {tx, ty, cols <= 1024 * 8 ? 1 : 2, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
 }
 
 constexpr int kMostSms = 160;  // the workspace's size is asked for without a device: at least an sm_103 GPU's SMs
@@ -253,7 +253,9 @@ gtp_status launch_grad(const GradArgs &a, bool vec, const GradShape &s, cudaStre
   if (vec) kernel = s.V == 1 ? norm_grad_kernel<TD, TS, 1, N> : norm_grad_kernel<TD, TS, 4, 1>;
   else
     kernel = s.tx == 32 ? norm_grad_elements_kernel<TD, TS, 32, 8>
-             : s.tx == 256 ? norm_grad_elements_kernel<TD, TS, 256, 8> : norm_grad_elements_kernel<TD, TS, kRowThreads, 32>;
+             : s.tx == 256 ? norm_grad_elements_kernel<TD, TS, 256, 8>
+             : s.tx == 512 ? norm_grad_elements_kernel<TD, TS, 512, 8>
+             : s.V == 1    ? norm_grad_elements_kernel<TD, TS, 1024, 8> : norm_grad_elements_kernel<TD, TS, 1024, 16>;
   return gtp::launch_overlapped(kernel, unsigned(s.grid), dim3(s.tx, s.ty), 0, st, "rmsnorm_grad", a);
 }
 

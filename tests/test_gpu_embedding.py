@@ -97,9 +97,11 @@ def test_gradient(T, rows, C, first, offset, dd, gd):
         assert torch.equal(grad[:offset], before[:offset]) and torch.equal(grad[end:], before[end:])
 
 
-@pytest.mark.parametrize("T,rows", [(16384, 500), (16385, 500), (40000, 70000), (9000, 500000)])
+@pytest.mark.parametrize("T,rows", [(16384, 500), (16385, 500), (40000, 70000), (9000, 500000), (10241, 700), (12200, 20),
+                                    (12288, 500), (12289, 500), (2560, 900), (2561, 900),
+                                    (32768, 300), (32769, 300), (131072, 300), (131073, 70000), (70000, 17000000)])
 def test_gradient_both_ways_of_sorting(T, rows):
-    """Around the border between counting and the radix sort, and keys of one to three digits."""
+    """Around the borders between counting and the radix sort, and keys of one to four digits."""
     C = 8
     g = torch.Generator().manual_seed(T)
     ids = torch.randint(-10, rows + 10, (T,), generator=g)
