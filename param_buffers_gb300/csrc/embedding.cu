@@ -544,7 +544,7 @@ __device__ __forceinline__ void join_row(const SumArgs &a, int tile, int first, 
 
 // A tile a thread row (whole warps, so that a warp's lanes read the keys of 32 places at once and hand them round), eight
 // columns a thread, kFlight tokens' rows in flight.
-constexpr int kFlight = 8;
+constexpr int kFlight = 4;
 
 template <typename TD, typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ SumArgs a) {
