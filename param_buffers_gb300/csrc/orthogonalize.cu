@@ -50,8 +50,7 @@ using namespace gtp::ptx;
 __device__ unsigned int g_ortho_wait_timeouts;  // this unit's part of gtp_wait_timeouts' word
 
 constexpr int kMostMatrices = 64, kMostSteps = 16;
-constexpr int kCounters = kMostMatrices * kMostSteps;  // of a launch's CTAs: one a phase, or one a matrix and iteration
-static_assert(3 * kMostSteps <= kCounters, "");
+constexpr int kCounters = 3 * kMostSteps * kMostMatrices;  // of a launch: one a product and matrix
 
 // --------------------------------------------------------------------------- the norm, the momentum, the first X
 
@@ -232,8 +231,10 @@ __global__ void __launch_bounds__(kPassThreads)
 // --------------------------------------------------------------------------- the products
 
 // All products of a call in one cooperative launch of CTA pairs.  A phase is one product of one iteration over all
-// matrices; its pair tiles go round the pairs, and a phase starts on a CTA when every CTA that had a tile of the one
-// before has counted itself off (arrived[phase], one word each, cleared by first_x_kernel).
+// matrices; its pair tiles go round the pairs, on from where the phase before ended.  A matrix's product waits for that
+// matrix's product before alone: every CTA counts off each tile it has finished (arrived[phase][matrix], cleared by
+// first_x_kernel), so that with several matrices the pairs go from phase to phase without a pause.  No wait can close
+// a circle: a pair takes its tiles in the order of phases, and waits only for earlier phases.
 //
 // Inside a CTA: warp 0 and warp 2 copy A and B tiles to a ring of shared-memory stages, warp 1 of the even CTA issues the
 // M = 256 MMAs of the pair into one of two accumulators, warp 3 waits for phases, warps 4-11 finish the tiles: 32 x 32
@@ -267,7 +268,7 @@ static_assert(sizeof(Maps) == 14 * sizeof(CUtensorMap), "prefetched one by one")
 
 struct Args {
   Phase phase[3];
-  int steps, m, step;  // step: the last product moves the master instead of writing dst
+  int count, steps, m, step;  // step: the last product moves the master instead of writing dst
   unsigned int *arrived;
   float *diag, *e;       // [count][m]
   // powers of two: what makes the accumulators, A', B' and X true values and the reverse
@@ -339,10 +340,27 @@ __device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
 __device__ __forceinline__ void add_release(unsigned int *p) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {  // without a pause
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all_but_one() { asm volatile("cp.async.bulk.wait_group 1;" ::: "memory"); }
 
-// Waits until this CTA may start `phase` (warp 3 says so); false when the CTA gives up.
+// The pair's first unit of the phase that follows one of `units`.
+__device__ __forceinline__ int next_first(int first, int units, int step) {
+  first -= units % step;
+  return first < 0 ? first + step : first;
+}
+
+// Waits until warp 3 has said that this CTA may start `phase` (of newton_schulz_kernel: phase * count + matrix); false
+// when the CTA gives up.
 __device__ __forceinline__ bool wait_ready(volatile int *ready, int phase, volatile int *abort_flag, unsigned int *err) {
   if (*ready < phase) {
     const uint64_t t0 = globaltimer_ns();
@@ -615,12 +633,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cfull + SLOTS * kEpilogueWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *ready = abort_flag + 1;
-  int *finished = const_cast<int *>(ready + 1);  // warps that have finished their part of a phase, over all phases
-  static_assert((2 * STAGES + 5 + SLOTS * kEpilogueWarps) * 8 + 16 <= SMEM_CTRL, "control block");
+  int *finished = const_cast<int *>(ready + 1);  // [4], by units in turn: the warps that have finished their part of one
+  static_assert((2 * STAGES + 5 + SLOTS * kEpilogueWarps) * 8 + 28 <= SMEM_CTRL, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int first = int(blockIdx.x >> 1), step = int(gridDim.x >> 1), phases = 3 * a.steps;
+  const int pair = int(blockIdx.x >> 1), step = int(gridDim.x >> 1), phases = 3 * a.steps;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -634,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < SLOTS * kEpilogueWarps; ++i) mbar_init(&cfull[i], 1);
     *abort_flag = 0;
     *ready = 0;
-    *finished = 0;
+    for (int i = 0; i < 4; ++i) finished[i] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < 14) tma_prefetch_desc(reinterpret_cast<const CUtensorMap *>(&maps) + lane);
@@ -659,7 +677,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t parity = 0, armed = 0, armed_parity = 0;  // bit s: stage s has been armed, and for which phase
       const uint32_t bars = mapa_shared(full, 0);
       bool ok = true;
-      for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+      for (int ph = 0, kind = 0, first = pair; ok && ph < phases;
+           ++ph, first = next_first(first, a.phase[kind].units, step), kind = kind == 2 ? 0 : kind + 1) {
         const Phase &p = a.phase[kind];
         if (first >= p.units) continue;
         const int xi = (ph / 3) & 1;
@@ -668,7 +687,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const CUtensorMap *map = of_x ? &maps.x[xi] : kind == kPoly ? &maps.gram : &maps.poly;
         const CUtensorMap *tall_map = of_x ? &maps.x_tall[xi] : kind == kPoly ? &maps.gram_tall : &maps.poly_tall;
         const int rows = is_a ? p.a_rows : p.b_rows;
-        bool waited = false;
         for (int u = first; ok && u < p.units; u += step) {
           int k, row, col;
           bool half;
@@ -678,8 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int i0 = is_a ? row + BMC * int(rank) : col + (half ? 64 : 128) * int(rank), r0 = k * rows;
           const uint32_t bytes = half ? 2u * (A_STAGE + BOX) : 2u * STAGE;
           const CUtensorMap *const use = whole && !mn ? tall_map : map;
-          if (!waited && !(ok = wait_ready(ready, ph, abort_flag, err))) break;
-          waited = true;
+          if (ph > 0 && !(ok = wait_ready(ready, ph * a.count + k, abort_flag, err))) break;
           int cx = mn ? i0 : 0, cy = mn ? r0 : r0 + i0;
           const int dx = mn ? 0 : BK, dy = mn ? BK : 0;
           uint8_t *const base = is_a ? sA : sB;
@@ -712,7 +729,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t parity = 0, acc_parity = 0;
       bool ok = true;
-      for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+      for (int ph = 0, kind = 0, first = pair; ok && ph < phases;
+           ++ph, first = next_first(first, a.phase[kind].units, step), kind = kind == 2 ? 0 : kind + 1) {
         const Phase &p = a.phase[kind];
         const bool a_mn = kind == kGram && TALL, b_mn = a_mn || (kind == kUpdate && !TALL);
         for (int u = first; ok && u < p.units; u += step) {
@@ -765,27 +783,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) drain(drained, 0);
   } else if (warp == 3) {
     if (lane == 0) {  // ---------------------------------------------------- the phases' order
-      for (int ph = 1; ph < phases; ++ph) {
-        if (first >= a.phase[ph % 3].units) continue;
-        const unsigned int all = 2u * unsigned(min(a.phase[(ph - 1) % 3].units, step));
-        const uint64_t t0 = globaltimer_ns();
-        bool ok = true;
-        while (load_acquire(&a.arrived[ph - 1]) < all) {
-          if (*abort_flag) ok = false;
-          if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, 0x200u);
-            ok = false;
+      bool ok = true;
+      for (int ph = 0, kind = 0, first = pair; ok && ph < phases;
+           ++ph, first = next_first(first, a.phase[kind].units, step), kind = kind == 2 ? 0 : kind + 1) {
+        if (ph == 0) continue;
+        const Phase &p = a.phase[kind], &before = a.phase[kind == 0 ? 2 : kind - 1];
+        int said = -1;
+        for (int u = first; ok && u < p.units; u += step) {
+          int k, row, col;
+          bool half;
+          if (!decode<TALL>(p, kind, u, k, row, col, half) || k == said) continue;
+          // units of the matrix in the phase before, counted off by both CTAs
+          const int whole = min(max(before.full - k * before.each, 0), before.each);
+          const unsigned int all = 2u * unsigned(2 * before.each - whole);
+          const uint64_t t0 = globaltimer_ns();
+          while (load_acquire(&a.arrived[(ph - 1) * a.count + k]) < all) {
+            if (*abort_flag) ok = false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+              atomicOr(err, 0x200u);
+              ok = false;
+            }
+            if (!ok) break;
           }
-          if (!ok) break;
+          if (!ok) {
+            *abort_flag = 1;
+            break;
+          }
+          // what the other CTAs' copies wrote, before this CTA's copies read it
+          fence_proxy_async_global();
+          __threadfence_block();
+          *ready = ph * a.count + k;
+          said = k;
         }
-        if (!ok) {
-          *abort_flag = 1;
-          break;
-        }
-        // what the other CTAs' copies wrote, before this CTA's copies read it
-        fence_proxy_async_global();
-        __threadfence_block();
-        *ready = ph;
       }
     }
   } else {  // -------------------------------------------------------------- finishing the tiles (both CTAs)
@@ -798,16 +827,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t acc_parity = 0, cparity = 0;  // bit s: the parity that slot s's next copy completes
     int flying = 0;                        // bit s: a copy into slot s that nobody has waited for
     bool ok = true;
-    for (int ph = 0, kind = 0; ok && ph < phases; ++ph, kind = kind == 2 ? 0 : kind + 1) {
+    // The counter of a unit whose chunks have left and may not have arrived: this warp is done with it when they have, d
+    // and e having been written by its lanes before the warp's barrier.  The last of the warps counts the unit off and
+    // releases what it and, through `finished`, the others have written.  No warp gets to a unit four further on before
+    // all have: a unit's accumulator is the one of two before.
+    unsigned int *owed = nullptr;
+    int done = 0;
+    const auto settle = [&](bool all) {  // else all but the chunk sent last, which is another unit's
+      if (!owed) return;
+      if (lane == 0) {
+        if (all) bulk_wait_all();
+        else bulk_wait_all_but_one();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence_block();
+        if ((atomicAdd(&finished[done & 3], 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
+          __threadfence_block();
+          add_release(owed);
+        }
+      }
+      ++done;
+      owed = nullptr;
+    };
+    for (int ph = 0, kind = 0, first = pair; ok && ph < phases;
+           ++ph, first = next_first(first, a.phase[kind].units, step), kind = kind == 2 ? 0 : kind + 1) {
       const Phase &p = a.phase[kind];
       if (first >= p.units) continue;
       const bool last = ph + 1 == phases, early = ph < 6;
-      {
-        bool r = true;
-        if (lane == 0) r = wait_ready(ready, ph, abort_flag, err);
-        ok = __all_sync(0xFFFFFFFFu, r);
-        if (!ok) break;
-      }
+      unsigned int *const counters = a.arrived + ph * a.count;
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
       // Old values are fetched in the order in which chunks are worked on: the next chunk's before this one's new values
@@ -824,6 +872,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fwide = half ? BN / 4 : BN / 2;
             frow = row + BMC * int(rank) + 32 * quarter, fcol = col + side * fwide;
             funit = true;
+            bool r = true;
+            if (lane == 0) r = wait_ready(ready, ph * a.count + fk, abort_flag, err);
+            ok = __all_sync(0xFFFFFFFFu, r);
+            if (!ok) {
+              fu = p.units;
+              return;
+            }
           }
           if (fc < fwide && exists(frow, fcol + fc)) break;
         }
@@ -845,7 +900,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int u = first; ok && u < p.units; u += step) {
         int k, row, col;
         bool half;
-        if (!decode<TALL>(p, kind, u, k, row, col, half)) continue;
+        if (!decode<TALL>(p, kind, u, k, row, col, half)) {
+          if (ew == 0 && lane == 0 && !last) add_release(counters + k);
+          continue;
+        }
         const int wide = half ? BN / 4 : BN / 2;  // this warp's columns
         const int row0 = row + BMC * int(rank) + 32 * quarter, c0 = col + side * wide, me = row0 + lane;
         // d or e of this lane's row and of the columns
@@ -859,6 +917,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (c0 + 32 * i + lane < a.m) t[i] = __ldcg(d + c0 + 32 * i + lane);
           }
         }
+        // with time to spare the unit before is counted off here, else behind the first chunk
+        if (owed && !__all_sync(0xFFFFFFFFu, mbar_test(&tfull[acc], acc_parity))) settle(true);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_parity, abort_flag, err, 0x8u))) {
           ok = false;
           break;
@@ -965,12 +1025,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               bulk_commit_group();
             }
           }
+          if (c == 0) settle(false);
           if (kind != kGram) {
             slot ^= 1;
             --ahead;
           }
         }
         if (!ok) break;
+        settle(true);  // where this warp had no chunk
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[acc], 0));
@@ -978,19 +1040,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           acc = 0;
           acc_parity ^= 1u;
         }
+        if (!last) owed = counters + k;
       }
       if (!ok || last) break;
-      // This warp's part of the phase is in memory: its copies out have been written, d and e by its lanes before the
-      // warp's barrier.  The last of the warps releases what it and, through `finished`, the others have written.
-      if (lane == 0) bulk_wait_all();
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence_block();
-        if ((atomicAdd(finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
-          __threadfence_block();
-          add_release(&a.arrived[ph]);
-        }
-      }
+      settle(true);
     }
     if (!ok) *abort_flag = 1;
     if (lane == 0) {
@@ -1558,7 +1611,9 @@ gtp_status launch_together(void (*kernel)(KArgs...), int ctas, int smem, cudaStr
 }
 
 // Tiles of 256 x 256 in whole waves of the pairs, the rest as halves where those fit one wave or less time: a half-wide
-// unit takes 0.55 of a whole one's time.
+// unit takes 0.55 of a whole one's time (a call of 1536 x 2048 227 us; whole tiles alone 279, halves alone 231; 8192 x 2048
+// 538, 630, 593; 777 x 1111 167, 231, 165).  Where the other matrices' tiles fill a wave and a half, their phases go into
+// one another and whole tiles alone are better (eight of 1536 x 2048 668 us, with halves 679).
 void shape(Phase &p, int64_t count, bool symmetric, int64_t k, int pairs) {
   p.tiles_m = (p.m_dim + BMP - 1) / BMP, p.tiles_n = (p.n_dim + BN - 1) / BN;
   p.each = symmetric ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
@@ -1567,7 +1622,8 @@ void shape(Phase &p, int64_t count, bool symmetric, int64_t k, int pairs) {
   const auto waves = [&](int units) { return (units + pairs - 1) / pairs; };
   const int whole = tiles / pairs * pairs;
   const double all = waves(tiles), tail = whole / pairs + 0.55 * waves(2 * (tiles - whole)), none = 0.55 * waves(2 * tiles);
-  p.full = all <= tail && all <= none ? tiles : tail <= none ? whole : 0;
+  const bool flows = 2 * (count - 1) * p.each >= 3 * pairs;
+  p.full = flows || (all <= tail && all <= none) ? tiles : tail <= none ? whole : 0;
   p.units = p.full + 2 * (tiles - p.full);
 }
 
@@ -1600,6 +1656,7 @@ gtp_status iterate(Args a, const Plan &plan, char *ws, int64_t count, int64_t ro
                    cudaStream_t st) {
   static std::atomic<int> known[64];
   int pairs = 0;
+  a.count = int(count);
   if (gtp_status e = clusters_of(newton_schulz_kernel<TALL>, 2, SMEM_TOTAL, known, dev, &pairs)) return e;
   for (int kind = 0; kind < 3; ++kind) {
     Phase &p = a.phase[kind];

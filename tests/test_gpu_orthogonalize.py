@@ -64,7 +64,8 @@ def test_shapes(R, C, steps):
     assert gtp.gtp_wait_timeouts() == 0
 
 
-@pytest.mark.parametrize("count,R,C", [(3, 100, 200), (5, 200, 100), (2, 513, 512), (64, 8, 24)])
+@pytest.mark.parametrize("count,R,C", [(3, 100, 200), (5, 200, 100), (2, 513, 512), (64, 8, 24), (3, 700, 600), (7, 300, 520), (9, 264, 264),
+                                       (2, 1500, 1040)])
 def test_stacks(count, R, C):
     src = torch.stack([gradient(R, C, seed=k) * 10.0 ** k if k < 8 else gradient(R, C, seed=k) for k in range(count)])
     src[1] = 0
