@@ -244,16 +244,20 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX) norm_elements_kernel(cons
 
 // --------------------------------------------------------------------------- forward with the columnwise view
 
-// A block holds 32 rows of 256 VPL columns: its eight warps four rows each, a lane VPL vectors of eight columns of every
-// row.  The blocks of a cluster share the rows and trade their sums of squares through shared memory.  A column's 32
-// rows are one block of the columnwise view: its amax joins the warps' through shared memory, a lane's four rows are
-// one word of the column's 32 bytes.  STATS false: r is read, only the columnwise view is written (rows too wide for a
-// cluster; the sum, r and what goes by rows are norm_kernel's).
+// A block holds 32 rows of 256 columns: its eight warps four rows each, a lane eight columns of every row.  The blocks of
+// a cluster share the rows and trade their sums of squares through shared memory.  A column's 32 rows are one block of
+// the columnwise view: its amax joins the warps' through shared memory, a lane's four rows are one word of the column's
+// 32 bytes.  STATS false: r is read, only the columnwise view is written (rows too wide for a cluster; the sum, r and
+// what goes by rows are norm_kernel's).
+//
+// Both views of [8192, 2048] bf16 with a bf16 residual: 36.8 us, 3.7 TB/s of x, the residual, the sum and the views.
+// Bound by latency: load, exchange and two rounds through shared memory follow one another in a block, and four blocks
+// of 64 registers a thread are an SM's.  512 columns a block (two of them an SM) 42.3 us.
 constexpr int kTileThreads = 256, kTileRows = 32, kMostCluster = 8;
 
-template <typename TX, typename TS, bool RES, int VPL, bool STATS>
-__global__ void __launch_bounds__(kTileThreads, VPL == 1 ? 4 : 2) norm_tile_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int CW = 256 * VPL;
+template <typename TX, typename TS, bool RES, bool STATS>
+__global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int CW = 256;  // columns
   using TH = typename std::conditional<RES, TS, TX>::type;
   __shared__ __align__(16) uint32_t plane[8][CW];  // columns' amax of each warp, then their codes of each warp's rows
   __shared__ __align__(16) float inv[CW];
@@ -262,42 +266,35 @@ __global__ void __launch_bounds__(kTileThreads, VPL == 1 ? 4 : 2) norm_tile_kern
   gtp::ptx::wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row0 = int64_t(blockIdx.y) * kTileRows + 4 * warp, c0 = int64_t(blockIdx.x) * CW;
-  Eight<TX> x[4][VPL];
-  Eight<TH> h[4][VPL];
+  Eight<TX> x[4];
+  Eight<TH> h[4];
+  const int64_t c = c0 + 8 * lane;
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int64_t c = c0 + 8 * (32 * v + lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i][v].clear();
-      h[i][v].clear();
-      if (c < a.cols) {
-        x[i][v].load(static_cast<const TX *>(a.x) + (row0 + i) * a.x_ld + c);
-        if (RES) h[i][v].load(static_cast<const TH *>(a.residual) + (row0 + i) * a.residual_ld + c);
-      }
+  for (int i = 0; i < 4; ++i) {
+    x[i].clear();
+    h[i].clear();
+    if (c < a.cols) {
+      x[i].load(static_cast<const TX *>(a.x) + (row0 + i) * a.x_ld + c);
+      if (RES) h[i].load(static_cast<const TH *>(a.residual) + (row0 + i) * a.residual_ld + c);
     }
   }
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int64_t c = c0 + 8 * (32 * v + lane);
+  for (int i = 0; i < 4; ++i) {
+    float f[8];
+    x[i].get(f);
+    if (RES) {
+      float res[8];
+      h[i].get(res);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float f[8];
-      x[i][v].get(f);
-      if (RES) {
-        float res[8];
-        h[i][v].get(res);
+      for (int k = 0; k < 8; ++k) f[k] += res[k];
+    }
+    h[i].set(f);
+    if (STATS) {
+      h[i].get(f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] += res[k];
-      }
-      h[i][v].set(f);
-      if (STATS) {
-        h[i][v].get(f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[i] = fmaf(f[k], f[k], s[i]);
-        if (RES && c < a.cols) h[i][v].store(static_cast<TH *>(a.sum) + (row0 + i) * a.sum_ld + c);
-      }
+      for (int k = 0; k < 8; ++k) s[i] = fmaf(f[k], f[k], s[i]);
+      if (RES && c < a.cols) h[i].store(static_cast<TH *>(a.sum) + (row0 + i) * a.sum_ld + c);
     }
   }
   float r[4];
@@ -324,81 +321,62 @@ __global__ void __launch_bounds__(kTileThreads, VPL == 1 ? 4 : 2) norm_tile_kern
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = a.rstd[row0 + i];
   }
+  const bool live = c < a.cols;
+  float w[8];
+  uint32_t amax[8];
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int64_t c = c0 + 8 * (32 * v + lane);
-    const bool live = c < a.cols;
-    float w[8];
-    uint32_t amax[8];
+  for (int k = 0; k < 8; ++k) w[k] = 0.f, amax[k] = 0;
+  if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = 0.f, amax[k] = 0;
-    if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[8];
-      h[i][v].get(y);
-      uint32_t bits = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        y[k] = y[k] * r[i] * w[k];
-        const uint32_t b = __float_as_uint(y[k]) & 0x7FFFFFFFu;
-        amax[k] = max(amax[k], b);
-        bits = max(bits, b);
-      }
-      if (STATS && a.y && live) store_y(a, row0 + i, c, y);
-      if (STATS && a.row_codes) store_row_view(a, row0 + i, c, live, y, bits);
-    }
-    uint4 *p = reinterpret_cast<uint4 *>(&plane[warp][8 * (32 * v + lane)]);
-    p[0] = make_uint4(amax[0], amax[1], amax[2], amax[3]);
-    p[1] = make_uint4(amax[4], amax[5], amax[6], amax[7]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int j = 256 * v + threadIdx.x;
+  for (int i = 0; i < 4; ++i) {
+    float y[8];
+    h[i].get(y);
     uint32_t bits = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) bits = max(bits, plane[q][j]);
-    const uint32_t byte = block_scale(bits, inv[j]);
-    if (c0 + j < a.cols) a.col_scales[scale_at(c0 + j, blockIdx.y, a.rows >> 5, a.col_words)] = uint8_t(byte);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int64_t c = c0 + 8 * (32 * v + lane);
-    const int j = 8 * (32 * v + lane);
-    float w[8], f[8], y[4][8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = 0.f;
-    if (c < a.cols) gtp::load8_of(a.weight, a.weight_f32, c, w);
-    gtp::load8_of(inv, 1, j, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // the same y again, from registers
-      h[i][v].get(y[i]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[i][k] = y[i][k] * r[i] * w[k] * f[k];
+    for (int k = 0; k < 8; ++k) {
+      y[k] = y[k] * r[i] * w[k];
+      const uint32_t b = __float_as_uint(y[k]) & 0x7FFFFFFFu;
+      amax[k] = max(amax[k], b);
+      bits = max(bits, b);
     }
-    uint32_t code[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) code[k] = gtp::mx::encode4(y[0][k], y[1][k], y[2][k], y[3][k]);
-    uint4 *p = reinterpret_cast<uint4 *>(&plane[warp][j]);
-    p[0] = make_uint4(code[0], code[1], code[2], code[3]);
-    p[1] = make_uint4(code[4], code[5], code[6], code[7]);
+    if (STATS && a.y && live) store_y(a, row0 + i, c, y);
+    if (STATS && a.row_codes) store_row_view(a, row0 + i, c, live, y, bits);
   }
+  uint4 *const p = reinterpret_cast<uint4 *>(&plane[warp][8 * lane]);
+  p[0] = make_uint4(amax[0], amax[1], amax[2], amax[3]);
+  p[1] = make_uint4(amax[4], amax[5], amax[6], amax[7]);
   __syncthreads();
+  const int j = threadIdx.x;
+  uint32_t bits = 0;
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int j = 256 * v + threadIdx.x;
-    if (c0 + j < a.cols) {
-      uint8_t *const dst = a.col_codes + (c0 + j) * a.rows + int64_t(blockIdx.y) * kTileRows;
-      const uint32_t w[8] = {plane[0][j], plane[1][j], plane[2][j], plane[3][j],
-                             plane[4][j], plane[5][j], plane[6][j], plane[7][j]};
-      if (a.codes_on_32) {
-        gtp::store_32b(dst, w);
-      } else {
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+  for (int q = 0; q < 8; ++q) bits = max(bits, plane[q][j]);
+  const uint32_t byte = block_scale(bits, inv[j]);
+  if (c0 + j < a.cols) a.col_scales[scale_at(c0 + j, blockIdx.y, a.rows >> 5, a.col_words)] = uint8_t(byte);
+  __syncthreads();
+  float f[8], y[4][8];
+  if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);  // again, as y: not kept over the barriers
+  gtp::load8_of(inv, 1, 8 * lane, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // the same y again, from registers
+    h[i].get(y[i]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[i][k] = y[i][k] * r[i] * w[k] * f[k];
+  }
+  uint32_t code[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) code[k] = gtp::mx::encode4(y[0][k], y[1][k], y[2][k], y[3][k]);
+  p[0] = make_uint4(code[0], code[1], code[2], code[3]);
+  p[1] = make_uint4(code[4], code[5], code[6], code[7]);
+  __syncthreads();
+  if (c0 + j < a.cols) {
+    uint8_t *const dst = a.col_codes + (c0 + j) * a.rows + int64_t(blockIdx.y) * kTileRows;
+    const uint32_t bytes[8] = {plane[0][j], plane[1][j], plane[2][j], plane[3][j],
+                               plane[4][j], plane[5][j], plane[6][j], plane[7][j]};
+    if (a.codes_on_32) {
+      gtp::store_32b(dst, bytes);
+    } else {
+      reinterpret_cast<uint4 *>(dst)[0] = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
+      reinterpret_cast<uint4 *>(dst)[1] = make_uint4(bytes[4], bytes[5], bytes[6], bytes[7]);
     }
   }
 }
@@ -457,7 +435,8 @@ __global__ void __launch_bounds__(256)
 
 // --------------------------------------------------------------------------- host
 
-// Threads a row, rows a block, groups of eight a thread: one group up to 4096 columns, else four.
+// Threads a row, rows a block, groups of eight a thread: one group up to 4096 columns ([8192, 4096] bf16 42.8 us, with four
+// a thread 46.6; [8192, 2048] 22.5 and 24.9), else four.
 struct RowShape {
   int tx, ty, V;
 };
@@ -474,7 +453,8 @@ gtp_status launch_rows(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream
   const RowShape s = row_shape(a.cols);
   const dim3 block(s.tx, s.ty);
   const int64_t blocks = (a.rows + s.ty - 1) / s.ty, most = int64_t(dev.sm_count) * std::max(1, 2048 / (s.tx * s.ty));
-  // rows a time: as many bytes in flight a thread as 64 registers leave; few rows: one, spread over the machine
+  // rows a time: four of bf16 ([8192, 2048] with a residual 22.5 us, one at a time 26.9), one where a row has more bytes (all
+  // fp32 36.5 us, two at a time 39.5); few rows: one, spread over the machine
   constexpr int MANY = sizeof(TX) + (RES ? sizeof(TS) : 0) > 4 ? 1 : 4;
   if (MANY > 1 && s.V == 1 && blocks > most)
     return gtp::launch_overlapped(norm_kernel<TX, TS, RES, 1, MANY>, unsigned((blocks + MANY - 1) / MANY), block, 0, st, "rmsnorm", a);
@@ -490,6 +470,9 @@ gtp_status launch_elements_of(const NormArgs &a, const gtp::DeviceInfo &dev, cud
                                 unsigned(std::min<int64_t>(blocks, int64_t(dev.sm_count) * 64)), block, 0, st, "rmsnorm", a);
 }
 
+// As many threads as eight elements each make up a row, so that a row is in registers after one round of loads: blocks of
+// 256 take 28.9 us for [8192, 1000], of 512 59.5; blocks of 512 81 us for [8192, 4095], of 1024 144; rows of 250 by
+// a warp each 6 us, by blocks of 256 26.
 template <typename TX, typename TS, bool RES>
 gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   if (a.cols <= 32 * 8) return launch_elements_of<TX, TS, RES, 32, 8>(a, dev, st);
@@ -499,9 +482,9 @@ gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaSt
   return launch_elements_of<TX, TS, RES, 1024, 16>(a, dev, st);
 }
 
-template <typename TX, typename TS, bool RES, int VPL, bool STATS>
+template <typename TX, typename TS, bool RES, bool STATS>
 gtp_status launch_tiles_of(const NormArgs &a, cudaStream_t st) {
-  const int64_t wide = (a.cols + 256 * VPL - 1) / (256 * VPL);
+  const int64_t wide = (a.cols + 255) / 256;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(wide), unsigned(a.rows / kTileRows));
   cfg.blockDim = dim3(kTileThreads);
@@ -520,21 +503,23 @@ gtp_status launch_tiles_of(const NormArgs &a, cudaStream_t st) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = unsigned(n);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_tile_kernel<TX, TS, RES, VPL, STATS>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_tile_kernel<TX, TS, RES, STATS>, a);
   if (e != cudaSuccess) return gtp::fail(GTP_E_CUDA, "rmsnorm: %s", cudaGetErrorString(e));
   return gtp::check_launch("rmsnorm");
 }
 
 template <typename TX, typename TS, bool RES>
 gtp_status launch_tiles(NormArgs a, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  if (a.cols <= 256 * kMostCluster) return launch_tiles_of<TX, TS, RES, 1, true>(a, st);
-  if (a.cols <= 512 * kMostCluster) return launch_tiles_of<TX, TS, RES, 2, true>(a, st);
+  // one launch where a cluster holds a row, two above: at [8192, 4096] 67 us (a cluster of eight blocks of 512 columns
+  // 76 to 79), at [8192, 2048] 35.2 against 36.8 with a bf16 residual, 47.2 against 43.3 with an fp32 one, and at
+  // [256, 2048] 6.3 against 5.0
+  if (a.cols <= 256 * kMostCluster) return launch_tiles_of<TX, TS, RES, true>(a, st);
   uint8_t *const codes = a.col_codes;
   a.col_codes = nullptr;
   if (gtp_status s = launch_rows<TX, TS, RES>(a, dev, st)) return s;
   a.col_codes = codes;
   if (RES) a.x = a.sum, a.x_ld = a.sum_ld;
-  return launch_tiles_of<TS, TS, false, 1, false>(a, st);
+  return launch_tiles_of<TS, TS, false, false>(a, st);
 }
 
 template <typename TX, typename TS, bool RES>

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const __grid_con
 
 // Rows that start anywhere: the elements TX apart are a thread's (as the forward's).
 template <typename TD, typename TS, int TX, int K>
-__global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 4 : 1024 / TX) norm_grad_elements_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX) norm_grad_elements_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float part[2][1][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
@@ -223,8 +223,9 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *part, in
 
 // --------------------------------------------------------------------------- host
 
-// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four) and blocks: those that run at
-// once, 512 threads an SM (128 registers each).  One rule for the workspace's size and the launch.
+// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four: [8192, 4096] bf16 54.1 and 57.7
+// us, [8192, 2048] 29.4 and 36.2) and blocks: those that run at once, 512 threads an SM (128 registers each).  One rule for
+// the workspace's size and the launch.
 struct GradShape {
   int tx, ty, V, grid;
 };
@@ -237,10 +238,11 @@ GradShape grad_shape(int64_t rows, int64_t cols, int sms) {
   return {tx, ty, V, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
 }
 
-// The same for rows that start anywhere.
+// The same for rows that start anywhere: 1024 threads an SM of 64 registers each ([8192, 2047] bf16 54.6 us, 768 of 80
+// registers 59.0), 768 where a warp has a row ([8192, 250] 28.4 us, 1024 of them 33.1).
 GradShape elements_shape(int64_t rows, int64_t cols, int sms) {
   const int tx = cols <= 32 * 8 ? 32 : cols <= 256 * 8 ? 256 : cols <= 512 * 8 ? 512 : 1024, ty = tx == 32 ? 8 : 1;
-  const int64_t most = int64_t(sms) * (1024 / (tx * ty));
+  const int64_t most = int64_t(sms) * (tx == 32 ? 3 : 1024 / tx);
   return {tx, ty, cols <= 1024 * 8 ? 1 : 2, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
 }
 
