@@ -621,6 +621,73 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
   if (open || goes) join_row<TG, VEC>(a, tile, open ? begins : tile, ends, row, group, c, tx, n);
 }
 
+// So few tokens that every block sorts them for itself, by counting: no second launch and no parts, a row's tokens are
+// summed where its first place's tile is.  64 tokens x 2048 take 5.2 us (two launches 7.6), 9 where all are one row's
+// (9.4); at 128 one row's take 18.9 and 10.7.
+constexpr int kFewTokens = 64, kFewTile = 4;
+
+struct FewArgs {
+  const void *ids, *dout;
+  void *grad;
+  int64_t dout_ld, first_row, rows, cols;
+  int32_t tokens, wide;
+  float scale;
+};
+
+template <typename TD, typename TG, bool VEC>
+__global__ void __launch_bounds__(kThreads) embedding_few_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int F = VEC ? 8 : 4;  // tokens' rows in flight
+  __shared__ int32_t seen[kFewTokens], key[kFewTokens + 1], token[kFewTokens];
+  gtp::ptx::allow_dependents();
+  gtp::ptx::wait_prior_grid();
+  const int me = threadIdx.y * blockDim.x + threadIdx.x, T = a.tokens, rows = int(a.rows);
+  for (int t = me; t < T; t += kThreads) seen[t] = int32_t(row_of(a.ids, a.wide, t, a.first_row, a.rows));
+  if (me == 0) key[T] = rows;
+  __syncthreads();
+  for (int t = me; t < T; t += kThreads) {
+    const int32_t k = seen[t];
+    int place = 0;
+    for (int s = 0; s < T; ++s) place += seen[s] < k || (seen[s] == k && s < t);
+    key[place] = k;
+    token[place] = t;
+  }
+  __syncthreads();
+  int64_t c;
+  int n;
+  if (!columns<VEC>(a.cols, c, n)) return;
+  const int p0 = (int(blockIdx.y) * blockDim.y + threadIdx.y) * kFewTile, p1 = min(p0 + kFewTile, T), tx = blockDim.x;
+  for (int p = p0; p < p1;) {
+    const int32_t row = key[p];
+    if (row >= rows) return;
+    int end = p + 1;
+    while (key[end] == row) ++end;
+    if (p > 0 && key[p - 1] == row) {  // begun before this tile
+      p = end;
+      continue;
+    }
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int q = p; q < end; q += F) {
+      Group<TD, VEC> x[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        x[i].clear();
+        if (q + i < end) x[i].load(static_cast<const TD *>(a.dout) + int64_t(token[q + i]) * a.dout_ld + c, tx, n);
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        float f[8];
+        x[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += f[j];
+      }
+    }
+    add8<VEC>(static_cast<TG *>(a.grad) + int64_t(row) * a.cols + c, tx, n, a.scale, acc);
+    p = end;
+  }
+}
+
 // --------------------------------------------------------------------------- host
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
@@ -751,6 +818,16 @@ gtp_status launch_sums(const SumArgs &a, cudaStream_t st) {
                                 "embedding_grad", a);
 }
 
+template <typename TD, typename TG>
+gtp_status launch_few(const FewArgs &a, cudaStream_t st) {
+  const bool vec = a.cols % 8 == 0 && in_eights(a.dout, a.dout_ld, sizeof(TD)) && in_eights(a.grad, a.cols, sizeof(TG));
+  const dim3 block = block_of(a.cols, 32);
+  const int tiles = (a.tokens + kFewTile - 1) / kFewTile;
+  const dim3 grid(unsigned((a.cols + 8 * block.x - 1) / (8 * block.x)), (tiles + block.y - 1) / block.y);
+  return gtp::launch_overlapped(vec ? embedding_few_kernel<TD, TG, true> : embedding_few_kernel<TD, TG, false>, grid, block, 0, st,
+                                "embedding_grad", a);
+}
+
 }  // namespace
 
 extern "C" gtp_status gtp_embedding(const gtp_embedding_desc *d, gtp_stream stream) {
@@ -819,19 +896,24 @@ extern "C" gtp_status gtp_embedding_grad_accum(const gtp_embedding_grad_desc *d,
     return gtp::fail(GTP_E_ARG, "the gradient view or the workspace overlaps an input or the other");
   gtp::DeviceInfo dev;
   if (gtp_status s = gtp::require_sm103(&dev)) return s;
+  cudaStream_t st = gtp::as_stream(stream);
+  using B = __nv_bfloat16;
+  if (T <= kFewTokens) {
+    const FewArgs a = {d->ids, d->dout, grad, dout_ld, d->first_row, R, C, int32_t(T), d->ids64, d->scale};
+    if (d->dout_dtype == GTP_F32) return d->grad_dtype == GTP_F32 ? launch_few<float, float>(a, st) : launch_few<float, B>(a, st);
+    return d->grad_dtype == GTP_F32 ? launch_few<B, float>(a, st) : launch_few<B, B>(a, st);
+  }
   const auto at = [&](int64_t place) { return reinterpret_cast<int32_t *>(ws + place); };
   SortArgs sort = {};
   sort.ids = d->ids, sort.first_row = d->first_row, sort.rows = R, sort.tokens = int32_t(T), sort.wide = d->ids64;
   sort.key = at(plan.key), sort.token = at(plan.token), sort.key2 = at(plan.key2), sort.token2 = at(plan.token2);
   sort.counts = at(plan.counts), sort.tiles = plan.sort_tiles;
   sort.counters = at(plan.counters), sort.counter_count = int64_t(3) * plan.tiles * plan.groups;
-  cudaStream_t st = gtp::as_stream(stream);
   if (gtp_status s = sort_tokens(sort, plan, st)) return s;
   SumArgs a = {};
   a.key = sort.key, a.token = sort.token, a.dout = d->dout, a.grad = grad, a.part = reinterpret_cast<float *>(ws + plan.part);
   a.counters = sort.counters, a.groups = plan.groups;
   a.dout_ld = dout_ld, a.rows = R, a.cols = C, a.tokens = int32_t(T), a.tile = plan.tile, a.tiles = plan.tiles, a.scale = d->scale;
-  using B = __nv_bfloat16;
   if (d->dout_dtype == GTP_F32) return d->grad_dtype == GTP_F32 ? launch_sums<float, float>(a, st) : launch_sums<float, B>(a, st);
   return d->grad_dtype == GTP_F32 ? launch_sums<B, float>(a, st) : launch_sums<B, B>(a, st);
 }

@@ -82,7 +82,8 @@ def test_lookup_strides_empty_and_infinite_scale():
 
 @pytest.mark.parametrize("dd,gd", [(B, F), (F, F), (B, B), (F, B)])
 @pytest.mark.parametrize("T,rows,C,first,offset", [(1, 5, 8, 0, 0), (1, 1, 1, 7, 3), (64, 10, 16, 0, 64), (65, 33, 40, 5, 1),
-                                                   (1111, 401, 1000, 401, 8), (700, 3, 77, 2, 5), (16, 50, 2056, 0, 0)])
+                                                   (1111, 401, 1000, 401, 8), (700, 3, 77, 2, 5), (16, 50, 2056, 0, 0), (63, 30, 24, 0, 8),
+                                                   (66, 30, 24, 0, 8), (62, 9, 333, 4, 1), (130, 40, 2051, 0, 3)])
 def test_gradient(T, rows, C, first, offset, dd, gd):
     for kind in ("mixed", "one row", "none"):
         ids = make_ids(T, rows, first, kind, wide=T % 2 == 1).to(DEV)
