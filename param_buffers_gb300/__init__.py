@@ -836,12 +836,14 @@ def _rng(rng):
 
 _F32, _BF16, _U8 = abi.GTP_F32, abi.GTP_BF16, abi.GTP_U8
 _TORCH_DTYPES: dict = {}  # torch dtype -> gtp_dtype; filled at the first call (torch is imported late)
+_FLOAT_DTYPES: dict = {}  # the same of the float types alone
 
 
 def _dtype_of(t, name: str):
     """The gtp_dtype of a tensor: the slow way, which fills the table or says what is wrong."""
     import torch
     _TORCH_DTYPES.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16, torch.uint8: abi.GTP_U8})
+    _FLOAT_DTYPES.update({torch.float32: abi.GTP_F32, torch.bfloat16: abi.GTP_BF16})
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     return _TORCH_DTYPES.get(t.dtype)
@@ -861,14 +863,19 @@ def _float_dtype(t, name: str) -> int:
 
 def _matrix(t, name: str):
     """(dtype, shape, row stride) of a 2-D float matrix whose rows are contiguous."""
-    dt = _float_dtype(t, name)
+    try:  # the usual case without another call
+        dt = _FLOAT_DTYPES[t.dtype] if t.is_cuda else _float_dtype(t, name)
+    except (AttributeError, KeyError, TypeError):
+        dt = _float_dtype(t, name)
     shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have 2 dims, got {len(shape)}")
+    try:
+        rows, cols = shape
+    except ValueError:
+        raise ValueError(f"{name} must have 2 dims, got {len(shape)}") from None
     ld, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return dt, shape, ld if shape[0] > 1 else shape[1]
+    return dt, shape, ld if rows > 1 else cols
 
 
 def _scale_bytes(rows: int, blocks: int) -> int:
@@ -1182,17 +1189,18 @@ def gtp_embedding_grad_accum(dout, ids, grad_data, grad_offset: int, rows: int, 
 # ----------------------------------------------------------------------------- root-mean-square norm
 
 def _vector(t, n: int, name: str) -> int:
-    dt = _float_dtype(t, name)
+    try:
+        dt = _FLOAT_DTYPES[t.dtype] if t.is_cuda else _float_dtype(t, name)
+    except (AttributeError, KeyError, TypeError):
+        dt = _float_dtype(t, name)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{n}]")
     return dt
 
 
 def _rstd(t, rows: int) -> int:
-    if _float_dtype(t, "rstd") != _F32:
+    if _vector(t, rows, "rstd") != _F32:
         raise TypeError(f"rstd must be float32, got {t.dtype}")
-    if t.shape != (rows,) or not t.is_contiguous():
-        raise ValueError(f"rstd must be contiguous [{rows}]")
     return t.data_ptr()
 
 
