@@ -766,8 +766,8 @@ gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld
  *   token, or none's: any id is allowed),  one rounding to out's type;
  *   grad_data[grad_offset : +rows*cols].view(rows, cols)[ids[t] - first_row] += scale * dout[t].
  * A row's tokens are sorted and summed in fp32 in an order that depends on the ids alone, and added to the
- * buffer (F32 or BF16, any view offset) in one rounding: equal calls give equal bits.  Rows without a token
- * are neither read nor written.
+ * buffer (F32 or BF16, any view offset) in one rounding: equal calls give equal bits.  The addition may take
+ * values of F32 below 2^-126 as 0.  Rows without a token are neither read nor written.
  * ids: device [tokens], int32 (ids64 = 0) or int64, aligned to their size.  table [rows, cols], out and dout
  * [tokens, cols]: F32 or BF16, row strides table_ld, out_ld, dout_ld (elements, >= cols), element-aligned.
  * No output overlaps an input (GTP_E_ARG).  workspace: device, 32-byte aligned, at least
@@ -811,7 +811,8 @@ gtp_status gtp_embedding_grad_accum(const gtp_embedding_grad_desc *desc, void *w
  * be x exactly (but not with a columnwise view and no residual); otherwise no output overlaps an input or
  * another output (GTP_E_ARG).  Row strides in elements, >= cols; arrays element-aligned; with a view, the
  * rows of every matrix on eight elements' size (16 bytes of BF16, 32 of F32), the weight and the codes on 16
- * bytes (GTP_E_ALIGN), cols % 32 == 0 and, columnwise, rows % 32 == 0 and rows <= 32 * 65535 (GTP_E_SHAPE).  cols <= 16384, rows <= 2^30 (GTP_E_SHAPE). */
+ * bytes (GTP_E_ALIGN), cols % 32 == 0 and, columnwise, rows % 32 == 0 and rows <= 32 * 65535 (GTP_E_SHAPE).
+ * cols <= 16384, rows <= 2^30 (GTP_E_SHAPE). */
 typedef struct {
   const void *x;            /* [rows, cols]                                                     */
   const void *residual;     /* [rows, cols] or NULL                                             */
@@ -863,9 +864,9 @@ gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_
  *   X = G / |G|_F (0 for a matrix of zeros);   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X,
  * (a, b, c) = coefficients[0..2], with the smaller Gram matrix (X^T X on the other side for rows > cols).
  * fp16 tensor-core products with fp32 accumulation, the diagonals of A and of b A + c A^2 in fp32 and the X of the
- * linear term in 22 bits: relative error 2e-4 to 1e-3 before the result's own rounding.  The sum of squares is taken in fp32 by
- * fours and in fp64 across: where it is not finite, the result is NaN.  A fixed order: equal calls give equal
- * bits.
+ * linear term in 22 bits: relative error 2e-4 to 1e-3 before the result's own rounding.  The sum of squares
+ * is taken in fp32 by sixteens and in fp64 across: where it is not finite, the result is NaN, and elements below
+ * 1e-22 or so count as 0.  A fixed order: equal calls give equal bits.
  * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane
  * (elements), element-aligned; dst likewise, and may be src or overlap it (src is read before dst is
  * written).  1 <= steps <= 16; coefficients (host) that let a singular value of [0, 1] grow past 2 are
