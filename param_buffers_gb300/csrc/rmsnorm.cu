@@ -16,6 +16,7 @@
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "device.h"
 #include "eight.cuh"
@@ -251,9 +252,10 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, RES && TX == 256 ? 5 : 0)
 // 32 bytes.  STATS false: r is read, only the columnwise view is written (rows too wide for a cluster; the sum, r and
 // what goes by rows are norm_kernel's).
 //
-// Both views of [8192, 2048] bf16 with a bf16 residual: 36.8 us, 3.7 TB/s of x, the residual, the sum and the views.
-// Bound by latency: load, exchange and two rounds through shared memory follow one another in a block, and four blocks
-// of 64 registers a thread are an SM's.  512 columns a block (two of them an SM) 42.3 us.
+// Both views of [8192, 2048] bf16 with a bf16 residual: 35.3 us, 3.9 TB/s of x, the residual, the sum and the views (36.8
+// with the sum written before the cluster's exchange).  Bound by latency: load, exchange and two rounds through shared
+// memory follow one another in a block, and four blocks of 64 registers a thread are an SM's (three 39.4 us, five 48.5;
+// 512 columns a block, two of them an SM, 42.3).
 constexpr int kTileThreads = 256, kTileRows = 32, kMostCluster = 8;
 
 template <typename TX, typename TS, bool RES, bool STATS>
@@ -295,10 +297,12 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
       h[i].get(f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[i] = fmaf(f[k], f[k], s[i]);
-      if (RES && c < a.cols) h[i].store(static_cast<TH *>(a.sum) + (row0 + i) * a.sum_ld + c);
     }
   }
-  float r[4];
+  const bool live = c < a.cols;
+  float r[4], w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = 0.f;
   if (STATS) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
@@ -309,7 +313,13 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < 4; ++i) there[i * kMostCluster] = s[i];
     }
-    cluster.sync();
+    auto token = cluster.barrier_arrive();  // the sum and the weight while the other blocks come
+    if (RES && live) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i].store(static_cast<TH *>(a.sum) + (row0 + i) * a.sum_ld + c);
+    }
+    if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);
+    cluster.barrier_wait(std::move(token));
     // lane 8 i + b: block b's part of row i; added up in the same order in every block
     float t = (lane & 7) < blocks ? squares[4 * warp + (lane >> 3)][lane & 7] : 0.f;
 #pragma unroll
@@ -321,13 +331,11 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = a.rstd[row0 + i];
+    if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);
   }
-  const bool live = c < a.cols;
-  float w[8];
   uint32_t amax[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = 0.f, amax[k] = 0;
-  if (live) gtp::load8_of(a.weight, a.weight_f32, c, w);
+  for (int k = 0; k < 8; ++k) amax[k] = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float y[8];
@@ -512,7 +520,7 @@ gtp_status launch_tiles_of(const NormArgs &a, cudaStream_t st) {
 template <typename TX, typename TS, bool RES>
 gtp_status launch_tiles(NormArgs a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   // one launch where a cluster holds a row, two above: at [8192, 4096] 67 us (a cluster of eight blocks of 512 columns
-  // 76 to 79), at [8192, 2048] 35.2 against 36.8 with a bf16 residual, 47.2 against 43.3 with an fp32 one, and at
+  // 76 to 79), at [8192, 2048] 35.2 against 35.3 with a bf16 residual, 47.2 against 43.0 with an fp32 one, and at
   // [256, 2048] 6.3 against 5.0
   if (a.cols <= 256 * kMostCluster) return launch_tiles_of<TX, TS, RES, true>(a, st);
   uint8_t *const codes = a.col_codes;
