@@ -1165,6 +1165,9 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   unsigned int *err = &g_ortho_wait_timeouts;
+  // A CTA that has a whole matrix reads nobody else's X: its last warp of an iteration starts the next one, without a round
+  // through the counters (84 x 26 33.7 us, with it 37.4).
+  const bool alone = G == 1 && s.parts == 1;
   // seq counts this CTA's iterations over all its matrices; `ready` holds the last one that may start
   if (warp == 0) {
     if (lane == 0) {  // -------------------------------------------------- producer: X's tiles, GRAM's then UPDATE's
@@ -1278,7 +1281,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = group; ok && k < s.count; k += s.groups)
         for (int it = 0; ok && it < a.steps; ++it, ++seq) {
-          if (it == 0) continue;
+          if (it == 0 || alone) continue;
           const unsigned int all = unsigned(G * s.parts);
           const uint64_t t0 = globaltimer_ns();
           uint32_t spins = 0;
@@ -1476,7 +1479,13 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             __threadfence_block();
             if ((atomicAdd(finished, 1) & (kEpilogueWarps - 1)) == kEpilogueWarps - 1) {
               __threadfence_block();
-              add_release(&a.arrived[k * kMostSteps + it]);
+              if (alone) {
+                fence_proxy_async_global();
+                __threadfence_block();
+                *ready = seq + 1;
+              } else {
+                add_release(&a.arrived[k * kMostSteps + it]);
+              }
             }
           }
         }
