@@ -133,3 +133,33 @@ def test_orthogonalize_rows_far_apart():
     for k in range(2):
         want = O.orthogonalize(f64(src[k]))
         assert np.linalg.norm(f64(out[k]) - want) <= 4e-3 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("R,C", [(65536, 16), (16, 65536), (3, 65536), (65536, 200), (300, 30000), (30000, 260)])
+def test_orthogonalize_long_sides(R, C):
+    src = 1e-3 * torch.randn(R, C, device=DEV)
+    out = torch.full((R, C), float("nan"), device=DEV)
+    ws = torch.empty(gtp.gtp_orthogonalize_workspace_bytes(1, R, C), dtype=torch.uint8, device=DEV).fill_(0xFF)
+    gtp.gtp_orthogonalize(src, out, ws)
+    want = O.orthogonalize(f64(src))
+    assert np.linalg.norm(f64(out) - want) <= 4e-3 * np.linalg.norm(want)
+    assert gtp.gtp_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("R,C", [(257, 270), (130, 40)])
+def test_a_step_of_64_weights(R, C):
+    n, each = 64, R * C
+    offsets = [k * (each + 1) for k in range(n)]
+    g, m, p = (torch.randn(n * (each + 1), device=DEV) * s for s in (1e-3, 1e-3, 0.02))
+    g0, m0, p0 = g.clone(), m.clone(), p.clone()
+    ws = torch.empty(gtp.gtp_orthogonalize_workspace_bytes(n, R, C), dtype=torch.uint8, device=DEV).fill_(0xFF)
+    h = gtp.MuonHparams(lr=0.02, momentum=0.9, weight_decay=0.1, scale=1.5)
+    gtp.gtp_muon_step(g, m, p, None, offsets, R, C, h, ws)
+    for k in (0, 1, 31, 62, 63):
+        view = lambda t: f64(t[offsets[k]:offsets[k] + each]).reshape(R, C)
+        _, w = O.step(view(g0), view(m0), view(p0), float(np.float32(0.9)), 0.02, 0.1, 1.5)
+        moved = np.linalg.norm(w - view(p0) * (1 - 0.002))
+        assert np.linalg.norm(view(p) - w) <= 4e-3 * moved + 2.0 ** -22 * np.linalg.norm(view(p0))
+    gap = torch.tensor([o + each for o in offsets], device=DEV)
+    assert torch.equal(p[gap], p0[gap]) and torch.equal(m[gap], m0[gap]) and torch.equal(g[gap], g0[gap])
+    assert gtp.gtp_wait_timeouts() == 0
