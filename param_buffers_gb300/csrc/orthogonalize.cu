@@ -1076,7 +1076,8 @@ constexpr int R_STAGE = 128 * BK * 2;  // 128 rows of 64 (or 64 of 128)
 struct SmallArgs {
   int count, rows, cols, stand;          // X: its rows in memory
   int parts, groups;                     // CTAs or pairs a matrix, matrices at a time
-  int tiles, gram_blocks, poly_blocks;   // X's tiles; blocks of 64 of the contractions
+  int tiles, half;                       // X's tiles; 1: half as wide (TALL: half of the columns each)
+  int gram_blocks, poly_blocks;          // blocks of 64 of the contractions
 };
 
 struct SmallMaps {
@@ -1180,19 +1181,19 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
         const int r0 = k * s.stand;
         for (int it = 0; ok && it < a.steps; ++it, ++seq) {
           if (it > 0 && !(ok = wait_ready(ready, seq, abort_flag, err))) break;
-          // blocks of 128 indices of a tile from i0 on, 64 of the contraction each; along: it runs along X's rows
-          const auto blocks = [&](bool along, int i0, int n) {
+          // blocks of 128 (or 64) indices of a tile from i0 on, 64 of the contraction each; along: it runs along X's rows
+          const auto blocks = [&](bool along, int i0, int n, int boxes) {
             const CUtensorMap *const x = along ? &maps.x_tall[it & 1] : &maps.x[it & 1];
             int cx = along ? 0 : i0, cy = along ? r0 + i0 : r0;
             for (int b = 0; b < n; ++b) {
               if (!mbar_wait(&empty[stage], parity ^ 1u, abort_flag, err, 0x1u)) return false;
               if (rank == 0) {
-                mbar_arrive_expect_tx_relaxed(&full[stage], G * R_STAGE);
+                mbar_arrive_expect_tx_relaxed(&full[stage], along ? G * R_STAGE : G * boxes * BOX);
                 armed |= 1u << stage;
                 armed_parity = (armed_parity & ~(1u << stage)) | parity << stage;
               }
               uint8_t *const to = ring + stage * R_STAGE;
-              for (int i = 0; i < (along ? 1 : 2); ++i) {
+              for (int i = 0; i < (along ? 1 : boxes); ++i) {
                 if (G == 2) tma_load_2d_pair(x, bars + 8 * stage, to + i * BOX, cx + 64 * i, cy);
                 else tma_load_2d(x, &full[stage], to + i * BOX, cx + 64 * i, cy);
               }
@@ -1205,8 +1206,10 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return true;
           };
-          ok = blocks(!TALL, 128 * int(rank), s.gram_blocks);
-          for (int t = part; ok && t < s.tiles; t += s.parts) ok = blocks(TALL, t * N + 128 * int(rank), s.poly_blocks);
+          ok = blocks(!TALL, 128 * int(rank), s.gram_blocks, 2);
+          const int each = TALL ? 128 : 128 >> s.half;  // of a tile, this CTA's
+          for (int t = part; ok && t < s.tiles; t += s.parts)
+            ok = blocks(TALL, G * each * (TALL ? t >> s.half : t) + each * int(rank), s.poly_blocks, 2 >> s.half);
         }
       }
       for (int i = 0; i < S::STAGES; ++i)
@@ -1225,13 +1228,13 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
         if (G == 2) mma_commit_pair(bar, 0x3);
         else mma_commit(bar);
       };
-      // One product: `kind`'s contraction into the next accumulator.
-      const auto product = [&](int kind, int blocks) {
+      // One product: `kind`'s contraction into the next accumulator, `wide` columns; rows: of B' before them.
+      const auto product = [&](int kind, int blocks, int wide, int rows) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_parity ^ 1u, abort_flag, err, 0x2u))) return false;
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(acc * N);
         const bool a_mn = kind == kGram && TALL, b_mn = a_mn || (kind == kUpdate && !TALL);
-        const uint32_t idesc = idesc_f16_f32(N, N, a_mn, b_mn);
+        const uint32_t idesc = idesc_f16_f32(N, wide, a_mn, b_mn);
         const uint32_t da = a_mn ? UK * 128 : UK * 2, db = b_mn ? UK * 128 : UK * 2;
         for (int b = 0; b < blocks; ++b) {
           if (kind != kPoly && !__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], parity, abort_flag, err, 0x4u))) return false;
@@ -1239,7 +1242,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           if (elect_one_sync()) {
             const uint32_t x0 = smem_u32(ring + stage * R_STAGE), o0 = smem_u32(op + b * R_STAGE);
             const uint32_t a0 = kind == kGram || (kind == kUpdate && TALL) ? x0 : o0;
-            const uint32_t b0 = kind == kGram || (kind == kUpdate && !TALL) ? x0 : o0;
+            const uint32_t b0 = kind == kGram || (kind == kUpdate && !TALL) ? x0 : o0 + uint32_t(rows) * 128;
 #pragma unroll
             for (int i = 0; i < BK / UK; ++i)
               issue(d, sdesc_sw128(a0 + i * da, a_mn ? BOX : 16, 1024), sdesc_sw128(b0 + i * db, b_mn ? BOX : 16, 1024), idesc,
@@ -1268,8 +1271,9 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
       };
       for (int k = group; ok && k < s.count; k += s.groups)
         for (int it = 0; ok && it < a.steps; ++it) {
-          ok = product(kGram, s.gram_blocks) && operand() && product(kPoly, s.poly_blocks) && operand();
-          for (int t = part; ok && t < s.tiles; t += s.parts) ok = product(kUpdate, s.poly_blocks);
+          ok = product(kGram, s.gram_blocks, N, 0) && operand() && product(kPoly, s.poly_blocks, N, 0) && operand();
+          for (int t = part; ok && t < s.tiles; t += s.parts)
+            ok = product(kUpdate, s.poly_blocks, N >> s.half, TALL ? 64 * (t & s.half) : 0);
         }
       if (elect_one_sync()) commit(drained);
       __syncwarp();
@@ -1367,9 +1371,11 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) r = wait_ready(ready, seq, abort_flag, err);
           if (!(ok = __all_sync(0xFFFFFFFFu, r))) break;
         }
+        // Half of the columns (TALL) are 64 of each CTA's rows of B'.
+        const int wide = (N / 2) >> s.half;  // a warp's columns of a tile
         const auto place = [&](int t, int &row0, int &col) {
-          row0 = (TALL ? t * N : 0) + 128 * int(rank) + 32 * quarter;
-          col = (TALL ? 0 : t * N) + side * (N / 2);
+          row0 = (TALL ? (t >> s.half) * N : 0) + 128 * int(rank) + 32 * quarter;
+          col = TALL ? 64 * (t & s.half) + side * (G == 2 ? N / 2 : wide) : 2 * t * wide + side * wide;
         };
         const auto exists = [&](int row0, int col) { return row0 < s.stand && col < n_dim; };
         int ft = part, fc = 0;  // the next chunk to fetch
@@ -1377,7 +1383,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           int row0 = 0, col = 0;
           for (; ft < s.tiles; ft += s.parts, fc = 0) {
             place(ft, row0, col);
-            if (fc < N / 2 && exists(row0, col + fc)) break;
+            if (fc < wide && exists(row0, col + fc)) break;
           }
           if (ft >= s.tiles) return;
           const int q = slot ^ ahead;  // ahead is 0 or 1
@@ -1449,10 +1455,10 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
           int row0, col;
           place(t, row0, col);
           if (!(ok = result())) break;
-          const uint32_t base = tmem_base + lanes + uint32_t(acc * N + first_col);
+          const uint32_t base = tmem_base + lanes + uint32_t(acc * N + side * wide);
           const float own = evec[me];
 #pragma unroll 1
-          for (int c = 0; c < N / 2 && exists(row0, col + c); c += 32) {
+          for (int c = 0; c < wide && exists(row0, col + c); c += 32) {
             if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&cbar[slot], (cparity >> slot) & 1u, abort_flag, err, 0x400u)))) break;
             cparity ^= 1u << slot;
             flying &= ~(1 << slot);
@@ -1703,6 +1709,10 @@ gtp_status iterate_small(const Args &a, const Plan &plan, char *ws, int64_t coun
   SmallArgs s = {};
   s.count = int(count), s.rows = int(rows), s.cols = int(cols), s.stand = int(plan.rows);
   s.tiles = int((plan.n + Small<G>::N - 1) / Small<G>::N);
+  // tiles half as wide where there are CTAs for twice as many and the second halves exist: finishing a tile is the
+  // longest part of an iteration (512 x 256 80 us, whole tiles 94; 128 x 512 52 and 57; eight of 256 x 512 88 and 102)
+  s.half = (G == 2 || s.tiles > 1) && 2 * s.tiles * s.count <= clusters && (!TALL || plan.m > 64);
+  if (s.half) s.tiles = TALL ? 2 * s.tiles : int((plan.n + Small<G>::N / 2 - 1) / (Small<G>::N / 2));
   s.gram_blocks = int((plan.n + BK - 1) / BK), s.poly_blocks = int((plan.m + BK - 1) / BK);
   s.parts = std::max(1, std::min(s.tiles, clusters / s.count));
   s.groups = std::min(s.count, clusters / s.parts);
@@ -1722,8 +1732,8 @@ gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_
                    const gtp::DeviceInfo &dev, cudaStream_t st) {
   fill(a, s, plan, ws);
   const bool tall = rows > cols;
-  // a CTA or a pair a matrix's Gram where one tile holds it: 128 x 128 49 us (a pair 71, phases 99), 512 x 256 96 us (phases
-  // 110), eight of 256 x 2048 157 us (176)
+  // a CTA or a pair a matrix's Gram where one tile holds it: 128 x 128 45 us (a pair 71, phases 99), 512 x 256 80 us (phases
+  // 110), 256 x 256 73 us (106)
   if (plan.m <= 128)
     return tall ? iterate_small<1, true>(a, plan, ws, count, rows, cols, dev, st)
                 : iterate_small<1, false>(a, plan, ws, count, rows, cols, dev, st);

@@ -64,6 +64,19 @@ def test_shapes(R, C, steps):
     assert gtp.gtp_wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("count,R,C", [(1, 256, 300), (1, 200, 129), (2, 129, 200), (1, 70, 300), (3, 300, 70), (1, 60, 500), (1, 500, 60),
+                                       (1, 128, 1000), (2, 1000, 128), (1, 65, 129), (1, 193, 2000), (1, 2000, 193), (1, 256, 256),
+                                       (20, 256, 300), (20, 300, 200), (70 // 2, 128, 300)])
+def test_small_sides(count, R, C):
+    """Where a Gram matrix is one tile: X's tiles whole and in halves, alone and shared."""
+    src = torch.stack([gradient(R, C, seed=k) for k in range(count)])
+    out = torch.full_like(src, float("nan"))
+    gtp.gtp_orthogonalize(src, out, workspace(count, R, C))
+    for k in range(count):
+        check(out[k], src[k])
+    assert gtp.gtp_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("count,R,C", [(3, 100, 200), (5, 200, 100), (2, 513, 512), (64, 8, 24), (3, 700, 600), (7, 300, 520), (9, 264, 264),
                                        (2, 1500, 1040)])
 def test_stacks(count, R, C):
