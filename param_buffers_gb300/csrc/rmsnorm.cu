@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(const __grid_constant
 // row's alignment.  One row a block of TX threads, K elements a thread, or (TX 32) eight rows.  [8001, 1535] bf16 onto an
 // fp32 stream 32.3 us (4.6 TB/s; with four blocks an SM 34.8): bound by the single loads' latency and count.
 template <typename T, typename TS, bool RES, int TX, int K>
-__global__ void __launch_bounds__(TX == 32 ? 256 : TX, RES && TX == 256 ? 5 : 0) norm_elements_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(TX == 32 ? 256 : TX, K == 16 ? 1024 / TX : RES && TX == 256 ? 5 : 0) norm_elements_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][1][32];
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
@@ -211,12 +211,15 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, RES && TX == 256 ? 5 : 0)
     const TS *const res = static_cast<const TS *>(a.residual) + (RES ? row * a.residual_ld + t : 0);
     TS *const sum = static_cast<TS *>(a.sum) + (RES ? row * a.sum_ld + t : 0);
     float h[K], squares[1] = {0.f};
-    TS old[RES ? K : 1];  // all loads before the first store
+    T in[K];
+    TS old[RES ? K : 1];  // all loads, as they lie in memory, before the first store
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      h[k] = live && t + k * TX < cols ? gtp::load1(x + k * TX) : 0.f;
+      in[k] = live && t + k * TX < cols ? x[k * TX] : T(0.f);
       if (RES) old[RES ? k : 0] = live && t + k * TX < cols ? res[k * TX] : TS(0.f);
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) h[k] = float(in[k]);
     if (RES) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -486,8 +489,8 @@ template <typename TX, typename TS, bool RES>
 gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   if (a.cols <= 32 * 8) return launch_elements_of<TX, TS, RES, 32, 8>(a, dev, st);
   if (a.cols <= 256 * 8) return launch_elements_of<TX, TS, RES, 256, 8>(a, dev, st);
-  if (a.cols <= 512 * 8) return launch_elements_of<TX, TS, RES, 512, 8>(a, dev, st);
-  if (a.cols <= 1024 * 8) return launch_elements_of<TX, TS, RES, 1024, 8>(a, dev, st);
+  if (a.cols <= 256 * 16) return launch_elements_of<TX, TS, RES, 256, 16>(a, dev, st);
+  if (a.cols <= 512 * 16) return launch_elements_of<TX, TS, RES, 512, 16>(a, dev, st);
   return launch_elements_of<TX, TS, RES, 1024, 16>(a, dev, st);
 }
 
