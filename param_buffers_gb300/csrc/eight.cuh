@@ -81,6 +81,21 @@ __device__ __forceinline__ void load8_of(const void *p, int f32, int64_t i, floa
     e.get(x);
   }
 }
+// K single elements TX apart of such a vector, those below n: all loads under way together.
+template <int TX, int K>
+__device__ __forceinline__ void load_apart_of(const void *p, int f32, int i, int n, float (&x)[K]) {
+  if (f32) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = i + k * TX < n ? static_cast<const float *>(p)[i + k * TX] : 0.f;
+  } else {
+    __nv_bfloat16 raw[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      raw[k] = i + k * TX < n ? static_cast<const __nv_bfloat16 *>(p)[i + k * TX] : __nv_bfloat16(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = __bfloat162float(raw[k]);
+  }
+}
 __device__ __forceinline__ float load1_of(const void *p, int f32, int64_t i) {
   return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(const __grid_constant
 
 // Rows that start anywhere: the elements TX apart are a thread's, so that a warp's accesses stand side by side whatever a
 // row's alignment.  One row a block of TX threads, K elements a thread, or (TX 32) eight rows.  [8001, 1535] bf16 onto an
-// fp32 stream 32.3 us (4.6 TB/s; with four blocks an SM 34.8): bound by the single loads' latency and count.
+// fp32 stream 27.8 us (5.3 TB/s): bound by the single accesses' latency and count.
 template <typename T, typename TS, bool RES, int TX, int K>
 __global__ void __launch_bounds__(TX == 32 ? 256 : TX, K == 16 ? 1024 / TX : RES && TX == 256 ? 5 : 0) norm_elements_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][1][32];
@@ -235,8 +235,12 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, K == 16 ? 1024 / TX : RES
     if (!a.y || !live) continue;
     const int64_t at = row * a.y_ld + t;
     float w[K];
+    if constexpr (RES) {  // one after the other, in the shadow of the sum's stores: 27.8 us of the case above, together 28.7
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k] = t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
+      for (int k = 0; k < K; ++k) w[k] = t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
+    } else {  // all together: [8192, 8001] bf16 85 us, one after the other 90
+      gtp::load_apart_of<TX>(a.weight, a.weight_f32, t, cols, w);
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (t + k * TX < cols) {
@@ -482,9 +486,10 @@ gtp_status launch_elements_of(const NormArgs &a, const gtp::DeviceInfo &dev, cud
                                 unsigned(std::min<int64_t>(blocks, int64_t(dev.sm_count) * 64)), block, 0, st, "rmsnorm", a);
 }
 
-// As many threads as eight elements each make up a row, so that a row is in registers after one round of loads: blocks of
-// 256 take 28.9 us for [8192, 1000], of 512 59.5; blocks of 512 81 us for [8192, 4095], of 1024 144; rows of 250 by
-// a warp each 6 us, by blocks of 256 26.
+// A row is in registers after one round of loads, eight elements a thread, above 2048 columns sixteen ([8192, 4095] 71 us
+// with 256 threads of sixteen, 80 with 512 of eight; [8192, 8001] 147 with 512 and 183 with 1024): more blocks an SM are
+// worth more than more threads a row ([8192, 1000] 28.9 us with 256 threads, 59.5 with 512; rows of 250 by a warp each 6
+// us, by 256 threads 26).
 template <typename TX, typename TS, bool RES>
 gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   if (a.cols <= 32 * 8) return launch_elements_of<TX, TS, RES, 32, 8>(a, dev, st);

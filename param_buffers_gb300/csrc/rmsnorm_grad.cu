@@ -154,10 +154,8 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX)
   constexpr bool KEEP = K <= 8;  // the weight in registers
   float w[KEEP ? K : 1], dw[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    dw[k] = 0.f;
-    if (KEEP) w[k] = t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
-  }
+  for (int k = 0; k < K; ++k) dw[k] = 0.f;
+  if constexpr (KEEP) gtp::load_apart_of<TX>(a.weight, a.weight_f32, t, cols, w);
   int flip = 0;
   for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < a.rows; r0 += int64_t(gridDim.x) * blockDim.y, flip ^= 1) {
     const int64_t row = r0 + threadIdx.y;
@@ -167,13 +165,27 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX)
     const TS *const s = static_cast<const TS *>(a.sum) + row * a.sum_ld + t;
     const TS *const ds = static_cast<const TS *>(a.dsum) + (a.dsum ? row * a.dsum_ld + t : 0);
     float g[K], n[K], dot[1] = {0.f};
+    TS d[K];  // loaded with the others, not behind the stores
+    if constexpr (KEEP) {  // as they lie in memory: all loads are under way together ([8192, 2047] 38.6 us, converted one by one 55)
+      TD dy_in[K];
+      TS s_in[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) g[k] = live && t + k * TX < cols ? gtp::load1(dy + k * TX) : 0.f;
+      for (int k = 0; k < K; ++k) {
+        const bool there = live && t + k * TX < cols;
+        dy_in[k] = there ? dy[k * TX] : TD(0.f);
+        s_in[k] = there ? s[k * TX] : TS(0.f);
+        d[k] = there && a.dsum ? ds[k * TX] : TS(0.f);
+      }
 #pragma unroll
-    for (int k = 0; k < K; ++k) n[k] = live && t + k * TX < cols ? gtp::load1(s + k * TX) : 0.f;
-    TS d[K];  // with the others, not behind the stores
+      for (int k = 0; k < K; ++k) g[k] = float(dy_in[k]), n[k] = float(s_in[k]);
+    } else {  // sixteen elements: the registers do not hold them twice ([4096, 16001] 287 us, as above 598)
 #pragma unroll
-    for (int k = 0; k < K; ++k) d[k] = live && a.dsum && t + k * TX < cols ? ds[k * TX] : TS(0.f);
+      for (int k = 0; k < K; ++k) g[k] = live && t + k * TX < cols ? gtp::load1(dy + k * TX) : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) n[k] = live && t + k * TX < cols ? gtp::load1(s + k * TX) : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) d[k] = live && a.dsum && t + k * TX < cols ? ds[k * TX] : TS(0.f);
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float wk = KEEP ? w[KEEP ? k : 0] : t + k * TX < cols ? gtp::load1_of(a.weight, a.weight_f32, t + k * TX) : 0.f;
@@ -238,8 +250,8 @@ GradShape grad_shape(int64_t rows, int64_t cols, int sms) {
   return {tx, ty, V, int(std::min<int64_t>((rows + ty - 1) / ty, most))};
 }
 
-// The same for rows that start anywhere: 1024 threads an SM of 64 registers each ([8192, 2047] bf16 54.6 us, 768 of 80
-// registers 59.0), 768 where a warp has a row ([8192, 250] 28.4 us, 1024 of them 33.1).
+// The same for rows that start anywhere: 1024 threads an SM of 64 registers each, 768 where a warp has a row ([8192, 250]
+// 26.1 us).
 GradShape elements_shape(int64_t rows, int64_t cols, int sms) {
   const int tx = cols <= 32 * 8 ? 32 : cols <= 256 * 8 ? 256 : cols <= 512 * 8 ? 512 : 1024, ty = tx == 32 ? 8 : 1;
   const int64_t most = int64_t(sms) * (tx == 32 ? 3 : 1024 / tx);
