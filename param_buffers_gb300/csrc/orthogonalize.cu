@@ -78,43 +78,53 @@ struct FirstX {
   unsigned int *arrived;  // the products' counters, cleared here
 };
 
-__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4 *>(p);
-  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(p);
-  x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+// Elements as they lie in memory, until they are wanted: a load whose value is converted at once is waited for at once.
+template <typename T, bool VEC>
+struct Raw {
+  T v;
+  __device__ __forceinline__ void load(const T *p) { v = *p; }
+  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = float(v); }
+};
+template <>
+struct Raw<float, true> {
+  float4 v;
+  __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+};
+template <>
+struct Raw<__nv_bfloat16, true> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+};
 
 // Item i of matrix k, four consecutive elements of a row with VEC, else one: the matrix's own, or the gradient and the
 // momentum that the step's u comes from.
 template <typename T, bool VEC, bool STEP>
 struct Item {
   static constexpr int E = VEC ? 4 : 1;
-  float g[E], m[STEP ? E : 1];
+  Raw<T, VEC> raw;
+  Raw<float, VEC> old;  // the momentum, of a step
+  float g[E], m[E];
   int row, col;
 
   __device__ __forceinline__ int64_t at(const Source &s, int k) const { return s.offset[k] + int64_t(row) * s.cols + col; }
   __device__ __forceinline__ void load(const Source &s, int k, int i) {
     row = gtp::fast_div(i, s.by_cols);
     col = (i - row * (s.cols / E)) * E;
-    const T *const p = STEP ? static_cast<const T *>(s.grad) + at(s, k) : static_cast<const T *>(s.src) + k * s.plane + row * s.ld + col;
-    if constexpr (VEC) load4(p, g);
-    else g[0] = load1(p);
-    if constexpr (STEP) {
-      if constexpr (VEC) load4(s.momentum + at(s, k), m);
-      else m[0] = s.momentum[at(s, k)];
-    }
+    raw.load(STEP ? static_cast<const T *>(s.grad) + at(s, k) : static_cast<const T *>(s.src) + k * s.plane + row * s.ld + col);
+    if constexpr (STEP) old.load(s.momentum + at(s, k));
   }
   // The values to orthogonalise, in g.  FIRST: the pass that writes the momentum; the second one finds it written and
   // clears the gradient.
   template <bool FIRST>
   __device__ __forceinline__ void finish(const Source &s, int k, float g_scale) {
+    raw.get(g);
     if constexpr (STEP) {
+      old.get(m);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         g[e] *= g_scale;
