@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
   __shared__ __align__(16) uint32_t plane[8][CW];  // columns' amax of each warp, then their codes of each warp's rows
   __shared__ __align__(16) float inv[CW];
   __shared__ float squares[kTileRows][kMostCluster];
+  if (STATS) gtp::ptx::cluster_arrive_relaxed();
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
     const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = warp_sum(s[i]);
+    gtp::ptx::cluster_wait();  // the other blocks run, and have their shared memory
     if (lane < blocks) {
       float *const there = cluster.map_shared_rank(&squares[4 * warp][rank], lane);
 #pragma unroll
