@@ -19,11 +19,14 @@
 //     the square is d^2 + (d_i + d_j) A' + A'^2, and X <- e X + B' X;
 //   - the X of the linear term is fp16 high part + fp16 low part (22 bits); the products read the high part alone.  The
 //     low part is scaled by e where X is nearly orthogonal (B' is small there: what its product leaves out is small),
-//     but by a alone in the first two iterations, where small singular values, on which a + diag(B) acts as far more
-//     than a + B does, still grow threefold each;
+//     but by a alone in the first iterations, where small singular values, on which e acts as far less than a + B does,
+//     still grow a-fold each.  Those that matter in the end are small until the last three (`early_of`);
 //   - A' enters B' with a low part of its own (the square reads the high part).
-// Against fp64, relative error of the result: 2e-4 to 1e-3 over Gaussian, row-scaled and low-rank matrices; without the
-// first two 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.
+// Against fp64, relative error of the result at five steps: 1e-4 to 1e-3 over Gaussian, row-scaled and low-rank matrices
+// (singular values over six decades 1.3e-3, rank 8 and 1e-3 of noise in 16 x 4096 2.6e-3); without the first two choices
+// 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.  Later iterations carry the
+// roundings of earlier ones on by the polynomial's slopes: 3e-3 at ten steps, 1.2e-2 and on a single small matrix 2.3e-2
+// at sixteen.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -279,6 +282,7 @@ static_assert(sizeof(Maps) == 14 * sizeof(CUtensorMap), "prefetched one by one")
 struct Args {
   Phase phase[3];
   int count, steps, m, step;  // step: the last product moves the master instead of writing dst
+  int early;             // the iterations that scale X's low part by a
   unsigned int *arrived;
   float *diag, *e;       // [count][m]
   // powers of two: what makes the accumulators, A', B' and X true values and the reverse
@@ -864,7 +868,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
            ++ph, first = next_first(first, a.phase[kind].units, step), kind = kind == 2 ? 0 : kind + 1) {
       const Phase &p = a.phase[kind];
       if (first >= p.units) continue;
-      const bool last = ph + 1 == phases, early = ph < 6;
+      const bool last = ph + 1 == phases, early = ph < 3 * a.early;
       unsigned int *const counters = a.arrived + ph * a.count;
       const CUtensorMap *const from_hi = kind == kPoly ? &maps.c_gram : &maps.c_hi[(ph / 3) & 1];
       const CUtensorMap *const from_lo = kind == kPoly ? &maps.c_gram_lo : &maps.c_lo;
@@ -1373,7 +1377,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
     };
     for (int k = group; ok && k < s.count; k += s.groups) {
       for (int it = 0; ok && it < a.steps; ++it, ++seq) {
-        const bool early = it < 2, last = it + 1 == a.steps;
+        const bool early = it < a.early, last = it + 1 == a.steps;
         const CUtensorMap *const from = &maps.c_hi[it & 1], *const to = &maps.c_hi[~it & 1];
         // ---- the old X of this group's first chunks, under way while A and B are formed
         if (it > 0) {
@@ -1662,6 +1666,11 @@ gtp_status map_of(CUtensorMap *map, const void *base, int64_t inner, int64_t sta
                              box == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How many iterations scale X's low part by a (see the top): all but the last three.  Singular values spread over four
+// decades, the rounding simulated: ten steps 3.0e-3 with seven and 1.2e-2 with two; Gaussian matrices 2.8e-3 with seven
+// and 3.2e-3 with two.  Two at least: of five steps, three 8.4e-4 and two 6.5e-4 on a Gaussian matrix.
+int early_of(int steps) { return std::max(2, steps - 3); }
+
 // What both kernels need: the iteration's constants and the powers of two that keep every fp16 value in range.
 void fill(Args &a, const Schedule &s, const Plan &plan, char *ws) {
   const int xs = 12, gs = 12;
@@ -1670,7 +1679,7 @@ void fill(Args &a, const Schedule &s, const Plan &plan, char *ws) {
   const auto pow2 = [](int e) { return std::ldexp(1.f, e); };
   a.x_scale = pow2(xs), a.x_inv = pow2(-xs), a.gram_scale = pow2(gs), a.gram_inv = pow2(-gs);
   a.poly_scale = pow2(ps), a.poly_inv = pow2(-ps);
-  a.a = s.a, a.b = s.b, a.c = s.c, a.steps = s.steps, a.m = int(plan.m);
+  a.a = s.a, a.b = s.b, a.c = s.c, a.steps = s.steps, a.early = early_of(s.steps), a.m = int(plan.m);
   a.diag = reinterpret_cast<float *>(ws + plan.diag), a.e = reinterpret_cast<float *>(ws + plan.e);
   a.arrived = reinterpret_cast<unsigned int *>(ws + plan.arrived);
 }
