@@ -805,6 +805,9 @@ gtp_status gtp_embedding_grad_accum(const gtp_embedding_grad_desc *desc, void *w
  * rule of gtp_mxfp8_quantize_rowwise: row_codes [rows, cols] with row_scales [rows, cols / 32], and the
  * columnwise view col_codes [cols, rows] with col_scales [cols, rows / 32]; tiled_scales = 1: both scale
  * arrays in gtp_sf_tile's order (padding bytes not written).  One read of x and residual serves all outputs.
+ * Rows of any finite size: squares that leave fp32's range are summed at the row's own scale.  (rstd itself has fewer
+ * bits where it is a subnormal number, a row above 2^126, and is Inf where it passes fp32, eps = 0 and a row of zeros or
+ * below 2^-128.)
  * Equal calls give equal bits; a call that asks for other outputs may sum a row's squares in another order.
  * Outputs that are NULL are not written; residual and sum are given together, a view's two arrays as well,
  * and with a columnwise view rstd too.  sum may be x or residual exactly (same start, stride and type), y may

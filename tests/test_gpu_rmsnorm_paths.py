@@ -1,5 +1,5 @@
-"""The norm where its kernels change: clusters of every size for the columnwise view.  Tolerances as test_gpu_rmsnorm.py
-derives them."""
+"""The norm where its kernels change: clusters of every size for the columnwise view, rows whose squares leave fp32's range
+on every path.  Tolerances as test_gpu_rmsnorm.py derives them."""
 import pytest
 import torch
 
@@ -29,3 +29,98 @@ def test_clusters_of_one_to_eight(C, xd, rd):
         check_forward(x if rd is None else out, w, 1e-5, rstd, y)
     check_view(row, y, False)
     check_view(col, y.t().contiguous(), False)
+
+
+def sizes(R, C, dt):
+    """Rows from 1e-18 to 3e38, each with a few elements far above its others, and some whose elements differ by decades; every
+    fourth an ordinary one.  Scales are powers of two, so that bf16 holds them."""
+    x = torch.randn(R, C, device=DEV).to(B).float()
+    x[x == 0] = 1.0
+    exponents = [60, 0, 63, 64, 65, 0, 90, 126, 100, 0, -58, 124]
+    for r in range(R):
+        x[r] *= 2.0 ** exponents[r % len(exponents)] / (8 if exponents[r % len(exponents)] > 120 else 1)
+    for r in range(0, R, 5):  # one element holds the row's size
+        x[r, (37 * r) % C] = -(2.0 ** 80)
+    return x.to(dt)
+
+
+def check_any(s, w, eps, rstd, y):
+    from oracle import rmsnorm as N
+    import numpy as np
+    r, ref = N.forward(s.double().cpu().numpy(), w.double().cpu().numpy(), float(np.float32(eps)))
+    got = rstd.double().cpu().numpy()
+    tol = 26 * 2.0 ** -24 * r + 2.0 ** -149  # subnormal ones have a spacing of 2^-149
+    assert np.all(np.abs(got - r) <= tol)
+    assert np.all(r < 2.0 ** 128)
+    tol = (29 * 2.0 ** -24 + 2.0 ** -149 / r[:, None]) * np.abs(ref)
+    if y.dtype == B:
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= tol + 2.0 ** -133)
+
+
+# whole vectors and rows that start anywhere, by one warp and by many; from 1301 on several rows a thread, or more than a block
+RANGES = [(1, 8), (40, 33), (13, 250), (30, 1000), (24, 2047), (14, 4001), (14, 8001), (13, 12345), (300, 72), (14, 4096),
+          (13, 5120), (13, 16384), (1301, 2048), (701, 4096), (1301, 5120), (5003, 512), (13003, 100), (1500, 1001)]
+
+
+@pytest.mark.parametrize("R,C", RANGES)
+@pytest.mark.parametrize("xd,rd", [(B, None), (F, None), (B, B), (F, F)])
+def test_rows_of_any_size(R, C, xd, rd):
+    x, w = sizes(R, C, xd), (1 + 0.2 * torch.randn(C, device=DEV)).to(F)
+    y, rstd = torch.full((R, C), float("nan"), device=DEV), torch.empty(R, device=DEV)
+    kw, s = {}, x
+    if rd is not None:
+        res = x.to(rd) * 0.5
+        s = torch.empty_like(res)
+        kw = dict(residual=res, sum=s)
+    for eps in (1e-5, 0.0, 1e-30):
+        gtp.gtp_rmsnorm(x, w, eps, y=y, rstd=rstd, **kw)
+        if rd is not None:
+            assert torch.equal(s, (x.float() + res.float()).to(rd))
+        check_any(s, w, eps, rstd, y)
+    into = torch.full_like(y, float("nan")).to(xd) if rd is None else y
+    gtp.gtp_rmsnorm(x, w, eps, y=into, **kw)
+    # y in x's place, and the sum in the residual's
+    want = [into.clone(), s.clone()]
+    if rd is not None:
+        kw["sum"] = s = kw["residual"]
+    into = x if rd is None or rd == F else into
+    gtp.gtp_rmsnorm(x, w, eps, y=into, **kw)
+    assert torch.equal(into, want[0]) and (rd is None or torch.equal(s, want[1]))
+
+
+@pytest.mark.parametrize("R,C", [(7, 8), (20, 250), (20, 256), (20, 1000), (20, 2048), (20, 4001), (14, 5120), (14, 9001)])
+def test_small_rows_without_eps(R, C):
+    """Squares below fp32's smallest number; eps so small that it is of the mean's size or the other way round."""
+    w = 1 + 0.2 * torch.randn(C, device=DEV)
+    x = torch.randn(R, C, device=DEV)
+    for r in range(R):
+        x[r] *= 2.0 ** (-50 - 11 * (r % 7))  # down to 2^-116
+    y, rstd = torch.empty_like(x), torch.empty(R, device=DEV)
+    for eps in (0.0, 2.0 ** -100, 2.0 ** -149, 2.0 ** -80):
+        gtp.gtp_rmsnorm(x, w, eps, y=y, rstd=rstd)
+        check_any(x, w, eps, rstd, y)
+
+
+@pytest.mark.parametrize("xd,rd", [(B, B), (F, None), (B, None), (F, F)])
+@pytest.mark.parametrize("R,C", [(32, 32), (64, 256), (64, 768), (64, 2016), (32, 2048), (64, 4096), (32, 8192)])
+def test_views_of_rows_of_any_size(R, C, xd, rd):
+    x, w = sizes(R, C, xd), (1 + 0.2 * torch.randn(C, device=DEV)).to(B)
+    kw, s = {}, x
+    if rd is not None:
+        res = x.to(rd) * 0.5
+        s = torch.empty_like(res)
+        kw = dict(residual=res, sum=s)
+    for eps in (1e-5, 0.0):
+        y, rstd = torch.empty(R, C, device=DEV), torch.empty(R, device=DEV)
+        row, col = views(R, C, False)
+        gtp.gtp_rmsnorm(x, w, eps, y=y, rstd=rstd, row=row, col=col, **kw)
+        check_any(s, w, eps, rstd, y)
+        check_view(row, y, False)
+        check_view(col, y.t().contiguous(), False)
+        # with the sum in x's or the residual's place
+        if rd is not None:
+            a, b, y2 = x.clone(), res.clone(), torch.empty_like(y)
+            into = a if xd == rd else b
+            gtp.gtp_rmsnorm(a, w, eps, residual=b, sum=into, y=y2, rstd=rstd, row=row, col=col)
+            assert torch.equal(into, s) and torch.equal(y2, y)
