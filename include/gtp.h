@@ -871,8 +871,8 @@ gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_
  * at up to 5 steps (to 3e-3 where a few directions hold nearly all of the matrix), 3e-3 at 10, to 3e-2 at 16.  What a
  * matrix has below 2^-22 of its norm is rounding, which every iteration multiplies by a like any small singular value:
  * 1e-2 of the result at 10 steps on a matrix of lower rank, as large as the result at 16.  The sum of squares
- * is taken in fp32 by sixteens and in fp64 across: where it is not finite, the result is NaN, and elements below
- * 1e-22 or so count as 0.  A fixed order: equal calls give equal bits.
+ * is taken in fp32 by sixteens and in fp64 across, in fp64 alone where fp32 does not hold it: elements of any finite
+ * size; a matrix with NaN or Inf becomes NaN.  A fixed order: equal calls give equal bits.
  * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane
  * (elements), element-aligned; dst likewise, and may be src or overlap it (src is read before dst is
  * written).  1 <= steps <= 16; coefficients (host) that let a singular value of [0, 1] grow past 2 are

@@ -185,14 +185,24 @@ __global__ void __launch_bounds__(kPassThreads)
         for (int e = 0; e < Item<T, VEC, STEP>::E; ++e) sum = fmaf(x[j].g[e], x[j].g[e], sum);
       }
     }
-    total += double(sum);
+    if (sum >= 0x1p-100f && sum <= 0x1p120f) {
+      total += double(sum);
+    } else {  // squares that fp32 does not hold, or not in full: each one in fp64, but for zeros
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j)
+        if (i0 + j * step < s.items) {
+#pragma unroll
+          for (int e = 0; e < Item<T, VEC, STEP>::E; ++e)
+            if (x[j].g[e] != 0.f) total = fma(double(x[j].g[e]), double(x[j].g[e]), total);
+        }
+    }
   }
   total = block_sum(total);
   if (threadIdx.x == 0) f.part[blockIdx.y * gridDim.x + blockIdx.x] = total;
 }
 
-// X = G / |G|_F as fp16 high and low parts, times a power of two.  A matrix of zeros stays zero; one whose squares'
-// sum is not finite becomes NaN.
+// X = G / |G|_F as fp16 high and low parts, times a power of two.  A matrix of zeros stays zero; one with NaN or Inf
+// becomes NaN.
 template <typename T, bool VEC, bool STEP>
 __global__ void __launch_bounds__(kPassThreads)
     first_x_kernel(const __grid_constant__ Source s, const __grid_constant__ FirstX f) {
@@ -202,7 +212,10 @@ __global__ void __launch_bounds__(kPassThreads)
   double total = 0;
   for (int p = threadIdx.x; p < f.parts; p += kPassThreads) total += f.part[blockIdx.y * f.parts + p];
   total = block_sum(total);
-  const float r = total == 0 ? 0.f : isfinite(total) ? float(double(f.xscale) / sqrt(total)) : nanf("");
+  // 1 / |G|: a power of two that its elements can take first, exactly, and what is left, where fp32 does not hold it in one
+  const double inv = total == 0 ? 0. : isfinite(total) ? double(f.xscale) / sqrt(total) : double(nanf(""));
+  const float p = inv > 0x1p100 ? 0x1p100f : inv < 0x1p-100 ? 0x1p-64f : 1.f;
+  const float r = float(inv * (inv > 0x1p100 ? 0x1p-100 : inv < 0x1p-100 ? 0x1p64 : 1.));
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < kCounters; i += kPassThreads) f.arrived[i] = 0;
   const int step = int(gridDim.x) * kPassThreads, me = int(blockIdx.x) * kPassThreads + int(threadIdx.x);
@@ -226,7 +239,7 @@ __global__ void __launch_bounds__(kPassThreads)
       __half hi[E], lo[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float v = x[j].g[e] * r;
+        const float v = x[j].g[e] * p * r;
         hi[e] = __float2half_rn(v);
         lo[e] = __float2half_rn(v - __half2float(hi[e]));
       }
