@@ -862,7 +862,7 @@ extern "C" gtp_status gtp_embedding(const gtp_embedding_desc *d, gtp_stream stre
 }
 
 extern "C" int64_t gtp_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols) {
-  if (tokens < 0 || rows < 0 || cols < 0 || tokens > kMaxDim || rows > kMaxDim || cols > kMaxDim) return -1;
+  if (check_sizes(tokens, 0, rows, cols, 0)) return -1;
   if (tokens == 0 || rows == 0 || cols == 0) return 0;
   return grad_plan(tokens, rows, cols).bytes;
 }
