@@ -1,10 +1,11 @@
-"""The norm where its kernels change: clusters of every size for the columnwise view, rows whose squares leave fp32's range
-on every path.  Tolerances as test_gpu_rmsnorm.py derives them."""
+"""The norm where its kernels change: clusters of every size for the columnwise view, more rows than the machine has blocks
+(several a thread at once, or one after the other), rows whose squares leave fp32's range on every path.  Tolerances as
+test_gpu_rmsnorm.py derives them."""
 import pytest
 import torch
 
 import param_buffers_gb300 as gtp
-from test_gpu_rmsnorm import B, DEV, F, check_forward, check_view, matrix, views
+from test_gpu_rmsnorm import B, DEV, F, check_forward, check_view, forward, matrix, test_gradient as gradient, views
 
 pytestmark = pytest.mark.gpu
 
@@ -29,6 +30,50 @@ def test_clusters_of_one_to_eight(C, xd, rd):
         check_forward(x if rd is None else out, w, 1e-5, rstd, y)
     check_view(row, y, False)
     check_view(col, y.t().contiguous(), False)
+
+
+@pytest.mark.parametrize("xd,rd", [(B, None), (F, None), (B, B), (B, F), (F, F), (F, B)])
+@pytest.mark.parametrize("R,C", [(8191, 2048), (1301, 4096), (20003, 256), (5003, 520), (1303, 5120), (700, 16384), (20003, 250),
+                                 (30001, 31), (20003, 1001)])
+def test_more_rows_than_blocks(R, C, xd, rd):
+    """Borders of the dispatch at 152 multiprocessors: 1216 rows of 2048 columns, 608 of 4096, 9728 of 256, 19456 in eights."""
+    forward(R, C, xd, rd, B, B)
+    forward(R, C, xd, rd, F, F, pad=8)
+
+
+@pytest.mark.parametrize("xd,rd", [(B, B), (F, None), (F, F)])
+@pytest.mark.parametrize("R,C", [(1301, 2048), (701, 4096), (10001, 256), (1300, 5120), (333, 96)])
+def test_rowwise_view_alone(R, C, xd, rd):
+    x, w = matrix(R, C, xd), (1 + 0.2 * torch.randn(C, device=DEV)).to(B)
+    x[R // 2] = 0
+    x[R - 1, C - 1] = float("inf")
+    kw = {} if rd is None else dict(residual=matrix(R, C, rd, 3.0), sum=torch.empty(R, C, dtype=rd, device=DEV))
+    y, row = torch.empty(R, C, device=DEV), views(32 * (R // 32 + 1), C, False)[0]
+    row = tuple(t[:R] for t in row)
+    gtp.gtp_rmsnorm(x, w, 1e-5, y=y, row=row, **kw)
+    check_view(row, y, False)
+    again = tuple(torch.empty_like(t) for t in row)
+    gtp.gtp_rmsnorm(x, w, 1e-5, row=again, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(row, again))
+
+
+@pytest.mark.parametrize("xd,rd", [(B, B), (F, F)])
+@pytest.mark.parametrize("R,C", [(1312, 4096), (2528, 2048)])
+def test_views_of_many_rows(R, C, xd, rd):
+    x, res, w = matrix(R, C, xd), matrix(R, C, rd, 3.0), (1 + 0.2 * torch.randn(C, device=DEV)).to(F)
+    y, rstd, out = torch.empty(R, C, device=DEV), torch.empty(R, device=DEV), torch.empty(R, C, dtype=rd, device=DEV)
+    row, col = views(R, C, True)
+    gtp.gtp_rmsnorm(x, w, 1e-5, residual=res, sum=out, y=y, rstd=rstd, row=row, col=col)
+    check_forward(out, w, 1e-5, rstd, y)
+    check_view(row, y, True)
+    check_view(col, y.t().contiguous(), True)
+
+
+@pytest.mark.parametrize("dd,sd", [(B, B), (F, F), (B, F)])
+@pytest.mark.parametrize("R,C", [(8191, 2048), (1001, 4096), (650, 8192), (611, 5120), (401, 16384), (3001, 12345), (1500, 5001), (1301, 2047),
+                                 (5003, 31)])
+def test_gradient_of_more_rows_than_blocks(R, C, dd, sd):
+    gradient(R, C, dd, sd, F)
 
 
 def sizes(R, C, dt):
