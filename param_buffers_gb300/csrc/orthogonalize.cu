@@ -148,15 +148,16 @@ struct Item {
   }
 };
 
+// The sum over the block, in thread 0 (fp64 is slow here: nothing of it in more threads than have to).
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double sums[32];
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0;
-  for (int w = 0; w < int(blockDim.x >> 5); ++w) v += sums[w];
+  if (threadIdx.x == 0)
+    for (int w = 0; w < int(blockDim.x >> 5); ++w) v += sums[w];
   return v;
 }
 
@@ -187,14 +188,17 @@ __global__ void __launch_bounds__(kPassThreads)
     }
     if (sum >= 0x1p-100f && sum <= 0x1p120f) {
       total += double(sum);
-    } else {  // squares that fp32 does not hold, or not in full: each one in fp64, but for zeros
+    } else {  // squares that fp32 does not hold, or not in full: of elements below 2^-50 and above 2^57 times a power of two
+      const float by = sum < 1.f ? 0x1p100f : 0x1p-72f;
+      const double back = sum < 1.f ? 0x1p-200 : 0x1p144;
+      sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kFlight; ++j)
         if (i0 + j * step < s.items) {
 #pragma unroll
-          for (int e = 0; e < Item<T, VEC, STEP>::E; ++e)
-            if (x[j].g[e] != 0.f) total = fma(double(x[j].g[e]), double(x[j].g[e]), total);
+          for (int e = 0; e < Item<T, VEC, STEP>::E; ++e) sum = fmaf(x[j].g[e] * by, x[j].g[e] * by, sum);
         }
+      total = fma(double(sum), back, total);
     }
   }
   total = block_sum(total);
@@ -212,10 +216,15 @@ __global__ void __launch_bounds__(kPassThreads)
   double total = 0;
   for (int p = threadIdx.x; p < f.parts; p += kPassThreads) total += f.part[blockIdx.y * f.parts + p];
   total = block_sum(total);
-  // 1 / |G|: a power of two that its elements can take first, exactly, and what is left, where fp32 does not hold it in one
-  const double inv = total == 0 ? 0. : isfinite(total) ? double(f.xscale) / sqrt(total) : double(nanf(""));
-  const float p = inv > 0x1p100 ? 0x1p100f : inv < 0x1p-100 ? 0x1p-64f : 1.f;
-  const float r = float(inv * (inv > 0x1p100 ? 0x1p-100 : inv < 0x1p-100 ? 0x1p64 : 1.));
+  __shared__ float scale[2];  // 1 / |G|: a power of two that its elements take first, exactly, and what fp32 then holds
+  if (threadIdx.x == 0) {
+    const double inv = total == 0 ? 0. : isfinite(total) ? double(f.xscale) / sqrt(total) : double(nanf(""));
+    const bool large = inv > 0x1p100, small = inv < 0x1p-100;
+    scale[0] = large ? 0x1p100f : small ? 0x1p-64f : 1.f;
+    scale[1] = float(inv * (large ? 0x1p-100 : small ? 0x1p64 : 1.));
+  }
+  __syncthreads();
+  const float p = scale[0], r = scale[1];
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < kCounters; i += kPassThreads) f.arrived[i] = 0;
   const int step = int(gridDim.x) * kPassThreads, me = int(blockIdx.x) * kPassThreads + int(threadIdx.x);
