@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX)
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int cols = int(a.cols), t = threadIdx.x;
-  constexpr bool KEEP = K <= 8;  // the weight in registers
+  // the weight in registers, and elements as they lie in memory, so that all loads are under way together ([8192, 2047] bf16 38.5
+  // us, converted one by one 55); of sixteen fp32 elements the registers do not hold that ([4096, 16001] all fp32 336 us, so 384;
+  // bf16 239, one by one 287)
+  constexpr bool KEEP = K <= 8 || sizeof(TD) + 2 * sizeof(TS) < 12;
   float w[KEEP ? K : 1], dw[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) dw[k] = 0.f;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX)
     const TS *const ds = static_cast<const TS *>(a.dsum) + (a.dsum ? row * a.dsum_ld + t : 0);
     float g[K], n[K], dot[1] = {0.f};
     TS d[K];  // loaded with the others, not behind the stores
-    if constexpr (KEEP) {  // as they lie in memory: all loads are under way together ([8192, 2047] 38.6 us, converted one by one 55)
+    if constexpr (KEEP) {
       TD dy_in[K];
       TS s_in[K];
 #pragma unroll
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(TX == 32 ? 256 : TX, TX == 32 ? 3 : 1024 / TX)
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) g[k] = float(dy_in[k]), n[k] = float(s_in[k]);
-    } else {  // sixteen elements: the registers do not hold them twice ([4096, 16001] 287 us, as above 598)
+    } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) g[k] = live && t + k * TX < cols ? gtp::load1(dy + k * TX) : 0.f;
 #pragma unroll
@@ -235,8 +238,8 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *part, in
 
 // --------------------------------------------------------------------------- host
 
-// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four: [8192, 4096] bf16 54.1 and 57.7
-// us, [8192, 2048] 29.4 and 36.2) and blocks: those that run at once, 512 threads an SM (128 registers each).  One rule for
+// Threads a row, rows a block, groups of eight a thread (one up to 4096 columns, else four: [8192, 4096] bf16 53.9 and 57.4
+// us, [8192, 2048] 29.2 and 36.2) and blocks: those that run at once, 512 threads an SM (128 registers each).  One rule for
 // the workspace's size and the launch.
 struct GradShape {
   int tx, ty, V, grid;
@@ -251,7 +254,7 @@ GradShape grad_shape(int64_t rows, int64_t cols, int sms) {
 }
 
 // The same for rows that start anywhere: 1024 threads an SM of 64 registers each, 768 where a warp has a row ([8192, 250]
-// 26.1 us).
+// 26.4 us).
 GradShape elements_shape(int64_t rows, int64_t cols, int sms) {
   const int tx = cols <= 32 * 8 ? 32 : cols <= 256 * 8 ? 256 : cols <= 512 * 8 ? 512 : 1024, ty = tx == 32 ? 8 : 1;
   const int64_t most = int64_t(sms) * (tx == 32 ? 3 : 1024 / tx);
