@@ -733,13 +733,14 @@ gtp_status launch_lookup(const LookupArgs &a, const gtp::DeviceInfo &dev, cudaSt
   const dim3 block = block_of(a.cols, 1);
   const int64_t gx = (a.cols + 8 * block.x - 1) / (8 * block.x), fill = std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / gx);
   const int64_t rows = (a.tokens + block.y - 1) / block.y;  // of blocks, at a token a thread
-  // tokens a thread: four of whole vectors ([8192, 2048] bf16 12.8 us, 5.2 TB/s; one at a time 15.3), two of single elements
-  // ([8192, 2047] 25.9 us, four 26.9); few tokens one at a time, spread over the machine (512 of them 2.45 us and 2.60)
-  const bool many = rows > fill;
-  const int n = many ? (vec ? 4 : 2) : 1;
+  // tokens a thread: four of whole vectors ([8192, 2048] bf16 12.8 us, 5.2 TB/s; one at a time 15.2), one of single elements
+  // ([8192, 2047] 25.2 us, two 25.5, four 26.9; into fp32 26.4 and 27.5); few tokens one at a time, spread over the machine
+  const bool many = vec && rows > fill;
+  const int n = many ? 4 : 1;
   const dim3 grid(unsigned(gx), unsigned(std::min<int64_t>((rows + n - 1) / n, 65535)));
-  const auto kernel = many ? (vec ? embedding_kernel<TI, TO, true, 4> : embedding_kernel<TI, TO, false, 2>)
-                           : (vec ? embedding_kernel<TI, TO, true, 1> : embedding_kernel<TI, TO, false, 1>);
+  const auto kernel = many  ? embedding_kernel<TI, TO, true, 4>
+                      : vec ? embedding_kernel<TI, TO, true, 1>
+                            : embedding_kernel<TI, TO, false, 1>;
   return gtp::launch_overlapped(kernel, grid, block, 0, st, "embedding", a);
 }
 
