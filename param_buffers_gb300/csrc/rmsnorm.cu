@@ -7,8 +7,8 @@
 //
 //   s = x + residual (rounded to the stream's type; s = x without one)     r = 1 / sqrt(mean s^2 + eps) per row
 //   y = (s r) w                                                             views: MXFP8 of the fp32 y, one rounding
-// Sums in fp32.  Everything is bound by the bytes: one pass over them, a row's elements staying in registers between
-// the sum of squares and the outputs.
+// Sums in fp32.  One pass over the bytes, a row's elements staying in registers between the sum of squares and the outputs:
+// long calls on whole vectors are bound by the bytes, the others by latency as their kernels say.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -415,11 +415,15 @@ __device__ __noinline__ void redo_tile(const NormArgs &a, const float (&squares)
 // 32 bytes.  STATS false: r is read, only the columnwise view is written (rows too wide for a cluster; the sum, r and
 // what goes by rows are norm_kernel's).
 //
-// Both views of [8192, 2048] bf16 with a bf16 residual: 35.6 us, 3.8 TB/s of x, the residual, the sum and the views (37.1
+// Both views of [8192, 2048] bf16 with a bf16 residual: 35.5 us, 3.8 TB/s of x, the residual, the sum and the views (37.1
 // with the sum written before the cluster's exchange).  Bound by latency: load, exchange and two rounds through shared
-// memory follow one another in a block, and four blocks of 64 registers a thread are an SM's (three 39.4 us, five 48.5;
-// 512 columns a block, two of them an SM, 42.3).
+// memory follow one another in a block, and four blocks of 64 registers a thread are an SM's (three 38.1 us, five 48.1).
 constexpr int kTileThreads = 256, kTileRows = 32, kMostCluster = 8;
+
+// A barrier of the cluster in two halves and without an ordering of memory, by warps whose lanes may have parted: after the
+// wait every block of the cluster has come to its arrive, so that its shared memory may be written to.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <typename TX, typename TS, bool RES, bool STATS>
 __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid_constant__ NormArgs a) {
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
   __shared__ __align__(16) float inv[CW];
   __shared__ float squares[kTileRows][kMostCluster];
   __shared__ int odd;  // a row is not in range
-  if (STATS) gtp::ptx::cluster_arrive_relaxed();
+  if (STATS) cluster_arrive_relaxed();
   gtp::ptx::allow_dependents();
   gtp::ptx::wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) norm_tile_kernel(const __grid
     const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = warp_sum(s[i]);
-    gtp::ptx::cluster_wait();  // the other blocks run, and have their shared memory
+    cluster_wait();  // the other blocks run, and have their shared memory
     if (lane < blocks) {
       float *const there = cluster.map_shared_rank(&squares[4 * warp][rank], lane);
 #pragma unroll
@@ -610,8 +614,8 @@ __global__ void __launch_bounds__(256)
 
 // --------------------------------------------------------------------------- host
 
-// Threads a row, rows a block, groups of eight a thread: one group up to 4096 columns ([8192, 4096] bf16 42.8 us, with four
-// a thread 46.6; [8192, 2048] 22.5 and 24.9), else four.
+// Threads a row, rows a block, groups of eight a thread: one group up to 4096 columns ([8192, 4096] bf16 42.6 us, with four
+// a thread 45.0; [8192, 2048] 22.7 and 23.5), else four ([8192, 5120] 55.8, 8192 columns 85.8).
 struct RowShape {
   int tx, ty, V;
 };
@@ -628,8 +632,8 @@ gtp_status launch_rows(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream
   const RowShape s = row_shape(a.cols);
   const dim3 block(s.tx, s.ty);
   const int64_t blocks = (a.rows + s.ty - 1) / s.ty, most = int64_t(dev.sm_count) * std::max(1, 2048 / (s.tx * s.ty));
-  // rows a time: four of bf16 ([8192, 2048] with a residual 22.5 us, one at a time 26.9), one where a row has more bytes (all
-  // fp32 36.5 us, two at a time 39.5); few rows: one, spread over the machine
+  // rows a time: four of bf16 ([8192, 2048] with a residual 22.7 us, one at a time 26.8), one where a row has more bytes (all
+  // fp32 36.3 us, two at a time 40.0); few rows: one, spread over the machine
   constexpr int MANY = sizeof(TX) + (RES ? sizeof(TS) : 0) > 4 ? 1 : 4;
   if (MANY > 1 && s.V == 1 && blocks > most)
     return gtp::launch_overlapped(norm_kernel<TX, TS, RES, 1, MANY>, unsigned((blocks + MANY - 1) / MANY), block, 0, st, "rmsnorm", a);
@@ -645,10 +649,10 @@ gtp_status launch_elements_of(const NormArgs &a, const gtp::DeviceInfo &dev, cud
                                 unsigned(std::min<int64_t>(blocks, int64_t(dev.sm_count) * 64)), block, 0, st, "rmsnorm", a);
 }
 
-// A row is in registers after one round of loads, eight elements a thread, above 2048 columns sixteen ([8192, 4095] 71 us
-// with 256 threads of sixteen, 80 with 512 of eight; [8192, 8001] 147 with 512 and 183 with 1024): more blocks an SM are
-// worth more than more threads a row ([8192, 1000] 28.9 us with 256 threads, 59.5 with 512; rows of 250 by a warp each 6
-// us, by 256 threads 26).
+// A row is in registers after one round of loads, eight elements a thread, above 2048 columns sixteen ([8192, 4095] 65 us
+// with 256 threads of sixteen, 73 with 512 of eight; [8192, 8001] 132 with 512 and 194 with 1024): more blocks an SM are
+// worth more than more threads a row ([8192, 1000] 26.2 us with 256 threads, 59.4 with 512; rows of 250 by a warp each 6
+// us, by 256 threads 25).
 template <typename TX, typename TS, bool RES>
 gtp_status launch_elements(const NormArgs &a, const gtp::DeviceInfo &dev, cudaStream_t st) {
   if (a.cols <= 32 * 8) return launch_elements_of<TX, TS, RES, 32, 8>(a, dev, st);
@@ -686,9 +690,9 @@ gtp_status launch_tiles_of(const NormArgs &a, cudaStream_t st) {
 
 template <typename TX, typename TS, bool RES>
 gtp_status launch_tiles(NormArgs a, const gtp::DeviceInfo &dev, cudaStream_t st) {
-  // one launch where a cluster holds a row, two above: at [8192, 4096] 67 us (a cluster of eight blocks of 512 columns
-  // 76 to 79), at [8192, 2048] 35.2 against 35.3 with a bf16 residual, 47.2 against 43.0 with an fp32 one, and at
-  // [256, 2048] 6.3 against 5.0
+  // one launch where a cluster holds a row: [8192, 2048] with a bf16 residual 35.3 us and by two launches 35.4, with an fp32 one
+  // 44.3 and 47.4, without 29.1 and 32.3; [256, 2048] 5.2 and 6.4.  Two above: [8192, 4096] 67.4, where a cluster of eight
+  // blocks of 512 columns took 76 to 79
   if (a.cols <= 256 * kMostCluster) return launch_tiles_of<TX, TS, RES, true>(a, st);
   uint8_t *const codes = a.col_codes;
   a.col_codes = nullptr;

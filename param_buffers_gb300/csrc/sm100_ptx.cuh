@@ -259,11 +259,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The same in two halves and without an ordering of memory, by warps whose lanes may have parted: after the wait every
-// CTA of the cluster has come to its arrive, so that its shared memory may be written to.
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
 // The shared::cluster address of `p` (a local shared-memory object) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t mapa_shared(const void *p, uint32_t rank) {
   uint32_t r;
