@@ -765,9 +765,9 @@ gtp_status gtp_dropout_grad(const void *dout, gtp_dtype dout_dt, int64_t dout_ld
  *   out[t] = scale * table[ids[t] - first_row]  where that row is in [0, rows), else 0 (another shard's
  *   token, or none's: any id is allowed),  one rounding to out's type;
  *   grad_data[grad_offset : +rows*cols].view(rows, cols)[ids[t] - first_row] += scale * dout[t].
- * A row's tokens are sorted and summed in fp32 in an order that depends on the ids alone, and added to the
- * buffer (F32 or BF16, any view offset) in one rounding: equal calls give equal bits.  The addition may take
- * values of F32 below 2^-126 as 0.  Rows without a token are neither read nor written.
+ * A row's tokens are sorted and summed in fp32 in an order that depends on the ids alone, and the sum times the
+ * scale is added to the buffer (any view offset; F32: the product and the addition rounded each, BF16: the two in
+ * one, then to bf16): equal calls give equal bits.  The addition may take values of F32 below 2^-126 as 0.  Rows without a token are neither read nor written.
  * ids: device [tokens], int32 (ids64 = 0) or int64, aligned to their size.  table [rows, cols], out and dout
  * [tokens, cols]: F32 or BF16, row strides table_ld, out_ld, dout_ld (elements, >= cols), element-aligned.
  * No output overlaps an input (GTP_E_ARG).  workspace: device, 32-byte aligned, at least
@@ -875,8 +875,8 @@ gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_
  * size; a matrix with NaN or Inf becomes NaN.  A fixed order: equal calls give equal bits.
  * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane
  * (elements), element-aligned; dst likewise, and may be src or overlap it (src is read before dst is
- * written).  1 <= steps <= 16; coefficients (host) that let a singular value of [0, 1] grow past 2 are
- * refused (GTP_E_ARG).  count <= 64 (GTP_E_CAPACITY), rows and cols <= 65536, rows * cols < 2^31
+ * written).  1 <= steps <= 16; coefficients (host) that let a singular value of [0, 1] grow past 2
+ * before the last step are refused (GTP_E_ARG).  count <= 64 (GTP_E_CAPACITY), rows and cols <= 65536, rows * cols < 2^31
  * (GTP_E_SHAPE).  workspace: device, 256-byte aligned, gtp_orthogonalize_workspace_bytes(count, rows, cols)
  * bytes (-1 for sizes that the call refuses), apart from src and dst; its contents are not needed afterwards,
  * and calls that may overlap on the GPU need one each. */
@@ -889,7 +889,8 @@ gtp_status gtp_orthogonalize(const void *src, gtp_dtype src_dt, int64_t src_ld, 
 
 typedef struct {
   float lr, momentum, weight_decay;  /* lr, weight_decay >= 0; 0 <= momentum < 1                    */
-  float scale;                       /* of the update, say 0.2 sqrt(max(rows, cols))                */
+  float scale;                       /* of the update, say 0.2 sqrt(max(rows, cols)); lr times it    */
+                                     /* and lr times weight_decay finite in fp32                    */
   float grad_factor;                 /* host factor of the gradient (a bucket's scaling)            */
   float coefficients[3];
   int32_t steps;

@@ -1203,7 +1203,7 @@ __global__ void __cluster_dims__(G, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   unsigned int *err = &g_ortho_wait_timeouts;
   // A CTA that has a whole matrix reads nobody else's X: its last warp of an iteration starts the next one, without a round
-  // through the counters (84 x 26 33.7 us, with it 37.4).
+  // through the counters (84 x 26 32.8 us, with it 36.5).
   const bool alone = G == 1 && s.parts == 1;
   // seq counts this CTA's iterations over all its matrices; `ready` holds the last one that may start
   if (warp == 0) {
@@ -1662,9 +1662,9 @@ gtp_status launch_together(void (*kernel)(KArgs...), int ctas, int smem, cudaStr
 }
 
 // Tiles of 256 x 256 in whole waves of the pairs, the rest as halves where those fit one wave or less time: a half-wide
-// unit takes 0.55 of a whole one's time (a call of 1536 x 2048 227 us; whole tiles alone 279, halves alone 231; 8192 x 2048
-// 538, 630, 593; 777 x 1111 167, 231, 165).  Where the other matrices' tiles fill a wave and a half, their phases go into
-// one another and whole tiles alone are better (eight of 1536 x 2048 668 us, with halves 679).
+// unit takes 0.55 of a whole one's time (a call of 1536 x 2048 217 us; whole tiles alone 268, halves alone 226; 8192 x 2048
+// 537, 617, 596; 777 x 1111 155, 218, 155).  Where the other matrices' tiles fill a wave and a half, their phases go into
+// one another and whole tiles alone are better (eight of 1536 x 2048 682 us, with halves 690).
 void shape(Phase &p, int64_t count, bool symmetric, int64_t k, int pairs) {
   p.tiles_m = (p.m_dim + BMP - 1) / BMP, p.tiles_n = (p.n_dim + BN - 1) / BN;
   p.each = symmetric ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
@@ -1751,7 +1751,7 @@ gtp_status iterate_small(const Args &a, const Plan &plan, char *ws, int64_t coun
   s.count = int(count), s.rows = int(rows), s.cols = int(cols), s.stand = int(plan.rows);
   s.tiles = int((plan.n + Small<G>::N - 1) / Small<G>::N);
   // tiles half as wide where there are CTAs for twice as many and the second halves exist: finishing a tile is the
-  // longest part of an iteration (512 x 256 80 us, whole tiles 94; 128 x 512 52 and 57; eight of 256 x 512 88 and 102)
+  // longest part of an iteration (512 x 256 80 us, whole tiles 93; 128 x 512 50 and 57; eight of 256 x 512 84 and 99)
   s.half = (G == 2 || s.tiles > 1) && 2 * s.tiles * s.count <= clusters && (!TALL || plan.m > 64);
   if (s.half) s.tiles = TALL ? 2 * s.tiles : int((plan.n + Small<G>::N / 2 - 1) / (Small<G>::N / 2));
   s.gram_blocks = int((plan.n + BK - 1) / BK), s.poly_blocks = int((plan.m + BK - 1) / BK);
@@ -1773,8 +1773,8 @@ gtp_status iterate(Args a, const Schedule &s, const Plan &plan, char *ws, int64_
                    const gtp::DeviceInfo &dev, cudaStream_t st) {
   fill(a, s, plan, ws);
   const bool tall = rows > cols;
-  // a CTA or a pair a matrix's Gram where one tile holds it: 128 x 128 45 us (a pair 71, phases 99), 512 x 256 80 us (phases
-  // 110), 256 x 256 73 us (106)
+  // a CTA or a pair a matrix's Gram where one tile holds it: 128 x 128 45 us (a pair 61, phases 89), 512 x 256 80 us (phases
+  // 103), 256 x 256 71 us (97)
   if (plan.m <= 128)
     return tall ? iterate_small<1, true>(a, plan, ws, count, rows, cols, dev, st)
                 : iterate_small<1, false>(a, plan, ws, count, rows, cols, dev, st);
@@ -1909,6 +1909,9 @@ extern "C" gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *m
   if (!(h->lr >= 0.f) || !(h->weight_decay >= 0.f) || !(h->momentum >= 0.f && h->momentum < 1.f) || !std::isfinite(h->lr) ||
       !std::isfinite(h->weight_decay) || !std::isfinite(h->scale) || !std::isfinite(h->grad_factor))
     return gtp::fail(GTP_E_ARG, "lr, weight_decay >= 0, momentum in [0, 1), scale and grad_factor finite");
+  const float keep = float(1.0 - double(h->lr) * double(h->weight_decay)), rate = float(double(h->lr) * double(h->scale));
+  if (!std::isfinite(keep) || !std::isfinite(rate))
+    return gtp::fail(GTP_E_ARG, "lr * weight_decay or lr * scale passes fp32");
   if (h->reserved) return gtp::fail(GTP_E_ARG, "reserved must be 0");
   if ((h->nesterov & ~1) || (h->zero_grad_after & ~1)) return gtp::fail(GTP_E_ARG, "nesterov and zero_grad_after are 0 or 1");
   if (!aligned(h->grad_scale, 4)) return gtp::fail(GTP_E_ALIGN, "grad_scale must be 4-byte aligned");
@@ -1950,7 +1953,7 @@ extern "C" gtp_status gtp_muon_step(void *grad_data, gtp_dtype grad_dt, float *m
   source.mu = h->momentum, source.factor = h->grad_factor, source.nesterov = h->nesterov, source.zero_grad = h->zero_grad_after;
   Args a = {};
   a.step = 1, a.master = master, a.param = static_cast<__nv_bfloat16 *>(param_data);
-  a.keep = float(1.0 - double(h->lr) * double(h->weight_decay)), a.rate = float(double(h->lr) * double(h->scale));
+  a.keep = keep, a.rate = rate;
   for (int64_t k = 0; k < count; ++k) source.offset[k] = a.offset[k] = offsets[k];
   vec = vec && aligned(grad_data, 4 * gs) && aligned(momentum, 16);
   if (gtp_status s = first<true>(source, grad_dt == GTP_F32, vec, first_x(plan, ws), count, rows, cols, dev, st)) return s;

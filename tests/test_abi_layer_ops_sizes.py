@@ -1,4 +1,5 @@
-"""The embedding gradient's workspace size answers -1 wherever the call refuses the sizes (host only)."""
+"""The embedding gradient's workspace size answers -1 wherever the call refuses the sizes; a step whose rates fp32 does not hold is
+refused (host only)."""
 import ctypes as C
 
 import pytest
@@ -26,3 +27,21 @@ def test_refused_sizes(tokens, rows, cols):
 def test_sizes_at_the_limit(tokens, rows, cols):
     need = abi.load().gtp_embedding_grad_workspace_bytes(tokens, rows, cols)
     assert need > 0 and call(tokens, rows, cols, need - 1) == abi.GTP_E_CAPACITY
+
+
+def step(**h):
+    """A step whose hyper-parameters pass every check but, it may be, the last; its workspace is too small."""
+    p = abi.gtp_muon_hparams(lr=1e-3, momentum=0.9, weight_decay=0.1, scale=1.0, grad_factor=1.0, coefficients=(3.4445, -4.7750, 2.0315),
+                             steps=5, nesterov=1, zero_grad_after=1)
+    for k, v in h.items():
+        setattr(p, k, v)
+    at = [1 << (40 + k) for k in range(5)]
+    return abi.load().gtp_muon_step(at[0], abi.GTP_F32, at[1], at[2], at[3], 64, (C.c_int64 * 1)(0), 1, 8, 8, C.byref(p), at[4], 8, None)
+
+
+@pytest.mark.parametrize("h,status", [(dict(lr=1e20, scale=1e20), abi.GTP_E_ARG), (dict(lr=1e20, scale=-1e20), abi.GTP_E_ARG),
+                                      (dict(lr=1e30, weight_decay=1e30), abi.GTP_E_ARG), (dict(lr=1e15, scale=1e15), abi.GTP_E_CAPACITY),
+                                      (dict(lr=0.0, scale=3e38), abi.GTP_E_CAPACITY)])
+def test_rates_that_fp32_does_not_hold(h, status):
+    """lr scale and 1 - lr weight_decay are formed on the host: Inf there would make every weight Inf or NaN."""
+    assert step(**h) == status, abi.load().gtp_last_error()
