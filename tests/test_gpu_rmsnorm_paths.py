@@ -149,7 +149,8 @@ def test_small_rows_without_eps(R, C):
 
 @pytest.mark.parametrize("xd,rd", [(B, B), (F, None), (B, None), (F, F)])
 @pytest.mark.parametrize("R,C", [(32, 32), (64, 256), (64, 768), (64, 2016), (32, 2048), (64, 4096), (32, 8192)])
-def test_views_of_rows_of_any_size(R, C, xd, rd):
+@pytest.mark.parametrize("tiled", [False, True])
+def test_views_of_rows_of_any_size(R, C, xd, rd, tiled):
     x, w = sizes(R, C, xd), (1 + 0.2 * torch.randn(C, device=DEV)).to(B)
     kw, s = {}, x
     if rd is not None:
@@ -158,11 +159,11 @@ def test_views_of_rows_of_any_size(R, C, xd, rd):
         kw = dict(residual=res, sum=s)
     for eps in (1e-5, 0.0):
         y, rstd = torch.empty(R, C, device=DEV), torch.empty(R, device=DEV)
-        row, col = views(R, C, False)
+        row, col = views(R, C, tiled)
         gtp.gtp_rmsnorm(x, w, eps, y=y, rstd=rstd, row=row, col=col, **kw)
         check_any(s, w, eps, rstd, y)
-        check_view(row, y, False)
-        check_view(col, y.t().contiguous(), False)
+        check_view(row, y, tiled)
+        check_view(col, y.t().contiguous(), tiled)
         # with the sum in x's or the residual's place
         if rd is not None:
             a, b, y2 = x.clone(), res.clone(), torch.empty_like(y)
