@@ -165,8 +165,8 @@ COEFFICIENTS_PACK = struct.Struct("<3f").pack
 VP, I64, I32 = C.c_void_p, C.c_int64, C.c_int32
 P = C.POINTER
 
-# A gtp_rng, gtp_rotary_desc, gtp_embedding_desc, gtp_embedding_grad_desc, gtp_rmsnorm_desc, gtp_rmsnorm_grad_desc or gtp_muon_hparams goes by reference or packed
-# (VP takes both).
+# A gtp_rng, gtp_rotary_desc, gtp_embedding_desc, gtp_embedding_grad_desc, gtp_rmsnorm_desc, gtp_rmsnorm_grad_desc or
+# gtp_muon_hparams goes by reference or packed (VP takes both).
 # name -> (restype, argtypes); every entry point declared in include/gtp.h
 PROTOTYPES = {
     "gtp_last_error": (C.c_char_p, []),

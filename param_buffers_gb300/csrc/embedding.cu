@@ -159,8 +159,8 @@ __device__ __forceinline__ void clear_counters(const SortArgs &a) {
 // Few tokens: the place of a token is the number of tokens that sort before it, counted outright.  A block owns
 // kOwn tokens, keeps every token of the shard as one 32-bit number row * tokens + t in shared memory (any order: the
 // numbers differ), and its warps count, 32 owned tokens a warp, each over a part of the list.  tokens^2 comparisons
-// but one launch and no exchange between blocks: the whole gradient of [2048, 256] takes 12.4 us, 15.7 with the radix
-// sort; at 4096 tokens 21.1 and 18.2.
+// but one launch and no exchange between blocks: the whole gradient of [2048, 256] takes 15.0 us, 16.4 with the radix
+// sort; at 4096 tokens 21.5 and 19.6.
 constexpr int kOwn = 64, kRankThreads = 512, kRankMost = 2560;
 
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constant__ SortArgs a) {
@@ -451,7 +451,7 @@ __device__ __forceinline__ void load_part(const float *p, int step, int n, float
 // warp counts its tile off once its part is written; the one that counts the last off adds them up in their order, up to
 // kJoin of them.  Of a longer row the tiles of an aligned group of kJoin count among themselves, their sum takes the place
 // of the group's first part, and the groups count in turn.
-constexpr int kJoin = 16;  // all one row's tokens 43.0 us, of 200 rows 30.3; 32: 41.3 and 31.2
+constexpr int kJoin = 16;  // 8192 x 2048 of one row 36.8 us, of 200 rows 28.8; 32: 35.6 and 28.9
 
 // The tile in which the row that comes into `tile` begins: the last one before it that the row does not fill.  A lane
 // looks at one tile's first place, 32 tiles at a time, or far from here at steps that narrow by 32.
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
 }
 
 // So few tokens that every block sorts them for itself, by counting: no second launch and no parts, a row's tokens are
-// summed where its first place's tile is.  64 tokens x 2048 take 5.2 us (two launches 7.6), 9 where all are one row's
-// (9.4); at 128 one row's take 18.9 and 10.7.
+// summed where its first place's tile is.  64 tokens x 2048 take 5.2 us (two launches 7.6), 10.0 where all are one row's
+// (9.6); at 128 one row's take 19.4 and 10.7.
 constexpr int kFewTokens = 64, kFewTile = 4;
 
 struct FewArgs {
@@ -751,15 +751,16 @@ struct GradPlan {
   int64_t key, token, key2, token2, counts, counters, part, bytes;  // places in the workspace
 };
 
-// Tokens a thread of a sort tile: few where that keeps the tiles in kFewTiles (16384 tokens: 27 us with 2, 34 with 8), else
-// more, so that their counts stay few (65536: 72 us with 2, 58 with 4).
+// Tokens a thread of a sort tile: few where that keeps the tiles in kFewTiles (16384 x 256: 30 us with 2, 37 with 8), else
+// more, so that their counts stay few (65536: 75 us with 2, 47 with 8).
 int rounds_of(int64_t tokens) { return tokens <= 2 * kTileThreads * kFewTiles ? 2 : 8; }
 
 GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t cols) {
   GradPlan p = {};
   p.radix = tokens > kRankMost || rows * tokens >= (int64_t(1) << 32) - 1;
   // tiles: short ones spread few tokens over the machine, and longer ones keep the parts few from 4096 tiles on.  Eight
-  // tokens: [8192, 2048] that are all one row's 37 us, of 200 rows 25; with tiles of four 52 and 32
+  // tokens: [8192, 2048] that are all one row's 37 us, of 200 rows 29; with tiles of four 52 and 37 (but [2048, 256] 15.1 and
+  // 12.6)
   p.tile = int32_t(std::max<int64_t>(8, (tokens + 4095) / 4096));
   p.tiles = int32_t((tokens + p.tile - 1) / p.tile);
   const int64_t each = kTileThreads * rounds_of(tokens);
@@ -800,12 +801,14 @@ gtp_status sort_tokens(SortArgs &a, const GradPlan &plan, cudaStream_t st) {
   for (int i = 0; i < passes; ++i) {  // the last pass writes the result
     const bool into_first = (passes - 1 - i) % 2 == 0;
     int32_t *key_out = into_first ? a.key : a.key2, *token_out = into_first ? a.token : a.token2;
-    gtp_status s = gtp::launch_overlapped(wide ? radix_count_kernel<8> : radix_count_kernel<2>, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key,
-                                          8 * i);
+    gtp_status s = gtp::launch_overlapped(wide ? radix_count_kernel<8> : radix_count_kernel<2>, unsigned(a.tiles), kTileThreads, 0, st,
+                                          "embedding_grad", a, key, 8 * i);
     if (!s && a.scan) s = gtp::launch_overlapped(radix_scan_kernel, 1, kScanThreads, 0, st, "embedding_grad", a);
     if (!s)
-      s = gtp::launch_overlapped(a.scan ? radix_scatter_kernel<8, true> : wide ? radix_scatter_kernel<8, false> : radix_scatter_kernel<2, false>, unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key, token,
-                                 key_out, token_out, 8 * i);
+      s = gtp::launch_overlapped(a.scan ? radix_scatter_kernel<8, true>
+                                 : wide ? radix_scatter_kernel<8, false>
+                                        : radix_scatter_kernel<2, false>,
+                                 unsigned(a.tiles), kTileThreads, 0, st, "embedding_grad", a, key, token, key_out, token_out, 8 * i);
     if (s) return s;
     key = key_out, token = token_out;
   }
