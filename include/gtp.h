@@ -867,10 +867,12 @@ gtp_status gtp_mxfp8_dequantize(const uint8_t *e4m3, const uint8_t *e8m0, int32_
  *   X = G / |G|_F (0 for a matrix of zeros);   steps times:  A = X X^T,  X <- a X + (b A + c A^2) X,
  * (a, b, c) = coefficients[0..2], with the smaller Gram matrix (X^T X on the other side for rows > cols).
  * fp16 tensor-core products with fp32 accumulation, the diagonals of A and of b A + c A^2 in fp32 and the X of the
- * linear term in 22 bits.  Relative error with the usual coefficients, before the result's own rounding: 1e-4 to 1e-3
- * at up to 5 steps (to 3e-3 where a few directions hold nearly all of the matrix), 3e-3 at 10, to 3e-2 at 16.  What a
- * matrix has below 2^-22 of its norm is rounding, which every iteration multiplies by a like any small singular value:
- * 1e-2 of the result at 10 steps on a matrix of lower rank, as large as the result at 16.  The sum of squares
+ * linear term in 22 bits.  Relative error with the usual coefficients, before the result's own rounding, on sides of
+ * 16 and more: 1e-4 to 1.5e-3 at up to 5 steps (to 3e-3 where a few directions hold nearly all of the matrix); 3e-3
+ * and seldom to 7e-3 at 10, 4e-3 and seldom to 5e-2 at 16, where the polynomial throws singular values apart.  Shorter
+ * sides do not average the roundings out: to 1e-2 at 5 steps, 1e-1 at 10.  What a matrix has below 2^-22 of its norm is
+ * rounding, which every iteration multiplies by a like any small singular value: 1e-2 of the result at 10 steps on a
+ * matrix of lower rank, as large as the result at 16.  The sum of squares
  * is taken in fp32 by sixteens and in fp64 across, in fp64 alone where fp32 does not hold it: elements of any finite
  * size; a matrix with NaN or Inf becomes NaN.  A fixed order: equal calls give equal bits.
  * src: [count] matrices of [rows, cols], F32 or BF16, row stride src_ld and matrix stride src_plane

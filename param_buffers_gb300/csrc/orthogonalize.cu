@@ -22,11 +22,10 @@
 //     but by a alone in the first iterations, where small singular values, on which e acts as far less than a + B does,
 //     still grow a-fold each.  Those that matter in the end are small until the last three (`early_of`);
 //   - A' enters B' with a low part of its own (the square reads the high part).
-// Against fp64, relative error of the result at five steps: 1e-4 to 1e-3 over Gaussian, row-scaled and low-rank matrices
-// (singular values over six decades 1.3e-3, rank 8 and 1e-3 of noise in 16 x 4096 2.6e-3); without the first two choices
-// 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.  Later iterations carry the
-// roundings of earlier ones on by the polynomial's slopes: 3e-3 at ten steps, 1.2e-2 and on a single small matrix 2.3e-2
-// at sixteen.
+// Against fp64, relative error of the result at five steps: 1e-4 to 1.5e-3 over Gaussian, row-scaled and low-rank matrices with
+// sides of 16 and more (rank 8 and 1e-3 of noise in 16 x 4096 2.6e-3; with a side of 2 to 9e-3); without the first two
+// choices 2e-3 to 9e-3, with bf16 operands 1.4e-2 to 6e-2.  A bf16 result's own rounding is 1.7e-3.  Later iterations carry
+// the roundings of earlier ones on by the polynomial's slopes: mostly 3e-3 at ten steps and 4e-3 at sixteen.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
