@@ -415,7 +415,7 @@ __device__ __noinline__ void redo_tile(const NormArgs &a, const float (&squares)
 // 32 bytes.  STATS false: r is read, only the columnwise view is written (rows too wide for a cluster; the sum, r and
 // what goes by rows are norm_kernel's).
 //
-// Both views of [8192, 2048] bf16 with a bf16 residual: 35.5 us, 3.8 TB/s of x, the residual, the sum and the views (37.1
+// Both views of [8192, 2048] bf16 with a bf16 residual: 35.5 us, 3.8 TB/s of x, the residual, the sum and the views (36.1
 // with the sum written before the cluster's exchange).  Bound by latency: load, exchange and two rounds through shared
 // memory follow one another in a block, and four blocks of 64 registers a thread are an SM's (three 38.1 us, five 48.1).
 constexpr int kTileThreads = 256, kTileRows = 32, kMostCluster = 8;
@@ -789,7 +789,8 @@ extern "C" gtp_status gtp_rmsnorm(const gtp_rmsnorm_desc *d, gtp_stream stream) 
   a.col_words = d->tiled_scales ? (R / 32 + 3) / 4 : 0;
   a.inv_cols = 1.f / float(C), a.codes_on_32 = aligned(d->col_codes, 32);
   // a mean that the squares' last bits, 2^-149 each, do not reach in any case is left alone
-  a.eps = d->eps, a.least = d->eps >= 0x1p-80f ? 0.f : 0x1p-100f, a.weight_f32 = d->weight_dtype == GTP_F32, a.y_f32 = d->y_dtype == GTP_F32;
+  a.eps = d->eps, a.least = d->eps >= 0x1p-80f ? 0.f : 0x1p-100f;
+  a.weight_f32 = d->weight_dtype == GTP_F32, a.y_f32 = d->y_dtype == GTP_F32;
   cudaStream_t st = gtp::as_stream(stream);
   using B = __nv_bfloat16;
   if (!res) return d->x_dtype == GTP_F32 ? launch<float, float, false>(a, vec, dev, st) : launch<B, B, false>(a, vec, dev, st);
